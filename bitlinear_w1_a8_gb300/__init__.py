@@ -20,9 +20,13 @@ __all__ = [
     "bitlinear_forward_workspace", "bitlinear_forward_ws",
     "bitlinear_device_status", "bitlinear_quantize_weights_noalloc",
     "bitlinear_selftest_wait_timeout", "bitlinear_linear", "bitlinear_linear_ws", "bitlinear_argmax",
-    "BitLinearWeight",
+    "bitlinear_rope_frequencies", "bitlinear_rope", "bitlinear_kv_append", "bitlinear_kv_read",
+    "bitlinear_attention_workspace", "bitlinear_attention",
+    "BitLinearWeight", "BitLinearKVPages", "BitLinearRopeSpec",
     "EXPORTED_SYMBOLS",
     "ALGO_AUTO", "ALGO_DECODE", "ALGO_PREFILL", "ALGO_BATCHED", "ALGO_WIDE", "FLAG_PDL",
+    "KV_INT8", "KV_FP8", "KV_BF16", "ROPE_HALF", "ROPE_INTERLEAVED",
+    "ROPE_SCALE_NONE", "ROPE_SCALE_LINEAR", "ROPE_SCALE_BASE", "ROPE_SCALE_PARTS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -31,6 +35,10 @@ _LIB_PATH = os.path.join(_HERE, "_build", "libbitlinear.so")
 ALGO_AUTO, ALGO_DECODE, ALGO_PREFILL, ALGO_BATCHED, ALGO_WIDE = 0, 1, 2, 3, 4
 FLAG_PDL = 1
 FLAG_GATED = 2  # bitlinear_linear: gate, up pair; the first output receives (r * r) * up, r = max(gate, 0)
+
+KV_INT8, KV_FP8, KV_BF16 = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_BASE, ROPE_SCALE_PARTS = 0, 1, 2, 3
 
 STATUS = {0: "OK", -1: "ERR_NULL", -2: "ERR_SHAPE", -3: "ERR_ALIGN", -4: "ERR_UNSUPPORTED",
           -5: "ERR_CUDA", -6: "ERR_TIMEOUT", -7: "ERR_WORKSPACE"}
@@ -43,6 +51,8 @@ EXPORTED_SYMBOLS = (
     "bitlinear_forward_workspace", "bitlinear_forward_ws",
     "bitlinear_device_status", "bitlinear_quantize_weights_noalloc",
     "bitlinear_selftest_wait_timeout", "bitlinear_linear", "bitlinear_linear_ws", "bitlinear_argmax",
+    "bitlinear_rope_frequencies", "bitlinear_rope", "bitlinear_kv_append", "bitlinear_kv_read",
+    "bitlinear_attention_workspace", "bitlinear_attention",
 )
 
 _lib = None
@@ -52,6 +62,19 @@ class BitLinearWeight(ctypes.Structure):
     """ctypes mirror of the C struct bitlinear_weight."""
     _fields_ = [("packed", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("N", ctypes.c_int64),
                 ("y", ctypes.c_void_p), ("acc", ctypes.c_void_p)]
+
+
+class BitLinearKVPages(ctypes.Structure):
+    """ctypes mirror of the C struct bitlinear_kv_pages."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_step", ctypes.c_void_p),
+                ("v_step", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("num_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class BitLinearRopeSpec(ctypes.Structure):
+    """ctypes mirror of the C struct bitlinear_rope_spec."""
+    _fields_ = [("freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("amplitude", ctypes.c_float)]
 
 
 class BitLinearError(RuntimeError):
@@ -109,6 +132,21 @@ def load_library(path: str | None = None):
     lib.bitlinear_linear_ws.restype = st
     lib.bitlinear_argmax.argtypes = [vp, i64, i64, vp, vp]
     lib.bitlinear_argmax.restype = st
+    ci, dbl, pages, spec = ctypes.c_int, ctypes.c_double, ctypes.POINTER(BitLinearKVPages), ctypes.POINTER(BitLinearRopeSpec)
+    lib.bitlinear_rope_frequencies.argtypes = [ci, dbl, ci, dbl, dbl, dbl, dbl, vp]
+    lib.bitlinear_rope_frequencies.restype = st
+    lib.bitlinear_rope.argtypes = [vp, i64, i64, ci, ci, vp, spec, vp, i64, ci, vp]
+    lib.bitlinear_rope.restype = st
+    lib.bitlinear_kv_append.argtypes = [vp, i64, ci, vp, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, i64, i64, spec,
+                                        pages, ci, vp]
+    lib.bitlinear_kv_append.restype = st
+    lib.bitlinear_kv_read.argtypes = [pages, i64, vp, vp, vp, i64, i64, i64, vp, i64, vp, i64, ci, vp]
+    lib.bitlinear_kv_read.restype = st
+    lib.bitlinear_attention_workspace.argtypes = [i64, ci, ci, ci]
+    lib.bitlinear_attention_workspace.restype = sz
+    lib.bitlinear_attention.argtypes = [vp, i64, i64, ci, pages, vp, i64, i64, vp, i64, ctypes.c_float, vp, i64, vp,
+                                        sz, ci, vp]
+    lib.bitlinear_attention.restype = st
     lib.bitlinear_device_status.argtypes = [vp, ctypes.c_int]
     lib.bitlinear_device_status.restype = st
     if path is None:
@@ -361,3 +399,195 @@ def bitlinear_linear_ws(x, weights, xq, x_scale, workspace, mul=None, rms_weight
         _ptr(x), _ptr(mul), M, K, _ptr(rms_weight), float(rms_eps), arr, len(weights), _ptr(xq),
         _ptr(x_scale), int(flags), _ptr(workspace), 0 if workspace is None else workspace.numel(),
         _stream(stream)), "bitlinear_linear_ws")
+
+
+# --- rotary positions, the paged key-value cache and attention over it ---
+
+
+def _rows(t, name, T, H=None, D=None):
+    """The row stride (elements) of fp32 [T, H, D] rows: heads side by side, rows any
+    stride apart.  H, D None: any."""
+    import torch
+    if not getattr(t, "is_cuda", False):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or (H is not None and shape[1] != H) or (D is not None and shape[2] != D):
+        raise ValueError(f"{name} must have shape ({T}, {'heads' if H is None else H}, "
+                         f"{'head_dim' if D is None else D}), got {tuple(shape)}")
+    if t.is_contiguous():  # strides of dims of size 1 say nothing
+        return shape[1] * shape[2]
+    strides = t.stride()
+    if strides[2] != 1 or (shape[1] > 1 and strides[1] != shape[2]):
+        raise ValueError(f"{name}'s heads must lie side by side in each row, got strides {tuple(strides)}")
+    return strides[0] if T > 1 else shape[1] * shape[2]
+
+
+def _ints(t, name, shape):
+    import torch
+    _need(t, torch.int32, name, shape)
+
+
+def _pages_table(t, rows=None):
+    """(rows, columns, row stride) of the int32 page table: contiguous rows, any stride apart."""
+    import torch
+    if not getattr(t, "is_cuda", False) or t.dtype != torch.int32:
+        raise TypeError("page_table must be an int32 CUDA tensor")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"page_table must be [{'sequences' if rows is None else rows}, pages], got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("page_table's rows must be contiguous")
+    n, cols = t.shape
+    return n, cols, t.stride(0) if n > 1 else cols
+
+
+def _same_device(first, *others):
+    """Every tensor on the current device: the library launches there."""
+    import torch
+    at = torch.cuda.current_device()
+    for t in (first, *others):
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"every tensor must be on the current device cuda:{at}, got one on {t.device}")
+
+
+def _kv_pages(cache):
+    """BitLinearKVPages of (k, v, k_step, v_step), the steps None for bf16."""
+    import torch
+    k, v = cache[0], cache[1]
+    k_step, v_step = (cache[2], cache[3]) if len(cache) > 2 else (None, None)
+    if not getattr(k, "is_cuda", False):
+        raise TypeError("the cache must be CUDA tensors")
+    if k.dim() != 4:
+        raise ValueError(f"the cache's k must be [pages, heads, page_size, head_dim], got {tuple(k.shape)}")
+    fmt = (KV_INT8 if k.dtype == torch.int8 else KV_FP8 if k.dtype == torch.float8_e4m3fn
+           else KV_BF16 if k.dtype == torch.bfloat16 else None)
+    if fmt is None:
+        raise TypeError(f"the cache must be int8, float8_e4m3fn or bfloat16, got {k.dtype}")
+    shape = k.shape
+    _need(k, k.dtype, "the cache's k")
+    _need(v, k.dtype, "the cache's v", shape)
+    if fmt == KV_BF16:
+        if k_step is not None or v_step is not None:
+            raise ValueError("a bfloat16 cache has no steps")
+    else:
+        _need(k_step, torch.float32, "the cache's k_step", shape[:3])
+        _need(v_step, torch.float32, "the cache's v_step", shape[:3])
+    return BitLinearKVPages(k.data_ptr(), v.data_ptr(), _ptr(k_step), _ptr(v_step), shape[0], shape[1], shape[2],
+                            shape[3], fmt)
+
+
+def _rope_spec(rope):
+    """BitLinearRopeSpec of (freq, layout) or (freq, layout, amplitude)."""
+    import torch
+    freq = rope[0]
+    _need(freq, torch.float64, "rope's freq")
+    return BitLinearRopeSpec(freq.data_ptr(), 2 * freq.numel(), int(rope[1]), float(rope[2]) if len(rope) > 2 else 1.0)
+
+
+def bitlinear_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = ROPE_SCALE_NONE,
+                               factor: float = 1.0, original_length: float = 0.0, low: float = 1.0,
+                               high: float = 32.0):
+    """The rot_dim / 2 rotary frequencies (radians a position) as a fp64 CPU tensor; move it
+    to the device once."""
+    import torch
+    n = max(0, int(rot_dim)) // 2
+    out = (ctypes.c_double * max(1, n))()
+    _check(load_library().bitlinear_rope_frequencies(
+        int(rot_dim), float(base), int(scaling), float(factor), float(original_length), float(low), float(high),
+        ctypes.addressof(out)), "bitlinear_rope_frequencies")
+    return torch.tensor(list(out), dtype=torch.float64)
+
+
+def bitlinear_rope(x, positions, rope, y, flags: int = 0, stream=None):
+    """y [T, H, D] = x [T, H, D] rotated to positions [T] (int32).
+
+    rope: (freq, layout) or (freq, layout, amplitude) with freq a fp64 CUDA tensor
+    (bitlinear_rope_frequencies) and layout ROPE_HALF or ROPE_INTERLEAVED.  y may be x.
+    Rows may lie any multiple of 4 floats apart.
+    """
+    T = x.shape[0]
+    x_stride = _rows(x, "x", T)
+    _, H, D = x.shape
+    y_stride = _rows(y, "y", T, H, D)
+    _ints(positions, "positions", (T,))
+    spec = _rope_spec(rope)
+    _same_device(x, y, positions, rope[0])
+    _check(load_library().bitlinear_rope(_ptr(x), x_stride, T, H, D, _ptr(positions), spec, _ptr(y), y_stride,
+                                         int(flags), _stream(stream)), "bitlinear_rope")
+
+
+def bitlinear_kv_append(k, v, cache, positions, page_table, seq=None, q=None, q_out=None, rope=None,
+                        flags: int = 0, stream=None):
+    """Writes T new tokens into the paged cache: k and v [T, heads, head_dim] quantised as they
+    are written, k and the optional q [T, q_heads, head_dim] rotated first (q into q_out).
+
+    cache: (k, v, k_step, v_step), codes [pages, heads, page_size, head_dim] of int8 or
+    float8_e4m3fn with fp32 steps [pages, heads, page_size], or (k, v) of bfloat16.
+    positions, seq: int32 [T]; page_table: int32 [sequences, pages]; seq None: row i is of
+    sequence i.  Rows with a negative position are padding.  rope: as for bitlinear_rope.
+    """
+    pages = _kv_pages(cache)
+    T, Hk, D = k.shape[0], pages.num_heads, pages.head_dim
+    k_stride = _rows(k, "k", T, Hk, D)
+    v_stride = _rows(v, "v", T, Hk, D)
+    _ints(positions, "positions", (T,))
+    if seq is not None:
+        _ints(seq, "seq", (T,))
+    num_seqs, max_pages, table_stride = _pages_table(page_table)
+    Hq = q_stride = q_out_stride = 0
+    if q is not None:
+        q_stride = _rows(q, "q", T, None, D)
+        Hq = q.shape[1]
+        q_out_stride = _rows(q_out, "q_out", T, Hq, D)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    spec = None if rope is None else _rope_spec(rope)
+    _same_device(k, v, cache[0], cache[1], positions, page_table, seq, q, q_out, None if rope is None else rope[0])
+    _check(load_library().bitlinear_kv_append(
+        _ptr(q), q_stride, Hq, _ptr(q_out), q_out_stride, _ptr(k), k_stride, _ptr(v), v_stride, T, _ptr(positions),
+        _ptr(seq), _ptr(page_table), table_stride, num_seqs, max_pages, spec, pages, int(flags), _stream(stream)),
+        "bitlinear_kv_append")
+
+
+def bitlinear_kv_read(cache, positions, page_table, k_out, v_out, seq=None, flags: int = 0, stream=None):
+    """k_out, v_out [T, heads, head_dim] fp32 = the cached rows at (seq[i], positions[i])."""
+    pages = _kv_pages(cache)
+    T, Hk, D = k_out.shape[0], pages.num_heads, pages.head_dim
+    k_stride = _rows(k_out, "k_out", T, Hk, D)
+    v_stride = _rows(v_out, "v_out", T, Hk, D)
+    _ints(positions, "positions", (T,))
+    if seq is not None:
+        _ints(seq, "seq", (T,))
+    num_seqs, max_pages, table_stride = _pages_table(page_table)
+    _same_device(k_out, v_out, cache[0], cache[1], positions, page_table, seq)
+    _check(load_library().bitlinear_kv_read(
+        pages, T, _ptr(positions), _ptr(seq), _ptr(page_table), table_stride, num_seqs, max_pages, _ptr(k_out),
+        k_stride, _ptr(v_out), v_stride, int(flags), _stream(stream)), "bitlinear_kv_read")
+
+
+def bitlinear_attention_workspace(B: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of device workspace with which bitlinear_attention may split its sequences further."""
+    return int(load_library().bitlinear_attention_workspace(int(B), int(num_q_heads), int(num_kv_heads), int(head_dim)))
+
+
+def bitlinear_attention(q, cache, page_table, lengths, out, workspace=None, scale: float | None = None,
+                        window: int = 0, flags: int = 0, stream=None):
+    """out [B, q_heads, head_dim] = attention of q over the lengths[b] cached tokens of each
+    sequence (the last `window` of them when it is not 0); scale None: 1 / sqrt(head_dim).
+    cache and page_table: as for bitlinear_kv_append; lengths: int32 [B]."""
+    import torch
+    pages = _kv_pages(cache)
+    B, D = q.shape[0], pages.head_dim
+    q_stride = _rows(q, "q", B, None, D)
+    Hq = q.shape[1]
+    out_stride = _rows(out, "out", B, Hq, D)
+    _ints(lengths, "lengths", (B,))
+    _, max_pages, table_stride = _pages_table(page_table, B)
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+    _same_device(q, out, cache[0], cache[1], page_table, lengths, workspace)
+    _check(load_library().bitlinear_attention(
+        _ptr(q), q_stride, B, Hq, pages, _ptr(page_table), table_stride, max_pages, _ptr(lengths), int(window),
+        D ** -0.5 if scale is None else float(scale), _ptr(out), out_stride, _ptr(workspace),
+        0 if workspace is None else workspace.numel(), int(flags), _stream(stream)), "bitlinear_attention")

@@ -26,7 +26,8 @@ NVCC_FLAGS = ARCH + [
     "-prec-div=true", "-prec-sqrt=true",
     "-I", INCLUDE, "-I", CSRC,
 ]
-SOURCES = ["abi.cu", "wquant.cu", "aquant.cu", "decode.cu", "prefill.cu", "wide.cu", "argmax.cu"]
+SOURCES = ["abi.cu", "wquant.cu", "aquant.cu", "decode.cu", "prefill.cu", "wide.cu", "argmax.cu",
+           "rope_kv.cu", "attention.cu"]
 
 
 def _nvcc() -> str:

@@ -1,8 +1,11 @@
 // abi.cu -- the extern "C" entry points: argument checks, device discovery and
 // dispatch to the kernel launchers.  Nothing here allocates device memory.
+#include <math.h>
+
 #include <mutex>
 
 #include "common.cuh"
+#include "kv.cuh"
 
 namespace bitlinear {
 // argmax.cu: index[m] = first n of the largest y[m, n], M rows of N floats.
@@ -482,6 +485,222 @@ bitlinear_status bitlinear_quantize_weights_noalloc(const float* W, int64_t N, i
   if (st != BITLINEAR_OK) return st;
   return from_cuda(launch_weight_quant(W, N, K, packed, w_scale, static_cast<unsigned long long*>(scratch),
                                        dev, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Rotary positions, the paged key-value cache and attention over it.
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kMaxHeads = 4096;
+constexpr int kMaxHeadDim = 256;
+
+bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Rows of `heads` heads of D floats, `stride` floats apart.
+bool stride_ok(int64_t stride, int64_t heads, int64_t D) {
+  return stride >= heads * D && stride % 4 == 0 && stride < ((int64_t)1 << 40);
+}
+
+bitlinear_status check_rope(const bitlinear_rope_spec* r, int D, RopeArgs* out) {
+  *out = RopeArgs{};
+  if (!r) return BITLINEAR_OK;
+  if (!r->freq) return BITLINEAR_ERR_NULL;
+  if (r->rot_dim < 2 || r->rot_dim > D || r->rot_dim % 2 != 0) return BITLINEAR_ERR_SHAPE;
+  if (!isfinite(r->amplitude)) return BITLINEAR_ERR_SHAPE;
+  if (r->layout != BITLINEAR_ROPE_HALF && r->layout != BITLINEAR_ROPE_INTERLEAVED) return BITLINEAR_ERR_UNSUPPORTED;
+  if (!aligned_to(r->freq, 8)) return BITLINEAR_ERR_ALIGN;
+  *out = RopeArgs{r->freq, r->rot_dim, r->layout, r->amplitude};
+  return BITLINEAR_OK;
+}
+
+bitlinear_status check_pages(const bitlinear_kv_pages* c, KvPages* out) {
+  if (!c) return BITLINEAR_ERR_NULL;
+  if (c->format != BITLINEAR_KV_INT8 && c->format != BITLINEAR_KV_FP8 && c->format != BITLINEAR_KV_BF16)
+    return BITLINEAR_ERR_UNSUPPORTED;
+  if (c->num_pages < 1 || c->num_pages > 0x7fffffffLL || c->num_heads < 1 || c->num_heads > kMaxHeads)
+    return BITLINEAR_ERR_SHAPE;
+  if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1))) return BITLINEAR_ERR_SHAPE;
+  if (c->head_dim < 16 || c->head_dim > kMaxHeadDim || c->head_dim % 16 != 0) return BITLINEAR_ERR_SHAPE;
+  // num_pages < 2^31 and the rest <= 2^32: the product fits in 64 bits
+  if (c->num_pages * ((int64_t)c->num_heads * c->page_size * c->head_dim) >= ((int64_t)1 << 48))
+    return BITLINEAR_ERR_SHAPE;
+  const bool steps = c->format != BITLINEAR_KV_BF16;
+  if (!c->k || !c->v || (steps && (!c->k_step || !c->v_step))) return BITLINEAR_ERR_NULL;
+  if (!aligned16(c->k) || !aligned16(c->v) || (steps && (!aligned16(c->k_step) || !aligned16(c->v_step))))
+    return BITLINEAR_ERR_ALIGN;
+  int shift = 4;
+  while ((1 << shift) < c->page_size) ++shift;
+  *out = KvPages{c->k, c->v, steps ? c->k_step : nullptr, steps ? c->v_step : nullptr, c->num_pages,
+                 c->num_heads, shift, c->head_dim, c->format};
+  return BITLINEAR_OK;
+}
+
+bool table_ok(int64_t table_stride, int64_t max_pages) {
+  return max_pages >= 1 && max_pages <= kMaxDim && (table_stride == 0 || table_stride >= max_pages) &&
+         table_stride <= kMaxDim;
+}
+
+bitlinear_status check_rows(int64_t T, const int32_t* positions, const int32_t* seq, const int32_t* table,
+                            int64_t table_stride, int64_t num_seqs, int64_t max_pages, KvRows* out) {
+  if (T < 0 || T > kMaxDim || num_seqs < 1 || num_seqs > kMaxDim || !table_ok(table_stride, max_pages))
+    return BITLINEAR_ERR_SHAPE;
+  if (!seq && T > num_seqs) return BITLINEAR_ERR_SHAPE;
+  if (T == 0) return BITLINEAR_OK;
+  if (!positions || !table) return BITLINEAR_ERR_NULL;
+  if (!aligned_to(positions, 4) || !aligned_to(table, 4) || !aligned_to(seq, 4)) return BITLINEAR_ERR_ALIGN;
+  *out = KvRows{positions, seq, table, table_stride, num_seqs, max_pages, T};
+  return BITLINEAR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+bitlinear_status bitlinear_rope_frequencies(int rot_dim, double base, int scaling, double factor,
+                                            double original_length, double low, double high, double* freq_host) {
+  if (!freq_host) return BITLINEAR_ERR_NULL;
+  if (scaling < BITLINEAR_ROPE_SCALE_NONE || scaling > BITLINEAR_ROPE_SCALE_PARTS) return BITLINEAR_ERR_UNSUPPORTED;
+  if (rot_dim < 2 || rot_dim > kMaxHeadDim || rot_dim % 2 != 0) return BITLINEAR_ERR_SHAPE;
+  if (!isfinite(base) || !(base > 0.0)) return BITLINEAR_ERR_SHAPE;
+  if (scaling != BITLINEAR_ROPE_SCALE_NONE && (!isfinite(factor) || !(factor > 0.0))) return BITLINEAR_ERR_SHAPE;
+  if (scaling == BITLINEAR_ROPE_SCALE_BASE) {
+    if (rot_dim == 2) return BITLINEAR_ERR_SHAPE;
+    base *= pow(factor, (double)rot_dim / (rot_dim - 2));
+    if (!isfinite(base) || !(base > 0.0)) return BITLINEAR_ERR_SHAPE;
+  }
+  if (scaling == BITLINEAR_ROPE_SCALE_PARTS &&
+      (!isfinite(original_length) || !(original_length > 0.0) || !isfinite(low) || !isfinite(high) || !(high > low)))
+    return BITLINEAR_ERR_SHAPE;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot_dim);
+    if (scaling == BITLINEAR_ROPE_SCALE_LINEAR) f /= factor;
+    if (scaling == BITLINEAR_ROPE_SCALE_PARTS) {
+      const double turns = original_length * f / 6.283185307179586477;
+      const double g = fmin(1.0, fmax(0.0, (turns - low) / (high - low)));
+      f *= g + (1.0 - g) / factor;
+    }
+    freq_host[i] = f;
+  }
+  return BITLINEAR_OK;
+}
+
+bitlinear_status bitlinear_rope(const float* x, int64_t x_stride, int64_t T, int H, int D, const int32_t* positions,
+                                const bitlinear_rope_spec* rope, float* y, int64_t y_stride, int flags,
+                                void* stream) {
+  if (!rope) return BITLINEAR_ERR_NULL;
+  if (T < 0 || T > kMaxDim || H < 1 || H > kMaxHeads || D < 4 || D > kMaxHeadDim || D % 4 != 0)
+    return BITLINEAR_ERR_SHAPE;
+  if (!stride_ok(x_stride, H, D) || !stride_ok(y_stride, H, D)) return BITLINEAR_ERR_SHAPE;
+  if (x == y && x_stride != y_stride) return BITLINEAR_ERR_SHAPE;
+  if (flags & ~BITLINEAR_FLAG_PDL) return BITLINEAR_ERR_UNSUPPORTED;
+  RopeArgs r;
+  bitlinear_status st = check_rope(rope, D, &r);
+  if (st != BITLINEAR_OK) return st;
+  if (T == 0) return BITLINEAR_OK;
+  if (!x || !y || !positions) return BITLINEAR_ERR_NULL;
+  if (!aligned16(x) || !aligned16(y) || !aligned_to(positions, 4)) return BITLINEAR_ERR_ALIGN;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  return from_cuda(launch_rope(x, x_stride, T, H, D, positions, r, y, y_stride, (flags & BITLINEAR_FLAG_PDL) != 0,
+                               dev, static_cast<cudaStream_t>(stream)));
+}
+
+bitlinear_status bitlinear_kv_append(const float* q, int64_t q_stride, int num_q_heads, float* q_out,
+                                     int64_t q_out_stride, const float* k, int64_t k_stride, const float* v,
+                                     int64_t v_stride, int64_t T, const int32_t* positions, const int32_t* seq,
+                                     const int32_t* page_table, int64_t table_stride, int64_t num_seqs,
+                                     int64_t max_pages, const bitlinear_rope_spec* rope,
+                                     const bitlinear_kv_pages* cache, int flags, void* stream) {
+  KvPages c;
+  bitlinear_status st = check_pages(cache, &c);
+  if (st != BITLINEAR_OK) return st;
+  KvRows rows = {};
+  st = check_rows(T, positions, seq, page_table, table_stride, num_seqs, max_pages, &rows);
+  if (st != BITLINEAR_OK) return st;
+  RopeArgs r;
+  st = check_rope(rope, c.head_dim, &r);
+  if (st != BITLINEAR_OK) return st;
+  if (flags & ~BITLINEAR_FLAG_PDL) return BITLINEAR_ERR_UNSUPPORTED;
+  if (num_q_heads < 0 || num_q_heads > kMaxHeads) return BITLINEAR_ERR_SHAPE;
+  if (num_q_heads > 0 &&
+      (!stride_ok(q_stride, num_q_heads, c.head_dim) || !stride_ok(q_out_stride, num_q_heads, c.head_dim) ||
+       (q == q_out && q_stride != q_out_stride)))
+    return BITLINEAR_ERR_SHAPE;
+  if (!stride_ok(k_stride, c.heads, c.head_dim) || !stride_ok(v_stride, c.heads, c.head_dim))
+    return BITLINEAR_ERR_SHAPE;
+  if (T == 0) return BITLINEAR_OK;
+  if (!k || !v || (num_q_heads > 0 && (!q || !q_out))) return BITLINEAR_ERR_NULL;
+  if (num_q_heads == 0 && (q || q_out)) return BITLINEAR_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out)) return BITLINEAR_ERR_ALIGN;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  return from_cuda(launch_kv_append(q, q_stride, num_q_heads, q_out, q_out_stride, k, k_stride, v, v_stride, rows, r,
+                                    c, (flags & BITLINEAR_FLAG_PDL) != 0, dev, static_cast<cudaStream_t>(stream)));
+}
+
+bitlinear_status bitlinear_kv_read(const bitlinear_kv_pages* cache, int64_t T, const int32_t* positions,
+                                   const int32_t* seq, const int32_t* page_table, int64_t table_stride,
+                                   int64_t num_seqs, int64_t max_pages, float* k_out, int64_t k_stride, float* v_out,
+                                   int64_t v_stride, int flags, void* stream) {
+  KvPages c;
+  bitlinear_status st = check_pages(cache, &c);
+  if (st != BITLINEAR_OK) return st;
+  KvRows rows = {};
+  st = check_rows(T, positions, seq, page_table, table_stride, num_seqs, max_pages, &rows);
+  if (st != BITLINEAR_OK) return st;
+  if (flags & ~BITLINEAR_FLAG_PDL) return BITLINEAR_ERR_UNSUPPORTED;
+  if (!stride_ok(k_stride, c.heads, c.head_dim) || !stride_ok(v_stride, c.heads, c.head_dim))
+    return BITLINEAR_ERR_SHAPE;
+  if (T == 0) return BITLINEAR_OK;
+  if (!k_out || !v_out) return BITLINEAR_ERR_NULL;
+  if (!aligned16(k_out) || !aligned16(v_out)) return BITLINEAR_ERR_ALIGN;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  return from_cuda(launch_kv_read(c, rows, k_out, k_stride, v_out, v_stride, (flags & BITLINEAR_FLAG_PDL) != 0, dev,
+                                  static_cast<cudaStream_t>(stream)));
+}
+
+size_t bitlinear_attention_workspace(int64_t B, int num_q_heads, int num_kv_heads, int head_dim) {
+  if (B < 1 || B > kMaxDim || num_q_heads < 1 || num_q_heads > kMaxHeads || num_kv_heads < 1 ||
+      num_q_heads % num_kv_heads != 0 || head_dim < 16 || head_dim > kMaxHeadDim || head_dim % 16 != 0)
+    return 0;
+  return attention_workspace_bytes(B, num_q_heads, num_kv_heads, head_dim);
+}
+
+bitlinear_status bitlinear_attention(const float* q, int64_t q_stride, int64_t B, int num_q_heads,
+                                     const bitlinear_kv_pages* cache, const int32_t* page_table,
+                                     int64_t table_stride, int64_t max_pages, const int32_t* lengths, int64_t window,
+                                     float scale, float* out, int64_t out_stride, void* workspace,
+                                     size_t workspace_bytes, int flags, void* stream) {
+  KvPages c;
+  bitlinear_status st = check_pages(cache, &c);
+  if (st != BITLINEAR_OK) return st;
+  if (B < 0 || B > kMaxDim || !table_ok(table_stride, max_pages) || window < 0 || !isfinite(scale))
+    return BITLINEAR_ERR_SHAPE;
+  if (num_q_heads < 1 || num_q_heads > kMaxHeads || num_q_heads % c.heads != 0) return BITLINEAR_ERR_SHAPE;
+  if (!stride_ok(q_stride, num_q_heads, c.head_dim) || !stride_ok(out_stride, num_q_heads, c.head_dim))
+    return BITLINEAR_ERR_SHAPE;
+  if (flags & ~BITLINEAR_FLAG_PDL) return BITLINEAR_ERR_UNSUPPORTED;
+  if (B == 0) return BITLINEAR_OK;
+  if (!q || !out || !page_table || !lengths) return BITLINEAR_ERR_NULL;
+  if (!aligned16(q) || !aligned16(out) || !aligned_to(page_table, 4) || !aligned_to(lengths, 4))
+    return BITLINEAR_ERR_ALIGN;
+  if (workspace && workspace_bytes < attention_workspace_bytes(B, num_q_heads, c.heads, c.head_dim))
+    return BITLINEAR_ERR_WORKSPACE;
+  if (workspace && !aligned16(workspace)) return BITLINEAR_ERR_ALIGN;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  const AttendArgs a = {q, out, q_stride, out_stride, page_table, table_stride, max_pages, lengths, window, scale,
+                        B, num_q_heads};
+  return from_cuda(launch_attention(a, c, workspace, (flags & BITLINEAR_FLAG_PDL) != 0, dev,
+                                    static_cast<cudaStream_t>(stream)));
 }
 
 bitlinear_status bitlinear_selftest_wait_timeout(int64_t limit_ns, void* stream) {

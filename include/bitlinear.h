@@ -353,6 +353,169 @@ bitlinear_status bitlinear_quantize_weights_noalloc(const float* W, int64_t N, i
  * 4-byte aligned), BITLINEAR_ERR_CUDA. */
 bitlinear_status bitlinear_argmax(const float* y, int64_t M, int64_t N, int32_t* index, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The attention side of a block: what lies between the q || k || v call and
+ * the o call ("Hesper.Layers.TransformerBlock" page: attention with rotary
+ * positions and a key-value cache; "Hesper.Models.BitNet" page, section
+ * "Configuration": ropeBase, kvDim = numKVHeads * headDim, and "KV cache").
+ *
+ * Rows are fp32, one per token, a row holding its heads side by side (head h
+ * at h * head_dim), rows `stride` floats apart; a stride is a multiple of 4
+ * and at least heads * head_dim, so a slice of a wider row (a q || k || v
+ * buffer) is taken as it is.
+ *
+ * The cache is paged.  Token `pos` of sequence s lies in page
+ * page_table[s * table_stride + pos / page_size], at pos % page_size.  Several
+ * sequences may name one page (a shared prompt), table_stride may be 0 (every
+ * row uses one list of pages), and a page number out of range is no fault:
+ * what it would hold is skipped (written nowhere, read nowhere, masked).
+ * ------------------------------------------------------------------------- */
+
+enum {
+  BITLINEAR_KV_INT8 = 0, /* int8 codes and one fp32 step per (token, head) */
+  BITLINEAR_KV_FP8 = 1,  /* e4m3 codes and one fp32 step per (token, head) */
+  BITLINEAR_KV_BF16 = 2  /* bf16 values, no steps */
+};
+
+/* A paged key-value cache in caller-owned device memory. */
+typedef struct bitlinear_kv_pages {
+  void* k;           /* device, [num_pages, num_heads, page_size, head_dim] codes, 16-byte aligned */
+  void* v;           /* the same for the values */
+  float* k_step;     /* device fp32 [num_pages, num_heads, page_size], 16-byte aligned: a key is */
+  float* v_step;     /* code * step; ignored (may be NULL) for BITLINEAR_KV_BF16 */
+  int64_t num_pages; /* 1 .. 2^31 - 1; fewer than 2^48 codes in all */
+  int32_t num_heads; /* key / value heads, 1 .. 4096 */
+  int32_t page_size; /* tokens a page: a power of two, 16 .. 4096 */
+  int32_t head_dim;  /* a multiple of 16, 16 .. 256 */
+  int32_t format;    /* BITLINEAR_KV_* */
+} bitlinear_kv_pages;
+
+enum {
+  BITLINEAR_ROPE_HALF = 0,       /* pair i of a head is (i, i + rot_dim / 2) */
+  BITLINEAR_ROPE_INTERLEAVED = 1 /* pair i of a head is (2i, 2i + 1) */
+};
+
+/* How a rotation is made: the first rot_dim dims of every head turn, the rest
+ * stay.  Pair i = (a, b) at position p becomes
+ *   (a * c - b * s, b * c + a * s),  c, s = amplitude * cos, sin(p * freq[i])
+ * with the angle in fp64, its sine and cosine rounded once to fp32, and each
+ * product and sum of the pair rounded in fp32. */
+typedef struct bitlinear_rope_spec {
+  const double* freq; /* device fp64 [rot_dim / 2]: radians per position, 8-byte aligned */
+  int32_t rot_dim;    /* even, 2 .. head_dim */
+  int32_t layout;     /* BITLINEAR_ROPE_HALF or BITLINEAR_ROPE_INTERLEAVED */
+  float amplitude;    /* 1 unless a long-context scaling asks for more */
+} bitlinear_rope_spec;
+
+enum {
+  BITLINEAR_ROPE_SCALE_NONE = 0,   /* theta_i = base^(-2i / rot_dim) */
+  BITLINEAR_ROPE_SCALE_LINEAR = 1, /* theta_i / factor: positions squeezed into the trained range */
+  BITLINEAR_ROPE_SCALE_BASE = 2,   /* base * factor^(rot_dim / (rot_dim - 2)) in place of base: the
+                                      slowest pair is stretched by factor, the fastest stays */
+  BITLINEAR_ROPE_SCALE_PARTS = 3   /* by parts: theta_i * (g + (1 - g) / factor) with g = clamp((r -
+                                      low) / (high - low), 0, 1) and r = original_length * theta_i / 2 pi,
+                                      the turns of the pair within the trained length */
+};
+
+/* The frequencies of rot_dim / 2 pairs, into freq_host (host memory; the caller
+ * copies them to the device once).  base > 0 (10000 in the page's configuration);
+ * factor > 0; original_length > 0 and high > low only matter by parts.
+ * Errors: BITLINEAR_ERR_NULL, BITLINEAR_ERR_SHAPE (rot_dim odd, below 2 or above
+ * 256; a value that is not finite or out of its range; SCALE_BASE with
+ * rot_dim == 2), BITLINEAR_ERR_UNSUPPORTED (unknown scaling). */
+bitlinear_status bitlinear_rope_frequencies(int rot_dim, double base, int scaling, double factor,
+                                            double original_length, double low, double high, double* freq_host);
+
+/* Rotary positions: y[t, h] = x[t, h] rotated to positions[t].
+ *   x, y       device fp32, T rows of H heads of D dims; y may be x (equal strides),
+ *              and must not overlap it otherwise.
+ *   T, H, D    T >= 0 (0 enqueues nothing), H 1 .. 4096, D a multiple of 4, 4 .. 256.
+ *   positions  device int32 [T].  A negative position turns the other way: rows
+ *              rotated to p and then to -p are the rows again (and a gradient of
+ *              y comes back to x so), up to rounding and amplitude^2.
+ *   flags      BITLINEAR_FLAG_PDL or 0: launched with programmatic dependent
+ *              launch; every read follows the wait for the kernel before.
+ * Errors: BITLINEAR_ERR_NULL, BITLINEAR_ERR_SHAPE, BITLINEAR_ERR_ALIGN (rows 16
+ * bytes, positions 4, freq 8), BITLINEAR_ERR_UNSUPPORTED (layout, flag),
+ * BITLINEAR_ERR_CUDA. */
+bitlinear_status bitlinear_rope(const float* x, int64_t x_stride, int64_t T, int H, int D,
+                                const int32_t* positions, const bitlinear_rope_spec* rope, float* y,
+                                int64_t y_stride, int flags, void* stream);
+
+/* Writes new tokens into the cache, in one launch: q and k are rotated, q goes
+ * to q_out, k and v are quantised as they are written.
+ *   q, q_out   device fp32, T rows of num_q_heads heads, or both NULL
+ *              (num_q_heads 0); q_out may be q (equal strides).
+ *   k, v       device fp32, T rows of cache->num_heads heads.
+ *   T          rows, >= 0 (0 enqueues nothing).
+ *   positions  device int32 [T]: each row's place in its sequence, and its angle.
+ *   seq        device int32 [T]: each row's sequence, or NULL: row i is of
+ *              sequence i (then T <= num_seqs).
+ *   page_table device int32, num_seqs rows of max_pages page numbers, table_stride
+ *              apart (>= max_pages, or 0).
+ *   rope       NULL: q and k are not rotated (q is copied).
+ * A row's (token, head) is quantised as bitlinear_quant_act does a token, with the
+ * step kept in place of the scale: a = max(max|x|, 1e-5); int8 code = clamp(rne(x *
+ * s), -128, 127) with s = 127 * (1 / a) and step = a / 127; e4m3 code = x * s to the
+ * nearest, ties to even, with s = 448 * (1 / a) and step = a / 448, every step in
+ * fp32; bf16 to the nearest, ties to even.
+ * A row without a place -- a negative position (padding), a sequence, page column
+ * or page number out of range -- is skipped, its q_out row included; every other
+ * row of the cache stays as it was.  Two rows of one call with the same place
+ * leave that place with codes and steps of either or both.
+ * Errors: as bitlinear_rope; also BITLINEAR_ERR_SHAPE for a cache outside the
+ * limits above. */
+bitlinear_status bitlinear_kv_append(const float* q, int64_t q_stride, int num_q_heads, float* q_out,
+                                     int64_t q_out_stride, const float* k, int64_t k_stride, const float* v,
+                                     int64_t v_stride, int64_t T, const int32_t* positions, const int32_t* seq,
+                                     const int32_t* page_table, int64_t table_stride, int64_t num_seqs,
+                                     int64_t max_pages, const bitlinear_rope_spec* rope,
+                                     const bitlinear_kv_pages* cache, int flags, void* stream);
+
+/* Reads rows of the cache back: row i of k_out and v_out (device fp32, T rows of
+ * cache->num_heads heads) receives code * step (one fp32 product) of the key and
+ * value at (seq[i], positions[i]), the places of bitlinear_kv_append.  The rows
+ * of k_out and v_out whose place does not exist are left as they were.
+ * Errors: as bitlinear_kv_append. */
+bitlinear_status bitlinear_kv_read(const bitlinear_kv_pages* cache, int64_t T, const int32_t* positions,
+                                   const int32_t* seq, const int32_t* page_table, int64_t table_stride,
+                                   int64_t num_seqs, int64_t max_pages, float* k_out, int64_t k_stride,
+                                   float* v_out, int64_t v_stride, int flags, void* stream);
+
+/* Workspace bytes that let bitlinear_attention split its sequences further (0
+ * where no split beyond one launch's is ever taken, and for sizes out of range). */
+size_t bitlinear_attention_workspace(int64_t B, int num_q_heads, int num_kv_heads, int head_dim);
+
+/* Attention of one new token per sequence over its cached tokens:
+ *   out[b, h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q[b, h] . k_t)
+ * over tokens t of sequence b, max(0, lengths[b] - window) <= t < lengths[b]
+ * (every t < lengths[b] when window is 0), keys and values those of the key head
+ * h / (num_q_heads / cache->num_heads).
+ *   q, out     device fp32, B rows of num_q_heads heads (a multiple of
+ *              cache->num_heads, at most 4096); out must not overlap q.
+ *   B          sequences, >= 0 (0 enqueues nothing).
+ *   page_table device int32, B rows of max_pages page numbers, table_stride apart
+ *              (>= max_pages, or 0).
+ *   lengths    device int32 [B], the new token included (append it first).  A length
+ *              past max_pages * page_size counts as that; one of 0 or below, or one
+ *              whose every page is out of range, gives a row of zeros.
+ *   window     0, or the number of last tokens that count (> 0).
+ *   scale      finite; 1 / sqrt(head_dim) in most models.
+ *   workspace  device, 16-byte aligned, at least bitlinear_attention_workspace()
+ *              bytes, contents irrelevant, not shared with a call that may run at the
+ *              same time; or NULL: very long sequences of few heads run slower.
+ * Nothing past a row's length is read.  Results do not depend on timing: the parts of
+ * a split sequence are joined in a fixed order.
+ * Several rows may attend to one sequence (rows of one page list with lengths n,
+ * n + 1, ...: the causal rows of a prompt's end).
+ * Errors: as bitlinear_kv_append; BITLINEAR_ERR_WORKSPACE for a workspace that is too
+ * small. */
+bitlinear_status bitlinear_attention(const float* q, int64_t q_stride, int64_t B, int num_q_heads,
+                                     const bitlinear_kv_pages* cache, const int32_t* page_table,
+                                     int64_t table_stride, int64_t max_pages, const int32_t* lengths,
+                                     int64_t window, float scale, float* out, int64_t out_stride,
+                                     void* workspace, size_t workspace_bytes, int flags, void* stream);
+
 /* Exercises the failure-detection path without faulting anything: launches a
  * one-warp kernel that waits on an mbarrier nothing ever arrives on, with the
  * same bounded wait the kernels use, giving up after limit_ns (0 < limit_ns
