@@ -1,109 +1,650 @@
 // attention.cu -- attention of one new token over the paged key-value cache.
 //
-//   out[b, h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q[b, h] . k_t - m)
-// over the tokens t of sequence b that its length and the window leave, m the
-// running maximum of the logits: one pass over keys and values.
+//   out[b, h] = sum_t p_t v_t / sum_t p_t,  p_t = 2^(x_t - m),  x_t = log2(e) scale q[b, h] . k_t
+// over the tokens t of sequence b that its length and the window leave, in one
+// pass over keys and values with a running m, sum and weighted sum.
 //
-// One CTA per (sequence, q head); its warps take every fourth token and a lane
-// holds every 32nd dim; the warps' (m, sum, weighted sum) meet in shared memory.
+// One CTA takes a run of tokens of one key head of one sequence, for up to 8 of
+// the q heads that share it; the runs of a sequence are the CTAs of one
+// thread-block cluster and join through distributed shared memory, in the order
+// of the runs.  Inside a CTA a warp works alone: it streams its own steps of
+// tokens (every kWarps-th step of the run) through a ring of shared-memory stages
+// with asynchronous copies, so no barrier stands between copy and use.
+//
+// Both products run on the warp-level MMA (m16n8k16, fp32 sums) whatever the
+// number of q heads: a cache is bound by its bytes, and the MMA takes a token's
+// key in fewer instructions than fp32 arithmetic on widened codes (one widening
+// per code, no multiply-add; 8 q heads cost what one does).  Its 16 rows carry the
+// 8 heads twice: rows 0-7 the leading parts of q (or p), rows 8-15 what they leave.
+//   8-bit codes are exact in fp16; q and p are split into two fp16 parts (22 bits,
+//   the second scaled by 2^11), q after scaling each head's row by a power of two.
+//   bf16 values are used as they are; q and p are split into three bf16 parts (24
+//   bits), the third in a second MMA.
+// So a logit and a weighted sum keep fp32 accuracy.  The key's step multiplies the
+// logit, the value's step multiplies p.
+//
+// Lazy references: m (per head) moves only when some logit exceeds it by 8, so p
+// stays at or below 2^8, and p times the value's step is scaled by a power of two
+// that moves the same way, so its fp16 parts keep their bits whatever the steps are.
+// The MMA sums of a step (16 or 32 tokens) start from zero and are added to fp32
+// sums in registers: a chain of roundings no longer than the steps of a warp.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "kv.cuh"
 
 namespace bitlinear {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxHead = 256;
-constexpr int kLaneDims = kMaxHead / 32;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRowHeads = 8;   // q heads of one CTA
+constexpr int kStages = 3;
+constexpr int kMaxCluster = 8;
+constexpr float kLazy = 8.0f;  // how far a logit (base 2) may exceed its reference
+
+// Sizes of one instantiation: DT dims a head (a smaller head_dim is padded with
+// zeros), codes of kBytes, steps of kTokens tokens.
+template <int FORMAT, int DT>
+struct Shape {
+  static constexpr int kBytes = FORMAT == BITLINEAR_KV_BF16 ? 2 : 1;
+  static constexpr int kRow = DT * kBytes;
+  // rows an odd number of 16-byte chunks apart: the fragments' loads (8 rows x 4
+  // words, or 4 pairs of rows x 8 words) then touch every bank once
+  static constexpr int kPitch = (kRow / 16) % 2 ? kRow : kRow + 16;
+  static constexpr int kTokens = kRow <= 128 ? 32 : 16;
+  static constexpr int kTiles = kTokens / 8;       // n-tiles of the logits
+  static constexpr int kSteps = DT / 16;           // k-steps of the logits
+  static constexpr int kChunks = kRow / 16;
+  static constexpr int kOutTiles = DT / 8;         // n-tiles of the weighted sums
+  static constexpr int kStage = 2 * kTokens * kPitch + 2 * kTokens * 4;
+  static constexpr int kWarpBytes = kStages * kStage;
+  static constexpr int kPartial = (DT + 4) * 4;    // a head's weighted sum, m and sum, padded to 16 bytes
+  static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes;
+  static_assert(kRowHeads * kPartial <= kWarpBytes, "a warp's partials reuse its ring");
+  static_assert(kStage % 16 == 0 && DT % 16 == 0, "");
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 lds_float2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+// A float of CTA `rank` of the cluster, at the address that `a` has in this CTA.
+__device__ __forceinline__ float lds_cluster(uint32_t a, int rank) {
+  uint32_t r;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float exp2_of(float x) {  // relative error 2^-22, 0 below -126
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^e for |e| <= 126, and the exponent of a positive normal x.
+__device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+__device__ __forceinline__ int clamp_exponent(int e) { return max(-100, min(100, e)); }
 
 template <int FORMAT>
-__device__ __forceinline__ float value_at(const void* codes, int64_t i) {
-  if constexpr (FORMAT == BITLINEAR_KV_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(codes)[i]);
-  if constexpr (FORMAT == BITLINEAR_KV_INT8) return (float)static_cast<const int8_t*>(codes)[i];
-  return __half2float(__ushort_as_half((unsigned short)half2_of_e4m3x2(static_cast<const uint8_t*>(codes)[i])));
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (FORMAT == BITLINEAR_KV_BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The bytes `pair` selects of two code words, widened to two halves.  int8 codes
+// come with their sign bit flipped (excess 128): 0x6400 | u is the half 1024 + u.
+__device__ __forceinline__ uint32_t halves_of_int8(uint32_t w, uint32_t selector) {
+  const uint32_t u = __byte_perm(w, 0x64646464u, selector);
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int FORMAT>
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {  // bytes 0, 1 and 2, 3
+  if constexpr (FORMAT == BITLINEAR_KV_INT8) {
+    w ^= 0x80808080u;
+    lo = halves_of_int8(w, 0x4140);
+    hi = halves_of_int8(w, 0x4342);
+  } else {
+    lo = half2_of_e4m3x2((uint16_t)w);
+    hi = half2_of_e4m3x2((uint16_t)(w >> 16));
+  }
+}
+
+// x, y as leading parts and what they leave, the latter times 2^11 (fp16).
+__device__ __forceinline__ void split2(float x, float y, uint32_t& lead, uint32_t& rest) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const __half2 r = __floats2half2_rn((x - __low2float(h)) * 2048.0f, (y - __high2float(h)) * 2048.0f);
+  lead = *reinterpret_cast<const uint32_t*>(&h);
+  rest = *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t next_part(float& x, float& y) {  // bf16 parts, taken off x and y
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  x -= __low2float(h);
+  y -= __high2float(h);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The run of one CTA and what it needs to know of its sequence.
+struct Run {
+  const int32_t* table;    // the sequence's pages
+  const uint8_t *k, *v;    // the key head's first page row (page 0)
+  const float *ks, *vs;
+  int64_t first, len;      // tokens first <= t < len count
+  int64_t u0;              // the warp's first step (in steps of kTokens tokens)
+};
+
+// Requests one step's keys, values and steps into a stage; the low bits of the
+// result say which 16-token halves have a page.  Rows that do not count are zeroed.
+template <int FORMAT, int DT>
+__device__ __forceinline__ uint32_t request(const Run& r, const KvPages& c, int64_t t0, const int32_t (&page)[2],
+                                            uint32_t stage, int lane) {
+  using S = Shape<FORMAT, DT>;
+  constexpr int kHalves = S::kTokens / 16;
+  const int row_bytes = c.head_dim * S::kBytes, chunks = row_bytes / 16;
+  uint32_t ok = 0;
+#pragma unroll
+  for (int s = 0; s < kHalves; ++s) {
+    const int64_t t = t0 + 16 * s;
+    const bool have = t < r.len && page[s] >= 0 && page[s] < c.num_pages;
+    ok |= have ? 1u << s : 0u;
+    const int64_t row = have ? (((int64_t)page[s] * c.heads) << c.page_shift) + (t & ((1 << c.page_shift) - 1)) : 0;
+    const uint8_t* ks = r.k + row * row_bytes;
+    const uint8_t* vs = r.v + row * row_bytes;
+    const uint32_t kd = stage + 16 * s * S::kPitch, vd = kd + S::kTokens * S::kPitch;
+#pragma unroll
+    for (int j = 0; j < (16 * S::kChunks + 31) / 32; ++j) {
+      const int i = lane + 32 * j, n = i / S::kChunks, ch = i % S::kChunks;
+      if (n < 16 && ch < chunks) {
+        const bool there = have && t + n >= r.first && t + n < r.len;
+        const int64_t off = there ? (int64_t)n * row_bytes + 16 * ch : 0;
+        copy16(kd + n * S::kPitch + 16 * ch, ks + off, there);
+        copy16(vd + n * S::kPitch + 16 * ch, vs + off, there);
+      }
+    }
+    if constexpr (FORMAT != BITLINEAR_KV_BF16) {
+      const int n = lane & 15;
+      const bool there = have && t + n >= r.first && t + n < r.len;
+      const uint32_t sd = stage + 2 * S::kTokens * S::kPitch + (lane >> 4) * S::kTokens * 4 + (16 * s + n) * 4;
+      copy4(sd, (lane < 16 ? r.ks : r.vs) + row + (there ? n : 0), there);
+    }
+  }
+  return ok;
+}
+
+// Joins `parts` partials of one head's dim d: part i is at base + i * apart (its
+// dims, then m and the sum) of this CTA, or of CTA i of the cluster.
+struct Joined {
+  float value, m, sum;
+};
+template <bool CLUSTER>
+__device__ __forceinline__ Joined join(uint32_t base, uint32_t apart, int parts, int d, int dims) {
+  Joined j = {0.0f, -INFINITY, 0.0f};
+  auto at = [&](int i, int f) {
+    float v;
+    if constexpr (CLUSTER) return lds_cluster(base + 4 * f, i);
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(base + i * apart + 4 * f));
+    return v;
+  };
+  for (int i = 0; i < parts; ++i) j.m = fmaxf(j.m, at(i, dims));
+  if (j.m == -INFINITY) return j;
+  for (int i = 0; i < parts; ++i) {
+    const float f = exp2_of(at(i, dims) - j.m);
+    j.sum = fmaf(at(i, dims + 1), f, j.sum);
+    j.value = fmaf(at(i, d), f, j.value);
+  }
+  return j;
+}
+
+template <int FORMAT, int DT>
+__global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages c, int64_t b0, int splits) {
+  using S = Shape<FORMAT, DT>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  pdl_release_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
+  const int group = a.q_heads / c.heads, groups = (group + kRowHeads - 1) / kRowHeads;
+  const int split = blockIdx.x % splits;
+  int64_t rest = blockIdx.x / splits;
+  const int first_of_group = (int)(rest % groups) * kRowHeads;
+  rest /= groups;
+  const int hk = (int)(rest % c.heads);
+  const int64_t b = b0 + rest / c.heads;
+  const int heads = min(kRowHeads, group - first_of_group), hq = hk * group + first_of_group;
+  const int D = c.head_dim;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * S::kWarpBytes;
+  if (D < DT) {  // the padding of every row, once: copies never write it
+    for (int i = lane; i < S::kWarpBytes / 16; i += 32)
+      reinterpret_cast<uint4*>(smem + warp * S::kWarpBytes)[i] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+  }
+  pdl_wait_primary();
+
+  Run r;
+  const int64_t most = a.max_pages << c.page_shift;
+  r.len = a.lengths[b];
+  r.len = r.len < most ? r.len : most;
+  r.first = a.window > 0 && r.len > a.window ? r.len - a.window : 0;
+  r.table = a.table + b * a.table_stride;
+  const int64_t head_row = (int64_t)hk << c.page_shift;
+  r.k = static_cast<const uint8_t*>(c.k) + head_row * D * S::kBytes;
+  r.v = static_cast<const uint8_t*>(c.v) + head_row * D * S::kBytes;
+  r.ks = c.k_step + head_row;
+  r.vs = c.v_step + head_row;
+  const int64_t begin = r.first / S::kTokens;
+  const int64_t units = r.len > r.first ? (r.len + S::kTokens - 1) / S::kTokens - begin : 0;
+  const int64_t share = (units + splits - 1) / splits;
+  const int64_t u1 = min(units, (split + 1) * share);
+  r.u0 = split * share + warp;
+  const int64_t mine = u1 > r.u0 ? (u1 - r.u0 + kWarps - 1) / kWarps : 0;  // steps of this warp
+
+  int32_t page[2] = {-1, -1};
+  auto token_of = [&](int64_t i) { return (begin + r.u0 + i * kWarps) * S::kTokens; };
+  auto look_up = [&](int64_t i) {
+    const int64_t t = token_of(i);
+    page[0] = i < mine && t < r.len ? r.table[t >> c.page_shift] : -1;
+    if constexpr (S::kTokens == 32) page[1] = i < mine && t + 16 < r.len ? r.table[(t + 16) >> c.page_shift] : -1;
+  };
+  uint32_t oks = 0;  // two bits a requested step, the newest lowest
+  auto ask = [&](int64_t i) {
+    oks <<= 2;
+    if (i < mine) oks |= request<FORMAT, DT>(r, c, token_of(i), page, ring + (uint32_t)(i % kStages) * S::kStage, lane);
+    copies_commit();
+  };
+  look_up(0);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    ask(i);
+    look_up(i + 1);
+  }
+
+  // q as the MMA's A operand: rows g the leading parts of head g, rows g + 8 the
+  // next, the dims of a k-step in the order the key words give them.
+  constexpr bool kBf16 = FORMAT == BITLINEAR_KV_BF16;
+  uint32_t qa[S::kSteps][4], qb[kBf16 ? S::kSteps : 1][2];
+  float row_scale = 1.0f;
+  {
+    const float* q = a.q + b * a.q_stride + (int64_t)(hq + min(g, heads - 1)) * D;
+    const float factor = a.scale * 1.44269504088896341f;
+    float v[S::kSteps][4], top = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S::kSteps; ++s) {
+      // 8-bit: dims 4 qd .. 4 qd + 3 of the k-step (one word); bf16: dims 2 qd, 2 qd + 1 and 8 more
+      const int d0 = 16 * s + (kBf16 ? 2 : 4) * qd, d1 = kBf16 ? d0 + 8 : d0 + 2;
+      const float2 x = d0 < D ? *reinterpret_cast<const float2*>(q + d0) : make_float2(0.0f, 0.0f);
+      const float2 y = d1 < D ? *reinterpret_cast<const float2*>(q + d1) : make_float2(0.0f, 0.0f);
+      v[s][0] = x.x * factor; v[s][1] = x.y * factor; v[s][2] = y.x * factor; v[s][3] = y.y * factor;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = fmaxf(top, fabsf(v[s][j]));
+    }
+    if constexpr (!kBf16) {
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+      const int e = clamp_exponent(exponent_of(top));
+      row_scale = power2(e);
+      const float down = power2(-e);
+#pragma unroll
+      for (int s = 0; s < S::kSteps; ++s) {
+        split2(v[s][0] * down, v[s][1] * down, qa[s][0], qa[s][1]);
+        split2(v[s][2] * down, v[s][3] * down, qa[s][2], qa[s][3]);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < S::kSteps; ++s) {
+        qa[s][0] = next_part(v[s][0], v[s][1]); qa[s][1] = next_part(v[s][0], v[s][1]); qb[s][0] = next_part(v[s][0], v[s][1]);
+        qa[s][2] = next_part(v[s][2], v[s][3]); qa[s][3] = next_part(v[s][2], v[s][3]); qb[s][1] = next_part(v[s][2], v[s][3]);
+      }
+    }
+  }
+
+  float m = -INFINITY, sum = 0.0f;                     // of row g; the sum over this lane's tokens
+  float up = 1.0f, limit = kBf16 ? INFINITY : 0.0f;    // the power of two on p * step, and when it moves
+  float out[S::kOutTiles][2];                          // row g: dims 2 qd, 2 qd + 1 of every n-tile (in the tiles' order)
+#pragma unroll
+  for (int n = 0; n < S::kOutTiles; ++n) out[n][0] = out[n][1] = 0.0f;
+  constexpr float kRest = kBf16 ? 1.0f : 1.0f / 2048.0f;
+
+  for (int64_t i = 0; i < mine; ++i) {
+    copies_wait<kStages - 2>();
+    __syncwarp();  // every lane's copies of step i, and every lane is done with the stage before
+    ask(i + kStages - 1);
+    look_up(i + kStages);
+    const uint32_t st = ring + (uint32_t)(i % kStages) * S::kStage;
+    const uint32_t vst = st + S::kTokens * S::kPitch, kst = vst + S::kTokens * S::kPitch;
+    const uint32_t ok = (oks >> (2 * (kStages - 1))) & 3u;
+    const int64_t t0 = token_of(i);
+
+    float x[S::kTiles][4];
+#pragma unroll
+    for (int j = 0; j < S::kTiles; ++j) x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S::kSteps; ++s)
+#pragma unroll
+      for (int j = 0; j < S::kTiles; ++j) {
+        uint32_t k0, k1;
+        const uint32_t row = st + (8 * j + g) * S::kPitch + 16 * s * S::kBytes + 4 * qd;
+        if constexpr (kBf16) {
+          k0 = lds32(row);
+          k1 = lds32(row + 16);
+          mma<FORMAT>(x[j], qa[s], k0, k1);
+          const uint32_t third[4] = {qb[s][0], 0u, qb[s][1], 0u};
+          mma<FORMAT>(x[j], third, k0, k1);
+        } else {
+          widen<FORMAT>(lds32(row), k0, k1);
+          mma<FORMAT>(x[j], qa[s], k0, k1);
+        }
+      }
+
+    // logits of row g, tokens 8 j + 2 qd and the next
+    float2 lg[S::kTiles];
+    float top = -INFINITY;
+    const bool whole = ok == (S::kTokens == 32 ? 3u : 1u) && t0 >= r.first && t0 + S::kTokens <= r.len;
+#pragma unroll
+    for (int j = 0; j < S::kTiles; ++j) {
+      lg[j].x = fmaf(x[j][2], kRest, x[j][0]);
+      lg[j].y = fmaf(x[j][3], kRest, x[j][1]);
+      if constexpr (!kBf16) {
+        const float2 step = lds_float2(kst + (8 * j + 2 * qd) * 4);
+        lg[j].x *= row_scale * step.x;
+        lg[j].y *= row_scale * step.y;
+      }
+      if (!whole) {
+        const int64_t t = t0 + 8 * j + 2 * qd;
+        const bool have = (ok >> (j / 2)) & 1u;
+        if (!have || t < r.first || t >= r.len) lg[j].x = -INFINITY;
+        if (!have || t + 1 < r.first || t + 1 >= r.len) lg[j].y = -INFINITY;
+      }
+      top = fmaxf(top, fmaxf(lg[j].x, lg[j].y));
+    }
+    if (__any_sync(kFullMask, top > m + kLazy)) {
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+      if (top > m + kLazy) {
+        const float f = exp2_of(m - top);  // 0 from the first reference
+        m = top;
+        sum *= f;
+#pragma unroll
+        for (int n = 0; n < S::kOutTiles; ++n) {
+          out[n][0] *= f;
+          out[n][1] *= f;
+        }
+      }
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float high = 0.0f;
+#pragma unroll
+    for (int j = 0; j < S::kTiles; ++j) {
+      lg[j].x = exp2_of(lg[j].x - ref);
+      lg[j].y = exp2_of(lg[j].y - ref);
+      sum += lg[j].x + lg[j].y;
+      if constexpr (!kBf16) {
+        const float2 step = lds_float2(kst + (S::kTokens + 8 * j + 2 * qd) * 4);
+        lg[j].x *= step.x;
+        lg[j].y *= step.y;
+        high = fmaxf(high, fmaxf(lg[j].x, lg[j].y));
+      }
+    }
+    if constexpr (!kBf16) {
+      if (__any_sync(kFullMask, high > limit)) {
+        high = fmaxf(high, __shfl_xor_sync(kFullMask, high, 1));
+        high = fmaxf(high, __shfl_xor_sync(kFullMask, high, 2));
+        if (high > limit) {
+          const int e = clamp_exponent(exponent_of(high));
+          const float to = power2(-e), f = to / up;
+          if (limit > 0.0f) {
+#pragma unroll
+            for (int n = 0; n < S::kOutTiles; ++n) {
+              out[n][0] *= f;
+              out[n][1] *= f;
+            }
+          }
+          up = to;
+          limit = power2(e + 8);
+        }
+      }
+    }
+
+    // p (times the step and `up`) as the A operand: token pairs of tiles 2 kk, 2 kk + 1
+    uint32_t pa[S::kTokens / 16][4], pb[kBf16 ? S::kTokens / 16 : 1][2];
+#pragma unroll
+    for (int kk = 0; kk < S::kTokens / 16; ++kk) {
+      if constexpr (kBf16) {
+        pa[kk][0] = next_part(lg[2 * kk].x, lg[2 * kk].y);
+        pa[kk][1] = next_part(lg[2 * kk].x, lg[2 * kk].y);
+        pb[kk][0] = next_part(lg[2 * kk].x, lg[2 * kk].y);
+        pa[kk][2] = next_part(lg[2 * kk + 1].x, lg[2 * kk + 1].y);
+        pa[kk][3] = next_part(lg[2 * kk + 1].x, lg[2 * kk + 1].y);
+        pb[kk][1] = next_part(lg[2 * kk + 1].x, lg[2 * kk + 1].y);
+      } else {
+        split2(lg[2 * kk].x * up, lg[2 * kk].y * up, pa[kk][0], pa[kk][1]);
+        split2(lg[2 * kk + 1].x * up, lg[2 * kk + 1].y * up, pa[kk][2], pa[kk][3]);
+      }
+    }
+
+    // weighted sums: a word of 4 tokens gives the B operands of as many n-tiles as it
+    // holds dims; n-tile i of a group takes dim (dims a word) * g + i
+    constexpr int kWide = kBf16 ? 2 : 4;             // dims a word
+    constexpr int kGroups = DT / (8 * kWide);
+    auto add = [&](int n, const float (&t)[4]) {
+      out[n][0] += fmaf(t[2], kRest, t[0]);
+      out[n][1] += fmaf(t[3], kRest, t[1]);
+    };
+#pragma unroll
+    for (int dg = 0; dg < kGroups; ++dg) {
+      float t[kWide][4];
+#pragma unroll
+      for (int n = 0; n < kWide; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < S::kTokens / 16; ++kk) {
+        const uint32_t row = vst + (16 * kk + 2 * qd) * S::kPitch + 32 * dg + 4 * g;
+        uint32_t w[4] = {lds32(row), lds32(row + S::kPitch), lds32(row + 8 * S::kPitch), lds32(row + 9 * S::kPitch)};
+        if constexpr (kBf16) {
+          const uint32_t third[4] = {pb[kk][0], 0u, pb[kk][1], 0u};
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t sel = n ? 0x7632 : 0x5410;
+            const uint32_t v0 = __byte_perm(w[0], w[1], sel), v1 = __byte_perm(w[2], w[3], sel);
+            mma<FORMAT>(t[n], pa[kk], v0, v1);
+            mma<FORMAT>(t[n], third, v0, v1);
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < 4; n += 2) {
+            uint32_t v0[2], v1[2];  // bytes n, n + 1 of both tokens of a pair, side by side
+            widen<FORMAT>(__byte_perm(w[0], w[1], n ? 0x7362 : 0x5140), v0[0], v0[1]);
+            widen<FORMAT>(__byte_perm(w[2], w[3], n ? 0x7362 : 0x5140), v1[0], v1[1]);
+            mma<FORMAT>(t[n], pa[kk], v0[0], v1[0]);
+            mma<FORMAT>(t[n + 1], pa[kk], v0[1], v1[1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < kWide; ++n) add(kWide * dg + n, t[n]);
+    }
+    if constexpr (!kBf16 && DT % 32 == 16) {  // the last 16 dims: two a token, n-tile i takes dim 2 g + i
+      constexpr int n0 = S::kOutTiles - 2;
+      float t[2][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < S::kTokens / 16; ++kk) {
+        const uint32_t row = vst + (16 * kk + 2 * qd) * S::kPitch + (DT - 16) + 2 * g;
+        const uint32_t w0 = lds16(row), w1 = lds16(row + S::kPitch), w2 = lds16(row + 8 * S::kPitch), w3 = lds16(row + 9 * S::kPitch);
+        uint32_t v0[2], v1[2];
+        widen<FORMAT>(__byte_perm(w0, w1, 0x5140), v0[0], v0[1]);
+        widen<FORMAT>(__byte_perm(w2, w3, 0x5140), v1[0], v1[1]);
+        mma<FORMAT>(t[0], pa[kk], v0[0], v1[0]);
+        mma<FORMAT>(t[1], pa[kk], v0[1], v1[1]);
+      }
+      add(n0, t[0]);
+      add(n0 + 1, t[1]);
+    }
+  }
+  copies_wait<0>();
+  __syncwarp();
+
+  // The warp's partials over its ring: [head][dims, m, sum].
+  sum += __shfl_xor_sync(kFullMask, sum, 1);
+  sum += __shfl_xor_sync(kFullMask, sum, 2);
+  float* part = reinterpret_cast<float*>(smem + warp * S::kWarpBytes + g * S::kPartial);
+  const float back = kBf16 ? 1.0f : 1.0f / up;  // a power of two
+  constexpr int kWideOut = kBf16 ? 2 : 4;
+#pragma unroll
+  for (int n = 0; n < S::kOutTiles; ++n) {
+    const bool tail = !kBf16 && DT % 32 == 16 && n >= S::kOutTiles - 2;
+    const int wide = tail ? 2 : kWideOut, first = tail ? DT - 16 : n / kWideOut * 8 * kWideOut;
+    const int of = tail ? n - (S::kOutTiles - 2) : n % kWideOut;
+    part[first + wide * (2 * qd) + of] = out[n][0] * back;
+    part[first + wide * (2 * qd + 1) + of] = out[n][1] * back;
+  }
+  if (qd == 0) {
+    part[DT] = m;
+    part[DT + 1] = sum;
+  }
+  __syncthreads();
+
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+  float* dst = a.out + b * a.out_stride + (int64_t)hq * D;
+  if (splits == 1) {
+    for (int i = threadIdx.x; i < heads * D; i += kThreads) {
+      const int h = i / D, d = i - h * D;
+      const Joined j = join<false>(base + h * S::kPartial, S::kWarpBytes, kWarps, d, DT);
+      dst[i] = j.sum > 0.0f ? j.value / j.sum : 0.0f;  // no token: zeros
+    }
+    return;
+  }
+  // The CTA's own partials first (kept in registers across the barrier: the
+  // warps' partials share their memory), then the cluster's.
+  constexpr int kMine = (kRowHeads * DT + kThreads - 1) / kThreads;
+  Joined own[kMine];
+#pragma unroll
+  for (int n = 0; n < kMine; ++n) {
+    const int i = threadIdx.x + n * kThreads;
+    if (i < heads * DT) own[n] = join<false>(base + i / DT * S::kPartial, S::kWarpBytes, kWarps, i % DT, DT);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < kMine; ++n) {
+    const int i = threadIdx.x + n * kThreads;
+    if (i >= heads * DT) continue;
+    float* p = reinterpret_cast<float*>(smem + i / DT * S::kPartial);
+    p[i % DT] = own[n].value;
+    if (i % DT == 0) {
+      p[DT] = own[n].m;
+      p[DT + 1] = own[n].sum;
+    }
+  }
+  cluster_sync();
+  for (int i = split * kThreads + threadIdx.x; i < heads * D; i += splits * kThreads) {
+    const int h = i / D, d = i - h * D;
+    const Joined j = join<true>(base + h * S::kPartial, 0, splits, d, DT);
+    dst[i] = j.sum > 0.0f ? j.value / j.sum : 0.0f;
+  }
+  cluster_sync();  // no CTA leaves while another reads its partials
+}
+
+// Runs a sequence is split into: a power of two up to kMaxCluster, while the CTAs
+// stay within two an SM and every run may hold a step for each warp.
+int splits_for(int64_t rows, int64_t units, const DeviceInfo& dev) {
+  int s = 1;
+  while (s < kMaxCluster && rows * s * 2 <= 2 * (int64_t)dev.num_sms && units >= 2 * s * kWarps) s *= 2;
+  return s;
+}
+
+template <int FORMAT, int DT>
+cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, bool pdl, const DeviceInfo& dev, cudaStream_t stream) {
+  using S = Shape<FORMAT, DT>;
+  const auto kernel = attend_kernel<FORMAT, DT>;
+  static thread_local int configured_device = -1;
+  if (configured_device != dev.device) {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    if (err != cudaSuccess) return err;
+    configured_device = dev.device;
+  }
+  const int group = a.q_heads / c.heads;
+  const int64_t per_seq = (int64_t)c.heads * ((group + kRowHeads - 1) / kRowHeads);
+  int64_t tokens = a.max_pages << c.page_shift;
+  if (a.window > 0 && a.window < tokens) tokens = a.window;
+  const int splits = splits_for(a.B * per_seq, (tokens + S::kTokens - 1) / S::kTokens, dev);
+  const int64_t per_launch = (int64_t)0x7fffffff / (per_seq * splits);  // sequences a grid holds
+  for (int64_t b0 = 0; b0 < a.B; b0 += per_launch) {
+    const int64_t n = a.B - b0 < per_launch ? a.B - b0 : per_launch;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(n * per_seq * splits), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    if (splits > 1) {
+      attr[na].id = cudaLaunchAttributeClusterDimension;
+      attr[na].val.clusterDim.x = (unsigned)splits;
+      attr[na].val.clusterDim.y = 1;
+      attr[na].val.clusterDim.z = 1;
+      ++na;
+    }
+    if (pdl) {
+      attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[na].val.programmaticStreamSerializationAllowed = 1;
+      ++na;
+    }
+    cfg.attrs = na ? attr : nullptr;
+    cfg.numAttrs = (unsigned)na;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, c, b0, splits);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
 }
 
 template <int FORMAT>
-__global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages c) {
-  __shared__ float sm[kWarps], sl[kWarps], sacc[kWarps][kMaxHead];
-  pdl_release_dependents();
-  pdl_wait_primary();
-  const int hq = blockIdx.x, hk = hq / (a.q_heads / c.heads), D = c.head_dim;
-  const int64_t b = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
-  if (b >= a.B) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t len = a.lengths[b];
-  const int64_t most = a.max_pages << c.page_shift;
-  len = len < most ? len : most;
-  const int64_t first = a.window > 0 && len > a.window ? len - a.window : 0;
-  float q[kLaneDims], acc[kLaneDims];
-#pragma unroll
-  for (int j = 0; j < kLaneDims; ++j) {
-    const int d = lane + 32 * j;
-    q[j] = d < D ? a.q[b * a.q_stride + (int64_t)hq * D + d] * a.scale : 0.0f;
-    acc[j] = 0.0f;
-  }
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t t = first + warp; t < len; t += kWarps) {
-    const int32_t page = a.table[b * a.table_stride + (t >> c.page_shift)];
-    if (page < 0 || page >= c.num_pages) continue;
-    const int64_t row = (((int64_t)page * c.heads + hk) << c.page_shift) + (t & ((1 << c.page_shift) - 1));
-    float x = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kLaneDims; ++j)
-      if (lane + 32 * j < D) x = fmaf(q[j], value_at<FORMAT>(c.k, row * D + lane + 32 * j), x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFullMask, x, o);
-    if (FORMAT != BITLINEAR_KV_BF16) x *= c.k_step[row];
-    const float up = fmaxf(m, x), f = expf(m - up), p = expf(x - up);
-    const float w = FORMAT != BITLINEAR_KV_BF16 ? p * c.v_step[row] : p;
-    m = up;
-    l = fmaf(l, f, p);
-#pragma unroll
-    for (int j = 0; j < kLaneDims; ++j)
-      if (lane + 32 * j < D) acc[j] = fmaf(acc[j], f, w * value_at<FORMAT>(c.v, row * D + lane + 32 * j));
-  }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-#pragma unroll
-  for (int j = 0; j < kLaneDims; ++j) sacc[warp][lane + 32 * j] = acc[j];
-  __syncthreads();
-  float top = -INFINITY, sum = 0.0f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-  for (int w = 0; w < kWarps; ++w)
-    if (sm[w] > -INFINITY) sum += sl[w] * expf(sm[w] - top);
-  for (int d = threadIdx.x; d < D; d += kThreads) {
-    float o = 0.0f;
-    for (int w = 0; w < kWarps; ++w)
-      if (sm[w] > -INFINITY) o += sacc[w][d] * expf(sm[w] - top);
-    a.out[b * a.out_stride + (int64_t)hq * D + d] = sum > 0.0f ? o / sum : 0.0f;  // no token: zeros
-  }
+cudaError_t launch_format(const AttendArgs& a, const KvPages& c, bool pdl, const DeviceInfo& dev, cudaStream_t s) {
+  if (c.head_dim <= 64) return launch_shape<FORMAT, 64>(a, c, pdl, dev, s);
+  if (c.head_dim <= 80) return launch_shape<FORMAT, 80>(a, c, pdl, dev, s);
+  if (c.head_dim <= 96) return launch_shape<FORMAT, 96>(a, c, pdl, dev, s);
+  if (c.head_dim <= 128) return launch_shape<FORMAT, 128>(a, c, pdl, dev, s);
+  return launch_shape<FORMAT, 256>(a, c, pdl, dev, s);
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int64_t, int, int, int) { return 0; }
 
-cudaError_t launch_attention(const AttendArgs& a, const KvPages& cache, void*, bool pdl, const DeviceInfo&,
+cudaError_t launch_attention(const AttendArgs& a, const KvPages& cache, void*, bool pdl, const DeviceInfo& dev,
                              cudaStream_t stream) {
-  const auto kernel = cache.format == BITLINEAR_KV_INT8  ? attend_kernel<BITLINEAR_KV_INT8>
-                      : cache.format == BITLINEAR_KV_FP8 ? attend_kernel<BITLINEAR_KV_FP8>
-                                                         : attend_kernel<BITLINEAR_KV_BF16>;
-  const int64_t rows = a.B < 65535 ? a.B : 65535;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.q_heads, (unsigned)rows, (unsigned)((a.B + rows - 1) / rows));
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = pdl ? attr : nullptr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a, cache);
+  if (cache.format == BITLINEAR_KV_INT8) return launch_format<BITLINEAR_KV_INT8>(a, cache, pdl, dev, stream);
+  if (cache.format == BITLINEAR_KV_FP8) return launch_format<BITLINEAR_KV_FP8>(a, cache, pdl, dev, stream);
+  return launch_format<BITLINEAR_KV_BF16>(a, cache, pdl, dev, stream);
 }
 
 }  // namespace bitlinear
