@@ -167,7 +167,10 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        try:  # the handle alone: a third of the time of building a Stream object
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -408,73 +411,77 @@ def _rows(t, name, T, H=None, D=None):
     """The row stride (elements) of fp32 [T, H, D] rows: heads side by side, rows any
     stride apart.  H, D None: any."""
     import torch
+    try:  # the common case first; the detailed checks only where it fails
+        shape = t.shape
+        if (t.is_cuda and t.dtype == torch.float32 and t.is_contiguous() and len(shape) == 3
+                and shape == (T, shape[1] if H is None else H, shape[2] if D is None else D)):
+            return shape[1] * shape[2]
+    except AttributeError:
+        pass
     if not getattr(t, "is_cuda", False):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
-    shape = t.shape
     if len(shape) != 3 or shape[0] != T or (H is not None and shape[1] != H) or (D is not None and shape[2] != D):
         raise ValueError(f"{name} must have shape ({T}, {'heads' if H is None else H}, "
                          f"{'head_dim' if D is None else D}), got {tuple(shape)}")
-    if t.is_contiguous():  # strides of dims of size 1 say nothing
-        return shape[1] * shape[2]
     strides = t.stride()
-    if strides[2] != 1 or (shape[1] > 1 and strides[1] != shape[2]):
+    if (shape[2] > 1 and strides[2] != 1) or (shape[1] > 1 and strides[1] != shape[2]):
         raise ValueError(f"{name}'s heads must lie side by side in each row, got strides {tuple(strides)}")
     return strides[0] if T > 1 else shape[1] * shape[2]
 
 
-def _ints(t, name, shape):
-    import torch
-    _need(t, torch.int32, name, shape)
-
-
-def _pages_table(t, rows=None):
+def _page_table(t, rows=None):
     """(rows, columns, row stride) of the int32 page table: contiguous rows, any stride apart."""
     import torch
     if not getattr(t, "is_cuda", False) or t.dtype != torch.int32:
         raise TypeError("page_table must be an int32 CUDA tensor")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"page_table must be [{'sequences' if rows is None else rows}, pages], got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows):
+        raise ValueError(f"page_table must be [{'sequences' if rows is None else rows}, pages], got {tuple(shape)}")
+    n, cols = shape
+    if t.is_contiguous():
+        return n, cols, cols
+    if cols > 1 and t.stride(1) != 1:
         raise ValueError("page_table's rows must be contiguous")
-    n, cols = t.shape
     return n, cols, t.stride(0) if n > 1 else cols
 
 
-def _same_device(first, *others):
+def _same_device(tensors):
     """Every tensor on the current device: the library launches there."""
     import torch
     at = torch.cuda.current_device()
-    for t in (first, *others):
+    for t in tensors:
         if t is not None and t.get_device() != at:
             raise ValueError(f"every tensor must be on the current device cuda:{at}, got one on {t.device}")
+
+
+_FORMATS = {}  # torch dtype -> BITLINEAR_KV_*, once torch is there
 
 
 def _kv_pages(cache):
     """BitLinearKVPages of (k, v, k_step, v_step), the steps None for bf16."""
     import torch
+    if not _FORMATS:
+        _FORMATS.update({torch.int8: KV_INT8, torch.float8_e4m3fn: KV_FP8, torch.bfloat16: KV_BF16})
     k, v = cache[0], cache[1]
     k_step, v_step = (cache[2], cache[3]) if len(cache) > 2 else (None, None)
     if not getattr(k, "is_cuda", False):
         raise TypeError("the cache must be CUDA tensors")
-    if k.dim() != 4:
-        raise ValueError(f"the cache's k must be [pages, heads, page_size, head_dim], got {tuple(k.shape)}")
-    fmt = (KV_INT8 if k.dtype == torch.int8 else KV_FP8 if k.dtype == torch.float8_e4m3fn
-           else KV_BF16 if k.dtype == torch.bfloat16 else None)
+    fmt, shape = _FORMATS.get(k.dtype), k.shape
     if fmt is None:
         raise TypeError(f"the cache must be int8, float8_e4m3fn or bfloat16, got {k.dtype}")
-    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"the cache's k must be [pages, heads, page_size, head_dim], got {tuple(shape)}")
     _need(k, k.dtype, "the cache's k")
     _need(v, k.dtype, "the cache's v", shape)
     if fmt == KV_BF16:
         if k_step is not None or v_step is not None:
             raise ValueError("a bfloat16 cache has no steps")
-    else:
-        _need(k_step, torch.float32, "the cache's k_step", shape[:3])
-        _need(v_step, torch.float32, "the cache's v_step", shape[:3])
-    return BitLinearKVPages(k.data_ptr(), v.data_ptr(), _ptr(k_step), _ptr(v_step), shape[0], shape[1], shape[2],
-                            shape[3], fmt)
+        return BitLinearKVPages(k.data_ptr(), v.data_ptr(), None, None, *shape, fmt)
+    _need(k_step, torch.float32, "the cache's k_step", shape[:3])
+    _need(v_step, torch.float32, "the cache's v_step", shape[:3])
+    return BitLinearKVPages(k.data_ptr(), v.data_ptr(), k_step.data_ptr(), v_step.data_ptr(), *shape, fmt)
 
 
 def _rope_spec(rope):
@@ -506,13 +513,14 @@ def bitlinear_rope(x, positions, rope, y, flags: int = 0, stream=None):
     (bitlinear_rope_frequencies) and layout ROPE_HALF or ROPE_INTERLEAVED.  y may be x.
     Rows may lie any multiple of 4 floats apart.
     """
+    import torch
     T = x.shape[0]
     x_stride = _rows(x, "x", T)
     _, H, D = x.shape
     y_stride = _rows(y, "y", T, H, D)
-    _ints(positions, "positions", (T,))
+    _need(positions, torch.int32, "positions", (T,))
     spec = _rope_spec(rope)
-    _same_device(x, y, positions, rope[0])
+    _same_device((x, y, positions, rope[0]))
     _check(load_library().bitlinear_rope(_ptr(x), x_stride, T, H, D, _ptr(positions), spec, _ptr(y), y_stride,
                                          int(flags), _stream(stream)), "bitlinear_rope")
 
@@ -527,14 +535,15 @@ def bitlinear_kv_append(k, v, cache, positions, page_table, seq=None, q=None, q_
     positions, seq: int32 [T]; page_table: int32 [sequences, pages]; seq None: row i is of
     sequence i.  Rows with a negative position are padding.  rope: as for bitlinear_rope.
     """
+    import torch
     pages = _kv_pages(cache)
     T, Hk, D = k.shape[0], pages.num_heads, pages.head_dim
     k_stride = _rows(k, "k", T, Hk, D)
     v_stride = _rows(v, "v", T, Hk, D)
-    _ints(positions, "positions", (T,))
+    _need(positions, torch.int32, "positions", (T,))
     if seq is not None:
-        _ints(seq, "seq", (T,))
-    num_seqs, max_pages, table_stride = _pages_table(page_table)
+        _need(seq, torch.int32, "seq", (T,))
+    num_seqs, max_pages, table_stride = _page_table(page_table)
     Hq = q_stride = q_out_stride = 0
     if q is not None:
         q_stride = _rows(q, "q", T, None, D)
@@ -543,7 +552,7 @@ def bitlinear_kv_append(k, v, cache, positions, page_table, seq=None, q=None, q_
     elif q_out is not None:
         raise ValueError("q_out without q")
     spec = None if rope is None else _rope_spec(rope)
-    _same_device(k, v, cache[0], cache[1], positions, page_table, seq, q, q_out, None if rope is None else rope[0])
+    _same_device((k, v, *cache, positions, page_table, seq, q, q_out, None if rope is None else rope[0]))
     _check(load_library().bitlinear_kv_append(
         _ptr(q), q_stride, Hq, _ptr(q_out), q_out_stride, _ptr(k), k_stride, _ptr(v), v_stride, T, _ptr(positions),
         _ptr(seq), _ptr(page_table), table_stride, num_seqs, max_pages, spec, pages, int(flags), _stream(stream)),
@@ -552,15 +561,16 @@ def bitlinear_kv_append(k, v, cache, positions, page_table, seq=None, q=None, q_
 
 def bitlinear_kv_read(cache, positions, page_table, k_out, v_out, seq=None, flags: int = 0, stream=None):
     """k_out, v_out [T, heads, head_dim] fp32 = the cached rows at (seq[i], positions[i])."""
+    import torch
     pages = _kv_pages(cache)
     T, Hk, D = k_out.shape[0], pages.num_heads, pages.head_dim
     k_stride = _rows(k_out, "k_out", T, Hk, D)
     v_stride = _rows(v_out, "v_out", T, Hk, D)
-    _ints(positions, "positions", (T,))
+    _need(positions, torch.int32, "positions", (T,))
     if seq is not None:
-        _ints(seq, "seq", (T,))
-    num_seqs, max_pages, table_stride = _pages_table(page_table)
-    _same_device(k_out, v_out, cache[0], cache[1], positions, page_table, seq)
+        _need(seq, torch.int32, "seq", (T,))
+    num_seqs, max_pages, table_stride = _page_table(page_table)
+    _same_device((k_out, v_out, *cache, positions, page_table, seq))
     _check(load_library().bitlinear_kv_read(
         pages, T, _ptr(positions), _ptr(seq), _ptr(page_table), table_stride, num_seqs, max_pages, _ptr(k_out),
         k_stride, _ptr(v_out), v_stride, int(flags), _stream(stream)), "bitlinear_kv_read")
@@ -582,11 +592,11 @@ def bitlinear_attention(q, cache, page_table, lengths, out, workspace=None, scal
     q_stride = _rows(q, "q", B, None, D)
     Hq = q.shape[1]
     out_stride = _rows(out, "out", B, Hq, D)
-    _ints(lengths, "lengths", (B,))
-    _, max_pages, table_stride = _pages_table(page_table, B)
+    _need(lengths, torch.int32, "lengths", (B,))
+    _, max_pages, table_stride = _page_table(page_table, B)
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace")
-    _same_device(q, out, cache[0], cache[1], page_table, lengths, workspace)
+    _same_device((q, out, *cache, page_table, lengths, workspace))
     _check(load_library().bitlinear_attention(
         _ptr(q), q_stride, B, Hq, pages, _ptr(page_table), table_stride, max_pages, _ptr(lengths), int(window),
         D ** -0.5 if scale is None else float(scale), _ptr(out), out_stride, _ptr(workspace),
