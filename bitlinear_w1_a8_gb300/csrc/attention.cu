@@ -4,8 +4,8 @@
 // over the tokens t of sequence b that its length and the window leave, in one
 // pass over keys and values with a running m, sum and weighted sum.
 //
-// One CTA takes a run of tokens of one key head of one sequence, for up to 8 of
-// the q heads that share it; the runs of a sequence are the CTAs of one
+// One CTA takes a share of the tokens of one key head of one sequence, for up to 8
+// of the q heads that share it; the shares of a sequence are the CTAs of one
 // thread-block cluster and join through distributed shared memory, in the order
 // of the runs.  Inside a CTA a warp works alone: it streams its own steps of
 // tokens (every kWarps-th step of the run) through a ring of shared-memory stages
@@ -23,11 +23,16 @@
 // So a logit and a weighted sum keep fp32 accuracy.  The key's step multiplies the
 // logit, the value's step multiplies p.
 //
-// Lazy references: m (per head) moves only when some logit exceeds it by 8, so p
-// stays at or below 2^8, and p times the value's step is scaled by a power of two
-// that moves the same way, so its fp16 parts keep their bits whatever the steps are.
+// One lazy reference a head: p_t = 2^(x_t - ref), with ref moved only when some
+// p_t times its value's step exceeds 2^8, to the largest x_t + log2(step).  So the
+// weights that enter the second product stay in fp16's range and keep their bits
+// whatever the steps are, and sum, weighted sum and ref need no other scale.
 // The MMA sums of a step (16 or 32 tokens) start from zero and are added to fp32
 // sums in registers: a chain of roundings no longer than the steps of a warp.
+//
+// Where one cluster a sequence leaves SMs idle (few heads, long sequences), several
+// clusters take a sequence, each writing its joined part to the workspace, and a
+// second small launch joins those.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -39,9 +44,14 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRowHeads = 8;   // q heads of one CTA
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kMaxCluster = 8;
-constexpr float kLazy = 8.0f;  // how far a logit (base 2) may exceed its reference
+constexpr int kMaxClusters = 16;  // clusters a sequence, with a workspace
+constexpr int kClusterSteps = 8;  // steps a warp has before a second cluster is worth a second launch
+constexpr int kSms = 152;
+constexpr float kLimit = 256.0f;  // the largest weight before the reference moves
+constexpr float kUnset = -1e30f;  // a reference below every logit
+constexpr float kLeastStep = 8.2718061e-25f;  // 2^-80: a value's step counts as that at least (a cache of zeros holds 0)
 
 // Sizes of one instantiation: DT dims a head (a smaller head_dim is padded with
 // zeros), codes of kBytes, steps of kTokens tokens.
@@ -61,12 +71,16 @@ struct Shape {
   static constexpr int kWarpBytes = kStages * kStage;
   static constexpr int kPartial = (DT + 4) * 4;    // a head's weighted sum, m and sum, padded to 16 bytes
   static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes;
+  static constexpr int kCtas = DT <= 96 ? 4 : DT <= 128 ? 3 : 2;  // CTAs an SM that the registers allow
   static_assert(kRowHeads * kPartial <= kWarpBytes, "a warp's partials reuse its ring");
   static_assert(kStage % 16 == 0 && DT % 16 == 0, "");
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
@@ -109,21 +123,28 @@ __device__ __forceinline__ float exp2_of(float x) {  // relative error 2^-22, 0 
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float log2_of(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // 2^e for |e| <= 126, and the exponent of a positive normal x.
 __device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }
 __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 __device__ __forceinline__ int clamp_exponent(int e) { return max(-100, min(100, e)); }
 
-template <int FORMAT>
+// c = a b (FIRST) or c += a b.
+template <int FORMAT, bool FIRST>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  const float c0 = FIRST ? 0.0f : c[0], c1 = FIRST ? 0.0f : c[1], c2 = FIRST ? 0.0f : c[2], c3 = FIRST ? 0.0f : c[3];
   if constexpr (FORMAT == BITLINEAR_KV_BF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // The bytes `pair` selects of two code words, widened to two halves.  int8 codes
@@ -159,51 +180,74 @@ __device__ __forceinline__ uint32_t next_part(float& x, float& y) {  // bf16 par
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The run of one CTA and what it needs to know of its sequence.
-struct Run {
-  const int32_t* table;    // the sequence's pages
-  const uint8_t *k, *v;    // the key head's first page row (page 0)
+// A key head's part of the cache and the tokens of the sequence that count.
+struct Source {
+  const uint8_t *k, *v;    // the head's rows of page 0
   const float *ks, *vs;
-  int64_t first, len;      // tokens first <= t < len count
-  int64_t u0;              // the warp's first step (in steps of kTokens tokens)
+  int64_t first, len;      // first <= t < len
 };
 
-// Requests one step's keys, values and steps into a stage; the low bits of the
-// result say which 16-token halves have a page.  Rows that do not count are zeroed.
+// Requests a step whose every token counts and has a page, head_dim == DT: a
+// half's 16 rows are one run of bytes, 512 of them an instruction.
 template <int FORMAT, int DT>
-__device__ __forceinline__ uint32_t request(const Run& r, const KvPages& c, int64_t t0, const int32_t (&page)[2],
-                                            uint32_t stage, int lane) {
+__device__ __forceinline__ void request_whole(const Source& r, const int64_t (&row)[2], uint32_t stage, int lane) {
   using S = Shape<FORMAT, DT>;
-  constexpr int kHalves = S::kTokens / 16;
-  const int row_bytes = c.head_dim * S::kBytes, chunks = row_bytes / 16;
-  uint32_t ok = 0;
+  constexpr int kTurns = 16 * S::kChunks / 32;  // whole turns of the warp over a half's chunks
+  auto place = [](int i) { return (uint32_t)(i / S::kChunks * S::kPitch + i % S::kChunks * 16); };
 #pragma unroll
-  for (int s = 0; s < kHalves; ++s) {
-    const int64_t t = t0 + 16 * s;
-    const bool have = t < r.len && page[s] >= 0 && page[s] < c.num_pages;
-    ok |= have ? 1u << s : 0u;
-    const int64_t row = have ? (((int64_t)page[s] * c.heads) << c.page_shift) + (t & ((1 << c.page_shift) - 1)) : 0;
-    const uint8_t* ks = r.k + row * row_bytes;
-    const uint8_t* vs = r.v + row * row_bytes;
+  for (int s = 0; s < S::kTokens / 16; ++s) {
+    const uint8_t* k = r.k + row[s] * S::kRow;
+    const uint8_t* v = r.v + row[s] * S::kRow;
     const uint32_t kd = stage + 16 * s * S::kPitch, vd = kd + S::kTokens * S::kPitch;
 #pragma unroll
-    for (int j = 0; j < (16 * S::kChunks + 31) / 32; ++j) {
-      const int i = lane + 32 * j, n = i / S::kChunks, ch = i % S::kChunks;
-      if (n < 16 && ch < chunks) {
-        const bool there = have && t + n >= r.first && t + n < r.len;
-        const int64_t off = there ? (int64_t)n * row_bytes + 16 * ch : 0;
-        copy16(kd + n * S::kPitch + 16 * ch, ks + off, there);
-        copy16(vd + n * S::kPitch + 16 * ch, vs + off, there);
-      }
+    for (int j = 0; j < kTurns; ++j) {
+      copy16(kd + place(lane + 32 * j), k + 16 * (lane + 32 * j));
+      copy16(vd + place(lane + 32 * j), v + 16 * (lane + 32 * j));
+    }
+    if constexpr (S::kChunks % 2) {  // half a turn of each is left
+      const int i = (lane & 15) + 32 * kTurns;
+      copy16((lane < 16 ? kd : vd) + place(i), (lane < 16 ? k : v) + 16 * i);
+    }
+  }
+  if constexpr (FORMAT != BITLINEAR_KV_BF16) {
+    if (lane < S::kTokens / 2) {  // 16 bytes: key steps of the halves, then value steps
+      const int in_kind = lane % (S::kTokens / 4), half = in_kind / 4;
+      copy16(stage + 2 * S::kTokens * S::kPitch + 16 * lane,
+             (lane < S::kTokens / 4 ? r.ks : r.vs) + (half ? row[1] : row[0]) + 4 * (in_kind % 4));
+    }
+  }
+}
+
+// Requests any step; `ok` says which halves have a page.  Rows that do not count
+// are zeroed, so that whatever they hold (NaN among it) meets no weight of 0.
+template <int FORMAT, int DT>
+__device__ __forceinline__ void request_part(const Source& r, const KvPages& c, int64_t t0, const int64_t (&row)[2],
+                                             uint32_t ok, uint32_t stage, int lane) {
+  using S = Shape<FORMAT, DT>;
+  const int row_bytes = c.head_dim * S::kBytes, chunks = row_bytes / 16;
+#pragma unroll
+  for (int s = 0; s < S::kTokens / 16; ++s) {
+    const int64_t t = t0 + 16 * s;
+    const bool have = (ok >> s) & 1u;
+    const uint8_t* k = r.k + row[s] * row_bytes;
+    const uint8_t* v = r.v + row[s] * row_bytes;
+    const uint32_t kd = stage + 16 * s * S::kPitch, vd = kd + S::kTokens * S::kPitch;
+#pragma unroll 1
+    for (int i = lane; i < 16 * S::kChunks; i += 32) {
+      const int n = i / S::kChunks, ch = i % S::kChunks;
+      if (ch >= chunks) continue;
+      const bool there = have && t + n >= r.first && t + n < r.len;
+      const int off = there ? n * row_bytes + 16 * ch : 0;
+      copy16(kd + n * S::kPitch + 16 * ch, k + off, there);
+      copy16(vd + n * S::kPitch + 16 * ch, v + off, there);
     }
     if constexpr (FORMAT != BITLINEAR_KV_BF16) {
       const int n = lane & 15;
       const bool there = have && t + n >= r.first && t + n < r.len;
-      const uint32_t sd = stage + 2 * S::kTokens * S::kPitch + (lane >> 4) * S::kTokens * 4 + (16 * s + n) * 4;
-      copy4(sd, (lane < 16 ? r.ks : r.vs) + row + (there ? n : 0), there);
+      copy4(stage + 2 * S::kTokens * S::kPitch + (lane >> 4) * S::kTokens * 4 + (16 * s + n) * 4,
+            (lane < 16 ? r.ks : r.vs) + row[s] + (there ? n : 0), there);
     }
   }
-  return ok;
 }
 
 // Joins `parts` partials of one head's dim d: part i is at base + i * apart (its
@@ -213,7 +257,7 @@ struct Joined {
 };
 template <bool CLUSTER>
 __device__ __forceinline__ Joined join(uint32_t base, uint32_t apart, int parts, int d, int dims) {
-  Joined j = {0.0f, -INFINITY, 0.0f};
+  Joined j = {0.0f, kUnset, 0.0f};
   auto at = [&](int i, int f) {
     float v;
     if constexpr (CLUSTER) return lds_cluster(base + 4 * f, i);
@@ -221,7 +265,6 @@ __device__ __forceinline__ Joined join(uint32_t base, uint32_t apart, int parts,
     return v;
   };
   for (int i = 0; i < parts; ++i) j.m = fmaxf(j.m, at(i, dims));
-  if (j.m == -INFINITY) return j;
   for (int i = 0; i < parts; ++i) {
     const float f = exp2_of(at(i, dims) - j.m);
     j.sum = fmaf(at(i, dims + 1), f, j.sum);
@@ -231,14 +274,17 @@ __device__ __forceinline__ Joined join(uint32_t base, uint32_t apart, int parts,
 }
 
 template <int FORMAT, int DT>
-__global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages c, int64_t b0, int splits) {
+__global__ void __launch_bounds__(kThreads, Shape<FORMAT, DT>::kCtas)
+attend_kernel(AttendArgs a, KvPages c, int64_t b0, int splits, int clusters, float* __restrict__ parts) {
   using S = Shape<FORMAT, DT>;
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_release_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
   const int group = a.q_heads / c.heads, groups = (group + kRowHeads - 1) / kRowHeads;
-  const int split = blockIdx.x % splits;
+  const int split = blockIdx.x % splits;  // the CTA's rank in its cluster
   int64_t rest = blockIdx.x / splits;
+  const int cluster = (int)(rest % clusters);
+  rest /= clusters;
   const int first_of_group = (int)(rest % groups) * kRowHeads;
   rest /= groups;
   const int hk = (int)(rest % c.heads);
@@ -253,43 +299,59 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages 
   }
   pdl_wait_primary();
 
-  Run r;
+  Source r;
   const int64_t most = a.max_pages << c.page_shift;
   r.len = a.lengths[b];
-  r.len = r.len < most ? r.len : most;
-  r.first = a.window > 0 && r.len > a.window ? r.len - a.window : 0;
-  r.table = a.table + b * a.table_stride;
+  const int32_t* table = a.table + b * a.table_stride;
   const int64_t head_row = (int64_t)hk << c.page_shift;
   r.k = static_cast<const uint8_t*>(c.k) + head_row * D * S::kBytes;
   r.v = static_cast<const uint8_t*>(c.v) + head_row * D * S::kBytes;
   r.ks = c.k_step + head_row;
   r.vs = c.v_step + head_row;
-  const int64_t begin = r.first / S::kTokens;
-  const int64_t units = r.len > r.first ? (r.len + S::kTokens - 1) / S::kTokens - begin : 0;
-  const int64_t share = (units + splits - 1) / splits;
-  const int64_t u1 = min(units, (split + 1) * share);
-  r.u0 = split * share + warp;
-  const int64_t mine = u1 > r.u0 ? (u1 - r.u0 + kWarps - 1) / kWarps : 0;  // steps of this warp
-
+  // The warp's steps are every (clusters * splits * kWarps)-th one, from the window's first on.
+  const int64_t lap = (int64_t)clusters * splits * kWarps * S::kTokens;
+  int64_t t_ask = ((int64_t)(cluster * splits + split) * kWarps + warp) * S::kTokens;
   int32_t page[2] = {-1, -1};
-  auto token_of = [&](int64_t i) { return (begin + r.u0 + i * kWarps) * S::kTokens; };
-  auto look_up = [&](int64_t i) {
-    const int64_t t = token_of(i);
-    page[0] = i < mine && t < r.len ? r.table[t >> c.page_shift] : -1;
-    if constexpr (S::kTokens == 32) page[1] = i < mine && t + 16 < r.len ? r.table[(t + 16) >> c.page_shift] : -1;
+  auto look_up = [&](int64_t t) {  // the pages of the step at t (columns of the table, whatever the length)
+    page[0] = t < most ? table[t >> c.page_shift] : -1;
+    if constexpr (S::kTokens == 32) page[1] = t + 16 < most ? table[(t + 16) >> c.page_shift] : -1;
   };
-  uint32_t oks = 0;  // two bits a requested step, the newest lowest
-  auto ask = [&](int64_t i) {
-    oks <<= 2;
-    if (i < mine) oks |= request<FORMAT, DT>(r, c, token_of(i), page, ring + (uint32_t)(i % kStages) * S::kStage, lane);
-    copies_commit();
-  };
-  look_up(0);
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    ask(i);
-    look_up(i + 1);
+  if (a.window <= 0) look_up(t_ask);
+  r.len = r.len < most ? r.len : most;
+  r.first = a.window > 0 && r.len > a.window ? r.len - a.window : 0;
+  if (a.window > 0) {
+    t_ask += r.first / S::kTokens * S::kTokens;
+    look_up(t_ask);
   }
+  int64_t t0 = t_ask;  // the step in hand
+
+  uint32_t oks = 0;  // two bits a requested step (its halves have pages), the newest lowest
+  uint32_t ask_at = ring;
+  auto ask = [&]() {  // requests the step at t_ask into the next stage and looks the one after up
+    oks <<= 2;
+    if (t_ask < r.len) {
+      int64_t row[2] = {0, 0};
+      uint32_t ok = 0;
+#pragma unroll
+      for (int s = 0; s < S::kTokens / 16; ++s) {
+        if (t_ask + 16 * s < r.len && (uint32_t)page[s] < (uint32_t)c.num_pages) {
+          ok |= 1u << s;
+          row[s] = (((int64_t)page[s] * c.heads) << c.page_shift) + ((int)(t_ask + 16 * s) & ((1 << c.page_shift) - 1));
+        }
+      }
+      oks |= ok;
+      if (D == DT && ok == (S::kTokens == 32 ? 3u : 1u) && t_ask >= r.first && t_ask + S::kTokens <= r.len)
+        request_whole<FORMAT, DT>(r, row, ask_at, lane);
+      else
+        request_part<FORMAT, DT>(r, c, t_ask, row, ok, ask_at, lane);
+    }
+    copies_commit();
+    t_ask += lap;
+    look_up(t_ask);
+    ask_at = ask_at == ring + (kStages - 1) * S::kStage ? ring : ask_at + S::kStage;
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) ask();
 
   // q as the MMA's A operand: rows g the leading parts of head g, rows g + 8 the
   // next, the dims of a k-step in the order the key words give them.
@@ -330,26 +392,20 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages 
     }
   }
 
-  float m = -INFINITY, sum = 0.0f;                     // of row g; the sum over this lane's tokens
-  float up = 1.0f, limit = kBf16 ? INFINITY : 0.0f;    // the power of two on p * step, and when it moves
+  float ref = kUnset, sum = 0.0f;                      // of row g; the sum over this lane's tokens
   float out[S::kOutTiles][2];                          // row g: dims 2 qd, 2 qd + 1 of every n-tile (in the tiles' order)
 #pragma unroll
   for (int n = 0; n < S::kOutTiles; ++n) out[n][0] = out[n][1] = 0.0f;
   constexpr float kRest = kBf16 ? 1.0f : 1.0f / 2048.0f;
 
-  for (int64_t i = 0; i < mine; ++i) {
-    copies_wait<kStages - 2>();
-    __syncwarp();  // every lane's copies of step i, and every lane is done with the stage before
-    ask(i + kStages - 1);
-    look_up(i + kStages);
-    const uint32_t st = ring + (uint32_t)(i % kStages) * S::kStage;
+  for (uint32_t st = ring; t0 < r.len; t0 += lap, st = st == ring + (kStages - 1) * S::kStage ? ring : st + S::kStage) {
+    __syncwarp();  // every lane is done with the stage that is requested next
+    ask();
+    copies_wait<kStages - 1>();
+    __syncwarp();  // every lane's copies of this step
     const uint32_t vst = st + S::kTokens * S::kPitch, kst = vst + S::kTokens * S::kPitch;
-    const uint32_t ok = (oks >> (2 * (kStages - 1))) & 3u;
-    const int64_t t0 = token_of(i);
 
     float x[S::kTiles][4];
-#pragma unroll
-    for (int j = 0; j < S::kTiles; ++j) x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.0f;
 #pragma unroll
     for (int s = 0; s < S::kSteps; ++s)
 #pragma unroll
@@ -359,42 +415,75 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages 
         if constexpr (kBf16) {
           k0 = lds32(row);
           k1 = lds32(row + 16);
-          mma<FORMAT>(x[j], qa[s], k0, k1);
-          const uint32_t third[4] = {qb[s][0], 0u, qb[s][1], 0u};
-          mma<FORMAT>(x[j], third, k0, k1);
         } else {
           widen<FORMAT>(lds32(row), k0, k1);
-          mma<FORMAT>(x[j], qa[s], k0, k1);
+        }
+        if (s == 0)
+          mma<FORMAT, true>(x[j], qa[s], k0, k1);
+        else
+          mma<FORMAT, false>(x[j], qa[s], k0, k1);
+        if constexpr (kBf16) {
+          const uint32_t third[4] = {qb[s][0], 0u, qb[s][1], 0u};
+          mma<FORMAT, false>(x[j], third, k0, k1);
         }
       }
 
-    // logits of row g, tokens 8 j + 2 qd and the next
-    float2 lg[S::kTiles];
-    float top = -INFINITY;
-    const bool whole = ok == (S::kTokens == 32 ? 3u : 1u) && t0 >= r.first && t0 + S::kTokens <= r.len;
+    // logits of row g (times 1 / row_scale), tokens 8 j + 2 qd and the next
+    float2 lg[S::kTiles], p[S::kTiles], w[S::kTiles];
 #pragma unroll
     for (int j = 0; j < S::kTiles; ++j) {
       lg[j].x = fmaf(x[j][2], kRest, x[j][0]);
       lg[j].y = fmaf(x[j][3], kRest, x[j][1]);
       if constexpr (!kBf16) {
         const float2 step = lds_float2(kst + (8 * j + 2 * qd) * 4);
-        lg[j].x *= row_scale * step.x;
-        lg[j].y *= row_scale * step.y;
+        lg[j].x *= step.x;
+        lg[j].y *= step.y;
       }
-      if (!whole) {
+    }
+    const uint32_t ok = (oks >> (2 * (kStages - 1))) & 3u;
+    if (ok != (S::kTokens == 32 ? 3u : 1u) || t0 < r.first || t0 + S::kTokens > r.len) {
+#pragma unroll
+      for (int j = 0; j < S::kTiles; ++j) {
         const int64_t t = t0 + 8 * j + 2 * qd;
         const bool have = (ok >> (j / 2)) & 1u;
         if (!have || t < r.first || t >= r.len) lg[j].x = -INFINITY;
         if (!have || t + 1 < r.first || t + 1 >= r.len) lg[j].y = -INFINITY;
       }
-      top = fmaxf(top, fmaxf(lg[j].x, lg[j].y));
     }
-    if (__any_sync(kFullMask, top > m + kLazy)) {
+    // p and its weights (p times the value's step); `high` the largest
+    auto weights = [&](float& high) {
+#pragma unroll
+      for (int j = 0; j < S::kTiles; ++j) {
+        p[j].x = exp2_of(fmaf(lg[j].x, row_scale, -ref));
+        p[j].y = exp2_of(fmaf(lg[j].y, row_scale, -ref));
+        w[j] = p[j];
+        if constexpr (!kBf16) {
+          const float2 step = lds_float2(kst + (S::kTokens + 8 * j + 2 * qd) * 4);
+          w[j].x *= fmaxf(step.x, kLeastStep);
+          w[j].y *= fmaxf(step.y, kLeastStep);
+        }
+        high = fmaxf(high, fmaxf(w[j].x, w[j].y));
+      }
+    };
+    float high = 0.0f;
+    weights(high);
+    if (__any_sync(kFullMask, high > kLimit)) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < S::kTiles; ++j) {
+        float2 z = make_float2(lg[j].x * row_scale, lg[j].y * row_scale);
+        if constexpr (!kBf16) {
+          const float2 step = lds_float2(kst + (S::kTokens + 8 * j + 2 * qd) * 4);
+          z.x += log2_of(fmaxf(step.x, kLeastStep));
+          z.y += log2_of(fmaxf(step.y, kLeastStep));
+        }
+        top = fmaxf(top, fmaxf(z.x, z.y));
+      }
       top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
       top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-      if (top > m + kLazy) {
-        const float f = exp2_of(m - top);  // 0 from the first reference
-        m = top;
+      if (top > ref) {
+        const float f = exp2_of(ref - top);  // 0 from the first reference
+        ref = top;
         sum *= f;
 #pragma unroll
         for (int n = 0; n < S::kOutTiles; ++n) {
@@ -402,55 +491,25 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages 
           out[n][1] *= f;
         }
       }
+      weights(high);
     }
-    const float ref = m == -INFINITY ? 0.0f : m;
-    float high = 0.0f;
 #pragma unroll
-    for (int j = 0; j < S::kTiles; ++j) {
-      lg[j].x = exp2_of(lg[j].x - ref);
-      lg[j].y = exp2_of(lg[j].y - ref);
-      sum += lg[j].x + lg[j].y;
-      if constexpr (!kBf16) {
-        const float2 step = lds_float2(kst + (S::kTokens + 8 * j + 2 * qd) * 4);
-        lg[j].x *= step.x;
-        lg[j].y *= step.y;
-        high = fmaxf(high, fmaxf(lg[j].x, lg[j].y));
-      }
-    }
-    if constexpr (!kBf16) {
-      if (__any_sync(kFullMask, high > limit)) {
-        high = fmaxf(high, __shfl_xor_sync(kFullMask, high, 1));
-        high = fmaxf(high, __shfl_xor_sync(kFullMask, high, 2));
-        if (high > limit) {
-          const int e = clamp_exponent(exponent_of(high));
-          const float to = power2(-e), f = to / up;
-          if (limit > 0.0f) {
-#pragma unroll
-            for (int n = 0; n < S::kOutTiles; ++n) {
-              out[n][0] *= f;
-              out[n][1] *= f;
-            }
-          }
-          up = to;
-          limit = power2(e + 8);
-        }
-      }
-    }
+    for (int j = 0; j < S::kTiles; ++j) sum += p[j].x + p[j].y;
 
-    // p (times the step and `up`) as the A operand: token pairs of tiles 2 kk, 2 kk + 1
+    // the weights as the A operand: token pairs of tiles 2 kk, 2 kk + 1
     uint32_t pa[S::kTokens / 16][4], pb[kBf16 ? S::kTokens / 16 : 1][2];
 #pragma unroll
     for (int kk = 0; kk < S::kTokens / 16; ++kk) {
       if constexpr (kBf16) {
-        pa[kk][0] = next_part(lg[2 * kk].x, lg[2 * kk].y);
-        pa[kk][1] = next_part(lg[2 * kk].x, lg[2 * kk].y);
-        pb[kk][0] = next_part(lg[2 * kk].x, lg[2 * kk].y);
-        pa[kk][2] = next_part(lg[2 * kk + 1].x, lg[2 * kk + 1].y);
-        pa[kk][3] = next_part(lg[2 * kk + 1].x, lg[2 * kk + 1].y);
-        pb[kk][1] = next_part(lg[2 * kk + 1].x, lg[2 * kk + 1].y);
+        pa[kk][0] = next_part(w[2 * kk].x, w[2 * kk].y);
+        pa[kk][1] = next_part(w[2 * kk].x, w[2 * kk].y);
+        pb[kk][0] = next_part(w[2 * kk].x, w[2 * kk].y);
+        pa[kk][2] = next_part(w[2 * kk + 1].x, w[2 * kk + 1].y);
+        pa[kk][3] = next_part(w[2 * kk + 1].x, w[2 * kk + 1].y);
+        pb[kk][1] = next_part(w[2 * kk + 1].x, w[2 * kk + 1].y);
       } else {
-        split2(lg[2 * kk].x * up, lg[2 * kk].y * up, pa[kk][0], pa[kk][1]);
-        split2(lg[2 * kk + 1].x * up, lg[2 * kk + 1].y * up, pa[kk][2], pa[kk][3]);
+        split2(w[2 * kk].x, w[2 * kk].y, pa[kk][0], pa[kk][1]);
+        split2(w[2 * kk + 1].x, w[2 * kk + 1].y, pa[kk][2], pa[kk][3]);
       }
     }
 
@@ -466,8 +525,6 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages 
     for (int dg = 0; dg < kGroups; ++dg) {
       float t[kWide][4];
 #pragma unroll
-      for (int n = 0; n < kWide; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.0f;
-#pragma unroll
       for (int kk = 0; kk < S::kTokens / 16; ++kk) {
         const uint32_t row = vst + (16 * kk + 2 * qd) * S::kPitch + 32 * dg + 4 * g;
         uint32_t w[4] = {lds32(row), lds32(row + S::kPitch), lds32(row + 8 * S::kPitch), lds32(row + 9 * S::kPitch)};
@@ -477,8 +534,11 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages 
           for (int n = 0; n < 2; ++n) {
             const uint32_t sel = n ? 0x7632 : 0x5410;
             const uint32_t v0 = __byte_perm(w[0], w[1], sel), v1 = __byte_perm(w[2], w[3], sel);
-            mma<FORMAT>(t[n], pa[kk], v0, v1);
-            mma<FORMAT>(t[n], third, v0, v1);
+            if (kk == 0)
+              mma<FORMAT, true>(t[n], pa[kk], v0, v1);
+            else
+              mma<FORMAT, false>(t[n], pa[kk], v0, v1);
+            mma<FORMAT, false>(t[n], third, v0, v1);
           }
         } else {
 #pragma unroll
@@ -486,8 +546,13 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages 
             uint32_t v0[2], v1[2];  // bytes n, n + 1 of both tokens of a pair, side by side
             widen<FORMAT>(__byte_perm(w[0], w[1], n ? 0x7362 : 0x5140), v0[0], v0[1]);
             widen<FORMAT>(__byte_perm(w[2], w[3], n ? 0x7362 : 0x5140), v1[0], v1[1]);
-            mma<FORMAT>(t[n], pa[kk], v0[0], v1[0]);
-            mma<FORMAT>(t[n + 1], pa[kk], v0[1], v1[1]);
+            if (kk == 0) {
+              mma<FORMAT, true>(t[n], pa[kk], v0[0], v1[0]);
+              mma<FORMAT, true>(t[n + 1], pa[kk], v0[1], v1[1]);
+            } else {
+              mma<FORMAT, false>(t[n], pa[kk], v0[0], v1[0]);
+              mma<FORMAT, false>(t[n + 1], pa[kk], v0[1], v1[1]);
+            }
           }
         }
       }
@@ -496,7 +561,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages 
     }
     if constexpr (!kBf16 && DT % 32 == 16) {  // the last 16 dims: two a token, n-tile i takes dim 2 g + i
       constexpr int n0 = S::kOutTiles - 2;
-      float t[2][4] = {};
+      float t[2][4];
 #pragma unroll
       for (int kk = 0; kk < S::kTokens / 16; ++kk) {
         const uint32_t row = vst + (16 * kk + 2 * qd) * S::kPitch + (DT - 16) + 2 * g;
@@ -504,8 +569,13 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages 
         uint32_t v0[2], v1[2];
         widen<FORMAT>(__byte_perm(w0, w1, 0x5140), v0[0], v0[1]);
         widen<FORMAT>(__byte_perm(w2, w3, 0x5140), v1[0], v1[1]);
-        mma<FORMAT>(t[0], pa[kk], v0[0], v1[0]);
-        mma<FORMAT>(t[1], pa[kk], v0[1], v1[1]);
+        if (kk == 0) {
+          mma<FORMAT, true>(t[0], pa[kk], v0[0], v1[0]);
+          mma<FORMAT, true>(t[1], pa[kk], v0[1], v1[1]);
+        } else {
+          mma<FORMAT, false>(t[0], pa[kk], v0[0], v1[0]);
+          mma<FORMAT, false>(t[1], pa[kk], v0[1], v1[1]);
+        }
       }
       add(n0, t[0]);
       add(n0 + 1, t[1]);
@@ -518,30 +588,34 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages 
   sum += __shfl_xor_sync(kFullMask, sum, 1);
   sum += __shfl_xor_sync(kFullMask, sum, 2);
   float* part = reinterpret_cast<float*>(smem + warp * S::kWarpBytes + g * S::kPartial);
-  const float back = kBf16 ? 1.0f : 1.0f / up;  // a power of two
   constexpr int kWideOut = kBf16 ? 2 : 4;
 #pragma unroll
   for (int n = 0; n < S::kOutTiles; ++n) {
     const bool tail = !kBf16 && DT % 32 == 16 && n >= S::kOutTiles - 2;
     const int wide = tail ? 2 : kWideOut, first = tail ? DT - 16 : n / kWideOut * 8 * kWideOut;
     const int of = tail ? n - (S::kOutTiles - 2) : n % kWideOut;
-    part[first + wide * (2 * qd) + of] = out[n][0] * back;
-    part[first + wide * (2 * qd + 1) + of] = out[n][1] * back;
+    part[first + wide * (2 * qd) + of] = out[n][0];
+    part[first + wide * (2 * qd + 1) + of] = out[n][1];
   }
   if (qd == 0) {
-    part[DT] = m;
+    part[DT] = ref;
     part[DT + 1] = sum;
   }
   __syncthreads();
 
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
-  float* dst = a.out + b * a.out_stride + (int64_t)hq * D;
-  if (splits == 1) {
-    for (int i = threadIdx.x; i < heads * D; i += kThreads) {
-      const int h = i / D, d = i - h * D;
-      const Joined j = join<false>(base + h * S::kPartial, S::kWarpBytes, kWarps, d, DT);
-      dst[i] = j.sum > 0.0f ? j.value / j.sum : 0.0f;  // no token: zeros
+  auto finish = [&](int h, int d, const Joined& j) {
+    if (clusters > 1) {  // [cluster][sequence][q head][dims, m, sum]
+      float* p = parts + (((int64_t)cluster * a.B + b) * a.q_heads + hq + h) * (D + 4);
+      p[d] = j.value;
+      if (d == 0) *reinterpret_cast<float2*>(p + D) = make_float2(j.m, j.sum);
+    } else {
+      a.out[b * a.out_stride + (int64_t)(hq + h) * D + d] = j.sum > 0.0f ? j.value / j.sum : 0.0f;  // no token: zeros
     }
+  };
+  if (splits == 1) {
+    for (int i = threadIdx.x; i < heads * D; i += kThreads)
+      finish(i / D, i % D, join<false>(base + i / D * S::kPartial, S::kWarpBytes, kWarps, i % D, DT));
     return;
   }
   // The CTA's own partials first (kept in registers across the barrier: the
@@ -566,24 +640,51 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a, KvPages 
     }
   }
   cluster_sync();
-  for (int i = split * kThreads + threadIdx.x; i < heads * D; i += splits * kThreads) {
-    const int h = i / D, d = i - h * D;
-    const Joined j = join<true>(base + h * S::kPartial, 0, splits, d, DT);
-    dst[i] = j.sum > 0.0f ? j.value / j.sum : 0.0f;
-  }
+  for (int i = split * kThreads + threadIdx.x; i < heads * D; i += splits * kThreads)
+    finish(i / D, i % D, join<true>(base + i / D * S::kPartial, 0, splits, i % D, DT));
   cluster_sync();  // no CTA leaves while another reads its partials
 }
 
-// Runs a sequence is split into: a power of two up to kMaxCluster, while the CTAs
-// stay within two an SM and every run may hold a step for each warp.
-int splits_for(int64_t rows, int64_t units, const DeviceInfo& dev) {
+// Joins the clusters' parts of one (sequence, q head): dim threadIdx.x.
+__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ parts, int clusters, int64_t rows, int D,
+                                                   int q_heads, float* __restrict__ out, int64_t out_stride) {
+  pdl_release_dependents();
+  pdl_wait_primary();
+  const int d = threadIdx.x;
+  const float* p = parts + (int64_t)blockIdx.x * (D + 4);
+  const int64_t apart = rows * (D + 4);
+  float m = kUnset, sum = 0.0f, value = 0.0f;
+  for (int i = 0; i < clusters; ++i) m = fmaxf(m, p[i * apart + D]);
+  for (int i = 0; i < clusters; ++i) {
+    const float f = exp2_of(p[i * apart + D] - m);
+    sum = fmaf(p[i * apart + D + 1], f, sum);
+    if (d < D) value = fmaf(p[i * apart + d], f, value);
+  }
+  if (d < D) out[blockIdx.x / q_heads * out_stride + blockIdx.x % q_heads * (int64_t)D + d] = sum > 0.0f ? value / sum : 0.0f;
+}
+
+int64_t rows_of(int64_t B, int q_heads, int kv_heads) {
+  return B * kv_heads * ((q_heads / kv_heads + kRowHeads - 1) / kRowHeads);
+}
+
+// Clusters a sequence may have: as many as two CTAs an SM leave room for beyond
+// one full-sized cluster a row.
+int clusters_for(int64_t rows) {
+  const int64_t n = 2 * kSms / (rows * kMaxCluster);
+  return (int)(n < 1 ? 1 : n > kMaxClusters ? kMaxClusters : n);
+}
+
+// CTAs of a cluster: a power of two up to kMaxCluster, while the CTAs stay within
+// two an SM and every warp may have a step.
+int splits_for(int64_t rows, int64_t steps) {
   int s = 1;
-  while (s < kMaxCluster && rows * s * 2 <= 2 * (int64_t)dev.num_sms && units >= 2 * s * kWarps) s *= 2;
+  while (s < kMaxCluster && rows * s * 2 <= 2 * kSms && steps >= 2 * s * kWarps) s *= 2;
   return s;
 }
 
 template <int FORMAT, int DT>
-cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, bool pdl, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, float* parts, bool pdl, const DeviceInfo& dev,
+                         cudaStream_t stream) {
   using S = Shape<FORMAT, DT>;
   const auto kernel = attend_kernel<FORMAT, DT>;
   static thread_local int configured_device = -1;
@@ -592,59 +693,75 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, bool pdl, const 
     if (err != cudaSuccess) return err;
     configured_device = dev.device;
   }
-  const int group = a.q_heads / c.heads;
-  const int64_t per_seq = (int64_t)c.heads * ((group + kRowHeads - 1) / kRowHeads);
+  const int64_t rows = rows_of(a.B, a.q_heads, c.heads), per_seq = rows / a.B;
   int64_t tokens = a.max_pages << c.page_shift;
   if (a.window > 0 && a.window < tokens) tokens = a.window;
-  const int splits = splits_for(a.B * per_seq, (tokens + S::kTokens - 1) / S::kTokens, dev);
-  const int64_t per_launch = (int64_t)0x7fffffff / (per_seq * splits);  // sequences a grid holds
+  const int64_t steps = (tokens + S::kTokens - 1) / S::kTokens;
+  const int splits = splits_for(rows, steps);
+  // further clusters once each of their warps has kClusterSteps steps (a second launch costs as much as several)
+  int clusters = parts ? clusters_for(rows) : 1;
+  while (clusters > 1 && steps < (int64_t)clusters * splits * kWarps * kClusterSteps) --clusters;
+  const int64_t per_launch = (int64_t)0x7fffffff / (per_seq * splits * clusters);  // sequences a grid holds
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
   for (int64_t b0 = 0; b0 < a.B; b0 += per_launch) {
     const int64_t n = a.B - b0 < per_launch ? a.B - b0 : per_launch;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(n * per_seq * splits), 1, 1);
+    cfg.gridDim = dim3((unsigned)(n * per_seq * splits * clusters), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    int na = 0;
+    cfg.numAttrs = 0;
     if (splits > 1) {
-      attr[na].id = cudaLaunchAttributeClusterDimension;
-      attr[na].val.clusterDim.x = (unsigned)splits;
-      attr[na].val.clusterDim.y = 1;
-      attr[na].val.clusterDim.z = 1;
-      ++na;
+      attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+      attr[cfg.numAttrs].val.clusterDim.x = (unsigned)splits;
+      attr[cfg.numAttrs].val.clusterDim.y = 1;
+      attr[cfg.numAttrs].val.clusterDim.z = 1;
+      ++cfg.numAttrs;
     }
     if (pdl) {
-      attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr[na].val.programmaticStreamSerializationAllowed = 1;
-      ++na;
+      attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+      ++cfg.numAttrs;
     }
-    cfg.attrs = na ? attr : nullptr;
-    cfg.numAttrs = (unsigned)na;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, c, b0, splits);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, c, b0, splits, clusters, parts);
     if (err != cudaSuccess) return err;
   }
-  return cudaSuccess;
+  if (clusters == 1) return cudaSuccess;
+  // clusters > 1 only with few rows: one launch above, and the join overlaps its tail
+  cfg.gridDim = dim3((unsigned)(a.B * a.q_heads), 1, 1);
+  cfg.blockDim = dim3((unsigned)((DT + 31) / 32 * 32), 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel, (const float*)parts, clusters, a.B * a.q_heads, c.head_dim, a.q_heads,
+                            a.out, a.out_stride);
 }
 
 template <int FORMAT>
-cudaError_t launch_format(const AttendArgs& a, const KvPages& c, bool pdl, const DeviceInfo& dev, cudaStream_t s) {
-  if (c.head_dim <= 64) return launch_shape<FORMAT, 64>(a, c, pdl, dev, s);
-  if (c.head_dim <= 80) return launch_shape<FORMAT, 80>(a, c, pdl, dev, s);
-  if (c.head_dim <= 96) return launch_shape<FORMAT, 96>(a, c, pdl, dev, s);
-  if (c.head_dim <= 128) return launch_shape<FORMAT, 128>(a, c, pdl, dev, s);
-  return launch_shape<FORMAT, 256>(a, c, pdl, dev, s);
+cudaError_t launch_format(const AttendArgs& a, const KvPages& c, float* parts, bool pdl, const DeviceInfo& dev,
+                          cudaStream_t s) {
+  if (c.head_dim <= 64) return launch_shape<FORMAT, 64>(a, c, parts, pdl, dev, s);
+  if (c.head_dim <= 80) return launch_shape<FORMAT, 80>(a, c, parts, pdl, dev, s);
+  if (c.head_dim <= 96) return launch_shape<FORMAT, 96>(a, c, parts, pdl, dev, s);
+  if (c.head_dim <= 128) return launch_shape<FORMAT, 128>(a, c, parts, pdl, dev, s);
+  return launch_shape<FORMAT, 256>(a, c, parts, pdl, dev, s);
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(int64_t, int, int, int) { return 0; }
+size_t attention_workspace_bytes(int64_t B, int q_heads, int kv_heads, int head_dim) {
+  const int clusters = clusters_for(rows_of(B, q_heads, kv_heads));
+  return clusters > 1 ? (size_t)clusters * B * q_heads * (head_dim + 4) * sizeof(float) : 0;
+}
 
-cudaError_t launch_attention(const AttendArgs& a, const KvPages& cache, void*, bool pdl, const DeviceInfo& dev,
-                             cudaStream_t stream) {
-  if (cache.format == BITLINEAR_KV_INT8) return launch_format<BITLINEAR_KV_INT8>(a, cache, pdl, dev, stream);
-  if (cache.format == BITLINEAR_KV_FP8) return launch_format<BITLINEAR_KV_FP8>(a, cache, pdl, dev, stream);
-  return launch_format<BITLINEAR_KV_BF16>(a, cache, pdl, dev, stream);
+cudaError_t launch_attention(const AttendArgs& a, const KvPages& cache, void* workspace, bool pdl,
+                             const DeviceInfo& dev, cudaStream_t stream) {
+  float* parts = static_cast<float*>(workspace);
+  if (cache.format == BITLINEAR_KV_INT8) return launch_format<BITLINEAR_KV_INT8>(a, cache, parts, pdl, dev, stream);
+  if (cache.format == BITLINEAR_KV_FP8) return launch_format<BITLINEAR_KV_FP8>(a, cache, parts, pdl, dev, stream);
+  return launch_format<BITLINEAR_KV_BF16>(a, cache, parts, pdl, dev, stream);
 }
 
 }  // namespace bitlinear

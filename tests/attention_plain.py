@@ -45,8 +45,10 @@ def held(cache, name):
     return (x if step is None else x * step.double()[..., None]).cpu().numpy()
 
 
-def attend(q, keys, values, table, lengths, page_size, scale, window=0):
-    """-> (out [B, Hq, D], bound): keys, values [pages, heads, page_size, D] float64."""
+def attend(q, cache, table, lengths, page_size, scale, window=0):
+    """-> (out [B, Hq, D], bound) over the cache's exact values, in float64."""
+    keys, values = held(cache, "k"), held(cache, "v")
+    steps = None if cache[3] is None else cache[3].double().cpu().numpy()
     B, Hq, D = q.shape
     Hkv, G = keys.shape[1], Hq // keys.shape[1]
     out, bound = np.zeros((B, Hq, D)), np.zeros((B, Hq, D))
@@ -70,6 +72,13 @@ def attend(q, keys, values, table, lengths, page_size, scale, window=0):
             d = abs(scale) * (np.abs(k) @ np.abs(qq)) * 2 * U * (D + 16)
             rel = np.expm1(2 * (d.max() + 8 * U + 2 * U * (x.max() - x).clip(0, 100).max())) + 2 * U * (len(x) + 64)
             bound[b, h] = 2 * rel * (w @ np.abs(v)) / w.sum() + 1e-37
+            # 8-bit codes are weighted by p * step as two fp16 parts, in units that make the largest such
+            # weight 1 or more.  Below 2^-14 the first part is subnormal (off by 2^-25), what it leaves,
+            # times 2^11, is again (off by 2^-25 / 2^11): 2^-36 of the largest weight a token, times its code.
+            if steps is not None:
+                s = steps[p, h // G, o]
+                codes = np.abs(v) / np.where(s > 0, s, 1.0)[:, None]
+                bound[b, h] += 2.0 ** -36 * (w * s).max() * codes.sum(0) / w.sum()
     return out, bound
 
 

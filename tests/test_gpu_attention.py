@@ -257,7 +257,7 @@ def attend_case(fmt, Hq, Hk, D, page, lengths, window=0, seed=0, value_std=1.0, 
     need = bl.bitlinear_attention_workspace(B, Hq, Hk, D) if workspace else 0
     ws, ws_full = guarded(need, torch.uint8, 0x3C) if need else (None, None)
     bl.bitlinear_attention(q, cache, ints(table.tolist()), ints(lengths), out, workspace=ws, window=window, scale=scale)
-    want, bound = plain.attend(q.cpu().numpy(), plain.held(cache, "k"), plain.held(cache, "v"), table, lengths, page,
+    want, bound = plain.attend(q.cpu().numpy(), cache, table, lengths, page,
                                D ** -0.5 if scale is None else scale, window)
     within(out, want, bound)
     check_canary(full, -7.0)
@@ -316,6 +316,22 @@ def test_attention_values_of_one_sign_and_peaked_rows(fmt):
     attend_case(fmt, 4, 1, 96, 16, [600, 100], seed=10, value_std=1e-3, spread_steps=True)
 
 
+@pytest.mark.parametrize("fmt", plain.FORMATS)
+def test_attention_over_rows_of_zeros(fmt):
+    """Rows never written in a cache of zeros: keys and values of 0 (steps of 0), which count in the sum."""
+    B, H, D, page = 3, 2, 64, 16
+    cache = tuple(None if c is None else torch.zeros_like(c) for c in plain.make_cache(fmt, 12, H, page, D, 0))
+    table = np.arange(12).reshape(3, 4)
+    t = torch.tensor([5, 40, 41], device="cuda")
+    for b, rows in ((1, t[:1]), (2, t)):
+        plain.fill_row(cache, fmt, torch.tensor(table[b], device="cuda")[rows // page], rows % page,
+                       normal((len(rows), H, D), b).cuda() * 30, normal((len(rows), H, D), b + 5).cuda())
+    q, out = normal((B, 2 * H, D), 3).cuda(), torch.full((B, 2 * H, D), -1.0, device="cuda")
+    bl.bitlinear_attention(q, cache, ints(table.tolist()), ints([33, 60, 64]), out)
+    want, bound = plain.attend(q.cpu().numpy(), cache, table, [33, 60, 64], page, D ** -0.5)
+    within(out, want, bound)
+
+
 def test_attention_length_beyond_the_table_counts_as_the_table():
     cache = plain.make_cache("int8", 4, 1, 16, 64, 0)
     t = torch.arange(32, device="cuda")
@@ -340,7 +356,7 @@ def test_attention_strides_and_one_page_list_for_all_rows():
     out = out_wide[:, 4:4 + H * D].unflatten(1, (H, D))
     lengths = [n + 1 + i for i in range(rows)]
     bl.bitlinear_attention(q, cache[:2], table.expand(rows, 5), ints(lengths), out)
-    want, bound = plain.attend(q.cpu().numpy(), plain.held(cache, "k"), plain.held(cache, "v"), table.expand(rows, 5).cpu().numpy(), lengths, page, D ** -0.5)
+    want, bound = plain.attend(q.cpu().numpy(), cache, table.expand(rows, 5).cpu().numpy(), lengths, page, D ** -0.5)
     within(out, want, bound)
     assert (out_wide[:, :4] == 2.5).all() and (out_wide[:, 4 + H * D:] == 2.5).all()
 
@@ -364,7 +380,7 @@ def test_cache_past_32_bit_offsets():
     q, out = normal((1, H, D), 3).cuda(), torch.empty(1, H, D, device="cuda")
     bl.bitlinear_attention(q, cache, table, ints([T]), out)
     small = tuple(c[-1:] for c in cache)
-    want, bound = plain.attend(q.cpu().numpy(), plain.held(small, "k"), plain.held(small, "v"), np.array([[0]]), [T], page, D ** -0.5)
+    want, bound = plain.attend(q.cpu().numpy(), small, np.array([[0]]), [T], page, D ** -0.5)
     within(out, want, bound)
 
 
@@ -391,7 +407,7 @@ def decode_steps(fmt, B, Hq, Hk, D, page, steps, run):
             st[x].copy_(normal(st[x].shape, 1000 * j + i))
         one()
         torch.cuda.synchronize()
-        want, bound = plain.attend(st["q"].cpu().numpy(), plain.held(st["cache"], "k"), plain.held(st["cache"], "v"),
+        want, bound = plain.attend(st["q"].cpu().numpy(), st["cache"],
                                    st["table"].cpu().numpy(), [i + 1] * B, page, D ** -0.5)
         within(st["out"], want, bound)
         st["positions"] += 1
