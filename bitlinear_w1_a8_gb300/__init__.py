@@ -405,33 +405,53 @@ def bitlinear_linear_ws(x, weights, xq, x_scale, workspace, mul=None, rms_weight
 
 
 # --- rotary positions, the paged key-value cache and attention over it ---
+#
+# These calls take many tensors and are made once or twice a layer and token, so each
+# checks its tensors in one expression and goes through them one by one only when that
+# fails: for an unusual layout, or to say what is wrong.
 
 
-def _rows(t, name, T, H=None, D=None):
-    """The row stride (elements) of fp32 [T, H, D] rows: heads side by side, rows any
-    stride apart.  H, D None: any."""
+def _device(t, name):
+    """The index of the tensor's device, which must be the current one: the library launches there."""
     import torch
-    try:  # the common case first; the detailed checks only where it fails
-        shape = t.shape
-        if (t.is_cuda and t.dtype == torch.float32 and t.is_contiguous() and len(shape) == 3
-                and shape == (T, shape[1] if H is None else H, shape[2] if D is None else D)):
-            return shape[1] * shape[2]
+    try:
+        at = t.get_device()
     except AttributeError:
-        pass
+        at = -1
+    if at < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if at != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current device cuda:{torch.cuda.current_device()}, got {t.device}")
+    return at
+
+
+def _need_on(t, at, dtype, name, shape=None):
+    _need(t, dtype, name, shape)
+    if t.get_device() != at:
+        raise ValueError(f"{name} must be on cuda:{at}, got {t.device}")
+
+
+def _rows(t, at, name, shape):
+    """The row stride (elements) of fp32 [T, H, D] rows: heads side by side, rows any stride apart."""
+    import torch
     if not getattr(t, "is_cuda", False):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
-    if len(shape) != 3 or shape[0] != T or (H is not None and shape[1] != H) or (D is not None and shape[2] != D):
-        raise ValueError(f"{name} must have shape ({T}, {'heads' if H is None else H}, "
-                         f"{'head_dim' if D is None else D}), got {tuple(shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != at:
+        raise ValueError(f"{name} must be on cuda:{at}, got {t.device}")
+    T, H, D = shape
+    if t.is_contiguous():  # strides of dims of size 1 say nothing
+        return H * D
     strides = t.stride()
-    if (shape[2] > 1 and strides[2] != 1) or (shape[1] > 1 and strides[1] != shape[2]):
+    if strides[2] != 1 or (H > 1 and strides[1] != D):
         raise ValueError(f"{name}'s heads must lie side by side in each row, got strides {tuple(strides)}")
-    return strides[0] if T > 1 else shape[1] * shape[2]
+    return strides[0] if T > 1 else H * D
 
 
-def _page_table(t, rows=None):
+def _page_table(t, at, rows=None):
     """(rows, columns, row stride) of the int32 page table: contiguous rows, any stride apart."""
     import torch
     if not getattr(t, "is_cuda", False) or t.dtype != torch.int32:
@@ -439,6 +459,8 @@ def _page_table(t, rows=None):
     shape = t.shape
     if len(shape) != 2 or (rows is not None and shape[0] != rows):
         raise ValueError(f"page_table must be [{'sequences' if rows is None else rows}, pages], got {tuple(shape)}")
+    if t.get_device() != at:
+        raise ValueError(f"page_table must be on cuda:{at}, got {t.device}")
     n, cols = shape
     if t.is_contiguous():
         return n, cols, cols
@@ -447,48 +469,44 @@ def _page_table(t, rows=None):
     return n, cols, t.stride(0) if n > 1 else cols
 
 
-def _same_device(tensors):
-    """Every tensor on the current device: the library launches there."""
+def _kv_pages(cache, at):
+    """BitLinearKVPages of (k, v, k_step, v_step), the steps None or left out for bf16."""
     import torch
-    at = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != at:
-            raise ValueError(f"every tensor must be on the current device cuda:{at}, got one on {t.device}")
-
-
-_FORMATS = {}  # torch dtype -> BITLINEAR_KV_*, once torch is there
-
-
-def _kv_pages(cache):
-    """BitLinearKVPages of (k, v, k_step, v_step), the steps None for bf16."""
-    import torch
-    if not _FORMATS:
-        _FORMATS.update({torch.int8: KV_INT8, torch.float8_e4m3fn: KV_FP8, torch.bfloat16: KV_BF16})
     k, v = cache[0], cache[1]
     k_step, v_step = (cache[2], cache[3]) if len(cache) > 2 else (None, None)
     if not getattr(k, "is_cuda", False):
         raise TypeError("the cache must be CUDA tensors")
-    fmt, shape = _FORMATS.get(k.dtype), k.shape
-    if fmt is None:
-        raise TypeError(f"the cache must be int8, float8_e4m3fn or bfloat16, got {k.dtype}")
+    dtype, shape = k.dtype, k.shape
     if len(shape) != 4:
         raise ValueError(f"the cache's k must be [pages, heads, page_size, head_dim], got {tuple(shape)}")
-    _need(k, k.dtype, "the cache's k")
-    _need(v, k.dtype, "the cache's v", shape)
-    if fmt == KV_BF16:
+    if dtype is torch.bfloat16:
         if k_step is not None or v_step is not None:
             raise ValueError("a bfloat16 cache has no steps")
-        return BitLinearKVPages(k.data_ptr(), v.data_ptr(), None, None, *shape, fmt)
-    _need(k_step, torch.float32, "the cache's k_step", shape[:3])
-    _need(v_step, torch.float32, "the cache's v_step", shape[:3])
-    return BitLinearKVPages(k.data_ptr(), v.data_ptr(), k_step.data_ptr(), v_step.data_ptr(), *shape, fmt)
+        _need_on(k, at, dtype, "the cache's k")
+        _need_on(v, at, dtype, "the cache's v", shape)
+        return BitLinearKVPages(k.data_ptr(), v.data_ptr(), None, None, *shape, KV_BF16)
+    if dtype is not torch.int8 and dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"the cache must be int8, float8_e4m3fn or bfloat16, got {dtype}")
+    rows = shape[:3]
+    f32 = torch.float32
+    if not (v_step is not None and k_step is not None and k.get_device() == v.get_device() == k_step.get_device()
+            == v_step.get_device() == at and v.dtype is dtype and k_step.dtype is f32 and v_step.dtype is f32
+            and v.shape == shape and k_step.shape == rows and v_step.shape == rows and k.is_contiguous()
+            and v.is_contiguous() and k_step.is_contiguous() and v_step.is_contiguous()):
+        _need_on(k, at, dtype, "the cache's k")
+        _need_on(v, at, dtype, "the cache's v", shape)
+        _need_on(k_step, at, f32, "the cache's k_step", rows)
+        _need_on(v_step, at, f32, "the cache's v_step", rows)
+    return BitLinearKVPages(k.data_ptr(), v.data_ptr(), k_step.data_ptr(), v_step.data_ptr(), *shape,
+                            KV_INT8 if dtype is torch.int8 else KV_FP8)
 
 
-def _rope_spec(rope):
+def _rope_spec(rope, at):
     """BitLinearRopeSpec of (freq, layout) or (freq, layout, amplitude)."""
     import torch
     freq = rope[0]
-    _need(freq, torch.float64, "rope's freq")
+    if not (freq.get_device() == at and freq.dtype is torch.float64 and freq.is_contiguous()):
+        _need_on(freq, at, torch.float64, "rope's freq")
     return BitLinearRopeSpec(freq.data_ptr(), 2 * freq.numel(), int(rope[1]), float(rope[2]) if len(rope) > 2 else 1.0)
 
 
@@ -514,15 +532,39 @@ def bitlinear_rope(x, positions, rope, y, flags: int = 0, stream=None):
     Rows may lie any multiple of 4 floats apart.
     """
     import torch
-    T = x.shape[0]
-    x_stride = _rows(x, "x", T)
-    _, H, D = x.shape
-    y_stride = _rows(y, "y", T, H, D)
-    _need(positions, torch.int32, "positions", (T,))
-    spec = _rope_spec(rope)
-    _same_device((x, y, positions, rope[0]))
-    _check(load_library().bitlinear_rope(_ptr(x), x_stride, T, H, D, _ptr(positions), spec, _ptr(y), y_stride,
-                                         int(flags), _stream(stream)), "bitlinear_rope")
+    at = _device(x, "x")
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError(f"x must be [rows, heads, head_dim], got {tuple(shape)}")
+    T, H, D = shape
+    x_stride = y_stride = H * D
+    f32 = torch.float32
+    if not (y.get_device() == positions.get_device() == at and x.dtype is f32 and y.dtype is f32
+            and positions.dtype is torch.int32 and y.shape == shape and positions.shape == (T,)
+            and x.is_contiguous() and y.is_contiguous() and positions.is_contiguous()):
+        x_stride, y_stride = _rows(x, at, "x", shape), _rows(y, at, "y", shape)
+        _need_on(positions, at, torch.int32, "positions", (T,))
+    _check(load_library().bitlinear_rope(x.data_ptr(), x_stride, T, H, D, positions.data_ptr(), _rope_spec(rope, at),
+                                         y.data_ptr(), y_stride, flags, _stream(stream)), "bitlinear_rope")
+
+
+def _row_places(positions, page_table, seq, T, at):
+    """(positions, seq, table addresses, table stride, sequences, pages) of T rows."""
+    import torch
+    i32 = torch.int32
+    if (positions.dtype is i32 and page_table.dtype is i32 and positions.get_device() == page_table.get_device() == at
+            and positions.shape == (T,) and positions.is_contiguous() and page_table.is_contiguous()
+            and len(page_table.shape) == 2):
+        n, cols = page_table.shape
+        stride = cols
+    else:
+        _need_on(positions, at, i32, "positions", (T,))
+        n, cols, stride = _page_table(page_table, at)
+    if seq is None:
+        return positions.data_ptr(), None, page_table.data_ptr(), stride, n, cols
+    if not (seq.dtype is i32 and seq.get_device() == at and seq.shape == (T,) and seq.is_contiguous()):
+        _need_on(seq, at, i32, "seq", (T,))
+    return positions.data_ptr(), seq.data_ptr(), page_table.data_ptr(), stride, n, cols
 
 
 def bitlinear_kv_append(k, v, cache, positions, page_table, seq=None, q=None, q_out=None, rope=None,
@@ -536,44 +578,51 @@ def bitlinear_kv_append(k, v, cache, positions, page_table, seq=None, q=None, q_
     sequence i.  Rows with a negative position are padding.  rope: as for bitlinear_rope.
     """
     import torch
-    pages = _kv_pages(cache)
-    T, Hk, D = k.shape[0], pages.num_heads, pages.head_dim
-    k_stride = _rows(k, "k", T, Hk, D)
-    v_stride = _rows(v, "v", T, Hk, D)
-    _need(positions, torch.int32, "positions", (T,))
-    if seq is not None:
-        _need(seq, torch.int32, "seq", (T,))
-    num_seqs, max_pages, table_stride = _page_table(page_table)
+    at = _device(k, "k")
+    pages = _kv_pages(cache, at)
+    f32, T, Hk, D = torch.float32, k.shape[0], pages.num_heads, pages.head_dim
+    shape = (T, Hk, D)
+    k_stride = v_stride = Hk * D
+    if not (v.get_device() == at and k.dtype is f32 and v.dtype is f32 and k.shape == shape and v.shape == shape
+            and k.is_contiguous() and v.is_contiguous()):
+        k_stride, v_stride = _rows(k, at, "k", shape), _rows(v, at, "v", shape)
+    positions_at, seq_at, table_at, table_stride, num_seqs, max_pages = _row_places(positions, page_table, seq, T, at)
     Hq = q_stride = q_out_stride = 0
+    q_at = q_out_at = None
     if q is not None:
-        q_stride = _rows(q, "q", T, None, D)
+        if q.dim() != 3:
+            raise ValueError(f"q must be [rows, heads, head_dim], got {tuple(q.shape)}")
         Hq = q.shape[1]
-        q_out_stride = _rows(q_out, "q_out", T, Hq, D)
+        q_shape = (T, Hq, D)
+        q_stride = q_out_stride = Hq * D
+        if not (q_out is not None and q.get_device() == q_out.get_device() == at and q.dtype is f32
+                and q_out.dtype is f32 and q.shape == q_shape and q_out.shape == q_shape and q.is_contiguous()
+                and q_out.is_contiguous()):
+            q_stride, q_out_stride = _rows(q, at, "q", q_shape), _rows(q_out, at, "q_out", q_shape)
+        q_at, q_out_at = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    spec = None if rope is None else _rope_spec(rope)
-    _same_device((k, v, *cache, positions, page_table, seq, q, q_out, None if rope is None else rope[0]))
     _check(load_library().bitlinear_kv_append(
-        _ptr(q), q_stride, Hq, _ptr(q_out), q_out_stride, _ptr(k), k_stride, _ptr(v), v_stride, T, _ptr(positions),
-        _ptr(seq), _ptr(page_table), table_stride, num_seqs, max_pages, spec, pages, int(flags), _stream(stream)),
-        "bitlinear_kv_append")
+        q_at, q_stride, Hq, q_out_at, q_out_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, T, positions_at,
+        seq_at, table_at, table_stride, num_seqs, max_pages, None if rope is None else _rope_spec(rope, at), pages,
+        flags, _stream(stream)), "bitlinear_kv_append")
 
 
 def bitlinear_kv_read(cache, positions, page_table, k_out, v_out, seq=None, flags: int = 0, stream=None):
     """k_out, v_out [T, heads, head_dim] fp32 = the cached rows at (seq[i], positions[i])."""
     import torch
-    pages = _kv_pages(cache)
-    T, Hk, D = k_out.shape[0], pages.num_heads, pages.head_dim
-    k_stride = _rows(k_out, "k_out", T, Hk, D)
-    v_stride = _rows(v_out, "v_out", T, Hk, D)
-    _need(positions, torch.int32, "positions", (T,))
-    if seq is not None:
-        _need(seq, torch.int32, "seq", (T,))
-    num_seqs, max_pages, table_stride = _page_table(page_table)
-    _same_device((k_out, v_out, *cache, positions, page_table, seq))
+    at = _device(k_out, "k_out")
+    pages = _kv_pages(cache, at)
+    f32, T, Hk, D = torch.float32, k_out.shape[0], pages.num_heads, pages.head_dim
+    shape = (T, Hk, D)
+    k_stride = v_stride = Hk * D
+    if not (v_out.get_device() == at and k_out.dtype is f32 and v_out.dtype is f32 and k_out.shape == shape
+            and v_out.shape == shape and k_out.is_contiguous() and v_out.is_contiguous()):
+        k_stride, v_stride = _rows(k_out, at, "k_out", shape), _rows(v_out, at, "v_out", shape)
+    positions_at, seq_at, table_at, table_stride, num_seqs, max_pages = _row_places(positions, page_table, seq, T, at)
     _check(load_library().bitlinear_kv_read(
-        pages, T, _ptr(positions), _ptr(seq), _ptr(page_table), table_stride, num_seqs, max_pages, _ptr(k_out),
-        k_stride, _ptr(v_out), v_stride, int(flags), _stream(stream)), "bitlinear_kv_read")
+        pages, T, positions_at, seq_at, table_at, table_stride, num_seqs, max_pages, k_out.data_ptr(), k_stride,
+        v_out.data_ptr(), v_stride, flags, _stream(stream)), "bitlinear_kv_read")
 
 
 def bitlinear_attention_workspace(B: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
@@ -587,17 +636,30 @@ def bitlinear_attention(q, cache, page_table, lengths, out, workspace=None, scal
     sequence (the last `window` of them when it is not 0); scale None: 1 / sqrt(head_dim).
     cache and page_table: as for bitlinear_kv_append; lengths: int32 [B]."""
     import torch
-    pages = _kv_pages(cache)
-    B, D = q.shape[0], pages.head_dim
-    q_stride = _rows(q, "q", B, None, D)
-    Hq = q.shape[1]
-    out_stride = _rows(out, "out", B, Hq, D)
-    _need(lengths, torch.int32, "lengths", (B,))
-    _, max_pages, table_stride = _page_table(page_table, B)
+    at = _device(q, "q")
+    pages = _kv_pages(cache, at)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != pages.head_dim:
+        raise ValueError(f"q must be [sequences, heads, {pages.head_dim}], got {tuple(shape)}")
+    B, Hq, D = shape
+    q_stride = out_stride = Hq * D
+    f32, i32 = torch.float32, torch.int32
+    if (out.get_device() == page_table.get_device() == lengths.get_device() == at and q.dtype is f32
+            and out.dtype is f32 and page_table.dtype is i32 and lengths.dtype is i32 and out.shape == shape
+            and lengths.shape == (B,) and page_table.shape[0] == B and len(page_table.shape) == 2
+            and q.is_contiguous() and out.is_contiguous() and page_table.is_contiguous()
+            and lengths.is_contiguous()):
+        table_stride = max_pages = page_table.shape[1]
+    else:
+        q_stride, out_stride = _rows(q, at, "q", shape), _rows(out, at, "out", shape)
+        _need_on(lengths, at, i32, "lengths", (B,))
+        _, max_pages, table_stride = _page_table(page_table, at, B)
+    space = None
     if workspace is not None:
-        _need(workspace, torch.uint8, "workspace")
-    _same_device((q, out, *cache, page_table, lengths, workspace))
+        if not (workspace.get_device() == at and workspace.dtype is torch.uint8 and workspace.is_contiguous()):
+            _need_on(workspace, at, torch.uint8, "workspace")
+        space = workspace.data_ptr()
     _check(load_library().bitlinear_attention(
-        _ptr(q), q_stride, B, Hq, pages, _ptr(page_table), table_stride, max_pages, _ptr(lengths), int(window),
-        D ** -0.5 if scale is None else float(scale), _ptr(out), out_stride, _ptr(workspace),
-        0 if workspace is None else workspace.numel(), int(flags), _stream(stream)), "bitlinear_attention")
+        q.data_ptr(), q_stride, B, Hq, pages, page_table.data_ptr(), table_stride, max_pages, lengths.data_ptr(),
+        window, D ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, space,
+        0 if workspace is None else workspace.numel(), flags, _stream(stream)), "bitlinear_attention")
