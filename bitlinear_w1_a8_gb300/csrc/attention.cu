@@ -30,9 +30,11 @@
 // The MMA sums of a step (16 or 32 tokens) start from zero and are added to fp32
 // sums in registers: a chain of roundings no longer than the steps of a warp.
 //
-// Where one cluster a sequence leaves SMs idle (few heads, long sequences), several
-// clusters take a sequence, each writing its joined part to the workspace, and a
-// second small launch joins those.
+// With a workspace and long sequences, rows (a key head of a sequence, for up to 8 q
+// heads) get CTAs in proportion to their steps instead, all of them resident at once,
+// so lengths of any mix end together; a row of several CTAs leaves their partials in
+// the workspace and a second small launch joins them in the order of the CTAs.
+// Without one, rows that fill the GPU more than once start with the longest.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -46,9 +48,10 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRowHeads = 8;   // q heads of one CTA
 constexpr int kStages = 2;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxClusters = 16;  // clusters a sequence, with a workspace
-constexpr int kClusterSteps = 8;  // steps a warp has before a second cluster is worth a second launch
 constexpr int kSms = 152;
+constexpr int kLeastSteps = 2;    // steps a warp at least: short rows take fewer CTAs
+constexpr int kShareSeqs = 1024;  // sequences that a CTA adds up to find its row
+constexpr int kSortSeqs = kThreads;  // sequences that a CTA ranks by length
 constexpr float kLimit = 256.0f;  // the largest weight before the reference moves
 constexpr float kUnset = -1e30f;  // a reference below every logit
 constexpr float kLeastStep = 8.2718061e-25f;  // 2^-80: a value's step counts as that at least (a cache of zeros holds 0)
@@ -62,7 +65,7 @@ struct Shape {
   // rows an odd number of 16-byte chunks apart: the fragments' loads (8 rows x 4
   // words, or 4 pairs of rows x 8 words) then touch every bank once
   static constexpr int kPitch = (kRow / 16) % 2 ? kRow : kRow + 16;
-  static constexpr int kTokens = kRow <= 128 ? 32 : 16;
+  static constexpr int kTokens = kRow <= 96 || (kBytes == 2 && kRow <= 128) ? 32 : 16;
   static constexpr int kTiles = kTokens / 8;       // n-tiles of the logits
   static constexpr int kSteps = DT / 16;           // k-steps of the logits
   static constexpr int kChunks = kRow / 16;
@@ -71,7 +74,9 @@ struct Shape {
   static constexpr int kWarpBytes = kStages * kStage;
   static constexpr int kPartial = (DT + 4) * 4;    // a head's weighted sum, m and sum, padded to 16 bytes
   static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes;
-  static constexpr int kCtas = DT <= 96 ? 4 : DT <= 128 ? 3 : 2;  // CTAs an SM that the registers allow
+  static constexpr int kCtas = DT <= (kBytes == 1 ? 128 : 96) ? 4 : DT <= 128 ? 3 : 2;  // CTAs an SM that the registers allow
+  static constexpr int kFit = (int)(227 * 1024 / (kSmem + 1024));   // and that its shared memory does
+  static constexpr int kResident = kCtas < kFit ? kCtas : kFit;
   static_assert(kRowHeads * kPartial <= kWarpBytes, "a warp's partials reuse its ring");
   static_assert(kStage % 16 == 0 && DT % 16 == 0, "");
 };
@@ -273,24 +278,118 @@ __device__ __forceinline__ Joined join(uint32_t base, uint32_t apart, int parts,
   return j;
 }
 
+// How rows are shared out: `splits` CTAs each (a cluster), or (splits == 0) in
+// proportion to their steps.
+struct Shares {
+  int64_t b0;      // the launch's first sequence
+  int splits;
+  bool sorted;     // sequences in order of length, the longest first
+  float* parts;    // splits == 0: [CTA][q heads of a row, at most 8][dims, m, sum]
+  int2* rows;      // splits == 0: a row's first CTA and how many it has
+};
+
+// Tokens first <= t < len of a sequence that count, in steps of T from first / T on.
+template <int T>
+struct Span {
+  int64_t first, len;
+  __device__ __forceinline__ Span(int64_t length, int64_t most, int64_t window) {
+    len = length < most ? length : most;
+    first = window > 0 && len > window ? len - window : 0;
+  }
+  __device__ __forceinline__ int64_t begin() const { return first / T * T; }
+  __device__ __forceinline__ int64_t steps() const { return len > first ? (len + T - 1) / T - first / T : 0; }
+};
+
+// Sums of a value over the block's threads: of those up to this one, and of all.
+__device__ __forceinline__ int2 block_sums(int mine, int* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int upto = mine, all = 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(kFullMask, upto, o);
+    if (lane >= o) upto += n;
+  }
+  if (lane == 31) scratch[warp] = upto;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) upto += scratch[w];
+    all += scratch[w];
+  }
+  __syncthreads();
+  return make_int2(upto, all);
+}
+
+// This CTA's row and which part of it.  Every row with any step has ceil(steps /
+// share) CTAs, in the order of the rows; share is the least for which the grid has
+// enough of them (each row rounds up by less than one).
+struct Part {
+  int64_t b;
+  int row, part, parts;  // parts == 0: the CTA has nothing
+};
+template <int T>
+__device__ __forceinline__ Part find_part(const AttendArgs& a, int64_t most, int rows_a_seq) {
+  __shared__ int scratch[kWarps], found[3];
+  const int each = ((int)a.B + kThreads - 1) / kThreads, from = threadIdx.x * each, to = min((int)a.B, from + each);
+  auto steps_of = [&](int b) { return (int)Span<T>(a.lengths[b], most, a.window).steps(); };
+  int steps = 0, some = 0;
+  for (int b = from; b < to; ++b) {
+    const int n = steps_of(b);
+    steps += n;
+    some += n > 0;
+  }
+  const int total = block_sums(steps, scratch).y * rows_a_seq, rows = block_sums(some, scratch).y * rows_a_seq;
+  const int spare = (int)gridDim.x - rows;  // > 0: the host takes this path for rows well below the grid
+  const int share = max((total + spare - 1) / spare, kLeastSteps * kWarps);
+  int ctas = 0;
+  for (int b = from; b < to; ++b) ctas += (steps_of(b) + share - 1) / share * rows_a_seq;
+  if (threadIdx.x == 0) found[2] = 0;
+  const int upto = block_sums(ctas, scratch).x;
+  int at = upto - ctas;
+  for (int b = from; b < to; ++b) {
+    const int n = (steps_of(b) + share - 1) / share;
+    if ((int)blockIdx.x >= at && (int)blockIdx.x < at + n * rows_a_seq) {
+      found[0] = b;
+      found[1] = at;
+      found[2] = n;
+    }
+    at += n * rows_a_seq;
+  }
+  __syncthreads();
+  Part p = {found[0], 0, 0, found[2]};
+  if (p.parts > 0) {
+    const int i = (int)blockIdx.x - found[1];
+    p.row = i / p.parts;
+    p.part = i - p.row * p.parts;
+  }
+  return p;
+}
+
+// The sequence that comes at place `at` when the longest is first.
+__device__ __forceinline__ int64_t by_length(const AttendArgs& a, int at) {
+  __shared__ int lengths[kSortSeqs];
+  __shared__ int found;
+  const int B = (int)a.B, b = threadIdx.x, mine = b < B ? a.lengths[b] : 0;
+  if (b < B) lengths[b] = mine;
+  __syncthreads();
+  int rank = 0;
+  for (int i = 0; i < B; ++i) rank += lengths[i] > mine || (lengths[i] == mine && i < b);
+  if (b < B && rank == at) found = b;
+  __syncthreads();
+  return found;
+}
+
 template <int FORMAT, int DT>
 __global__ void __launch_bounds__(kThreads, Shape<FORMAT, DT>::kCtas)
-attend_kernel(AttendArgs a, KvPages c, int64_t b0, int splits, int clusters, float* __restrict__ parts) {
+attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   using S = Shape<FORMAT, DT>;
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_release_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
-  const int group = a.q_heads / c.heads, groups = (group + kRowHeads - 1) / kRowHeads;
-  const int split = blockIdx.x % splits;  // the CTA's rank in its cluster
-  int64_t rest = blockIdx.x / splits;
-  const int cluster = (int)(rest % clusters);
-  rest /= clusters;
-  const int first_of_group = (int)(rest % groups) * kRowHeads;
-  rest /= groups;
-  const int hk = (int)(rest % c.heads);
-  const int64_t b = b0 + rest / c.heads;
-  const int heads = min(kRowHeads, group - first_of_group), hq = hk * group + first_of_group;
+  const int group = a.q_heads / c.heads, groups = (group + kRowHeads - 1) / kRowHeads, rows_a_seq = c.heads * groups;
   const int D = c.head_dim;
+  const int64_t most = a.max_pages << c.page_shift;
+  const bool shared_out = sh.splits == 0;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * S::kWarpBytes;
   if (D < DT) {  // the padding of every row, once: copies never write it
     for (int i = lane; i < S::kWarpBytes / 16; i += 32)
@@ -299,30 +398,51 @@ attend_kernel(AttendArgs a, KvPages c, int64_t b0, int splits, int clusters, flo
   }
   pdl_wait_primary();
 
-  Source r;
-  const int64_t most = a.max_pages << c.page_shift;
-  r.len = a.lengths[b];
+  // The CTA's row (sequence b, head `row` of its key heads and groups of q heads)
+  // and its place among the row's CTAs.
+  int64_t b;
+  int row, split, splits;
+  if (shared_out) {
+    const Part p = find_part<S::kTokens>(a, most, rows_a_seq);
+    if (p.parts == 0) return;
+    b = p.b;
+    row = p.row;
+    split = p.part;
+    splits = p.parts;
+    if (split == 0 && threadIdx.x == 0) sh.rows[b * rows_a_seq + row] = make_int2(blockIdx.x, splits);
+  } else {
+    splits = sh.splits;
+    split = blockIdx.x % splits;
+    const int64_t rest = blockIdx.x / splits;
+    row = (int)(rest % rows_a_seq);
+    b = sh.sorted ? by_length(a, (int)(rest / rows_a_seq)) : sh.b0 + rest / rows_a_seq;
+  }
+
+  // The warp's steps are every (splits * kWarps)-th one of the row's.
   const int32_t* table = a.table + b * a.table_stride;
-  const int64_t head_row = (int64_t)hk << c.page_shift;
-  r.k = static_cast<const uint8_t*>(c.k) + head_row * D * S::kBytes;
-  r.v = static_cast<const uint8_t*>(c.v) + head_row * D * S::kBytes;
-  r.ks = c.k_step + head_row;
-  r.vs = c.v_step + head_row;
-  // The warp's steps are every (clusters * splits * kWarps)-th one, from the window's first on.
-  const int64_t lap = (int64_t)clusters * splits * kWarps * S::kTokens;
-  int64_t t_ask = ((int64_t)(cluster * splits + split) * kWarps + warp) * S::kTokens;
   int32_t page[2] = {-1, -1};
   auto look_up = [&](int64_t t) {  // the pages of the step at t (columns of the table, whatever the length)
     page[0] = t < most ? table[t >> c.page_shift] : -1;
     if constexpr (S::kTokens == 32) page[1] = t + 16 < most ? table[(t + 16) >> c.page_shift] : -1;
   };
-  if (a.window <= 0) look_up(t_ask);
-  r.len = r.len < most ? r.len : most;
-  r.first = a.window > 0 && r.len > a.window ? r.len - a.window : 0;
+  const int64_t lap = (int64_t)splits * kWarps * S::kTokens;
+  int64_t t_ask = (int64_t)(split * kWarps + warp) * S::kTokens;
+  if (a.window <= 0) look_up(t_ask);  // the first page is known before the length
+  const Span<S::kTokens> span(a.lengths[b], most, a.window);
   if (a.window > 0) {
-    t_ask += r.first / S::kTokens * S::kTokens;
+    t_ask += span.begin();
     look_up(t_ask);
   }
+  const int hk = row / groups, first_of_group = row % groups * kRowHeads;
+  const int heads = min(kRowHeads, group - first_of_group), hq = hk * group + first_of_group;
+  Source r;
+  const int64_t head_row = (int64_t)hk << c.page_shift;
+  r.k = static_cast<const uint8_t*>(c.k) + head_row * D * S::kBytes;
+  r.v = static_cast<const uint8_t*>(c.v) + head_row * D * S::kBytes;
+  r.ks = c.k_step + head_row;
+  r.vs = c.v_step + head_row;
+  r.first = span.first;
+  r.len = span.len;
   int64_t t0 = t_ask;  // the step in hand
 
   uint32_t oks = 0;  // two bits a requested step (its halves have pages), the newest lowest
@@ -330,20 +450,20 @@ attend_kernel(AttendArgs a, KvPages c, int64_t b0, int splits, int clusters, flo
   auto ask = [&]() {  // requests the step at t_ask into the next stage and looks the one after up
     oks <<= 2;
     if (t_ask < r.len) {
-      int64_t row[2] = {0, 0};
+      int64_t place[2] = {0, 0};
       uint32_t ok = 0;
 #pragma unroll
       for (int s = 0; s < S::kTokens / 16; ++s) {
         if (t_ask + 16 * s < r.len && (uint32_t)page[s] < (uint32_t)c.num_pages) {
           ok |= 1u << s;
-          row[s] = (((int64_t)page[s] * c.heads) << c.page_shift) + ((int)(t_ask + 16 * s) & ((1 << c.page_shift) - 1));
+          place[s] = (((int64_t)page[s] * c.heads) << c.page_shift) + ((int)(t_ask + 16 * s) & ((1 << c.page_shift) - 1));
         }
       }
       oks |= ok;
       if (D == DT && ok == (S::kTokens == 32 ? 3u : 1u) && t_ask >= r.first && t_ask + S::kTokens <= r.len)
-        request_whole<FORMAT, DT>(r, row, ask_at, lane);
+        request_whole<FORMAT, DT>(r, place, ask_at, lane);
       else
-        request_part<FORMAT, DT>(r, c, t_ask, row, ok, ask_at, lane);
+        request_part<FORMAT, DT>(r, c, t_ask, place, ok, ask_at, lane);
     }
     copies_commit();
     t_ask += lap;
@@ -605,17 +725,20 @@ attend_kernel(AttendArgs a, KvPages c, int64_t b0, int splits, int clusters, flo
 
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
   auto finish = [&](int h, int d, const Joined& j) {
-    if (clusters > 1) {  // [cluster][sequence][q head][dims, m, sum]
-      float* p = parts + (((int64_t)cluster * a.B + b) * a.q_heads + hq + h) * (D + 4);
-      p[d] = j.value;
-      if (d == 0) *reinterpret_cast<float2*>(p + D) = make_float2(j.m, j.sum);
-    } else {
-      a.out[b * a.out_stride + (int64_t)(hq + h) * D + d] = j.sum > 0.0f ? j.value / j.sum : 0.0f;  // no token: zeros
-    }
+    a.out[b * a.out_stride + (int64_t)(hq + h) * D + d] = j.sum > 0.0f ? j.value / j.sum : 0.0f;  // no token: zeros
   };
-  if (splits == 1) {
-    for (int i = threadIdx.x; i < heads * D; i += kThreads)
-      finish(i / D, i % D, join<false>(base + i / D * S::kPartial, S::kWarpBytes, kWarps, i % D, DT));
+  if (splits == 1 || shared_out) {
+    float* part = sh.parts + (int64_t)blockIdx.x * min(kRowHeads, group) * (D + 4);
+    for (int i = threadIdx.x; i < heads * D; i += kThreads) {
+      const int h = i / D, d = i - h * D;
+      const Joined j = join<false>(base + h * S::kPartial, S::kWarpBytes, kWarps, d, DT);
+      if (splits == 1) {
+        finish(h, d, j);
+      } else {
+        part[h * (D + 4) + d] = j.value;
+        if (d == 0) *reinterpret_cast<float2*>(part + h * (D + 4) + D) = make_float2(j.m, j.sum);
+      }
+    }
     return;
   }
   // The CTA's own partials first (kept in registers across the barrier: the
@@ -645,45 +768,86 @@ attend_kernel(AttendArgs a, KvPages c, int64_t b0, int splits, int clusters, flo
   cluster_sync();  // no CTA leaves while another reads its partials
 }
 
-// Joins the clusters' parts of one (sequence, q head): dim threadIdx.x.
-__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ parts, int clusters, int64_t rows, int D,
-                                                   int q_heads, float* __restrict__ out, int64_t out_stride) {
+// Joins the parts of rows that several CTAs had: one CTA a (sequence, q head); groups
+// of threads, a thread a dim, take the parts in turn, and their sums meet in order.
+constexpr int kJoinThreads = 512;
+template <int T>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a, KvPages c, Shares sh) {
+  __shared__ float tops[kJoinThreads / 32];
+  __shared__ float values[kJoinThreads], sums[kJoinThreads];
   pdl_release_dependents();
   pdl_wait_primary();
-  const int d = threadIdx.x;
-  const float* p = parts + (int64_t)blockIdx.x * (D + 4);
-  const int64_t apart = rows * (D + 4);
-  float m = kUnset, sum = 0.0f, value = 0.0f;
-  for (int i = 0; i < clusters; ++i) m = fmaxf(m, p[i * apart + D]);
-  for (int i = 0; i < clusters; ++i) {
-    const float f = exp2_of(p[i * apart + D] - m);
-    sum = fmaf(p[i * apart + D + 1], f, sum);
-    if (d < D) value = fmaf(p[i * apart + d], f, value);
+  const int group = a.q_heads / c.heads, groups = (group + kRowHeads - 1) / kRowHeads, D = c.head_dim;
+  const int64_t b = blockIdx.x / a.q_heads;
+  const int h = blockIdx.x % a.q_heads, in_group = h % group;
+  float* out = a.out + b * a.out_stride + (int64_t)h * D;
+  if (Span<T>(a.lengths[b], a.max_pages << c.page_shift, a.window).steps() == 0) {
+    if (threadIdx.x < D) out[threadIdx.x] = 0.0f;
+    return;
   }
-  if (d < D) out[blockIdx.x / q_heads * out_stride + blockIdx.x % q_heads * (int64_t)D + d] = sum > 0.0f ? value / sum : 0.0f;
+  const int2 row = sh.rows[(b * c.heads + h / group) * groups + in_group / kRowHeads];
+  if (row.y == 1) return;  // one CTA had all of it and has written it
+  const int64_t apart = (int64_t)min(kRowHeads, group) * (D + 4);
+  const float* p = sh.parts + row.x * apart + in_group % kRowHeads * (D + 4);
+  float m = kUnset;
+  for (int i = threadIdx.x; i < row.y; i += kJoinThreads) m = fmaxf(m, p[i * apart + D]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, tops[w]);
+  const int teams = kJoinThreads / D, team = threadIdx.x / D, d = threadIdx.x % D;
+  if (team < teams) {
+    float sum = 0.0f, value = 0.0f;
+#pragma unroll 8
+    for (int i = team; i < row.y; i += teams) {
+      const float* q = p + i * apart;
+      const float f = exp2_of(q[D] - m);
+      sum = fmaf(q[D + 1], f, sum);
+      value = fmaf(q[d], f, value);
+    }
+    values[threadIdx.x] = value;
+    sums[threadIdx.x] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float sum = 0.0f, value = 0.0f;
+    for (int t = 0; t < teams; ++t) {
+      sum += sums[t * D + d];
+      value += values[t * D + d];
+    }
+    out[d] = sum > 0.0f ? value / sum : 0.0f;
+  }
 }
 
 int64_t rows_of(int64_t B, int q_heads, int kv_heads) {
   return B * kv_heads * ((q_heads / kv_heads + kRowHeads - 1) / kRowHeads);
 }
 
-// Clusters a sequence may have: as many as two CTAs an SM leave room for beyond
-// one full-sized cluster a row.
-int clusters_for(int64_t rows) {
-  const int64_t n = 2 * kSms / (rows * kMaxCluster);
-  return (int)(n < 1 ? 1 : n > kMaxClusters ? kMaxClusters : n);
-}
+// The most CTAs that rows are shared out over, of any format and padded head size,
+// and whether so many rows are few enough for it (rows round up to whole CTAs).
+constexpr int kShareCtas = 4 * kSms;
+bool shares_fit(int64_t B, int64_t rows, int ctas) { return B <= kShareSeqs && rows <= ctas / 3; }
 
-// CTAs of a cluster: a power of two up to kMaxCluster, while the CTAs stay within
-// two an SM and every warp may have a step.
-int splits_for(int64_t rows, int64_t steps) {
+// CTAs of a cluster: a power of two up to kMaxCluster, while all CTAs are resident
+// at once and every warp may have a step.
+int splits_for(int64_t rows, int64_t steps, int ctas) {
   int s = 1;
-  while (s < kMaxCluster && rows * s * 2 <= 2 * kSms && steps >= 2 * s * kWarps) s *= 2;
+  while (s < kMaxCluster && rows * s * 2 <= ctas && steps >= 2 * s * kWarps) s *= 2;
   return s;
 }
 
+// Sharing out costs ~5 us more than clusters do (finding the row, the second
+// launch) and fills what they leave idle.
+bool share_out_wins(int64_t B, int64_t rows, int64_t tokens, int splits, int ctas) {
+  const int64_t a_warp = tokens / (splits * kWarps);
+  if (B > 1 && a_warp >= 1024) return true;  // lengths may differ: the longest row would end alone
+  return a_warp * (ctas - rows * splits) >= (int64_t)192 * ctas;
+}
+
 template <int FORMAT, int DT>
-cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, float* parts, bool pdl, const DeviceInfo& dev,
+cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace, bool pdl, const DeviceInfo& dev,
                          cudaStream_t stream) {
   using S = Shape<FORMAT, DT>;
   const auto kernel = attend_kernel<FORMAT, DT>;
@@ -695,73 +859,82 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, float* parts, bo
   }
   const int64_t rows = rows_of(a.B, a.q_heads, c.heads), per_seq = rows / a.B;
   int64_t tokens = a.max_pages << c.page_shift;
-  if (a.window > 0 && a.window < tokens) tokens = a.window;
+  if (a.window > 0 && a.window < tokens) tokens = a.window + S::kTokens;  // a window may begin inside a step
   const int64_t steps = (tokens + S::kTokens - 1) / S::kTokens;
-  const int splits = splits_for(rows, steps);
-  // further clusters once each of their warps has kClusterSteps steps (a second launch costs as much as several)
-  int clusters = parts ? clusters_for(rows) : 1;
-  while (clusters > 1 && steps < (int64_t)clusters * splits * kWarps * kClusterSteps) --clusters;
-  const int64_t per_launch = (int64_t)0x7fffffff / (per_seq * splits * clusters);  // sequences a grid holds
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
   cfg.attrs = attr;
-  for (int64_t b0 = 0; b0 < a.B; b0 += per_launch) {
-    const int64_t n = a.B - b0 < per_launch ? a.B - b0 : per_launch;
-    cfg.gridDim = dim3((unsigned)(n * per_seq * splits * clusters), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = S::kSmem;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = S::kSmem;
+  auto programmatic = [&] {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  };
+  const int ctas = (dev.num_sms < kSms ? dev.num_sms : kSms) * S::kResident;
+  Shares sh = {0, splits_for(rows, steps, ctas), false, nullptr, nullptr};
+  if (workspace && shares_fit(a.B, rows, ctas) && steps <= 0x7fffffff / rows &&
+      share_out_wins(a.B, rows, tokens, sh.splits, ctas)) {
+    const int64_t heads = a.q_heads / c.heads < kRowHeads ? a.q_heads / c.heads : kRowHeads;
+    sh.splits = 0;
+    sh.parts = static_cast<float*>(workspace);
+    sh.rows = reinterpret_cast<int2*>(sh.parts + (int64_t)kShareCtas * heads * (c.head_dim + 4));
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    if (pdl) programmatic();
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, c, sh);
+    if (err != cudaSuccess) return err;
+    cfg.gridDim = dim3((unsigned)(a.B * a.q_heads), 1, 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 0;
-    if (splits > 1) {
+    programmatic();
+    return cudaLaunchKernelEx(&cfg, join_kernel<S::kTokens>, a, c, sh);
+  }
+  sh.sorted = a.B > 1 && a.B <= kSortSeqs && rows * sh.splits > ctas;
+  const int64_t per_launch = (int64_t)0x7fffffff / (per_seq * sh.splits);  // sequences a grid holds
+  for (; sh.b0 < a.B; sh.b0 += per_launch) {
+    const int64_t n = a.B - sh.b0 < per_launch ? a.B - sh.b0 : per_launch;
+    cfg.gridDim = dim3((unsigned)(n * per_seq * sh.splits), 1, 1);
+    cfg.numAttrs = 0;
+    if (sh.splits > 1) {
       attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-      attr[cfg.numAttrs].val.clusterDim.x = (unsigned)splits;
+      attr[cfg.numAttrs].val.clusterDim.x = (unsigned)sh.splits;
       attr[cfg.numAttrs].val.clusterDim.y = 1;
       attr[cfg.numAttrs].val.clusterDim.z = 1;
       ++cfg.numAttrs;
     }
-    if (pdl) {
-      attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
-      ++cfg.numAttrs;
-    }
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, c, b0, splits, clusters, parts);
+    if (pdl) programmatic();
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, c, sh);
     if (err != cudaSuccess) return err;
   }
-  if (clusters == 1) return cudaSuccess;
-  // clusters > 1 only with few rows: one launch above, and the join overlaps its tail
-  cfg.gridDim = dim3((unsigned)(a.B * a.q_heads), 1, 1);
-  cfg.blockDim = dim3((unsigned)((DT + 31) / 32 * 32), 1, 1);
-  cfg.dynamicSmemBytes = 0;
-  cfg.numAttrs = 1;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel, (const float*)parts, clusters, a.B * a.q_heads, c.head_dim, a.q_heads,
-                            a.out, a.out_stride);
+  return cudaSuccess;
 }
 
 template <int FORMAT>
-cudaError_t launch_format(const AttendArgs& a, const KvPages& c, float* parts, bool pdl, const DeviceInfo& dev,
+cudaError_t launch_format(const AttendArgs& a, const KvPages& c, void* workspace, bool pdl, const DeviceInfo& dev,
                           cudaStream_t s) {
-  if (c.head_dim <= 64) return launch_shape<FORMAT, 64>(a, c, parts, pdl, dev, s);
-  if (c.head_dim <= 80) return launch_shape<FORMAT, 80>(a, c, parts, pdl, dev, s);
-  if (c.head_dim <= 96) return launch_shape<FORMAT, 96>(a, c, parts, pdl, dev, s);
-  if (c.head_dim <= 128) return launch_shape<FORMAT, 128>(a, c, parts, pdl, dev, s);
-  return launch_shape<FORMAT, 256>(a, c, parts, pdl, dev, s);
+  if (c.head_dim <= 64) return launch_shape<FORMAT, 64>(a, c, workspace, pdl, dev, s);
+  if (c.head_dim <= 80) return launch_shape<FORMAT, 80>(a, c, workspace, pdl, dev, s);
+  if (c.head_dim <= 96) return launch_shape<FORMAT, 96>(a, c, workspace, pdl, dev, s);
+  if (c.head_dim <= 128) return launch_shape<FORMAT, 128>(a, c, workspace, pdl, dev, s);
+  return launch_shape<FORMAT, 256>(a, c, workspace, pdl, dev, s);
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int64_t B, int q_heads, int kv_heads, int head_dim) {
-  const int clusters = clusters_for(rows_of(B, q_heads, kv_heads));
-  return clusters > 1 ? (size_t)clusters * B * q_heads * (head_dim + 4) * sizeof(float) : 0;
+  const int64_t rows = rows_of(B, q_heads, kv_heads);
+  if (!shares_fit(B, rows, kShareCtas)) return 0;
+  const int group = q_heads / kv_heads, heads = group < kRowHeads ? group : kRowHeads;
+  return (size_t)kShareCtas * heads * (head_dim + 4) * sizeof(float) + (size_t)rows * sizeof(int2);
 }
 
 cudaError_t launch_attention(const AttendArgs& a, const KvPages& cache, void* workspace, bool pdl,
                              const DeviceInfo& dev, cudaStream_t stream) {
-  float* parts = static_cast<float*>(workspace);
-  if (cache.format == BITLINEAR_KV_INT8) return launch_format<BITLINEAR_KV_INT8>(a, cache, parts, pdl, dev, stream);
-  if (cache.format == BITLINEAR_KV_FP8) return launch_format<BITLINEAR_KV_FP8>(a, cache, parts, pdl, dev, stream);
-  return launch_format<BITLINEAR_KV_BF16>(a, cache, parts, pdl, dev, stream);
+  if (cache.format == BITLINEAR_KV_INT8) return launch_format<BITLINEAR_KV_INT8>(a, cache, workspace, pdl, dev, stream);
+  if (cache.format == BITLINEAR_KV_FP8) return launch_format<BITLINEAR_KV_FP8>(a, cache, workspace, pdl, dev, stream);
+  return launch_format<BITLINEAR_KV_BF16>(a, cache, workspace, pdl, dev, stream);
 }
 
 }  // namespace bitlinear

@@ -232,8 +232,9 @@ def test_empty_calls_touch_nothing():
 
 
 def attend_case(fmt, Hq, Hk, D, page, lengths, window=0, seed=0, value_std=1.0, value_mean=0.0, workspace=False,
-                bad_page=None, key_std=1.0, scale=None, spread_steps=False):
-    """A cache filled to each sequence's length, garbage everywhere else; -> worst error over the bound."""
+                bad_page=None, key_std=1.0, scale=None, spread_steps=False, columns=0):
+    """A cache filled to each sequence's length, garbage everywhere else (and in the table's columns past
+    the longest sequence, at least `columns` in all); -> the output."""
     B, width = len(lengths), max(1, -(-max(1, max(lengths)) // page)) + 1
     rng = np.random.default_rng(seed)
     pages = B * width + 2
@@ -251,6 +252,8 @@ def attend_case(fmt, Hq, Hk, D, page, lengths, window=0, seed=0, value_std=1.0, 
         plain.fill_row(cache, fmt, at, t % page, k, v)
     if bad_page is not None:
         table[bad_page] = [-1, pages, 10 ** 9][seed % 3]
+    if columns > width:
+        table = np.concatenate([table, rng.integers(-2 ** 31, 2 ** 31 - 1, (B, columns - width))], 1)
     q = torch.randn(B, Hq, D, generator=g, device="cuda") * 1.5
     out, full = guarded(B * Hq * D, torch.float32, -7.0)
     out = out.view(B, Hq, D)
@@ -304,6 +307,28 @@ def test_attention_long_and_ragged(fmt):
     attend_case(fmt, 2, 1, 80, 16, [9001], seed=2, workspace=True)
     attend_case(fmt, 2, 1, 80, 16, [9001], seed=3)
     attend_case(fmt, 4, 4, 64, 32, [1 + 37 * i % 900 for i in range(70)], seed=4)
+
+
+# A table wide enough that a call with a workspace cuts one line through all sequences and heads.
+WIDE = 1 << 16
+
+
+@pytest.mark.parametrize("fmt", plain.FORMATS)
+@pytest.mark.parametrize("Hq,Hk,D,page,lengths,window", [
+    (4, 1, 128, 64, [3000], 0), (8, 8, 80, 16, [5], 0), (2, 2, 64, 32, [0, 0, 700, 0, 1, 33, 2050, 0], 0),
+    (18, 2, 96, 16, [900, 0, 31, 32, 33, 1], 0), (5, 5, 112, 64, [1500, 64, 4097], 0), (4, 2, 256, 16, [513, 2000], 0),
+    (4, 4, 80, 64, [4000, 3999, 17, 0, 250], 700), (8, 1, 32, 128, [9000, 100], 33), (2, 1, 64, 16, [0, 0], 0),
+    (3, 1, 128, 4096, [10000, 1, 5000], 0)])
+def test_attention_as_one_line(fmt, Hq, Hk, D, page, lengths, window):
+    attend_case(fmt, Hq, Hk, D, page, lengths, window=window, seed=len(lengths) + D, workspace=True, columns=WIDE * 16 // page)
+
+
+@pytest.mark.parametrize("fmt", plain.FORMATS)
+def test_attention_as_one_line_of_many_short_rows(fmt):
+    lengths = [(37 * i) % 90 for i in range(300)]
+    attend_case(fmt, 4, 2, 64, 16, lengths, seed=1, workspace=True, columns=WIDE // 16)
+    attend_case(fmt, 4, 4, 80, 16, lengths[:100], seed=2, workspace=True, columns=WIDE // 16,
+                bad_page=([3, 3, 4, 99], [0, 1, 0, 2]))
 
 
 @pytest.mark.parametrize("fmt", plain.FORMATS)
