@@ -2,26 +2,30 @@
 // quantised and written where their page is, and read back.
 //
 // Rotation ("Hesper.Models.BitNet" page, section "Configuration": ropeBase):
-// pair i of a head turns by the angle positions[t] * freq[i], taken in quarter
-// turns in fp64, positions * (freq * 2 / pi), so its whole turns drop out without
-// loss and a far position keeps its fraction of a turn to 2^-53 of the whole
-// angle.  Sine and cosine of what is left (|a| <= pi / 4) are their Taylor series, the
-// leading terms in fp64 and the tail, whose fp32 rounding is below 2^-38 of the
-// result, in fp32 (the fp64 pipe is narrow: ~15 fp64 operations a pair), rounded
-// once to fp32.  The rotation itself is two fp32 products and one sum, unfused, so
-// it can be repeated bit for bit.
+// pair i of a head turns by the angle positions[t] * freq[i].  The angle is kept in
+// turns as a 64-bit fraction, positions times the frequency's fraction modulo 2^64, so
+// whole turns drop out exactly and a far position keeps its angle to 2^-53 of it.
+// What is left of the nearest quarter turn, |a| <= pi / 4, becomes a pair of fp32
+// (leading part and rest), its sine and cosine the Taylor series with the first three
+// terms in such pairs, rounded once to fp32: the nearest fp32 value but for one in
+// ~10^4.  (In fp64 the same took ~20 instructions a pair of a pipe that takes one in
+// ~14 cycles: 3 us of 11 for 2048 tokens of 32 heads.)  The
+// rotation itself is two fp32 products and one sum, unfused, so that it can be
+// repeated bit for bit.
 //
 // Quantisation follows activation_quant, a row being one (token, head):
 //   int8: code = clamp(rne(x * s), -128, 127), s = 127 * (1 / a), a = max(max|x|, 1e-5)
 //   e4m3: code = e4m3(x * s), s = 448 * (1 / a), round to nearest even, saturating
 // with step = a / 127 or a / 448, the fp32 value of one unit; bf16 rounds.
 //
-// Layout: four lanes hold a row, lane j its 16-byte chunks j, j + 4, ...: a warp
-// takes 8 rows, every lane has a chunk in every load whatever the head size (80
-// dims fill 20 of 32 lanes one row a warp), all of a row's loads are in flight
-// together, and its maximum takes two shuffles.  A CTA takes one token (or, while
-// the tokens alone leave SMs idle, a share of its heads), so a token's sines and
-// cosines are made once, behind the loads of its first rows.
+// Layout: four or eight lanes hold a row, each 16-byte chunks in pairs; the chunks of
+// a pair are the two halves of the same rotated dims, so both of a rotation's operands
+// and its angle are one lane's (loading the partners a second time took 5 us of 27 for
+// 2039 tokens), and nearly every lane has a chunk in every load whatever the head size
+// (80 dims fill 20 of 24; 20 of 32 with a row a warp).  A warp works alone: one token,
+// or a share of its heads while tokens alone do not fill the GPU, with the next turn's
+// rows loaded before this one's are used and the token's sines and cosines in its own
+// shared memory, so no barrier holds it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -33,188 +37,272 @@ namespace bitlinear {
 namespace {
 
 constexpr int kMaxHead = 256;     // head_dim limit
-constexpr int kMaxThreads = 512;
-constexpr int kMinThreads = 64;
-constexpr int kRowLanes = 4;      // lanes of a row
-constexpr int kWarpRows = 32 / kRowLanes;
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
 
-__device__ __forceinline__ void sin_cos_quarter(double q, float* sine, float* cosine) {
-  const double whole = rint(q);
-  const double a = (q - whole) * 1.57079632679489661923;  // |a| <= pi / 4
-  const double a2 = a * a;
-  const float u = (float)a2;
-  // sin a = a - a^3/3! + a^5/5! - ..., cos a = 1 - a^2/2! + a^4/4! - ..., from a^7 and a^8 on in fp32
-  const float ts = fmaf(u, fmaf(u, fmaf(u, 1.0f / 6227020800.0f, -1.0f / 39916800.0f), 1.0f / 362880.0f), -1.0f / 5040.0f);
-  const float tc = fmaf(u, fmaf(u, 1.0f / 479001600.0f, -1.0f / 3628800.0f), 1.0f / 40320.0f);
-  const double s = fma(a * a2, fma(a2, fma(a2, (double)ts, 1.0 / 120.0), -1.0 / 6.0), a);
-  const double c = fma(a2, fma(a2, fma(a2, fma(a2, (double)tc, -1.0 / 720.0), 1.0 / 24.0), -0.5), 1.0);
-  const int n = (int)(long long)whole & 3;  // quarter turns past whole turns
-  const float fs = (float)s, fc = (float)c;
-  const float x = n & 1 ? fs : fc, y = n & 1 ? fc : fs;
-  *cosine = n == 1 || n == 2 ? -x : x;
-  *sine = n >= 2 ? -y : y;
+// The fraction of a turn that a position adds, in units of 2^-64 turns.
+__device__ __forceinline__ uint64_t turn_fraction(double freq) {
+  const uint64_t bits = (uint64_t)__double_as_longlong(freq * 0.15915494309189533577);
+  const int shift = (int)((bits >> 52) & 0x7ff) - 1011;  // mantissa * 2^(exponent - 1075) turns
+  const uint64_t m = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
+  uint64_t f;
+  if (shift >= 0)
+    f = shift < 64 ? m << shift : 0;
+  else
+    f = shift > -54 ? ((m >> (-shift - 1)) + 1) >> 1 : 0;
+  return (bits >> 63) ? 0 - f : f;
 }
 
-// cos and sin of every pair of one position, into shared memory.
+// Sine and cosine of `phase` / 2^64 turns.  h and l name a value's leading part and
+// rest; a product's rest is an exact fma, and a sum's follows from larger + smaller.
+__device__ __forceinline__ void sin_cos_turns(uint64_t phase, float* sine, float* cosine) {
+  const uint64_t from_eighth = phase + (1ull << 61);
+  const int quarter = (int)(from_eighth >> 62);
+  const int64_t r = (int64_t)(from_eighth & ((1ull << 62) - 1)) - (1ll << 61);
+  const float top = (float)(int)(r >> 40), low = (float)((uint32_t)(r >> 16) & 0xffffffu) * 5.9604644775390625e-8f;
+  // a = 2 pi / 2^24 (top + low)
+  constexpr float kH = 3.7450704e-07f, kL = -1.0421607e-14f;
+  float h = top * kH, l = fmaf(low, kH, fmaf(top, kL, fmaf(top, kH, -h)));
+  const float ah = h + l, al = l - (ah - h);
+  const float uh = ah * ah, ul = fmaf(ah + ah, al, fmaf(ah, ah, -uh));  // a^2
+  const float zh = uh * uh, zl = fmaf(uh + uh, ul, fmaf(uh, uh, -zh));  // a^4
+  // sin a = a + a q, q = -a^2 / 3! + a^4 / 5! + a^4 (-a^2 / 7! + a^4 / 9! - a^6 / 11!)
+  constexpr float k6H = 0.16666667f, k6L = -4.967054e-09f, k120H = 0.008333334f, k120L = -4.346172e-10f;
+  h = zh * k120H;
+  l = fmaf(zl, k120H, fmaf(zh, k120L, fmaf(zh, k120H, -h)));
+  l = fmaf(zh, uh * fmaf(uh, fmaf(uh, -1.0f / 39916800.0f, 1.0f / 362880.0f), -1.0f / 5040.0f), l);
+  const float th = uh * k6H, tl = fmaf(ul, k6H, fmaf(uh, k6L, fmaf(uh, k6H, -th)));
+  const float qh = h - th, ql = ((-th - qh) + h) + (l - tl);
+  const float ch = ah * qh, cl = fmaf(al, qh, fmaf(ah, ql, fmaf(ah, qh, -ch))) + al;
+  const float sh = ah + ch, s = sh + ((ch - (sh - ah)) + cl);
+  // cos a = 1 - a^2 / 2! + a^4 / 4! + a^4 (-a^2 / 6! + a^4 / 8! - a^6 / 10! + a^8 / 12!)
+  constexpr float k24H = 0.041666668f, k24L = -1.2417635e-09f;
+  const float yh = zh * k24H;
+  float yl = fmaf(zl, k24H, fmaf(zh, k24L, fmaf(zh, k24H, -yh)));
+  yl = fmaf(zh, uh * fmaf(uh, fmaf(uh, fmaf(uh, 1.0f / 479001600.0f, -1.0f / 3628800.0f), 1.0f / 40320.0f), -1.0f / 720.0f), yl);
+  const float dh = -0.5f * uh, dl = -0.5f * ul;
+  const float c1 = 1.0f + dh, e1 = dh - (c1 - 1.0f), c2 = c1 + yh, e2 = yh - (c2 - c1);
+  const float c = c2 + ((e1 + e2) + (dl + yl));
+  const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
+  *cosine = quarter == 1 || quarter == 2 ? -x : x;
+  *sine = quarter >= 2 ? -y : y;
+}
+
+// cos and sin of every pair of one position, into the warp's shared memory.
 __device__ __forceinline__ void fill_angles(const RopeArgs& r, int32_t pos, float2* cs) {
-  for (int i = threadIdx.x; i < r.rot_dim / 2; i += blockDim.x) {
+  for (int i = threadIdx.x & 31; i < r.rot_dim / 2; i += 32) {
     float s, c;
-    sin_cos_quarter((double)pos * (r.freq[i] * 0.63661977236758134308), &s, &c);
+    sin_cos_turns(turn_fraction(r.freq[i]) * (uint64_t)(int64_t)pos, &s, &c);
     cs[i] = make_float2(__fmul_rn(c, r.amplitude), __fmul_rn(s, r.amplitude));
   }
+  __syncwarp();
 }
 
-// The lane's chunks of a row of D floats.
-template <int NC>
-__device__ __forceinline__ void load_row(const float* row, int D, int j, float4 (&v)[NC]) {
+// A warp's work: units first <= u < end of one token, ROWS a turn.
+struct Task {
+  int64_t token;
+  int first, end;
+};
+template <int ROWS>
+__device__ __forceinline__ Task task_of_warp(int64_t T, int units, int shares) {
+  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int share = (int)(w % shares), turns = (units + ROWS - 1) / ROWS;
+  Task t = {w / shares, turns * share / shares * ROWS, turns * (share + 1) / shares * ROWS};
+  t.end = t.token < T ? min(t.end, units) : t.first;
+  return t;
+}
+
+// A head size and where a lane's chunks are: DX dims known at compile time, or, DX == 0,
+// any up to 8 * L * NP.  Pair p = j + L i of lane j of a row is chunks p and p + together
+// for p < together (the pairs of a rotation by halves), else the next two in order.
+template <int NP_, int L_, int DX>
+struct Head {
+  static constexpr int NP = NP_, L = L_, kRows = 32 / L;
+  static constexpr int kCtas = NP == 1 ? 8 : NP == 2 ? 5 : 4;        // CTAs an SM, without spilled registers
+  static constexpr int kReadCtas = NP == 1 ? 12 : NP <= 3 ? 8 : 6;  // the same of the reading kernel
+  int D, j, a[NP], b[NP];  // first dims of the two chunks of each pair
+  __device__ __forceinline__ Head(int dims, int together) : D(DX ? DX : dims), j((threadIdx.x & 31) % L) {
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int d = 4 * (j + kRowLanes * i);
-    if (d < D) v[i] = *reinterpret_cast<const float4*>(row + d);
+    for (int i = 0; i < NP; ++i) {
+      const int p = j + L * i;
+      a[i] = 4 * (p < together ? p : 2 * p);
+      b[i] = 4 * (p < together ? p + together : 2 * p + 1);
+    }
+  }
+  __device__ __forceinline__ bool has_a(int i) const { return 8 * L * (i + 1) <= DX || 8 * (j + L * i) < D; }
+  __device__ __forceinline__ bool has_b(int i) const { return has_a(i) && (DX || b[i] < D); }
+};
+// How many pairs of chunks a rotation keeps together in heads of D dims.
+__host__ __device__ __forceinline__ int pairs_together(int D, const RopeArgs& r) {
+  return r.freq && r.layout == BITLINEAR_ROPE_HALF && r.rot_dim % 8 == 0 ? r.rot_dim / 8 : D / 8;
+}
+
+// The lane's chunks of a row.
+template <typename H>
+struct Row {
+  float4 a[H::NP], b[H::NP];
+};
+template <typename H>
+__device__ __forceinline__ void load_row(const H& head, const float* row, Row<H>& v) {
+  const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < H::NP; ++i) {
+    v.a[i] = head.has_a(i) ? *reinterpret_cast<const float4*>(row + head.a[i]) : none;
+    v.b[i] = head.has_b(i) ? *reinterpret_cast<const float4*>(row + head.b[i]) : none;
+  }
+}
+template <typename H>
+__device__ __forceinline__ void store_row(const H& head, float* row, const Row<H>& v) {
+#pragma unroll
+  for (int i = 0; i < H::NP; ++i) {
+    if (head.has_a(i)) *reinterpret_cast<float4*>(row + head.a[i]) = v.a[i];
+    if (head.has_b(i)) *reinterpret_cast<float4*>(row + head.b[i]) = v.b[i];
   }
 }
 
-__device__ __forceinline__ float turn_first(float own, float other, float2 a) {
-  return __fsub_rn(__fmul_rn(own, a.x), __fmul_rn(other, a.y));
+// own * c + other * s, each step rounded; the first of a pair takes -s.
+__device__ __forceinline__ float turn(float own, float other, float c, float s) {
+  return __fadd_rn(__fmul_rn(own, c), __fmul_rn(other, s));
 }
-__device__ __forceinline__ float turn_second(float own, float other, float2 a) {
-  return __fadd_rn(__fmul_rn(own, a.x), __fmul_rn(other, a.y));
+__device__ __forceinline__ void turn_halves(float4& v, float4& o, const float2* cs) {
+  const float4 p = reinterpret_cast<const float4*>(cs)[0], q = reinterpret_cast<const float4*>(cs)[1];
+  const float4 x = make_float4(turn(v.x, o.x, p.x, -p.y), turn(v.y, o.y, p.z, -p.w), turn(v.z, o.z, q.x, -q.y), turn(v.w, o.w, q.z, -q.w));
+  o = make_float4(turn(o.x, v.x, p.x, p.y), turn(o.y, v.y, p.z, p.w), turn(o.z, v.z, q.x, q.y), turn(o.w, v.w, q.z, q.w));
+  v = x;
+}
+// Interleaved pairs of the chunk at dim d, of which those below rot turn.
+__device__ __forceinline__ void turn_pairs(float4& v, const float2* cs, int d, int rot) {
+  const float4 p = *reinterpret_cast<const float4*>(cs + d / 2);
+  if (d < rot) {
+    const float x = turn(v.x, v.y, p.x, -p.y);
+    v.y = turn(v.y, v.x, p.x, p.y);
+    v.x = x;
+  }
+  if (d + 2 < rot) {
+    const float z = turn(v.z, v.w, p.z, -p.w);
+    v.w = turn(v.w, v.z, p.z, p.w);
+    v.z = z;
+  }
+}
+// Halves whose length is no multiple of a chunk: the partners come from the row again.
+__device__ __forceinline__ void turn_scattered(float4& v, const float* row, const float2* cs, int d0, int rot) {
+  float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int d = d0 + k, n = rot / 2, other = d < n ? d + n : d - n;
+    if (d >= rot) continue;
+    const float2 p = cs[min(d, other)];
+    e[k] = turn(e[k], row[other], p.x, d < n ? -p.y : p.y);
+  }
+  v = make_float4(e[0], e[1], e[2], e[3]);
 }
 
-// Rotates the lane's chunks (v, of the row at `row`) in registers.
-template <int NC>
-__device__ __forceinline__ void rotate_row(const float* row, int D, int j, const RopeArgs& r, const float2* cs,
-                                           float4 (&v)[NC]) {
-  const int n = r.rot_dim / 2;
+// Rotates the lane's chunks (of the row at `row`) in registers.
+template <typename H>
+__device__ __forceinline__ void rotate_row(const H& head, const float* row, const RopeArgs& r, const float2* cs,
+                                           Row<H>& v) {
   if (r.layout == BITLINEAR_ROPE_INTERLEAVED) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int d = 4 * (j + kRowLanes * i);
-      if (d < r.rot_dim) {
-        const float2 a = cs[d / 2];
-        const float x = turn_first(v[i].x, v[i].y, a), y = turn_second(v[i].y, v[i].x, a);
-        v[i].x = x;
-        v[i].y = y;
-      }
-      if (d + 2 < r.rot_dim) {
-        const float2 a = cs[d / 2 + 1];
-        const float z = turn_first(v[i].z, v[i].w, a), w = turn_second(v[i].w, v[i].z, a);
-        v[i].z = z;
-        v[i].w = w;
-      }
+    for (int i = 0; i < H::NP; ++i) {
+      if (head.has_a(i)) turn_pairs(v.a[i], cs, head.a[i], r.rot_dim);
+      if (head.has_b(i)) turn_pairs(v.b[i], cs, head.b[i], r.rot_dim);
     }
-    return;
-  }
-  // Halves: the partners (loaded a moment ago by this row's lanes) come from the row again.
-  if (n % 4 == 0) {
+  } else if (r.rot_dim % 8 == 0) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int d = 4 * (j + kRowLanes * i);
-      if (d >= r.rot_dim) continue;
-      const bool second = d >= n;
-      const float4 o = *reinterpret_cast<const float4*>(row + (second ? d - n : d + n));
-      const float4* a4 = reinterpret_cast<const float4*>(cs + (second ? d - n : d));
-      const float4 a = a4[0], b = a4[1];
-      if (second) {
-        v[i] = make_float4(turn_second(v[i].x, o.x, make_float2(a.x, a.y)), turn_second(v[i].y, o.y, make_float2(a.z, a.w)),
-                           turn_second(v[i].z, o.z, make_float2(b.x, b.y)), turn_second(v[i].w, o.w, make_float2(b.z, b.w)));
-      } else {
-        v[i] = make_float4(turn_first(v[i].x, o.x, make_float2(a.x, a.y)), turn_first(v[i].y, o.y, make_float2(a.z, a.w)),
-                           turn_first(v[i].z, o.z, make_float2(b.x, b.y)), turn_first(v[i].w, o.w, make_float2(b.z, b.w)));
-      }
-    }
-    return;
-  }
+    for (int i = 0; i < H::NP; ++i)
+      if (head.has_a(i) && 2 * head.a[i] < r.rot_dim) turn_halves(v.a[i], v.b[i], cs + head.a[i]);
+  } else {
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int d0 = 4 * (j + kRowLanes * i);
-    float* e = reinterpret_cast<float*>(&v[i]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int d = d0 + k;
-      if (d >= r.rot_dim) continue;
-      e[k] = d < n ? turn_first(e[k], row[d + n], cs[d]) : turn_second(e[k], row[d - n], cs[d - n]);
+    for (int i = 0; i < H::NP; ++i) {
+      if (head.has_a(i)) turn_scattered(v.a[i], row, cs, head.a[i], r.rot_dim);
+      if (head.has_b(i)) turn_scattered(v.b[i], row, cs, head.b[i], r.rot_dim);
     }
   }
 }
 
-template <int NC>
-__device__ __forceinline__ void store_row(float* row, int D, int j, const float4 (&v)[NC]) {
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int d = 4 * (j + kRowLanes * i);
-    if (d < D) *reinterpret_cast<float4*>(row + d) = v[i];
-  }
-}
-
-// blockIdx.x is the token, blockIdx.y shares its heads out.
-template <int NC>
-__global__ void __launch_bounds__(kMaxThreads) rope_kernel(const float* x, int64_t x_stride, int H, int D,
-                                                           const int32_t* __restrict__ positions, RopeArgs r, float* y,
-                                                           int64_t y_stride) {
-  __shared__ __align__(16) float2 cs[kMaxHead / 2];
+// Lanes past the last head of a turn repeat it: no turn asks whether a lane has a row.
+template <typename H>
+__global__ void __launch_bounds__(kThreads, H::kCtas)
+rope_kernel(const float* x, int64_t x_stride, int64_t T, int heads, int D, int shares,
+            const int32_t* __restrict__ positions, RopeArgs r, float* y, int64_t y_stride) {
+  __shared__ __align__(16) float2 angles[kWarps][kMaxHead / 2];
   pdl_release_dependents();
   pdl_wait_primary();
-  const int64_t t = blockIdx.x;
-  const int j = threadIdx.x % kRowLanes, step = gridDim.y * (blockDim.x / kRowLanes);
-  int h = blockIdx.y * (blockDim.x / kRowLanes) + threadIdx.x / kRowLanes;
-  x += t * x_stride;
-  y += t * y_stride;
-  float4 v[NC];
-  if (h < H) load_row(x + (int64_t)h * D, D, j, v);
-  fill_angles(r, positions[t], cs);
-  __syncthreads();
-  // every lane of a warp makes every turn: y may be x, and a row's partners are read before it is written
-  for (int at = h - (int)(threadIdx.x & 31) / kRowLanes; at < H; at += step, h += step) {
-    if (h < H) rotate_row(x + (int64_t)h * D, D, j, r, cs, v);
-    __syncwarp();
-    if (h < H) store_row(y + (int64_t)h * D, D, j, v);
-    if (h + step < H) load_row(x + (int64_t)(h + step) * D, D, j, v);
+  const H head(D, pairs_together(D, r));
+  const Task task = task_of_warp<H::kRows>(T, heads, shares);
+  if (task.first >= task.end) return;
+  float2* cs = angles[threadIdx.x >> 5];
+  const int sub = (threadIdx.x & 31) / H::L;
+  x += task.token * x_stride;
+  y += task.token * y_stride;
+  int at = task.first, h = min(at + sub, task.end - 1);
+  Row<H> v;
+  load_row(head, x + h * head.D, v);
+  fill_angles(r, positions[task.token], cs);
+  while (true) {
+    at += H::kRows;
+    const int h_next = min(at + sub, task.end - 1);
+    Row<H> next;
+    if (at < task.end) load_row(head, x + h_next * head.D, next);
+    rotate_row(head, x + h * head.D, r, cs, v);
+    __syncwarp();  // y may be x: a row is read before it is written
+    store_row(head, y + h * head.D, v);
+    if (at >= task.end) return;
+    h = h_next;
+    v = next;
   }
 }
 
-// Quantises a row held by four lanes and writes codes and step.
-template <int FORMAT, int NC>
-__device__ __forceinline__ void write_row(const float4 (&v)[NC], int D, int j, int64_t row, void* codes, float* steps) {
+// Four floats as codes of 8 bits, x * s each.
+template <int FORMAT>
+__device__ __forceinline__ uint32_t codes_of(const float4& v, float s) {
+  float e[4] = {__fmul_rn(v.x, s), __fmul_rn(v.y, s), __fmul_rn(v.z, s), __fmul_rn(v.w, s)};
+  if constexpr (FORMAT == BITLINEAR_KV_INT8) {
+    // |x * s| <= 127 (1 + 2^-22): plus 1.5 * 2^23 the sum's last bits are the code, rounded half to even
+#pragma unroll
+    for (int k = 0; k < 4; ++k) e[k] = __fadd_rn(e[k], 12582912.0f);
+    return __byte_perm(__byte_perm(__float_as_uint(e[0]), __float_as_uint(e[1]), 0x0040),
+                       __byte_perm(__float_as_uint(e[2]), __float_as_uint(e[3]), 0x0040), 0x5410);
+  } else {
+    return e4m3x2(e[1], e[0]) | e4m3x2(e[3], e[2]) << 16;
+  }
+}
+__device__ __forceinline__ uint2 bf16_of(const float4& v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ float largest(float a, const float4& v) {
+  return fmaxf(fmaxf(a, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+}
+
+// Quantises a row held by its lanes and writes codes and step.  Only the row's
+// lanes need to be here (a warp may hold q rows beside it).
+template <int FORMAT, typename H>
+__device__ __forceinline__ void write_row(const H& head, const Row<H>& v, int64_t row, void* codes, float* steps) {
   if constexpr (FORMAT == BITLINEAR_KV_BF16) {
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(codes) + row * head.D;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int d = 4 * (j + kRowLanes * i);
-      if (d >= D) continue;
-      const __nv_bfloat162 a = __floats2bfloat162_rn(v[i].x, v[i].y), b = __floats2bfloat162_rn(v[i].z, v[i].w);
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(codes) + row * D + d) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    for (int i = 0; i < H::NP; ++i) {
+      if (head.has_a(i)) *reinterpret_cast<uint2*>(out + head.a[i]) = bf16_of(v.a[i]);
+      if (head.has_b(i)) *reinterpret_cast<uint2*>(out + head.b[i]) = bf16_of(v.b[i]);
     }
-    return;
-  }
-  constexpr float kTop = FORMAT == BITLINEAR_KV_INT8 ? 127.0f : 448.0f;
-  float a = 0.0f;
+  } else {
+    constexpr float kTop = FORMAT == BITLINEAR_KV_INT8 ? 127.0f : 448.0f;
+    const unsigned lanes = ((1u << H::L) - 1) << ((threadIdx.x & 31) / H::L * H::L);
+    float a = 1e-5f;
 #pragma unroll
-  for (int i = 0; i < NC; ++i)
-    if (4 * (j + kRowLanes * i) < D)
-      a = fmaxf(fmaxf(a, fmaxf(fabsf(v[i].x), fabsf(v[i].y))), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
-  a = fmaxf(a, __shfl_xor_sync(kFullMask, a, 1));
-  a = fmaxf(a, __shfl_xor_sync(kFullMask, a, 2));
-  a = fmaxf(a, 1e-5f);
-  if (row < 0) return;  // a lane without a row: only its part in the shuffles
-  const float s = __fmul_rn(__frcp_rn(a), kTop);
-  uint8_t* out = static_cast<uint8_t*>(codes) + row * D;
+    for (int i = 0; i < H::NP; ++i) a = largest(largest(a, v.a[i]), v.b[i]);
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int d = 4 * (j + kRowLanes * i);
-    if (d >= D) continue;
-    const float e[4] = {__fmul_rn(v[i].x, s), __fmul_rn(v[i].y, s), __fmul_rn(v[i].z, s), __fmul_rn(v[i].w, s)};
-    uint32_t w;
-    if constexpr (FORMAT == BITLINEAR_KV_INT8) {
-      w = 0;
+    for (int o = 1; o < H::L; o <<= 1) a = fmaxf(a, __shfl_xor_sync(lanes, a, o));
+    const float s = __fmul_rn(__frcp_rn(a), kTop);
+    uint8_t* out = static_cast<uint8_t*>(codes) + row * head.D;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w |= (uint32_t)(uint8_t)(int8_t)max(-128, min(127, __float2int_rn(e[k]))) << (8 * k);
-    } else {
-      w = e4m3x2(e[1], e[0]) | e4m3x2(e[3], e[2]) << 16;
+    for (int i = 0; i < H::NP; ++i) {
+      if (head.has_a(i)) *reinterpret_cast<uint32_t*>(out + head.a[i]) = codes_of<FORMAT>(v.a[i], s);
+      if (head.has_b(i)) *reinterpret_cast<uint32_t*>(out + head.b[i]) = codes_of<FORMAT>(v.b[i], s);
     }
-    *reinterpret_cast<uint32_t*>(out + d) = w;
+    if (head.j == 0) steps[row] = __fdiv_rn(a, kTop);
   }
-  if (j == 0) steps[row] = __fdiv_rn(a, kTop);
 }
 
 // Units of a token: its q heads (rotated into q_out), its k heads (rotated and
@@ -228,114 +316,160 @@ struct Append {
   int q_heads;
 };
 
-template <int FORMAT, int NC>
-__global__ void __launch_bounds__(kMaxThreads) append_kernel(Append a, KvRows rows, RopeArgs r, KvPages c) {
-  __shared__ __align__(16) float2 cs[kMaxHead / 2];
+template <int FORMAT, typename H>
+__global__ void __launch_bounds__(kThreads, H::kCtas)
+append_kernel(Append a, KvRows rows, RopeArgs r, KvPages c, int shares) {
+  __shared__ __align__(16) float2 angles[kWarps][kMaxHead / 2];
   pdl_release_dependents();
   pdl_wait_primary();
-  const int64_t t = blockIdx.x;
-  const int D = c.head_dim, units = a.q_heads + 2 * c.heads;
-  const int j = threadIdx.x % kRowLanes, step = gridDim.y * (blockDim.x / kRowLanes);
-  int u = blockIdx.y * (blockDim.x / kRowLanes) + threadIdx.x / kRowLanes;
-  auto input = [&](int unit) {
-    if (unit < a.q_heads) return a.q + t * a.q_stride + (int64_t)unit * D;
-    unit -= a.q_heads;
-    if (unit < c.heads) return a.k + t * a.k_stride + (int64_t)unit * D;
-    return a.v + t * a.v_stride + (int64_t)(unit - c.heads) * D;
+  const H head(c.head_dim, pairs_together(c.head_dim, r));
+  const int units = a.q_heads + 2 * c.heads;
+  const Task task = task_of_warp<H::kRows>(rows.T, units, shares);
+  if (task.first >= task.end) return;
+  float2* cs = angles[threadIdx.x >> 5];
+  const int64_t t = task.token;
+  const int sub = (threadIdx.x & 31) / H::L;
+  const float* qt = a.q + t * a.q_stride;
+  const float* kt = a.k + t * a.k_stride;
+  const float* vt = a.v + t * a.v_stride;
+  float* qo = a.q_out + t * a.q_out_stride;
+  auto input = [&](int u) {
+    const int kv = u - a.q_heads;
+    return kv < 0 ? qt + u * head.D : kv < c.heads ? kt + kv * head.D : vt + (kv - c.heads) * head.D;
   };
-  float4 v[NC];
-  if (u < units) load_row(input(u), D, j, v);
+  int at = task.first, u = min(at + sub, task.end - 1);
+  const float* in = input(u);
+  Row<H> v;
+  load_row(head, in, v);
   const int64_t place = kv_place(rows, c, t);
-  if (r.freq) fill_angles(r, rows.positions[t], cs);
-  __syncthreads();
+  if (r.freq && at < a.q_heads + c.heads) fill_angles(r, rows.positions[t], cs);
   if (place < 0) return;
-  // every lane of a warp makes every turn: shuffles, and q_out may be q
-  for (int at = u - (int)(threadIdx.x & 31) / kRowLanes; at < units; at += step, u += step) {
-    const bool have = u < units, is_q = u < a.q_heads, is_v = u >= a.q_heads + c.heads;
-    if (have && !is_v && r.freq) rotate_row(input(u), D, j, r, cs, v);
-    __syncwarp();
-    const int h = u - a.q_heads - (is_v ? c.heads : 0);
-    const int64_t row = have && !is_q ? place + ((int64_t)h << c.page_shift) : -1;
-    if (FORMAT != BITLINEAR_KV_BF16 || row >= 0)
-      write_row<FORMAT>(v, D, j, row, is_v ? c.v : c.k, is_v ? c.v_step : c.k_step);
-    if (have && is_q) store_row(a.q_out + t * a.q_out_stride + (int64_t)u * D, D, j, v);
-    if (u + step < units) load_row(input(u + step), D, j, v);
+  while (true) {
+    at += H::kRows;
+    const int u_next = min(at + sub, task.end - 1);
+    const float* in_next = input(u_next);
+    Row<H> next;
+    if (at < task.end) load_row(head, in_next, next);
+    const int kv = u - a.q_heads;
+    const bool is_v = kv >= c.heads;
+    if (!is_v && r.freq) rotate_row(head, in, r, cs, v);
+    __syncwarp();  // q_out may be q: a row is read before it is written
+    if (kv < 0) {
+      store_row(head, qo + u * head.D, v);
+    } else {
+      const int64_t row = place + ((int64_t)(is_v ? kv - c.heads : kv) << c.page_shift);
+      write_row<FORMAT>(head, v, row, is_v ? c.v : c.k, is_v ? c.v_step : c.k_step);
+    }
+    if (at >= task.end) return;
+    u = u_next;
+    in = in_next;
+    v = next;
   }
 }
 
-template <int FORMAT, int NC>
-__global__ void __launch_bounds__(kMaxThreads) read_kernel(KvPages c, KvRows rows, float* __restrict__ k_out,
-                                                           int64_t k_stride, float* __restrict__ v_out,
-                                                           int64_t v_stride) {
+// The codes of a chunk (8-bit: one word) as floats.
+template <int FORMAT>
+__device__ __forceinline__ float4 widened(uint32_t w) {
+  if constexpr (FORMAT == BITLINEAR_KV_INT8) {
+    return make_float4((float)(int8_t)w, (float)(int8_t)(w >> 8), (float)(int8_t)(w >> 16), (float)(int8_t)(w >> 24));
+  } else {
+    const uint32_t lo = half2_of_e4m3x2((uint16_t)w), hi = half2_of_e4m3x2((uint16_t)(w >> 16));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+}
+
+// The lane's chunks of a row of codes: a word each of 8-bit codes, two of bf16.
+template <int FORMAT, typename H>
+struct CodeRow {
+  uint2 a[H::NP], b[H::NP];
+  float step;
+};
+template <int FORMAT>
+__device__ __forceinline__ uint2 load_codes(const uint8_t* row, int d) {
+  if constexpr (FORMAT == BITLINEAR_KV_BF16) return *reinterpret_cast<const uint2*>(row + 2 * d);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(row + d), 0u);
+}
+template <int FORMAT>
+__device__ __forceinline__ float4 values_of(const uint2& w, float step) {
+  if constexpr (FORMAT == BITLINEAR_KV_BF16)
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xffff0000u));
+  const float4 e = widened<FORMAT>(w.x);
+  return make_float4(__fmul_rn(e.x, step), __fmul_rn(e.y, step), __fmul_rn(e.z, step), __fmul_rn(e.w, step));
+}
+
+template <int FORMAT, typename H>
+__global__ void __launch_bounds__(kThreads, H::kReadCtas)
+read_kernel(KvPages c, KvRows rows, int shares, float* __restrict__ k_out, int64_t k_stride,
+            float* __restrict__ v_out, int64_t v_stride) {
   pdl_release_dependents();
   pdl_wait_primary();
-  const int64_t t = blockIdx.x;
-  const int64_t place = kv_place(rows, c, t);
+  const H head(c.head_dim, c.head_dim / 8);
+  const Task task = task_of_warp<H::kRows>(rows.T, 2 * c.heads, shares);
+  if (task.first >= task.end) return;
+  const int64_t t = task.token, place = kv_place(rows, c, t);
   if (place < 0) return;
-  const int D = c.head_dim, j = threadIdx.x % kRowLanes;
-  for (int u = blockIdx.y * (blockDim.x / kRowLanes) + threadIdx.x / kRowLanes; u < 2 * c.heads;
-       u += gridDim.y * (blockDim.x / kRowLanes)) {
+  const int sub = (threadIdx.x & 31) / H::L;
+  float* kt = k_out + t * k_stride;
+  float* vt = v_out + t * v_stride;
+  auto fetch = [&](int u, CodeRow<FORMAT, H>& w) {
     const bool is_v = u >= c.heads;
-    const int h = is_v ? u - c.heads : u;
-    const int64_t row = place + ((int64_t)h << c.page_shift);
-    const void* codes = is_v ? c.v : c.k;
-    float4 v[NC];
-    if constexpr (FORMAT == BITLINEAR_KV_BF16) {
+    const int64_t row = place + ((int64_t)(is_v ? u - c.heads : u) << c.page_shift);
+    const uint8_t* codes = static_cast<const uint8_t*>(is_v ? c.v : c.k) + row * head.D * (FORMAT == BITLINEAR_KV_BF16 ? 2 : 1);
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int d = 4 * (j + kRowLanes * i);
-        if (d >= D) continue;
-        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(codes) + row * D + d);
-        v[i] = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                           __uint_as_float(w.y & 0xffff0000u));
-      }
-    } else {
-      uint32_t w[NC];
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int d = 4 * (j + kRowLanes * i);
-        if (d < D) w[i] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(codes) + row * D + d);
-      }
-      const float step = (is_v ? c.v_step : c.k_step)[row];
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        float e[4];
-        if constexpr (FORMAT == BITLINEAR_KV_INT8) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) e[k] = (float)(int8_t)(w[i] >> (8 * k));
-        } else {
-          const uint32_t lo = half2_of_e4m3x2((uint16_t)w[i]), hi = half2_of_e4m3x2((uint16_t)(w[i] >> 16));
-          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-          e[0] = a.x; e[1] = a.y; e[2] = b.x; e[3] = b.y;
-        }
-        v[i] = make_float4(__fmul_rn(e[0], step), __fmul_rn(e[1], step), __fmul_rn(e[2], step), __fmul_rn(e[3], step));
-      }
+    for (int i = 0; i < H::NP; ++i) {
+      w.a[i] = head.has_a(i) ? load_codes<FORMAT>(codes, head.a[i]) : make_uint2(0u, 0u);
+      w.b[i] = head.has_b(i) ? load_codes<FORMAT>(codes, head.b[i]) : make_uint2(0u, 0u);
     }
-    store_row((is_v ? v_out + t * v_stride : k_out + t * k_stride) + (int64_t)h * D, D, j, v);
+    w.step = FORMAT == BITLINEAR_KV_BF16 ? 1.0f : (is_v ? c.v_step : c.k_step)[row];
+  };
+  int at = task.first, u = min(at + sub, task.end - 1);
+  CodeRow<FORMAT, H> w;
+  fetch(u, w);
+  while (true) {
+    at += H::kRows;
+    const int u_next = min(at + sub, task.end - 1);
+    CodeRow<FORMAT, H> next;
+    if (at < task.end) fetch(u_next, next);
+    Row<H> v;
+#pragma unroll
+    for (int i = 0; i < H::NP; ++i) {
+      v.a[i] = values_of<FORMAT>(w.a[i], w.step);
+      v.b[i] = values_of<FORMAT>(w.b[i], w.step);
+    }
+    store_row(head, u >= c.heads ? vt + (u - c.heads) * head.D : kt + u * head.D, v);
+    if (at >= task.end) return;
+    u = u_next;
+    w = next;
   }
 }
 
-// One CTA per token while tokens fill the GPU (two CTAs an SM), else a token's
-// units shared out; a CTA's threads take its units in one turn up to kMaxThreads.
-struct Launch {
-  dim3 grid;
-  int threads;
-};
-Launch launch_for(int64_t T, int units, const DeviceInfo& dev) {
-  int64_t shares = (2 * (int64_t)dev.num_sms + T - 1) / T;
-  const int64_t most = ((int64_t)units * kRowLanes + kMinThreads - 1) / kMinThreads;
-  if (shares > most) shares = most;
-  const int64_t per = (units + shares - 1) / shares;
-  int64_t threads = (per + kWarpRows - 1) / kWarpRows * 32;
-  threads = threads < kMinThreads ? kMinThreads : threads > kMaxThreads ? kMaxThreads : threads;
-  return Launch{dim3((unsigned)T, (unsigned)shares, 1), (int)threads};
+// Warps that share a token's units.  A warp's time is its turns and about two more
+// (the lookups, the angles, the first rows' way), and warps beyond those resident wait
+// for a whole round: the number that makes rounds * time least.  (2039 tokens of 96
+// heads of 80: one warp a token 20.4 us, two 25.9.)
+int shares_for(int64_t T, int units, int rows, int ctas, const DeviceInfo& dev) {
+  const int64_t resident = (int64_t)dev.num_sms * ctas * kWarps;
+  const int turns = (units + rows - 1) / rows;
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= turns; ++s) {
+    const double time = (double)((T * s + resident - 1) / resident) * ((turns + s - 1) / s + 2);
+    if (s == 1 || time < least) {
+      least = time;
+      best = s;
+    }
+    if (T * s >= 8 * resident) break;
+  }
+  return best;
 }
 
 template <typename... Params, typename... Args>
-cudaError_t launch(void (*kernel)(Params...), const Launch& l, bool pdl, cudaStream_t stream, Args... args) {
+cudaError_t launch(void (*kernel)(Params...), int64_t warps, bool pdl, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = l.grid;
-  cfg.blockDim = dim3((unsigned)l.threads, 1, 1);
+  cfg.gridDim = dim3((unsigned)((warps + kWarps - 1) / kWarps), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -345,13 +479,20 @@ cudaError_t launch(void (*kernel)(Params...), const Launch& l, bool pdl, cudaStr
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
-// f(NC) with NC the smallest instantiated number of chunks a lane that holds D dims.
+// f(type) with the Head of D dims: of its own up to 128 in steps that models use, else of any.
+template <typename T>
+struct Tag {
+  using type = T;
+};
 template <typename F>
-cudaError_t with_chunks(int D, F f) {
-  if (D <= 64) return f(std::integral_constant<int, 4>());
-  if (D <= 80) return f(std::integral_constant<int, 5>());
-  if (D <= 128) return f(std::integral_constant<int, 8>());
-  return f(std::integral_constant<int, 16>());
+cudaError_t with_head(int D, F f) {
+  switch (D) {
+    case 64: return f(Tag<Head<1, 8, 64>>());
+    case 80: return f(Tag<Head<3, 4, 80>>());
+    case 96: return f(Tag<Head<3, 4, 96>>());
+    case 128: return f(Tag<Head<2, 8, 128>>());
+    default: return D <= 128 ? f(Tag<Head<2, 8, 0>>()) : f(Tag<Head<4, 8, 0>>());
+  }
 }
 template <typename F>
 cudaError_t with_format(int format, F f) {
@@ -365,9 +506,10 @@ cudaError_t with_format(int format, F f) {
 cudaError_t launch_rope(const float* x, int64_t x_stride, int64_t T, int H, int D, const int32_t* positions,
                         const RopeArgs& rope, float* y, int64_t y_stride, bool pdl, const DeviceInfo& dev,
                         cudaStream_t stream) {
-  return with_chunks(D, [&](auto nc) {
-    return launch(rope_kernel<decltype(nc)::value>, launch_for(T, H, dev), pdl, stream, x, x_stride, H, D, positions,
-                  rope, y, y_stride);
+  return with_head(D, [&](auto head) {
+    const int shares = shares_for(T, H, decltype(head)::type::kRows, decltype(head)::type::kCtas, dev);
+    return launch(rope_kernel<typename decltype(head)::type>, T * shares, pdl, stream, x, x_stride, T, H, D, shares,
+                  positions, rope, y, y_stride);
   });
 }
 
@@ -377,9 +519,10 @@ cudaError_t launch_kv_append(const float* q, int64_t q_stride, int q_heads, floa
                              cudaStream_t stream) {
   const Append a = {q, k, v, q_out, q_stride, k_stride, v_stride, q_out_stride, q_heads};
   return with_format(cache.format, [&](auto fmt) {
-    return with_chunks(cache.head_dim, [&](auto nc) {
-      return launch(append_kernel<decltype(fmt)::value, decltype(nc)::value>,
-                    launch_for(rows.T, q_heads + 2 * cache.heads, dev), pdl, stream, a, rows, rope, cache);
+    return with_head(cache.head_dim, [&](auto head) {
+      const int shares = shares_for(rows.T, q_heads + 2 * cache.heads, decltype(head)::type::kRows, decltype(head)::type::kCtas, dev);
+      return launch(append_kernel<decltype(fmt)::value, typename decltype(head)::type>, rows.T * shares, pdl, stream,
+                    a, rows, rope, cache, shares);
     });
   });
 }
@@ -387,9 +530,10 @@ cudaError_t launch_kv_append(const float* q, int64_t q_stride, int q_heads, floa
 cudaError_t launch_kv_read(const KvPages& cache, const KvRows& rows, float* k_out, int64_t k_stride, float* v_out,
                            int64_t v_stride, bool pdl, const DeviceInfo& dev, cudaStream_t stream) {
   return with_format(cache.format, [&](auto fmt) {
-    return with_chunks(cache.head_dim, [&](auto nc) {
-      return launch(read_kernel<decltype(fmt)::value, decltype(nc)::value>, launch_for(rows.T, 2 * cache.heads, dev),
-                    pdl, stream, cache, rows, k_out, k_stride, v_out, v_stride);
+    return with_head(cache.head_dim, [&](auto head) {
+      const int shares = shares_for(rows.T, 2 * cache.heads, decltype(head)::type::kRows, decltype(head)::type::kReadCtas, dev);
+      return launch(read_kernel<decltype(fmt)::value, typename decltype(head)::type>, rows.T * shares, pdl, stream,
+                    cache, rows, shares, k_out, k_stride, v_out, v_stride);
     });
   });
 }
