@@ -61,6 +61,8 @@ def parse_args():
     ap.add_argument("--no-prefill", action="store_true", help="skip the M=2048 prefill measurement")
     ap.add_argument("--no-weight-set", action="store_true",
                     help="skip the full BitNet-3B weight-set measurement (M = 1, 8, 32, 64)")
+    ap.add_argument("--attention", type=int, default=0, metavar="TOKENS",
+                    help="also measure the full weight set's step with every layer attending to so many cached tokens")
     ap.add_argument("--separate", action="store_true",
                     help="time separate act_quant + forward calls instead of bitlinear_linear")
     return ap.parse_args()
@@ -565,7 +567,7 @@ def measure_prefill(bl, dev, stream, dist, M=2048, launches=30):
     return out
 
 
-def measure_weight_set(bl, dev, stream, dist, Ms=(1, 8, 32, 64), reps=10):
+def measure_weight_set(bl, dev, stream, dist, Ms=(1, 8, 32, 64), reps=10, attention=0):
     """BitNet-3B full per-token weight set: 32 layers x (q, k, v, o 2560x2560;
     gate, up 2560->10240; down 10240->2560) plus the LM head 2560->50000, every
     matrix independently seeded N(0, 0.02) and quantised once (870,860,800
@@ -574,7 +576,10 @@ def measure_weight_set(bl, dev, stream, dist, Ms=(1, 8, 32, 64), reps=10):
     then the LM head and the greedy token (bitlinear_argmax, 4 bytes a token)
     -- each a bitlinear_linear_ws call (one shared workspace) on seeded synthetic inputs
     (attention and residuals are not part of this path), replayed as one CUDA
-    graph with PDL."""
+    graph with PDL.  With attention = n > 0 each layer also rotates and caches
+    its new tokens (bitlinear_kv_append, an int8 cache of its own) and attends
+    to n tokens a sequence (bitlinear_attention) between q||k||v and o, which
+    then reads the attention's output."""
     import torch
     from bitlinear_w1_a8_gb300 import synth
     D, F, V, L = synth.DIM_3B, synth.FFN_3B, synth.VOCAB, synth.LAYERS_3B
@@ -599,7 +604,7 @@ def measure_weight_set(bl, dev, stream, dist, Ms=(1, 8, 32, 64), reps=10):
     total_bytes += head_pk.numel()
     del W
     weights_n = sum(N * K for N, K in shapes) * L + V * D
-    out = {"packed_bytes_per_step": total_bytes, "weights": weights_n, "launch_calls_per_step": 4 * L + 2}
+    out = {"packed_bytes_per_step": total_bytes, "weights": weights_n, "launch_calls_per_step": (6 if attention else 4) * L + 2}
     for M in Ms:
         xa = synth.activations(M, D, synth.SEEDS["weight_set"]["x"]).to(dev)
         xb = synth.activations(M, F, synth.SEEDS["weight_set"]["x"] + 1).to(dev)
@@ -612,13 +617,17 @@ def measure_weight_set(bl, dev, stream, dist, Ms=(1, 8, 32, 64), reps=10):
         yu = torch.empty(M, F, dtype=torch.float32, device=dev)
         token = torch.empty(M, dtype=torch.int32, device=dev)
         fws = torch.empty(bl.bitlinear_forward_workspace(M, F), dtype=torch.uint8, device=dev)
+        attend = layer_attention(bl, dev, M, D, L, attention, (yq, yk, yv)) if attention else None
+        xo = attend.out.view(M, D) if attention else xa
 
         def step(s):
-            for mats in layers:
+            for layer, mats in enumerate(layers):
                 (q, sq, _), (k, sk, _), (v, sv, _), (o, so, _), (g, sg, _), (u, su, _), (d, sd, _) = mats
                 bl.bitlinear_linear_ws(xa, [(q, sq, yq), (k, sk, yk), (v, sv, yv)], xq_a, sx_a, fws,
                                        flags=bl.FLAG_PDL, stream=s)
-                bl.bitlinear_linear_ws(xa, [(o, so, ys[D])], xq_a, sx_a, fws, flags=bl.FLAG_PDL, stream=s)
+                if attention:
+                    attend(layer, s)
+                bl.bitlinear_linear_ws(xo, [(o, so, ys[D])], xq_a, sx_a, fws, flags=bl.FLAG_PDL, stream=s)
                 bl.bitlinear_linear_ws(xa, [(g, sg, ys[F]), (u, su, yu)], xq_a, sx_a, fws, flags=bl.FLAG_PDL,
                                        stream=s)
                 bl.bitlinear_linear_ws(xb, [(d, sd, ys[D])], xq_b, sx_b, fws, flags=bl.FLAG_PDL, stream=s)
@@ -647,8 +656,43 @@ def measure_weight_set(bl, dev, stream, dist, Ms=(1, 8, 32, 64), reps=10):
                         "packed_GBps": round(total_bytes / (ms * 1e-3) / 1e9, 1),
                         "tops": round(2.0 * M * weights_n / (ms * 1e-3) / 1e12, 2),
                         "us_per_token": round(ms * 1e3 / M, 3)}
-        del g
+        del g, attend
+    if attention:
+        out["attention_tokens"] = attention
+        out["cache_bytes_per_token_and_layer"] = 2 * D + 2 * synth.HEADS_3B * 4
     return out
+
+
+def layer_attention(bl, dev, M, D, layers, tokens, qkv):
+    """A callable (layer, stream) that caches the new tokens of q, k, v [M, D] in the layer's own
+    paged int8 cache, `tokens` long, and attends to it; its `out` is [M, heads, head_dim]."""
+    import torch
+    from bitlinear_w1_a8_gb300 import synth
+    H, page = synth.HEADS_3B, 64
+    hd, width = D // H, -(-tokens // page)
+    g = torch.Generator(device=dev)
+    g.manual_seed(synth.SEEDS["weight_set"]["x"])
+    shape = (M * width, H, page, hd)
+    caches = []
+    for _ in range(layers):
+        codes = [torch.randint(-127, 128, shape, generator=g, dtype=torch.int8, device=dev) for _ in "kv"]
+        caches.append((*codes, *(torch.full(shape[:3], 1 / 64, device=dev) for _ in "kv")))
+    table = torch.randperm(M * width, generator=g, device=dev).to(torch.int32).view(M, width)
+    lengths = torch.full((M,), tokens, dtype=torch.int32, device=dev)
+    positions = lengths - 1
+    rope = (bl.bitlinear_rope_frequencies(hd).to(dev), bl.ROPE_HALF)
+    q, k, v = (t.view(M, H, hd) for t in qkv)
+    out = torch.empty(M, H, hd, dtype=torch.float32, device=dev)
+    need = bl.bitlinear_attention_workspace(M, H, H, hd)
+    space = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+
+    def attend(layer, stream):
+        bl.bitlinear_kv_append(k, v, caches[layer], positions, table, q=q, q_out=q, rope=rope, flags=bl.FLAG_PDL,
+                               stream=stream)
+        bl.bitlinear_attention(q, caches[layer], table, lengths, out, workspace=space, flags=bl.FLAG_PDL, stream=stream)
+
+    attend.out = out
+    return attend
 
 
 def measure_ffn_1b3(bl, dev, stream, dist, Ms=(1, 512), reps=50):
@@ -973,6 +1017,7 @@ def run_ours(args, rank, world, local_rank):
 
     prefill = None if args.no_prefill else measure_prefill(bl, dev, stream, dist)
     weight_set = None if args.no_weight_set else measure_weight_set(bl, dev, stream, dist)
+    with_attention = measure_weight_set(bl, dev, stream, dist, attention=args.attention) if args.attention > 0 else None
     ffn_1b3 = None if args.no_weight_set else measure_ffn_1b3(bl, dev, stream, dist)
 
     cpu = None
@@ -1026,6 +1071,8 @@ def run_ours(args, rank, world, local_rank):
             line["prefill_m2048"] = prefill
         if weight_set:
             line["weight_set_3b"] = weight_set
+        if with_attention:
+            line["weight_set_3b_attention"] = with_attention
         if ffn_1b3:
             line["ffn_1b3"] = ffn_1b3
         if cpu:

@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 # BitNet-3B and 1.3B dimensions ("Model Configurations").
-DIM_3B, FFN_3B, VOCAB, LAYERS_3B = 2560, 10240, 50000, 32
+DIM_3B, FFN_3B, VOCAB, LAYERS_3B, HEADS_3B = 2560, 10240, 50000, 32, 32
 DIM_1B3, FFN_1B3 = 2048, 8192
 
 WEIGHT_STD = 0.02
