@@ -111,17 +111,19 @@ __device__ __forceinline__ float2 lds_float2(uint32_t a) {
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
   return v;
 }
-// A float of CTA `rank` of the cluster, at the address that `a` has in this CTA.
-__device__ __forceinline__ float lds_cluster(uint32_t a, int rank) {
+// Stores a float in CTA `rank` of the cluster, at the address that `a` has in this CTA.
+__device__ __forceinline__ void sts_cluster(uint32_t a, int rank, float v) {
   uint32_t r;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
+}
+__device__ __forceinline__ float lds_float(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float exp2_of(float x) {  // relative error 2^-22, 0 below -126
   float y;
@@ -189,7 +191,7 @@ __device__ __forceinline__ uint32_t next_part(float& x, float& y) {  // bf16 par
 struct Source {
   const uint8_t *k, *v;    // the head's rows of page 0
   const float *ks, *vs;
-  int64_t first, len;      // first <= t < len
+  uint32_t first, len;     // first <= t < len
 };
 
 // Requests a step whose every token counts and has a page, head_dim == DT: a
@@ -226,13 +228,13 @@ __device__ __forceinline__ void request_whole(const Source& r, const int64_t (&r
 // Requests any step; `ok` says which halves have a page.  Rows that do not count
 // are zeroed, so that whatever they hold (NaN among it) meets no weight of 0.
 template <int FORMAT, int DT>
-__device__ __forceinline__ void request_part(const Source& r, const KvPages& c, int64_t t0, const int64_t (&row)[2],
+__device__ __forceinline__ void request_part(const Source& r, const KvPages& c, uint32_t t0, const int64_t (&row)[2],
                                              uint32_t ok, uint32_t stage, int lane) {
   using S = Shape<FORMAT, DT>;
   const int row_bytes = c.head_dim * S::kBytes, chunks = row_bytes / 16;
 #pragma unroll
   for (int s = 0; s < S::kTokens / 16; ++s) {
-    const int64_t t = t0 + 16 * s;
+    const uint32_t t = t0 + 16 * s;
     const bool have = (ok >> s) & 1u;
     const uint8_t* k = r.k + row[s] * row_bytes;
     const uint8_t* v = r.v + row[s] * row_bytes;
@@ -255,27 +257,28 @@ __device__ __forceinline__ void request_part(const Source& r, const KvPages& c, 
   }
 }
 
-// Joins `parts` partials of one head's dim d: part i is at base + i * apart (its
-// dims, then m and the sum) of this CTA, or of CTA i of the cluster.
+// Joins `parts` partials: the values are at `value` and every `apart` bytes on, the
+// references and sums (side by side) at `scale` and every `scales_apart`.
 struct Joined {
   float value, m, sum;
 };
-template <bool CLUSTER>
-__device__ __forceinline__ Joined join(uint32_t base, uint32_t apart, int parts, int d, int dims) {
+__device__ __forceinline__ Joined join(uint32_t value, uint32_t apart, uint32_t scale, uint32_t scales_apart, int parts) {
   Joined j = {0.0f, kUnset, 0.0f};
-  auto at = [&](int i, int f) {
-    float v;
-    if constexpr (CLUSTER) return lds_cluster(base + 4 * f, i);
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(base + i * apart + 4 * f));
-    return v;
-  };
-  for (int i = 0; i < parts; ++i) j.m = fmaxf(j.m, at(i, dims));
+  for (int i = 0; i < parts; ++i) j.m = fmaxf(j.m, lds_float(scale + i * scales_apart));
   for (int i = 0; i < parts; ++i) {
-    const float f = exp2_of(at(i, dims) - j.m);
-    j.sum = fmaf(at(i, dims + 1), f, j.sum);
-    j.value = fmaf(at(i, d), f, j.value);
+    const float2 s = lds_float2(scale + i * scales_apart);
+    const float f = exp2_of(s.x - j.m);
+    j.sum = fmaf(s.y, f, j.sum);
+    j.value = fmaf(lds_float(value + i * apart), f, j.value);
   }
   return j;
+}
+
+// Where a CTA receives what its cluster's CTAs have for its share of a row's dims:
+// [CTA][share's dims] and [CTA][head][m, sum], behind the rings.
+__host__ __device__ __forceinline__ int share_of(int heads, int D, int splits) { return (heads * D + splits - 1) / splits; }
+__host__ __device__ __forceinline__ int received_bytes(int heads, int D, int splits) {
+  return splits > 1 ? splits * (share_of(heads, D, splits) + 1 + 2 * heads) * 4 : 0;
 }
 
 // How rows are shared out: `splits` CTAs each (a cluster), or (splits == 0) in
@@ -289,15 +292,16 @@ struct Shares {
 };
 
 // Tokens first <= t < len of a sequence that count, in steps of T from first / T on.
+// A length is at most 2^31 - 1, so tokens and the steps past them fit in 32 bits.
 template <int T>
 struct Span {
-  int64_t first, len;
-  __device__ __forceinline__ Span(int64_t length, int64_t most, int64_t window) {
-    len = length < most ? length : most;
-    first = window > 0 && len > window ? len - window : 0;
+  uint32_t first, len;
+  __device__ __forceinline__ Span(int32_t length, int64_t most, int64_t window) {
+    len = length <= 0 ? 0u : length < most ? (uint32_t)length : (uint32_t)most;
+    first = window > 0 && len > window ? len - (uint32_t)window : 0u;
   }
-  __device__ __forceinline__ int64_t begin() const { return first / T * T; }
-  __device__ __forceinline__ int64_t steps() const { return len > first ? (len + T - 1) / T - first / T : 0; }
+  __device__ __forceinline__ uint32_t begin() const { return first / T * T; }
+  __device__ __forceinline__ int steps() const { return len > first ? (int)((len + T - 1) / T - first / T) : 0; }
 };
 
 // Sums of a value over the block's threads: of those up to this one, and of all.
@@ -331,7 +335,7 @@ template <int T>
 __device__ __forceinline__ Part find_part(const AttendArgs& a, int64_t most, int rows_a_seq) {
   __shared__ int scratch[kWarps], found[3];
   const int each = ((int)a.B + kThreads - 1) / kThreads, from = threadIdx.x * each, to = min((int)a.B, from + each);
-  auto steps_of = [&](int b) { return (int)Span<T>(a.lengths[b], most, a.window).steps(); };
+  auto steps_of = [&](int b) { return Span<T>(a.lengths[b], most, a.window).steps(); };
   int steps = 0, some = 0;
   for (int b = from; b < to; ++b) {
     const int n = steps_of(b);
@@ -396,6 +400,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
       reinterpret_cast<uint4*>(smem + warp * S::kWarpBytes)[i] = make_uint4(0, 0, 0, 0);
     __syncwarp();
   }
+  if (sh.splits > 1) cluster_arrive();  // waited for before the first word goes to another CTA
   pdl_wait_primary();
 
   // The CTA's row (sequence b, head `row` of its key heads and groups of q heads)
@@ -420,13 +425,17 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
 
   // The warp's steps are every (splits * kWarps)-th one of the row's.
   const int32_t* table = a.table + b * a.table_stride;
+  const uint32_t columns = (uint32_t)(most < 0x7fffffff ? most : 0x7fffffff);  // tokens that the table has room for
   int32_t page[2] = {-1, -1};
-  auto look_up = [&](int64_t t) {  // the pages of the step at t (columns of the table, whatever the length)
-    page[0] = t < most ? table[t >> c.page_shift] : -1;
-    if constexpr (S::kTokens == 32) page[1] = t + 16 < most ? table[(t + 16) >> c.page_shift] : -1;
+  auto look_up = [&](uint32_t t) {  // the pages of the step at t (columns of the table, whatever the length)
+    page[0] = t < columns ? table[t >> c.page_shift] : -1;
+    if constexpr (S::kTokens == 32) {
+      page[1] = page[0];
+      if (c.page_shift == 4) page[1] = t + 16 < columns ? table[(t + 16) >> 4] : -1;
+    }
   };
-  const int64_t lap = (int64_t)splits * kWarps * S::kTokens;
-  int64_t t_ask = (int64_t)(split * kWarps + warp) * S::kTokens;
+  const uint32_t lap = (uint32_t)splits * (kWarps * S::kTokens);
+  uint32_t t_ask = (uint32_t)(split * kWarps + warp) * S::kTokens;
   if (a.window <= 0) look_up(t_ask);  // the first page is known before the length
   const Span<S::kTokens> span(a.lengths[b], most, a.window);
   if (a.window > 0) {
@@ -443,7 +452,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   r.vs = c.v_step + head_row;
   r.first = span.first;
   r.len = span.len;
-  int64_t t0 = t_ask;  // the step in hand
+  uint32_t t0 = t_ask;  // the step in hand
 
   uint32_t oks = 0;  // two bits a requested step (its halves have pages), the newest lowest
   uint32_t ask_at = ring;
@@ -456,7 +465,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
       for (int s = 0; s < S::kTokens / 16; ++s) {
         if (t_ask + 16 * s < r.len && (uint32_t)page[s] < (uint32_t)c.num_pages) {
           ok |= 1u << s;
-          place[s] = (((int64_t)page[s] * c.heads) << c.page_shift) + ((int)(t_ask + 16 * s) & ((1 << c.page_shift) - 1));
+          place[s] = (((int64_t)page[s] * c.heads) << c.page_shift) + ((t_ask + 16 * s) & ((1u << c.page_shift) - 1));
         }
       }
       oks |= ok;
@@ -564,7 +573,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     if (ok != (S::kTokens == 32 ? 3u : 1u) || t0 < r.first || t0 + S::kTokens > r.len) {
 #pragma unroll
       for (int j = 0; j < S::kTiles; ++j) {
-        const int64_t t = t0 + 8 * j + 2 * qd;
+        const uint32_t t = t0 + 8 * j + 2 * qd;
         const bool have = (ok >> (j / 2)) & 1u;
         if (!have || t < r.first || t >= r.len) lg[j].x = -INFINITY;
         if (!have || t + 1 < r.first || t + 1 >= r.len) lg[j].y = -INFINITY;
@@ -724,6 +733,10 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   __syncthreads();
 
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+  auto of_warps = [&](int h, int d) {
+    const uint32_t p = base + h * S::kPartial;
+    return join(p + 4 * d, S::kWarpBytes, p + 4 * DT, S::kWarpBytes, kWarps);
+  };
   auto finish = [&](int h, int d, const Joined& j) {
     a.out[b * a.out_stride + (int64_t)(hq + h) * D + d] = j.sum > 0.0f ? j.value / j.sum : 0.0f;  // no token: zeros
   };
@@ -731,7 +744,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     float* part = sh.parts + (int64_t)blockIdx.x * min(kRowHeads, group) * (D + 4);
     for (int i = threadIdx.x; i < heads * D; i += kThreads) {
       const int h = i / D, d = i - h * D;
-      const Joined j = join<false>(base + h * S::kPartial, S::kWarpBytes, kWarps, d, DT);
+      const Joined j = of_warps(h, d);
       if (splits == 1) {
         finish(h, d, j);
       } else {
@@ -741,31 +754,26 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     }
     return;
   }
-  // The CTA's own partials first (kept in registers across the barrier: the
-  // warps' partials share their memory), then the cluster's.
-  constexpr int kMine = (kRowHeads * DT + kThreads - 1) / kThreads;
-  Joined own[kMine];
-#pragma unroll
-  for (int n = 0; n < kMine; ++n) {
-    const int i = threadIdx.x + n * kThreads;
-    if (i < heads * DT) own[n] = join<false>(base + i / DT * S::kPartial, S::kWarpBytes, kWarps, i % DT, DT);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < kMine; ++n) {
-    const int i = threadIdx.x + n * kThreads;
-    if (i >= heads * DT) continue;
-    float* p = reinterpret_cast<float*>(smem + i / DT * S::kPartial);
-    p[i % DT] = own[n].value;
-    if (i % DT == 0) {
-      p[DT] = own[n].m;
-      p[DT + 1] = own[n].sum;
+  // Every CTA sends each of the cluster its share of the dims, then joins its own.
+  const int share = share_of(heads, D, splits);
+  const uint32_t values = base + (uint32_t)S::kSmem, scales = values + (splits * share + 1) / 2 * 8;
+  cluster_wait();  // all of the cluster's CTAs have begun
+  for (int i = threadIdx.x; i < heads * D; i += kThreads) {
+    const int h = i / D, d = i - h * D;
+    const Joined j = of_warps(h, d);
+    sts_cluster(values + (split * share + i % share) * 4, i / share, j.value);
+    if (d < splits) {  // dim r's thread tells CTA r (16 dims at least, 8 CTAs at most)
+      sts_cluster(scales + (split * heads + h) * 8, d, j.m);
+      sts_cluster(scales + (split * heads + h) * 8 + 4, d, j.sum);
     }
   }
-  cluster_sync();
-  for (int i = split * kThreads + threadIdx.x; i < heads * D; i += splits * kThreads)
-    finish(i / D, i % D, join<true>(base + i / D * S::kPartial, 0, splits, i % D, DT));
-  cluster_sync();  // no CTA leaves while another reads its partials
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  for (int i = threadIdx.x; i < share && split * share + i < heads * D; i += kThreads) {
+    const int h = (split * share + i) / D, d = split * share + i - h * D;
+    finish(h, d, join(values + 4 * i, 4 * share, scales + 8 * h, 8 * heads, splits));
+  }
 }
 
 // Joins the parts of rows that several CTAs had: one CTA a (sequence, q head); groups
@@ -853,7 +861,8 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
   const auto kernel = attend_kernel<FORMAT, DT>;
   static thread_local int configured_device = -1;
   if (configured_device != dev.device) {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)S::kSmem + received_bytes(kRowHeads, DT, kMaxCluster));
     if (err != cudaSuccess) return err;
     configured_device = dev.device;
   }
@@ -892,6 +901,7 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
     return cudaLaunchKernelEx(&cfg, join_kernel<S::kTokens>, a, c, sh);
   }
   sh.sorted = a.B > 1 && a.B <= kSortSeqs && rows * sh.splits > ctas;
+  cfg.dynamicSmemBytes = S::kSmem + received_bytes(a.q_heads / c.heads < kRowHeads ? a.q_heads / c.heads : kRowHeads, c.head_dim, sh.splits);
   const int64_t per_launch = (int64_t)0x7fffffff / (per_seq * sh.splits);  // sequences a grid holds
   for (; sh.b0 < a.B; sh.b0 += per_launch) {
     const int64_t n = a.B - sh.b0 < per_launch ? a.B - sh.b0 : per_launch;
