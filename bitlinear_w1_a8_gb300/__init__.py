@@ -12,6 +12,11 @@ import ctypes
 import functools
 import os
 
+try:
+    import torch
+except ImportError:  # every call that takes tensors needs it
+    torch = None
+
 __all__ = [
     "BitLinearError", "load_library", "library_path",
     "bitlinear_abi_version", "bitlinear_status_string", "bitlinear_packed_bytes",
@@ -411,17 +416,23 @@ def bitlinear_linear_ws(x, weights, xq, x_scale, workspace, mul=None, rms_weight
 # fails: for an unusual layout, or to say what is wrong.
 
 
+def _current_device():
+    try:  # without torch.cuda's lazy initialisation: a CUDA tensor is there already
+        return torch._C._cuda_getDevice()
+    except AttributeError:
+        return torch.cuda.current_device()
+
+
 def _device(t, name):
     """The index of the tensor's device, which must be the current one: the library launches there."""
-    import torch
     try:
         at = t.get_device()
     except AttributeError:
         at = -1
     if at < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if at != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current device cuda:{torch.cuda.current_device()}, got {t.device}")
+    if at != _current_device():
+        raise ValueError(f"{name} must be on the current device cuda:{_current_device()}, got {t.device}")
     return at
 
 
@@ -433,7 +444,6 @@ def _need_on(t, at, dtype, name, shape=None):
 
 def _rows(t, at, name, shape):
     """The row stride (elements) of fp32 [T, H, D] rows: heads side by side, rows any stride apart."""
-    import torch
     if not getattr(t, "is_cuda", False):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.float32:
@@ -453,7 +463,6 @@ def _rows(t, at, name, shape):
 
 def _page_table(t, at, rows=None):
     """(rows, columns, row stride) of the int32 page table: contiguous rows, any stride apart."""
-    import torch
     if not getattr(t, "is_cuda", False) or t.dtype != torch.int32:
         raise TypeError("page_table must be an int32 CUDA tensor")
     shape = t.shape
@@ -471,7 +480,6 @@ def _page_table(t, at, rows=None):
 
 def _kv_pages(cache, at):
     """BitLinearKVPages of (k, v, k_step, v_step), the steps None or left out for bf16."""
-    import torch
     k, v = cache[0], cache[1]
     k_step, v_step = (cache[2], cache[3]) if len(cache) > 2 else (None, None)
     if not getattr(k, "is_cuda", False):
@@ -503,7 +511,6 @@ def _kv_pages(cache, at):
 
 def _rope_spec(rope, at):
     """BitLinearRopeSpec of (freq, layout) or (freq, layout, amplitude)."""
-    import torch
     freq = rope[0]
     if not (freq.get_device() == at and freq.dtype is torch.float64 and freq.is_contiguous()):
         _need_on(freq, at, torch.float64, "rope's freq")
@@ -515,7 +522,6 @@ def bitlinear_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int
                                high: float = 32.0):
     """The rot_dim / 2 rotary frequencies (radians a position) as a fp64 CPU tensor; move it
     to the device once."""
-    import torch
     n = max(0, int(rot_dim)) // 2
     out = (ctypes.c_double * max(1, n))()
     _check(load_library().bitlinear_rope_frequencies(
@@ -531,7 +537,6 @@ def bitlinear_rope(x, positions, rope, y, flags: int = 0, stream=None):
     (bitlinear_rope_frequencies) and layout ROPE_HALF or ROPE_INTERLEAVED.  y may be x.
     Rows may lie any multiple of 4 floats apart.
     """
-    import torch
     at = _device(x, "x")
     shape = x.shape
     if len(shape) != 3:
@@ -550,7 +555,6 @@ def bitlinear_rope(x, positions, rope, y, flags: int = 0, stream=None):
 
 def _row_places(positions, page_table, seq, T, at):
     """(positions, seq, table addresses, table stride, sequences, pages) of T rows."""
-    import torch
     i32 = torch.int32
     if (positions.dtype is i32 and page_table.dtype is i32 and positions.get_device() == page_table.get_device() == at
             and positions.shape == (T,) and positions.is_contiguous() and page_table.is_contiguous()
@@ -577,7 +581,6 @@ def bitlinear_kv_append(k, v, cache, positions, page_table, seq=None, q=None, q_
     positions, seq: int32 [T]; page_table: int32 [sequences, pages]; seq None: row i is of
     sequence i.  Rows with a negative position are padding.  rope: as for bitlinear_rope.
     """
-    import torch
     at = _device(k, "k")
     pages = _kv_pages(cache, at)
     f32, T, Hk, D = torch.float32, k.shape[0], pages.num_heads, pages.head_dim
@@ -610,7 +613,6 @@ def bitlinear_kv_append(k, v, cache, positions, page_table, seq=None, q=None, q_
 
 def bitlinear_kv_read(cache, positions, page_table, k_out, v_out, seq=None, flags: int = 0, stream=None):
     """k_out, v_out [T, heads, head_dim] fp32 = the cached rows at (seq[i], positions[i])."""
-    import torch
     at = _device(k_out, "k_out")
     pages = _kv_pages(cache, at)
     f32, T, Hk, D = torch.float32, k_out.shape[0], pages.num_heads, pages.head_dim
@@ -635,7 +637,6 @@ def bitlinear_attention(q, cache, page_table, lengths, out, workspace=None, scal
     """out [B, q_heads, head_dim] = attention of q over the lengths[b] cached tokens of each
     sequence (the last `window` of them when it is not 0); scale None: 1 / sqrt(head_dim).
     cache and page_table: as for bitlinear_kv_append; lengths: int32 [B]."""
-    import torch
     at = _device(q, "q")
     pages = _kv_pages(cache, at)
     shape = q.shape

@@ -482,8 +482,9 @@ bitlinear_status bitlinear_kv_read(const bitlinear_kv_pages* cache, int64_t T, c
                                    int64_t num_seqs, int64_t max_pages, float* k_out, int64_t k_stride,
                                    float* v_out, int64_t v_stride, int flags, void* stream);
 
-/* Workspace bytes that let bitlinear_attention split its sequences further (0
- * where no split beyond one launch's is ever taken, and for sizes out of range). */
+/* Workspace bytes with which bitlinear_attention gives long sequences workers in
+ * proportion to their lengths (0 where the call has rows enough without, and for sizes
+ * out of range).  A function of these sizes alone. */
 size_t bitlinear_attention_workspace(int64_t B, int num_q_heads, int num_kv_heads, int head_dim);
 
 /* Attention of one new token per sequence over its cached tokens:
@@ -503,7 +504,8 @@ size_t bitlinear_attention_workspace(int64_t B, int num_q_heads, int num_kv_head
  *   scale      finite; 1 / sqrt(head_dim) in most models.
  *   workspace  device, 16-byte aligned, at least bitlinear_attention_workspace()
  *              bytes, contents irrelevant, not shared with a call that may run at the
- *              same time; or NULL: very long sequences of few heads run slower.
+ *              same time; or NULL: every sequence then has one thread-block cluster a
+ *              key head, and very long sequences of few heads run slower.
  * Nothing past a row's length is read.  Results do not depend on timing: the parts of
  * a split sequence are joined in a fixed order.
  * Several rows may attend to one sequence (rows of one page list with lengths n,
