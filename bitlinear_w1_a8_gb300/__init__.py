@@ -61,6 +61,7 @@ EXPORTED_SYMBOLS = (
 )
 
 _lib = None
+_marshal = None  # the compiled common case of the attention calls (csrc/marshal.cpp), where it was built
 
 
 class BitLinearWeight(ctypes.Structure):
@@ -156,7 +157,26 @@ def load_library(path: str | None = None):
     lib.bitlinear_device_status.restype = st
     if path is None:
         _lib = lib
+        _load_marshal(lib)
     return lib
+
+
+def _load_marshal(lib):
+    global _marshal
+    at = os.path.join(_HERE, "_build", "bitlinear_marshal.so")
+    if torch is None or not os.path.exists(at):
+        return
+    import importlib.machinery
+    import importlib.util
+    loader = importlib.machinery.ExtensionFileLoader("bitlinear_marshal", at)
+    try:
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("bitlinear_marshal", loader))
+        loader.exec_module(module)
+    except ImportError:  # built for another torch
+        return
+    module.bind(*(ctypes.cast(getattr(lib, "bitlinear_" + name), ctypes.c_void_p).value
+                  for name in ("rope", "kv_append", "kv_read", "attention")))
+    _marshal = module
 
 
 def _check(status: int, what: str):
@@ -411,9 +431,11 @@ def bitlinear_linear_ws(x, weights, xq, x_scale, workspace, mul=None, rms_weight
 
 # --- rotary positions, the paged key-value cache and attention over it ---
 #
-# These calls take many tensors and are made once or twice a layer and token, so each
-# checks its tensors in one expression and goes through them one by one only when that
-# fails: for an unusual layout, or to say what is wrong.
+# These calls take many tensors and are made once or twice a layer and token, so the
+# compiled marshal takes the common case (contiguous tensors that fit).  It answers None
+# for every other; then, or where it was not built, each call checks its tensors here, in
+# one expression, and one by one when that fails: for an unusual layout, or to say what
+# is wrong.
 
 
 def _current_device():
@@ -537,6 +559,10 @@ def bitlinear_rope(x, positions, rope, y, flags: int = 0, stream=None):
     (bitlinear_rope_frequencies) and layout ROPE_HALF or ROPE_INTERLEAVED.  y may be x.
     Rows may lie any multiple of 4 floats apart.
     """
+    if _marshal is not None:
+        status = _marshal.rope(x, positions, rope, y, flags, stream)
+        if status is not None:
+            return _check(status, "bitlinear_rope")
     at = _device(x, "x")
     shape = x.shape
     if len(shape) != 3:
@@ -581,6 +607,10 @@ def bitlinear_kv_append(k, v, cache, positions, page_table, seq=None, q=None, q_
     positions, seq: int32 [T]; page_table: int32 [sequences, pages]; seq None: row i is of
     sequence i.  Rows with a negative position are padding.  rope: as for bitlinear_rope.
     """
+    if _marshal is not None:
+        status = _marshal.kv_append(k, v, cache, positions, page_table, seq, q, q_out, rope, flags, stream)
+        if status is not None:
+            return _check(status, "bitlinear_kv_append")
     at = _device(k, "k")
     pages = _kv_pages(cache, at)
     f32, T, Hk, D = torch.float32, k.shape[0], pages.num_heads, pages.head_dim
@@ -613,6 +643,10 @@ def bitlinear_kv_append(k, v, cache, positions, page_table, seq=None, q=None, q_
 
 def bitlinear_kv_read(cache, positions, page_table, k_out, v_out, seq=None, flags: int = 0, stream=None):
     """k_out, v_out [T, heads, head_dim] fp32 = the cached rows at (seq[i], positions[i])."""
+    if _marshal is not None:
+        status = _marshal.kv_read(cache, positions, page_table, k_out, v_out, seq, flags, stream)
+        if status is not None:
+            return _check(status, "bitlinear_kv_read")
     at = _device(k_out, "k_out")
     pages = _kv_pages(cache, at)
     f32, T, Hk, D = torch.float32, k_out.shape[0], pages.num_heads, pages.head_dim
@@ -637,6 +671,10 @@ def bitlinear_attention(q, cache, page_table, lengths, out, workspace=None, scal
     """out [B, q_heads, head_dim] = attention of q over the lengths[b] cached tokens of each
     sequence (the last `window` of them when it is not 0); scale None: 1 / sqrt(head_dim).
     cache and page_table: as for bitlinear_kv_append; lengths: int32 [B]."""
+    if _marshal is not None:
+        status = _marshal.attention(q, cache, page_table, lengths, out, workspace, scale, window, flags, stream)
+        if status is not None:
+            return _check(status, "bitlinear_attention")
     at = _device(q, "q")
     pages = _kv_pages(cache, at)
     shape = q.shape

@@ -3,6 +3,9 @@
 Each .cu file is compiled by nvcc in parallel into bitlinear_w1_a8_gb300/_build/
 and linked into bitlinear_w1_a8_gb300/_build/libbitlinear.so.  Needs nvcc but
 no GPU (the container cross-compiles; the GPU host rebuilds for its own CPU).
+Beside it, _build/bitlinear_marshal.so (host code, g++ with the headers of Python
+and torch) reads the attention calls' tensors faster than the Python binding can;
+where it cannot be built the binding does all of it.
 """
 from __future__ import annotations
 
@@ -11,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(BUILD, "libbitlinear.so")
+MARSHAL = os.path.join(BUILD, "bitlinear_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -42,6 +47,40 @@ def _stale(out: str, deps: list[str]) -> bool:
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _marshal_command(out: str) -> list[str] | None:
+    """The compile command of marshal.cpp, or None without torch or the headers it takes."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    at, python = os.path.dirname(torch.__file__), sysconfig.get_paths()["include"]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    if not (os.path.exists(os.path.join(python, "Python.h"))
+            and os.path.exists(os.path.join(at, "include", "torch", "csrc", "autograd", "python_variable.h"))
+            and shutil.which("g++")):
+        return None
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", os.path.join(at, "include"),
+            "-I", os.path.join(at, "include", "torch", "csrc", "api", "include"), "-I", cuda, "-I", python,
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", os.path.join(CSRC, "marshal.cpp"),
+            "-o", out, "-L", os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
+def _build_marshal(force: bool, verbose: bool) -> None:
+    if not (force or _stale(MARSHAL, [os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "bitlinear.h"), __file__])):
+        return
+    tmp = MARSHAL + f".{os.getpid()}.tmp"
+    cmd = _marshal_command(tmp)
+    if cmd is None:
+        return
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(f"{os.path.basename(MARSHAL)} not built, the Python binding does its work:\n{r.stderr[-2000:]}\n")
+        return
+    os.replace(tmp, MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
@@ -69,10 +108,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, max(1, len(jobs)))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, 1 + len(jobs))) as ex:
+        marshal = ex.submit(_build_marshal, force, verbose)
         for err in ex.map(run, jobs):
             if ptxas_verbose and err:
                 sys.stderr.write(err)
+        marshal.result()
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         run([nvcc, *ARCH, "-shared", "-Xlinker", "--no-undefined", "-o", tmp, *objs])

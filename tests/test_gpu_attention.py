@@ -492,7 +492,35 @@ def test_results_repeat_bit_for_bit_and_streams_do_not_mix():
             assert torch.equal(want, o)
 
 
-def test_binding_refusals():
+def test_binding_with_and_without_the_compiled_marshal(monkeypatch):
+    if bl._marshal is None:
+        pytest.skip("bitlinear_marshal.so was not built")
+    T, Hq, Hk, D, page = 5, 6, 3, 80, 16
+    for fmt in plain.FORMATS:
+        results = []
+        for marshal in (bl._marshal, None):
+            monkeypatch.setattr(bl, "_marshal", marshal)
+            cache = tuple(c if c is None else c.zero_() if c.dtype != torch.float8_e4m3fn else c.view(torch.uint8).zero_().view(c.dtype)
+                          for c in plain.make_cache(fmt, 2 * T, Hk, page, D, 4))
+            cache = cache[:2] if fmt == "bf16" else cache
+            q, k, v = normal((T, Hq, D), 1).cuda(), normal((T, Hk, D), 2).cuda(), normal((T, Hk, D), 3).cuda()
+            table, pos, freq = torch.arange(2 * T, dtype=torch.int32, device="cuda").view(T, 2), ints([3, 17, 0, 31, -1]), bl.bitlinear_rope_frequencies(64).cuda()
+            y, q_out, ks, vs, out = torch.zeros_like(k), torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v), torch.zeros_like(q)
+            bl.bitlinear_rope(k, pos, (freq, bl.ROPE_INTERLEAVED, 1.5), y)
+            bl.bitlinear_kv_append(k, v, cache, pos, table, q=q, q_out=q_out, rope=(freq, bl.ROPE_HALF))
+            bl.bitlinear_kv_append(k, v, cache, pos - 1, table, seq=ints([1, 0, 2, 4, 3]), stream=torch.cuda.current_stream())
+            bl.bitlinear_kv_read(cache, pos, table, ks, vs)
+            bl.bitlinear_attention(q_out, cache, table, pos + 1, out, scale=0.3, window=9)
+            bl.bitlinear_attention(q_out, cache, table, pos + 1, q, flags=bl.FLAG_PDL, stream=torch.cuda.current_stream().cuda_stream)
+            results.append([y, q_out, ks, vs, out, q])
+        for a, b in zip(*results):
+            assert torch.isfinite(a).all() and a.abs().sum() > 0 and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("compiled", [True, False])
+def test_binding_refusals(compiled, monkeypatch):
+    if not compiled:
+        monkeypatch.setattr(bl, "_marshal", None)
     cache = plain.make_cache("int8", 4, 2, 16, 64, 0)
     x, p, table = torch.zeros(2, 2, 64, device="cuda"), ints([0, 1]), ints([[0, 1], [2, 3]])
     freq = torch.ones(32, dtype=torch.float64, device="cuda")
