@@ -272,25 +272,36 @@ __device__ __forceinline__ void request_part(const Source& r, const KvPages& c, 
   }
 }
 
-// Joins `parts` partials: the values are at `value` and every `apart` bytes on, the
-// references and sums (side by side) at `scale` and every `scales_apart`.
+// Joins `parts` partials, at most MOST: the values are at `value` and every `apart`
+// bytes on, the references and sums (side by side) at `scale` and every `scales_apart`.
+// Unrolled, so that all of them are on their way together.
 struct Joined {
   float value, m, sum;
 };
+template <int MOST>
 __device__ __forceinline__ Joined join(uint32_t value, uint32_t apart, uint32_t scale, uint32_t scales_apart, int parts) {
   Joined j = {0.0f, kUnset, 0.0f};
-  for (int i = 0; i < parts; ++i) j.m = fmaxf(j.m, lds_float(scale + i * scales_apart));
-  for (int i = 0; i < parts; ++i) {
-    const float2 s = lds_float2(scale + i * scales_apart);
-    const float f = exp2_of(s.x - j.m);
-    j.sum = fmaf(s.y, f, j.sum);
-    j.value = fmaf(lds_float(value + i * apart), f, j.value);
+  float2 s[MOST];
+  float v[MOST];
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    s[i] = i < parts ? lds_float2(scale + i * scales_apart) : make_float2(kUnset, 0.0f);
+    v[i] = i < parts ? lds_float(value + i * apart) : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) j.m = fmaxf(j.m, s[i].x);
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    const float f = exp2_of(s[i].x - j.m);
+    j.sum = fmaf(s[i].y, f, j.sum);
+    j.value = fmaf(v[i], f, j.value);
   }
   return j;
 }
 
-// Where a CTA receives what its cluster's CTAs have for its share of a row's dims:
-// [CTA][share's dims] and [CTA][head][m, sum], behind the rings.
+// Where a CTA receives what its cluster's CTAs have for its share of a row's dims (dim
+// i of the row is CTA i % splits's): [CTA][share's dims] and [CTA][head][m, sum], behind
+// the rings.
 __host__ __device__ __forceinline__ int share_of(int heads, int D, int splits) { return (heads * D + splits - 1) / splits; }
 __host__ __device__ __forceinline__ int received_bytes(int heads, int D, int splits) {
   return splits > 1 ? splits * (share_of(heads, D, splits) + 1 + 2 * heads) * 4 : 0;
@@ -300,7 +311,9 @@ __host__ __device__ __forceinline__ int received_bytes(int heads, int D, int spl
 // proportion to their steps.
 struct Shares {
   int64_t b0;      // the launch's first sequence
-  int splits;
+  int group, groups, rows_a_seq;  // q heads a key head, groups of them, rows of a sequence
+  int splits;      // a power of two
+  int splits_log2;
   bool sorted;     // sequences in order of length, the longest first
   float* parts;    // splits == 0: [CTA][q heads of a row, at most 8][dims, m, sum]
   int2* rows;      // splits == 0: a row's first CTA and how many it has
@@ -405,7 +418,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_release_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
-  const int group = a.q_heads / c.heads, groups = (group + kRowHeads - 1) / kRowHeads, rows_a_seq = c.heads * groups;
+  const int group = sh.group, rows_a_seq = sh.rows_a_seq;
   const int D = c.head_dim;
   const int64_t most = a.max_pages << c.page_shift;
   const bool shared_out = sh.splits == 0;
@@ -432,10 +445,10 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     if (split == 0 && threadIdx.x == 0) sh.rows[b * rows_a_seq + row] = make_int2(blockIdx.x, splits);
   } else {
     splits = sh.splits;
-    split = blockIdx.x % splits;
-    const int64_t rest = blockIdx.x / splits;
-    row = (int)(rest % rows_a_seq);
-    b = sh.sorted ? by_length(a, (int)(rest / rows_a_seq)) : sh.b0 + rest / rows_a_seq;
+    split = blockIdx.x & (splits - 1);
+    const uint32_t rest = blockIdx.x >> sh.splits_log2, place = rest / (uint32_t)rows_a_seq;
+    row = (int)(rest - place * rows_a_seq);
+    b = sh.sorted ? by_length(a, (int)place) : sh.b0 + place;
   }
 
   // The warp's steps are every (splits * kWarps)-th one of the row's.
@@ -457,7 +470,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     t_ask += span.begin();
     look_up(t_ask);
   }
-  const int hk = row / groups, first_of_group = row % groups * kRowHeads;
+  const int hk = sh.groups == 1 ? row : row / sh.groups, first_of_group = (row - hk * sh.groups) * kRowHeads;
   const int heads = min(kRowHeads, group - first_of_group), hq = hk * group + first_of_group;
   Source r;
   const int64_t head_row = (int64_t)hk << c.page_shift;
@@ -750,15 +763,16 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
   auto of_warps = [&](int h, int d) {
     const uint32_t p = base + h * S::kPartial;
-    return join(p + 4 * d, S::kWarpBytes, p + 4 * DT, S::kWarpBytes, kWarps);
+    return join<kWarps>(p + 4 * d, S::kWarpBytes, p + 4 * DT, S::kWarpBytes, kWarps);
   };
+  auto head_of = [&](int i) { return heads == 1 ? 0 : (int)((uint32_t)i / (uint32_t)D); };
   auto finish = [&](int h, int d, const Joined& j) {
     a.out[b * a.out_stride + (int64_t)(hq + h) * D + d] = j.sum > 0.0f ? j.value / j.sum : 0.0f;  // no token: zeros
   };
   if (splits == 1 || shared_out) {
     float* part = sh.parts + (int64_t)blockIdx.x * min(kRowHeads, group) * (D + 4);
     for (int i = threadIdx.x; i < heads * D; i += kThreads) {
-      const int h = i / D, d = i - h * D;
+      const int h = head_of(i), d = i - h * D;
       const Joined j = of_warps(h, d);
       if (splits == 1) {
         finish(h, d, j);
@@ -770,13 +784,13 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     return;
   }
   // Every CTA sends each of the cluster its share of the dims, then joins its own.
-  const int share = share_of(heads, D, splits);
+  const int share = (heads * D + splits - 1) >> sh.splits_log2;
   const uint32_t values = base + (uint32_t)S::kSmem, scales = values + (splits * share + 1) / 2 * 8;
   cluster_wait();  // all of the cluster's CTAs have begun
   for (int i = threadIdx.x; i < heads * D; i += kThreads) {
-    const int h = i / D, d = i - h * D;
+    const int h = head_of(i), d = i - h * D;
     const Joined j = of_warps(h, d);
-    sts_cluster(values + (split * share + i % share) * 4, i / share, j.value);
+    sts_cluster(values + (split * share + (i >> sh.splits_log2)) * 4, i & (splits - 1), j.value);
     if (d < splits) {  // dim r's thread tells CTA r (16 dims at least, 8 CTAs at most)
       sts_cluster(scales + (split * heads + h) * 8, d, j.m);
       sts_cluster(scales + (split * heads + h) * 8 + 4, d, j.sum);
@@ -785,9 +799,11 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   __syncwarp();
   cluster_arrive();
   cluster_wait();
-  for (int i = threadIdx.x; i < share && split * share + i < heads * D; i += kThreads) {
-    const int h = (split * share + i) / D, d = split * share + i - h * D;
-    finish(h, d, join(values + 4 * i, 4 * share, scales + 8 * h, 8 * heads, splits));
+  for (int n = threadIdx.x; n < share; n += kThreads) {
+    const int i = n * splits + split;
+    if (i >= heads * D) break;
+    const int h = head_of(i);
+    finish(h, i - h * D, join<kMaxCluster>(values + 4 * n, 4 * share, scales + 8 * h, 8 * heads, splits));
   }
 }
 
@@ -897,10 +913,12 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
     ++cfg.numAttrs;
   };
   const int ctas = (dev.num_sms < kSms ? dev.num_sms : kSms) * S::kResident;
-  Shares sh = {0, splits_for(rows, steps, ctas), false, nullptr, nullptr};
+  const int group = a.q_heads / c.heads, groups = (group + kRowHeads - 1) / kRowHeads;
+  Shares sh = {0, group, groups, c.heads * groups, splits_for(rows, steps, ctas), 0, false, nullptr, nullptr};
+  while ((1 << sh.splits_log2) < sh.splits) ++sh.splits_log2;
   if (workspace && shares_fit(a.B, rows, ctas) && steps <= 0x7fffffff / rows &&
       share_out_wins(a.B, rows, tokens, sh.splits, ctas)) {
-    const int64_t heads = a.q_heads / c.heads < kRowHeads ? a.q_heads / c.heads : kRowHeads;
+    const int64_t heads = group < kRowHeads ? group : kRowHeads;
     sh.splits = 0;
     sh.parts = static_cast<float*>(workspace);
     sh.rows = reinterpret_cast<int2*>(sh.parts + (int64_t)kShareCtas * heads * (c.head_dim + 4));
@@ -916,7 +934,7 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
     return cudaLaunchKernelEx(&cfg, join_kernel<S::kTokens>, a, c, sh);
   }
   sh.sorted = a.B > 1 && a.B <= kSortSeqs && rows * sh.splits > ctas;
-  cfg.dynamicSmemBytes = S::kSmem + received_bytes(a.q_heads / c.heads < kRowHeads ? a.q_heads / c.heads : kRowHeads, c.head_dim, sh.splits);
+  cfg.dynamicSmemBytes = S::kSmem + received_bytes(group < kRowHeads ? group : kRowHeads, c.head_dim, sh.splits);
   const int64_t per_launch = (int64_t)0x7fffffff / (per_seq * sh.splits);  // sequences a grid holds
   for (; sh.b0 < a.B; sh.b0 += per_launch) {
     const int64_t n = a.B - sh.b0 < per_launch ? a.B - sh.b0 : per_launch;

@@ -88,12 +88,18 @@ __device__ __forceinline__ void sin_cos_turns(uint64_t phase, float* sine, float
   *sine = quarter >= 2 ? -y : y;
 }
 
-// cos and sin of every pair of one position, into the warp's shared memory.
+// cos and sin of every pair of one position, into the warp's shared memory; two pairs
+// a lane side by side, their chains of operations overlapping.
 __device__ __forceinline__ void fill_angles(const RopeArgs& r, int32_t pos, float2* cs) {
-  for (int i = threadIdx.x & 31; i < r.rot_dim / 2; i += 32) {
-    float s, c;
-    sin_cos_turns(turn_fraction(r.freq[i]) * (uint64_t)(int64_t)pos, &s, &c);
-    cs[i] = make_float2(__fmul_rn(c, r.amplitude), __fmul_rn(s, r.amplitude));
+  const int n = r.rot_dim / 2;
+  const uint64_t p = (uint64_t)(int64_t)pos;
+  for (int i = threadIdx.x & 31; i < n; i += 64) {
+    const double f0 = r.freq[i], f1 = r.freq[min(i + 32, n - 1)];
+    float s0, c0, s1, c1;
+    sin_cos_turns(turn_fraction(f0) * p, &s0, &c0);
+    sin_cos_turns(turn_fraction(f1) * p, &s1, &c1);
+    cs[i] = make_float2(__fmul_rn(c0, r.amplitude), __fmul_rn(s0, r.amplitude));
+    if (i + 32 < n) cs[i + 32] = make_float2(__fmul_rn(c1, r.amplitude), __fmul_rn(s1, r.amplitude));
   }
   __syncwarp();
 }
@@ -105,9 +111,10 @@ struct Task {
 };
 template <int ROWS>
 __device__ __forceinline__ Task task_of_warp(int64_t T, int units, int shares) {
-  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int share = (int)(w % shares), turns = (units + ROWS - 1) / ROWS;
-  Task t = {w / shares, turns * share / shares * ROWS, turns * (share + 1) / shares * ROWS};
+  const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);  // T <= 2^30, and more than one share only of few
+  const uint32_t token = shares == 1 ? w : w / (uint32_t)shares, share = w - token * shares;
+  const uint32_t turns = (units + ROWS - 1) / ROWS;
+  Task t = {token, (int)(turns * share / shares * ROWS), (int)(turns * (share + 1) / shares * ROWS)};
   t.end = t.token < T ? min(t.end, units) : t.first;
   return t;
 }
