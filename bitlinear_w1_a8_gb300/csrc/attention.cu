@@ -42,14 +42,15 @@
 //
 // What bounds it (GB300, DRAM copy peak 6.78 TB/s; a graph's replay, so with launches):
 // with the GPU full the cache's bytes and, for 8-bit codes, the instructions that widen
-// them (two thirds of a step's ~700 for 32 tokens of 80 dims): 304 sequences of 1024
-// tokens read 95 % (bf16, 128 dims), 84 % (e4m3, 128) and 80 % (int8, 80) of the peak.
-// 64 ragged sequences of up to 2048 tokens, 32 heads of 80, int8: 71 us, 72 %.
-// Few tokens are bound by latency: 2048 tokens of 32 heads 7.3 us, of which 3.9 without
-// any step (launch, lookups, joins), 2.6 the first and 0.9 the second step.
-// Tried and slower or no faster: three stages, 8 warps a CTA, clusters of 16, fewer CTAs
-// with more registers, one scratch logit a lane where a key head has one q head, pieces
-// of a single line through all rows (cut rows drain their pipelines twice).
+// them: 456 sequences of 1024 tokens, 8 key heads, are read at 99 % (bf16, 128 dims), 93 %
+// (e4m3, 128, 4 q heads a key head) and 87 % (int8, 80) of the peak.  64 ragged sequences
+// of up to 2048 tokens, 32 heads of 80, int8: 69 us, 74 %.  Few tokens are bound by
+// latency: 2048 tokens of 32 heads 6.5 us, of which 3.4 without any step (launch, lookups,
+// joins), about 2.3 the first and 0.8 the second step.
+// Tried and slower or no faster: five CTAs an SM at 96 registers (104 for 107 us with the
+// GPU full, but 60 for 55 in one wave), three stages, 8 warps a CTA, clusters of 16, one
+// logit a lane through shared memory where a key head has one q head, pieces of a single
+// line through all rows (cut rows drain their pipelines twice).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -64,6 +65,7 @@ constexpr int kRowHeads = 8;   // q heads of one CTA
 constexpr int kStages = 2;
 constexpr int kMaxCluster = 8;
 constexpr int kSms = 152;
+constexpr int kOtherSmem = 2048;  // of a CTA, beside the dynamic: static arrays and the system's 1 KB
 constexpr int kLeastSteps = 2;    // steps a warp at least: short rows take fewer CTAs
 constexpr int kShareSeqs = 1024;  // sequences that a CTA adds up to find its row
 constexpr int kSortSeqs = kThreads;  // sequences that a CTA ranks by length
@@ -80,7 +82,7 @@ struct Shape {
   // rows an odd number of 16-byte chunks apart: the fragments' loads (8 rows x 4
   // words, or 4 pairs of rows x 8 words) then touch every bank once
   static constexpr int kPitch = (kRow / 16) % 2 ? kRow : kRow + 16;
-  static constexpr int kTokens = kRow <= 96 || (kBytes == 2 && kRow <= 128) ? 32 : 16;
+  static constexpr int kTokens = kRow <= 80 ? 32 : 16;
   static constexpr int kTiles = kTokens / 8;       // n-tiles of the logits
   static constexpr int kSteps = DT / 16;           // k-steps of the logits
   static constexpr int kChunks = kRow / 16;
@@ -89,9 +91,10 @@ struct Shape {
   static constexpr int kWarpBytes = kStages * kStage;
   static constexpr int kPartial = (DT + 4) * 4;    // a head's weighted sum, m and sum, padded to 16 bytes
   static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes;
-  static constexpr int kCtas = DT <= (kBytes == 1 ? 128 : 96) ? 4 : DT <= 128 ? 3 : 2;  // CTAs an SM that the registers allow
-  static constexpr int kFit = (int)(227 * 1024 / (kSmem + 1024));   // and that its shared memory does
-  static constexpr int kResident = kCtas < kFit ? kCtas : kFit;
+  static constexpr int kCtas = kRow <= 192 ? 4 : kRow <= 256 && kBytes == 2 ? 3 : 2;  // CTAs an SM that the registers allow
+  // q's parts of a head: 4 lanes' 16 bytes a k-step (leading part and rest, two words each), and 8
+  // bytes of third parts for bf16
+  static constexpr int kHeadBytes = 4 * kSteps * (kBytes == 1 ? 16 : 24);
   static_assert(kRowHeads * kPartial <= kWarpBytes, "a warp's partials reuse its ring");
   static_assert(kStage % 16 == 0 && DT % 16 == 0, "");
 };
@@ -114,6 +117,11 @@ __device__ __forceinline__ void copies_wait() {
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
@@ -511,11 +519,13 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   for (int i = 0; i < kStages - 1; ++i) ask();
 
   // q as the MMA's A operand: rows g the leading parts of head g, rows g + 8 the
-  // next, the dims of a k-step in the order the key words give them.
+  // next, the dims of a k-step in the order the key words give them.  Kept in shared
+  // memory behind the rings and read again in every step: in registers it was 20 to 64
+  // of them a thread, a CTA less an SM, and spills.
   constexpr bool kBf16 = FORMAT == BITLINEAR_KV_BF16;
-  uint32_t qa[S::kSteps][4], qb[kBf16 ? S::kSteps : 1][2];
-  float row_scale = 1.0f;
-  {
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem), q_area = base + (uint32_t)S::kSmem;
+  const uint32_t thirds = q_area + S::kSteps * heads * 64, q_scales = q_area + heads * S::kHeadBytes;
+  if (warp == 0) {
     const float* q = a.q + b * a.q_stride + (int64_t)(hq + min(g, heads - 1)) * D;
     const float factor = a.scale * 1.44269504088896341f;
     float v[S::kSteps][4], top = 0.0f;
@@ -529,25 +539,36 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) top = fmaxf(top, fabsf(v[s][j]));
     }
+    float down = 1.0f, up = 1.0f;
     if constexpr (!kBf16) {
       top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
       top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
       const int e = clamp_exponent(exponent_of(top));
-      row_scale = power2(e);
-      const float down = power2(-e);
+      up = power2(e);
+      down = power2(-e);
+    }
+    if (g < heads) {
+      const uint32_t to = q_area + (g * 4 + qd) * 16, to_third = thirds + (g * 4 + qd) * 8;
 #pragma unroll
       for (int s = 0; s < S::kSteps; ++s) {
-        split2(v[s][0] * down, v[s][1] * down, qa[s][0], qa[s][1]);
-        split2(v[s][2] * down, v[s][3] * down, qa[s][2], qa[s][3]);
+        uint4 w;
+        if constexpr (!kBf16) {
+          split2(v[s][0] * down, v[s][1] * down, w.x, w.y);
+          split2(v[s][2] * down, v[s][3] * down, w.z, w.w);
+        } else {
+          uint2 third;
+          w.x = next_part(v[s][0], v[s][1]); w.y = next_part(v[s][0], v[s][1]); third.x = next_part(v[s][0], v[s][1]);
+          w.z = next_part(v[s][2], v[s][3]); w.w = next_part(v[s][2], v[s][3]); third.y = next_part(v[s][2], v[s][3]);
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to_third + s * (heads * 32)), "r"(third.x), "r"(third.y) : "memory");
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + s * (heads * 64)), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
       }
-    } else {
-#pragma unroll
-      for (int s = 0; s < S::kSteps; ++s) {
-        qa[s][0] = next_part(v[s][0], v[s][1]); qa[s][1] = next_part(v[s][0], v[s][1]); qb[s][0] = next_part(v[s][0], v[s][1]);
-        qa[s][2] = next_part(v[s][2], v[s][3]); qa[s][3] = next_part(v[s][2], v[s][3]); qb[s][1] = next_part(v[s][2], v[s][3]);
-      }
+      if (qd == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(q_scales + 4 * g), "f"(up) : "memory");
     }
   }
+  __syncthreads();
+  const uint32_t q_lane = min(g, heads - 1) * 4 + qd, q_stride = heads * 64;  // [k-step][head][lane]: no bank twice
+  const float row_scale = lds_float(q_scales + 4 * min(g, heads - 1));
 
   float ref = kUnset, sum = 0.0f;                      // of row g; the sum over this lane's tokens
   float out[S::kOutTiles][2];                          // row g: dims 2 qd, 2 qd + 1 of every n-tile (in the tiles' order)
@@ -564,7 +585,14 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
 
     float x[S::kTiles][4];
 #pragma unroll
-    for (int s = 0; s < S::kSteps; ++s)
+    for (int s = 0; s < S::kSteps; ++s) {
+      const uint4 w = lds128(q_area + q_lane * 16 + s * q_stride);
+      const uint32_t qa[4] = {w.x, w.y, w.z, w.w};
+      uint32_t third[4] = {0u, 0u, 0u, 0u};
+      if constexpr (kBf16) {
+        third[0] = lds32(thirds + q_lane * 8 + s * (q_stride / 2));
+        third[2] = lds32(thirds + q_lane * 8 + s * (q_stride / 2) + 4);
+      }
 #pragma unroll
       for (int j = 0; j < S::kTiles; ++j) {
         uint32_t k0, k1;
@@ -576,14 +604,12 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
           widen<FORMAT>(lds32(row), k0, k1);
         }
         if (s == 0)
-          mma<FORMAT, true>(x[j], qa[s], k0, k1);
+          mma<FORMAT, true>(x[j], qa, k0, k1);
         else
-          mma<FORMAT, false>(x[j], qa[s], k0, k1);
-        if constexpr (kBf16) {
-          const uint32_t third[4] = {qb[s][0], 0u, qb[s][1], 0u};
-          mma<FORMAT, false>(x[j], third, k0, k1);
-        }
+          mma<FORMAT, false>(x[j], qa, k0, k1);
+        if constexpr (kBf16) mma<FORMAT, false>(x[j], third, k0, k1);
       }
+    }
 
     // logits of row g (times 1 / row_scale), tokens 8 j + 2 qd and the next
     float2 lg[S::kTiles], p[S::kTiles], w[S::kTiles];
@@ -760,7 +786,6 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   }
   __syncthreads();
 
-  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
   auto of_warps = [&](int h, int d) {
     const uint32_t p = base + h * S::kPartial;
     return join<kWarps>(p + 4 * d, S::kWarpBytes, p + 4 * DT, S::kWarpBytes, kWarps);
@@ -785,7 +810,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   }
   // Every CTA sends each of the cluster its share of the dims, then joins its own.
   const int share = (heads * D + splits - 1) >> sh.splits_log2;
-  const uint32_t values = base + (uint32_t)S::kSmem, scales = values + (splits * share + 1) / 2 * 8;
+  const uint32_t values = q_scales + kRowHeads * 4, scales = values + (splits * share + 1) / 2 * 8;
   cluster_wait();  // all of the cluster's CTAs have begun
   for (int i = threadIdx.x; i < heads * D; i += kThreads) {
     const int h = head_of(i), d = i - h * D;
@@ -893,7 +918,8 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
   static thread_local int configured_device = -1;
   if (configured_device != dev.device) {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)S::kSmem + received_bytes(kRowHeads, DT, kMaxCluster));
+                                                 (int)S::kSmem + kRowHeads * (S::kHeadBytes + 4) +
+                                                     received_bytes(kRowHeads, DT, kMaxCluster));
     if (err != cudaSuccess) return err;
     configured_device = dev.device;
   }
@@ -901,27 +927,29 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
   int64_t tokens = a.max_pages << c.page_shift;
   if (a.window > 0 && a.window < tokens) tokens = a.window + S::kTokens;  // a window may begin inside a step
   const int64_t steps = (tokens + S::kTokens - 1) / S::kTokens;
+  const int group = a.q_heads / c.heads, groups = (group + kRowHeads - 1) / kRowHeads;
+  const int heads = group < kRowHeads ? group : kRowHeads;
+  const int smem = (int)S::kSmem + heads * S::kHeadBytes + kRowHeads * 4;  // the rings, q's parts and scales
+  const int fit = (int)(dev.smem_per_sm / (smem + received_bytes(heads, c.head_dim, kMaxCluster) + kOtherSmem));
+  const int ctas = (dev.num_sms < kSms ? dev.num_sms : kSms) * (fit < S::kCtas ? fit : S::kCtas);
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.dynamicSmemBytes = smem;
   auto programmatic = [&] {
     attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
     ++cfg.numAttrs;
   };
-  const int ctas = (dev.num_sms < kSms ? dev.num_sms : kSms) * S::kResident;
-  const int group = a.q_heads / c.heads, groups = (group + kRowHeads - 1) / kRowHeads;
   Shares sh = {0, group, groups, c.heads * groups, splits_for(rows, steps, ctas), 0, false, nullptr, nullptr};
   while ((1 << sh.splits_log2) < sh.splits) ++sh.splits_log2;
   if (workspace && shares_fit(a.B, rows, ctas) && steps <= 0x7fffffff / rows &&
       share_out_wins(a.B, rows, tokens, sh.splits, ctas)) {
-    const int64_t heads = group < kRowHeads ? group : kRowHeads;
     sh.splits = 0;
     sh.parts = static_cast<float*>(workspace);
-    sh.rows = reinterpret_cast<int2*>(sh.parts + (int64_t)kShareCtas * heads * (c.head_dim + 4));
+    sh.rows = reinterpret_cast<int2*>(sh.parts + (size_t)kShareCtas * heads * (c.head_dim + 4));
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
     if (pdl) programmatic();
     const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, c, sh);
@@ -934,7 +962,7 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
     return cudaLaunchKernelEx(&cfg, join_kernel<S::kTokens>, a, c, sh);
   }
   sh.sorted = a.B > 1 && a.B <= kSortSeqs && rows * sh.splits > ctas;
-  cfg.dynamicSmemBytes = S::kSmem + received_bytes(group < kRowHeads ? group : kRowHeads, c.head_dim, sh.splits);
+  cfg.dynamicSmemBytes = smem + received_bytes(heads, c.head_dim, sh.splits);
   const int64_t per_launch = (int64_t)0x7fffffff / (per_seq * sh.splits);  // sequences a grid holds
   for (; sh.b0 < a.B; sh.b0 += per_launch) {
     const int64_t n = a.B - sh.b0 < per_launch ? a.B - sh.b0 : per_launch;
