@@ -782,14 +782,13 @@ cudaError_t launch_mt(DecodeParams p, int grid_x, bool pdl, const DeviceInfo& de
   const size_t smem = wbytes + decode_front_bytes(p.K, p.XS, MT, p.rows_max, NORM);
   const size_t limit = dev.smem_optin - sizeof(RowQuantScratch) - 1024;
   if (smem > limit) return cudaErrorInvalidValue;
-  if (smem > 48 * 1024) {
-    static thread_local int configured_device = -1;
-    if (configured_device != dev.device) {
-      cudaError_t err =
-          cudaFuncSetAttribute(decode_kernel<MT, FUSED, NORM, NJ, MMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
-      if (err != cudaSuccess) return err;
-      configured_device = dev.device;
-    }
+  // Whatever the dynamic size: the 48 KB that need no attribute hold the static arrays too.
+  static thread_local int configured_device = -1;
+  if (configured_device != dev.device) {
+    cudaError_t err =
+        cudaFuncSetAttribute(decode_kernel<MT, FUSED, NORM, NJ, MMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
+    if (err != cudaSuccess) return err;
+    configured_device = dev.device;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(grid_x * ks), (unsigned)((p.M + MT - 1) / MT), 1);
