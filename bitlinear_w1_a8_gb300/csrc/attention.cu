@@ -832,57 +832,70 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   }
 }
 
-// Joins the parts of rows that several CTAs had: one CTA a (sequence, q head); groups
-// of threads, a thread a dim, take the parts in turn, and their sums meet in order.
+// Joins the parts of rows that several CTAs had: one CTA a (sequence, q head); teams of
+// D threads, a thread a dim, take the parts in turn, each against a maximum of its own,
+// and meet in order.  Two trips to memory: what the row has, and all of its parts.
 constexpr int kJoinThreads = 512;
 template <int T>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a, KvPages c, Shares sh) {
-  __shared__ float tops[kJoinThreads / 32];
-  __shared__ float values[kJoinThreads], sums[kJoinThreads];
+  __shared__ float values[kJoinThreads];
+  __shared__ float2 scales[kJoinThreads / 16];
   pdl_release_dependents();
   pdl_wait_primary();
-  const int group = a.q_heads / c.heads, groups = (group + kRowHeads - 1) / kRowHeads, D = c.head_dim;
-  const int64_t b = blockIdx.x / a.q_heads;
-  const int h = blockIdx.x % a.q_heads, in_group = h % group;
+  const int D = c.head_dim, team = threadIdx.x / D, teams = blockDim.x / D, d = threadIdx.x - team * D;
+  const uint32_t b = blockIdx.x / (uint32_t)a.q_heads;
+  const int h = blockIdx.x - b * a.q_heads, hk = h / sh.group, in_group = h - hk * sh.group;
+  const int32_t length = a.lengths[b];
+  const int2 row = sh.rows[(int64_t)b * sh.rows_a_seq + hk * sh.groups + in_group / kRowHeads];
   float* out = a.out + b * a.out_stride + (int64_t)h * D;
-  if (Span<T>(a.lengths[b], a.max_pages << c.page_shift, a.window).steps() == 0) {
-    if (threadIdx.x < D) out[threadIdx.x] = 0.0f;
-    return;
-  }
-  const int2 row = sh.rows[(b * c.heads + h / group) * groups + in_group / kRowHeads];
-  if (row.y == 1) return;  // one CTA had all of it and has written it
-  const int64_t apart = (int64_t)min(kRowHeads, group) * (D + 4);
+  const bool empty = Span<T>(length, a.max_pages << c.page_shift, a.window).steps() == 0;  // then no CTA had the row
+  if (empty && threadIdx.x < D) out[d] = 0.0f;
+  if (empty || row.y == 1) return;  // one CTA had all of it and has written it
+  const int64_t apart = (int64_t)min(kRowHeads, sh.group) * (D + 4);
   const float* p = sh.parts + row.x * apart + in_group % kRowHeads * (D + 4);
-  float m = kUnset;
-  for (int i = threadIdx.x; i < row.y; i += kJoinThreads) m = fmaxf(m, p[i * apart + D]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, tops[w]);
-  const int teams = kJoinThreads / D, team = threadIdx.x / D, d = threadIdx.x % D;
+  float m = kUnset, sum = 0.0f, value = 0.0f;
   if (team < teams) {
-    float sum = 0.0f, value = 0.0f;
-#pragma unroll 8
-    for (int i = team; i < row.y; i += teams) {
-      const float* q = p + i * apart;
-      const float f = exp2_of(q[D] - m);
-      sum = fmaf(q[D + 1], f, sum);
-      value = fmaf(q[d], f, value);
+    constexpr int kTogether = 8;
+    for (int i = team; i < row.y; i += kTogether * teams) {
+      float2 s[kTogether];
+      float v[kTogether], top = m;
+#pragma unroll
+      for (int n = 0; n < kTogether; ++n) {
+        const float* q = p + (i + n * teams) * apart;
+        const bool have = i + n * teams < row.y;
+        s[n] = have ? *reinterpret_cast<const float2*>(q + D) : make_float2(kUnset, 0.0f);
+        v[n] = have ? q[d] : 0.0f;
+      }
+#pragma unroll
+      for (int n = 0; n < kTogether; ++n) top = fmaxf(top, s[n].x);
+      const float down = exp2_of(m - top);
+      m = top;
+      sum *= down;
+      value *= down;
+#pragma unroll
+      for (int n = 0; n < kTogether; ++n) {
+        const float f = exp2_of(s[n].x - m);
+        sum = fmaf(s[n].y, f, sum);
+        value = fmaf(v[n], f, value);
+      }
     }
-    values[threadIdx.x] = value;
-    sums[threadIdx.x] = sum;
+    if (teams > 1) {
+      values[threadIdx.x] = value;
+      if (d == 0) scales[team] = make_float2(m, sum);
+    }
   }
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float sum = 0.0f, value = 0.0f;
+  if (teams > 1) {
+    __syncthreads();
+    if (threadIdx.x >= D) return;
+    for (int t = 0; t < teams; ++t) m = fmaxf(m, scales[t].x);
+    sum = value = 0.0f;
     for (int t = 0; t < teams; ++t) {
-      sum += sums[t * D + d];
-      value += values[t * D + d];
+      const float f = exp2_of(scales[t].x - m);
+      sum = fmaf(scales[t].y, f, sum);
+      value = fmaf(values[t * D + d], f, value);
     }
-    out[d] = sum > 0.0f ? value / sum : 0.0f;
   }
+  if (team == 0) out[d] = sum > 0.0f ? value / sum : 0.0f;
 }
 
 int64_t rows_of(int64_t B, int q_heads, int kv_heads) {
@@ -902,11 +915,13 @@ int splits_for(int64_t rows, int64_t steps, int ctas) {
   return s;
 }
 
-// Sharing out costs ~5 us more than clusters do (finding the row, the second
-// launch) and fills what they leave idle.
+// Sharing out costs ~4 us more than clusters do (finding the row, the second launch)
+// and fills what they leave idle.  Measured, clusters / shared out, us: one key head of
+// 65536 tokens 104 / 35; 8 sequences of 8 key heads, e4m3, up to 16384 tokens each 39.8 /
+// 33.9 ragged, up to 8192 23.1 / 22.7 ragged, 29.0 / 32.0 when all are that long.
 bool share_out_wins(int64_t B, int64_t rows, int64_t tokens, int splits, int ctas) {
   const int64_t a_warp = tokens / (splits * kWarps);
-  if (B > 1 && a_warp >= 1024) return true;  // lengths may differ: the longest row would end alone
+  if (B > 1 && a_warp >= 512) return true;  // lengths may differ: the longest row would end alone
   return a_warp * (ctas - rows * splits) >= (int64_t)192 * ctas;
 }
 
@@ -955,7 +970,9 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
     const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, c, sh);
     if (err != cudaSuccess) return err;
     cfg.gridDim = dim3((unsigned)(a.B * a.q_heads), 1, 1);
-    cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    // teams of D threads, 8 parts each at a time: as many as the parts of an average row want
+    const int64_t parts = (ctas / rows + 7) / 8, most = kJoinThreads / c.head_dim;
+    cfg.blockDim = dim3((unsigned)(c.head_dim * (parts < 1 ? 1 : parts < most ? parts : most)), 1, 1);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 0;
     programmatic();
