@@ -65,7 +65,7 @@ constexpr int kRowHeads = 8;   // q heads of one CTA
 constexpr int kStages = 2;
 constexpr int kMaxCluster = 8;
 constexpr int kSms = 152;
-constexpr int kOtherSmem = 2048;  // of a CTA, beside the dynamic: static arrays and the system's 1 KB
+constexpr int kOtherSmem = 1024 + 640;  // of a CTA, beside the dynamic: the system's and the static arrays
 constexpr int kLeastSteps = 2;    // steps a warp at least: short rows take fewer CTAs
 constexpr int kShareSeqs = 1024;  // sequences that a CTA adds up to find its row
 constexpr int kSortSeqs = kThreads;  // sequences that a CTA ranks by length
@@ -945,8 +945,12 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
   const int group = a.q_heads / c.heads, groups = (group + kRowHeads - 1) / kRowHeads;
   const int heads = group < kRowHeads ? group : kRowHeads;
   const int smem = (int)S::kSmem + heads * S::kHeadBytes + kRowHeads * 4;  // the rings, q's parts and scales
-  const int fit = (int)(dev.smem_per_sm / (smem + received_bytes(heads, c.head_dim, kMaxCluster) + kOtherSmem));
-  const int ctas = (dev.num_sms < kSms ? dev.num_sms : kSms) * (fit < S::kCtas ? fit : S::kCtas);
+  // CTAs resident at once, with so much shared memory more each
+  auto resident = [&](int more) {
+    const int fit = (int)(dev.smem_per_sm / (smem + more + kOtherSmem));
+    return (dev.num_sms < kSms ? dev.num_sms : kSms) * (fit < S::kCtas ? fit : S::kCtas);
+  };
+  const int ctas = resident(0), cluster_ctas = resident(received_bytes(heads, c.head_dim, kMaxCluster));
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
@@ -958,7 +962,7 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
     attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
     ++cfg.numAttrs;
   };
-  Shares sh = {0, group, groups, c.heads * groups, splits_for(rows, steps, ctas), 0, false, nullptr, nullptr};
+  Shares sh = {0, group, groups, c.heads * groups, splits_for(rows, steps, cluster_ctas), 0, false, nullptr, nullptr};
   while ((1 << sh.splits_log2) < sh.splits) ++sh.splits_log2;
   if (workspace && shares_fit(a.B, rows, ctas) && steps <= 0x7fffffff / rows &&
       share_out_wins(a.B, rows, tokens, sh.splits, ctas)) {
@@ -1005,6 +1009,7 @@ cudaError_t launch_format(const AttendArgs& a, const KvPages& c, void* workspace
   if (c.head_dim <= 64) return launch_shape<FORMAT, 64>(a, c, workspace, pdl, dev, s);
   if (c.head_dim <= 80) return launch_shape<FORMAT, 80>(a, c, workspace, pdl, dev, s);
   if (c.head_dim <= 96) return launch_shape<FORMAT, 96>(a, c, workspace, pdl, dev, s);
+  if (c.head_dim <= 112) return launch_shape<FORMAT, 112>(a, c, workspace, pdl, dev, s);
   if (c.head_dim <= 128) return launch_shape<FORMAT, 128>(a, c, workspace, pdl, dev, s);
   return launch_shape<FORMAT, 256>(a, c, workspace, pdl, dev, s);
 }
