@@ -405,16 +405,24 @@ __device__ __forceinline__ Part find_part(const AttendArgs& a, int64_t most, int
   return p;
 }
 
-// The sequence that comes at place `at` when the longest is first.
+// The sequence that comes at place `at` when the longest is first (of equal ones, and
+// beyond 2^24 tokens, the one with the lowest number).  Every CTA of a full grid starts
+// with it, so a key holds length and number: one compare a pair of sequences.
 __device__ __forceinline__ int64_t by_length(const AttendArgs& a, int at) {
-  __shared__ int lengths[kSortSeqs];
+  __shared__ __align__(16) int keys[kSortSeqs];
   __shared__ int found;
-  const int B = (int)a.B, b = threadIdx.x, mine = b < B ? a.lengths[b] : 0;
-  if (b < B) lengths[b] = mine;
+  const int B = (int)a.B, b = threadIdx.x;
+  const int mine = b < B ? min(max(a.lengths[b], 0), 0xffffff) * kSortSeqs + (kSortSeqs - 1 - b) : -1;
+  keys[b] = mine;
   __syncthreads();
-  int rank = 0;
-  for (int i = 0; i < B; ++i) rank += lengths[i] > mine || (lengths[i] == mine && i < b);
-  if (b < B && rank == at) found = b;
+  if (b < B) {
+    int rank = 0;
+    for (int i = 0; i < B; i += 4) {
+      const int4 k = *reinterpret_cast<const int4*>(keys + i);
+      rank += (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine);
+    }
+    if (rank == at) found = b;
+  }
   __syncthreads();
   return found;
 }
