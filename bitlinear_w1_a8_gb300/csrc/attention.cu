@@ -163,6 +163,33 @@ __device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127)
 __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 __device__ __forceinline__ int clamp_exponent(int e) { return max(-100, min(100, e)); }
 
+// Two at a time: one instruction for both, each rounded as alone.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // c = a b (FIRST) or c += a b.
 template <int FORMAT, bool FIRST>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -199,7 +226,9 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) { 
 // x, y as leading parts and what they leave, the latter times 2^11 (fp16).
 __device__ __forceinline__ void split2(float x, float y, uint32_t& lead, uint32_t& rest) {
   const __half2 h = __floats2half2_rn(x, y);
-  const __half2 r = __floats2half2_rn((x - __low2float(h)) * 2048.0f, (y - __high2float(h)) * 2048.0f);
+  // exact, as (x - h) 2^11 is: h is x's leading part
+  const float2 d = fma2(__half22float2(h), both(-2048.0f), mul2(make_float2(x, y), both(2048.0f)));
+  const __half2 r = __floats2half2_rn(d.x, d.y);
   lead = *reinterpret_cast<const uint32_t*>(&h);
   rest = *reinterpret_cast<const uint32_t*>(&r);
 }
@@ -587,10 +616,11 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   const uint32_t q_lane = min(g, heads - 1) * 4 + qd, q_stride = heads * 64;  // [k-step][head][lane]: no bank twice
   const float row_scale = lds_float(q_scales + 4 * min(g, heads - 1));
 
-  float ref = kUnset, sum = 0.0f;                      // of row g; the sum over this lane's tokens
-  float out[S::kOutTiles][2];                          // row g: dims 2 qd, 2 qd + 1 of every n-tile (in the tiles' order)
+  float ref = kUnset;                                  // of row g
+  float2 sums = both(0.0f);                            // over this lane's tokens, the even and the odd ones
+  float2 out[S::kOutTiles];                            // row g: dims 2 qd, 2 qd + 1 of every n-tile (in the tiles' order)
 #pragma unroll
-  for (int n = 0; n < S::kOutTiles; ++n) out[n][0] = out[n][1] = 0.0f;
+  for (int n = 0; n < S::kOutTiles; ++n) out[n] = both(0.0f);
   constexpr float kRest = kBf16 ? 1.0f : 1.0f / 2048.0f;
 
   for (uint32_t st = ring; t0 < r.len; t0 += lap, st = st == ring + (kStages - 1) * S::kStage ? ring : st + S::kStage) {
@@ -632,12 +662,9 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     float2 lg[S::kTiles], p[S::kTiles], w[S::kTiles];
 #pragma unroll
     for (int j = 0; j < S::kTiles; ++j) {
-      lg[j].x = fmaf(x[j][2], kRest, x[j][0]);
-      lg[j].y = fmaf(x[j][3], kRest, x[j][1]);
+      lg[j] = fma2(make_float2(x[j][2], x[j][3]), both(kRest), make_float2(x[j][0], x[j][1]));
       if constexpr (!kBf16) {
-        const float2 step = lds_float2(kst + (8 * j + 2 * qd) * 4);
-        lg[j].x *= step.x;
-        lg[j].y *= step.y;
+        lg[j] = mul2(lg[j], lds_float2(kst + (8 * j + 2 * qd) * 4));
       }
     }
     const uint32_t ok = (oks >> (2 * (kStages - 1))) & 3u;
@@ -654,13 +681,12 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     auto weights = [&](float& high) {
 #pragma unroll
       for (int j = 0; j < S::kTiles; ++j) {
-        p[j].x = exp2_of(fmaf(lg[j].x, row_scale, -ref));
-        p[j].y = exp2_of(fmaf(lg[j].y, row_scale, -ref));
+        const float2 z = fma2(lg[j], both(row_scale), both(-ref));
+        p[j] = make_float2(exp2_of(z.x), exp2_of(z.y));
         w[j] = p[j];
         if constexpr (!kBf16) {
           const float2 step = lds_float2(kst + (S::kTokens + 8 * j + 2 * qd) * 4);
-          w[j].x *= fmaxf(step.x, kLeastStep);
-          w[j].y *= fmaxf(step.y, kLeastStep);
+          w[j] = mul2(w[j], make_float2(fmaxf(step.x, kLeastStep), fmaxf(step.y, kLeastStep)));
         }
         high = fmaxf(high, fmaxf(w[j].x, w[j].y));
       }
@@ -684,17 +710,16 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
       if (top > ref) {
         const float f = exp2_of(ref - top);  // 0 from the first reference
         ref = top;
-        sum *= f;
+        sums = mul2(sums, both(f));
 #pragma unroll
         for (int n = 0; n < S::kOutTiles; ++n) {
-          out[n][0] *= f;
-          out[n][1] *= f;
+          out[n] = mul2(out[n], both(f));
         }
       }
       weights(high);
     }
 #pragma unroll
-    for (int j = 0; j < S::kTiles; ++j) sum += p[j].x + p[j].y;
+    for (int j = 0; j < S::kTiles; ++j) sums = add2(sums, p[j]);
 
     // the weights as the A operand: token pairs of tiles 2 kk, 2 kk + 1
     uint32_t pa[S::kTokens / 16][4], pb[kBf16 ? S::kTokens / 16 : 1][2];
@@ -718,8 +743,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     constexpr int kWide = kBf16 ? 2 : 4;             // dims a word
     constexpr int kGroups = DT / (8 * kWide);
     auto add = [&](int n, const float (&t)[4]) {
-      out[n][0] += fmaf(t[2], kRest, t[0]);
-      out[n][1] += fmaf(t[3], kRest, t[1]);
+      out[n] = add2(out[n], fma2(make_float2(t[2], t[3]), both(kRest), make_float2(t[0], t[1])));
     };
 #pragma unroll
     for (int dg = 0; dg < kGroups; ++dg) {
@@ -785,6 +809,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   __syncwarp();
 
   // The warp's partials over its ring: [head][dims, m, sum].
+  float sum = sums.x + sums.y;
   sum += __shfl_xor_sync(kFullMask, sum, 1);
   sum += __shfl_xor_sync(kFullMask, sum, 2);
   float* part = reinterpret_cast<float*>(smem + warp * S::kWarpBytes + g * S::kPartial);
@@ -794,8 +819,8 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     const bool tail = !kBf16 && DT % 32 == 16 && n >= S::kOutTiles - 2;
     const int wide = tail ? 2 : kWideOut, first = tail ? DT - 16 : n / kWideOut * 8 * kWideOut;
     const int of = tail ? n - (S::kOutTiles - 2) : n % kWideOut;
-    part[first + wide * (2 * qd) + of] = out[n][0];
-    part[first + wide * (2 * qd + 1) + of] = out[n][1];
+    part[first + wide * (2 * qd) + of] = out[n].x;
+    part[first + wide * (2 * qd + 1) + of] = out[n].y;
   }
   if (qd == 0) {
     part[DT] = ref;
