@@ -42,15 +42,16 @@
 //
 // What bounds it (GB300, DRAM copy peak 6.78 TB/s; a graph's replay, so with launches):
 // with the GPU full the cache's bytes and, for 8-bit codes, the instructions that widen
-// them: 456 sequences of 1024 tokens, 8 key heads, are read at 99 % (bf16, 128 dims), 93 %
-// (e4m3, 128, 4 q heads a key head) and 87 % (int8, 80) of the peak.  64 ragged sequences
-// of up to 2048 tokens, 32 heads of 80, int8: 69 us, 74 %.  Few tokens are bound by
-// latency: 2048 tokens of 32 heads 6.5 us, of which 3.4 without any step (launch, lookups,
+// them: 456 sequences of 1024 tokens, 8 key heads, are read at 100 % (bf16, 128 dims), 90 %
+// (e4m3, 128, 4 q heads a key head) and 91 % (int8, 80) of the peak.  64 ragged sequences
+// of up to 2048 tokens, 32 heads of 80, int8: 64.2 us, 79 %.  Few tokens are bound by
+// latency: 2048 tokens of 32 heads 6.4 us, of which 3.3 without any step (launch, lookups,
 // joins), about 2.3 the first and 0.8 the second step.
 // Tried and slower or no faster: five CTAs an SM at 96 registers (104 for 107 us with the
 // GPU full, but 60 for 55 in one wave), three stages, 8 warps a CTA, clusters of 16, one
 // logit a lane through shared memory where a key head has one q head, pieces of a single
-// line through all rows (cut rows drain their pipelines twice).
+// line through all rows (cut rows drain their pipelines twice), keys and values requested
+// apart (a step and a half on their way, 75.5 for 67.8 us on the ragged batch).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -626,8 +627,8 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   for (uint32_t st = ring; t0 < r.len; t0 += lap, st = st == ring + (kStages - 1) * S::kStage ? ring : st + S::kStage) {
     // The next step is asked for once this one has come, into the stage that the last one
     // has left: one meeting of the warp a step.  Asked for before the wait (a second
-    // meeting): 51.7 for 47.6 us on 64 x 2048 tokens of 8 key heads e4m3, 47.6 for 45.9 on
-    // 32 x 2048 bf16, 59.3 for 61.0 on 32 x 2048 of 32 heads of 80 int8; the others equal.
+    // meeting): 51.2 for 47.4 us on 64 x 2048 tokens of 8 key heads e4m3, 47.6 for 45.8 on
+    // 32 x 2048 bf16; with the GPU full several times 159.0 for 161.0 (456 x 1024, e4m3).
     copies_wait<0>();
     __syncwarp();
     ask();
