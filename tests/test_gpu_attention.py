@@ -80,6 +80,26 @@ def test_rope_in_place_strided_and_back():
     within(x, back, again + carried)
 
 
+@pytest.mark.parametrize("T,H,D,rot,layout", [(12001, 9, 80, 80, "half"), (10007, 33, 32, 16, "interleaved"), (11003, 5, 64, 20, "half")])
+def test_rope_of_many_tokens(T, H, D, rot, layout):
+    """Warps in several rounds, whose rows are asked for early: in place, rows apart, the last row at the end of its memory."""
+    wide = normal((T * (H * D + 4) - 4,), T).cuda()
+    x = wide.as_strided((T, H, D), (H * D + 4, D, 1))
+    before, keep = x.cpu().numpy(), wide.clone()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 7
+    freq = bl.bitlinear_rope_frequencies(rot)
+    y = torch.empty(T, H, D, device="cuda")
+    bl.bitlinear_rope(x, pos, (freq.cuda(), LAYOUTS[layout]), y)
+    want, bound = plain.rotate(before, pos.cpu().numpy(), freq.numpy(), LAYOUTS[layout])
+    within(y, want, bound)
+    assert torch.equal(wide, keep)
+    bl.bitlinear_rope(x, pos, (freq.cuda(), LAYOUTS[layout]), x)
+    assert torch.equal(x, y)
+    between = torch.ones_like(wide, dtype=torch.bool)
+    between.as_strided((T, H, D), (H * D + 4, D, 1)).fill_(False)
+    assert torch.equal(wide[between], keep[between])
+
+
 def test_rope_is_the_gradient_of_itself():
     """d/dx of sum(g * rope(x, p)) is rope(g, -p): against differences of the 64-bit form."""
     T, H, D = 2, 1, 8
@@ -384,6 +404,27 @@ def test_attention_strides_and_one_page_list_for_all_rows():
     want, bound = plain.attend(q.cpu().numpy(), cache, table.expand(rows, 5).cpu().numpy(), lengths, page, D ** -0.5)
     within(out, want, bound)
     assert (out_wide[:, :4] == 2.5).all() and (out_wide[:, 4 + H * D:] == 2.5).all()
+
+
+@pytest.mark.parametrize("fmt", plain.FORMATS)
+@pytest.mark.parametrize("B,H", [(77, 8), (127, 5), (128, 8), (129, 8)])
+def test_attention_of_batches_that_start_with_the_longest(fmt, B, H):
+    """More rows than fit at once, of equal, empty, negative and far too large lengths."""
+    D, page, cols = 64, 16, 9
+    n = cols * page
+    cache = plain.make_cache(fmt, cols, H, page, D, B)
+    table = ints([[3, 1, 8, 0, 2, 7, 5, 4, 6]])
+    t = torch.arange(n, device="cuda")
+    plain.fill_row(cache, fmt, table[0].long()[t // page], t % page, normal((n, H, D), 1).cuda(), normal((n, H, D), 2).cuda())
+    rng = np.random.default_rng(B)
+    lengths = rng.integers(0, n + 1, B)
+    lengths[rng.permutation(B)[:40]] = [0, 2 ** 31 - 1, -5, n, 1 << 24, (1 << 24) + 1, -2 ** 31, 1] * 5
+    q, (out, full) = normal((B, H, D), 3).cuda(), guarded(B * H * D, torch.float32, -7.0)
+    out = out.view(B, H, D)
+    bl.bitlinear_attention(q, cache, table.expand(B, cols), ints(lengths.tolist()), out)
+    want, bound = plain.attend(q.cpu().numpy(), cache, table.expand(B, cols).cpu().numpy(), lengths, page, D ** -0.5)
+    within(out, want, bound)
+    check_canary(full, -7.0)
 
 
 def test_cache_past_32_bit_offsets():
