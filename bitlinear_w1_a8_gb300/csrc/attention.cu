@@ -80,9 +80,16 @@ template <int FORMAT, int DT>
 struct Shape {
   static constexpr int kBytes = FORMAT == BITLINEAR_KV_BF16 ? 2 : 1;
   static constexpr int kRow = DT * kBytes;
-  // rows an odd number of 16-byte chunks apart: the fragments' loads (8 rows x 4
-  // words, or 4 pairs of rows x 8 words) then touch every bank once
-  static constexpr int kPitch = (kRow / 16) % 2 ? kRow : kRow + 16;
+  // The fragments' loads (8 rows x 4 words, or 4 pairs of rows x 8 words) touch every bank
+  // once when rows lie an odd number of 16-byte chunks apart, or, rows of whole 128 bytes,
+  // when chunk c of row n is at c ^ (n % 8).  The latter and rows that are odd by themselves
+  // keep both halves of a 32-byte sector in one such block, and a copy is one write; a pad
+  // of 16 bytes splits half of them.
+  static constexpr bool kTurned = kRow % 128 == 0;
+  static constexpr int kPitch = (kRow / 16) % 2 || kTurned ? kRow : kRow + 16;
+  static __device__ __forceinline__ uint32_t place(int n, int chunk) {
+    return n * kPitch + (kTurned ? chunk ^ (n & 7) : chunk) * 16;
+  }
   static constexpr int kTokens = kRow <= 80 ? 32 : 16;
   static constexpr int kTiles = kTokens / 8;       // n-tiles of the logits
   static constexpr int kSteps = DT / 16;           // k-steps of the logits
@@ -253,7 +260,7 @@ template <int FORMAT, int DT>
 __device__ __forceinline__ void request_whole(const Source& r, const int64_t (&row)[2], uint32_t stage, int lane) {
   using S = Shape<FORMAT, DT>;
   constexpr int kTurns = 16 * S::kChunks / 32;  // whole turns of the warp over a half's chunks
-  auto place = [](int i) { return (uint32_t)(i / S::kChunks * S::kPitch + i % S::kChunks * 16); };
+  auto place = [](int i) { return S::place(i / S::kChunks, i % S::kChunks); };
 #pragma unroll
   for (int s = 0; s < S::kTokens / 16; ++s) {
     const uint8_t* k = r.k + row[s] * S::kRow;
@@ -298,8 +305,8 @@ __device__ __forceinline__ void request_part(const Source& r, const KvPages& c, 
       if (ch >= chunks) continue;
       const bool there = have && t + n >= r.first && t + n < r.len;
       const int off = there ? n * row_bytes + 16 * ch : 0;
-      copy16(kd + n * S::kPitch + 16 * ch, k + off, there);
-      copy16(vd + n * S::kPitch + 16 * ch, v + off, there);
+      copy16(kd + S::place(n, ch), k + off, there);
+      copy16(vd + S::place(n, ch), v + off, there);
     }
     if constexpr (FORMAT != BITLINEAR_KV_BF16) {
       const int n = lane & 15;
@@ -461,7 +468,7 @@ template <int FORMAT, int DT>
 __global__ void __launch_bounds__(kThreads, Shape<FORMAT, DT>::kCtas)
 attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   using S = Shape<FORMAT, DT>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   pdl_release_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
   const int group = sh.group, rows_a_seq = sh.rows_a_seq;
@@ -634,6 +641,11 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     ask();
     const uint32_t vst = st + S::kTokens * S::kPitch, kst = vst + S::kTokens * S::kPitch;
 
+    // where this lane's words are: keys of row g, chunk 0; values of row 2 qd, chunk g / 4
+    const uint32_t key_at = st + S::place(g, 0) + 4 * qd, value_at = vst + S::place(2 * qd, g >> 2) + 4 * (g & 3);
+    auto in_row = [](uint32_t at, int chunk) {  // the same place of a row, `chunk` (a constant) chunks on
+      return S::kTurned ? (at ^ ((chunk & 7) * 16)) + (chunk & ~7) * 16 : at + chunk * 16;
+    };
     float x[S::kTiles][4];
 #pragma unroll
     for (int s = 0; s < S::kSteps; ++s) {
@@ -647,12 +659,12 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
 #pragma unroll
       for (int j = 0; j < S::kTiles; ++j) {
         uint32_t k0, k1;
-        const uint32_t row = st + (8 * j + g) * S::kPitch + 16 * s * S::kBytes + 4 * qd;
+        const uint32_t rows = 8 * j * S::kPitch;
         if constexpr (kBf16) {
-          k0 = lds32(row);
-          k1 = lds32(row + 16);
+          k0 = lds32(in_row(key_at, 2 * s) + rows);
+          k1 = lds32(in_row(key_at, 2 * s + 1) + rows);
         } else {
-          widen<FORMAT>(lds32(row), k0, k1);
+          widen<FORMAT>(lds32(in_row(key_at, s) + rows), k0, k1);
         }
         if (s == 0)
           mma<FORMAT, true>(x[j], qa, k0, k1);
@@ -754,8 +766,9 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
       float t[kWide][4];
 #pragma unroll
       for (int kk = 0; kk < S::kTokens / 16; ++kk) {
-        const uint32_t row = vst + (16 * kk + 2 * qd) * S::kPitch + 32 * dg + 4 * g;
-        uint32_t w[4] = {lds32(row), lds32(row + S::kPitch), lds32(row + 8 * S::kPitch), lds32(row + 9 * S::kPitch)};
+        const uint32_t even = in_row(value_at, 2 * dg) + 16 * kk * S::kPitch;  // row 2 qd; the next one's chunks are turned by one
+        const uint32_t odd = (S::kTurned ? in_row(value_at ^ 16, 2 * dg) : in_row(value_at, 2 * dg)) + (16 * kk + 1) * S::kPitch;
+        uint32_t w[4] = {lds32(even), lds32(odd), lds32(even + 8 * S::kPitch), lds32(odd + 8 * S::kPitch)};
         if constexpr (kBf16) {
           const uint32_t third[4] = {pb[kk][0], 0u, pb[kk][1], 0u};
 #pragma unroll
