@@ -352,16 +352,15 @@ __host__ __device__ __forceinline__ int received_bytes(int heads, int D, int spl
   return splits > 1 ? splits * (share_of(heads, D, splits) + 1 + 2 * heads) * 4 : 0;
 }
 
-// How rows are shared out: `splits` CTAs each (a cluster), or (splits == 0) in
-// proportion to their steps.
+// How rows are shared out.
 struct Shares {
   int64_t b0;      // the launch's first sequence
   int group, groups, rows_a_seq;  // q heads a key head, groups of them, rows of a sequence
-  int splits;      // a power of two
+  int splits;      // CTAs a row where each has as many: a power of two
   int splits_log2;
   bool sorted;     // sequences in order of length, the longest first
-  float* parts;    // splits == 0: [CTA][q heads of a row, at most 8][dims, m, sum]
-  int2* rows;      // splits == 0: a row's first CTA and how many it has
+  float* parts;    // rows shared out by their steps: [CTA][q heads of a row, at most 8][dims, m, sum]
+  int2* rows;      // and a row's first CTA and how many it has
 };
 
 // Tokens first <= t < len of a sequence that count, in steps of T from first / T on.
@@ -377,37 +376,18 @@ struct Span {
   __device__ __forceinline__ int steps() const { return len > first ? (int)((len + T - 1) / T - first / T) : 0; }
 };
 
-// Sums of a value over the block's threads: of those up to this one, and of all.
-__device__ __forceinline__ int2 block_sums(int mine, int* scratch) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int upto = mine, all = 0;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(kFullMask, upto, o);
-    if (lane >= o) upto += n;
-  }
-  if (lane == 31) scratch[warp] = upto;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) upto += scratch[w];
-    all += scratch[w];
-  }
-  __syncthreads();
-  return make_int2(upto, all);
-}
-
 // This CTA's row and which part of it.  Every row with any step has ceil(steps /
 // share) CTAs, in the order of the rows; share is the least for which the grid has
 // enough of them (each row rounds up by less than one).
+// Every warp finds it for itself, a lane for one sequence in 32: no barrier.
 struct Part {
   int64_t b;
   int row, part, parts;  // parts == 0: the CTA has nothing
 };
 template <int T>
 __device__ __forceinline__ Part find_part(const AttendArgs& a, int64_t most, int rows_a_seq) {
-  __shared__ int scratch[kWarps], found[3];
-  const int each = ((int)a.B + kThreads - 1) / kThreads, from = threadIdx.x * each, to = min((int)a.B, from + each);
+  const int lane = threadIdx.x & 31, here = blockIdx.x;
+  const int each = ((int)a.B + 31) / 32, from = min((int)a.B, lane * each), to = min((int)a.B, from + each);
   auto steps_of = [&](int b) { return Span<T>(a.lengths[b], most, a.window).steps(); };
   int steps = 0, some = 0;
   for (int b = from; b < to; ++b) {
@@ -415,36 +395,32 @@ __device__ __forceinline__ Part find_part(const AttendArgs& a, int64_t most, int
     steps += n;
     some += n > 0;
   }
-  const int total = block_sums(steps, scratch).y * rows_a_seq, rows = block_sums(some, scratch).y * rows_a_seq;
+  const int total = __reduce_add_sync(kFullMask, steps) * rows_a_seq, rows = __reduce_add_sync(kFullMask, some) * rows_a_seq;
   const int spare = (int)gridDim.x - rows;  // > 0: the host takes this path for rows well below the grid
   const int share = max((total + spare - 1) / spare, kLeastSteps * kWarps);
+  auto parts_of = [&](int b) { return (steps_of(b) + share - 1) / share; };
   int ctas = 0;
-  for (int b = from; b < to; ++b) ctas += (steps_of(b) + share - 1) / share * rows_a_seq;
-  if (threadIdx.x == 0) found[2] = 0;
-  const int upto = block_sums(ctas, scratch).x;
-  int at = upto - ctas;
-  for (int b = from; b < to; ++b) {
-    const int n = (steps_of(b) + share - 1) / share;
-    if ((int)blockIdx.x >= at && (int)blockIdx.x < at + n * rows_a_seq) {
-      found[0] = b;
-      found[1] = at;
-      found[2] = n;
-    }
-    at += n * rows_a_seq;
+  for (int b = from; b < to; ++b) ctas += parts_of(b) * rows_a_seq;
+  int upto = ctas;  // CTAs of this lane's sequences and all before
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(kFullMask, upto, o);
+    if (lane >= o) upto += n;
   }
-  __syncthreads();
-  Part p = {found[0], 0, 0, found[2]};
-  if (p.parts > 0) {
-    const int i = (int)blockIdx.x - found[1];
-    p.row = i / p.parts;
-    p.part = i - p.row * p.parts;
-  }
-  return p;
+  const uint32_t mine = __ballot_sync(kFullMask, here >= upto - ctas && here < upto);
+  if (mine == 0) return {0, 0, 0, 0};
+  int b = from, at = upto - ctas, n = 0;
+  if ((mine >> lane) & 1u)
+    for (; n = parts_of(b), here >= at + n * rows_a_seq; ++b) at += n * rows_a_seq;
+  const int owner = __ffs(mine) - 1;
+  n = __shfl_sync(kFullMask, n, owner);
+  const int i = here - __shfl_sync(kFullMask, at, owner), row = i / n;
+  return {__shfl_sync(kFullMask, b, owner), row, i - row * n, n};
 }
 
 // The sequence that comes at place `at` when the longest is first (of equal ones, and
-// beyond 2^24 tokens, the one with the lowest number).  Every CTA of a full grid starts
-// with it, so a key holds length and number: one compare a pair of sequences.
+// beyond 2^24 tokens, the one with the lowest number).  A key holds length and number:
+// one compare a pair of sequences.
 __device__ __forceinline__ int64_t by_length(const AttendArgs& a, int at) {
   __shared__ __align__(16) int keys[kSortSeqs];
   __shared__ int found;
@@ -464,7 +440,8 @@ __device__ __forceinline__ int64_t by_length(const AttendArgs& a, int at) {
   return found;
 }
 
-template <int FORMAT, int DT>
+// Rows of `splits` CTAs each, a cluster, or (SHARED_OUT) of CTAs in proportion to their steps.
+template <int FORMAT, int DT, bool SHARED_OUT>
 __global__ void __launch_bounds__(kThreads, Shape<FORMAT, DT>::kCtas)
 attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   using S = Shape<FORMAT, DT>;
@@ -474,21 +451,20 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   const int group = sh.group, rows_a_seq = sh.rows_a_seq;
   const int D = c.head_dim;
   const int64_t most = a.max_pages << c.page_shift;
-  const bool shared_out = sh.splits == 0;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * S::kWarpBytes;
   if (D < DT) {  // the padding of every row, once: copies never write it
     for (int i = lane; i < S::kWarpBytes / 16; i += 32)
       reinterpret_cast<uint4*>(smem + warp * S::kWarpBytes)[i] = make_uint4(0, 0, 0, 0);
     __syncwarp();
   }
-  if (sh.splits > 1) cluster_arrive();  // waited for before the first word goes to another CTA
+  if (!SHARED_OUT && sh.splits > 1) cluster_arrive();  // waited for before the first word goes to another CTA
   pdl_wait_primary();
 
   // The CTA's row (sequence b, head `row` of its key heads and groups of q heads)
   // and its place among the row's CTAs.
   int64_t b;
   int row, split, splits;
-  if (shared_out) {
+  if constexpr (SHARED_OUT) {
     const Part p = find_part<S::kTokens>(a, most, rows_a_seq);
     if (p.parts == 0) return;
     b = p.b;
@@ -853,8 +829,8 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   auto finish = [&](int h, int d, const Joined& j) {
     a.out[b * a.out_stride + (int64_t)(hq + h) * D + d] = j.sum > 0.0f ? j.value / j.sum : 0.0f;  // no token: zeros
   };
-  if (splits == 1 || shared_out) {
-    float* part = sh.parts + (int64_t)blockIdx.x * min(kRowHeads, group) * (D + 4);
+  if (SHARED_OUT || splits == 1) {
+    float* part = splits == 1 ? nullptr : sh.parts + (int64_t)blockIdx.x * min(kRowHeads, group) * (D + 4);
     for (int i = threadIdx.x; i < heads * D; i += kThreads) {
       const int h = head_of(i), d = i - h * D;
       const Joined j = of_warps(h, d);
@@ -988,13 +964,14 @@ template <int FORMAT, int DT>
 cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace, bool pdl, const DeviceInfo& dev,
                          cudaStream_t stream) {
   using S = Shape<FORMAT, DT>;
-  const auto kernel = attend_kernel<FORMAT, DT>;
+  const auto clusters = attend_kernel<FORMAT, DT, false>, shared_out = attend_kernel<FORMAT, DT, true>;
   static thread_local int configured_device = -1;
   if (configured_device != dev.device) {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)S::kSmem + kRowHeads * (S::kHeadBytes + 4) +
-                                                     received_bytes(kRowHeads, DT, kMaxCluster));
-    if (err != cudaSuccess) return err;
+    const int most = (int)S::kSmem + kRowHeads * (S::kHeadBytes + 4) + received_bytes(kRowHeads, DT, kMaxCluster);
+    for (const auto kernel : {clusters, shared_out}) {
+      const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+      if (err != cudaSuccess) return err;
+    }
     configured_device = dev.device;
   }
   const int64_t rows = rows_of(a.B, a.q_heads, c.heads), per_seq = rows / a.B;
@@ -1025,12 +1002,11 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
   while ((1 << sh.splits_log2) < sh.splits) ++sh.splits_log2;
   if (workspace && shares_fit(a.B, rows, ctas) && steps <= 0x7fffffff / rows &&
       share_out_wins(a.B, rows, tokens, sh.splits, ctas)) {
-    sh.splits = 0;
     sh.parts = static_cast<float*>(workspace);
     sh.rows = reinterpret_cast<int2*>(sh.parts + (size_t)kShareCtas * heads * (c.head_dim + 4));
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
     if (pdl) programmatic();
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, c, sh);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, shared_out, a, c, sh);
     if (err != cudaSuccess) return err;
     cfg.gridDim = dim3((unsigned)(a.B * a.q_heads), 1, 1);
     // teams of D threads, 8 parts each at a time: as many as the parts of an average row want
@@ -1041,7 +1017,11 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
     programmatic();
     return cudaLaunchKernelEx(&cfg, join_kernel<S::kTokens>, a, c, sh);
   }
-  sh.sorted = a.B > 1 && a.B <= kSortSeqs && rows * sh.splits > ctas;
+  // The longest sequences first, where rows come in more than one round and up to five: each
+  // CTA then ranks all sequences.  Measured in their own order / sorted, us: 64 sequences of
+  // up to 2048 tokens, 32 heads of 80, int8 (3.4 rounds) 69 / 63; 128 of 8 key heads e4m3 (1.7)
+  // 60 / 48.5; 128 of up to 1024, 32 heads (6.7) 73 / 80.
+  sh.sorted = a.B > 1 && a.B <= kSortSeqs && rows * sh.splits > ctas && rows <= 5 * (int64_t)ctas;
   cfg.dynamicSmemBytes = smem + received_bytes(heads, c.head_dim, sh.splits);
   const int64_t per_launch = (int64_t)0x7fffffff / (per_seq * sh.splits);  // sequences a grid holds
   for (; sh.b0 < a.B; sh.b0 += per_launch) {
@@ -1056,7 +1036,7 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
       ++cfg.numAttrs;
     }
     if (pdl) programmatic();
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, c, sh);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, clusters, a, c, sh);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
