@@ -48,7 +48,7 @@
 // latency: 2048 tokens of 32 heads 6.4 us, of which 3.3 without any step (launch, lookups,
 // joins), about 2.3 the first and 0.8 the second step.
 // Tried and slower or no faster: five CTAs an SM at 96 registers (104 for 107 us with the
-// GPU full, but 60 for 55 in one wave), three stages, 8 warps a CTA, clusters of 16, one
+// GPU full, but 60 for 55 in one wave), three and four stages, 8 warps a CTA, one
 // logit a lane through shared memory where a key head has one q head, pieces of a single
 // line through all rows (cut rows drain their pipelines twice), keys and values requested
 // apart (a step and a half on their way, 75.5 for 67.8 us on the ragged batch).
@@ -64,7 +64,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRowHeads = 8;   // q heads of one CTA
 constexpr int kStages = 2;     // the step in hand and the next
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;  // where the device schedules one; else kPortableCluster
+constexpr int kPortableCluster = 8;
 constexpr int kSms = 152;
 constexpr int kOtherSmem = 1024 + 640;  // of a CTA, beside the dynamic: the system's and the static arrays
 constexpr int kLeastSteps = 2;    // steps a warp at least: short rows take fewer CTAs
@@ -851,7 +852,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     const int h = head_of(i), d = i - h * D;
     const Joined j = of_warps(h, d);
     sts_cluster(values + (split * share + (i >> sh.splits_log2)) * 4, i & (splits - 1), j.value);
-    if (d < splits) {  // dim r's thread tells CTA r (16 dims at least, 8 CTAs at most)
+    if (d < splits) {  // dim r's thread tells CTA r (16 dims at least, 16 CTAs at most)
       sts_cluster(scales + (split * heads + h) * 8, d, j.m);
       sts_cluster(scales + (split * heads + h) * 8 + 4, d, j.sum);
     }
@@ -863,7 +864,9 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     const int i = n * splits + split;
     if (i >= heads * D) break;
     const int h = head_of(i);
-    finish(h, i - h * D, join<kMaxCluster>(values + 4 * n, 4 * share, scales + 8 * h, 8 * heads, splits));
+    const uint32_t value = values + 4 * n, scale = scales + 8 * h;
+    finish(h, i - h * D, splits > 8 ? join<16>(value, 4 * share, scale, 8 * heads, splits)
+                                    : join<8>(value, 4 * share, scale, 8 * heads, splits));
   }
 }
 
@@ -942,18 +945,22 @@ int64_t rows_of(int64_t B, int q_heads, int kv_heads) {
 constexpr int kShareCtas = 4 * kSms;
 bool shares_fit(int64_t B, int64_t rows, int ctas) { return B <= kShareSeqs && rows <= ctas / 3; }
 
-// CTAs of a cluster: a power of two up to kMaxCluster, while all CTAs are resident
-// at once and every warp may have a step.
-int splits_for(int64_t rows, int64_t steps, int ctas) {
+// CTAs of a cluster: a power of two up to `most`, while all CTAs are resident at once and
+// every warp may have a step, or two from 16 CTAs on.  (One sequence, 8 / 16 CTAs at most, us:
+// 8192 tokens of 32 heads of 80, int8 15.5 / 14.3; 4096 of 8 key heads bf16 10.1 / 8.9, of one
+// e4m3 8.9 / 7.1; a step a warp: 2048 of 32 heads 5.8 / 6.0, 1024 of one key head 5.7 / 5.5.)
+int splits_for(int64_t rows, int64_t steps, int ctas, int most) {
   int s = 1;
-  while (s < kMaxCluster && rows * s * 2 <= ctas && steps >= 2 * s * kWarps) s *= 2;
+  while (s < most && rows * s * 2 <= ctas && steps >= (s >= 8 ? 4 : 2) * s * kWarps) s *= 2;
   return s;
 }
 
-// Sharing out costs ~4 us more than clusters do (finding the row, the second launch)
-// and fills what they leave idle.  Measured, clusters / shared out, us: one key head of
-// 65536 tokens 104 / 35; 8 sequences of 8 key heads, e4m3, up to 16384 tokens each 39.8 /
-// 33.9 ragged, up to 8192 23.1 / 22.7 ragged, 29.0 / 32.0 when all are that long.
+// Sharing out costs ~3 us more than clusters do (finding the row, the second launch)
+// and fills what they leave idle.  Measured, clusters / shared out, us: one sequence of 8 key
+// heads bf16, 8192 tokens 12.9 / 14.9, 16384 20.9 / 20.6, 32768 36.5 / 29.9; of one key head
+// e4m3, 8192 9.2 / 10.4, 32768 21.8 / 16.0; of 32 heads of 80 int8, 16384 21.9 / 24.1; 4 ragged
+// ones of 8 key heads e4m3, up to 16384 18.1 / 19.4, up to 32768 29.5 / 26.4; 8 equal ones of
+// 8192 26.3 / 30.1.
 bool share_out_wins(int64_t B, int64_t rows, int64_t tokens, int splits, int ctas) {
   const int64_t a_warp = tokens / (splits * kWarps);
   if (B > 1 && a_warp >= 512) return true;  // lengths may differ: the longest row would end alone
@@ -965,13 +972,29 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
                          cudaStream_t stream) {
   using S = Shape<FORMAT, DT>;
   const auto clusters = attend_kernel<FORMAT, DT, false>, shared_out = attend_kernel<FORMAT, DT, true>;
-  static thread_local int configured_device = -1;
+  static thread_local int configured_device = -1, most_cluster;
   if (configured_device != dev.device) {
     const int most = (int)S::kSmem + kRowHeads * (S::kHeadBytes + 4) + received_bytes(kRowHeads, DT, kMaxCluster);
     for (const auto kernel : {clusters, shared_out}) {
       const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
       if (err != cudaSuccess) return err;
     }
+    most_cluster = kPortableCluster;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {kMaxCluster, 1, 1};
+    cfg.gridDim = dim3(kMaxCluster, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = most;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    if (cudaFuncSetAttribute(clusters, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&fit, clusters, &cfg) == cudaSuccess && fit > 0)
+      most_cluster = kMaxCluster;
+    else
+      cudaGetLastError();  // not this call's: the smaller size always runs
     configured_device = dev.device;
   }
   const int64_t rows = rows_of(a.B, a.q_heads, c.heads), per_seq = rows / a.B;
@@ -998,7 +1021,7 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
     attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
     ++cfg.numAttrs;
   };
-  Shares sh = {0, group, groups, c.heads * groups, splits_for(rows, steps, cluster_ctas), 0, false, nullptr, nullptr};
+  Shares sh = {0, group, groups, c.heads * groups, splits_for(rows, steps, cluster_ctas, most_cluster), 0, false, nullptr, nullptr};
   while ((1 << sh.splits_log2) < sh.splits) ++sh.splits_log2;
   if (workspace && shares_fit(a.B, rows, ctas) && steps <= 0x7fffffff / rows &&
       share_out_wins(a.B, rows, tokens, sh.splits, ctas)) {

@@ -329,6 +329,15 @@ def test_attention_long_and_ragged(fmt):
     attend_case(fmt, 4, 4, 64, 32, [1 + 37 * i % 900 for i in range(70)], seed=4)
 
 
+@pytest.mark.parametrize("fmt", plain.FORMATS)
+@pytest.mark.parametrize("Hq,Hk,D,page,lengths,window", [
+    (8, 1, 16, 16, [5000, 0, 3, 2049], 0), (1, 1, 256, 64, [2600], 0), (24, 3, 48, 32, [4000, 10], 0), (5, 5, 96, 16, [8000], 0),
+    (32, 32, 80, 64, [4100], 0), (16, 2, 112, 4096, [9000], 2500), (7, 1, 128, 16, [0], 0), (4, 2, 64, 64, [4096, 4097, 4095, 1], 4096)])
+def test_attention_one_cluster_a_row(fmt, Hq, Hk, D, page, lengths, window):
+    """Long sequences of few heads without a workspace: the largest clusters."""
+    attend_case(fmt, Hq, Hk, D, page, lengths, window=window, seed=Hq + D, columns=16384 // page)
+
+
 # A table wide enough that a call with a workspace cuts one line through all sequences and heads.
 WIDE = 1 << 16
 
