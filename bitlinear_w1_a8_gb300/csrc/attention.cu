@@ -95,7 +95,7 @@ struct Shape {
     const int slot = kTurn == 1 ? (n & ~7) | (n & 1) << 2 | (n & 6) >> 1 : kTurn == 2 ? (n & ~3) | (n & 1) << 1 | (n & 2) >> 1 : n;
     return slot * kRow + (kTurn ? chunk ^ ((slot & 7) >> (3 - kTurn)) : chunk) * 16;
   }
-  static constexpr int kTokens = kRow <= 80 ? 32 : 16;
+  static constexpr int kTokens = kRow <= 96 ? 32 : 16;
   static constexpr int kTiles = kTokens / 8;       // n-tiles of the logits
   static constexpr int kSteps = DT / 16;           // k-steps of the logits
   static constexpr int kChunks = kRow / 16;
