@@ -42,16 +42,19 @@
 //
 // What bounds it (GB300, DRAM copy peak 6.78 TB/s; a graph's replay, so with launches):
 // with the GPU full the cache's bytes and, for 8-bit codes, the instructions that widen
-// them: 456 sequences of 1024 tokens, 8 key heads, are read at 100 % (bf16, 128 dims), 90 %
-// (e4m3, 128, 4 q heads a key head) and 91 % (int8, 80) of the peak.  64 ragged sequences
-// of up to 2048 tokens, 32 heads of 80, int8: 64.2 us, 79 %.  Few tokens are bound by
-// latency: 2048 tokens of 32 heads 6.4 us, of which 3.3 without any step (launch, lookups,
-// joins), about 2.3 the first and 0.8 the second step.
+// them: 456 sequences of 1024 tokens, 8 key heads, are read at 100 % (bf16, 128 dims), 94 %
+// (e4m3, 128, 4 q heads a key head) and 92 % (int8, 80) of the peak.  64 ragged sequences
+// of up to 2048 tokens, 32 heads of 80, int8: 62.8 us, 81 %.  Few tokens are bound by
+// latency: 2048 tokens of 32 heads take 5.9 us, 1.6 us of it bytes (a launch, the lookups,
+// two steps of a warp one after the other, the joins).
 // Tried and slower or no faster: five CTAs an SM at 96 registers (104 for 107 us with the
-// GPU full, but 60 for 55 in one wave), three and four stages, 8 warps a CTA, one
-// logit a lane through shared memory where a key head has one q head, pieces of a single
-// line through all rows (cut rows drain their pipelines twice), keys and values requested
-// apart (a step and a half on their way, 75.5 for 67.8 us on the ragged batch).
+// GPU full, but 60 for 55 in one wave), three and four stages, two steps requested before the
+// first is used, 8 warps a CTA, one logit a lane through shared memory where a key head has
+// one q head, pieces of a single line through all rows (cut rows drain their pipelines
+// twice), keys and values requested apart (a step and a half on their way, 75.5 for 67.8 us
+// on the ragged batch), two CTAs a row where rows alone fill the GPU half to once (lengths
+// are known on the GPU alone: 24.0 for 30.3 us on 48 ragged sequences of 8 key heads, 31.6
+// for 26.6 on 12 equal ones of 32).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -84,7 +87,7 @@ struct Shape {
   // Where chunk c (16 bytes) of row n is, so that the fragments' loads (8 rows x 4 words for
   // keys, 4 even or 4 odd rows x 8 words for values) touch every bank once.  Rows of an odd
   // number of chunks do so as they are.  Else the last kTurn bits of the chunk are xor-ed
-  // with the last of the row's place among eight, and each eight rows are kept in the order
+  // with the first of the row's place among eight, and each eight rows are kept in the order
   // 0 2 4 6 1 3 5 7 (one bit), 0 2 1 3 4 6 5 7 (two) or as they come (three).  Both chunks of
   // a 32-byte sector stay in one such block, so that a copied sector is one write; a pad of
   // 16 bytes a row splits every other row's (95.3 for 85.3 us on one sequence of 131072
