@@ -38,7 +38,8 @@
 // heads) get CTAs in proportion to their steps instead, all of them resident at once,
 // so lengths of any mix end together; a row of several CTAs leaves their partials in
 // the workspace and a second small launch joins them in the order of the CTAs.
-// Without one, rows that fill the GPU more than once start with the longest.
+// Without one, rows that fill the GPU more than once (up to five times, of up to 128
+// sequences) start with the longest.
 //
 // What bounds it (GB300, DRAM copy peak 6.78 TB/s; a graph's replay, so with launches):
 // with the GPU full the cache's bytes and, for 8-bit codes, the instructions that widen
