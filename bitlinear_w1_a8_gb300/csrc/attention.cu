@@ -113,7 +113,7 @@ struct Shape {
   // bytes of third parts for bf16
   static constexpr int kHeadBytes = 4 * kSteps * (kBytes == 1 ? 16 : 24);
   static_assert(kRowHeads * kPartial <= kWarpBytes, "a warp's partials reuse its ring");
-  static_assert(kStage % 16 == 0 && DT % 16 == 0, "");
+  static_assert(kTokens * kRow % 128 == 0 && kStage % 128 == 0, "chunks are turned within 128 bytes");
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
