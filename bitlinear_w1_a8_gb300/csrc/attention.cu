@@ -60,6 +60,7 @@
 #include <cuda_fp16.h>
 
 #include "kv.cuh"
+#include "shares.h"
 
 namespace bitlinear {
 namespace {
@@ -406,7 +407,7 @@ __device__ __forceinline__ Part find_part(const AttendArgs& a, int64_t most, int
   }
   const int total = __reduce_add_sync(kFullMask, steps) * rows_a_seq, rows = __reduce_add_sync(kFullMask, some) * rows_a_seq;
   const int spare = (int)gridDim.x - rows;  // > 0: the host takes this path for rows well below the grid
-  const int share = max((total + spare - 1) / spare, kLeastSteps * kWarps);
+  const int share = share_of_steps(total, spare, kLeastSteps * kWarps);
   auto parts_of = [&](int b) { return (steps_of(b) + share - 1) / share; };
   int ctas = 0;
   for (int b = from; b < to; ++b) ctas += parts_of(b) * rows_a_seq;
@@ -1032,7 +1033,7 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace,
   };
   Shares sh = {0, group, groups, c.heads * groups, splits_for(rows, steps, cluster_ctas, most_cluster), 0, false, nullptr, nullptr};
   while ((1 << sh.splits_log2) < sh.splits) ++sh.splits_log2;
-  if (workspace && shares_fit(a.B, rows, ctas) && steps <= 0x7fffffff / rows &&
+  if (workspace && shares_fit(a.B, rows, ctas) && steps_fit(rows, steps) &&
       share_out_wins(a.B, rows, tokens, sh.splits, ctas)) {
     sh.parts = static_cast<float*>(workspace);
     sh.rows = reinterpret_cast<int2*>(sh.parts + (size_t)kShareCtas * heads * (c.head_dim + 4));
