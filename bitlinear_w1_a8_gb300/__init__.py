@@ -162,17 +162,22 @@ def load_library(path: str | None = None):
 
 
 def _load_marshal(lib):
+    """The module built from these sources for this Python and torch, if it is there."""
     global _marshal
-    at = os.path.join(_HERE, "_build", "bitlinear_marshal.so")
-    if torch is None or not os.path.exists(at):
-        return
     import importlib.machinery
     import importlib.util
+    from .build import marshal_path
+    try:
+        at = marshal_path()
+    except OSError:  # without its sources none can be told to belong to the library
+        return
+    if at is None or not os.path.exists(at):
+        return
     loader = importlib.machinery.ExtensionFileLoader("bitlinear_marshal", at)
     try:
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("bitlinear_marshal", loader))
         loader.exec_module(module)
-    except ImportError:  # built for another torch
+    except ImportError:
         return
     module.bind(*(ctypes.cast(getattr(lib, "bitlinear_" + name), ctypes.c_void_p).value
                   for name in ("rope", "kv_append", "kv_read", "attention")))

@@ -3,13 +3,16 @@
 Each .cu file is compiled by nvcc in parallel into bitlinear_w1_a8_gb300/_build/
 and linked into bitlinear_w1_a8_gb300/_build/libbitlinear.so.  Needs nvcc but
 no GPU (the container cross-compiles; the GPU host rebuilds for its own CPU).
-Beside it, _build/bitlinear_marshal.so (host code, g++ with the headers of Python
-and torch) reads the attention calls' tensors faster than the Python binding can;
-where it cannot be built the binding does all of it.
+Beside it, _build/bitlinear_marshal-<key>.so (host code, g++ with the headers of
+Python and torch) reads the attention calls' tensors faster than the Python binding
+can; where it cannot be built the binding does all of it.  The key stands for its
+source, the library's header and the Python and torch it was compiled against.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import glob
+import hashlib
 import os
 import shutil
 import subprocess
@@ -22,7 +25,6 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(BUILD, "libbitlinear.so")
-MARSHAL = os.path.join(BUILD, "bitlinear_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -67,20 +69,41 @@ def _marshal_command(out: str) -> list[str] | None:
             "-o", out, "-L", os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
-def _build_marshal(force: bool, verbose: bool) -> None:
-    if not (force or _stale(MARSHAL, [os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "bitlinear.h"), __file__])):
-        return
-    tmp = MARSHAL + f".{os.getpid()}.tmp"
+def marshal_path() -> str | None:
+    """Where the module is that belongs to the sources as they are and to this Python and torch; None
+    without torch.  It holds torch's and Python's layouts and the C ABI's, so no other may be loaded."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    key = hashlib.sha256()
+    for at in (os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "bitlinear.h")):
+        with open(at, "rb") as f:
+            key.update(hashlib.sha256(f.read()).digest())
+    key.update(repr((torch.__version__, torch.version.git_version, sysconfig.get_config_var("SOABI"))).encode())
+    return os.path.join(BUILD, f"bitlinear_marshal-{key.hexdigest()[:16]}.so")
+
+
+def _build_marshal(force: bool, verbose: bool) -> tuple[str, str] | None:
+    """Compiles the module unless it is there -> (the new file, its place), or None.  Those of other
+    sources or versions are removed first, whatever becomes of this one."""
+    at = marshal_path()
+    for old in glob.glob(os.path.join(glob.escape(BUILD), "bitlinear_marshal*.so")):
+        if force or old != at:
+            os.unlink(old)
+    if at is None or os.path.exists(at):
+        return None
+    tmp = at + f".{os.getpid()}.tmp"
     cmd = _marshal_command(tmp)
     if cmd is None:
-        return
+        return None
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        sys.stderr.write(f"{os.path.basename(MARSHAL)} not built, the Python binding does its work:\n{r.stderr[-2000:]}\n")
-        return
-    os.replace(tmp, MARSHAL)
+        sys.stderr.write(f"bitlinear_marshal not built, the Python binding does its work:\n{r.stderr[-2000:]}\n")
+        return None
+    return tmp, at
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
@@ -113,11 +136,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         for err in ex.map(run, jobs):
             if ptxas_verbose and err:
                 sys.stderr.write(err)
-        marshal.result()
+        built = marshal.result()
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         run([nvcc, *ARCH, "-shared", "-Xlinker", "--no-undefined", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if built:  # once the library that it calls is there
+        os.replace(*built)
     return LIB
 
 
