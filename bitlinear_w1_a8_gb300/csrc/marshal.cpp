@@ -153,6 +153,14 @@ PyObject* common_case(F f) {
   return PyLong_FromLong(status);
 }
 
+// Lets other Python threads run while the library enqueues (a launch waits where the queue is
+// full, and what it waits for may be a host callback that needs Python).  The caller's
+// references keep the tensors.
+struct Released {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Released() { PyEval_RestoreThread(state); }
+};
+
 // rope(x, positions, rope, y, flags, stream)
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return common_case([&](int* status) {
@@ -167,6 +175,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !stream_of(a[5], d, &stream))
       return false;
     const int64_t stride = x->size(1) * x->size(2);
+    Released released;
     *status = g_rope(at_of<float>(x), stride, x->size(0), (int)x->size(1), (int)x->size(2), at_of<int32_t>(p), &spec,
                      at_of<float>(y), stride, flags, stream);
     return true;
@@ -200,6 +209,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if ((a[8] != Py_None && !spec_of(a[8], d, &spec)) || !flags_of(a[9], &flags) || !stream_of(a[10], d, &stream))
       return false;
+    Released released;
     *status = g_append(at_of<float>(q), heads * pages.head_dim, (int)heads, at_of<float>(q_out), heads * pages.head_dim,
                        at_of<float>(k), stride, at_of<float>(v), stride, T, at.positions, at.seq, at.table, at.columns,
                        at.sequences, at.columns, a[8] == Py_None ? nullptr : &spec, &pages, flags, stream);
@@ -222,6 +232,7 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !places_of(a[1], a[2], a[5], k->size(0), d, &at) || !flags_of(a[6], &flags) || !stream_of(a[7], d, &stream))
       return false;
     const int64_t stride = k->size(1) * k->size(2);
+    Released released;
     *status = g_read(&pages, k->size(0), at.positions, at.seq, at.table, at.columns, at.sequences, at.columns,
                      at_of<float>(k), stride, at_of<float>(v), stride, flags, stream);
     return true;
@@ -248,6 +259,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return false;
     if (a[6] == Py_None) scale = std::pow((double)pages.head_dim, -0.5);
     const int64_t stride = q->size(1) * q->size(2);
+    Released released;
     *status = g_attention(at_of<float>(q), stride, q->size(0), (int)q->size(1), &pages, at_of<int32_t>(table),
                           table->size(1), table->size(1), at_of<int32_t>(lengths), window, (float)scale,
                           at_of<float>(out), stride, at_of(space), space ? (size_t)space->numel() : 0, flags, stream);
