@@ -11,11 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
-
-try:
-    import torch
-except ImportError:  # every call that takes tensors needs it
-    torch = None
+import sys
 
 __all__ = [
     "BitLinearError", "load_library", "library_path",
@@ -61,7 +57,9 @@ EXPORTED_SYMBOLS = (
 )
 
 _lib = None
+torch = None     # imported by the first attention call: the C ABI alone needs no torch
 _marshal = None  # the compiled common case of the attention calls (csrc/marshal.cpp), where it was built
+_ready = False   # both of them sought
 
 
 class BitLinearWeight(ctypes.Structure):
@@ -157,8 +155,18 @@ def load_library(path: str | None = None):
     lib.bitlinear_device_status.restype = st
     if path is None:
         _lib = lib
-        _load_marshal(lib)
+        if "torch" in sys.modules:
+            _get_ready()
     return lib
+
+
+def _get_ready():
+    """Imports torch and, once the library is there, the marshal."""
+    global torch, _ready
+    import torch
+    if _lib is not None and not _ready:
+        _ready = True
+        _load_marshal(_lib)
 
 
 def _load_marshal(lib):
@@ -554,6 +562,7 @@ def bitlinear_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int
     _check(load_library().bitlinear_rope_frequencies(
         int(rot_dim), float(base), int(scaling), float(factor), float(original_length), float(low), float(high),
         ctypes.addressof(out)), "bitlinear_rope_frequencies")
+    import torch
     return torch.tensor(list(out), dtype=torch.float64)
 
 
@@ -564,6 +573,8 @@ def bitlinear_rope(x, positions, rope, y, flags: int = 0, stream=None):
     (bitlinear_rope_frequencies) and layout ROPE_HALF or ROPE_INTERLEAVED.  y may be x.
     Rows may lie any multiple of 4 floats apart.
     """
+    if not _ready:
+        _get_ready()
     if _marshal is not None:
         status = _marshal.rope(x, positions, rope, y, flags, stream)
         if status is not None:
@@ -612,6 +623,8 @@ def bitlinear_kv_append(k, v, cache, positions, page_table, seq=None, q=None, q_
     positions, seq: int32 [T]; page_table: int32 [sequences, pages]; seq None: row i is of
     sequence i.  Rows with a negative position are padding.  rope: as for bitlinear_rope.
     """
+    if not _ready:
+        _get_ready()
     if _marshal is not None:
         status = _marshal.kv_append(k, v, cache, positions, page_table, seq, q, q_out, rope, flags, stream)
         if status is not None:
@@ -648,6 +661,8 @@ def bitlinear_kv_append(k, v, cache, positions, page_table, seq=None, q=None, q_
 
 def bitlinear_kv_read(cache, positions, page_table, k_out, v_out, seq=None, flags: int = 0, stream=None):
     """k_out, v_out [T, heads, head_dim] fp32 = the cached rows at (seq[i], positions[i])."""
+    if not _ready:
+        _get_ready()
     if _marshal is not None:
         status = _marshal.kv_read(cache, positions, page_table, k_out, v_out, seq, flags, stream)
         if status is not None:
@@ -676,6 +691,8 @@ def bitlinear_attention(q, cache, page_table, lengths, out, workspace=None, scal
     """out [B, q_heads, head_dim] = attention of q over the lengths[b] cached tokens of each
     sequence (the last `window` of them when it is not 0); scale None: 1 / sqrt(head_dim).
     cache and page_table: as for bitlinear_kv_append; lengths: int32 [B]."""
+    if not _ready:
+        _get_ready()
     if _marshal is not None:
         status = _marshal.attention(q, cache, page_table, lengths, out, workspace, scale, window, flags, stream)
         if status is not None:

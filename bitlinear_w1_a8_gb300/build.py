@@ -55,7 +55,7 @@ def _marshal_command(out: str) -> list[str] | None:
     """The compile command of marshal.cpp, or None without torch or the headers it takes."""
     try:
         import torch
-    except ImportError:
+    except Exception:  # missing, or broken: the library needs none
         return None
     at, python = os.path.dirname(torch.__file__), sysconfig.get_paths()["include"]
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
@@ -74,7 +74,7 @@ def marshal_path() -> str | None:
     without torch.  It holds torch's and Python's layouts and the C ABI's, so no other may be loaded."""
     try:
         import torch
-    except ImportError:
+    except Exception:  # missing, or broken: the library needs none
         return None
     key = hashlib.sha256()
     for at in (os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "bitlinear.h")):
@@ -88,10 +88,12 @@ def _build_marshal(force: bool, verbose: bool) -> tuple[str, str] | None:
     """Compiles the module unless it is there -> (the new file, its place), or None.  Those of other
     sources or versions are removed first, whatever becomes of this one."""
     at = marshal_path()
+    if at is None:
+        return None
     for old in glob.glob(os.path.join(glob.escape(BUILD), "bitlinear_marshal*.so")):
         if force or old != at:
             os.unlink(old)
-    if at is None or os.path.exists(at):
+    if os.path.exists(at):
         return None
     tmp = at + f".{os.getpid()}.tmp"
     cmd = _marshal_command(tmp)
