@@ -171,6 +171,11 @@ __device__ __forceinline__ float exp2_of(float x) {  // relative error 2^-22, 0 
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float at_least(float x, float least) {  // NaN stays NaN
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(least));
+  return y;
+}
 __device__ __forceinline__ float log2_of(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -325,6 +330,12 @@ __device__ __forceinline__ void request_part(const Source& r, const KvPages& c, 
             (lane < 16 ? r.ks : r.vs) + row[s] + (there ? n : 0), there);
     }
   }
+}
+
+// A row's output: zeros where no token counted (no reference, no sum).  Whatever else the
+// sum is, a NaN on the way here is one of the output too.
+__device__ __forceinline__ float output_of(float value, float m, float sum) {
+  return value / (m == kUnset && sum == 0.0f ? 1.0f : sum);
 }
 
 // Joins `parts` partials, at most MOST: the values are at `value` and every `apart`
@@ -689,7 +700,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
         w[j] = p[j];
         if constexpr (!kBf16) {
           const float2 step = lds_float2(kst + (S::kTokens + 8 * j + 2 * qd) * 4);
-          w[j] = mul2(w[j], make_float2(fmaxf(step.x, kLeastStep), fmaxf(step.y, kLeastStep)));
+          w[j] = mul2(w[j], make_float2(at_least(step.x, kLeastStep), at_least(step.y, kLeastStep)));
         }
         high = fmaxf(high, fmaxf(w[j].x, w[j].y));
       }
@@ -838,7 +849,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   };
   auto head_of = [&](int i) { return heads == 1 ? 0 : (int)((uint32_t)i / (uint32_t)D); };
   auto finish = [&](int h, int d, const Joined& j) {
-    a.out[b * a.out_stride + (int64_t)(hq + h) * D + d] = j.sum > 0.0f ? j.value / j.sum : 0.0f;  // no token: zeros
+    a.out[b * a.out_stride + (int64_t)(hq + h) * D + d] = output_of(j.value, j.m, j.sum);
   };
   if (SHARED_OUT || splits == 1) {
     float* part = splits == 1 ? nullptr : sh.parts + (int64_t)blockIdx.x * min(kRowHeads, group) * (D + 4);
@@ -943,7 +954,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a, KvPage
       value = fmaf(values[t * D + d], f, value);
     }
   }
-  if (team == 0) out[d] = sum > 0.0f ? value / sum : 0.0f;
+  if (team == 0) out[d] = output_of(value, m, sum);
 }
 
 int64_t rows_of(int64_t B, int q_heads, int kv_heads) {

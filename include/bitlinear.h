@@ -506,7 +506,8 @@ size_t bitlinear_attention_workspace(int64_t B, int num_q_heads, int num_kv_head
  *              bytes, contents irrelevant, not shared with a call that may run at the
  *              same time; or NULL: every sequence then has one thread-block cluster a
  *              key head, and very long sequences of few heads run slower.
- * Nothing past a row's length is read.  Results do not depend on timing: the parts of
+ * Nothing past a row's length is read.  A NaN in q, or in a key, value or step that
+ * counts, gives NaN in the heads that meet it.  Results do not depend on timing: the parts of
  * a split sequence are joined in a fixed order.
  * Several rows may attend to one sequence (rows of one page list with lengths n,
  * n + 1, ...: the causal rows of a prompt's end).
