@@ -23,7 +23,9 @@
 //   8-bit codes are exact in fp16; q and p are split into two fp16 parts (22 bits,
 //   the second scaled by 2^11), q after scaling each head's row by a power of two.
 //   bf16 values are used as they are; q and p are split into three bf16 parts (24
-//   bits), the third in a second MMA.
+//   bits), the third in a second MMA, of rows 8-15 too: the adder cuts a sum toward zero
+//   (-1.8 of 2^-24 of a logit of 80 dims; -3.5 with the third parts on the leading rows,
+//   and twice the error of an output).
 // So a logit and a weighted sum keep fp32 accuracy.  The key's step multiplies the
 // logit, the value's step multiplies p.
 //
@@ -651,8 +653,8 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
       const uint32_t qa[4] = {w.x, w.y, w.z, w.w};
       uint32_t third[4] = {0u, 0u, 0u, 0u};
       if constexpr (kBf16) {
-        third[0] = lds32(thirds + q_lane * 8 + s * (q_stride / 2));
-        third[2] = lds32(thirds + q_lane * 8 + s * (q_stride / 2) + 4);
+        third[1] = lds32(thirds + q_lane * 8 + s * (q_stride / 2));
+        third[3] = lds32(thirds + q_lane * 8 + s * (q_stride / 2) + 4);
       }
 #pragma unroll
       for (int j = 0; j < S::kTiles; ++j) {
@@ -768,7 +770,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
         const uint32_t odd = in_row(S::kTurn ? value_at ^ 16 : value_at, 2 * dg) + (16 * kk + S::kNext) * S::kRow;
         uint32_t w[4] = {lds32(even), lds32(odd), lds32(even + 8 * S::kRow), lds32(odd + 8 * S::kRow)};
         if constexpr (kBf16) {
-          const uint32_t third[4] = {pb[kk][0], 0u, pb[kk][1], 0u};
+          const uint32_t third[4] = {0u, pb[kk][0], 0u, pb[kk][1]};
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const uint32_t sel = n ? 0x7632 : 0x5410;
