@@ -24,7 +24,7 @@
 //   the second scaled by 2^11), q after scaling each head's row by a power of two.
 //   bf16 values are used as they are; q and p are split into three bf16 parts (24
 //   bits), the third in a second MMA, of rows 8-15 too: the adder cuts a sum toward zero
-//   (-1.8 of 2^-24 of a logit of 80 dims; -3.5 with the third parts on the leading rows,
+//   (-1.1 of 2^-24 of a logit of 80 dims; -3 with the third parts on the leading rows,
 //   and twice the error of an output).
 // So a logit and a weighted sum keep fp32 accuracy.  The key's step multiplies the
 // logit, the value's step multiplies p.
@@ -248,11 +248,14 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) { 
   }
 }
 
-// x, y as leading parts and what they leave, the latter times 2^11 (fp16).
-__device__ __forceinline__ void split2(float x, float y, uint32_t& lead, uint32_t& rest) {
+// x, y as leading parts and what they leave, the latter times 2^11 (fp16).  MORE: of x and y
+// (1 + more 2^-11) each.
+template <bool MORE = false>
+__device__ __forceinline__ void split2(float x, float y, uint32_t& lead, uint32_t& rest, float more = 0.0f) {
   const __half2 h = __floats2half2_rn(x, y);
   // exact, as (x - h) 2^11 is: h is x's leading part
-  const float2 d = fma2(__half22float2(h), both(-2048.0f), mul2(make_float2(x, y), both(2048.0f)));
+  float2 d = fma2(__half22float2(h), both(-2048.0f), mul2(make_float2(x, y), both(2048.0f)));
+  if constexpr (MORE) d = fma2(make_float2(x, y), both(more), d);
   const __half2 r = __floats2half2_rn(d.x, d.y);
   lead = *reinterpret_cast<const uint32_t*>(&h);
   rest = *reinterpret_cast<const uint32_t*>(&r);
@@ -584,7 +587,9 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem), q_area = base + (uint32_t)S::kSmem;
   const uint32_t thirds = q_area + S::kSteps * heads * 64, q_scales = q_area + heads * S::kHeadBytes;
   if (warp == 0) {
-    const float factor = a.scale * 1.44269504088896341f;
+    // scale log2(e) is a pair: its second part goes into q's last, so a row's logits have no
+    // rounding of it in common
+    const float factor = a.factor, more = a.factor_rest;
     float v[S::kSteps][4], top = 0.0f;
 #pragma unroll
     for (int s = 0; s < S::kSteps; ++s) {
@@ -606,12 +611,15 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
       for (int s = 0; s < S::kSteps; ++s) {
         uint4 w;
         if constexpr (!kBf16) {
-          split2(v[s][0] * down, v[s][1] * down, w.x, w.y);
-          split2(v[s][2] * down, v[s][3] * down, w.z, w.w);
+          split2<true>(v[s][0] * down, v[s][1] * down, w.x, w.y, more * 2048.0f);
+          split2<true>(v[s][2] * down, v[s][3] * down, w.z, w.w, more * 2048.0f);
         } else {
           uint2 third;
-          w.x = next_part(v[s][0], v[s][1]); w.y = next_part(v[s][0], v[s][1]); third.x = next_part(v[s][0], v[s][1]);
-          w.z = next_part(v[s][2], v[s][3]); w.w = next_part(v[s][2], v[s][3]); third.y = next_part(v[s][2], v[s][3]);
+          const float2 x = mul2(make_float2(v[s][0], v[s][1]), both(more)), y = mul2(make_float2(v[s][2], v[s][3]), both(more));
+          w.x = next_part(v[s][0], v[s][1]); w.y = next_part(v[s][0], v[s][1]);
+          w.z = next_part(v[s][2], v[s][3]); w.w = next_part(v[s][2], v[s][3]);
+          v[s][0] += x.x; v[s][1] += x.y; v[s][2] += y.x; v[s][3] += y.y;
+          third.x = next_part(v[s][0], v[s][1]); third.y = next_part(v[s][2], v[s][3]);
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to_third + s * (heads * 32)), "r"(third.x), "r"(third.y) : "memory");
         }
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + s * (heads * 64)), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
@@ -991,9 +999,12 @@ bool share_out_wins(int64_t B, int64_t rows, int64_t tokens, int splits, int cta
 }
 
 template <int FORMAT, int DT>
-cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, void* workspace, bool pdl, const DeviceInfo& dev,
+cudaError_t launch_shape(AttendArgs a, const KvPages& c, void* workspace, bool pdl, const DeviceInfo& dev,
                          cudaStream_t stream) {
   using S = Shape<FORMAT, DT>;
+  const double factor = (double)a.scale * 1.4426950408889634;  // to the base of the weights
+  a.factor = (float)factor;
+  a.factor_rest = (float)(a.factor != 0.0f ? factor / a.factor - 1.0 : 0.0);
   const auto clusters = attend_kernel<FORMAT, DT, false>, shared_out = attend_kernel<FORMAT, DT, true>;
   static thread_local int configured_device = -1, most_cluster;
   if (configured_device != dev.device) {

@@ -85,6 +85,7 @@ struct AttendArgs {
   float scale;
   int64_t B;
   int q_heads;
+  float factor, factor_rest;  // launch_attention's: scale log2(e) = factor (1 + factor_rest)
 };
 size_t attention_workspace_bytes(int64_t B, int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_attention(const AttendArgs& a, const KvPages& cache, void* workspace, bool pdl,

@@ -4,6 +4,8 @@ out: a stretch of the logits.
 Values that name their token (one 1, else 0) give the weights themselves; the slope of log(weight / exact weight)
 against the exact logit is the stretch.  Each weight is off by some U (half a step of fp32, 2^-24) besides, so over
 thousands of weights and a spread of several in the logits the slope is known to a hundredth of U."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -24,6 +26,14 @@ def cache_of(fmt, k, v, page):
     rows = lambda x: x.transpose(1, 2).reshape(pages * page, heads, D).cuda()  # noqa: E731
     plain.fill_row(cache, fmt, at // page, at % page, rows(k), rows(v))
     return cache, plain.held(cache, "k"), plain.held(cache, "v")
+
+
+def worst_scales(D):
+    """Two fp32 scales whose products with log2(e), in fp32, are off by the most up and down (relative)."""
+    s = np.float32(D ** -0.5) * np.float32(1 + 2.0 ** -10) ** np.arange(700, dtype=np.float32)
+    off = (s * np.float32(math.log2(math.e))).astype(np.float64) / (s.astype(np.float64) * math.log2(math.e)) - 1
+    lo, hi = int(off.argmin()), int(off.argmax())
+    return [(float(s[i]), off[i]) for i in (lo, hi)]
 
 
 class Weights:
@@ -55,6 +65,16 @@ class Weights:
         keep = p > p.max(-1, keepdims=True) * 2.0 ** -12   # below that an 8-bit cache's weight has fewer bits
         above = np.where(keep, x - (x * keep).sum(-1, keepdims=True) / keep.sum(-1, keepdims=True), 0.0)
         return (above * np.where(keep, off, 0.0)).sum() / (above * above).sum()
+
+
+@pytest.mark.parametrize("fmt", plain.FORMATS)
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_scale_is_not_rounded(fmt, D):
+    """What else stretches a logit does so at two near scales alike, so it falls out of the difference."""
+    w, (down, up) = Weights(fmt, D), worst_scales(D)
+    assert up[1] - down[1] > 1.5 * U   # what the difference would be
+    stretches = [w.stretch(scale) / U for scale, _ in (down, up)]
+    assert abs(stretches[1] - stretches[0]) <= 0.25, stretches
 
 
 @pytest.mark.parametrize("fmt", plain.FORMATS)
