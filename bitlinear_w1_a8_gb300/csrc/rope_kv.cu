@@ -4,11 +4,13 @@
 // Rotation ("Hesper.Models.BitNet" page, section "Configuration": ropeBase):
 // pair i of a head turns by the angle positions[t] * freq[i].  The angle is kept in
 // turns as a 64-bit fraction, positions times the frequency's fraction modulo 2^64, so
-// whole turns drop out exactly and a far position keeps its angle to 2^-53 of it.
+// whole turns drop out exactly.  It is off by what rounds the frequency's fraction (1.5 *
+// 2^-53 of it for 1 / (2 pi) and the product, and 2^-65 turns for the last place), times the
+// position, and by what the series drop of it (below 2^-48 turns).
 // What is left of the nearest quarter turn, |a| <= pi / 4, becomes a pair of fp32
 // (leading part and rest), its sine and cosine the Taylor series with the first three
-// terms in such pairs, rounded once to fp32: the nearest fp32 value but for one in
-// ~10^4.  (In fp64 the same took ~20 instructions a pair of a pipe that takes one in
+// terms in such pairs, rounded once to fp32: the nearest fp32 value to those of that angle
+// but for one in ~10^4.  (In fp64 the same took ~20 instructions a pair of a pipe that takes one in
 // ~14 cycles: 3 us of 11 for 2048 tokens of 32 heads.)  The
 // rotation itself is two fp32 products and one sum, unfused, so that it can be
 // repeated bit for bit.
@@ -130,7 +132,7 @@ __device__ __forceinline__ Task task_of_warp(int64_t T, int units, int shares) {
 template <int NP_, int L_, int DX>
 struct Head {
   static constexpr int NP = NP_, L = L_, kRows = 32 / L;
-  static constexpr int kCtas = NP == 1 ? 8 : NP == 2 ? 5 : 4;        // CTAs an SM, without spilled registers
+  static constexpr int kCtas = NP == 1 ? 8 : NP == 2 ? 5 : 4;        // CTAs an SM, without spilled registers up to 128 dims (4 bytes of 96)
   static constexpr int kReadCtas = NP == 1 ? 12 : NP <= 3 ? 8 : 6;  // the same of the reading kernel
   int D, j, a[NP], b[NP];  // first dims of the two chunks of each pair
   __device__ __forceinline__ Head(int dims, int together) : D(DX ? DX : dims), j((threadIdx.x & 31) % L) {

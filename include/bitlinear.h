@@ -398,7 +398,8 @@ enum {
 /* How a rotation is made: the first rot_dim dims of every head turn, the rest
  * stay.  Pair i = (a, b) at position p becomes
  *   (a * c - b * s, b * c + a * s),  c, s = amplitude * cos, sin(p * freq[i])
- * with the angle in fp64, its sine and cosine rounded once to fp32, and each
+ * with the angle off by at most 2^-52 of itself and |p| 2^-62 + 2^-45 radians, its
+ * sine and cosine rounded once to fp32 (the nearest but for one in ~10^4), and each
  * product and sum of the pair rounded in fp32. */
 typedef struct bitlinear_rope_spec {
   const double* freq; /* device fp64 [rot_dim / 2]: radians per position, 8-byte aligned */
