@@ -30,13 +30,16 @@
  *    multiple of 64, M * N >= 2^40 or N * K >= 2^40, a pointer not aligned to
  *    16 bytes, or a too small workspace.  M == 0 is a valid empty batch and enqueues nothing.
  *  - A failed launch returns BITLINEAR_ERR_CUDA.  Every wait inside a kernel
- *    is bounded; a wait that runs out records BITLINEAR_ERR_TIMEOUT in a
- *    per-device status word that bitlinear_device_status() reports, and that
- *    launch's outputs are unspecified.  While that word is set, a
+ *    on an mbarrier is bounded (barriers that every thread they count reaches,
+ *    and a thread's wait for its own copies, complete by themselves); a wait
+ *    that runs out records BITLINEAR_ERR_TIMEOUT in a per-device status word
+ *    that bitlinear_device_status() reports, and that launch's outputs are
+ *    unspecified.  While that word is set, a
  *    decode launch whose K is split over a thread-block cluster writes no
  *    outputs at all (its CTAs learn of a peer's timeout through the word), so
  *    clear it before relying on results again.
- *  - Non-finite inputs (Inf, NaN) give unspecified outputs.
+ *  - Non-finite inputs (Inf, NaN) give unspecified outputs, where an entry
+ *    point does not say which.
  *  - Rounding: every quantisation decision is taken in IEEE fp32 with
  *    round-to-nearest-even and no fused multiply-add; the sums that feed the
  *    scales (sum|W| and the RMSNorm sum of squares) are exact, then rounded
@@ -382,7 +385,8 @@ typedef struct bitlinear_kv_pages {
   void* k;           /* device, [num_pages, num_heads, page_size, head_dim] codes, 16-byte aligned */
   void* v;           /* the same for the values */
   float* k_step;     /* device fp32 [num_pages, num_heads, page_size], 16-byte aligned: a key is */
-  float* v_step;     /* code * step; ignored (may be NULL) for BITLINEAR_KV_BF16 */
+  float* v_step;     /* code * step, a step >= 0 (attention takes a value's step below 2^-80 as */
+                     /* that); ignored (may be NULL) for BITLINEAR_KV_BF16 */
   int64_t num_pages; /* 1 .. 2^31 - 1; fewer than 2^48 codes in all */
   int32_t num_heads; /* key / value heads, 1 .. 4096 */
   int32_t page_size; /* tokens a page: a power of two, 16 .. 4096 */
