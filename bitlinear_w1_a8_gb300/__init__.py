@@ -177,7 +177,7 @@ def _load_marshal(lib):
     from .build import marshal_path
     try:
         at = marshal_path()
-    except OSError:  # without its sources none can be told to belong to the library
+    except (OSError, AttributeError):  # without its sources, or with half a torch, none is known to belong
         return
     if at is None or not os.path.exists(at):
         return

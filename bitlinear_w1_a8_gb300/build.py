@@ -92,7 +92,10 @@ def _build_marshal(force: bool, verbose: bool) -> tuple[str, str] | None:
         return None
     for old in glob.glob(os.path.join(glob.escape(BUILD), "bitlinear_marshal*.so")):
         if force or old != at:
-            os.unlink(old)
+            try:
+                os.unlink(old)
+            except FileNotFoundError:  # another build was faster
+                pass
     if os.path.exists(at):
         return None
     tmp = at + f".{os.getpid()}.tmp"

@@ -55,3 +55,15 @@ def test_a_build_that_fails_leaves_none_behind(monkeypatch, tmp_path, command):
     monkeypatch.setattr(blbuild, "_marshal_command", lambda out: command)
     assert blbuild._build_marshal(False, False) is None
     assert list(tmp_path.iterdir()) == []
+
+
+def test_builds_at_the_same_time(monkeypatch, tmp_path):
+    """What another build has removed already is no error."""
+    monkeypatch.setattr(blbuild, "BUILD", str(tmp_path))
+    monkeypatch.setattr(blbuild.glob, "glob", lambda pattern: [str(tmp_path / "bitlinear_marshal-gone.so")])
+    monkeypatch.setattr(blbuild, "_marshal_command", lambda out: None)
+    assert blbuild._build_marshal(False, False) is None
+
+
+def test_a_torch_that_is_still_importing_leaves_the_c_abi(built):
+    assert not loaded("import torch; del torch.__version__")
