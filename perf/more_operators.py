@@ -22,7 +22,7 @@ def listed():
     return [
         # two answers to one short question begin: latency alone
         {"name": "shared_pair_int8", "op": "shared", "groups": 1, "R": 2, "Hq": 16, "Hkv": 16, "D": 128, "S": 37, "own": 1, "ragged": False, "page": 32, "format": "int8"},
-        # drafted tokens of eight sequences of different ages: five rows of each share all that came before
+        # drafted tokens of eight sequences of different ages: the five rows of each share its pages, every one sees a token more
         {"name": "shared_drafts_int8", "op": "shared", "groups": 8, "R": 5, "Hq": 32, "Hkv": 32, "D": 80, "S": 2048, "own": 5, "ragged": True, "page": 64, "format": "int8"},
         # a served batch behind one system prompt, answers of different lengths
         {"name": "shared_prompt_int8", "op": "shared", "groups": 1, "R": 64, "Hq": 32, "Hkv": 32, "D": 80, "S": 2039, "own": 256, "ragged": True, "page": 64, "format": "int8"},
@@ -136,10 +136,14 @@ def prepare(case, seed):
         groups, R, page = c["groups"], c["R"], c["page"]
         B = groups * R
         shared = _host_ints(seed, max(1, c["S"] // 2), c["S"], groups) if c["ragged"] and groups > 1 else torch.full((groups,), c["S"], dtype=torch.int32)
-        if c["own"] == R and groups > 1:  # drafts: the rows of a sequence see one token more each
+        drafts = c["own"] == R and groups > 1  # the rows of a sequence see one token more each, and share all of its pages
+        if drafts:
             more = torch.arange(1, R + 1, dtype=torch.int32).repeat(groups)
         else:
             more = _host_ints(seed + 1, 1, c["own"], B) if c["ragged"] else torch.full((B,), c["own"], dtype=torch.int32)
+        lengths = shared.repeat_interleave(R) + more
+        if drafts:
+            shared = shared + R
         # a page table as a serving program keeps it: whole pages of the prefix are one and the same, later ones a row's own
         whole, width = c["S"] // page, -(-(c["S"] + c["own"]) // page)
         tail = width - whole
@@ -151,8 +155,8 @@ def prepare(case, seed):
         columns = torch.arange(width, device="cuda")[None]
         s["table"] = torch.where(columns < ends[:, None], first_row, table).contiguous()
         s["cache"] = _pool(g, c, groups * whole + B * tail)
-        s["shared"], s["lengths"] = shared.cuda(), (shared.repeat_interleave(R) + more).cuda()
-        s["most"], s["most_own"] = int(shared.max()), int(more.max())
+        s["shared"], s["lengths"] = shared.cuda(), lengths.cuda()
+        s["most"], s["most_own"] = int(shared.max()), 1 if drafts else int(more.max())
         s["q"] = torch.randn(B, c["Hq"], c["D"], generator=g, device="cuda") * 1.5
         s["out"] = torch.empty_like(s["q"])
         s["workspace"] = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
@@ -278,7 +282,8 @@ def _plain_shared(s):
     t = torch.arange(s["most"], device="cuda").expand(groups, -1)
     k, v = (_tokens(s["cache"], n, s["table"][::R], t, page).transpose(1, 2) for n in "kv")
     q = s["q"].view(groups, R, Hkv, G, D).transpose(1, 2).reshape(groups, Hkv, R * G, D)
-    there = (t < s["shared"].long()[:, None])[:, None, None]
+    limits = torch.minimum(s["lengths"].view(groups, R), s["shared"][:, None]).repeat_interleave(G, 1)  # of a key head's rows
+    there = (t[:, None] < limits.long()[..., None])[:, None]
     a, ma, za = (x.reshape(groups, Hkv, R, G, -1).transpose(1, 2).reshape(B, Hkv, G, -1) for x in _attend(q @ k.transpose(2, 3) * scale, there, v))
     # each row's own tokens
     t = s["shared"].long().repeat_interleave(R)[:, None] + torch.arange(s["most_own"], device="cuda")
