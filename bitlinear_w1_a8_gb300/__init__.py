@@ -23,7 +23,9 @@ __all__ = [
     "bitlinear_selftest_wait_timeout", "bitlinear_linear", "bitlinear_linear_ws", "bitlinear_argmax",
     "bitlinear_rope_frequencies", "bitlinear_rope", "bitlinear_kv_append", "bitlinear_kv_read",
     "bitlinear_attention_workspace", "bitlinear_attention",
-    "BitLinearWeight", "BitLinearKVPages", "BitLinearRopeSpec",
+    "bitlinear_attention_shared_workspace", "bitlinear_attention_shared", "bitlinear_kv_summarise",
+    "bitlinear_attention_select", "bitlinear_attention_blocks", "bitlinear_softmax", "bitlinear_verify",
+    "BitLinearWeight", "BitLinearKVPages", "BitLinearRopeSpec", "BitLinearKVSummary",
     "EXPORTED_SYMBOLS",
     "ALGO_AUTO", "ALGO_DECODE", "ALGO_PREFILL", "ALGO_BATCHED", "ALGO_WIDE", "FLAG_PDL",
     "KV_INT8", "KV_FP8", "KV_BF16", "ROPE_HALF", "ROPE_INTERLEAVED",
@@ -54,7 +56,12 @@ EXPORTED_SYMBOLS = (
     "bitlinear_selftest_wait_timeout", "bitlinear_linear", "bitlinear_linear_ws", "bitlinear_argmax",
     "bitlinear_rope_frequencies", "bitlinear_rope", "bitlinear_kv_append", "bitlinear_kv_read",
     "bitlinear_attention_workspace", "bitlinear_attention",
+    "bitlinear_attention_shared_workspace", "bitlinear_attention_shared", "bitlinear_kv_summarise",
+    "bitlinear_attention_select", "bitlinear_attention_blocks", "bitlinear_softmax", "bitlinear_verify",
 )
+
+# The calls of a serving step that the compiled marshal takes, in bind_serving's order.
+_SERVING = ("attention_shared", "kv_summarise", "attention_select", "attention_blocks", "softmax", "verify")
 
 _lib = None
 torch = None     # imported by the first attention call: the C ABI alone needs no torch
@@ -79,6 +86,11 @@ class BitLinearRopeSpec(ctypes.Structure):
     """ctypes mirror of the C struct bitlinear_rope_spec."""
     _fields_ = [("freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
                 ("amplitude", ctypes.c_float)]
+
+
+class BitLinearKVSummary(ctypes.Structure):
+    """ctypes mirror of the C struct bitlinear_kv_summary."""
+    _fields_ = [("bounds", ctypes.c_void_p), ("step", ctypes.c_void_p)]
 
 
 class BitLinearError(RuntimeError):
@@ -151,6 +163,21 @@ def load_library(path: str | None = None):
     lib.bitlinear_attention.argtypes = [vp, i64, i64, ci, pages, vp, i64, i64, vp, i64, ctypes.c_float, vp, i64, vp,
                                         sz, ci, vp]
     lib.bitlinear_attention.restype = st
+    summary, f32 = ctypes.POINTER(BitLinearKVSummary), ctypes.c_float
+    lib.bitlinear_attention_shared_workspace.argtypes = [i64, ci, ci, ci, i64]
+    lib.bitlinear_attention_shared_workspace.restype = sz
+    lib.bitlinear_attention_shared.argtypes = [vp, i64, i64, ci, pages, vp, i64, i64, vp, vp, i64, f32, vp, i64, vp, sz, ci, vp]
+    lib.bitlinear_attention_shared.restype = st
+    lib.bitlinear_kv_summarise.argtypes = [pages, summary, vp, i64, i64, i64, vp, vp, ci, vp]
+    lib.bitlinear_kv_summarise.restype = st
+    lib.bitlinear_attention_select.argtypes = [vp, i64, i64, ci, pages, summary, vp, i64, i64, vp, ci, ci, vp, ci, ci, vp]
+    lib.bitlinear_attention_select.restype = st
+    lib.bitlinear_attention_blocks.argtypes = [vp, i64, i64, ci, pages, vp, i64, i64, vp, vp, ci, f32, vp, i64, ci, vp]
+    lib.bitlinear_attention_blocks.restype = st
+    lib.bitlinear_softmax.argtypes = [vp, i64, i64, vp, vp, ci, vp]
+    lib.bitlinear_softmax.restype = st
+    lib.bitlinear_verify.argtypes = [vp, vp, i64, ci, i64, vp, vp, vp, vp, ci, vp]
+    lib.bitlinear_verify.restype = st
     lib.bitlinear_device_status.argtypes = [vp, ctypes.c_int]
     lib.bitlinear_device_status.restype = st
     if path is None:
@@ -189,6 +216,7 @@ def _load_marshal(lib):
         return
     module.bind(*(ctypes.cast(getattr(lib, "bitlinear_" + name), ctypes.c_void_p).value
                   for name in ("rope", "kv_append", "kv_read", "attention")))
+    module.bind_serving(*(ctypes.cast(getattr(lib, "bitlinear_" + name), ctypes.c_void_p).value for name in _SERVING))
     _marshal = module
 
 
@@ -724,3 +752,179 @@ def bitlinear_attention(q, cache, page_table, lengths, out, workspace=None, scal
         q.data_ptr(), q_stride, B, Hq, pages, page_table.data_ptr(), table_stride, max_pages, lengths.data_ptr(),
         window, D ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, space,
         0 if workspace is None else workspace.numel(), flags, _stream(stream)), "bitlinear_attention")
+
+
+# --- a serving step: shared prefixes, chosen blocks, probabilities and drafted tokens ---
+#
+# As above: the compiled marshal takes the common case, and each call does every other here.
+
+
+def bitlinear_attention_shared_workspace(B: int, num_q_heads: int, num_kv_heads: int, head_dim: int, num_groups: int) -> int:
+    """Bytes of device workspace that bitlinear_attention_shared needs."""
+    return int(load_library().bitlinear_attention_shared_workspace(int(B), int(num_q_heads), int(num_kv_heads), int(head_dim),
+                                                                   int(num_groups)))
+
+
+def _attention_tensors(q, cache, page_table, lengths, out):
+    """(device, pages, the arguments q .. lengths and out, out_stride) of an attention call."""
+    at = _device(q, "q")
+    pages = _kv_pages(cache, at)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != pages.head_dim:
+        raise ValueError(f"q must be [sequences, heads, {pages.head_dim}], got {tuple(shape)}")
+    B, Hq, D = shape
+    q_stride, out_stride = _rows(q, at, "q", shape), _rows(out, at, "out", shape)
+    _need_on(lengths, at, torch.int32, "lengths", (B,))
+    _, max_pages, table_stride = _page_table(page_table, at, B)
+    return at, pages, (q.data_ptr(), q_stride, B, Hq, pages, page_table.data_ptr(), table_stride, max_pages,
+                       lengths.data_ptr()), (out.data_ptr(), out_stride)
+
+
+def bitlinear_attention_shared(q, cache, page_table, lengths, shared, out, workspace=None, scale: float | None = None,
+                               flags: int = 0, stream=None):
+    """bitlinear_attention of rows that share their first shared[g] (int32 [groups]) tokens in groups of
+    B / groups consecutive rows: those tokens are read once for all of a group's rows.  page_table and
+    lengths are each row's own, shared tokens included; workspace: uint8, at least
+    bitlinear_attention_shared_workspace() bytes."""
+    if not _ready:
+        _get_ready()
+    if _marshal is not None:
+        status = _marshal.attention_shared(q, cache, page_table, lengths, shared, out, workspace, scale, flags, stream)
+        if status is not None:
+            return _check(status, "bitlinear_attention_shared")
+    at, pages, tensors, written = _attention_tensors(q, cache, page_table, lengths, out)
+    _need_on(shared, at, torch.int32, "shared")
+    if shared.dim() != 1:
+        raise ValueError(f"shared must be [groups], got {tuple(shared.shape)}")
+    if workspace is not None:
+        _need_on(workspace, at, torch.uint8, "workspace")
+    _check(load_library().bitlinear_attention_shared(
+        *tensors, shared.data_ptr(), shared.shape[0], pages.head_dim ** -0.5 if scale is None else scale, *written,
+        _ptr(workspace), 0 if workspace is None else workspace.numel(), flags, _stream(stream)), "bitlinear_attention_shared")
+
+
+def _kv_summary(summary, pages, at):
+    """BitLinearKVSummary of (bounds, step)."""
+    bounds, step = summary
+    _need_on(bounds, at, torch.int8, "the summary's bounds", (pages.num_pages, pages.num_heads, 2, pages.head_dim))
+    _need_on(step, at, torch.float32, "the summary's step", (pages.num_pages, pages.num_heads))
+    return BitLinearKVSummary(bounds.data_ptr(), step.data_ptr())
+
+
+def bitlinear_kv_summarise(cache, summary, page_table, first, lengths, flags: int = 0, stream=None):
+    """Writes the bounds of the keys of the pages that hold tokens first[b] .. lengths[b] - 1 (int32 [B]).
+
+    summary: (bounds, step), int8 [pages, heads, 2, head_dim] and fp32 [pages, heads]; cache and
+    page_table as for bitlinear_attention."""
+    if not _ready:
+        _get_ready()
+    if _marshal is not None:
+        status = _marshal.kv_summarise(cache, summary, page_table, first, lengths, flags, stream)
+        if status is not None:
+            return _check(status, "bitlinear_kv_summarise")
+    at = _device(page_table, "page_table")
+    pages = _kv_pages(cache, at)
+    B, max_pages, table_stride = _page_table(page_table, at)
+    _need_on(first, at, torch.int32, "first", (B,))
+    _need_on(lengths, at, torch.int32, "lengths", (B,))
+    _check(load_library().bitlinear_kv_summarise(
+        pages, _kv_summary(summary, pages, at), page_table.data_ptr(), table_stride, B, max_pages, first.data_ptr(),
+        lengths.data_ptr(), flags, _stream(stream)), "bitlinear_kv_summarise")
+
+
+def _blocks(blocks, B, pages, at):
+    """How many pages a list of int32 [B, heads, count] names."""
+    _need_on(blocks, at, torch.int32, "blocks")
+    if blocks.dim() != 3 or blocks.shape[:2] != (B, pages.num_heads):
+        raise ValueError(f"blocks must be [{B}, {pages.num_heads}, count], got {tuple(blocks.shape)}")
+    return blocks.shape[2]
+
+
+def bitlinear_attention_select(q, cache, summary, page_table, lengths, blocks, keep_first: int = 1, keep_last: int = 1,
+                               flags: int = 0, stream=None):
+    """blocks [B, heads, count] (int32) = the pages (columns of the page table) of the largest scores for
+    each key head, the first keep_first and last keep_last of a sequence among them, in order, then -1.
+    summary: as bitlinear_kv_summarise wrote it; other arguments as for bitlinear_attention."""
+    if not _ready:
+        _get_ready()
+    if _marshal is not None:
+        status = _marshal.attention_select(q, cache, summary, page_table, lengths, blocks, keep_first, keep_last, flags, stream)
+        if status is not None:
+            return _check(status, "bitlinear_attention_select")
+    at = _device(q, "q")
+    pages = _kv_pages(cache, at)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != pages.head_dim:
+        raise ValueError(f"q must be [sequences, heads, {pages.head_dim}], got {tuple(shape)}")
+    q_stride = _rows(q, at, "q", shape)
+    _need_on(lengths, at, torch.int32, "lengths", (shape[0],))
+    _, max_pages, table_stride = _page_table(page_table, at, shape[0])
+    count = _blocks(blocks, shape[0], pages, at)
+    _check(load_library().bitlinear_attention_select(
+        q.data_ptr(), q_stride, shape[0], shape[1], pages, _kv_summary(summary, pages, at), page_table.data_ptr(), table_stride,
+        max_pages, lengths.data_ptr(), int(keep_first), int(keep_last), blocks.data_ptr(), count, flags, _stream(stream)),
+        "bitlinear_attention_select")
+
+
+def bitlinear_attention_blocks(q, cache, page_table, lengths, blocks, out, scale: float | None = None, flags: int = 0, stream=None):
+    """bitlinear_attention over the tokens of the pages that blocks [B, heads, count] (int32) lists for each key
+    head, in place of all tokens."""
+    if not _ready:
+        _get_ready()
+    if _marshal is not None:
+        status = _marshal.attention_blocks(q, cache, page_table, lengths, blocks, out, scale, flags, stream)
+        if status is not None:
+            return _check(status, "bitlinear_attention_blocks")
+    at, pages, tensors, written = _attention_tensors(q, cache, page_table, lengths, out)
+    count = _blocks(blocks, q.shape[0], pages, at)
+    _check(load_library().bitlinear_attention_blocks(
+        *tensors, blocks.data_ptr(), count, pages.head_dim ** -0.5 if scale is None else scale, *written, flags,
+        _stream(stream)), "bitlinear_attention_blocks")
+
+
+def bitlinear_softmax(y, p, temperature=None, flags: int = 0, stream=None):
+    """p [M, N] = softmax(y / temperature) of logits y [M, N] (fp32; p may be y); temperature: fp32 [M], 0 for the
+    first maximum alone, or None for 1."""
+    if not _ready:
+        _get_ready()
+    if _marshal is not None:
+        status = _marshal.softmax(y, p, temperature, flags, stream)
+        if status is not None:
+            return _check(status, "bitlinear_softmax")
+    at = _device(y, "y")
+    _need_on(y, at, torch.float32, "y")
+    if y.dim() != 2:
+        raise ValueError(f"y must be [M, N], got {tuple(y.shape)}")
+    _need_on(p, at, torch.float32, "p", y.shape)
+    if temperature is not None:
+        _need_on(temperature, at, torch.float32, "temperature", y.shape[:1])
+    _check(load_library().bitlinear_softmax(y.data_ptr(), y.shape[0], y.shape[1], _ptr(temperature), p.data_ptr(), flags,
+                                            _stream(stream)), "bitlinear_softmax")
+
+
+def bitlinear_verify(p, q, draft, uniform, tokens, accepted, flags: int = 0, stream=None):
+    """Verifies drafts [B, K] (int32) against the target's probabilities p [B, K + 1, N], given the draft's
+    q [B, K, N] and random numbers uniform [B, K + 1] in [0, 1): tokens [B, K + 1] (int32) = the drafts taken, one token
+    drawn, then -1; accepted [B] (int32) = how many were taken.  q and draft None: K = 0, a token is drawn."""
+    if not _ready:
+        _get_ready()
+    if _marshal is not None:
+        status = _marshal.verify(p, q, draft, uniform, tokens, accepted, flags, stream)
+        if status is not None:
+            return _check(status, "bitlinear_verify")
+    at = _device(p, "p")
+    f32, i32 = torch.float32, torch.int32
+    _need_on(p, at, f32, "p")
+    if p.dim() != 3 or p.shape[1] < 1:
+        raise ValueError(f"p must be [sequences, drafts + 1, N], got {tuple(p.shape)}")
+    B, K, N = p.shape[0], p.shape[1] - 1, p.shape[2]
+    if K > 0 or q is not None:
+        _need_on(q, at, f32, "q", (B, K, N))
+    if K > 0 or draft is not None:
+        _need_on(draft, at, i32, "draft", (B, K))
+    _need_on(uniform, at, f32, "uniform", (B, K + 1))
+    _need_on(tokens, at, i32, "tokens", (B, K + 1))
+    _need_on(accepted, at, i32, "accepted", (B,))
+    _check(load_library().bitlinear_verify(p.data_ptr(), _ptr(q) if K else None, B, K, N, _ptr(draft) if K else None,
+                                           uniform.data_ptr(), tokens.data_ptr(), accepted.data_ptr(), flags,
+                                           _stream(stream)), "bitlinear_verify")

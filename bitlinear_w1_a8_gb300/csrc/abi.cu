@@ -6,6 +6,7 @@
 
 #include "common.cuh"
 #include "kv.cuh"
+#include "serve.cuh"
 
 namespace bitlinear {
 // argmax.cu: index[m] = first n of the largest y[m, n], M rows of N floats.
@@ -555,6 +556,35 @@ bitlinear_status check_rows(int64_t T, const int32_t* positions, const int32_t* 
   return BITLINEAR_OK;
 }
 
+constexpr int kMostChosen = 4096;   // pages a list names
+constexpr int kMostDrafts = 65535;  // of a sequence
+
+bitlinear_status check_summary(const bitlinear_kv_summary* s, Summary* out) {
+  if (!s || !s->bounds || !s->step) return BITLINEAR_ERR_NULL;
+  if (!aligned16(s->bounds) || !aligned16(s->step)) return BITLINEAR_ERR_ALIGN;
+  *out = Summary{s->bounds, s->step};
+  return BITLINEAR_OK;
+}
+
+// What the attention calls without a window have in common; an empty batch passes.
+bitlinear_status check_attention(const float* q, int64_t q_stride, int64_t B, int num_q_heads,
+                                 const bitlinear_kv_pages* cache, const int32_t* page_table, int64_t table_stride,
+                                 int64_t max_pages, const int32_t* lengths, float scale, const float* out,
+                                 int64_t out_stride, int flags, KvPages* c) {
+  const bitlinear_status st = check_pages(cache, c);
+  if (st != BITLINEAR_OK) return st;
+  if (B < 0 || B > kMaxDim || !table_ok(table_stride, max_pages) || !isfinite(scale)) return BITLINEAR_ERR_SHAPE;
+  if (num_q_heads < 1 || num_q_heads > kMaxHeads || num_q_heads % c->heads != 0) return BITLINEAR_ERR_SHAPE;
+  if (!stride_ok(q_stride, num_q_heads, c->head_dim) || !stride_ok(out_stride, num_q_heads, c->head_dim))
+    return BITLINEAR_ERR_SHAPE;
+  if (flags & ~BITLINEAR_FLAG_PDL) return BITLINEAR_ERR_UNSUPPORTED;
+  if (B == 0) return BITLINEAR_OK;
+  if (!q || !out || !page_table || !lengths) return BITLINEAR_ERR_NULL;
+  if (!aligned16(q) || !aligned16(out) || !aligned_to(page_table, 4) || !aligned_to(lengths, 4))
+    return BITLINEAR_ERR_ALIGN;
+  return BITLINEAR_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -701,6 +731,141 @@ bitlinear_status bitlinear_attention(const float* q, int64_t q_stride, int64_t B
                         B, num_q_heads};
   return from_cuda(launch_attention(a, c, workspace, (flags & BITLINEAR_FLAG_PDL) != 0, dev,
                                     static_cast<cudaStream_t>(stream)));
+}
+
+size_t bitlinear_attention_shared_workspace(int64_t B, int num_q_heads, int num_kv_heads, int head_dim,
+                                            int64_t num_groups) {
+  if (B < 1 || B > kMaxDim || num_q_heads < 1 || num_q_heads > kMaxHeads || num_kv_heads < 1 ||
+      num_q_heads % num_kv_heads != 0 || head_dim < 16 || head_dim > kMaxHeadDim || head_dim % 16 != 0 ||
+      B * num_q_heads > 0x7fffffffLL || num_groups < 1 || B % num_groups != 0)
+    return 0;
+  return attention_shared_workspace_bytes(B, num_q_heads, num_kv_heads, head_dim, num_groups);
+}
+
+bitlinear_status bitlinear_attention_shared(const float* q, int64_t q_stride, int64_t B, int num_q_heads,
+                                            const bitlinear_kv_pages* cache, const int32_t* page_table,
+                                            int64_t table_stride, int64_t max_pages, const int32_t* lengths,
+                                            const int32_t* shared, int64_t num_groups, float scale, float* out,
+                                            int64_t out_stride, void* workspace, size_t workspace_bytes, int flags,
+                                            void* stream) {
+  KvPages c;
+  bitlinear_status st = check_attention(q, q_stride, B, num_q_heads, cache, page_table, table_stride, max_pages, lengths,
+                                        scale, out, out_stride, flags, &c);
+  if (st != BITLINEAR_OK) return st;
+  if (num_groups < 1 || B % num_groups != 0 || B * num_q_heads > 0x7fffffffLL) return BITLINEAR_ERR_SHAPE;
+  if (B == 0) return BITLINEAR_OK;
+  if (!shared) return BITLINEAR_ERR_NULL;
+  if (!aligned_to(shared, 4)) return BITLINEAR_ERR_ALIGN;
+  const size_t need = attention_shared_workspace_bytes(B, num_q_heads, c.heads, c.head_dim, num_groups);
+  if (workspace ? workspace_bytes < need : num_groups < B && need > 0) return BITLINEAR_ERR_WORKSPACE;
+  if (workspace && !aligned16(workspace)) return BITLINEAR_ERR_ALIGN;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  const AttendArgs a = {q, out, q_stride, out_stride, page_table, table_stride, max_pages, lengths, 0, scale, B, num_q_heads};
+  return from_cuda(launch_attention_shared(a, c, shared, num_groups, workspace, (flags & BITLINEAR_FLAG_PDL) != 0, dev,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+bitlinear_status bitlinear_attention_blocks(const float* q, int64_t q_stride, int64_t B, int num_q_heads,
+                                            const bitlinear_kv_pages* cache, const int32_t* page_table,
+                                            int64_t table_stride, int64_t max_pages, const int32_t* lengths,
+                                            const int32_t* blocks, int count, float scale, float* out,
+                                            int64_t out_stride, int flags, void* stream) {
+  KvPages c;
+  bitlinear_status st = check_attention(q, q_stride, B, num_q_heads, cache, page_table, table_stride, max_pages, lengths,
+                                        scale, out, out_stride, flags, &c);
+  if (st != BITLINEAR_OK) return st;
+  if (count < 1 || count > kMostChosen) return BITLINEAR_ERR_SHAPE;
+  if (B == 0) return BITLINEAR_OK;
+  if (!blocks) return BITLINEAR_ERR_NULL;
+  if (!aligned_to(blocks, 4)) return BITLINEAR_ERR_ALIGN;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  const AttendArgs a = {q, out, q_stride, out_stride, page_table, table_stride, max_pages, lengths, 0, scale, B, num_q_heads};
+  return from_cuda(launch_attention_blocks(a, c, blocks, count, (flags & BITLINEAR_FLAG_PDL) != 0, dev,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+bitlinear_status bitlinear_kv_summarise(const bitlinear_kv_pages* cache, const bitlinear_kv_summary* summary,
+                                        const int32_t* page_table, int64_t table_stride, int64_t B, int64_t max_pages,
+                                        const int32_t* first, const int32_t* lengths, int flags, void* stream) {
+  KvPages c;
+  Summary s;
+  bitlinear_status st = check_pages(cache, &c);
+  if (st == BITLINEAR_OK) st = check_summary(summary, &s);
+  if (st != BITLINEAR_OK) return st;
+  if (B < 0 || B > kMaxDim || !table_ok(table_stride, max_pages)) return BITLINEAR_ERR_SHAPE;
+  if (flags & ~BITLINEAR_FLAG_PDL) return BITLINEAR_ERR_UNSUPPORTED;
+  if (B == 0) return BITLINEAR_OK;
+  if (!page_table || !first || !lengths) return BITLINEAR_ERR_NULL;
+  if (!aligned_to(page_table, 4) || !aligned_to(first, 4) || !aligned_to(lengths, 4)) return BITLINEAR_ERR_ALIGN;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  return from_cuda(launch_summarise(c, s, page_table, table_stride, B, max_pages, first, lengths,
+                                    (flags & BITLINEAR_FLAG_PDL) != 0, dev, static_cast<cudaStream_t>(stream)));
+}
+
+bitlinear_status bitlinear_attention_select(const float* q, int64_t q_stride, int64_t B, int num_q_heads,
+                                            const bitlinear_kv_pages* cache, const bitlinear_kv_summary* summary,
+                                            const int32_t* page_table, int64_t table_stride, int64_t max_pages,
+                                            const int32_t* lengths, int keep_first, int keep_last, int32_t* blocks,
+                                            int count, int flags, void* stream) {
+  KvPages c;
+  Summary s;
+  bitlinear_status st = check_pages(cache, &c);
+  if (st == BITLINEAR_OK) st = check_summary(summary, &s);
+  if (st != BITLINEAR_OK) return st;
+  if (B < 0 || B > kMaxDim || !table_ok(table_stride, max_pages)) return BITLINEAR_ERR_SHAPE;
+  if (num_q_heads < 1 || num_q_heads > kMaxHeads || num_q_heads % c.heads != 0 ||
+      !stride_ok(q_stride, num_q_heads, c.head_dim))
+    return BITLINEAR_ERR_SHAPE;
+  if (keep_first < 0 || keep_last < 0 || count < 1 || count > kMostChosen) return BITLINEAR_ERR_SHAPE;
+  if (max_pages > kMostBlocks || (flags & ~BITLINEAR_FLAG_PDL)) return BITLINEAR_ERR_UNSUPPORTED;
+  if (B == 0) return BITLINEAR_OK;
+  if (!q || !page_table || !lengths || !blocks) return BITLINEAR_ERR_NULL;
+  if (!aligned16(q) || !aligned_to(page_table, 4) || !aligned_to(lengths, 4) || !aligned_to(blocks, 4))
+    return BITLINEAR_ERR_ALIGN;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  const SelectArgs a = {q, q_stride, num_q_heads, page_table, table_stride, max_pages, lengths, keep_first, keep_last, count, blocks, B};
+  return from_cuda(launch_select(a, c, s, (flags & BITLINEAR_FLAG_PDL) != 0, dev, static_cast<cudaStream_t>(stream)));
+}
+
+bitlinear_status bitlinear_softmax(const float* y, int64_t M, int64_t N, const float* temperature, float* p, int flags,
+                                   void* stream) {
+  if (M < 0 || M > kMaxDim || N <= 0 || N > 0x7fffffffLL || M > ((int64_t)1 << 48) / N) return BITLINEAR_ERR_SHAPE;
+  if (flags & ~BITLINEAR_FLAG_PDL) return BITLINEAR_ERR_UNSUPPORTED;
+  if (M == 0) return BITLINEAR_OK;
+  if (!y || !p) return BITLINEAR_ERR_NULL;
+  if (!aligned16(y) || !aligned16(p) || !aligned_to(temperature, 4)) return BITLINEAR_ERR_ALIGN;
+  DeviceInfo dev;
+  const bitlinear_status st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  return from_cuda(launch_softmax(y, p, temperature, M, N, (flags & BITLINEAR_FLAG_PDL) != 0, dev,
+                                  static_cast<cudaStream_t>(stream)));
+}
+
+bitlinear_status bitlinear_verify(const float* p, const float* q, int64_t B, int num_drafts, int64_t N,
+                                  const int32_t* draft, const float* uniform, int32_t* tokens, int32_t* accepted,
+                                  int flags, void* stream) {
+  if (B < 0 || B > kMaxDim || num_drafts < 0 || num_drafts > kMostDrafts || N <= 0 || N > 0x7fffffffLL ||
+      B > ((int64_t)1 << 48) / N / (num_drafts + 1))
+    return BITLINEAR_ERR_SHAPE;
+  if (flags & ~BITLINEAR_FLAG_PDL) return BITLINEAR_ERR_UNSUPPORTED;
+  if (B == 0) return BITLINEAR_OK;
+  if (!p || !uniform || !tokens || !accepted || (num_drafts > 0 && (!q || !draft))) return BITLINEAR_ERR_NULL;
+  if (!aligned16(p) || !aligned16(q) || !aligned_to(draft, 4) || !aligned_to(uniform, 4) || !aligned_to(tokens, 4) ||
+      !aligned_to(accepted, 4))
+    return BITLINEAR_ERR_ALIGN;
+  DeviceInfo dev;
+  const bitlinear_status st = current_device(&dev);
+  if (st != BITLINEAR_OK) return st;
+  return from_cuda(launch_verify(p, q, draft, uniform, B, num_drafts, N, tokens, accepted,
+                                 (flags & BITLINEAR_FLAG_PDL) != 0, dev, static_cast<cudaStream_t>(stream)));
 }
 
 bitlinear_status bitlinear_selftest_wait_timeout(int64_t limit_ns, void* stream) {

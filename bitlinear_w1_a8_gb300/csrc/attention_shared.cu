@@ -1,0 +1,120 @@
+// attention_shared.cu -- attention of a batch whose rows share their first tokens in groups.
+//
+// A group's sequences name the same pages for their first shared[g] tokens (a system prompt, a
+// document, all of a sequence that several drafted tokens go on from).  Those tokens are
+// attended to once for all of the group's q heads of a key head, eight to a CTA; what a
+// row has behind them is its own:
+//   out = (P_shared + P_own) / (sum_shared + sum_own), each sum under its reference, joined as the
+// parts of one sequence are (attend.cuh).  Two launches: the shared tokens, split over CTAs
+// that leave their parts in the workspace, and each row's own tokens with the join.
+#include "attend.cuh"
+#include "serve.cuh"
+
+namespace bitlinear {
+namespace {
+
+// The most CTAs that shared tokens are split over beside one a row.
+constexpr int kPrefixCtas = 4 * kSms;
+
+struct Sizes {
+  int64_t group_rows, rows;  // sequences a group; kPrefix's rows of all groups
+  int heads_a_key, tiles, heads;  // q heads a key head; rows a key head of a group; q heads of a row
+};
+Sizes sizes_of(int64_t B, int q_heads, int kv_heads, int64_t groups) {
+  Sizes s;
+  s.group_rows = B / groups;
+  s.heads_a_key = q_heads / kv_heads;
+  const int64_t all = s.group_rows * s.heads_a_key, tiles = (all + kRowHeads - 1) / kRowHeads;
+  s.tiles = (int)tiles;
+  s.heads = (int)(all < kRowHeads ? all : kRowHeads);
+  s.rows = groups * kv_heads * tiles;
+  return s;
+}
+int64_t slots_of(const Sizes& s) { return s.rows > kPrefixCtas ? s.rows : kPrefixCtas; }
+
+template <int FORMAT, int DT>
+cudaError_t launch_shape(AttendArgs a, const KvPages& c, const int32_t* shared, int64_t groups, void* workspace, bool pdl,
+                         const DeviceInfo& dev, cudaStream_t stream) {
+  using S = Shape<FORMAT, DT>;
+  set_factor(a);
+  static thread_local int configured_device = -1, most_cluster;
+  if (configured_device != dev.device) {
+    cudaError_t err = allow_shared_memory<S>(attend_kernel<FORMAT, DT, kPrefix>);
+    if (err == cudaSuccess) err = allow_clusters<S>(attend_kernel<FORMAT, DT, kOwn>, &most_cluster);
+    if (err != cudaSuccess) return err;
+    configured_device = dev.device;
+  }
+  const Sizes sizes = sizes_of(a.B, a.q_heads, c.heads, groups);
+  const int64_t steps = ((a.max_pages << c.page_shift) + S::kTokens - 1) / S::kTokens;
+
+  // The shared tokens: a group is a sequence, its rows' q heads those of one key head.
+  AttendArgs g = a;
+  g.B = groups;
+  g.lengths = shared;
+  g.table_stride = a.table_stride * sizes.group_rows;
+  Shares sh = {};
+  sh.group = (int)(sizes.group_rows * sizes.heads_a_key);
+  sh.groups = sizes.tiles;
+  sh.rows_a_seq = c.heads * sizes.tiles;
+  sh.parts = static_cast<float*>(workspace);
+  sh.rows = reinterpret_cast<int2*>(sh.parts + slots_of(sizes) * sizes.heads * (c.head_dim + 4));
+  sh.group_rows = (int)sizes.group_rows;
+  sh.shared = shared;
+  sh.lengths = a.lengths;
+  sh.heads_a_key = sizes.heads_a_key;
+  sh.prefix_tiles = sizes.tiles;
+  int smem = (int)S::kSmem + sizes.heads * S::kHeadBytes + kRowHeads * 4;
+  const int ctas = resident_ctas<S>(dev, smem);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  if (pdl) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+  }
+  if (groups <= kShareSeqs && sizes.rows <= ctas / 3 && steps_fit(sizes.rows, steps)) {
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  } else {
+    sh.splits = splits_for(sizes.rows, steps, ctas, kPortableCluster);
+    while ((1 << sh.splits_log2) < sh.splits) ++sh.splits_log2;
+    cfg.gridDim = dim3((unsigned)(sizes.rows * sh.splits), 1, 1);
+  }
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, attend_kernel<FORMAT, DT, kPrefix>, g, c, sh);
+  if (err != cudaSuccess) return err;
+
+  // Each row's own tokens, and the join.
+  sh.group = sizes.heads_a_key;
+  sh.groups = (sh.group + kRowHeads - 1) / kRowHeads;
+  sh.rows_a_seq = c.heads * sh.groups;
+  const int heads = sh.group < kRowHeads ? sh.group : kRowHeads;
+  smem = (int)S::kSmem + heads * S::kHeadBytes + kRowHeads * 4;
+  const int own_ctas = resident_ctas<S>(dev, smem + received_bytes(heads, c.head_dim, kMaxCluster));
+  sh.splits = splits_for(a.B * sh.rows_a_seq, steps, own_ctas, most_cluster);
+  sh.splits_log2 = 0;
+  while ((1 << sh.splits_log2) < sh.splits) ++sh.splits_log2;
+  return launch_clusters<FORMAT, DT, kOwn>(a, c, sh, smem + received_bytes(heads, c.head_dim, sh.splits), true, stream);
+}
+
+}  // namespace
+
+size_t attention_shared_workspace_bytes(int64_t B, int q_heads, int kv_heads, int head_dim, int64_t groups) {
+  const size_t alone = attention_workspace_bytes(B, q_heads, kv_heads, head_dim);
+  if (groups == B) return alone;
+  const Sizes s = sizes_of(B, q_heads, kv_heads, groups);
+  const size_t need = (size_t)slots_of(s) * s.heads * (head_dim + 4) * sizeof(float) + (size_t)s.rows * sizeof(int2);
+  return need > alone ? need : alone;
+}
+
+cudaError_t launch_attention_shared(const AttendArgs& a, const KvPages& cache, const int32_t* shared, int64_t groups,
+                                    void* workspace, bool pdl, const DeviceInfo& dev, cudaStream_t stream) {
+  if (groups == a.B) return launch_attention(a, cache, workspace, pdl, dev, stream);  // nothing is shared
+  return of_shape(cache, [&](auto format, auto dims) {
+    return launch_shape<decltype(format)::value, decltype(dims)::value>(a, cache, shared, groups, workspace, pdl, dev, stream);
+  });
+}
+
+}  // namespace bitlinear

@@ -24,6 +24,12 @@ decltype(&bitlinear_rope) g_rope;
 decltype(&bitlinear_kv_append) g_append;
 decltype(&bitlinear_kv_read) g_read;
 decltype(&bitlinear_attention) g_attention;
+decltype(&bitlinear_attention_shared) g_shared;
+decltype(&bitlinear_kv_summarise) g_summarise;
+decltype(&bitlinear_attention_select) g_select;
+decltype(&bitlinear_attention_blocks) g_blocks;
+decltype(&bitlinear_softmax) g_softmax;
+decltype(&bitlinear_verify) g_verify;
 
 constexpr auto kF32 = at::kFloat, kI32 = at::kInt;
 
@@ -267,6 +273,190 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// What the attention calls without a window have in common.
+struct Attended {
+  const at::Tensor *q, *table, *lengths;
+  int64_t device, stride;
+  bitlinear_kv_pages pages;
+};
+bool attended(PyObject* q, PyObject* cache, PyObject* table, PyObject* lengths, Attended* out) {
+  out->q = tensor(q);
+  out->table = tensor(table);
+  out->lengths = tensor(lengths);
+  const int64_t d = out->device = device_of(out->q);
+  if (d < 0 || !fits(out->q, d, kF32, 3) || !pages_of(cache, d, &out->pages) || out->q->size(2) != out->pages.head_dim ||
+      out->q->size(1) > 0x7fffffff || !fits(out->table, d, kI32, 2) || out->table->size(0) != out->q->size(0) ||
+      !fits(out->lengths, d, kI32, out->q->sizes().slice(0, 1)))
+    return false;
+  out->stride = out->q->size(1) * out->q->size(2);
+  return true;
+}
+bool scale_of(PyObject* o, const bitlinear_kv_pages& pages, double* out) {
+  if (o == Py_None) {
+    *out = std::pow((double)pages.head_dim, -0.5);
+    return true;
+  }
+  return real(o, out);
+}
+bool listed(PyObject* o, const Attended& a, const at::Tensor** out) {
+  const at::Tensor* t = *out = tensor(o);
+  return fits(t, a.device, kI32, 3) && t->size(0) == a.q->size(0) && t->size(1) == a.pages.num_heads && t->size(2) <= 0x7fffffff;
+}
+// (bounds, step) as the C struct.
+bool summary_of(PyObject* o, int64_t device, const bitlinear_kv_pages& pages, bitlinear_kv_summary* out) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 2) return false;
+  const at::Tensor *bounds = tensor(PyTuple_GET_ITEM(o, 0)), *step = tensor(PyTuple_GET_ITEM(o, 1));
+  const int64_t shape[4] = {pages.num_pages, pages.num_heads, 2, pages.head_dim};
+  if (!fits(bounds, device, at::kChar, at::IntArrayRef(shape, 4)) || !fits(step, device, kF32, at::IntArrayRef(shape, 2)))
+    return false;
+  *out = bitlinear_kv_summary{at_of<int8_t>(bounds), at_of<float>(step)};
+  return true;
+}
+
+// attention_shared(q, cache, page_table, lengths, shared, out, workspace, scale, flags, stream)
+PyObject* attention_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return common_case([&](int* status) {
+    if (n != 10) return false;
+    Attended t;
+    if (!attended(a[0], a[1], a[2], a[3], &t)) return false;
+    const at::Tensor *shared = tensor(a[4]), *out = tensor(a[5]), *space = a[6] == Py_None ? nullptr : tensor(a[6]);
+    double scale;
+    int flags;
+    void* stream;
+    if (!fits(shared, t.device, kI32, 1) || !fits(out, t.device, kF32, t.q->sizes()) ||
+        (a[6] != Py_None && !fits(space, t.device, at::kByte, 1)) || !scale_of(a[7], t.pages, &scale) ||
+        !flags_of(a[8], &flags) || !stream_of(a[9], t.device, &stream))
+      return false;
+    Released released;
+    *status = g_shared(at_of<float>(t.q), t.stride, t.q->size(0), (int)t.q->size(1), &t.pages, at_of<int32_t>(t.table),
+                       t.table->size(1), t.table->size(1), at_of<int32_t>(t.lengths), at_of<int32_t>(shared), shared->size(0),
+                       (float)scale, at_of<float>(out), t.stride, at_of(space), space ? (size_t)space->numel() : 0, flags, stream);
+    return true;
+  });
+}
+
+// kv_summarise(cache, summary, page_table, first, lengths, flags, stream)
+PyObject* kv_summarise(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return common_case([&](int* status) {
+    if (n != 7) return false;
+    const at::Tensor *table = tensor(a[2]), *first = tensor(a[3]), *lengths = tensor(a[4]);
+    const int64_t d = device_of(table);
+    bitlinear_kv_pages pages;
+    bitlinear_kv_summary summary;
+    int flags;
+    void* stream;
+    if (d < 0 || !fits(table, d, kI32, 2) || !pages_of(a[0], d, &pages) || !summary_of(a[1], d, pages, &summary) ||
+        !fits(first, d, kI32, table->sizes().slice(0, 1)) || !fits(lengths, d, kI32, table->sizes().slice(0, 1)) ||
+        !flags_of(a[5], &flags) || !stream_of(a[6], d, &stream))
+      return false;
+    Released released;
+    *status = g_summarise(&pages, &summary, at_of<int32_t>(table), table->size(1), table->size(0), table->size(1),
+                          at_of<int32_t>(first), at_of<int32_t>(lengths), flags, stream);
+    return true;
+  });
+}
+
+// attention_select(q, cache, summary, page_table, lengths, blocks, keep_first, keep_last, flags, stream)
+PyObject* attention_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return common_case([&](int* status) {
+    if (n != 10) return false;
+    Attended t;
+    if (!attended(a[0], a[1], a[3], a[4], &t)) return false;
+    const at::Tensor* blocks;
+    bitlinear_kv_summary summary;
+    long long first, last;
+    int flags;
+    void* stream;
+    if (!summary_of(a[2], t.device, t.pages, &summary) || !listed(a[5], t, &blocks) || !integer(a[6], &first) ||
+        !integer(a[7], &last) || first < 0 || first > 0x7fffffff || last < 0 || last > 0x7fffffff ||
+        !flags_of(a[8], &flags) || !stream_of(a[9], t.device, &stream))
+      return false;
+    Released released;
+    *status = g_select(at_of<float>(t.q), t.stride, t.q->size(0), (int)t.q->size(1), &t.pages, &summary, at_of<int32_t>(t.table),
+                       t.table->size(1), t.table->size(1), at_of<int32_t>(t.lengths), (int)first, (int)last,
+                       at_of<int32_t>(blocks), (int)blocks->size(2), flags, stream);
+    return true;
+  });
+}
+
+// attention_blocks(q, cache, page_table, lengths, blocks, out, scale, flags, stream)
+PyObject* attention_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return common_case([&](int* status) {
+    if (n != 9) return false;
+    Attended t;
+    if (!attended(a[0], a[1], a[2], a[3], &t)) return false;
+    const at::Tensor *blocks, *out = tensor(a[5]);
+    double scale;
+    int flags;
+    void* stream;
+    if (!listed(a[4], t, &blocks) || !fits(out, t.device, kF32, t.q->sizes()) || !scale_of(a[6], t.pages, &scale) ||
+        !flags_of(a[7], &flags) || !stream_of(a[8], t.device, &stream))
+      return false;
+    Released released;
+    *status = g_blocks(at_of<float>(t.q), t.stride, t.q->size(0), (int)t.q->size(1), &t.pages, at_of<int32_t>(t.table),
+                       t.table->size(1), t.table->size(1), at_of<int32_t>(t.lengths), at_of<int32_t>(blocks),
+                       (int)blocks->size(2), (float)scale, at_of<float>(out), t.stride, flags, stream);
+    return true;
+  });
+}
+
+// softmax(y, p, temperature, flags, stream)
+PyObject* softmax(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return common_case([&](int* status) {
+    if (n != 5) return false;
+    const at::Tensor *y = tensor(a[0]), *p = tensor(a[1]), *temperature = a[2] == Py_None ? nullptr : tensor(a[2]);
+    const int64_t d = device_of(y);
+    int flags;
+    void* stream;
+    if (d < 0 || !fits(y, d, kF32, 2) || !fits(p, d, kF32, y->sizes()) ||
+        (a[2] != Py_None && !fits(temperature, d, kF32, y->sizes().slice(0, 1))) || !flags_of(a[3], &flags) ||
+        !stream_of(a[4], d, &stream))
+      return false;
+    Released released;
+    *status = g_softmax(at_of<float>(y), y->size(0), y->size(1), at_of<float>(temperature), at_of<float>(p), flags, stream);
+    return true;
+  });
+}
+
+// verify(p, q, draft, uniform, tokens, accepted, flags, stream)
+PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return common_case([&](int* status) {
+    if (n != 8) return false;
+    const at::Tensor *p = tensor(a[0]), *q = tensor(a[1]), *draft = tensor(a[2]), *uniform = tensor(a[3]);
+    const at::Tensor *tokens = tensor(a[4]), *accepted = tensor(a[5]);
+    const int64_t d = device_of(p);
+    int flags;
+    void* stream;
+    if (d < 0 || !fits(p, d, kF32, 3) || p->size(1) < 2 || p->size(1) > 0x7fffffff) return false;
+    const int64_t B = p->size(0), K = p->size(1) - 1, rows[3] = {B, K, p->size(2)}, all[2] = {B, K + 1};
+    if (!fits(q, d, kF32, at::IntArrayRef(rows, 3)) || !fits(draft, d, kI32, at::IntArrayRef(rows, 2)) ||
+        !fits(uniform, d, kF32, at::IntArrayRef(all, 2)) || !fits(tokens, d, kI32, at::IntArrayRef(all, 2)) ||
+        !fits(accepted, d, kI32, at::IntArrayRef(rows, 1)) || !flags_of(a[6], &flags) || !stream_of(a[7], d, &stream))
+      return false;
+    Released released;
+    *status = g_verify(at_of<float>(p), at_of<float>(q), B, (int)K, p->size(2), at_of<int32_t>(draft), at_of<float>(uniform),
+                       at_of<int32_t>(tokens), at_of<int32_t>(accepted), flags, stream);
+    return true;
+  });
+}
+
+// bind_serving(attention_shared, kv_summarise, attention_select, attention_blocks, softmax, verify): their addresses.
+PyObject* bind_serving(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  long long at[6];
+  for (int i = 0; i < 6; ++i)
+    if (n != 6 || !integer(a[i], &at[i]) || !at[i]) {
+      PyErr_SetString(PyExc_ValueError, "bind_serving takes six addresses");
+      return nullptr;
+    }
+  g_shared = reinterpret_cast<decltype(g_shared)>(at[0]);
+  g_summarise = reinterpret_cast<decltype(g_summarise)>(at[1]);
+  g_select = reinterpret_cast<decltype(g_select)>(at[2]);
+  g_blocks = reinterpret_cast<decltype(g_blocks)>(at[3]);
+  g_softmax = reinterpret_cast<decltype(g_softmax)>(at[4]);
+  g_verify = reinterpret_cast<decltype(g_verify)>(at[5]);
+  Py_RETURN_NONE;
+}
+
 // bind(rope, kv_append, kv_read, attention): the addresses of the library's entry points.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   long long at[4];
@@ -288,6 +478,13 @@ PyMethodDef g_methods[] = {
     {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(kv_append)), METH_FASTCALL, nullptr},
     {"kv_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(kv_read)), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(attention)), METH_FASTCALL, nullptr},
+    {"bind_serving", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(bind_serving)), METH_FASTCALL, nullptr},
+    {"attention_shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(attention_shared)), METH_FASTCALL, nullptr},
+    {"kv_summarise", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(kv_summarise)), METH_FASTCALL, nullptr},
+    {"attention_select", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(attention_select)), METH_FASTCALL, nullptr},
+    {"attention_blocks", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(attention_blocks)), METH_FASTCALL, nullptr},
+    {"softmax", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(softmax)), METH_FASTCALL, nullptr},
+    {"verify", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(verify)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "bitlinear_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,462 @@
+// select.cu -- a cheap score for every page of a long sequence, and the pages that it chooses
+// ("Hesper.Models.BitNet" page, section "KV cache": attention reads all of it for each token;
+// over chosen pages it reads a fixed part).
+//
+// Summary of a page's keys for a head: per dim the least and the largest value, lo and hi, of
+// code * step (one fp32 product) over the tokens that are there, kept as int8 codes under one step,
+//   a = max(max_d |lo_d|, max_d |hi_d|, 1e-5), s = 127 / a, step = a / 127,
+//   lower_d = max(floor(lo_d s), -127), upper_d = min(ceil(hi_d s), 127),
+// rounded outwards.  Least and largest do not depend on an order, so neither does a summary.
+//
+// Score of a page for a q head: with q's codes c_d = rne(q_d (127 / max(max|q|, 1e-5))) as
+// activation_quant has them,
+//   acc = sum_d max(c_d lower_d, c_d upper_d) = sum_d max(c_d, 0) upper_d + min(c_d, 0) lower_d,
+// an exact whole number (dp4a), and score = (acc * step) * (max|q| / 127), two fp32 products: no key of the
+// page has a larger product with those codes.  A key head's score is the largest of its q heads'.
+#include <cuda_fp16.h>
+
+#include "serve.cuh"
+
+namespace bitlinear {
+namespace {
+
+constexpr float kLeastTop = 1e-5f;
+
+// ---------------------------------------------------------------- summaries
+
+constexpr int kSumThreads = 128;
+constexpr int kSumWarps = kSumThreads / 32;
+
+// 16 bytes of a row of codes as fp32 values, times the row's step.
+template <int FORMAT>
+__device__ __forceinline__ void widen16(uint4 w, float step, float (&x)[FORMAT == BITLINEAR_KV_BF16 ? 8 : 16]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (FORMAT == BITLINEAR_KV_BF16) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    } else if constexpr (FORMAT == BITLINEAR_KV_INT8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[4 * i + j] = __fmul_rn((float)((int)(u[i] << (24 - 8 * j)) >> 24), step);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t h = half2_of_e4m3x2((uint16_t)(u[i] >> (16 * j)));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        x[4 * i + 2 * j] = __fmul_rn(f.x, step);
+        x[4 * i + 2 * j + 1] = __fmul_rn(f.y, step);
+      }
+    }
+  }
+}
+
+struct SummariseArgs {
+  KvPages c;
+  Summary summary;
+  const int32_t *table, *first, *lengths;
+  int64_t table_stride, max_pages;
+  int shares;  // warps a key head of a sequence, each every shares-th of its pages
+};
+
+// A warp takes a page of a head: a lane 16 bytes of a row, as many rows a turn as fit.
+template <int FORMAT>
+__global__ void __launch_bounds__(kSumThreads) summarise_kernel(SummariseArgs a) {
+  constexpr int kDims = FORMAT == BITLINEAR_KV_BF16 ? 8 : 16;  // of a lane
+  constexpr int kBytes = FORMAT == BITLINEAR_KV_BF16 ? 2 : 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_release_dependents();
+  pdl_wait_primary();
+  const KvPages& c = a.c;
+  const uint32_t part = blockIdx.x * kSumWarps + warp;  // of the key head
+  const int hk = blockIdx.y;
+  const int64_t b = blockIdx.z;
+  if (part >= (uint32_t)a.shares) return;
+  const int D = c.head_dim, chunks = D / kDims, rows = 32 / chunks;  // rows a turn, 1 at least
+  const int row = lane / chunks, chunk = lane - row * chunks;
+  const int page_size = 1 << c.page_shift;
+  const int64_t length = max((int64_t)0, min((int64_t)a.lengths[b], a.max_pages << c.page_shift));
+  const int64_t begin = max(0, a.first[b]) >> c.page_shift, end = (length + page_size - 1) >> c.page_shift;
+  for (int64_t column = begin + part; column < end; column += a.shares) {
+    const int32_t page = a.table[b * a.table_stride + column];
+    if (page < 0 || page >= c.num_pages) continue;
+    const int here = (int)min((int64_t)page_size, length - (column << c.page_shift));
+    const int64_t head = (int64_t)page * c.heads + hk, first_row = head << c.page_shift;
+    const uint8_t* k = static_cast<const uint8_t*>(c.k) + first_row * D * kBytes + 16 * chunk;
+    const float* steps = FORMAT == BITLINEAR_KV_BF16 ? nullptr : c.k_step + first_row;
+    float lo[kDims], hi[kDims];
+#pragma unroll
+    for (int i = 0; i < kDims; ++i) {
+      lo[i] = INFINITY;
+      hi[i] = -INFINITY;
+    }
+    if (row < rows) {
+#pragma unroll 4
+      for (int t = row; t < here; t += rows) {
+        float x[kDims];
+        widen16<FORMAT>(__ldg(reinterpret_cast<const uint4*>(k + (int64_t)t * D * kBytes)), FORMAT == BITLINEAR_KV_BF16 ? 1.0f : __ldg(steps + t), x);
+#pragma unroll
+        for (int i = 0; i < kDims; ++i) {
+          lo[i] = fminf(lo[i], x[i]);
+          hi[i] = fmaxf(hi[i], x[i]);
+        }
+      }
+    }
+    // the rows of a turn meet in the first row's lanes
+    for (int r = 1; r < rows; ++r) {
+#pragma unroll
+      for (int i = 0; i < kDims; ++i) {
+        lo[i] = fminf(lo[i], __shfl_sync(kFullMask, lo[i], (chunk + r * chunks) & 31));
+        hi[i] = fmaxf(hi[i], __shfl_sync(kFullMask, hi[i], (chunk + r * chunks) & 31));
+      }
+    }
+    float top = kLeastTop;
+#pragma unroll
+    for (int i = 0; i < kDims; ++i) top = row == 0 ? fmaxf(top, fmaxf(fabsf(lo[i]), fabsf(hi[i]))) : top;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+    const float s = __fdiv_rn(127.0f, top);
+    if (row == 0) {
+      int8_t lower[kDims], upper[kDims];
+#pragma unroll
+      for (int i = 0; i < kDims; ++i) {
+        lower[i] = (int8_t)(int)fmaxf(floorf(__fmul_rn(lo[i], s)), -127.0f);
+        upper[i] = (int8_t)(int)fminf(ceilf(__fmul_rn(hi[i], s)), 127.0f);
+      }
+      int8_t* to = a.summary.bounds + head * 2 * D + kDims * chunk;
+      if constexpr (kDims == 16) {
+        *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(lower);
+        *reinterpret_cast<uint4*>(to + D) = *reinterpret_cast<const uint4*>(upper);
+      } else {
+        *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(lower);
+        *reinterpret_cast<uint2*>(to + D) = *reinterpret_cast<const uint2*>(upper);
+      }
+      if (chunk == 0) a.summary.step[head] = __fdiv_rn(top, 127.0f);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the choice
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kHeadsAtOnce = 16;  // q heads whose codes are in shared memory together
+constexpr int kMostCtas = 8;      // of a cluster
+constexpr int kDigits = 256;
+constexpr uint32_t kKept = 0xffffffffu, kAbsent = 0u;  // keys of pages that are chosen whatever their score, and that are none
+
+__device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void send32(uint32_t at, int rank, uint32_t v) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(r), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Larger scores have larger keys, between kAbsent and kKept; NaN has the least.
+__device__ __forceinline__ uint32_t key_of(float score) {
+  const uint32_t u = __float_as_uint(score + 0.0f);
+  if (score != score) return 1u;
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// A cluster chooses for one key head of one sequence.  Every CTA scores a run of the pages and keeps
+// their keys; the count-th largest key is found a byte at a time from histograms that all CTAs add up,
+// and each CTA writes its own chosen pages where those of the CTAs before it end.
+template <int CHUNKS>  // of 16 dims, at most
+__global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, KvPages c, Summary summary, int share) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
+  __shared__ __align__(16) int8_t codes[kHeadsAtOnce][2][CHUNKS * 16];  // parts below and above 0
+  __shared__ float steps[kHeadsAtOnce];
+  __shared__ uint32_t histogram[kMostCtas][kDigits];
+  __shared__ uint32_t counted[kMostCtas][2];
+  __shared__ uint32_t of_warps[kWarps][2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ctas = gridDim.x, rank = blockIdx.x;
+  pdl_release_dependents();
+  pdl_wait_primary();
+  const int64_t b = (int64_t)blockIdx.z, hk = blockIdx.y;
+  const int D = c.head_dim, chunks = D / 16, group = a.q_heads / c.heads;
+  const int64_t length = max((int64_t)0, min((int64_t)a.lengths[b], a.max_pages << c.page_shift));
+  const int pages = (int)((length + (1 << c.page_shift) - 1) >> c.page_shift);
+  // runs as short as the sequence allows
+  const int run = min(share, (pages + ctas - 1) / ctas), from = min(pages, rank * run), here = min(pages, from + run) - from;
+  const int32_t* table = a.table + b * a.table_stride;
+  int32_t* out = a.blocks + (b * c.heads + hk) * a.count;
+
+  for (int h0 = 0; h0 < group; h0 += kHeadsAtOnce) {
+    const int heads = min(kHeadsAtOnce, group - h0);
+    if (h0 > 0) __syncthreads();
+    for (int h = warp; h < heads; h += kWarps) {  // a warp quantises a head
+      const float* q = a.q + b * a.q_stride + (hk * group + h0 + h) * D;
+      float top = kLeastTop;
+      for (int d = lane; d < D; d += 32) top = fmaxf(top, fabsf(q[d]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+      const float s = __fdiv_rn(127.0f, top);
+      for (int d = lane; d < D; d += 32) {
+        const int code = max(-127, min(127, __float2int_rn(__fmul_rn(q[d], s))));
+        codes[h][0][d] = (int8_t)min(code, 0);
+        codes[h][1][d] = (int8_t)max(code, 0);
+      }
+      if (lane == 0) steps[h] = __fdiv_rn(top, 127.0f);
+    }
+    __syncthreads();
+    // two lanes a page: one the lower bounds, one the upper
+    for (int i0 = 0; i0 < here; i0 += kThreads / 2) {
+      const int i = i0 + threadIdx.x / 2, side = threadIdx.x & 1, column = from + i;
+      int32_t page = -1;
+      if (i < here) page = table[column];
+      const bool there = page >= 0 && page < c.num_pages;
+      const int64_t head = (int64_t)(there ? page : 0) * c.heads + hk;
+      uint4 w[CHUNKS];
+      const uint4* bounds = reinterpret_cast<const uint4*>(summary.bounds + (head * 2 + side) * D);
+#pragma unroll
+      for (int k = 0; k < CHUNKS; ++k) w[k] = there && k < chunks ? __ldg(bounds + k) : make_uint4(0, 0, 0, 0);
+      const float step = there ? __ldg(summary.step + head) : 0.0f;
+      float best = -INFINITY;
+      bool nan = false;
+      for (int h = 0; h < heads; ++h) {
+        int acc = 0;
+#pragma unroll
+        for (int k = 0; k < CHUNKS; ++k) {
+          if (k < chunks) {
+            const uint4 x = *reinterpret_cast<const uint4*>(&codes[h][side][16 * k]);
+            acc = __dp4a((int)w[k].x, (int)x.x, acc);
+            acc = __dp4a((int)w[k].y, (int)x.y, acc);
+            acc = __dp4a((int)w[k].z, (int)x.z, acc);
+            acc = __dp4a((int)w[k].w, (int)x.w, acc);
+          }
+        }
+        acc += __shfl_xor_sync(kFullMask, acc, 1);
+        const float score = __fmul_rn(__fmul_rn((float)acc, step), steps[h]);
+        nan |= score != score;
+        best = fmaxf(best, score);
+      }
+      if (i < here && side == 0) {
+        uint32_t key = nan ? 1u : key_of(best);
+        if (h0 > 0) key = keys[i] == 1u || key == 1u ? 1u : max(key, keys[i]);
+        if (h0 + heads >= group && (column < a.keep_first || column >= pages - a.keep_last)) key = kKept;
+        keys[i] = there ? key : kAbsent;
+      }
+    }
+  }
+  __syncthreads();
+  if (ctas > 1) cluster_meet();  // all of the cluster's CTAs have begun
+
+  // The count-th largest key: its bytes from the highest on.
+  uint32_t known = 0, mask = 0;  // the bytes found, and where they are
+  uint32_t wanted = a.count;     // still to be taken among keys that agree with `known`
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    uint32_t* mine = histogram[rank];
+    for (int i = threadIdx.x; i < kDigits; i += kThreads) mine[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < here; i += kThreads) {
+      const uint32_t k = keys[i];
+      if (k != kAbsent && (k & mask) == known) atomicAdd(&mine[(k >> shift) & 0xff], 1u);
+    }
+    __syncthreads();
+    if (ctas > 1) {
+      for (int r = 0; r < ctas; ++r)
+        if (r != rank)
+          for (int i = threadIdx.x; i < kDigits; i += kThreads) send32(smem_at(&histogram[rank][i]), r, mine[i]);
+      cluster_meet();
+    }
+    // every warp finds the byte for itself: a lane has 8 digits, the highest digits in lane 0
+    uint32_t n[8], all = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      n[i] = 0;
+      for (int r = 0; r < ctas; ++r) n[i] += histogram[r][kDigits - 1 - (8 * lane + i)];
+      all += n[i];
+    }
+    uint32_t upto = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(kFullMask, upto, o);
+      if (lane >= o) upto += x;
+    }
+    uint32_t above = upto - all, digit = 0;
+    const uint32_t has = __ballot_sync(kFullMask, wanted > above && wanted <= upto);
+    if (has == 0) {  // fewer keys than are wanted: all of them
+      known = 0;
+      mask = 0;
+      wanted = 0xffffffffu;
+      break;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (wanted > above && wanted <= above + n[i]) {
+        digit = kDigits - 1 - (8 * lane + i);
+        break;
+      }
+      above += n[i];
+    }
+    const int owner = __ffs(has) - 1;
+    digit = __shfl_sync(kFullMask, digit, owner);
+    wanted -= __shfl_sync(kFullMask, above, owner);
+    known |= digit << shift;
+    mask |= 0xffu << shift;
+    __syncthreads();  // the histograms are read
+    if (ctas > 1) cluster_meet();
+  }
+  const bool all_taken = wanted == 0xffffffffu;
+  // Chosen: keys above `known`, and the first `wanted` that equal it.
+  auto above_it = [&](uint32_t k) { return all_taken ? k != kAbsent : k > known; };
+  auto equals_it = [&](uint32_t k) { return !all_taken && k == known; };
+  uint32_t more = 0, equal = 0;
+  for (int i = threadIdx.x; i < here; i += kThreads) {
+    more += above_it(keys[i]);
+    equal += equals_it(keys[i]);
+  }
+  more = __reduce_add_sync(kFullMask, more);
+  equal = __reduce_add_sync(kFullMask, equal);
+  if (lane == 0) {
+    of_warps[warp][0] = more;
+    of_warps[warp][1] = equal;
+  }
+  __syncthreads();
+  more = equal = 0;
+  for (int i = 0; i < kWarps; ++i) {
+    more += of_warps[i][0];
+    equal += of_warps[i][1];
+  }
+  if (threadIdx.x < ctas) {
+    send32(smem_at(&counted[rank][0]), threadIdx.x, more);
+    send32(smem_at(&counted[rank][1]), threadIdx.x, equal);
+  }
+  if (ctas > 1)
+    cluster_meet();
+  else
+    __syncthreads();
+  uint32_t more_before = 0, equal_before = 0, more_all = 0, equal_all = 0;
+  for (int r = 0; r < ctas; ++r) {
+    if (r < rank) {
+      more_before += counted[r][0];
+      equal_before += counted[r][1];
+    }
+    more_all += counted[r][0];
+    equal_all += counted[r][1];
+  }
+  // Written in order, a block of threads at a time.
+  for (int i0 = 0; i0 < here; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    const uint32_t k = i < here ? keys[i] : kAbsent;
+    const uint32_t m = __ballot_sync(kFullMask, above_it(k)), e = __ballot_sync(kFullMask, equals_it(k));
+    __syncthreads();
+    if (lane == 0) {
+      of_warps[warp][0] = __popc(m);
+      of_warps[warp][1] = __popc(e);
+    }
+    __syncthreads();
+    const uint32_t below = (1u << lane) - 1;
+    uint32_t m_at = more_before + __popc(m & below), e_at = equal_before + __popc(e & below);
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) {
+        m_at += of_warps[w][0];
+        e_at += of_warps[w][1];
+      }
+      more_before += of_warps[w][0];
+      equal_before += of_warps[w][1];
+    }
+    const bool chosen = above_it(k) || (equals_it(k) && e_at < wanted);
+    if (chosen) out[m_at + min(e_at, all_taken ? 0u : wanted)] = from + i;
+  }
+  const uint32_t chosen = more_all + (all_taken ? 0u : min(equal_all, wanted));
+  if (rank == 0)
+    for (int i = chosen + threadIdx.x; i < a.count; i += kThreads) out[i] = -1;
+}
+
+}  // namespace
+
+cudaError_t launch_summarise(const KvPages& cache, const Summary& summary, const int32_t* table, int64_t table_stride,
+                             int64_t B, int64_t max_pages, const int32_t* first, const int32_t* lengths, bool pdl,
+                             const DeviceInfo& dev, cudaStream_t stream) {
+  // Warps in all: the GPU full once, a page a warp at least.
+  const int64_t most = (int64_t)dev.num_sms * 16, heads = B * cache.heads;
+  int64_t shares = (most + heads - 1) / heads;
+  if (shares > max_pages) shares = max_pages;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.blockDim = dim3(kSumThreads, 1, 1);
+  if (pdl) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+  }
+  const auto kernel = cache.format == BITLINEAR_KV_INT8  ? summarise_kernel<BITLINEAR_KV_INT8>
+                      : cache.format == BITLINEAR_KV_FP8 ? summarise_kernel<BITLINEAR_KV_FP8>
+                                                         : summarise_kernel<BITLINEAR_KV_BF16>;
+  constexpr int64_t kMostSeqs = 65535;
+  for (int64_t b = 0; b < B; b += kMostSeqs) {
+    const SummariseArgs a = {cache, summary, table + b * table_stride, first + b, lengths + b, table_stride, max_pages, (int)shares};
+    cfg.gridDim = dim3((unsigned)((shares + kSumWarps - 1) / kSumWarps), (unsigned)cache.heads, (unsigned)(B - b < kMostSeqs ? B - b : kMostSeqs));
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+template <int CHUNKS>
+static cudaError_t launch_select_chunks(SelectArgs a, const KvPages& cache, const Summary& summary, bool pdl,
+                                        const DeviceInfo& dev, cudaStream_t stream) {
+  constexpr int kMostShare = 24576;  // pages a CTA: 96 KB of keys
+  const int64_t heads = a.B * cache.heads;
+  int ctas = 1;
+  while (ctas < kMostCtas && (a.max_pages > (int64_t)ctas * kMostShare ||
+                              (a.max_pages > (int64_t)ctas * kThreads / 2 && heads * ctas * 2 <= 4 * dev.num_sms)))
+    ctas *= 2;
+  const int share = (int)((a.max_pages + ctas - 1) / ctas);
+  const auto kernel = select_kernel<CHUNKS>;
+  static thread_local int configured_device = -1;
+  if (configured_device != dev.device) {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShare * 4);
+    if (err != cudaSuccess) return err;
+    configured_device = dev.device;
+  }
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)share * 4;
+  if (ctas > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+  }
+  if (pdl) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  constexpr int64_t kMostSeqs = 65535;
+  const int64_t B = a.B;
+  for (int64_t b = 0; b < B; b += kMostSeqs) {
+    SelectArgs part = a;
+    part.q += b * a.q_stride;
+    part.table += b * a.table_stride;
+    part.lengths += b;
+    part.blocks += b * cache.heads * a.count;
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)cache.heads, (unsigned)(B - b < kMostSeqs ? B - b : kMostSeqs));
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, part, cache, summary, share);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_select(const SelectArgs& a, const KvPages& cache, const Summary& summary, bool pdl,
+                          const DeviceInfo& dev, cudaStream_t stream) {
+  if (cache.head_dim <= 80) return launch_select_chunks<5>(a, cache, summary, pdl, dev, stream);
+  if (cache.head_dim <= 128) return launch_select_chunks<8>(a, cache, summary, pdl, dev, stream);
+  return launch_select_chunks<16>(a, cache, summary, pdl, dev, stream);
+}
+
+}  // namespace bitlinear

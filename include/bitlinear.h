@@ -524,6 +524,129 @@ bitlinear_status bitlinear_attention(const float* q, int64_t q_stride, int64_t B
                                      int64_t window, float scale, float* out, int64_t out_stride,
                                      void* workspace, size_t workspace_bytes, int flags, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * What a serving step needs beyond one independent token a sequence: rows that
+ * share a prefix, a part of a long context, and several drafted tokens at once.
+ * ------------------------------------------------------------------------- */
+
+/* Workspace bytes of bitlinear_attention_shared (0 where it needs none, and for sizes out
+ * of range).  A function of these sizes alone. */
+size_t bitlinear_attention_shared_workspace(int64_t B, int num_q_heads, int num_kv_heads, int head_dim,
+                                            int64_t num_groups);
+
+/* bitlinear_attention (without a window) of rows that share their first tokens in groups: a
+ * system prompt or a document behind which each row has tokens of its own, or a sequence
+ * that several drafted tokens go on from.  Rows b of group g are g * R .. (g + 1) * R - 1, R =
+ * B / num_groups; the first shared[g] tokens of their sequences are read, and multiplied, once for
+ * all of them.
+ *   page_table, lengths  as for bitlinear_attention: each row's own table and whole length,
+ *              shared tokens included.  The tables of a group's rows name the same pages for its
+ *              shared tokens; where they do not, which row's are read is unspecified.
+ *   shared     device int32 [num_groups]; 0 or below: none.  A row shorter than that attends to its
+ *              own lengths[b] tokens alone, so the rows of drafted tokens (lengths n + 1, n + 2, ...,
+ *              one page list) may share everything: shared[g] the longest.
+ *   num_groups a divisor of B.  B * num_q_heads < 2^31.
+ *   workspace  as for bitlinear_attention, at least bitlinear_attention_shared_workspace() bytes; NULL
+ *              only where that is 0 or num_groups == B.
+ * Every other argument, and results, as for bitlinear_attention; a NaN or an infinity in a shared token
+ * that counts for one of a group's rows may reach each of them.  Nothing past the longest row
+ * of a group is read.  Results do not depend on timing.
+ * Errors: as bitlinear_attention. */
+bitlinear_status bitlinear_attention_shared(const float* q, int64_t q_stride, int64_t B, int num_q_heads,
+                                            const bitlinear_kv_pages* cache, const int32_t* page_table,
+                                            int64_t table_stride, int64_t max_pages, const int32_t* lengths,
+                                            const int32_t* shared, int64_t num_groups, float scale, float* out,
+                                            int64_t out_stride, void* workspace, size_t workspace_bytes, int flags,
+                                            void* stream);
+
+/* Bounds of the keys of every page of a cache, in caller-owned device memory. */
+typedef struct bitlinear_kv_summary {
+  int8_t* bounds; /* device [num_pages, num_heads, 2, head_dim]: lower, then upper; 16-byte aligned */
+  float* step;    /* device fp32 [num_pages, num_heads], 16-byte aligned: a bound is code * step */
+} bitlinear_kv_summary;
+
+/* Writes the summaries of the pages that hold the tokens first[b] <= t < lengths[b] of B sequences:
+ * first 0 for a prompt, lengths - 1 for the token that a decode step has just appended.
+ * With lo_d and hi_d the least and largest of dim d over the page's tokens before lengths[b] (each the fp32
+ * product code * step of the cache): a = max(max_d |lo_d|, max_d |hi_d|, 1e-5), s = 127 / a, step = a / 127,
+ *   lower_d = max(floor(lo_d * s), -127), upper_d = min(ceil(hi_d * s), 127), every step in fp32.
+ * Pages out of range and those of other tokens stay as they were; a page that two sequences name is
+ * either's.  Keys that are not finite give unspecified bounds of their page and head.
+ *   B >= 0 (0 enqueues nothing); page_table: B rows, as for bitlinear_attention; first, lengths device
+ *   int32 [B].
+ * Errors: BITLINEAR_ERR_NULL, BITLINEAR_ERR_SHAPE, BITLINEAR_ERR_ALIGN, BITLINEAR_ERR_UNSUPPORTED,
+ * BITLINEAR_ERR_CUDA. */
+bitlinear_status bitlinear_kv_summarise(const bitlinear_kv_pages* cache, const bitlinear_kv_summary* summary,
+                                        const int32_t* page_table, int64_t table_stride, int64_t B, int64_t max_pages,
+                                        const int32_t* first, const int32_t* lengths, int flags, void* stream);
+
+/* Chooses pages of each sequence for each key head by a cheap score.  With c = q's codes, as
+ * bitlinear_quant_act takes them (c_d = rne(q_d * (127 / m)), m = max(max|q|, 1e-5)), the score of page j for a q head is
+ *   (acc * step_j) * (m / 127),  acc = sum_d max(c_d lower_d, c_d upper_d) (exact),
+ * two fp32 products: no key of the page has a larger product with those codes (for scale > 0).  A key
+ * head's score is the largest of its q heads'.
+ *   cache      gives num_pages, num_heads, page_size and head_dim; its pointers are checked, its
+ *              codes not read.
+ *   keep_first, keep_last  pages at the sequence's start and end that are chosen whatever their score, >= 0.
+ *   blocks     device int32 [B, num_heads, count], written: the columns of the page table that are chosen, in
+ *              order, then -1.  A page whose number is out of range is not chosen; of equal scores the
+ *              earlier page is; a score that is NaN comes last.
+ *   count      1 .. 4096.
+ *   max_pages  at most 131072 (BITLINEAR_ERR_UNSUPPORTED beyond).
+ * lengths, page_table, q, B: as for bitlinear_attention.  Errors: as bitlinear_kv_summarise. */
+bitlinear_status bitlinear_attention_select(const float* q, int64_t q_stride, int64_t B, int num_q_heads,
+                                            const bitlinear_kv_pages* cache, const bitlinear_kv_summary* summary,
+                                            const int32_t* page_table, int64_t table_stride, int64_t max_pages,
+                                            const int32_t* lengths, int keep_first, int keep_last, int32_t* blocks,
+                                            int count, int flags, void* stream);
+
+/* bitlinear_attention over the tokens t < lengths[b] of the pages that a list names for each key
+ * head, in place of all tokens.
+ *   blocks     device int32 [B, num_heads, count]: columns of the page table, in any order; one below 0, past
+ *              max_pages, or past the row's length is none (a row of zeros where all are), one that is listed twice
+ *              counts twice.
+ *   count      1 .. 4096.
+ * Every other argument as for bitlinear_attention; no workspace.  Results do not depend on timing.
+ * Errors: as bitlinear_attention. */
+bitlinear_status bitlinear_attention_blocks(const float* q, int64_t q_stride, int64_t B, int num_q_heads,
+                                            const bitlinear_kv_pages* cache, const int32_t* page_table,
+                                            int64_t table_stride, int64_t max_pages, const int32_t* lengths,
+                                            const int32_t* blocks, int count, float scale, float* out,
+                                            int64_t out_stride, int flags, void* stream);
+
+/* Probabilities of logits: p[m, n] = exp(y[m, n] / T_m) / sum over n.
+ *   y, p         device, fp32 [M, N] row-major; p may be y, and must not overlap it otherwise.
+ *   M, N         M >= 0 (0 enqueues nothing), 1 <= N < 2^31, M * N <= 2^48.
+ *   temperature  device fp32 [M], or NULL (1 everywhere).  One that is not at least 1e-30 (0, for instance) gives 1 at
+ *                the row's first maximum (bitlinear_argmax's) and 0 elsewhere; one above 1e30 counts as that.
+ * A logit of -infinity has no probability; a row of them is a row of zeros.  With a temperature that is at
+ * least 1e-30, a NaN or +infinity in a row gives a row of NaN.
+ * Errors: BITLINEAR_ERR_NULL, BITLINEAR_ERR_SHAPE, BITLINEAR_ERR_ALIGN (y, p 16 bytes, temperature 4),
+ * BITLINEAR_ERR_UNSUPPORTED (flag), BITLINEAR_ERR_CUDA. */
+bitlinear_status bitlinear_softmax(const float* y, int64_t M, int64_t N, const float* temperature, float* p, int flags,
+                                   void* stream);
+
+/* Verifies drafted tokens against the target's probabilities, with random numbers that the caller
+ * gives, so that the tokens are distributed as if the target had drawn each of them.
+ *   p          device, fp32 [B, K + 1, N], K = num_drafts: the target's probabilities after each of the drafted tokens
+ *              (bitlinear_softmax), row i those of the token that draft i stands for.
+ *   q          device, fp32 [B, K, N]: the probabilities that the drafts were drawn from (NULL where K == 0).
+ *   draft      device int32 [B, K]; the first that is below 0 or at least N ends a sequence's drafts.
+ *   uniform    device fp32 [B, K + 1], each in [0, 1): one for each draft, the last for the token that is drawn.
+ *   tokens     device int32 [B, K + 1], written: the drafts taken, the token drawn, then -1.
+ *   accepted   device int32 [B], written: how many drafts are taken.
+ * Draft x at i is taken, after all before it, if uniform_i * q_i(x) < p_i(x) (exactly).  The next token
+ * is drawn from the weights max(p_i - q_i, 0) (one fp32 subtraction) at the first i that is refused, from p_i where the
+ * drafts end, and from p_i too where those weights are 0 everywhere: the first token at which the sum of weights so
+ * far is above uniform_K times their sum, each weight counted as a whole number of 2^-s, s = 62 - ceil(log2 N) (to
+ * the nearest, ties to even; NaN and what is below 0 as 0, what is above 2 as 2), the sums exact.  -1 where p_i has no
+ * weight either.  A uniform number outside [0, 1) counts as the nearest inside in the draw, and NaN as 0.
+ *   B >= 0 (0 enqueues nothing), 0 <= K <= 65535, 1 <= N < 2^31.  K == 0 draws a token a sequence.
+ * Errors: as bitlinear_softmax. */
+bitlinear_status bitlinear_verify(const float* p, const float* q, int64_t B, int num_drafts, int64_t N,
+                                  const int32_t* draft, const float* uniform, int32_t* tokens, int32_t* accepted,
+                                  int flags, void* stream);
+
 /* Exercises the failure-detection path without faulting anything: launches a
  * one-warp kernel that waits on an mbarrier nothing ever arrives on, with the
  * same bounded wait the kernels use, giving up after limit_ns (0 < limit_ns
