@@ -34,7 +34,7 @@ NVCC_FLAGS = ARCH + [
     "-I", INCLUDE, "-I", CSRC,
 ]
 SOURCES = ["abi.cu", "wquant.cu", "aquant.cu", "decode.cu", "prefill.cu", "wide.cu", "argmax.cu",
-           "rope_kv.cu", "attention.cu", "attention_blocks.cu", "attention_shared.cu", "select.cu", "sample.cu"]
+           "rope_kv.cu", "attention.cu", "attention_blocks.cu", "attention_shared.cu", "attention_prefix.cu", "select.cu", "sample.cu"]
 
 
 def _nvcc() -> str:

@@ -358,7 +358,9 @@ struct Shares {
   const int32_t* shared;
   const int32_t* lengths;
   int heads_a_key;
-  int prefix_tiles;  // kPrefix's rows a key head of a group
+  int prefix_tiles;  // rows a key head of a group, of
+  int prefix_heads;  // so many q heads, and
+  int slot_heads;    // their places in a part
 };
 
 // Tokens first <= t < len of a sequence that count, in steps of T from first / T on.
@@ -383,7 +385,7 @@ struct Part {
   int row, part, parts;  // parts == 0: the CTA has nothing
 };
 template <int T>
-__device__ __forceinline__ Part find_part(const AttendArgs& a, int64_t most, int rows_a_seq) {
+__device__ __forceinline__ Part find_part(const AttendArgs& a, int64_t most, int rows_a_seq, int least = kLeastSteps * kWarps) {
   const int lane = threadIdx.x & 31, here = blockIdx.x;
   const int each = ((int)a.B + 31) / 32, from = min((int)a.B, lane * each), to = min((int)a.B, from + each);
   auto steps_of = [&](int b) { return Span<T>(a.lengths[b], most, a.window).steps(); };
@@ -395,7 +397,7 @@ __device__ __forceinline__ Part find_part(const AttendArgs& a, int64_t most, int
   }
   const int total = __reduce_add_sync(kFullMask, steps) * rows_a_seq, rows = __reduce_add_sync(kFullMask, some) * rows_a_seq;
   const int spare = (int)gridDim.x - rows;  // > 0: the host takes this path for rows well below the grid
-  const int share = share_of_steps(total, spare, kLeastSteps * kWarps);
+  const int share = share_of_steps(total, spare, least);
   auto parts_of = [&](int b) { return (steps_of(b) + share - 1) / share; };
   int ctas = 0;
   for (int b = from; b < to; ++b) ctas += parts_of(b) * rows_a_seq;
@@ -446,11 +448,12 @@ __device__ __forceinline__ void add_prefix(const AttendArgs& a, const KvPages& c
   const int64_t g = b / sh.group_rows;
   const int member = (int)(b - g * sh.group_rows), D = c.head_dim;
   if (sh.shared[g] <= 0) return;  // then no CTA had the group's rows
-  const int rows = min(kRowHeads, sh.group_rows * sh.heads_a_key);
+  const int rows = sh.slot_heads;
   for (int h = 0; h < heads; ++h) {
     const int of_group = member * sh.heads_a_key + first_head + h;
-    const int2 row = sh.rows[(g * c.heads + hk) * sh.prefix_tiles + of_group / kRowHeads];
-    const float* p = sh.parts + ((int64_t)row.x * rows + of_group % kRowHeads) * (D + 4);
+    const int tile = of_group / sh.prefix_heads;
+    const int2 row = sh.rows[(g * c.heads + hk) * sh.prefix_tiles + tile];
+    const float* p = sh.parts + ((int64_t)row.x * rows + of_group - tile * sh.prefix_heads) * (D + 4);
     const uint32_t mine = at + h * PARTIAL;
     constexpr int kTurns = (DT + 127) / 128;  // of 4 dims a lane
     const float2 own = lds_float2(mine + 4 * DT);

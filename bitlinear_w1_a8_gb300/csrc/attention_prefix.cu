@@ -1,0 +1,697 @@
+// attention_prefix.cu -- the tokens that many rows share, on the fifth-generation tensor cores.
+//
+// A row of work is 128 q heads (all of a group's rows' for one key head, or 128 of them) and a run
+// of the group's shared tokens, in tiles of 128:
+//   S = Q K^T (TMEM), P = 2^(S - ref) in registers, back to TMEM as the next product's A operand, O = P V (TMEM).
+// fp32 accuracy takes two MMAs for one: q and the weights are split into two fp16 parts (22 bits), codes are exact
+// in fp16.  q's row is scaled to 2^13 .. 2^14 and the weights to at most 2^15, so that what a leading part
+// leaves is still a whole fp16 (its last place 2^-38 of the row's largest q, 2^-36 of the largest weight) and
+// both parts add up in one accumulator, the small ones first.  bf16 values become fp16 under a power
+// of two that a tile of 128 tokens has in common (below): those above 2^-22 of the tile's largest are exact.
+// Each tile's O starts from zero and is added to fp32 sums in registers: the tensor cores' adder cuts toward
+// zero, and a chain of tiles in it would show.
+//
+// 16 warps: two groups of four that turn logits into weights and add up O, each for every other tile with a reference
+// and sums of its own (a thread is a row: nothing is exchanged until the end); four that bring K and V,
+// widen the codes and lay them out for the MMA (128-byte swizzle, the same image for both: K is the B
+// operand along its rows, V across them); one that looks pages up, eight tiles ahead, and
+// asks for them to come into L2; one thread that issues the products of S and one that issues those of O.
+// Two S, two O, two K and two V are in flight; a weight overwrites its logit's place.
+#include "attend.cuh"
+#include "serve.cuh"
+#include "tc_util.cuh"
+
+namespace bitlinear {
+namespace {
+
+constexpr int kRows = kPrefixWide;      // q heads of a CTA: the MMA's rows
+constexpr int kTile = 128;              // tokens
+constexpr int kWideThreads = 512;
+constexpr int kEntries = 8;             // tiles whose pages and steps are known
+constexpr int kPanel = 128 * 128;       // bytes of 128 rows of 64 fp16 values
+constexpr float kTarget = 12.0f, kMost = 15.0f;  // log2 of the largest weight: where the reference puts it, what moves it
+constexpr int kAddRegisters = 184, kBringRegisters = 104, kIssueRegisters = 40;
+static_assert(2 * 128 * kAddRegisters + 128 * kBringRegisters + 128 * kIssueRegisters <= 65536, "the registers that 512 threads of 128 have");
+
+template <int FORMAT, int DT>
+struct Wide {
+  static constexpr bool kBf16 = FORMAT == BITLINEAR_KV_BF16;
+  static constexpr int kBytes = kBf16 ? 2 : 1;
+  static constexpr int kPanels = (DT + 63) / 64;
+  static constexpr int kOperand = kPanels * kPanel;
+  static constexpr int kLanes = 8 * kBytes;            // lanes of a token's row, 16 bytes each
+  static constexpr int kPieces = DT * kBytes / 16;     // of them that a row fills
+  static constexpr int kTurn = 128 / kLanes;           // tokens that 128 threads bring at once
+  static constexpr int kBatch = 8;                     // turns that a thread holds at once
+  static constexpr int kBatches = kTile / (kTurn * kBatch);
+  static constexpr int kSmem = 6 * kOperand + 1024;    // Q's parts, two K, two V; the base is rounded up to 1024
+};
+
+struct Entry {
+  int64_t row[kTile / 16];  // of each 16 tokens: ((page * heads) + head) * page_size + offset, or -1
+};
+
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+// The B operand across its rows (N along the row): panels of 64 columns a panel apart, 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t across_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)(kPanel >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+// After the wait: the registers of earlier loads are used behind it.
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ float4 lds_float4(uint32_t a) {
+  const uint4 w = lds128(a);
+  return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+}
+// Two values as the leading fp16 parts and what they leave, both whole.
+__device__ __forceinline__ void parts_of(float2 w, uint32_t& lead, uint32_t& rest) {
+  const __half2 h = __floats2half2_rn(w.x, w.y);
+  const float2 d = fma2(__half22float2(h), both(-1.0f), w);  // exact
+  const __half2 r = __floats2half2_rn(d.x, d.y);
+  lead = *reinterpret_cast<const uint32_t*>(&h);
+  rest = *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t of_panel(int row, int dim) {  // where a 16-byte piece (8 dims) of an operand is
+  return (uint32_t)((dim >> 6) * kPanel + row * 128 + ((((dim >> 3) & 7) ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ uint4 load16(const void* p) {  // in its place among the stores
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// The bounded wait of tc_util.cuh, inlined whole: a call has no place where warps' registers differ.
+__device__ __forceinline__ bool wait_bounded(unsigned long long* bar, uint32_t parity, int* abort_flag, int* status) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = tc::global_timer();
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0u) {
+      if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
+      if (tc::global_timer() - t0 > tc::kTimeoutNs) {
+        atomicExch(abort_flag, 1);
+        atomicExch(status, (int)BITLINEAR_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// Waits, with the same limit, for what this thread has issued, also after others have given up.
+__device__ __forceinline__ void drain(unsigned long long* bar, int* status) {
+  const unsigned long long t0 = tc::global_timer();
+#pragma unroll 1
+  for (uint32_t i = 0; !tc::mbar_try_wait(bar, 0); ++i) {
+    if ((i & 63u) == 63u && tc::global_timer() - t0 > tc::kTimeoutNs) {
+      atomicExch(status, (int)BITLINEAR_ERR_TIMEOUT);
+      return;
+    }
+  }
+}
+
+template <int FORMAT, int DT>
+__global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs a, KvPages c, Shares sh, int* status) {
+  using W = Wide<FORMAT, DT>;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(16) float k_steps[kEntries][W::kBf16 ? 4 : kTile], v_steps[kEntries][W::kBf16 ? 4 : kTile];
+  __shared__ __align__(16) float v_most[kEntries][4];
+  __shared__ __align__(16) Entry entries[kEntries];
+  __shared__ uint32_t entry_ok[kEntries];
+  __shared__ float row_tops[2][kRows];
+  __shared__ uint32_t tops[2][4];
+  __shared__ __align__(8) unsigned long long meta_full[kEntries], meta_empty[kEntries], k_full[2], k_empty[2], v_full[2], v_empty[2],
+      s_full[2], p_full[2], o_full[2], q_full, drained[2];
+  __shared__ uint32_t tmem_at;
+  __shared__ int abort_flag;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = c.head_dim;
+  const uint32_t base = ((uint32_t)__cvta_generic_to_shared(raw) + 1023u) & ~1023u;
+  const uint32_t q_at = base, k_at = base + 2 * W::kOperand, v_at = base + 4 * W::kOperand;
+
+  pdl_wait_primary();
+  pdl_release_dependents();
+  // The CTA's row of work: group b, key head and tile of q heads `row`, and its run of tiles.
+  const int64_t most = a.max_pages << c.page_shift;
+  int64_t b;
+  int row, part, parts;
+  if (sh.splits == 0) {
+    const Part p = find_part<kTile>(a, most, sh.rows_a_seq, 1);
+    if (p.parts == 0) return;
+    b = p.b;
+    row = p.row;
+    part = p.part;
+    parts = p.parts;
+  } else {
+    b = blockIdx.x / (uint32_t)sh.rows_a_seq;
+    row = blockIdx.x - (uint32_t)b * sh.rows_a_seq;
+    part = 0;
+    parts = 1;
+  }
+  if (part == 0 && threadIdx.x == 0) sh.rows[b * sh.rows_a_seq + row] = make_int2(blockIdx.x, parts);
+  const int hk = row / sh.groups, first_head = (row - hk * sh.groups) * kRows, heads = min(kRows, sh.group - first_head);
+  uint32_t len;
+  {
+    int longest = 0;
+    for (int i = lane; i < sh.group_rows; i += 32) longest = max(longest, sh.lengths[b * sh.group_rows + i]);
+    const Span<kTile> span(a.lengths[b], most, 0);
+    len = min(span.len, (uint32_t)__reduce_max_sync(kFullMask, longest));
+    const int steps = span.steps();  // shared out by what the group may share, whatever its rows have of it
+    const int each = (steps + parts - 1) / parts;
+    part *= each;
+    parts = min(steps, part + each);
+  }
+  const uint32_t begin = (uint32_t)part * kTile;
+  const int tiles = max(0, min(parts, (int)((len + kTile - 1) / kTile)) - part);
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < kEntries; ++i) {
+      tc::mbar_init(&meta_full[i], 1);
+      tc::mbar_init(&meta_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&k_full[i], 4);
+      tc::mbar_init(&v_full[i], 4);
+      tc::mbar_init(&p_full[i], 4);
+      tc::mbar_init(&k_empty[i], 1);
+      tc::mbar_init(&v_empty[i], 1);
+      tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&o_full[i], 1);
+      tc::mbar_init(&drained[i], 1);
+    }
+    tc::mbar_init(&q_full, 8);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) tc::tmem_alloc(&tmem_at, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  auto s_of = [&](int par) { return tmem + par * 128; };
+  auto o_of = [&](int par) { return tmem + 256 + par * 128; };
+
+  // Every role runs through all of its tiles, also after a wait has run out (`alive` false): it then
+  // waits and reads no more, and still arrives wherever others count it.
+  bool alive = true;
+  auto wait = [&](unsigned long long* bar, int phase) { alive = alive && wait_bounded(bar, phase & 1, &abort_flag, status); };
+
+  if (warp < 8) {
+    // ------------------------------------------------------- logits to weights, sums
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegisters));
+    const int par = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's lanes of TMEM
+    const bool there = r < heads;
+    const uint32_t of_group = first_head + (there ? r : 0), member = of_group / (uint32_t)sh.heads_a_key;
+    const int64_t seq = b * sh.group_rows + member;
+    // q's row: the two groups take half of its dims each
+    float row_scale = 0.0f;
+    {
+      const float* q = a.q + seq * a.q_stride + (int64_t)(hk * sh.heads_a_key + (of_group - member * sh.heads_a_key)) * D + par * (DT / 2);
+      const float factor = a.factor, more = a.factor_rest;
+      constexpr int kHalf = DT / 2;
+      float2 x[kHalf / 2];
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kHalf / 4; ++i) {
+        const float4 w = there && par * kHalf + 4 * i < D ? *reinterpret_cast<const float4*>(q + 4 * i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        x[2 * i] = mul2(make_float2(w.x, w.y), both(factor));
+        x[2 * i + 1] = mul2(make_float2(w.z, w.w), both(factor));
+        top = fmaxf(fmaxf(top, fmaxf(fabsf(x[2 * i].x), fabsf(x[2 * i].y))), fmaxf(fabsf(x[2 * i + 1].x), fabsf(x[2 * i + 1].y)));
+      }
+      row_tops[par][r] = top;
+      tc::named_bar_sync(1, 256);
+      const int e = clamp_exponent(exponent_of(fmaxf(top, row_tops[1 - par][r])));
+      const float2 up = both(power2(13 - e)), rest_up = both(power2(13 - e) * more);
+      row_scale = power2(e - 13);
+#pragma unroll
+      for (int i = 0; i < kHalf / 8; ++i) {
+        uint4 lead, rest;
+        uint32_t* l[4] = {&lead.x, &lead.y, &lead.z, &lead.w};
+        uint32_t* s[4] = {&rest.x, &rest.y, &rest.z, &rest.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 v = mul2(x[4 * i + j], up);
+          const __half2 h = __floats2half2_rn(v.x, v.y);
+          const float2 d = fma2(x[4 * i + j], rest_up, fma2(__half22float2(h), both(-1.0f), v));
+          const __half2 g = __floats2half2_rn(d.x, d.y);
+          *l[j] = *reinterpret_cast<const uint32_t*>(&h);
+          *s[j] = *reinterpret_cast<const uint32_t*>(&g);
+        }
+        const uint32_t at = q_at + of_panel(r, par * kHalf + 8 * i);
+        tc::st_shared_v4(at, lead.x, lead.y, lead.z, lead.w);
+        tc::st_shared_v4(at + W::kOperand, rest.x, rest.y, rest.z, rest.w);
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&q_full);
+    }
+    const bool none = (warp & 3) * 32 >= heads;  // rows of no q head: whatever comes of them is theirs
+    const uint32_t row_end = there ? min(len, (uint32_t)max(0, sh.lengths[seq])) : 0u;
+
+    float ref = kUnset;
+    float2 sums = both(0.0f);
+    float2 out[DT / 2];
+#pragma unroll
+    for (int i = 0; i < DT / 2; ++i) out[i] = both(0.0f);
+
+#pragma unroll 1
+    for (int n = par; n < tiles; n += 2) {
+      const int entry = n % kEntries;
+      const uint32_t t0 = begin + n * kTile;
+      wait(&s_full[par], n >> 1);
+      if constexpr (W::kBf16) wait(&v_full[par], n >> 1);  // the values' power of two
+      if (none) {
+        if (lane == 0) {
+          tc::mbar_arrive(&p_full[par]);
+          tc::mbar_arrive(&meta_empty[entry]);
+        }
+        wait(&o_full[par], n >> 1);
+        continue;
+      }
+      tc::tc_fence_after();
+      const uint32_t s_at = s_of(par) + lanes;
+      // the columns that count: all of them, or the first `count` of those 16 whose page is there
+      const uint32_t ok = alive ? entry_ok[entry] : 0u;
+      const int count = row_end > t0 ? (int)min((uint32_t)kTile, row_end - t0) : 0;
+      const bool whole = __all_sync(kFullMask, ok == 0xffu && count == kTile);
+      const uint32_t ks = (uint32_t)__cvta_generic_to_shared(k_steps[entry]), vs = (uint32_t)__cvta_generic_to_shared(v_steps[entry]);
+      const float4 vm = lds_float4((uint32_t)__cvta_generic_to_shared(v_most[entry]));
+      const float v_top = at_least(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), kLeastStep);
+      float unit = row_scale;
+      if constexpr (W::kBf16) unit = fmaxf(unit * k_steps[entry][0], 1.1754944e-38f);  // a masked logit times 0 is none
+      // the row's largest logit
+      float top = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < kTile / 16; ++g) {
+        uint32_t s[16];
+        tmem_load16(s_at + 16 * g, s);
+        tmem_loaded(s);
+        const int here = (ok >> g) & 1u ? count - 16 * g : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 x = make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
+          float2 y = make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
+          if constexpr (!W::kBf16) {
+            const float4 k = lds_float4(ks + (16 * g + 4 * i) * 4);
+            x = mul2(x, make_float2(k.x, k.y));
+            y = mul2(y, make_float2(k.z, k.w));
+          }
+          if (!whole) {
+            if (4 * i >= here) x.x = -INFINITY;
+            if (4 * i + 1 >= here) x.y = -INFINITY;
+            if (4 * i + 2 >= here) y.x = -INFINITY;
+            if (4 * i + 3 >= here) y.y = -INFINITY;
+          }
+          top = fmaxf(top, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
+        }
+      }
+      top = top * unit + log2_of(v_top);  // of a weight
+      if (top > ref + kMost) {
+        const float next = top - kTarget, down = exp2_of(ref - next);  // 0 from the first reference
+        ref = next;
+        sums = mul2(sums, both(down));
+#pragma unroll
+        for (int i = 0; i < DT / 2; ++i) out[i] = mul2(out[i], both(down));
+      }
+      float2 more = both(0.0f);
+#pragma unroll
+      for (int g = 0; g < kTile / 16; ++g) {
+        uint32_t s[16], w[16];
+        tmem_load16(s_at + 16 * g, s);
+        tmem_loaded(s);
+        const int here = (ok >> g) & 1u ? count - 16 * g : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 x = make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
+          float2 y = make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
+          if constexpr (!W::kBf16) {
+            const float4 k = lds_float4(ks + (16 * g + 4 * i) * 4);
+            x = mul2(x, make_float2(k.x, k.y));
+            y = mul2(y, make_float2(k.z, k.w));
+          }
+          if (!whole) {
+            if (4 * i >= here) x.x = -INFINITY;
+            if (4 * i + 1 >= here) x.y = -INFINITY;
+            if (4 * i + 2 >= here) y.x = -INFINITY;
+            if (4 * i + 3 >= here) y.y = -INFINITY;
+          }
+          x = fma2(x, both(unit), both(-ref));
+          y = fma2(y, both(unit), both(-ref));
+          x = make_float2(exp2_of(x.x), exp2_of(x.y));
+          y = make_float2(exp2_of(y.x), exp2_of(y.y));
+          more = add2(more, add2(x, y));
+          if constexpr (W::kBf16) {
+            x = mul2(x, both(v_top));
+            y = mul2(y, both(v_top));
+          } else {
+            const float4 v = lds_float4(vs + (16 * g + 4 * i) * 4);
+            x = mul2(x, make_float2(v.x, v.y));
+            y = mul2(y, make_float2(v.z, v.w));
+          }
+          parts_of(x, w[2 * i], w[8 + 2 * i]);
+          parts_of(y, w[2 * i + 1], w[8 + 2 * i + 1]);
+        }
+        tc::tmem_st16(s_at + 16 * g, w);
+      }
+      tc::tmem_st_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&p_full[par]);
+        tc::mbar_arrive(&meta_empty[entry]);
+      }
+      sums = add2(sums, more);
+      wait(&o_full[par], n >> 1);
+      tc::tc_fence_after();
+#pragma unroll
+      for (int g = 0; g < DT / 16; ++g) {
+        uint32_t o[16];
+        tmem_load16(o_of(par) + lanes + 16 * g, o);
+        tmem_loaded(o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          out[8 * g + i] = add2(out[8 * g + i], make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])));
+      }
+    }
+    // The two groups' sums meet in what was K's and V's place: [dim][row], 129 apart, then references and sums.
+    float sum = sums.x + sums.y;
+    constexpr int kApart = kRows + 1;
+    const uint32_t meet = k_at + 4 * r, scales = k_at + DT * kApart * 4;
+    static_assert((DT * kApart + 2 * kRows) * 4 <= 4 * W::kOperand, "what is joined fits where K and V were");
+    auto store = [](uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); };
+    tc::named_bar_sync(1, 256);
+    if (par == 1) {
+#pragma unroll
+      for (int i = 0; i < DT / 2; ++i) {
+        store(meet + 2 * i * kApart * 4, out[i].x);
+        store(meet + (2 * i + 1) * kApart * 4, out[i].y);
+      }
+      store(scales + 8 * r, ref);
+      store(scales + 8 * r + 4, sum);
+    }
+    tc::named_bar_sync(1, 256);
+    if (par == 0) {
+      const float2 other = lds_float2(scales + 8 * r);
+      const float m = fmaxf(ref, other.x), mine = exp2_of(ref - m), theirs = exp2_of(other.x - m);
+#pragma unroll
+      for (int i = 0; i < DT / 2; ++i) {
+        const uint32_t at = meet + 2 * i * kApart * 4;
+        store(at, out[i].x * mine + lds_float(at) * theirs);
+        store(at + kApart * 4, out[i].y * mine + lds_float(at + kApart * 4) * theirs);
+      }
+      store(scales + 8 * r, m);
+      store(scales + 8 * r + 4, sum * mine + other.y * theirs);
+    }
+    tc::named_bar_sync(1, 256);
+    float* slot = sh.parts + (int64_t)blockIdx.x * sh.slot_heads * (D + 4);
+    for (int i = warp; i < heads; i += 8) {
+      for (int d = lane; d < D; d += 32) slot[i * (D + 4) + d] = lds_float(k_at + (d * kApart + i) * 4);
+      if (lane == 0) *reinterpret_cast<float2*>(slot + i * (D + 4) + D) = lds_float2(scales + 8 * i);
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------- keys and values, widened
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBringRegisters));
+    const int tid = threadIdx.x - 256;
+    constexpr int kB = W::kBatch, kDims = 16 / W::kBytes;
+    uint4 held[kB];
+    float step_held[2] = {0.0f, 0.0f};
+    // A thread brings the same 16 bytes of every kTurn-th token's row.
+    const int of_turn = tid / W::kLanes, chunk = tid % W::kLanes, row_bytes = D * W::kBytes;
+    const bool loads = chunk * kDims < D, stores = chunk < W::kPieces;
+    const int64_t mine = (int64_t)of_turn * row_bytes + 16 * chunk;
+    const uint32_t place = of_panel(of_turn, kDims * chunk);  // and 128 kTurn bytes on for each turn
+    auto piece = [&](int n, int operand, int i) {  // of tile n's keys (operand 0) or values
+      if (n >= tiles) return make_uint4(0, 0, 0, 0);
+      const int64_t first = entries[n % kEntries].row[i * W::kTurn / 16];
+      if (!alive || first < 0 || !loads || begin + n * kTile + i * W::kTurn + of_turn >= len) return make_uint4(0, 0, 0, 0);
+      const uint8_t* from = static_cast<const uint8_t*>(operand ? c.v : c.k);
+      return load16(from + (first + i * W::kTurn % 16) * row_bytes + mine);
+    };
+    auto begin_tile = [&](int n) {  // before the first piece of a tile is asked for
+      if (n >= tiles) return;
+      wait(&meta_full[n % kEntries], n / kEntries);
+      if constexpr (!W::kBf16) {  // a thread has the steps of one token
+        const int64_t first = entries[n % kEntries].row[tid >> 4];
+        const bool have = alive && first >= 0 && begin + n * kTile + tid < len;
+        step_held[0] = have ? __ldg(c.k_step + first + (tid & 15)) : 0.0f;
+        step_held[1] = have ? __ldg(c.v_step + first + (tid & 15)) : 0.0f;
+      }
+    };
+    auto put = [&](uint32_t stage, int i, const uint4& w, float scale) {
+      uint32_t h[8];
+      if (!stores) return;
+      const uint32_t first = stage + place + i * W::kTurn * 128;
+      if constexpr (W::kBf16) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = mul2(make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u)), both(scale));
+          const __half2 x = __floats2half2_rn(f.x, f.y);
+          h[j] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        tc::st_shared_v4(first, h[0], h[1], h[2], h[3]);
+      } else {
+        widen<FORMAT>(w.x, h[0], h[1]);
+        widen<FORMAT>(w.y, h[2], h[3]);
+        widen<FORMAT>(w.z, h[4], h[5]);
+        widen<FORMAT>(w.w, h[6], h[7]);
+        // the second panel's pieces in the other order: each eighth of a store meets every bank once
+        const uint32_t second = first ^ 16;
+        if (chunk & 4) {
+          tc::st_shared_v4(second, h[4], h[5], h[6], h[7]);
+          tc::st_shared_v4(first, h[0], h[1], h[2], h[3]);
+        } else {
+          tc::st_shared_v4(first, h[0], h[1], h[2], h[3]);
+          tc::st_shared_v4(second, h[4], h[5], h[6], h[7]);
+        }
+      }
+    };
+    // bf16: the exponent that a tile's largest value is taken to have, K's and V's: put to 2^8, so that it may be
+    // 2^7 more, or 2^8 less, before the tile is done again with its own
+    int taken[2] = {127, 127};
+    begin_tile(0);
+#pragma unroll
+    for (int i = 0; i < kB; ++i) held[i] = piece(0, 0, i);
+#pragma unroll 1
+    for (int n = 0; n < tiles; ++n) {
+      const int entry = n % kEntries;
+#pragma unroll
+      for (int operand = 0; operand < 2; ++operand) {
+        const uint32_t stage = (operand ? v_at : k_at) + (n & 1) * W::kOperand;
+        if (n >= 2) wait(operand ? &v_empty[n & 1] : &k_empty[n & 1], (n >> 1) - 1);
+        uint32_t largest = 0;
+#pragma unroll
+        for (int half = 0; half < W::kBatches; ++half) {
+          if constexpr (!W::kBf16) {
+            if (operand == 0) {
+              k_steps[entry][tid] = step_held[0];
+              v_steps[entry][tid] = at_least(step_held[1], kLeastStep);
+              const uint32_t m = __reduce_max_sync(kFullMask, __float_as_uint(step_held[1]));
+              if (lane == 0) v_most[entry][warp - 8] = __uint_as_float(m);
+            }
+          }
+          // as a piece is laid down the next batch's is asked for
+          const bool last = half + 1 == W::kBatches;
+          const int next = last && operand == 1 ? n + 1 : n, next_operand = last ? 1 - operand : operand, next_half = last ? 0 : half + 1;
+          if (last && operand == 1) begin_tile(next);
+          const float scale = W::kBf16 ? power2(135 - taken[operand]) : 1.0f;
+#pragma unroll
+          for (int i = 0; i < kB; ++i) {
+            if constexpr (W::kBf16)
+              largest = __vmaxu2(largest, __vmaxu2(__vmaxu2(held[i].x & 0x7fff7fffu, held[i].y & 0x7fff7fffu), __vmaxu2(held[i].z & 0x7fff7fffu, held[i].w & 0x7fff7fffu)));
+            put(stage, half * kB + i, held[i], scale);
+            held[i] = piece(next, next_operand, next_half * kB + i);
+          }
+        }
+        if constexpr (W::kBf16) {
+          const uint32_t m = __reduce_max_sync(kFullMask, max(largest & 0xffffu, largest >> 16));
+          if (lane == 0) tops[operand][warp - 8] = m;
+          tc::named_bar_sync(2, 128);
+          const int e = (int)(max(max(tops[operand][0], tops[operand][1]), max(tops[operand][2], tops[operand][3])) >> 7);
+          if (e > taken[operand] + 6 || (e > 0 && e < taken[operand] - 8)) {
+            taken[operand] = max(30, min(230, e));
+            const float scale = power2(135 - taken[operand]);
+#pragma unroll 1
+            for (int i = 0; i < kB * W::kBatches; ++i) put(stage, i, piece(n, operand, i), scale);
+          }
+          if (tid == 0) {
+            (operand ? v_most[entry] : k_steps[entry])[0] = power2(taken[operand] - 135);
+            if (operand) v_most[entry][1] = v_most[entry][2] = v_most[entry][3] = 0.0f;
+          }
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(operand ? &v_full[n & 1] : &k_full[n & 1]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegisters));
+    if (warp == 12) {
+      // ----------------------------------------------------- S = Q K^T
+      if (lane == 0) {
+        const uint32_t idesc = tc::make_idesc(kRows, kTile);
+        wait(&q_full, 0);
+#pragma unroll 1
+        for (int n = 0; n < tiles; ++n) {
+          wait(&k_full[n & 1], n >> 1);
+          if (n >= 2) wait(&o_full[n & 1], (n >> 1) - 1);  // the weights that lie over the last S of this place are used
+          if (alive) {
+            tc::tc_fence_after();
+            uint32_t add = 0;
+#pragma unroll 1
+            for (int part = 1; part >= 0; --part) {
+#pragma unroll
+              for (int k = 0; k < DT / 16; ++k) {
+                const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
+                mma_f16_ss(s_of(n & 1), tc::smem_desc_sw128(q_at + part * W::kOperand + off), tc::smem_desc_sw128(k_at + (n & 1) * W::kOperand + off), idesc, add);
+                add = 1;
+              }
+            }
+            tc::mma_commit(&s_full[n & 1]);
+            tc::mma_commit(&k_empty[n & 1]);
+          }
+        }
+        tc::mma_commit(&drained[0]);
+        drain(&drained[0], status);
+      }
+    } else if (warp == 13) {
+      // ----------------------------------------------------- O = P V
+      if (lane == 0) {
+        constexpr uint32_t kAcross = 1u << 16;
+        const uint32_t idesc = tc::make_idesc(kRows, DT) | kAcross;
+#pragma unroll 1
+        for (int n = 0; n < tiles; ++n) {
+          wait(&v_full[n & 1], n >> 1);
+          wait(&p_full[n & 1], n >> 1);
+          if (alive) {
+            tc::tc_fence_after();
+            uint32_t add = 0;
+#pragma unroll 1
+            for (int part = 1; part >= 0; --part) {
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k) {
+                tc::mma_f16_ta(o_of(n & 1), s_of(n & 1) + 16 * k + 8 * part, across_desc(v_at + (n & 1) * W::kOperand + k * 2048), idesc, add);
+                add = 1;
+              }
+            }
+            tc::mma_commit(&o_full[n & 1]);
+            tc::mma_commit(&v_empty[n & 1]);
+          }
+        }
+        tc::mma_commit(&drained[1]);
+        drain(&drained[1], status);
+      }
+    } else if (warp == 14) {
+      // ----------------------------------------------------- pages
+      const int32_t* table = a.table + b * a.table_stride;
+      const int64_t head_row = (int64_t)hk << c.page_shift;
+      const int half = lane & 7;
+#pragma unroll 1
+      for (int n = 0; n < tiles; ++n) {
+        const int entry = n % kEntries;
+        const uint32_t t = begin + n * kTile + 16 * half;
+        int64_t at = -1;
+        if (t < len) {
+          const int32_t page = table[t >> c.page_shift];
+          if (page >= 0 && page < c.num_pages) at = (((int64_t)page * c.heads) << c.page_shift) + head_row + (t & ((1u << c.page_shift) - 1));
+        }
+        if (n >= kEntries) wait(&meta_empty[entry], n / kEntries - 1);
+        if (lane < 8) entries[entry].row[half] = at;
+        const uint32_t ok = __ballot_sync(kFullMask, at >= 0) & 0xffu;
+        if (lane == 0) entry_ok[entry] = ok;
+        if (lane < 16 && at >= 0) {  // 16 tokens of a head are one run of bytes
+          const uint8_t* from = static_cast<const uint8_t*>(lane < 8 ? c.k : c.v) + at * D * W::kBytes;
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(16 * D * W::kBytes) : "memory");
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&meta_full[entry]);
+      }
+    }
+    __syncwarp();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int FORMAT, int DT>
+cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, Shares sh, int64_t rows, bool pdl, const DeviceInfo& dev,
+                         cudaStream_t stream) {
+  using W = Wide<FORMAT, DT>;
+  const auto kernel = prefix_wide_kernel<FORMAT, DT>;
+  static thread_local int configured_device = -1;
+  if (configured_device != dev.device) {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);
+    if (err != cudaSuccess) return err;
+    configured_device = dev.device;
+  }
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.blockDim = dim3(kWideThreads, 1, 1);
+  cfg.dynamicSmemBytes = W::kSmem;
+  if (pdl) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+  }
+  const int sms = dev.num_sms < kSms ? dev.num_sms : kSms;
+  const int64_t steps = ((a.max_pages << c.page_shift) + kTile - 1) / kTile;
+  // in proportion to the tokens where rows round up to whole CTAs well below the GPU, else a CTA a row
+  if (a.B <= kShareSeqs && rows <= sms / 3 && steps_fit(rows, steps)) {
+    sh.splits = 0;
+    cfg.gridDim = dim3((unsigned)sms, 1, 1);
+  } else {
+    sh.splits = 1;
+    cfg.gridDim = dim3((unsigned)rows, 1, 1);
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, a, c, sh, dev.status);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_wide(const AttendArgs& a, const KvPages& c, const PrefixRows& p, bool pdl, const DeviceInfo& dev,
+                               cudaStream_t stream) {
+  Shares sh = {};
+  sh.group = p.group;
+  sh.groups = p.tiles;
+  sh.rows_a_seq = c.heads * p.tiles;
+  sh.parts = p.parts;
+  sh.rows = p.rows;
+  sh.group_rows = p.group_rows;
+  sh.lengths = p.lengths;
+  sh.heads_a_key = p.heads_a_key;
+  sh.slot_heads = p.slot_heads;
+  const int64_t rows = a.B * sh.rows_a_seq;
+  return of_shape(c, [&](auto format, auto dims) {
+    constexpr int kDims = decltype(dims)::value;
+    if constexpr (kDims <= 128)
+      return launch_shape<decltype(format)::value, kDims>(a, c, sh, rows, pdl, dev, stream);
+    else
+      return cudaErrorInvalidValue;  // not asked for
+  });
+}
+
+}  // namespace bitlinear

@@ -16,21 +16,28 @@ namespace {
 // The most CTAs that shared tokens are split over beside one a row.
 constexpr int kPrefixCtas = 4 * kSms;
 
+// How the shared tokens' q heads are cut into rows of work: eight a CTA (attend.cuh), or 128 on the tensor
+// cores (attention_prefix.cu).
 struct Sizes {
-  int64_t group_rows, rows;  // sequences a group; kPrefix's rows of all groups
-  int heads_a_key, tiles, heads;  // q heads a key head; rows a key head of a group; q heads of a row
+  int64_t group_rows, rows, slots;  // sequences a group; rows of all groups; parts that there may be
+  int heads_a_key, tiles, tile, heads;  // q heads a key head; rows a key head of a group, of so many q heads; places in a part
+  bool wide;
 };
-Sizes sizes_of(int64_t B, int q_heads, int kv_heads, int64_t groups) {
+constexpr int64_t kWideHeads = 24;
+Sizes sizes_of(int64_t B, int q_heads, int kv_heads, int head_dim, int64_t groups) {
   Sizes s;
   s.group_rows = B / groups;
   s.heads_a_key = q_heads / kv_heads;
-  const int64_t all = s.group_rows * s.heads_a_key, tiles = (all + kRowHeads - 1) / kRowHeads;
-  s.tiles = (int)tiles;
-  s.heads = (int)(all < kRowHeads ? all : kRowHeads);
-  s.rows = groups * kv_heads * tiles;
+  const int64_t all = s.group_rows * s.heads_a_key;
+  s.wide = all >= kWideHeads && head_dim <= 128;
+  s.tile = s.wide ? kPrefixWide : kRowHeads;
+  s.tiles = (int)((all + s.tile - 1) / s.tile);
+  s.heads = (int)(all < s.tile ? all : s.tile);
+  s.rows = groups * kv_heads * s.tiles;
+  const int64_t ctas = s.wide ? kSms : kPrefixCtas;
+  s.slots = s.rows > ctas ? s.rows : ctas;
   return s;
 }
-int64_t slots_of(const Sizes& s) { return s.rows > kPrefixCtas ? s.rows : kPrefixCtas; }
 
 template <int FORMAT, int DT>
 cudaError_t launch_shape(AttendArgs a, const KvPages& c, const int32_t* shared, int64_t groups, void* workspace, bool pdl,
@@ -44,7 +51,7 @@ cudaError_t launch_shape(AttendArgs a, const KvPages& c, const int32_t* shared, 
     if (err != cudaSuccess) return err;
     configured_device = dev.device;
   }
-  const Sizes sizes = sizes_of(a.B, a.q_heads, c.heads, groups);
+  const Sizes sizes = sizes_of(a.B, a.q_heads, c.heads, c.head_dim, groups);
   const int64_t steps = ((a.max_pages << c.page_shift) + S::kTokens - 1) / S::kTokens;
 
   // The shared tokens: a group is a sequence, its rows' q heads those of one key head.
@@ -57,33 +64,41 @@ cudaError_t launch_shape(AttendArgs a, const KvPages& c, const int32_t* shared, 
   sh.groups = sizes.tiles;
   sh.rows_a_seq = c.heads * sizes.tiles;
   sh.parts = static_cast<float*>(workspace);
-  sh.rows = reinterpret_cast<int2*>(sh.parts + slots_of(sizes) * sizes.heads * (c.head_dim + 4));
+  sh.rows = reinterpret_cast<int2*>(sh.parts + sizes.slots * sizes.heads * (c.head_dim + 4));
   sh.group_rows = (int)sizes.group_rows;
   sh.shared = shared;
   sh.lengths = a.lengths;
   sh.heads_a_key = sizes.heads_a_key;
   sh.prefix_tiles = sizes.tiles;
-  int smem = (int)S::kSmem + sizes.heads * S::kHeadBytes + kRowHeads * 4;
-  const int ctas = resident_ctas<S>(dev, smem);
-  cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  if (pdl) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
-  }
-  if (groups <= kShareSeqs && sizes.rows <= ctas / 3 && steps_fit(sizes.rows, steps)) {
-    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  sh.prefix_heads = sizes.tile;
+  sh.slot_heads = sizes.heads;
+  int smem = (int)S::kSmem + kRowHeads * (S::kHeadBytes + 4);
+  cudaError_t err;
+  if (sizes.wide) {
+    const PrefixRows p = {sh.group, sizes.tiles, sh.group_rows, sizes.heads_a_key, sizes.heads, a.lengths, sh.parts, sh.rows};
+    err = launch_prefix_wide(g, c, p, pdl, dev, stream);
   } else {
-    sh.splits = splits_for(sizes.rows, steps, ctas, kPortableCluster);
-    while ((1 << sh.splits_log2) < sh.splits) ++sh.splits_log2;
-    cfg.gridDim = dim3((unsigned)(sizes.rows * sh.splits), 1, 1);
+    const int ctas = resident_ctas<S>(dev, smem);
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    if (pdl) {
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.numAttrs = 1;
+    }
+    if (groups <= kShareSeqs && sizes.rows <= ctas / 3 && steps_fit(sizes.rows, steps)) {
+      cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    } else {
+      sh.splits = splits_for(sizes.rows, steps, ctas, kPortableCluster);
+      while ((1 << sh.splits_log2) < sh.splits) ++sh.splits_log2;
+      cfg.gridDim = dim3((unsigned)(sizes.rows * sh.splits), 1, 1);
+    }
+    err = cudaLaunchKernelEx(&cfg, attend_kernel<FORMAT, DT, kPrefix>, g, c, sh);
   }
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, attend_kernel<FORMAT, DT, kPrefix>, g, c, sh);
   if (err != cudaSuccess) return err;
 
   // Each row's own tokens, and the join.
@@ -104,8 +119,8 @@ cudaError_t launch_shape(AttendArgs a, const KvPages& c, const int32_t* shared, 
 size_t attention_shared_workspace_bytes(int64_t B, int q_heads, int kv_heads, int head_dim, int64_t groups) {
   const size_t alone = attention_workspace_bytes(B, q_heads, kv_heads, head_dim);
   if (groups == B) return alone;
-  const Sizes s = sizes_of(B, q_heads, kv_heads, groups);
-  const size_t need = (size_t)slots_of(s) * s.heads * (head_dim + 4) * sizeof(float) + (size_t)s.rows * sizeof(int2);
+  const Sizes s = sizes_of(B, q_heads, kv_heads, head_dim, groups);
+  const size_t need = (size_t)s.slots * s.heads * (head_dim + 4) * sizeof(float) + (size_t)s.rows * sizeof(int2);
   return need > alone ? need : alone;
 }
 

@@ -41,6 +41,19 @@ cudaError_t launch_select(const SelectArgs& a, const KvPages& cache, const Summa
 cudaError_t launch_attention_blocks(const AttendArgs& a, const KvPages& cache, const int32_t* blocks, int count, bool pdl,
                                     const DeviceInfo& dev, cudaStream_t stream);
 
+// attention_prefix.cu: the shared tokens of groups (a.B of them, a.lengths tokens each) for 128 q heads a CTA.
+constexpr int kPrefixWide = 128;
+struct PrefixRows {
+  int group, tiles;             // q heads of a group for a key head, in tiles of 128
+  int group_rows, heads_a_key;  // its sequences, and their q heads a key head
+  int slot_heads;               // places in a part
+  const int32_t* lengths;       // of every sequence
+  float* parts;                 // [CTA][slot_heads][dims, m, sum]
+  int2* rows;                   // of each group, key head and tile: its first CTA and how many it has
+};
+cudaError_t launch_prefix_wide(const AttendArgs& a, const KvPages& c, const PrefixRows& p, bool pdl, const DeviceInfo& dev,
+                               cudaStream_t stream);
+
 // attention_shared.cu
 size_t attention_shared_workspace_bytes(int64_t B, int q_heads, int kv_heads, int head_dim, int64_t groups);
 cudaError_t launch_attention_shared(const AttendArgs& a, const KvPages& cache, const int32_t* shared, int64_t groups,
