@@ -11,8 +11,8 @@
 // Each tile's O starts from zero and is added to fp32 sums in registers: the tensor cores' adder cuts toward
 // zero, and a chain of tiles in it would show.
 //
-// 16 warps: two groups of four that turn logits into weights and add up O, each for every other tile with a reference
-// and sums of its own (a thread is a row: nothing is exchanged until the end); four that bring K and V,
+// 20 warps: two groups of four that turn logits into weights and add up O, each for every other tile with a reference
+// and sums of its own (a thread is a row: nothing is exchanged until the end); eight that bring K and V,
 // widen the codes and lay them out for the MMA (128-byte swizzle, the same image for both: K is the B
 // operand along its rows, V across them); one that looks pages up, eight tiles ahead, and
 // asks for them to come into L2; one thread that issues the products of S and one that issues those of O.
@@ -26,12 +26,16 @@ namespace {
 
 constexpr int kRows = kPrefixWide;      // q heads of a CTA: the MMA's rows
 constexpr int kTile = 128;              // tokens
-constexpr int kWideThreads = 512;
+constexpr int kWideThreads = 640;
+constexpr int kBring = 8, kIssue = 16;  // the first warps that bring keys and values, and that issue
+constexpr int kBringThreads = 256;
 constexpr int kEntries = 8;             // tiles whose pages and steps are known
 constexpr int kPanel = 128 * 128;       // bytes of 128 rows of 64 fp16 values
 constexpr float kTarget = 12.0f, kMost = 15.0f;  // log2 of the largest weight: where the reference puts it, what moves it
-constexpr int kAddRegisters = 184, kBringRegisters = 104, kIssueRegisters = 40;
-static_assert(2 * 128 * kAddRegisters + 128 * kBringRegisters + 128 * kIssueRegisters <= 65536, "the registers that 512 threads of 128 have");
+// Registers a thread: at the launch, and as the groups of warps then share them out.
+constexpr int kLaunchRegisters = 96, kAddRegisters = 176, kBringRegisters = 48, kIssueRegisters = 32;
+static_assert(256 * kAddRegisters + kBringThreads * kBringRegisters + 128 * kIssueRegisters <= kWideThreads * kLaunchRegisters,
+              "more registers than were launched with would be waited for");
 
 template <int FORMAT, int DT>
 struct Wide {
@@ -41,8 +45,8 @@ struct Wide {
   static constexpr int kOperand = kPanels * kPanel;
   static constexpr int kLanes = 8 * kBytes;            // lanes of a token's row, 16 bytes each
   static constexpr int kPieces = DT * kBytes / 16;     // of them that a row fills
-  static constexpr int kTurn = 128 / kLanes;           // tokens that 128 threads bring at once
-  static constexpr int kBatch = 8;                     // turns that a thread holds at once
+  static constexpr int kTurn = kBringThreads / kLanes; // tokens that come at once
+  static constexpr int kBatch = 4;                     // turns that a thread holds at once
   static constexpr int kBatches = kTile / (kTurn * kBatch);
   static constexpr int kSmem = 6 * kOperand + 1024;    // Q's parts, two K, two V; the base is rounded up to 1024
 };
@@ -92,9 +96,20 @@ __device__ __forceinline__ uint32_t of_panel(int row, int dim) {  // where a 16-
   return (uint32_t)((dim >> 6) * kPanel + row * 128 + ((((dim >> 3) & 7) ^ (row & 7)) << 4));
 }
 
-__device__ __forceinline__ uint4 load16(const void* p) {  // in its place among the stores
+// Zeros, or what is at p: in its place among the stores, and no branch (behind one it would be waited for).
+__device__ __forceinline__ uint4 load16(const void* p, bool have) {
   uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)have));
+  return v;
+}
+
+__device__ __forceinline__ float load4(const float* p, bool have) {
+  float v;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t@p ld.global.nc.f32 %0, [%1];\n\t}" : "=&f"(v) : "l"(p), "r"((uint32_t)have));
   return v;
 }
 
@@ -134,10 +149,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
   extern __shared__ uint8_t raw[];
   __shared__ __align__(16) float k_steps[kEntries][W::kBf16 ? 4 : kTile], v_steps[kEntries][W::kBf16 ? 4 : kTile];
   __shared__ __align__(16) float v_most[kEntries][4];
+  __shared__ float row_scales[kRows];
   __shared__ __align__(16) Entry entries[kEntries];
   __shared__ uint32_t entry_ok[kEntries];
-  __shared__ float row_tops[2][kRows];
-  __shared__ uint32_t tops[2][4];
+  __shared__ uint32_t tops[2][8];
   __shared__ __align__(8) unsigned long long meta_full[kEntries], meta_empty[kEntries], k_full[2], k_empty[2], v_full[2], v_empty[2],
       s_full[2], p_full[2], o_full[2], q_full, drained[2];
   __shared__ uint32_t tmem_at;
@@ -146,6 +161,27 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
   const uint32_t base = ((uint32_t)__cvta_generic_to_shared(raw) + 1023u) & ~1023u;
   const uint32_t q_at = base, k_at = base + 2 * W::kOperand, v_at = base + 4 * W::kOperand;
 
+  if (warp == kIssue + 3 && lane == 0) {
+    abort_flag = 0;
+#pragma unroll 1
+    for (int i = 0; i < kEntries; ++i) {
+      tc::mbar_init(&meta_full[i], 1);
+      tc::mbar_init(&meta_empty[i], 4);
+    }
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&k_full[i], kBringThreads / 32);
+      tc::mbar_init(&v_full[i], kBringThreads / 32);
+      tc::mbar_init(&p_full[i], 4);
+      tc::mbar_init(&k_empty[i], 1);
+      tc::mbar_init(&v_empty[i], 1);
+      tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&o_full[i], 1);
+      tc::mbar_init(&drained[i], 1);
+    }
+    tc::mbar_init(&q_full, 8);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   pdl_wait_primary();
   pdl_release_dependents();
   // The CTA's row of work: group b, key head and tile of q heads `row`, and its run of tiles.
@@ -165,11 +201,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     part = 0;
     parts = 1;
   }
+  if (warp == kIssue) tc::tmem_alloc(&tmem_at, 512);
   if (part == 0 && threadIdx.x == 0) sh.rows[b * sh.rows_a_seq + row] = make_int2(blockIdx.x, parts);
   const int hk = row / sh.groups, first_head = (row - hk * sh.groups) * kRows, heads = min(kRows, sh.group - first_head);
   uint32_t len;
   {
     int longest = 0;
+#pragma unroll 1
     for (int i = lane; i < sh.group_rows; i += 32) longest = max(longest, sh.lengths[b * sh.group_rows + i]);
     const Span<kTile> span(a.lengths[b], most, 0);
     len = min(span.len, (uint32_t)__reduce_max_sync(kFullMask, longest));
@@ -180,27 +218,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
   }
   const uint32_t begin = (uint32_t)part * kTile;
   const int tiles = max(0, min(parts, (int)((len + kTile - 1) / kTile)) - part);
-
-  if (threadIdx.x == 0) {
-    abort_flag = 0;
-    for (int i = 0; i < kEntries; ++i) {
-      tc::mbar_init(&meta_full[i], 1);
-      tc::mbar_init(&meta_empty[i], 4);
-    }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&k_full[i], 4);
-      tc::mbar_init(&v_full[i], 4);
-      tc::mbar_init(&p_full[i], 4);
-      tc::mbar_init(&k_empty[i], 1);
-      tc::mbar_init(&v_empty[i], 1);
-      tc::mbar_init(&s_full[i], 1);
-      tc::mbar_init(&o_full[i], 1);
-      tc::mbar_init(&drained[i], 1);
-    }
-    tc::mbar_init(&q_full, 8);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  if (warp == 12) tc::tmem_alloc(&tmem_at, 512);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -213,7 +230,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
   bool alive = true;
   auto wait = [&](unsigned long long* bar, int phase) { alive = alive && wait_bounded(bar, phase & 1, &abort_flag, status); };
 
-  if (warp < 8) {
+  if (warp < kBring) {
     // ------------------------------------------------------- logits to weights, sums
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegisters));
     const int par = warp >> 2, r = threadIdx.x & 127;
@@ -221,48 +238,51 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     const bool there = r < heads;
     const uint32_t of_group = first_head + (there ? r : 0), member = of_group / (uint32_t)sh.heads_a_key;
     const int64_t seq = b * sh.group_rows + member;
-    // q's row: the two groups take half of its dims each
-    float row_scale = 0.0f;
+    // q's rows, a warp a row, four at a time: a lane has 4 dims
     {
-      const float* q = a.q + seq * a.q_stride + (int64_t)(hk * sh.heads_a_key + (of_group - member * sh.heads_a_key)) * D + par * (DT / 2);
       const float factor = a.factor, more = a.factor_rest;
-      constexpr int kHalf = DT / 2;
-      float2 x[kHalf / 2];
-      float top = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kHalf / 4; ++i) {
-        const float4 w = there && par * kHalf + 4 * i < D ? *reinterpret_cast<const float4*>(q + 4 * i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        x[2 * i] = mul2(make_float2(w.x, w.y), both(factor));
-        x[2 * i + 1] = mul2(make_float2(w.z, w.w), both(factor));
-        top = fmaxf(fmaxf(top, fmaxf(fabsf(x[2 * i].x), fabsf(x[2 * i].y))), fmaxf(fabsf(x[2 * i + 1].x), fabsf(x[2 * i + 1].y)));
-      }
-      row_tops[par][r] = top;
-      tc::named_bar_sync(1, 256);
-      const int e = clamp_exponent(exponent_of(fmaxf(top, row_tops[1 - par][r])));
-      const float2 up = both(power2(13 - e)), rest_up = both(power2(13 - e) * more);
-      row_scale = power2(e - 13);
-#pragma unroll
-      for (int i = 0; i < kHalf / 8; ++i) {
-        uint4 lead, rest;
-        uint32_t* l[4] = {&lead.x, &lead.y, &lead.z, &lead.w};
-        uint32_t* s[4] = {&rest.x, &rest.y, &rest.z, &rest.w};
+      const bool have = 4 * lane < D;
+#pragma unroll 1
+      for (int i0 = warp; i0 < kRows; i0 += 32) {
+        float4 w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 v = mul2(x[4 * i + j], up);
-          const __half2 h = __floats2half2_rn(v.x, v.y);
-          const float2 d = fma2(x[4 * i + j], rest_up, fma2(__half22float2(h), both(-1.0f), v));
-          const __half2 g = __floats2half2_rn(d.x, d.y);
-          *l[j] = *reinterpret_cast<const uint32_t*>(&h);
-          *s[j] = *reinterpret_cast<const uint32_t*>(&g);
+          const int i = i0 + 8 * j;
+          const uint32_t head = first_head + min(i, heads - 1), who = head / (uint32_t)sh.heads_a_key;
+          const float* q = a.q + (b * sh.group_rows + who) * a.q_stride + (int64_t)(hk * sh.heads_a_key + (head - who * sh.heads_a_key)) * D;
+          w[j] = have && i < heads ? *reinterpret_cast<const float4*>(q + 4 * lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
-        const uint32_t at = q_at + of_panel(r, par * kHalf + 8 * i);
-        tc::st_shared_v4(at, lead.x, lead.y, lead.z, lead.w);
-        tc::st_shared_v4(at + W::kOperand, rest.x, rest.y, rest.z, rest.w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + 8 * j;
+          const float2 x = mul2(make_float2(w[j].x, w[j].y), both(factor)), y = mul2(make_float2(w[j].z, w[j].w), both(factor));
+          const float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
+          const int e = clamp_exponent(exponent_of(__uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(top)))));
+          const float2 up = both(power2(13 - e)), rest_up = both(power2(13 - e) * more);
+          uint32_t lead[2], rest[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 z = k ? y : x, v = mul2(z, up);
+            const __half2 h = __floats2half2_rn(v.x, v.y);
+            const float2 d = fma2(z, rest_up, fma2(__half22float2(h), both(-1.0f), v));
+            const __half2 g = __floats2half2_rn(d.x, d.y);
+            lead[k] = *reinterpret_cast<const uint32_t*>(&h);
+            rest[k] = *reinterpret_cast<const uint32_t*>(&g);
+          }
+          if (4 * lane < DT) {
+            const uint32_t at = q_at + of_panel(i, 4 * lane) + (lane & 1) * 8;
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(lead[0]), "r"(lead[1]) : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + W::kOperand), "r"(rest[0]), "r"(rest[1]) : "memory");
+          }
+          if (lane == 0) row_scales[i] = power2(e - 13);
+        }
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&q_full);
     }
+    tc::named_bar_sync(1, 256);
+    const float row_scale = row_scales[r];
     const bool none = (warp & 3) * 32 >= heads;  // rows of no q head: whatever comes of them is theirs
     const uint32_t row_end = there ? min(len, (uint32_t)max(0, sh.lengths[seq])) : 0u;
 
@@ -297,31 +317,39 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       const float v_top = at_least(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), kLeastStep);
       float unit = row_scale;
       if constexpr (W::kBf16) unit = fmaxf(unit * k_steps[entry][0], 1.1754944e-38f);  // a masked logit times 0 is none
-      // the row's largest logit
-      float top = -INFINITY;
+      // 16 logits (over `unit`) of granule g; loops over granules stay rolled up: code is fetched as it runs, and
+      // unrolled these took three times as long
+      auto logits = [&](int g, uint32_t (&s)[16], float2 (&x)[8]) {
+        tmem_loaded(s);
 #pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+        if constexpr (!W::kBf16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 k = lds_float4(ks + (16 * g + 4 * i) * 4);
+            x[2 * i] = mul2(x[2 * i], make_float2(k.x, k.y));
+            x[2 * i + 1] = mul2(x[2 * i + 1], make_float2(k.z, k.w));
+          }
+        }
+        if (!whole) {
+          const int here = (ok >> g) & 1u ? count - 16 * g : 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (2 * i >= here) x[i].x = -INFINITY;
+            if (2 * i + 1 >= here) x[i].y = -INFINITY;
+          }
+        }
+      };
+      // the row's largest
+      float top = -INFINITY;
+#pragma unroll 1
       for (int g = 0; g < kTile / 16; ++g) {
         uint32_t s[16];
+        float2 x[8];
         tmem_load16(s_at + 16 * g, s);
-        tmem_loaded(s);
-        const int here = (ok >> g) & 1u ? count - 16 * g : 0;
+        logits(g, s, x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float2 x = make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
-          float2 y = make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
-          if constexpr (!W::kBf16) {
-            const float4 k = lds_float4(ks + (16 * g + 4 * i) * 4);
-            x = mul2(x, make_float2(k.x, k.y));
-            y = mul2(y, make_float2(k.z, k.w));
-          }
-          if (!whole) {
-            if (4 * i >= here) x.x = -INFINITY;
-            if (4 * i + 1 >= here) x.y = -INFINITY;
-            if (4 * i + 2 >= here) y.x = -INFINITY;
-            if (4 * i + 3 >= here) y.y = -INFINITY;
-          }
-          top = fmaxf(top, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
-        }
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
       }
       top = top * unit + log2_of(v_top);  // of a weight
       if (top > ref + kMost) {
@@ -332,43 +360,31 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         for (int i = 0; i < DT / 2; ++i) out[i] = mul2(out[i], both(down));
       }
       float2 more = both(0.0f);
-#pragma unroll
+#pragma unroll 1
       for (int g = 0; g < kTile / 16; ++g) {
         uint32_t s[16], w[16];
+        float2 x[8];
         tmem_load16(s_at + 16 * g, s);
-        tmem_loaded(s);
-        const int here = (ok >> g) & 1u ? count - 16 * g : 0;
+        logits(g, s, x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float2 x = make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
-          float2 y = make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
-          if constexpr (!W::kBf16) {
-            const float4 k = lds_float4(ks + (16 * g + 4 * i) * 4);
-            x = mul2(x, make_float2(k.x, k.y));
-            y = mul2(y, make_float2(k.z, k.w));
-          }
-          if (!whole) {
-            if (4 * i >= here) x.x = -INFINITY;
-            if (4 * i + 1 >= here) x.y = -INFINITY;
-            if (4 * i + 2 >= here) y.x = -INFINITY;
-            if (4 * i + 3 >= here) y.y = -INFINITY;
-          }
-          x = fma2(x, both(unit), both(-ref));
-          y = fma2(y, both(unit), both(-ref));
-          x = make_float2(exp2_of(x.x), exp2_of(x.y));
-          y = make_float2(exp2_of(y.x), exp2_of(y.y));
-          more = add2(more, add2(x, y));
-          if constexpr (W::kBf16) {
-            x = mul2(x, both(v_top));
-            y = mul2(y, both(v_top));
-          } else {
-            const float4 v = lds_float4(vs + (16 * g + 4 * i) * 4);
-            x = mul2(x, make_float2(v.x, v.y));
-            y = mul2(y, make_float2(v.z, v.w));
-          }
-          parts_of(x, w[2 * i], w[8 + 2 * i]);
-          parts_of(y, w[2 * i + 1], w[8 + 2 * i + 1]);
+        for (int i = 0; i < 8; ++i) {
+          x[i] = fma2(x[i], both(unit), both(-ref));
+          x[i] = make_float2(exp2_of(x[i].x), exp2_of(x[i].y));
+          more = add2(more, x[i]);
         }
+        if constexpr (W::kBf16) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], both(v_top));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 v = lds_float4(vs + (16 * g + 4 * i) * 4);
+            x[2 * i] = mul2(x[2 * i], make_float2(v.x, v.y));
+            x[2 * i + 1] = mul2(x[2 * i + 1], make_float2(v.z, v.w));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) parts_of(x[i], w[i], w[8 + i]);
         tc::tmem_st16(s_at + 16 * g, w);
       }
       tc::tmem_st_wait();
@@ -392,67 +408,82 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       }
     }
     // The two groups' sums meet in what was K's and V's place: [dim][row], 129 apart, then references and sums.
+    // Each group gives the other half of its dims and joins the other half of the other's.
     float sum = sums.x + sums.y;
-    constexpr int kApart = kRows + 1;
+    constexpr int kApart = kRows + 1, kHalf = DT / 4;  // in pairs of dims
     const uint32_t meet = k_at + 4 * r, scales = k_at + DT * kApart * 4;
-    static_assert((DT * kApart + 2 * kRows) * 4 <= 4 * W::kOperand, "what is joined fits where K and V were");
+    static_assert((DT * kApart + 4 * kRows) * 4 <= 4 * W::kOperand, "what is joined fits where K and V were");
     auto store = [](uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); };
-    tc::named_bar_sync(1, 256);
-    if (par == 1) {
+    auto give = [&](auto half) {
+      constexpr int h = decltype(half)::value;
 #pragma unroll
-      for (int i = 0; i < DT / 2; ++i) {
+      for (int i = h * kHalf; i < (h + 1) * kHalf; ++i) {
         store(meet + 2 * i * kApart * 4, out[i].x);
         store(meet + (2 * i + 1) * kApart * 4, out[i].y);
       }
-      store(scales + 8 * r, ref);
-      store(scales + 8 * r + 4, sum);
-    }
-    tc::named_bar_sync(1, 256);
-    if (par == 0) {
-      const float2 other = lds_float2(scales + 8 * r);
-      const float m = fmaxf(ref, other.x), mine = exp2_of(ref - m), theirs = exp2_of(other.x - m);
+    };
+    auto take = [&](auto half, float mine, float theirs) {
+      constexpr int h = decltype(half)::value;
 #pragma unroll
-      for (int i = 0; i < DT / 2; ++i) {
+      for (int i = h * kHalf; i < (h + 1) * kHalf; ++i) {
         const uint32_t at = meet + 2 * i * kApart * 4;
         store(at, out[i].x * mine + lds_float(at) * theirs);
         store(at + kApart * 4, out[i].y * mine + lds_float(at + kApart * 4) * theirs);
       }
-      store(scales + 8 * r, m);
-      store(scales + 8 * r + 4, sum * mine + other.y * theirs);
+    };
+    tc::named_bar_sync(1, 256);
+    if (par == 0)
+      give(std::integral_constant<int, 1>());
+    else
+      give(std::integral_constant<int, 0>());
+    store(scales + 16 * r + 8 * par, ref);
+    store(scales + 16 * r + 8 * par + 4, sum);
+    tc::named_bar_sync(1, 256);
+    const float2 other = lds_float2(scales + 16 * r + 8 * (1 - par));
+    const float m = fmaxf(ref, other.x), mine = exp2_of(ref - m), theirs = exp2_of(other.x - m);
+    if (par == 0)
+      take(std::integral_constant<int, 0>(), mine, theirs);
+    else
+      take(std::integral_constant<int, 1>(), mine, theirs);
+    tc::named_bar_sync(1, 256);  // the other's reference and sum are read
+    if (par == 0) {
+      store(scales + 16 * r, m);
+      store(scales + 16 * r + 4, sum * mine + other.y * theirs);
     }
     tc::named_bar_sync(1, 256);
     float* slot = sh.parts + (int64_t)blockIdx.x * sh.slot_heads * (D + 4);
     for (int i = warp; i < heads; i += 8) {
       for (int d = lane; d < D; d += 32) slot[i * (D + 4) + d] = lds_float(k_at + (d * kApart + i) * 4);
-      if (lane == 0) *reinterpret_cast<float2*>(slot + i * (D + 4) + D) = lds_float2(scales + 8 * i);
+      if (lane == 0) *reinterpret_cast<float2*>(slot + i * (D + 4) + D) = lds_float2(scales + 16 * i);
     }
-  } else if (warp < 12) {
+  } else if (warp < kIssue) {
     // ------------------------------------------------------- keys and values, widened
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBringRegisters));
-    const int tid = threadIdx.x - 256;
+    const int tid = threadIdx.x - 32 * kBring;
     constexpr int kB = W::kBatch, kDims = 16 / W::kBytes;
     uint4 held[kB];
-    float step_held[2] = {0.0f, 0.0f};
+    float step_held = 0.0f;
     // A thread brings the same 16 bytes of every kTurn-th token's row.
     const int of_turn = tid / W::kLanes, chunk = tid % W::kLanes, row_bytes = D * W::kBytes;
-    const bool loads = chunk * kDims < D, stores = chunk < W::kPieces;
-    const int64_t mine = (int64_t)of_turn * row_bytes + 16 * chunk;
-    const uint32_t place = of_panel(of_turn, kDims * chunk);  // and 128 kTurn bytes on for each turn
-    auto piece = [&](int n, int operand, int i) {  // of tile n's keys (operand 0) or values
-      if (n >= tiles) return make_uint4(0, 0, 0, 0);
-      const int64_t first = entries[n % kEntries].row[i * W::kTurn / 16];
-      if (!alive || first < 0 || !loads || begin + n * kTile + i * W::kTurn + of_turn >= len) return make_uint4(0, 0, 0, 0);
+    const bool loads = chunk * kDims < D, stores = chunk < W::kPieces, turned = !W::kBf16 && (chunk & 4);
+    // and 128 kTurn bytes on for each turn; the second panel's pieces go in the other order, so that each
+    // eighth of a store meets every bank once
+    const uint32_t place = of_panel(of_turn, kDims * chunk) ^ (turned ? 16 : 0);
+    // the i-th of tile n's keys (operand 0) or values; zeros for a token that is not there
+    auto piece = [&](int n, int operand, int i) {
+      const int64_t first = entries[n % kEntries].row[(i * W::kTurn + of_turn) >> 4];
+      const bool have = alive && n < tiles && first >= 0 && loads && i * W::kTurn + of_turn < (int)(len - begin) - n * kTile;
       const uint8_t* from = static_cast<const uint8_t*>(operand ? c.v : c.k);
-      return load16(from + (first + i * W::kTurn % 16) * row_bytes + mine);
+      return load16(from + (first + ((i * W::kTurn + of_turn) & 15)) * row_bytes + 16 * chunk, have);
     };
     auto begin_tile = [&](int n) {  // before the first piece of a tile is asked for
       if (n >= tiles) return;
       wait(&meta_full[n % kEntries], n / kEntries);
-      if constexpr (!W::kBf16) {  // a thread has the steps of one token
-        const int64_t first = entries[n % kEntries].row[tid >> 4];
-        const bool have = alive && first >= 0 && begin + n * kTile + tid < len;
-        step_held[0] = have ? __ldg(c.k_step + first + (tid & 15)) : 0.0f;
-        step_held[1] = have ? __ldg(c.v_step + first + (tid & 15)) : 0.0f;
+      if constexpr (!W::kBf16) {  // a thread has a step of one token, a key's or a value's
+        const int token = tid & 127;
+        const int64_t first = entries[n % kEntries].row[token >> 4];
+        const bool have = alive && first >= 0 && token < (int)(len - begin) - n * kTile;
+        step_held = load4((tid < 128 ? c.k_step : c.v_step) + first + (token & 15), have);
       }
     };
     auto put = [&](uint32_t stage, int i, const uint4& w, float scale) {
@@ -469,19 +500,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         }
         tc::st_shared_v4(first, h[0], h[1], h[2], h[3]);
       } else {
-        widen<FORMAT>(w.x, h[0], h[1]);
-        widen<FORMAT>(w.y, h[2], h[3]);
-        widen<FORMAT>(w.z, h[4], h[5]);
-        widen<FORMAT>(w.w, h[6], h[7]);
-        // the second panel's pieces in the other order: each eighth of a store meets every bank once
-        const uint32_t second = first ^ 16;
-        if (chunk & 4) {
-          tc::st_shared_v4(second, h[4], h[5], h[6], h[7]);
-          tc::st_shared_v4(first, h[0], h[1], h[2], h[3]);
-        } else {
-          tc::st_shared_v4(first, h[0], h[1], h[2], h[3]);
-          tc::st_shared_v4(second, h[4], h[5], h[6], h[7]);
-        }
+        widen<FORMAT>(turned ? w.z : w.x, h[0], h[1]);
+        widen<FORMAT>(turned ? w.w : w.y, h[2], h[3]);
+        widen<FORMAT>(turned ? w.x : w.z, h[4], h[5]);
+        widen<FORMAT>(turned ? w.y : w.w, h[6], h[7]);
+        tc::st_shared_v4(first, h[0], h[1], h[2], h[3]);
+        tc::st_shared_v4(first ^ 16, h[4], h[5], h[6], h[7]);
       }
     };
     // bf16: the exponent that a tile's largest value is taken to have, K's and V's: put to 2^8, so that it may be
@@ -493,19 +517,22 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
 #pragma unroll 1
     for (int n = 0; n < tiles; ++n) {
       const int entry = n % kEntries;
-#pragma unroll
+#pragma unroll 1
       for (int operand = 0; operand < 2; ++operand) {
         const uint32_t stage = (operand ? v_at : k_at) + (n & 1) * W::kOperand;
         if (n >= 2) wait(operand ? &v_empty[n & 1] : &k_empty[n & 1], (n >> 1) - 1);
         uint32_t largest = 0;
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < W::kBatches; ++half) {
           if constexpr (!W::kBf16) {
             if (operand == 0) {
-              k_steps[entry][tid] = step_held[0];
-              v_steps[entry][tid] = at_least(step_held[1], kLeastStep);
-              const uint32_t m = __reduce_max_sync(kFullMask, __float_as_uint(step_held[1]));
-              if (lane == 0) v_most[entry][warp - 8] = __uint_as_float(m);
+              if (tid < 128) {
+                k_steps[entry][tid] = step_held;
+              } else {
+                v_steps[entry][tid - 128] = at_least(step_held, kLeastStep);
+                const uint32_t m = __reduce_max_sync(kFullMask, __float_as_uint(step_held));
+                if (lane == 0) v_most[entry][warp - kBring - 4] = __uint_as_float(m);
+              }
             }
           }
           // as a piece is laid down the next batch's is asked for
@@ -523,9 +550,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         }
         if constexpr (W::kBf16) {
           const uint32_t m = __reduce_max_sync(kFullMask, max(largest & 0xffffu, largest >> 16));
-          if (lane == 0) tops[operand][warp - 8] = m;
-          tc::named_bar_sync(2, 128);
-          const int e = (int)(max(max(tops[operand][0], tops[operand][1]), max(tops[operand][2], tops[operand][3])) >> 7);
+          if (lane == 0) tops[operand][warp - kBring] = m;
+          tc::named_bar_sync(2, kBringThreads);
+          const int e = (int)(__reduce_max_sync(kFullMask, tops[operand][lane & 7]) >> 7);
           if (e > taken[operand] + 6 || (e > 0 && e < taken[operand] - 8)) {
             taken[operand] = max(30, min(230, e));
             const float scale = power2(135 - taken[operand]);
@@ -544,7 +571,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegisters));
-    if (warp == 12) {
+    if (warp == kIssue) {
       // ----------------------------------------------------- S = Q K^T
       if (lane == 0) {
         const uint32_t idesc = tc::make_idesc(kRows, kTile);
@@ -572,7 +599,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         tc::mma_commit(&drained[0]);
         drain(&drained[0], status);
       }
-    } else if (warp == 13) {
+    } else if (warp == kIssue + 1) {
       // ----------------------------------------------------- O = P V
       if (lane == 0) {
         constexpr uint32_t kAcross = 1u << 16;
@@ -599,7 +626,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         tc::mma_commit(&drained[1]);
         drain(&drained[1], status);
       }
-    } else if (warp == 14) {
+    } else if (warp == kIssue + 2) {
       // ----------------------------------------------------- pages
       const int32_t* table = a.table + b * a.table_stride;
       const int64_t head_row = (int64_t)hk << c.page_shift;
@@ -629,7 +656,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kIssue) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
@@ -642,7 +669,10 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, Shares sh, int64
   const auto kernel = prefix_wide_kernel<FORMAT, DT>;
   static thread_local int configured_device = -1;
   if (configured_device != dev.device) {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);
+    cudaFuncAttributes built;
+    cudaError_t err = cudaFuncGetAttributes(&built, kernel);
+    if (err == cudaSuccess && built.numRegs != kLaunchRegisters) err = cudaErrorInvalidKernelImage;  // what its groups share out
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);
     if (err != cudaSuccess) return err;
     configured_device = dev.device;
   }
