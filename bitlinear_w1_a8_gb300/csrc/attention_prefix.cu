@@ -33,9 +33,27 @@ constexpr int kEntries = 8;             // tiles whose pages and steps are known
 constexpr int kPanel = 128 * 128;       // bytes of 128 rows of 64 fp16 values
 constexpr float kTarget = 12.0f, kMost = 15.0f;  // log2 of the largest weight: where the reference puts it, what moves it
 // Registers a thread: at the launch, and as the groups of warps then share them out.
-constexpr int kLaunchRegisters = 96, kAddRegisters = 176, kBringRegisters = 48, kIssueRegisters = 32;
+constexpr int kLaunchRegisters = 96, kAddRegisters = 184, kBringRegisters = 40, kIssueRegisters = 32;
 static_assert(256 * kAddRegisters + kBringThreads * kBringRegisters + 128 * kIssueRegisters <= kWideThreads * kLaunchRegisters,
               "more registers than were launched with would be waited for");
+
+struct Entry {
+  int64_t row[kTile / 16];  // of each 16 tokens: ((page * heads) + head) * page_size + offset, or -1
+};
+
+// What the roles tell each other.
+template <bool BF16>
+struct State {
+  float k_steps[kEntries][BF16 ? 4 : kTile], v_steps[kEntries][BF16 ? 4 : kTile];  // bf16: a tile's power of two, first
+  float v_most[kEntries][4];
+  Entry entries[kEntries];
+  float row_scales[kRows];
+  uint32_t tops[2][8];
+  unsigned long long meta_full[kEntries], meta_empty[kEntries], raw_full[4], raw_empty[4], stage_full[4], stage_empty[4], s_full[2], p_full[2],
+      o_full[2], q_full, drained[2];
+  uint32_t entry_ok[kEntries], tmem_at;
+  int abort_flag;
+};
 
 template <int FORMAT, int DT>
 struct Wide {
@@ -45,14 +63,12 @@ struct Wide {
   static constexpr int kOperand = kPanels * kPanel;
   static constexpr int kLanes = 8 * kBytes;            // lanes of a token's row, 16 bytes each
   static constexpr int kPieces = DT * kBytes / 16;     // of them that a row fills
-  static constexpr int kTurn = kBringThreads / kLanes; // tokens that come at once
-  static constexpr int kBatch = 4;                     // turns that a thread holds at once
-  static constexpr int kBatches = kTile / (kTurn * kBatch);
-  static constexpr int kSmem = 6 * kOperand + 1024;    // Q's parts, two K, two V; the base is rounded up to 1024
-};
-
-struct Entry {
-  int64_t row[kTile / 16];  // of each 16 tokens: ((page * heads) + head) * page_size + offset, or -1
+  static constexpr int kTurn = kBringThreads / kLanes; // tokens that are widened at once
+  static constexpr int kStages = 3;                    // K and V tiles as operands
+  static constexpr int kRaw = kTile * DT * kBytes;     // and as they come, rows of the cache's size side by side
+  static constexpr int kRaws = kBf16 ? 2 : 3;
+  static constexpr int kOperands = 2 * kOperand + kStages * kOperand + kRaws * kRaw;  // Q's parts first
+  static constexpr int kSmem = kOperands + (int)sizeof(State<kBf16>) + 1024;          // the base is rounded up to 1024
 };
 
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
@@ -96,23 +112,6 @@ __device__ __forceinline__ uint32_t of_panel(int row, int dim) {  // where a 16-
   return (uint32_t)((dim >> 6) * kPanel + row * 128 + ((((dim >> 3) & 7) ^ (row & 7)) << 4));
 }
 
-// Zeros, or what is at p: in its place among the stores, and no branch (behind one it would be waited for).
-__device__ __forceinline__ uint4 load16(const void* p, bool have) {
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-      "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(p), "r"((uint32_t)have));
-  return v;
-}
-
-__device__ __forceinline__ float load4(const float* p, bool have) {
-  float v;
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t@p ld.global.nc.f32 %0, [%1];\n\t}" : "=&f"(v) : "l"(p), "r"((uint32_t)have));
-  return v;
-}
-
 // The bounded wait of tc_util.cuh, inlined whole: a call has no place where warps' registers differ.
 __device__ __forceinline__ bool wait_bounded(unsigned long long* bar, uint32_t parity, int* abort_flag, int* status) {
   if (tc::mbar_try_wait(bar, parity)) return true;
@@ -132,10 +131,10 @@ __device__ __forceinline__ bool wait_bounded(unsigned long long* bar, uint32_t p
 }
 
 // Waits, with the same limit, for what this thread has issued, also after others have given up.
-__device__ __forceinline__ void drain(unsigned long long* bar, int* status) {
+__device__ __forceinline__ void drain(unsigned long long* bar, uint32_t parity, int* status) {
   const unsigned long long t0 = tc::global_timer();
 #pragma unroll 1
-  for (uint32_t i = 0; !tc::mbar_try_wait(bar, 0); ++i) {
+  for (uint32_t i = 0; !tc::mbar_try_wait(bar, parity); ++i) {
     if ((i & 63u) == 63u && tc::global_timer() - t0 > tc::kTimeoutNs) {
       atomicExch(status, (int)BITLINEAR_ERR_TIMEOUT);
       return;
@@ -147,39 +146,33 @@ template <int FORMAT, int DT>
 __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs a, KvPages c, Shares sh, int* status) {
   using W = Wide<FORMAT, DT>;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(16) float k_steps[kEntries][W::kBf16 ? 4 : kTile], v_steps[kEntries][W::kBf16 ? 4 : kTile];
-  __shared__ __align__(16) float v_most[kEntries][4];
-  __shared__ float row_scales[kRows];
-  __shared__ __align__(16) Entry entries[kEntries];
-  __shared__ uint32_t entry_ok[kEntries];
-  __shared__ uint32_t tops[2][8];
-  __shared__ __align__(8) unsigned long long meta_full[kEntries], meta_empty[kEntries], k_full[2], k_empty[2], v_full[2], v_empty[2],
-      s_full[2], p_full[2], o_full[2], q_full, drained[2];
-  __shared__ uint32_t tmem_at;
-  __shared__ int abort_flag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = c.head_dim;
   const uint32_t base = ((uint32_t)__cvta_generic_to_shared(raw) + 1023u) & ~1023u;
-  const uint32_t q_at = base, k_at = base + 2 * W::kOperand, v_at = base + 4 * W::kOperand;
+  const uint32_t q_at = base, stage_at = base + 2 * W::kOperand, raw_at = stage_at + W::kStages * W::kOperand;
+  State<W::kBf16>& st = *reinterpret_cast<State<W::kBf16>*>(raw + (base - (uint32_t)__cvta_generic_to_shared(raw)) + W::kOperands);
 
   if (warp == kIssue + 3 && lane == 0) {
-    abort_flag = 0;
+    st.abort_flag = 0;
 #pragma unroll 1
     for (int i = 0; i < kEntries; ++i) {
-      tc::mbar_init(&meta_full[i], 1);
-      tc::mbar_init(&meta_empty[i], 4);
+      tc::mbar_init(&st.meta_full[i], 1);
+      tc::mbar_init(&st.meta_empty[i], 4);
+    }
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&st.raw_full[i], 1);
+      tc::mbar_init(&st.raw_empty[i], kBringThreads / 32);
+      tc::mbar_init(&st.stage_full[i], kBringThreads / 32);
+      tc::mbar_init(&st.stage_empty[i], 1);
     }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&k_full[i], kBringThreads / 32);
-      tc::mbar_init(&v_full[i], kBringThreads / 32);
-      tc::mbar_init(&p_full[i], 4);
-      tc::mbar_init(&k_empty[i], 1);
-      tc::mbar_init(&v_empty[i], 1);
-      tc::mbar_init(&s_full[i], 1);
-      tc::mbar_init(&o_full[i], 1);
-      tc::mbar_init(&drained[i], 1);
+      tc::mbar_init(&st.p_full[i], 4);
+      tc::mbar_init(&st.s_full[i], 1);
+      tc::mbar_init(&st.o_full[i], 1);
+      tc::mbar_init(&st.drained[i], 1);
     }
-    tc::mbar_init(&q_full, 8);
+    tc::mbar_init(&st.q_full, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait_primary();
@@ -201,7 +194,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     part = 0;
     parts = 1;
   }
-  if (warp == kIssue) tc::tmem_alloc(&tmem_at, 512);
+  if (warp == kIssue) tc::tmem_alloc(&st.tmem_at, 512);
   if (part == 0 && threadIdx.x == 0) sh.rows[b * sh.rows_a_seq + row] = make_int2(blockIdx.x, parts);
   const int hk = row / sh.groups, first_head = (row - hk * sh.groups) * kRows, heads = min(kRows, sh.group - first_head);
   uint32_t len;
@@ -221,14 +214,22 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = tmem_at;
+  const uint32_t tmem = st.tmem_at;
   auto s_of = [&](int par) { return tmem + par * 128; };
   auto o_of = [&](int par) { return tmem + 256 + par * 128; };
+
+  // K and V tiles take turns in one ring, in the order in which they are used: K0 K1 V0 K2 V1 ... and the last V.
+  auto place_of_k = [&](int n) { return n == 0 ? 0 : 2 * n - 1; };
+  auto place_of_v = [&](int n) { return n + 1 < tiles ? 2 * n + 2 : 2 * n + 1; };
+  auto at_place = [&](int i, int& operand, int& n) {
+    operand = i > 0 && ((i & 1) == 0 || i == 2 * tiles - 1);
+    n = operand ? (i == 2 * tiles - 1 ? tiles - 1 : i / 2 - 1) : (i + 1) / 2;
+  };
 
   // Every role runs through all of its tiles, also after a wait has run out (`alive` false): it then
   // waits and reads no more, and still arrives wherever others count it.
   bool alive = true;
-  auto wait = [&](unsigned long long* bar, int phase) { alive = alive && wait_bounded(bar, phase & 1, &abort_flag, status); };
+  auto wait = [&](unsigned long long* bar, int phase) { alive = alive && wait_bounded(bar, phase & 1, &st.abort_flag, status); };
 
   if (warp < kBring) {
     // ------------------------------------------------------- logits to weights, sums
@@ -274,15 +275,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
             asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(lead[0]), "r"(lead[1]) : "memory");
             asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + W::kOperand), "r"(rest[0]), "r"(rest[1]) : "memory");
           }
-          if (lane == 0) row_scales[i] = power2(e - 13);
+          if (lane == 0) st.row_scales[i] = power2(e - 13);
         }
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&q_full);
+      if (lane == 0) tc::mbar_arrive(&st.q_full);
     }
     tc::named_bar_sync(1, 256);
-    const float row_scale = row_scales[r];
+    const float row_scale = st.row_scales[r];
     const bool none = (warp & 3) * 32 >= heads;  // rows of no q head: whatever comes of them is theirs
     const uint32_t row_end = there ? min(len, (uint32_t)max(0, sh.lengths[seq])) : 0u;
 
@@ -296,31 +297,30 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     for (int n = par; n < tiles; n += 2) {
       const int entry = n % kEntries;
       const uint32_t t0 = begin + n * kTile;
-      wait(&s_full[par], n >> 1);
-      if constexpr (W::kBf16) wait(&v_full[par], n >> 1);  // the values' power of two
+      wait(&st.s_full[par], n >> 1);
+      if constexpr (W::kBf16) wait(&st.stage_full[place_of_v(n) % W::kStages], place_of_v(n) / W::kStages);  // the values' power of two
       if (none) {
         if (lane == 0) {
-          tc::mbar_arrive(&p_full[par]);
-          tc::mbar_arrive(&meta_empty[entry]);
+          tc::mbar_arrive(&st.p_full[par]);
+          tc::mbar_arrive(&st.meta_empty[entry]);
         }
-        wait(&o_full[par], n >> 1);
+        wait(&st.o_full[par], n >> 1);
         continue;
       }
       tc::tc_fence_after();
       const uint32_t s_at = s_of(par) + lanes;
       // the columns that count: all of them, or the first `count` of those 16 whose page is there
-      const uint32_t ok = alive ? entry_ok[entry] : 0u;
+      const uint32_t ok = alive ? st.entry_ok[entry] : 0u;
       const int count = row_end > t0 ? (int)min((uint32_t)kTile, row_end - t0) : 0;
       const bool whole = __all_sync(kFullMask, ok == 0xffu && count == kTile);
-      const uint32_t ks = (uint32_t)__cvta_generic_to_shared(k_steps[entry]), vs = (uint32_t)__cvta_generic_to_shared(v_steps[entry]);
-      const float4 vm = lds_float4((uint32_t)__cvta_generic_to_shared(v_most[entry]));
+      const uint32_t ks = (uint32_t)__cvta_generic_to_shared(st.k_steps[entry]), vs = (uint32_t)__cvta_generic_to_shared(st.v_steps[entry]);
+      const float4 vm = lds_float4((uint32_t)__cvta_generic_to_shared(st.v_most[entry]));
       const float v_top = at_least(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), kLeastStep);
       float unit = row_scale;
-      if constexpr (W::kBf16) unit = fmaxf(unit * k_steps[entry][0], 1.1754944e-38f);  // a masked logit times 0 is none
+      if constexpr (W::kBf16) unit = fmaxf(unit * st.k_steps[entry][0], 1.1754944e-38f);  // a masked logit times 0 is none
       // 16 logits (over `unit`) of granule g; loops over granules stay rolled up: code is fetched as it runs, and
       // unrolled these took three times as long
       auto logits = [&](int g, uint32_t (&s)[16], float2 (&x)[8]) {
-        tmem_loaded(s);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
         if constexpr (!W::kBf16) {
@@ -340,17 +340,41 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
           }
         }
       };
+      // the next granule is on its way while this one is worked on, where the registers allow it
+      auto granules = [&](auto ahead, auto work) {
+        if constexpr (!decltype(ahead)::value) {
+#pragma unroll 1
+          for (int g = 0; g < kTile / 16; ++g) {
+            uint32_t s[16];
+            float2 x[8];
+            tmem_load16(s_at + 16 * g, s);
+            tmem_loaded(s);
+            logits(g, s, x);
+            work(g, x);
+          }
+          return;
+        }
+        uint32_t s0[16], s1[16];
+        tmem_load16(s_at, s0);
+#pragma unroll 1
+        for (int g = 0; g < kTile / 16; g += 2) {
+          float2 x[8];
+          tmem_loaded(s0);
+          tmem_load16(s_at + 16 * g + 16, s1);
+          logits(g, s0, x);
+          work(g, x);
+          tmem_loaded(s1);
+          if (g + 2 < kTile / 16) tmem_load16(s_at + 16 * g + 32, s0);
+          logits(g + 1, s1, x);
+          work(g + 1, x);
+        }
+      };
       // the row's largest
       float top = -INFINITY;
-#pragma unroll 1
-      for (int g = 0; g < kTile / 16; ++g) {
-        uint32_t s[16];
-        float2 x[8];
-        tmem_load16(s_at + 16 * g, s);
-        logits(g, s, x);
+      granules(std::bool_constant<DT <= 112>(), [&](int, float2 (&x)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
-      }
+      });
       top = top * unit + log2_of(v_top);  // of a weight
       if (top > ref + kMost) {
         const float next = top - kTarget, down = exp2_of(ref - next);  // 0 from the first reference
@@ -360,12 +384,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         for (int i = 0; i < DT / 2; ++i) out[i] = mul2(out[i], both(down));
       }
       float2 more = both(0.0f);
-#pragma unroll 1
-      for (int g = 0; g < kTile / 16; ++g) {
-        uint32_t s[16], w[16];
-        float2 x[8];
-        tmem_load16(s_at + 16 * g, s);
-        logits(g, s, x);
+      granules(std::bool_constant<DT <= 96>(), [&](int g, float2 (&x)[8]) {
+        uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           x[i] = fma2(x[i], both(unit), both(-ref));
@@ -386,33 +406,34 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
 #pragma unroll
         for (int i = 0; i < 8; ++i) parts_of(x[i], w[i], w[8 + i]);
         tc::tmem_st16(s_at + 16 * g, w);
-      }
+      });
       tc::tmem_st_wait();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        tc::mbar_arrive(&p_full[par]);
-        tc::mbar_arrive(&meta_empty[entry]);
+        tc::mbar_arrive(&st.p_full[par]);
+        tc::mbar_arrive(&st.meta_empty[entry]);
       }
       sums = add2(sums, more);
-      wait(&o_full[par], n >> 1);
+      wait(&st.o_full[par], n >> 1);
       tc::tc_fence_after();
+      uint32_t o[2][16];
+      tmem_load16(o_of(par) + lanes, o[0]);
 #pragma unroll
       for (int g = 0; g < DT / 16; ++g) {
-        uint32_t o[16];
-        tmem_load16(o_of(par) + lanes + 16 * g, o);
-        tmem_loaded(o);
+        tmem_loaded(o[g & 1]);
+        if (g + 1 < DT / 16) tmem_load16(o_of(par) + lanes + 16 * (g + 1), o[(g + 1) & 1]);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          out[8 * g + i] = add2(out[8 * g + i], make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])));
+          out[8 * g + i] = add2(out[8 * g + i], make_float2(__uint_as_float(o[g & 1][2 * i]), __uint_as_float(o[g & 1][2 * i + 1])));
       }
     }
     // The two groups' sums meet in what was K's and V's place: [dim][row], 129 apart, then references and sums.
     // Each group gives the other half of its dims and joins the other half of the other's.
     float sum = sums.x + sums.y;
     constexpr int kApart = kRows + 1, kHalf = DT / 4;  // in pairs of dims
-    const uint32_t meet = k_at + 4 * r, scales = k_at + DT * kApart * 4;
-    static_assert((DT * kApart + 4 * kRows) * 4 <= 4 * W::kOperand, "what is joined fits where K and V were");
+    const uint32_t meet = stage_at + 4 * r, scales = stage_at + DT * kApart * 4;
+    static_assert((DT * kApart + 4 * kRows) * 4 <= W::kStages * W::kOperand + W::kRaws * W::kRaw, "what is joined fits where K and V were");
     auto store = [](uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); };
     auto give = [&](auto half) {
       constexpr int h = decltype(half)::value;
@@ -453,120 +474,97 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     tc::named_bar_sync(1, 256);
     float* slot = sh.parts + (int64_t)blockIdx.x * sh.slot_heads * (D + 4);
     for (int i = warp; i < heads; i += 8) {
-      for (int d = lane; d < D; d += 32) slot[i * (D + 4) + d] = lds_float(k_at + (d * kApart + i) * 4);
+      for (int d = lane; d < D; d += 32) slot[i * (D + 4) + d] = lds_float(stage_at + (d * kApart + i) * 4);
       if (lane == 0) *reinterpret_cast<float2*>(slot + i * (D + 4) + D) = lds_float2(scales + 16 * i);
     }
   } else if (warp < kIssue) {
     // ------------------------------------------------------- keys and values, widened
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBringRegisters));
     const int tid = threadIdx.x - 32 * kBring;
-    constexpr int kB = W::kBatch, kDims = 16 / W::kBytes;
-    uint4 held[kB];
-    float step_held = 0.0f;
-    // A thread brings the same 16 bytes of every kTurn-th token's row.
+    constexpr int kDims = 16 / W::kBytes, kTurns = kTile / W::kTurn;
+    // A thread takes the same 16 bytes of every kTurn-th token's row.
     const int of_turn = tid / W::kLanes, chunk = tid % W::kLanes, row_bytes = D * W::kBytes;
     const bool loads = chunk * kDims < D, stores = chunk < W::kPieces, turned = !W::kBf16 && (chunk & 4);
     // and 128 kTurn bytes on for each turn; the second panel's pieces go in the other order, so that each
     // eighth of a store meets every bank once
     const uint32_t place = of_panel(of_turn, kDims * chunk) ^ (turned ? 16 : 0);
-    // the i-th of tile n's keys (operand 0) or values; zeros for a token that is not there
-    auto piece = [&](int n, int operand, int i) {
-      const int64_t first = entries[n % kEntries].row[(i * W::kTurn + of_turn) >> 4];
-      const bool have = alive && n < tiles && first >= 0 && loads && i * W::kTurn + of_turn < (int)(len - begin) - n * kTile;
-      const uint8_t* from = static_cast<const uint8_t*>(operand ? c.v : c.k);
-      return load16(from + (first + ((i * W::kTurn + of_turn) & 15)) * row_bytes + 16 * chunk, have);
-    };
-    auto begin_tile = [&](int n) {  // before the first piece of a tile is asked for
-      if (n >= tiles) return;
-      wait(&meta_full[n % kEntries], n / kEntries);
-      if constexpr (!W::kBf16) {  // a thread has a step of one token, a key's or a value's
-        const int token = tid & 127;
-        const int64_t first = entries[n % kEntries].row[token >> 4];
-        const bool have = alive && first >= 0 && token < (int)(len - begin) - n * kTile;
-        step_held = load4((tid < 128 ? c.k_step : c.v_step) + first + (token & 15), have);
-      }
-    };
-    auto put = [&](uint32_t stage, int i, const uint4& w, float scale) {
-      uint32_t h[8];
-      if (!stores) return;
-      const uint32_t first = stage + place + i * W::kTurn * 128;
-      if constexpr (W::kBf16) {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = mul2(make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u)), both(scale));
-          const __half2 x = __floats2half2_rn(f.x, f.y);
-          h[j] = *reinterpret_cast<const uint32_t*>(&x);
-        }
-        tc::st_shared_v4(first, h[0], h[1], h[2], h[3]);
-      } else {
-        widen<FORMAT>(turned ? w.z : w.x, h[0], h[1]);
-        widen<FORMAT>(turned ? w.w : w.y, h[2], h[3]);
-        widen<FORMAT>(turned ? w.x : w.z, h[4], h[5]);
-        widen<FORMAT>(turned ? w.y : w.w, h[6], h[7]);
-        tc::st_shared_v4(first, h[0], h[1], h[2], h[3]);
-        tc::st_shared_v4(first ^ 16, h[4], h[5], h[6], h[7]);
-      }
-    };
     // bf16: the exponent that a tile's largest value is taken to have, K's and V's: put to 2^8, so that it may be
     // 2^7 more, or 2^8 less, before the tile is done again with its own
     int taken[2] = {127, 127};
-    begin_tile(0);
+#pragma unroll 1
+    for (int i = 0; i < 2 * tiles; ++i) {
+      int operand, n;
+      at_place(i, operand, n);
+      const int entry = n % kEntries, stage = i % W::kStages, slot = i % W::kRaws;
+      const uint32_t to = stage_at + stage * W::kOperand + place, from = raw_at + slot * W::kRaw + of_turn * row_bytes + 16 * chunk;
+      wait(&st.raw_full[slot], i / W::kRaws);
+      // the tokens that are there: of a turn's 16 the page, and the first `count`
+      const uint32_t ok = alive ? st.entry_ok[entry] : 0u;
+      const int count = (int)(len - begin) - n * kTile;
+      if constexpr (!W::kBf16) {  // their steps, of the operand that comes
+        if (tid < kTile) {
+          float* steps = operand ? st.v_steps[entry] : st.k_steps[entry];
+          float step = tid < count && ((ok >> (tid >> 4)) & 1u) ? steps[tid] : 0.0f;
+          if (operand) {
+            const uint32_t m = __reduce_max_sync(kFullMask, __float_as_uint(step));
+            if (lane == 0) st.v_most[entry][warp - kBring] = __uint_as_float(m);
+            step = at_least(step, kLeastStep);
+          }
+          steps[tid] = step;
+        }
+      }
+      if (i >= W::kStages) wait(&st.stage_empty[stage], i / W::kStages - 1);
+      uint32_t largest = 0;
+      const int mine = operand ? taken[1] : taken[0];
+      auto widen_turns = [&](float scale) {
 #pragma unroll
-    for (int i = 0; i < kB; ++i) held[i] = piece(0, 0, i);
-#pragma unroll 1
-    for (int n = 0; n < tiles; ++n) {
-      const int entry = n % kEntries;
-#pragma unroll 1
-      for (int operand = 0; operand < 2; ++operand) {
-        const uint32_t stage = (operand ? v_at : k_at) + (n & 1) * W::kOperand;
-        if (n >= 2) wait(operand ? &v_empty[n & 1] : &k_empty[n & 1], (n >> 1) - 1);
-        uint32_t largest = 0;
-#pragma unroll 1
-        for (int half = 0; half < W::kBatches; ++half) {
-          if constexpr (!W::kBf16) {
-            if (operand == 0) {
-              if (tid < 128) {
-                k_steps[entry][tid] = step_held;
-              } else {
-                v_steps[entry][tid - 128] = at_least(step_held, kLeastStep);
-                const uint32_t m = __reduce_max_sync(kFullMask, __float_as_uint(step_held));
-                if (lane == 0) v_most[entry][warp - kBring - 4] = __uint_as_float(m);
-              }
+        for (int t = 0; t < kTurns; ++t) {
+          const int token = t * W::kTurn + of_turn;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (loads && token < count && ((ok >> (token >> 4)) & 1u)) w = lds128(from + t * W::kTurn * row_bytes);
+          if (!stores) continue;
+          uint32_t h[8];
+          if constexpr (W::kBf16) {
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = mul2(make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u)), both(scale));
+              const __half2 x = __floats2half2_rn(f.x, f.y);
+              h[j] = *reinterpret_cast<const uint32_t*>(&x);
+              largest = __vmaxu2(largest, u[j] & 0x7fff7fffu);
             }
+          } else {
+            widen<FORMAT>(turned ? w.z : w.x, h[0], h[1]);
+            widen<FORMAT>(turned ? w.w : w.y, h[2], h[3]);
+            widen<FORMAT>(turned ? w.x : w.z, h[4], h[5]);
+            widen<FORMAT>(turned ? w.y : w.w, h[6], h[7]);
+            tc::st_shared_v4((to + t * W::kTurn * 128) ^ 16, h[4], h[5], h[6], h[7]);
           }
-          // as a piece is laid down the next batch's is asked for
-          const bool last = half + 1 == W::kBatches;
-          const int next = last && operand == 1 ? n + 1 : n, next_operand = last ? 1 - operand : operand, next_half = last ? 0 : half + 1;
-          if (last && operand == 1) begin_tile(next);
-          const float scale = W::kBf16 ? power2(135 - taken[operand]) : 1.0f;
-#pragma unroll
-          for (int i = 0; i < kB; ++i) {
-            if constexpr (W::kBf16)
-              largest = __vmaxu2(largest, __vmaxu2(__vmaxu2(held[i].x & 0x7fff7fffu, held[i].y & 0x7fff7fffu), __vmaxu2(held[i].z & 0x7fff7fffu, held[i].w & 0x7fff7fffu)));
-            put(stage, half * kB + i, held[i], scale);
-            held[i] = piece(next, next_operand, next_half * kB + i);
-          }
+          tc::st_shared_v4(to + t * W::kTurn * 128, h[0], h[1], h[2], h[3]);
         }
-        if constexpr (W::kBf16) {
-          const uint32_t m = __reduce_max_sync(kFullMask, max(largest & 0xffffu, largest >> 16));
-          if (lane == 0) tops[operand][warp - kBring] = m;
-          tc::named_bar_sync(2, kBringThreads);
-          const int e = (int)(__reduce_max_sync(kFullMask, tops[operand][lane & 7]) >> 7);
-          if (e > taken[operand] + 6 || (e > 0 && e < taken[operand] - 8)) {
-            taken[operand] = max(30, min(230, e));
-            const float scale = power2(135 - taken[operand]);
-#pragma unroll 1
-            for (int i = 0; i < kB * W::kBatches; ++i) put(stage, i, piece(n, operand, i), scale);
-          }
-          if (tid == 0) {
-            (operand ? v_most[entry] : k_steps[entry])[0] = power2(taken[operand] - 135);
-            if (operand) v_most[entry][1] = v_most[entry][2] = v_most[entry][3] = 0.0f;
-          }
+      };
+      widen_turns(W::kBf16 ? power2(135 - mine) : 1.0f);
+      if constexpr (W::kBf16) {
+        const uint32_t m = __reduce_max_sync(kFullMask, max(largest & 0xffffu, largest >> 16));
+        if (lane == 0) st.tops[i & 1][warp - kBring] = m;
+        tc::named_bar_sync(2, kBringThreads);
+        const int e = (int)(__reduce_max_sync(kFullMask, st.tops[i & 1][lane & 7]) >> 7);
+        int used = mine;
+        if (e > mine + 6 || (e > 0 && e < mine - 8)) {
+          used = max(30, min(230, e));
+          widen_turns(power2(135 - used));
+          (operand ? taken[1] : taken[0]) = used;
         }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(operand ? &v_full[n & 1] : &k_full[n & 1]);
+        if (tid == 0) {
+          (operand ? st.v_most[entry] : st.k_steps[entry])[0] = power2(used - 135);
+          if (operand) st.v_most[entry][1] = st.v_most[entry][2] = st.v_most[entry][3] = 0.0f;
+        }
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&st.stage_full[stage]);
+        tc::mbar_arrive(&st.raw_empty[slot]);
       }
     }
   } else {
@@ -575,11 +573,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       // ----------------------------------------------------- S = Q K^T
       if (lane == 0) {
         const uint32_t idesc = tc::make_idesc(kRows, kTile);
-        wait(&q_full, 0);
+        wait(&st.q_full, 0);
 #pragma unroll 1
         for (int n = 0; n < tiles; ++n) {
-          wait(&k_full[n & 1], n >> 1);
-          if (n >= 2) wait(&o_full[n & 1], (n >> 1) - 1);  // the weights that lie over the last S of this place are used
+          const int at = place_of_k(n), stage = at % W::kStages;
+          wait(&st.stage_full[stage], at / W::kStages);
+          if (n >= 2) wait(&st.o_full[n & 1], (n >> 1) - 1);  // the weights that lie over the last S of this place are used
           if (alive) {
             tc::tc_fence_after();
             uint32_t add = 0;
@@ -588,16 +587,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
 #pragma unroll
               for (int k = 0; k < DT / 16; ++k) {
                 const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
-                mma_f16_ss(s_of(n & 1), tc::smem_desc_sw128(q_at + part * W::kOperand + off), tc::smem_desc_sw128(k_at + (n & 1) * W::kOperand + off), idesc, add);
+                mma_f16_ss(s_of(n & 1), tc::smem_desc_sw128(q_at + part * W::kOperand + off), tc::smem_desc_sw128(stage_at + stage * W::kOperand + off), idesc, add);
                 add = 1;
               }
             }
-            tc::mma_commit(&s_full[n & 1]);
-            tc::mma_commit(&k_empty[n & 1]);
+            tc::mma_commit(&st.s_full[n & 1]);
+            tc::mma_commit(&st.stage_empty[stage]);
           }
         }
-        tc::mma_commit(&drained[0]);
-        drain(&drained[0], status);
+        tc::mma_commit(&st.drained[0]);
+        drain(&st.drained[0], 0, status);
       }
     } else if (warp == kIssue + 1) {
       // ----------------------------------------------------- O = P V
@@ -606,8 +605,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         const uint32_t idesc = tc::make_idesc(kRows, DT) | kAcross;
 #pragma unroll 1
         for (int n = 0; n < tiles; ++n) {
-          wait(&v_full[n & 1], n >> 1);
-          wait(&p_full[n & 1], n >> 1);
+          const int at = place_of_v(n), stage = at % W::kStages;
+          wait(&st.stage_full[stage], at / W::kStages);
+          wait(&st.p_full[n & 1], n >> 1);
           if (alive) {
             tc::tc_fence_after();
             uint32_t add = 0;
@@ -615,16 +615,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
             for (int part = 1; part >= 0; --part) {
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k) {
-                tc::mma_f16_ta(o_of(n & 1), s_of(n & 1) + 16 * k + 8 * part, across_desc(v_at + (n & 1) * W::kOperand + k * 2048), idesc, add);
+                tc::mma_f16_ta(o_of(n & 1), s_of(n & 1) + 16 * k + 8 * part, across_desc(stage_at + stage * W::kOperand + k * 2048), idesc, add);
                 add = 1;
               }
             }
-            tc::mma_commit(&o_full[n & 1]);
-            tc::mma_commit(&v_empty[n & 1]);
+            tc::mma_commit(&st.o_full[n & 1]);
+            tc::mma_commit(&st.stage_empty[stage]);
           }
         }
-        tc::mma_commit(&drained[1]);
-        drain(&drained[1], status);
+        tc::mma_commit(&st.drained[1]);
+        drain(&st.drained[1], 0, status);
       }
     } else if (warp == kIssue + 2) {
       // ----------------------------------------------------- pages
@@ -640,17 +640,45 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
           const int32_t page = table[t >> c.page_shift];
           if (page >= 0 && page < c.num_pages) at = (((int64_t)page * c.heads) << c.page_shift) + head_row + (t & ((1u << c.page_shift) - 1));
         }
-        if (n >= kEntries) wait(&meta_empty[entry], n / kEntries - 1);
-        if (lane < 8) entries[entry].row[half] = at;
+        if (n >= kEntries) wait(&st.meta_empty[entry], n / kEntries - 1);
+        if (lane < 8) st.entries[entry].row[half] = at;
         const uint32_t ok = __ballot_sync(kFullMask, at >= 0) & 0xffu;
-        if (lane == 0) entry_ok[entry] = ok;
+        if (lane == 0) st.entry_ok[entry] = ok;
         if (lane < 16 && at >= 0) {  // 16 tokens of a head are one run of bytes
           const uint8_t* from = static_cast<const uint8_t*>(lane < 8 ? c.k : c.v) + at * D * W::kBytes;
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(16 * D * W::kBytes) : "memory");
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&meta_full[entry]);
+        if (lane == 0) tc::mbar_arrive(&st.meta_full[entry]);
       }
+    } else {
+      // ----------------------------------------------------- copies of the cache's rows: a lane 16 tokens, or their steps
+      const int row_bytes = D * W::kBytes, half = lane & 7;
+#pragma unroll 1
+      for (int i = 0; i < 2 * tiles; ++i) {
+        int operand, n;
+        at_place(i, operand, n);
+        const int entry = n % kEntries, slot = i % W::kRaws;
+        if (!operand) wait(&st.meta_full[entry], n / kEntries);
+        if (i >= W::kRaws) wait(&st.raw_empty[slot], i / W::kRaws - 1);
+        const int64_t first = st.entries[entry].row[half];
+        const int rows = min(16, (int)(len - begin) - n * kTile - 16 * half);
+        const bool copies = alive && first >= 0 && rows > 0 && lane < (W::kBf16 ? 8 : 16);
+        const uint32_t bytes = lane < 8 ? rows * row_bytes : 64;
+        const uint32_t all = __reduce_add_sync(kFullMask, copies ? bytes : 0u);
+        if (lane == 0) tc::mbar_arrive_expect_tx(&st.raw_full[slot], all);
+        __syncwarp();
+        if (copies) {
+          if (lane < 8)
+            tc::bulk_copy_g2s(raw_at + slot * W::kRaw + 16 * half * row_bytes, static_cast<const uint8_t*>(operand ? c.v : c.k) + first * row_bytes, bytes, &st.raw_full[slot]);
+          else
+            tc::bulk_copy_g2s((uint32_t)__cvta_generic_to_shared(&(operand ? st.v_steps : st.k_steps)[entry][16 * half]), (operand ? c.v_step : c.k_step) + first, bytes, &st.raw_full[slot]);
+        }
+        __syncwarp();
+      }
+      // none of them is on its way when the CTA ends, also after a wait that has run out
+      if (lane == 0)
+        for (int i = max(0, 2 * tiles - W::kRaws); i < 2 * tiles; ++i) drain(&st.raw_full[i % W::kRaws], (i / W::kRaws) & 1, status);
     }
     __syncwarp();
   }
