@@ -11,10 +11,11 @@
 // Each tile's O starts from zero and is added to fp32 sums in registers: the tensor cores' adder cuts toward
 // zero, and a chain of tiles in it would show.
 //
-// 20 warps: two groups of four that turn logits into weights and add up O, each for every other tile with a reference
-// and sums of its own (a thread is a row: nothing is exchanged until the end); eight that bring K and V,
+// 28 warps: two groups of eight that turn logits into weights and add up O, each for every other tile with a
+// reference and sums of its own (two threads a row, half of a tile's tokens and half of the dims each: they tell each
+// other their largest logits); eight that widen K and V
 // widen the codes and lay them out for the MMA (128-byte swizzle, the same image for both: K is the B
-// operand along its rows, V across them); one that looks pages up, eight tiles ahead, and
+// operand along its rows, V across them); one that looks pages up, four tiles ahead, and
 // asks for them to come into L2; one thread that issues the products of S and one that issues those of O.
 // Two S, two O, two K and two V are in flight; a weight overwrites its logit's place.
 #include "attend.cuh"
@@ -26,15 +27,15 @@ namespace {
 
 constexpr int kRows = kPrefixWide;      // q heads of a CTA: the MMA's rows
 constexpr int kTile = 128;              // tokens
-constexpr int kWideThreads = 640;
-constexpr int kBring = 8, kIssue = 16;  // the first warps that bring keys and values, and that issue
+constexpr int kWideThreads = 896;
+constexpr int kBring = 16, kIssue = 24;  // the first warps that bring keys and values, and that issue
 constexpr int kBringThreads = 256;
-constexpr int kEntries = 8;             // tiles whose pages and steps are known
+constexpr int kEntries = 4;             // tiles whose pages and steps are known
 constexpr int kPanel = 128 * 128;       // bytes of 128 rows of 64 fp16 values
 constexpr float kTarget = 12.0f, kMost = 15.0f;  // log2 of the largest weight: where the reference puts it, what moves it
 // Registers a thread: at the launch, and as the groups of warps then share them out.
-constexpr int kLaunchRegisters = 96, kAddRegisters = 184, kBringRegisters = 40, kIssueRegisters = 32;
-static_assert(256 * kAddRegisters + kBringThreads * kBringRegisters + 128 * kIssueRegisters <= kWideThreads * kLaunchRegisters,
+constexpr int kLaunchRegisters = 72, kAddRegisters = 104, kBringRegisters = 32, kIssueRegisters = 24;
+static_assert(512 * kAddRegisters + kBringThreads * kBringRegisters + 128 * kIssueRegisters <= kWideThreads * kLaunchRegisters,
               "more registers than were launched with would be waited for");
 
 struct Entry {
@@ -47,7 +48,7 @@ struct State {
   float k_steps[kEntries][BF16 ? 4 : kTile], v_steps[kEntries][BF16 ? 4 : kTile];  // bf16: a tile's power of two, first
   float v_most[kEntries][4];
   Entry entries[kEntries];
-  float row_scales[kRows];
+  float row_tops[2][2][kRows];  // by tile's parity and half of its tokens; before the first tile q's scales, in the first
   uint32_t tops[2][8];
   unsigned long long meta_full[kEntries], meta_empty[kEntries], raw_full[4], raw_empty[4], stage_full[4], stage_empty[4], s_full[2], p_full[2],
       o_full[2], q_full, drained[2];
@@ -68,7 +69,10 @@ struct Wide {
   static constexpr int kRaw = kTile * DT * kBytes;     // and as they come, rows of the cache's size side by side
   static constexpr int kRaws = kBf16 ? 2 : 3;
   static constexpr int kOperands = 2 * kOperand + kStages * kOperand + kRaws * kRaw;  // Q's parts first
-  static constexpr int kSmem = kOperands + (int)sizeof(State<kBf16>) + 1024;          // the base is rounded up to 1024
+  static constexpr int kNeed = kOperands + (int)sizeof(State<kBf16>);
+  // the base is rounded up to 1024, where it is not there already (a kernel without static arrays has it there)
+  static constexpr int kSmem = kNeed + 1024 < 232448 ? kNeed + 1024 : 232448;
+  static_assert(kNeed <= 232448, "what a CTA may have");
 };
 
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
@@ -87,6 +91,13 @@ __device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
         "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(at));
+}
+__device__ __forceinline__ void tmem_load8(uint32_t at, uint32_t (&r)[16]) {  // the first 8
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at));
+#pragma unroll
+  for (int i = 8; i < 16; ++i) r[i] = 0;
 }
 // After the wait: the registers of earlier loads are used behind it.
 __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[16]) {
@@ -145,10 +156,16 @@ __device__ __forceinline__ void drain(unsigned long long* bar, uint32_t parity, 
 template <int FORMAT, int DT>
 __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs a, KvPages c, Shares sh, int* status) {
   using W = Wide<FORMAT, DT>;
-  extern __shared__ uint8_t raw[];
+  extern __shared__ __align__(1024) uint8_t raw[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = c.head_dim;
   const uint32_t base = ((uint32_t)__cvta_generic_to_shared(raw) + 1023u) & ~1023u;
   const uint32_t q_at = base, stage_at = base + 2 * W::kOperand, raw_at = stage_at + W::kStages * W::kOperand;
+  uint32_t given;
+  asm volatile("mov.u32 %0, %%dynamic_smem_size;" : "=r"(given));
+  if (base + W::kNeed > (uint32_t)__cvta_generic_to_shared(raw) + given) {  // not where it was expected
+    if (threadIdx.x == 0) atomicExch(status, (int)BITLINEAR_ERR_UNSUPPORTED);
+    return;
+  }
   State<W::kBf16>& st = *reinterpret_cast<State<W::kBf16>*>(raw + (base - (uint32_t)__cvta_generic_to_shared(raw)) + W::kOperands);
 
   if (warp == kIssue + 3 && lane == 0) {
@@ -156,7 +173,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
 #pragma unroll 1
     for (int i = 0; i < kEntries; ++i) {
       tc::mbar_init(&st.meta_full[i], 1);
-      tc::mbar_init(&st.meta_empty[i], 4);
+      tc::mbar_init(&st.meta_empty[i], 8);
     }
 #pragma unroll 1
     for (int i = 0; i < 4; ++i) {
@@ -167,12 +184,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&st.p_full[i], 4);
+      tc::mbar_init(&st.p_full[i], 8);
       tc::mbar_init(&st.s_full[i], 1);
       tc::mbar_init(&st.o_full[i], 1);
       tc::mbar_init(&st.drained[i], 1);
     }
-    tc::mbar_init(&st.q_full, 8);
+    tc::mbar_init(&st.q_full, kBring);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait_primary();
@@ -234,7 +251,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
   if (warp < kBring) {
     // ------------------------------------------------------- logits to weights, sums
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegisters));
-    const int par = warp >> 2, r = threadIdx.x & 127;
+    const int par = warp >> 3, side = (warp >> 2) & 1, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's lanes of TMEM
     const bool there = r < heads;
     const uint32_t of_group = first_head + (there ? r : 0), member = of_group / (uint32_t)sh.heads_a_key;
@@ -244,18 +261,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       const float factor = a.factor, more = a.factor_rest;
       const bool have = 4 * lane < D;
 #pragma unroll 1
-      for (int i0 = warp; i0 < kRows; i0 += 32) {
+      for (int i0 = warp; i0 < kRows; i0 += 4 * kBring) {
         float4 w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int i = i0 + 8 * j;
+          const int i = i0 + kBring * j;
           const uint32_t head = first_head + min(i, heads - 1), who = head / (uint32_t)sh.heads_a_key;
           const float* q = a.q + (b * sh.group_rows + who) * a.q_stride + (int64_t)(hk * sh.heads_a_key + (head - who * sh.heads_a_key)) * D;
           w[j] = have && i < heads ? *reinterpret_cast<const float4*>(q + 4 * lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int i = i0 + 8 * j;
+          const int i = i0 + kBring * j;
           const float2 x = mul2(make_float2(w[j].x, w[j].y), both(factor)), y = mul2(make_float2(w[j].z, w[j].w), both(factor));
           const float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
           const int e = clamp_exponent(exponent_of(__uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(top)))));
@@ -275,51 +292,51 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
             asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(lead[0]), "r"(lead[1]) : "memory");
             asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + W::kOperand), "r"(rest[0]), "r"(rest[1]) : "memory");
           }
-          if (lane == 0) st.row_scales[i] = power2(e - 13);
+          if (lane == 0) st.row_tops[0][0][i] = power2(e - 13);
         }
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&st.q_full);
     }
-    tc::named_bar_sync(1, 256);
-    const float row_scale = st.row_scales[r];
+    tc::named_bar_sync(3, 32 * kBring);
+    const float row_scale = st.row_tops[0][0][r];
+    tc::named_bar_sync(3, 32 * kBring);
     const bool none = (warp & 3) * 32 >= heads;  // rows of no q head: whatever comes of them is theirs
     const uint32_t row_end = there ? min(len, (uint32_t)max(0, sh.lengths[seq])) : 0u;
 
+    constexpr int kSide = kTile / 2, kGranules = kSide / 16;  // tokens of this thread, and 16s of them
+    constexpr int kDims = DT / 2;                             // and dims
     float ref = kUnset;
     float2 sums = both(0.0f);
-    float2 out[DT / 2];
+    float2 out[kDims / 2];
 #pragma unroll
-    for (int i = 0; i < DT / 2; ++i) out[i] = both(0.0f);
+    for (int i = 0; i < kDims / 2; ++i) out[i] = both(0.0f);
+    const uint32_t s_at = s_of(par) + lanes + side * kSide, o_at = o_of(par) + lanes + side * kDims;
 
 #pragma unroll 1
     for (int n = par; n < tiles; n += 2) {
       const int entry = n % kEntries;
-      const uint32_t t0 = begin + n * kTile;
+      const uint32_t t0 = begin + n * kTile + side * kSide;
       wait(&st.s_full[par], n >> 1);
-      if constexpr (W::kBf16) wait(&st.stage_full[place_of_v(n) % W::kStages], place_of_v(n) / W::kStages);  // the values' power of two
       if (none) {
-        if (lane == 0) {
-          tc::mbar_arrive(&st.p_full[par]);
-          tc::mbar_arrive(&st.meta_empty[entry]);
-        }
+        if (lane == 0) tc::mbar_arrive(&st.p_full[par]);
+        tc::named_bar_sync(1 + par, 256);
+        if (lane == 0) tc::mbar_arrive(&st.meta_empty[entry]);
         wait(&st.o_full[par], n >> 1);
         continue;
       }
       tc::tc_fence_after();
-      const uint32_t s_at = s_of(par) + lanes;
       // the columns that count: all of them, or the first `count` of those 16 whose page is there
-      const uint32_t ok = alive ? st.entry_ok[entry] : 0u;
-      const int count = row_end > t0 ? (int)min((uint32_t)kTile, row_end - t0) : 0;
-      const bool whole = __all_sync(kFullMask, ok == 0xffu && count == kTile);
-      const uint32_t ks = (uint32_t)__cvta_generic_to_shared(st.k_steps[entry]), vs = (uint32_t)__cvta_generic_to_shared(st.v_steps[entry]);
-      const float4 vm = lds_float4((uint32_t)__cvta_generic_to_shared(st.v_most[entry]));
-      const float v_top = at_least(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), kLeastStep);
+      const uint32_t ok = alive ? st.entry_ok[entry] >> (kGranules * side) & 0xfu : 0u;
+      const int count = row_end > t0 ? (int)min((uint32_t)kSide, row_end - t0) : 0;
+      const bool whole = __all_sync(kFullMask, ok == 0xfu && count == kSide);
+      const uint32_t ks = (uint32_t)__cvta_generic_to_shared(st.k_steps[entry]) + (W::kBf16 ? 0 : 4 * kSide * side);
+      const uint32_t vs = (uint32_t)__cvta_generic_to_shared(st.v_steps[entry]) + (W::kBf16 ? 0 : 4 * kSide * side);
       float unit = row_scale;
-      if constexpr (W::kBf16) unit = fmaxf(unit * st.k_steps[entry][0], 1.1754944e-38f);  // a masked logit times 0 is none
-      // 16 logits (over `unit`) of granule g; loops over granules stay rolled up: code is fetched as it runs, and
-      // unrolled these took three times as long
+      if constexpr (W::kBf16) unit = fmaxf(unit * lds_float(ks), 1.1754944e-38f);  // a masked logit times 0 is none
+      // The 16 logits (over `unit`) of granule g.  Loops over granules stay rolled up: code is fetched as it runs, and
+      // unrolled they took three times as long.
       auto logits = [&](int g, uint32_t (&s)[16], float2 (&x)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
@@ -340,52 +357,45 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
           }
         }
       };
-      // the next granule is on its way while this one is worked on, where the registers allow it
-      auto granules = [&](auto ahead, auto work) {
-        if constexpr (!decltype(ahead)::value) {
-#pragma unroll 1
-          for (int g = 0; g < kTile / 16; ++g) {
-            uint32_t s[16];
-            float2 x[8];
-            tmem_load16(s_at + 16 * g, s);
-            tmem_loaded(s);
-            logits(g, s, x);
-            work(g, x);
-          }
-          return;
-        }
-        uint32_t s0[16], s1[16];
-        tmem_load16(s_at, s0);
-#pragma unroll 1
-        for (int g = 0; g < kTile / 16; g += 2) {
-          float2 x[8];
-          tmem_loaded(s0);
-          tmem_load16(s_at + 16 * g + 16, s1);
-          logits(g, s0, x);
-          work(g, x);
-          tmem_loaded(s1);
-          if (g + 2 < kTile / 16) tmem_load16(s_at + 16 * g + 32, s0);
-          logits(g + 1, s1, x);
-          work(g + 1, x);
-        }
-      };
       // the row's largest
       float top = -INFINITY;
-      granules(std::bool_constant<DT <= 112>(), [&](int, float2 (&x)[8]) {
+      constexpr int kTogether = DT <= 96 ? 2 : 1;  // granules, as the registers allow
+#pragma unroll 1
+      for (int g = 0; g < kGranules; g += kTogether) {
+        uint32_t s[kTogether][16];
+        float2 x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
-      });
-      top = top * unit + log2_of(v_top);  // of a weight
+        for (int k = 0; k < kTogether; ++k) tmem_load16(s_at + 16 * (g + k), s[k]);
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) tmem_loaded(s[k]);
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) {
+          logits(g + k, s[k], x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
+        }
+      }
+      st.row_tops[par][side][r] = top;
+      wait(&st.stage_full[place_of_v(n) % W::kStages], place_of_v(n) / W::kStages);  // the values' steps
+      tc::named_bar_sync(1 + par, 256);
+      const float4 vm = lds_float4((uint32_t)__cvta_generic_to_shared(st.v_most[entry]));
+      const float v_top = at_least(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), kLeastStep);
+      top = fmaxf(top, st.row_tops[par][1 - side][r]) * unit + log2_of(v_top);  // of a weight
       if (top > ref + kMost) {
         const float next = top - kTarget, down = exp2_of(ref - next);  // 0 from the first reference
         ref = next;
         sums = mul2(sums, both(down));
 #pragma unroll
-        for (int i = 0; i < DT / 2; ++i) out[i] = mul2(out[i], both(down));
+        for (int i = 0; i < kDims / 2; ++i) out[i] = mul2(out[i], both(down));
       }
       float2 more = both(0.0f);
-      granules(std::bool_constant<DT <= 96>(), [&](int g, float2 (&x)[8]) {
-        uint32_t w[16];
+#pragma unroll 1
+      for (int g = 0; g < kGranules; ++g) {
+        uint32_t s[16], w[16];
+        float2 x[8];
+        tmem_load16(s_at + 16 * g, s);
+        tmem_loaded(s);
+        logits(g, s, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           x[i] = fma2(x[i], both(unit), both(-ref));
@@ -406,7 +416,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
 #pragma unroll
         for (int i = 0; i < 8; ++i) parts_of(x[i], w[i], w[8 + i]);
         tc::tmem_st16(s_at + 16 * g, w);
-      });
+      }
       tc::tmem_st_wait();
       tc::tc_fence_before();
       __syncwarp();
@@ -417,28 +427,29 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       sums = add2(sums, more);
       wait(&st.o_full[par], n >> 1);
       tc::tc_fence_after();
-      uint32_t o[2][16];
-      tmem_load16(o_of(par) + lanes, o[0]);
 #pragma unroll
-      for (int g = 0; g < DT / 16; ++g) {
-        tmem_loaded(o[g & 1]);
-        if (g + 1 < DT / 16) tmem_load16(o_of(par) + lanes + 16 * (g + 1), o[(g + 1) & 1]);
+      for (int d = 0; d < kDims; d += 16) {  // 8 or 16 dims
+        uint32_t o[16];
+        if (d + 16 <= kDims)
+          tmem_load16(o_at + d, o);
+        else
+          tmem_load8(o_at + d, o);
+        tmem_loaded(o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          out[8 * g + i] = add2(out[8 * g + i], make_float2(__uint_as_float(o[g & 1][2 * i]), __uint_as_float(o[g & 1][2 * i + 1])));
+        for (int i = 0; i < (d + 16 <= kDims ? 8 : 4); ++i)
+          out[d / 2 + i] = add2(out[d / 2 + i], make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])));
       }
     }
-    // The two groups' sums meet in what was K's and V's place: [dim][row], 129 apart, then references and sums.
-    // Each group gives the other half of its dims and joins the other half of the other's.
-    float sum = sums.x + sums.y;
-    constexpr int kApart = kRows + 1, kHalf = DT / 4;  // in pairs of dims
-    const uint32_t meet = stage_at + 4 * r, scales = stage_at + DT * kApart * 4;
-    static_assert((DT * kApart + 4 * kRows) * 4 <= W::kStages * W::kOperand + W::kRaws * W::kRaw, "what is joined fits where K and V were");
+    // The two groups meet in what was K's and V's place, [dim][row], 129 apart, then references and sums: each
+    // thread gives half of its dims and joins the other half of the other's.
+    constexpr int kApart = kRows + 1, kGiven = kDims / 4;  // in pairs of dims
+    const uint32_t meet = stage_at + (side * kDims * kApart + r) * 4, scales = stage_at + DT * kApart * 4;
+    static_assert((DT * kApart + 8 * kRows) * 4 <= W::kStages * W::kOperand + W::kRaws * W::kRaw, "what is joined fits where K and V were");
     auto store = [](uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); };
     auto give = [&](auto half) {
       constexpr int h = decltype(half)::value;
 #pragma unroll
-      for (int i = h * kHalf; i < (h + 1) * kHalf; ++i) {
+      for (int i = h * kGiven; i < (h + 1) * kGiven; ++i) {
         store(meet + 2 * i * kApart * 4, out[i].x);
         store(meet + (2 * i + 1) * kApart * 4, out[i].y);
       }
@@ -446,36 +457,38 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     auto take = [&](auto half, float mine, float theirs) {
       constexpr int h = decltype(half)::value;
 #pragma unroll
-      for (int i = h * kHalf; i < (h + 1) * kHalf; ++i) {
+      for (int i = h * kGiven; i < (h + 1) * kGiven; ++i) {
         const uint32_t at = meet + 2 * i * kApart * 4;
         store(at, out[i].x * mine + lds_float(at) * theirs);
         store(at + kApart * 4, out[i].y * mine + lds_float(at + kApart * 4) * theirs);
       }
     };
-    tc::named_bar_sync(1, 256);
+    static_assert(kDims % 8 == 0, "whole pairs to give and to take");
+    tc::named_bar_sync(3, 32 * kBring);
     if (par == 0)
       give(std::integral_constant<int, 1>());
     else
       give(std::integral_constant<int, 0>());
-    store(scales + 16 * r + 8 * par, ref);
-    store(scales + 16 * r + 8 * par + 4, sum);
-    tc::named_bar_sync(1, 256);
-    const float2 other = lds_float2(scales + 16 * r + 8 * (1 - par));
-    const float m = fmaxf(ref, other.x), mine = exp2_of(ref - m), theirs = exp2_of(other.x - m);
+    // a row's: [group][reference, sum of one half, sum of the other]
+    if (side == 0) store(scales + 32 * r + 16 * par, ref);
+    store(scales + 32 * r + 16 * par + 4 + 4 * side, sums.x + sums.y);
+    tc::named_bar_sync(3, 32 * kBring);
+    const float4 first = lds_float4(scales + 32 * r), second = lds_float4(scales + 32 * r + 16);
+    const float m = fmaxf(first.x, second.x), f0 = exp2_of(first.x - m), f1 = exp2_of(second.x - m);
     if (par == 0)
-      take(std::integral_constant<int, 0>(), mine, theirs);
+      take(std::integral_constant<int, 0>(), f0, f1);
     else
-      take(std::integral_constant<int, 1>(), mine, theirs);
-    tc::named_bar_sync(1, 256);  // the other's reference and sum are read
-    if (par == 0) {
-      store(scales + 16 * r, m);
-      store(scales + 16 * r + 4, sum * mine + other.y * theirs);
+      take(std::integral_constant<int, 1>(), f1, f0);
+    tc::named_bar_sync(3, 32 * kBring);  // all references and sums are read
+    if (par == 0 && side == 0) {
+      store(scales + 32 * r, m);
+      store(scales + 32 * r + 4, (first.y + first.z) * f0 + (second.y + second.z) * f1);
     }
-    tc::named_bar_sync(1, 256);
+    tc::named_bar_sync(3, 32 * kBring);
     float* slot = sh.parts + (int64_t)blockIdx.x * sh.slot_heads * (D + 4);
-    for (int i = warp; i < heads; i += 8) {
+    for (int i = warp; i < heads; i += kBring) {
       for (int d = lane; d < D; d += 32) slot[i * (D + 4) + d] = lds_float(stage_at + (d * kApart + i) * 4);
-      if (lane == 0) *reinterpret_cast<float2*>(slot + i * (D + 4) + D) = lds_float2(scales + 16 * i);
+      if (lane == 0) *reinterpret_cast<float2*>(slot + i * (D + 4) + D) = lds_float2(scales + 32 * i);
     }
   } else if (warp < kIssue) {
     // ------------------------------------------------------- keys and values, widened
@@ -488,8 +501,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     // and 128 kTurn bytes on for each turn; the second panel's pieces go in the other order, so that each
     // eighth of a store meets every bank once
     const uint32_t place = of_panel(of_turn, kDims * chunk) ^ (turned ? 16 : 0);
-    // bf16: the exponent that a tile's largest value is taken to have, K's and V's: put to 2^8, so that it may be
-    // 2^7 more, or 2^8 less, before the tile is done again with its own
+    // bf16: the exponent that a tile's largest value is taken to have, K's and V's (the last one's): put to 2^8, so
+    // that it may be up to 2^7 more, or 2^8 less, before the tile is done again with its own
     int taken[2] = {127, 127};
 #pragma unroll 1
     for (int i = 0; i < 2 * tiles; ++i) {
@@ -514,15 +527,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         }
       }
       if (i >= W::kStages) wait(&st.stage_empty[stage], i / W::kStages - 1);
-      uint32_t largest = 0;
+      uint32_t largest = 0;  // bf16: of the results, two halves
       const int mine = operand ? taken[1] : taken[0];
+      const bool whole = ok == 0xffu && count >= kTile;
       auto widen_turns = [&](float scale) {
+        largest = 0;
+        if (!stores) return;
 #pragma unroll
         for (int t = 0; t < kTurns; ++t) {
           const int token = t * W::kTurn + of_turn;
           uint4 w = make_uint4(0, 0, 0, 0);
-          if (loads && token < count && ((ok >> (token >> 4)) & 1u)) w = lds128(from + t * W::kTurn * row_bytes);
-          if (!stores) continue;
+          if (loads && (whole || (token < count && ((ok >> (token >> 4)) & 1u)))) w = lds128(from + t * W::kTurn * row_bytes);
           uint32_t h[8];
           if constexpr (W::kBf16) {
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -531,7 +546,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
               const float2 f = mul2(make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u)), both(scale));
               const __half2 x = __floats2half2_rn(f.x, f.y);
               h[j] = *reinterpret_cast<const uint32_t*>(&x);
-              largest = __vmaxu2(largest, u[j] & 0x7fff7fffu);
+              const __half2 y = __hmax2_nan(__habs2(x), *reinterpret_cast<const __half2*>(&largest));
+              largest = *reinterpret_cast<const uint32_t*>(&y);
             }
           } else {
             widen<FORMAT>(turned ? w.z : w.x, h[0], h[1]);
@@ -545,14 +561,27 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       };
       widen_turns(W::kBf16 ? power2(135 - mine) : 1.0f);
       if constexpr (W::kBf16) {
-        const uint32_t m = __reduce_max_sync(kFullMask, max(largest & 0xffffu, largest >> 16));
-        if (lane == 0) st.tops[i & 1][warp - kBring] = m;
-        tc::named_bar_sync(2, kBringThreads);
-        const int e = (int)(__reduce_max_sync(kFullMask, st.tops[i & 1][lane & 7]) >> 7);
+        auto largest_of_all = [&](uint32_t mine) {
+          mine = __reduce_max_sync(kFullMask, max(mine & 0xffffu, mine >> 16));
+          if (lane == 0) st.tops[i & 1][warp - kBring] = mine;
+          tc::named_bar_sync(4, kBringThreads);
+          return __reduce_max_sync(kFullMask, st.tops[i & 1][lane & 7]);
+        };
         int used = mine;
-        if (e > mine + 6 || (e > 0 && e < mine - 8)) {
-          used = max(30, min(230, e));
-          widen_turns(power2(135 - used));
+        const uint32_t m = largest_of_all(largest);  // as an fp16 value's bits
+        if (m >= 0x7c00u || m < 0x3c00u) {  // infinite or no number, or below 1: by its own exponent
+          uint32_t top = 0;
+          if (stores && loads)
+            for (int t = 0; t < kTurns; ++t) {
+              const int token = t * W::kTurn + of_turn;
+              if (token >= count || !((ok >> (token >> 4)) & 1u)) continue;
+              const uint4 w = lds128(from + t * W::kTurn * row_bytes);
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+            }
+          tc::named_bar_sync(4, kBringThreads);  // the first maximum is read
+          const int e = (int)(largest_of_all(top) >> 7);
+          used = e == 0 ? mine : max(30, min(230, e));
+          if (used != mine) widen_turns(power2(135 - used));
           (operand ? taken[1] : taken[0]) = used;
         }
         if (tid == 0) {
