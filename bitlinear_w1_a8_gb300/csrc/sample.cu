@@ -16,8 +16,6 @@
 namespace bitlinear {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMostCtas = 8;  // of a cluster
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -26,9 +24,8 @@ __device__ __forceinline__ void send64(uint32_t at, int rank, unsigned long long
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(r), "l"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_meet() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ float exp2_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -74,127 +71,135 @@ __device__ __forceinline__ unsigned long long order_key(float x, int64_t v) {
   return (unsigned long long)(u & 0x80000000u ? ~u : u | 0x80000000u) << 32 | (uint32_t)~(uint32_t)v;
 }
 
-// A row's CTAs each keep their share of its values in registers: NV chunks a thread.  NV == 0: any
-// number, read a second time.  Every warp sums under a maximum of its own and tells it to every CTA: one
-// meeting of the cluster.
-template <int NV>
-__global__ void __launch_bounds__(kThreads) softmax_kernel(const float* __restrict__ y, float* __restrict__ p,
-                                                           const float* __restrict__ temperature, int64_t V) {
-  __shared__ unsigned long long told[kMostCtas * kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ctas = gridDim.x, rank = blockIdx.x;
-  pdl_release_dependents();
-  pdl_wait_primary();
-  const int64_t m_row = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
-  const float* in = y + m_row * V;
-  float* out = p + m_row * V;
-  const Row r(in, V);
-  const int64_t share = (r.chunks + ctas - 1) / ctas, from = rank * share, to = min(r.chunks, from + share);
-  const float T = temperature ? __ldg(temperature + m_row) : 1.0f;
+constexpr int kRowThreads = 256;  // of a CTA
+
+// The cluster's exchange: every warp tells every CTA its word; `told` has room for all.
+template <int WARPS>
+__device__ __forceinline__ void tell(unsigned long long* told, unsigned long long mine, int ctas, int rank, int lane, int warp) {
+  if (ctas == 1) {
+    if (lane == 0) told[warp] = mine;
+    __syncthreads();
+  } else {
+    if (lane < ctas) send64(smem_at(told + rank * WARPS + warp), lane, mine);
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+// A row's probabilities from what its threads hold: `each` calls its argument with (chunk, its values) for
+// every chunk of the thread's.  m: the thread's largest logit.  AGAIN: `each` reads the logits anew.
+template <int WARPS, bool AGAIN, typename Each>
+__device__ __forceinline__ void finish_row(const Row& r, float* out, float T, float m, unsigned long long* told, int ctas, int rank,
+                                           int lane, int warp, Each each) {
   const bool greedy = !(T >= 1e-30f);
   const float c = 1.44269504f / fminf(T, 1e30f);
-
-  constexpr int kHeld = NV ? NV : 1;
-  float4 x[kHeld];
-  float m = -INFINITY;
-  if constexpr (NV > 0) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t i = from + threadIdx.x + j * kThreads;
-      x[j] = i < to ? load_chunk(in, r, i, -INFINITY) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      m = fmaxf(m, fmaxf(fmaxf(x[j].x, x[j].y), fmaxf(x[j].z, x[j].w)));
-    }
-  } else {
-    for (int64_t i = from + threadIdx.x; i < to; i += kThreads) {
-      const float4 v = load_chunk(in, r, i, -INFINITY);
-      m = fmaxf(m, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-    }
-  }
-  auto each = [&](auto f) {  // f(chunk, its values)
-    if constexpr (NV > 0) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int64_t i = from + threadIdx.x + j * kThreads;
-        if (i < to) f(i, x[j]);
-      }
-    } else {
-      for (int64_t i = from + threadIdx.x; i < to; i += kThreads) {
-        float4 v = load_chunk(in, r, i, -INFINITY);
-        f(i, v);
-      }
-    }
-  };
-  unsigned long long mine;
   if (greedy) {
-    mine = 0;
+    unsigned long long mine = 0;
     each([&](int64_t i, float4& v) {
       const int64_t at = 4 * i - r.shift;
       const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (at + j >= 0 && at + j < V && e[j] > -INFINITY) mine = max(mine, order_key(e[j], at + j));
+        if (at + j >= 0 && at + j < r.V && e[j] > -INFINITY) mine = max(mine, order_key(e[j], at + j));
     });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine = max(mine, __shfl_xor_sync(kFullMask, mine, o));
-  } else {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-    const float under = m == -INFINITY ? 0.0f : m;  // a row, or a warp's part, that is masked whole
-    float s = 0.0f;
-    each([&](int64_t, float4& v) {
-      v.x = exp2_of((v.x - under) * c);
-      v.y = exp2_of((v.y - under) * c);
-      v.z = exp2_of((v.z - under) * c);
-      v.w = exp2_of((v.w - under) * c);
-      s += (v.x + v.y) + (v.z + v.w);
-    });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
-    mine = packed(m, s);
-  }
-  if (ctas == 1) {
-    if (lane == 0) told[warp] = mine;
-    __syncthreads();
-  } else {
-    cluster_meet();  // all of the cluster's CTAs have begun
-    if (lane < ctas) send64(smem_at(told + rank * kWarps + warp), lane, mine);
-    cluster_meet();
-  }
-  if (greedy) {
+    tell<WARPS>(told, mine, ctas, rank, lane, warp);
     unsigned long long best = 0;
-    for (int i = lane; i < ctas * kWarps; i += 32) best = max(best, told[i]);
+    for (int i = lane; i < ctas * WARPS; i += 32) best = max(best, told[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(kFullMask, best, o));
     const int64_t at = best ? (int64_t)(uint32_t)~(uint32_t)best : -1;
-    each([&](int64_t i, float4& v) {
-      const int64_t d = at - (4 * i - r.shift);
-      v = make_float4(d == 0, d == 1, d == 2, d == 3);
-      if (at < 0) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      store_chunk(out, r, i, v);
+    each([&](int64_t i, float4&) {
+      const int64_t d = at < 0 ? -1 : at - (4 * i - r.shift);
+      store_chunk(out, r, i, make_float4(d == 0, d == 1, d == 2, d == 3));
     });
     return;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+  const float under = m == -INFINITY ? 0.0f : m;  // a row, or a warp's part, that is masked whole
+  float s = 0.0f;
+  each([&](int64_t, float4& v) {
+    v.x = exp2_of((v.x - under) * c);
+    v.y = exp2_of((v.y - under) * c);
+    v.z = exp2_of((v.z - under) * c);
+    v.w = exp2_of((v.w - under) * c);
+    s += (v.x + v.y) + (v.z + v.w);
+  });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
+  tell<WARPS>(told, packed(m, s), ctas, rank, lane, warp);
   float M = -INFINITY, S = 0.0f;
-  for (int i = lane; i < ctas * kWarps; i += 32) M = fmaxf(M, __uint_as_float((uint32_t)(told[i] >> 32)));
+  for (int i = lane; i < ctas * WARPS; i += 32) M = fmaxf(M, __uint_as_float((uint32_t)(told[i] >> 32)));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
   const float top = M == -INFINITY ? 0.0f : M;
-  for (int i = lane; i < ctas * kWarps; i += 32) {
-    const float s = __uint_as_float((uint32_t)told[i]);
-    S += s * exp2_of((__uint_as_float((uint32_t)(told[i] >> 32)) - top) * c);
-  }
+  for (int i = lane; i < ctas * WARPS; i += 32)
+    S += __uint_as_float((uint32_t)told[i]) * exp2_of((__uint_as_float((uint32_t)(told[i] >> 32)) - top) * c);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(kFullMask, S, o);
   const float inverse = S == 0.0f ? 0.0f : 1.0f / S;
-  const float f = NV > 0 ? exp2_of((m - top) * c) * inverse : inverse;
+  const float f = AGAIN ? inverse : exp2_of((m - top) * c) * inverse;
   each([&](int64_t i, float4& v) {
-    if constexpr (NV == 0) {
+    if constexpr (AGAIN) {
       v.x = exp2_of((v.x - top) * c);
       v.y = exp2_of((v.y - top) * c);
       v.z = exp2_of((v.z - top) * c);
       v.w = exp2_of((v.w - top) * c);
     }
     store_chunk(out, r, i, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+  });
+}
+
+__device__ __forceinline__ float largest_of(float m, const float4& v) { return fmaxf(m, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w))); }
+
+// A row a cluster.  A CTA keeps its share of the row in registers, NV chunks a thread; NV == 0: any number of
+// them, read a second and a third time.  Every warp sums under a maximum of its own and tells it to every CTA, so
+// the cluster meets once.
+template <int THREADS, int NV>
+__global__ void __launch_bounds__(THREADS) softmax_kernel(const float* __restrict__ y, float* __restrict__ p,
+                                                          const float* __restrict__ temperature, int64_t V) {
+  constexpr int kWarps = THREADS / 32;
+  __shared__ unsigned long long told[kMostCtas * kWarps];
+  const int ctas = gridDim.x, rank = blockIdx.x;
+  pdl_release_dependents();
+  if (ctas > 1) cluster_arrive();  // waited for before the first word goes to another CTA
+  pdl_wait_primary();
+  const int64_t m_row = blockIdx.y;
+  const float* in = y + m_row * V;
+  const Row r(in, V);
+  const int64_t share = (r.chunks + ctas - 1) / ctas, from = rank * share, to = min(r.chunks, from + share);
+  float4 x[NV ? NV : 1];
+  float m = -INFINITY;
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t i = from + threadIdx.x + j * THREADS;
+      x[j] = i < to ? load_chunk(in, r, i, -INFINITY) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    }
+  }
+  const float T = temperature ? __ldg(temperature + m_row) : 1.0f;
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) m = largest_of(m, x[j]);
+  } else {
+    for (int64_t i = from + threadIdx.x; i < to; i += THREADS) m = largest_of(m, load_chunk(in, r, i, -INFINITY));
+  }
+  if (ctas > 1) cluster_wait();
+  finish_row<kWarps, NV == 0>(r, p + m_row * V, T, m, told, ctas, rank, threadIdx.x & 31, threadIdx.x >> 5, [&](auto f) {
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int64_t i = from + threadIdx.x + j * THREADS;
+        if (i < to) f(i, x[j]);
+      }
+    } else {
+      for (int64_t i = from + threadIdx.x; i < to; i += THREADS) {
+        float4 v = load_chunk(in, r, i, -INFINITY);
+        f(i, v);
+      }
+    }
   });
 }
 
@@ -229,27 +234,50 @@ __device__ __forceinline__ unsigned long long warp_upto(unsigned long long x, in
   return x;
 }
 
-__global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
-  __shared__ unsigned long long told[2][kMostCtas];
-  __shared__ unsigned long long sums[2][kWarps];
+// Four values from v on, of a row of V; those past its end are 0.
+template <bool ALIGNED>
+__device__ __forceinline__ float4 load_four(const float* row, int64_t v, int64_t V) {
+  if constexpr (ALIGNED) {
+    return __ldg(reinterpret_cast<const float4*>(row + v));
+  } else {
+    float x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = v + j < V ? __ldg(row + v + j) : 0.0f;
+    return make_float4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+constexpr int kVerifyThreads = 256;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+
+// A CTA's run of the row in turns of four values a thread; the weights of NV turns stay in registers, and where
+// there are more of them (NV == 0) the run that has the token is walked through again.  Sums are told warp by
+// warp, so that the cluster meets once.  ALIGNED: rows start on 16 bytes.
+template <int NV, bool ALIGNED>
+__global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(VerifyArgs a) {
+  __shared__ unsigned long long told[2][kMostCtas * kVerifyWarps];
+  __shared__ unsigned long long turns[(NV ? NV : 1) * kVerifyWarps];  // of each turn and warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ctas = gridDim.x, rank = blockIdx.x;
   pdl_release_dependents();
+  if (ctas > 1) cluster_arrive();  // waited for before the first word goes to another CTA
   pdl_wait_primary();
-  const int64_t b = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
+  const int64_t b = blockIdx.y;
   const int K = a.K;
   const int64_t V = a.V;
 
   // The drafts taken: every warp asks for itself, 32 drafts at a time.
   int n = 0;
   bool refused = false;  // by the draw, and not because the drafts end
+  const float last = __ldg(a.uniform + b * (K + 1) + K);
   for (int i0 = 0; i0 < K; i0 += 32) {
     const int i = i0 + lane;
-    const int32_t x = i < K ? a.draft[b * K + i] : -1;
+    const float u = i < K ? __ldg(a.uniform + b * (K + 1) + i) : 0.0f;
+    const int32_t x = i < K ? __ldg(a.draft + b * K + i) : -1;
     const bool drafted = x >= 0 && x < V;
     bool take = false;
     if (drafted) {
-      const float px = a.p[(b * (K + 1) + i) * V + x], qx = a.q[(b * K + i) * V + x], u = a.uniform[b * (K + 1) + i];
+      const float px = __ldg(a.p + (b * (K + 1) + i) * V + x), qx = __ldg(a.q + (b * K + i) * V + x);
       take = (double)u * (double)qx < (double)px;
     }
     const uint32_t taken = __ballot_sync(kFullMask, take), drafts = __ballot_sync(kFullMask, drafted);
@@ -263,35 +291,63 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
   const float* p = a.p + (b * (K + 1) + n) * V;
   const float* q = refused ? a.q + (b * K + n) * V : nullptr;
 
-  const int64_t share = (V + ctas - 1) / ctas, from = min(V, rank * share), to = min(V, from + share);
+  const int64_t fours = (V + 3) / 4, share = (fours + ctas - 1) / ctas, from = min(fours, rank * share), to = min(fours, from + share);
+  auto weights = [&](int64_t i) {
+    float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i < to) {
+      w = load_four<ALIGNED>(p, 4 * i, V);
+      if (q) {
+        const float4 d = load_four<ALIGNED>(q, 4 * i, V);
+        w = make_float4(__fsub_rn(w.x, d.x), __fsub_rn(w.y, d.y), __fsub_rn(w.z, d.z), __fsub_rn(w.w, d.w));
+      }
+    }
+    return w;
+  };
+  auto sum_of = [&](const float4& w) { return units(w.x, a.scale) + units(w.y, a.scale) + units(w.z, a.scale) + units(w.w, a.scale); };
+  constexpr int kHeld = NV ? NV : 1;
+  float4 held[kHeld];
   unsigned long long total = 0, before = 0, mine = 0;
   for (int attempt = 0;; ++attempt) {
-    auto weight = [&](int64_t v) {
-      const float w = __ldg(p + v);
-      return units(q ? __fsub_rn(w, __ldg(q + v)) : w, a.scale);
-    };
     unsigned long long s = 0;
-    for (int64_t v = from + threadIdx.x; v < to; v += kThreads) s += weight(v);
-    s = warp_sum(s);
-    if (lane == 0) sums[attempt][warp] = s;
-    __syncthreads();
-    mine = warp_sum(lane < kWarps ? sums[attempt][lane] : 0ull);
-    if (ctas == 1) {
-      total = mine;
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) held[j] = weights(from + threadIdx.x + j * kVerifyThreads);
+      if (attempt > 0) __syncthreads();  // the first attempt's sums are read
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const unsigned long long t = warp_sum(sum_of(held[j]));
+        if (lane == 0) turns[j * kVerifyWarps + warp] = t;
+        s += t;
+      }
     } else {
-      if (attempt == 0) cluster_meet();  // all of the cluster's CTAs have begun
-      if (threadIdx.x < ctas) send64(smem_at(told[attempt] + rank), threadIdx.x, mine);
-      cluster_meet();
-      const unsigned long long t = lane < ctas ? told[attempt][lane] : 0ull;
-      total = warp_sum(t);
-      before = warp_sum(lane < rank ? t : 0ull);
+      for (int64_t i = from + threadIdx.x; i < to; i += kVerifyThreads) s += sum_of(weights(i));
+      s = warp_sum(s);
     }
+    if (ctas == 1) {
+      if (lane == 0) told[attempt][warp] = s;
+      __syncthreads();
+    } else {
+      if (attempt == 0) cluster_wait();  // all of the cluster's CTAs have begun
+      if (lane < ctas) send64(smem_at(told[attempt] + rank * kVerifyWarps + warp), lane, s);
+      cluster_arrive();
+      cluster_wait();
+    }
+    unsigned long long all = 0, ahead = 0, here = 0;
+    for (int i = lane; i < ctas * kVerifyWarps; i += 32) {
+      const unsigned long long t = told[attempt][i];
+      all += t;
+      ahead += i < rank * kVerifyWarps ? t : 0ull;
+      here += i / kVerifyWarps == rank ? t : 0ull;
+    }
+    total = warp_sum(all);
+    before = warp_sum(ahead);
+    mine = warp_sum(here);
     if (total != 0 || !q) break;
     q = nullptr;  // nothing is left of p - q: p itself
   }
 
   if (rank == 0) {
-    for (int i = threadIdx.x; i <= K; i += kThreads)
+    for (int i = threadIdx.x; i <= K; i += kVerifyThreads)
       if (i != n) a.tokens[b * (K + 1) + i] = i < n ? a.draft[b * K + i] : -1;
     if (threadIdx.x == 0) {
       a.accepted[b] = n;
@@ -299,38 +355,57 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
     }
   }
   // The first token whose running sum is above floor(r * total): r in [0, 1) as a 64-bit fraction.
-  const float r = fminf(fmaxf(a.uniform[b * (K + 1) + K], 0.0f), 0.99999994f);
+  const float r = fminf(fmaxf(last, 0.0f), 0.99999994f);
   const unsigned long long goal = __umul64hi((unsigned long long)((double)r * 18446744073709551616.0), total);
   if (total == 0 || goal < before || goal >= before + mine) return;
-  // This CTA's run has it: walked through again.
-  unsigned long long upto = before;
-  for (int64_t v0 = from; v0 < to; v0 += kThreads) {
-    const int64_t v = v0 + threadIdx.x;
-    unsigned long long w = 0;
-    if (v < to) {
-      const float x = __ldg(p + v);
-      w = units(q ? __fsub_rn(x, __ldg(q + v)) : x, a.scale);
+  // This CTA's run has it.  `upto`: the weights ahead of this lane's four, whose first is v; writes the token if one of
+  // them passes the goal.
+  auto look_at = [&](const float4& w, unsigned long long upto, int64_t v) {
+    const float x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const unsigned long long u = units(x[j], a.scale);
+      if (upto <= goal && upto + u > goal) a.tokens[b * (K + 1) + n] = (int32_t)(v + j);
+      upto += u;
     }
-    const unsigned long long in_warp = warp_upto(w, lane);
-    __syncthreads();
-    if (lane == 31) sums[0][warp] = in_warp;
-    __syncthreads();
-    const unsigned long long of_warps = lane < kWarps ? sums[0][lane] : 0ull;
-    const unsigned long long ahead = warp_sum(lane < warp ? of_warps : 0ull), all = warp_sum(of_warps);
-    const unsigned long long end = upto + ahead + in_warp;
-    if (w != 0 && end > goal && end - w <= goal) a.tokens[b * (K + 1) + n] = (int32_t)v;
-    if (upto + all > goal) return;
-    upto += all;
+  };
+  if constexpr (NV > 0) {
+    unsigned long long at = before;  // ahead of turn j of this warp
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const unsigned long long t = lane < kVerifyWarps ? turns[j * kVerifyWarps + lane] : 0ull;
+      const unsigned long long ahead = warp_sum(lane < warp ? t : 0ull), all = warp_sum(t);
+      if (goal >= at + ahead && goal < at + all) {  // this warp's, perhaps
+        const unsigned long long s = sum_of(held[j]);
+        look_at(held[j], at + ahead + warp_upto(s, lane) - s, 4 * (from + threadIdx.x + j * kVerifyThreads));
+      }
+      at += all;
+    }
+  } else {
+    unsigned long long at = before;
+    for (int64_t i0 = from; i0 < to; i0 += kVerifyThreads) {
+      const int64_t i = i0 + threadIdx.x;
+      const float4 w = weights(i);
+      const unsigned long long s = sum_of(w), in_warp = warp_upto(s, lane);
+      __syncthreads();
+      if (lane == 31) turns[warp] = in_warp;
+      __syncthreads();
+      const unsigned long long t = lane < kVerifyWarps ? turns[lane] : 0ull;
+      const unsigned long long ahead = warp_sum(lane < warp ? t : 0ull), all = warp_sum(t);
+      look_at(w, at + ahead + in_warp - s, 4 * i);
+      if (at + all > goal) return;
+      at += all;
+    }
   }
 }
 
 template <typename... Kernel, typename... Args>
-cudaError_t launch_rows(void (*kernel)(Kernel...), int64_t rows, int ctas, bool pdl, cudaStream_t stream, Args... args) {
+cudaError_t launch_grid(void (*kernel)(Kernel...), int threads, dim3 grid, int ctas, int smem, bool pdl, cudaStream_t stream, Args... args) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
   if (ctas > 1) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
     attr[cfg.numAttrs].val.clusterDim.x = (unsigned)ctas;
@@ -343,7 +418,8 @@ cudaError_t launch_rows(void (*kernel)(Kernel...), int64_t rows, int ctas, bool 
     attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
     ++cfg.numAttrs;
   }
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)rows, 1);
+  cfg.gridDim = grid;
+  cfg.dynamicSmemBytes = (size_t)smem;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -352,31 +428,46 @@ constexpr int64_t kMostRows = 65535;  // of a launch
 }  // namespace
 
 cudaError_t launch_softmax(const float* y, float* p, const float* temperature, int64_t M, int64_t V, bool pdl,
-                           const DeviceInfo&, cudaStream_t stream) {
+                           const DeviceInfo& dev, cudaStream_t stream) {
   const int64_t chunks = (V + 6) / 4;
+  // As few CTAs as hold a row, and more while they do not fill the GPU
   int ctas = 1;
-  while (ctas < kMostCtas && chunks > (int64_t)ctas * kThreads) ctas *= 2;
-  const int64_t held = ((chunks + ctas - 1) / ctas + kThreads - 1) / kThreads;
+  while (ctas < kMostCtas && (chunks > (int64_t)ctas * kRowThreads * 7 || (chunks > (int64_t)ctas * kRowThreads && M * ctas < 4 * (int64_t)dev.num_sms)))
+    ctas *= 2;
+  const int64_t held = ((chunks + ctas - 1) / ctas + kRowThreads - 1) / kRowThreads;
+  const auto kernel = held <= 1   ? softmax_kernel<kRowThreads, 1>
+                      : held <= 2 ? softmax_kernel<kRowThreads, 2>
+                      : held <= 4 ? softmax_kernel<kRowThreads, 4>
+                      : held <= 7 ? softmax_kernel<kRowThreads, 7>
+                                  : softmax_kernel<kRowThreads, 0>;
   for (int64_t m = 0; m < M; m += kMostRows) {
     const int64_t rows = M - m < kMostRows ? M - m : kMostRows;
-    const auto kernel = held <= 1 ? softmax_kernel<1> : held <= 2 ? softmax_kernel<2> : held <= 4 ? softmax_kernel<4> : held <= 8 ? softmax_kernel<8> : softmax_kernel<0>;
-    const cudaError_t err = launch_rows(kernel, rows, ctas, pdl, stream, y + m * V, p + m * V, temperature ? temperature + m : nullptr, V);
+    const cudaError_t err = launch_grid(kernel, kRowThreads, dim3((unsigned)ctas, (unsigned)rows, 1), ctas, 0, pdl, stream, y + m * V, p + m * V,
+                                        temperature ? temperature + m : nullptr, V);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
 }
 
 cudaError_t launch_verify(const float* p, const float* q, const int32_t* draft, const float* uniform, int64_t B, int K,
-                          int64_t V, int32_t* tokens, int32_t* accepted, bool pdl, const DeviceInfo&, cudaStream_t stream) {
+                          int64_t V, int32_t* tokens, int32_t* accepted, bool pdl, const DeviceInfo& dev, cudaStream_t stream) {
+  const int64_t fours = (V + 3) / 4;
   int ctas = 1;
-  while (ctas < kMostCtas && V > (int64_t)ctas * 2 * kThreads) ctas *= 2;
+  while (ctas < kMostCtas && (fours > (int64_t)ctas * kVerifyThreads * 7 || (fours > (int64_t)ctas * kVerifyThreads && B * ctas < 4 * (int64_t)dev.num_sms)))
+    ctas *= 2;
+  const int64_t held = ((fours + ctas - 1) / ctas + kVerifyThreads - 1) / kVerifyThreads;
+  const bool aligned = V % 4 == 0;
+  const auto kernel = held <= 1   ? (aligned ? verify_kernel<1, true> : verify_kernel<1, false>)
+                      : held <= 4 ? (aligned ? verify_kernel<4, true> : verify_kernel<4, false>)
+                      : held <= 7 ? (aligned ? verify_kernel<7, true> : verify_kernel<7, false>)
+                                  : (aligned ? verify_kernel<0, true> : verify_kernel<0, false>);
   int bits = 62;
   while (((int64_t)1 << (62 - bits)) < V) --bits;
   const float scale = (float)((int64_t)1 << bits);
   for (int64_t b = 0; b < B; b += kMostRows) {
     const int64_t rows = B - b < kMostRows ? B - b : kMostRows;
     const VerifyArgs a = {p + b * (K + 1) * V, q + b * K * V, uniform + b * (K + 1), draft + b * K, tokens + b * (K + 1), accepted + b, V, K, scale};
-    const cudaError_t err = launch_rows(verify_kernel, rows, ctas, pdl, stream, a);
+    const cudaError_t err = launch_grid(kernel, kVerifyThreads, dim3((unsigned)ctas, (unsigned)rows, 1), ctas, 0, pdl, stream, a);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;

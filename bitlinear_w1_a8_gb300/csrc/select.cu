@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kSumThreads) summarise_kernel(SummariseArgs a)
       hi[i] = -INFINITY;
     }
     if (row < rows) {
-#pragma unroll 4
+#pragma unroll 8
       for (int t = row; t < here; t += rows) {
         float x[kDims];
         widen16<FORMAT>(__ldg(reinterpret_cast<const uint4*>(k + (int64_t)t * D * kBytes)), FORMAT == BITLINEAR_KV_BF16 ? 1.0f : __ldg(steps + t), x);
@@ -151,8 +151,11 @@ __device__ __forceinline__ void send32(uint32_t at, int rank, uint32_t v) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(r), "r"(v) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_meet() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 
 // Larger scores have larger keys, between kAbsent and kKept; NaN has the least.
@@ -162,61 +165,265 @@ __device__ __forceinline__ uint32_t key_of(float score) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A cluster chooses for one key head of one sequence.  Every CTA scores a run of the pages and keeps
-// their keys; the count-th largest key is found a byte at a time from histograms that all CTAs add up,
-// and each CTA writes its own chosen pages where those of the CTAs before it end.
+constexpr int kGathered = 8192;  // pages whose keys one CTA chooses from
+constexpr int kBins = 2048, kBinBits = 11, kListed = 128;
+
+struct Scratch {
+  union {
+    uint32_t bins[kBins];
+    uint32_t histogram[kMostCtas][kDigits];
+  };
+  uint32_t listed[kListed];
+  uint32_t of_warps[kWarps][4];
+  uint32_t counted[kMostCtas][2];
+  uint32_t found[4];
+};
+
+// Over the CTA's threads: sums of x and y, smallest z, largest w.
+struct Totals {
+  uint32_t x, y, z, w;
+};
+__device__ __forceinline__ Totals totals(Scratch& t, uint32_t x, uint32_t y, uint32_t z, uint32_t w, int lane, int warp) {
+  x = __reduce_add_sync(kFullMask, x);
+  y = __reduce_add_sync(kFullMask, y);
+  z = __reduce_min_sync(kFullMask, z);
+  w = __reduce_max_sync(kFullMask, w);
+  __syncthreads();
+  if (lane == 0) {
+    t.of_warps[warp][0] = x;
+    t.of_warps[warp][1] = y;
+    t.of_warps[warp][2] = z;
+    t.of_warps[warp][3] = w;
+  }
+  __syncthreads();
+  const int i = lane & (kWarps - 1);
+  return {__reduce_add_sync(kFullMask, lane < kWarps ? t.of_warps[i][0] : 0u), __reduce_add_sync(kFullMask, lane < kWarps ? t.of_warps[i][1] : 0u),
+          __reduce_min_sync(kFullMask, t.of_warps[i][2]), __reduce_max_sync(kFullMask, t.of_warps[i][3])};
+}
+
+// The count-th largest of the CTA's keys (`known`), and how many that equal it are among the count largest
+// (`wanted`); known kAbsent and wanted 0 where there are fewer.  Keys of scores are put into 2048 bins of the range that
+// they cover, so that neighbours in score are neighbours in place: one round leaves a few, which are ranked.
+__device__ __forceinline__ void find_here(const uint32_t* keys, int here, uint32_t count, Scratch& t, uint32_t& known, uint32_t& wanted,
+                                          int lane, int warp) {
+  uint32_t kept = 0, scored = 0, lo = 0xffffffffu, hi = 0;
+  for (int i = threadIdx.x; i < here; i += kThreads) {
+    const uint32_t k = keys[i];
+    kept += k == kKept;
+    if (k != kKept && k != kAbsent) {
+      ++scored;
+      lo = min(lo, k);
+      hi = max(hi, k);
+    }
+  }
+  const Totals all = totals(t, kept, scored, lo, hi, lane, warp);
+  known = kAbsent;
+  wanted = 0;
+  if (all.x + all.y <= count) return;
+  if (all.x >= count) {
+    known = kKept;
+    wanted = count;
+    return;
+  }
+  wanted = count - all.x;  // of keys lo .. hi
+  lo = all.z;
+  hi = all.w;
+  for (;;) {
+    const int shift = max(0, 32 - __clz(hi - lo) - kBinBits);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kThreads) t.bins[i] = 0;
+    if (threadIdx.x == 0) t.found[2] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < here; i += kThreads) {
+      const uint32_t k = keys[i];
+      if (k >= lo && k <= hi && k != kAbsent) atomicAdd(&t.bins[(k - lo) >> shift], 1u);
+    }
+    __syncthreads();
+    // a thread has 8 bins, the highest in thread 0
+    uint32_t n[kBins / kThreads], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kBins / kThreads; ++i) mine += n[i] = t.bins[kBins - 1 - (kBins / kThreads * threadIdx.x + i)];
+    uint32_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(kFullMask, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) t.of_warps[warp][0] = upto;
+    __syncthreads();
+    upto += __reduce_add_sync(kFullMask, lane < warp ? t.of_warps[lane & (kWarps - 1)][0] : 0u);
+    uint32_t above = upto - mine;
+    if (wanted > above && wanted <= upto) {
+#pragma unroll
+      for (int i = 0; i < kBins / kThreads; ++i) {
+        if (wanted > above && wanted <= above + n[i]) {
+          t.found[0] = kBins - 1 - (kBins / kThreads * threadIdx.x + i);
+          t.found[1] = above;
+          t.found[3] = n[i];
+        }
+        above += n[i];
+      }
+    }
+    __syncthreads();
+    const uint32_t bin = t.found[0], inside = t.found[3];
+    wanted -= t.found[1];
+    lo += bin << shift;
+    hi = min(hi, lo + ((1u << shift) - 1));
+    if (shift == 0) {
+      known = lo;
+      return;
+    }
+    if (inside <= kListed) break;
+  }
+  for (int i = threadIdx.x; i < here; i += kThreads) {
+    const uint32_t k = keys[i];
+    if (k >= lo && k <= hi && k != kAbsent) t.listed[atomicAdd(&t.found[2], 1u)] = k;
+  }
+  __syncthreads();
+  const uint32_t n = t.found[2];
+  if (threadIdx.x < n) {
+    const uint32_t k = t.listed[threadIdx.x];
+    uint32_t greater = 0, equal = 0;
+    for (uint32_t i = 0; i < n; ++i) {
+      greater += t.listed[i] > k;
+      equal += t.listed[i] == k;
+    }
+    if (greater < wanted && wanted <= greater + equal) {  // the same from every equal key
+      t.found[0] = k;
+      t.found[1] = greater;
+    }
+  }
+  __syncthreads();
+  known = t.found[0];
+  wanted -= t.found[1];
+}
+
+// The same of all CTAs' keys together, a byte at a time from histograms that all CTAs add up.
+__device__ __forceinline__ void find_in_cluster(const uint32_t* keys, int here, uint32_t count, Scratch& t, uint32_t& known, uint32_t& wanted,
+                                                int ctas, int rank, int lane) {
+  known = 0;
+  wanted = count;
+  uint32_t mask = 0;  // where the bytes found are
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    uint32_t* mine = t.histogram[rank];
+    for (int i = threadIdx.x; i < kDigits; i += kThreads) mine[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < here; i += kThreads) {
+      const uint32_t k = keys[i];
+      if (k != kAbsent && (k & mask) == known) atomicAdd(&mine[(k >> shift) & 0xff], 1u);
+    }
+    __syncthreads();
+    for (int r = 0; r < ctas; ++r)
+      if (r != rank)
+        for (int i = threadIdx.x; i < kDigits; i += kThreads) send32(smem_at(&t.histogram[rank][i]), r, mine[i]);
+    cluster_meet();
+    // every warp finds the byte for itself: a lane has 8 digits, the highest digits in lane 0
+    uint32_t n[8], all = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      n[i] = 0;
+      for (int r = 0; r < ctas; ++r) n[i] += t.histogram[r][kDigits - 1 - (8 * lane + i)];
+      all += n[i];
+    }
+    uint32_t upto = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(kFullMask, upto, o);
+      if (lane >= o) upto += x;
+    }
+    uint32_t above = upto - all, digit = 0;
+    const uint32_t has = __ballot_sync(kFullMask, wanted > above && wanted <= upto);
+    if (has == 0) {  // fewer keys than are wanted: all of them
+      known = kAbsent;
+      wanted = 0;
+      cluster_meet();
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (wanted > above && wanted <= above + n[i]) {
+        digit = kDigits - 1 - (8 * lane + i);
+        break;
+      }
+      above += n[i];
+    }
+    const int owner = __ffs(has) - 1;
+    digit = __shfl_sync(kFullMask, digit, owner);
+    wanted -= __shfl_sync(kFullMask, above, owner);
+    known |= digit << shift;
+    mask |= 0xffu << shift;
+    cluster_meet();  // the histograms are read
+  }
+}
+
+// A cluster chooses for one key head of one sequence.  Every CTA scores a run of the pages; up to kGathered of them
+// (`gather`) all keys go to the first CTA, which chooses, and beyond each keeps its own and writes its chosen
+// pages where those of the CTAs before it end.
 template <int CHUNKS>  // of 16 dims, at most
-__global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, KvPages c, Summary summary, int share) {
+__global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, KvPages c, Summary summary, int share, bool gather) {
   extern __shared__ __align__(16) uint8_t smem[];
   uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
   __shared__ __align__(16) int8_t codes[kHeadsAtOnce][2][CHUNKS * 16];  // parts below and above 0
   __shared__ float steps[kHeadsAtOnce];
-  __shared__ uint32_t histogram[kMostCtas][kDigits];
-  __shared__ uint32_t counted[kMostCtas][2];
-  __shared__ uint32_t of_warps[kWarps][2];
+  __shared__ Scratch scratch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ctas = gridDim.x, rank = blockIdx.x;
+  int ctas = gridDim.x, rank = blockIdx.x;
   pdl_release_dependents();
+  if (ctas > 1) cluster_arrive();  // waited for before the first word goes to another CTA
   pdl_wait_primary();
   const int64_t b = (int64_t)blockIdx.z, hk = blockIdx.y;
   const int D = c.head_dim, chunks = D / 16, group = a.q_heads / c.heads;
   const int64_t length = max((int64_t)0, min((int64_t)a.lengths[b], a.max_pages << c.page_shift));
   const int pages = (int)((length + (1 << c.page_shift) - 1) >> c.page_shift);
   // runs as short as the sequence allows
-  const int run = min(share, (pages + ctas - 1) / ctas), from = min(pages, rank * run), here = min(pages, from + run) - from;
+  const int run = min(share, (pages + ctas - 1) / ctas);
+  int from = min(pages, rank * run), here = min(pages, from + run) - from;
   const int32_t* table = a.table + b * a.table_stride;
   int32_t* out = a.blocks + (b * c.heads + hk) * a.count;
 
+  // two lanes a page: one the lower bounds, one the upper
+  const int mine = threadIdx.x / 2, side = threadIdx.x & 1;
+  uint4 w[CHUNKS];
+  float step;
+  bool there;
+  auto bring = [&](int i) {
+    const int32_t page = i < here ? table[from + i] : -1;
+    there = page >= 0 && page < c.num_pages;
+    const int64_t head = (int64_t)(there ? page : 0) * c.heads + hk;
+    const uint4* bounds = reinterpret_cast<const uint4*>(summary.bounds + (head * 2 + side) * D);
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) w[k] = there && k < chunks ? __ldg(bounds + k) : make_uint4(0, 0, 0, 0);
+    step = there ? __ldg(summary.step + head) : 0.0f;
+  };
+  bring(mine);  // on their way while q is turned into codes
   for (int h0 = 0; h0 < group; h0 += kHeadsAtOnce) {
     const int heads = min(kHeadsAtOnce, group - h0);
     if (h0 > 0) __syncthreads();
     for (int h = warp; h < heads; h += kWarps) {  // a warp quantises a head
       const float* q = a.q + b * a.q_stride + (hk * group + h0 + h) * D;
-      float top = kLeastTop;
-      for (int d = lane; d < D; d += 32) top = fmaxf(top, fabsf(q[d]));
+      float x[(CHUNKS * 16 + 31) / 32], top = kLeastTop;
+#pragma unroll
+      for (int i = 0; i < (CHUNKS * 16 + 31) / 32; ++i) {
+        x[i] = lane + 32 * i < D ? q[lane + 32 * i] : 0.0f;
+        top = fmaxf(top, fabsf(x[i]));
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
       const float s = __fdiv_rn(127.0f, top);
-      for (int d = lane; d < D; d += 32) {
-        const int code = max(-127, min(127, __float2int_rn(__fmul_rn(q[d], s))));
-        codes[h][0][d] = (int8_t)min(code, 0);
-        codes[h][1][d] = (int8_t)max(code, 0);
+#pragma unroll
+      for (int i = 0; i < (CHUNKS * 16 + 31) / 32; ++i) {
+        if (lane + 32 * i < D) {
+          const int code = max(-127, min(127, __float2int_rn(__fmul_rn(x[i], s))));
+          codes[h][0][lane + 32 * i] = (int8_t)min(code, 0);
+          codes[h][1][lane + 32 * i] = (int8_t)max(code, 0);
+        }
       }
       if (lane == 0) steps[h] = __fdiv_rn(top, 127.0f);
     }
     __syncthreads();
-    // two lanes a page: one the lower bounds, one the upper
     for (int i0 = 0; i0 < here; i0 += kThreads / 2) {
-      const int i = i0 + threadIdx.x / 2, side = threadIdx.x & 1, column = from + i;
-      int32_t page = -1;
-      if (i < here) page = table[column];
-      const bool there = page >= 0 && page < c.num_pages;
-      const int64_t head = (int64_t)(there ? page : 0) * c.heads + hk;
-      uint4 w[CHUNKS];
-      const uint4* bounds = reinterpret_cast<const uint4*>(summary.bounds + (head * 2 + side) * D);
-#pragma unroll
-      for (int k = 0; k < CHUNKS; ++k) w[k] = there && k < chunks ? __ldg(bounds + k) : make_uint4(0, 0, 0, 0);
-      const float step = there ? __ldg(summary.step + head) : 0.0f;
+      const int i = i0 + mine, column = from + i;
+      if (i0 > 0 || h0 > 0) bring(i);
       float best = -INFINITY;
       bool nan = false;
       for (int h = 0; h < heads; ++h) {
@@ -245,129 +452,63 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, KvPages 
     }
   }
   __syncthreads();
-  if (ctas > 1) cluster_meet();  // all of the cluster's CTAs have begun
-
-  // The count-th largest key: its bytes from the highest on.
-  uint32_t known = 0, mask = 0;  // the bytes found, and where they are
-  uint32_t wanted = a.count;     // still to be taken among keys that agree with `known`
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    uint32_t* mine = histogram[rank];
-    for (int i = threadIdx.x; i < kDigits; i += kThreads) mine[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < here; i += kThreads) {
-      const uint32_t k = keys[i];
-      if (k != kAbsent && (k & mask) == known) atomicAdd(&mine[(k >> shift) & 0xff], 1u);
-    }
-    __syncthreads();
-    if (ctas > 1) {
-      for (int r = 0; r < ctas; ++r)
-        if (r != rank)
-          for (int i = threadIdx.x; i < kDigits; i += kThreads) send32(smem_at(&histogram[rank][i]), r, mine[i]);
+  if (ctas > 1) {
+    cluster_wait();  // all of the cluster's CTAs have begun
+    if (gather) {
+      if (rank > 0)
+        for (int i = threadIdx.x; i < here; i += kThreads) send32(smem_at(keys + from + i), 0, keys[i]);
       cluster_meet();
+      if (rank > 0) return;
+      ctas = 1;
+      from = 0;
+      here = pages;
     }
-    // every warp finds the byte for itself: a lane has 8 digits, the highest digits in lane 0
-    uint32_t n[8], all = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      n[i] = 0;
-      for (int r = 0; r < ctas; ++r) n[i] += histogram[r][kDigits - 1 - (8 * lane + i)];
-      all += n[i];
-    }
-    uint32_t upto = all;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(kFullMask, upto, o);
-      if (lane >= o) upto += x;
-    }
-    uint32_t above = upto - all, digit = 0;
-    const uint32_t has = __ballot_sync(kFullMask, wanted > above && wanted <= upto);
-    if (has == 0) {  // fewer keys than are wanted: all of them
-      known = 0;
-      mask = 0;
-      wanted = 0xffffffffu;
-      break;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (wanted > above && wanted <= above + n[i]) {
-        digit = kDigits - 1 - (8 * lane + i);
-        break;
-      }
-      above += n[i];
-    }
-    const int owner = __ffs(has) - 1;
-    digit = __shfl_sync(kFullMask, digit, owner);
-    wanted -= __shfl_sync(kFullMask, above, owner);
-    known |= digit << shift;
-    mask |= 0xffu << shift;
-    __syncthreads();  // the histograms are read
-    if (ctas > 1) cluster_meet();
   }
-  const bool all_taken = wanted == 0xffffffffu;
+
   // Chosen: keys above `known`, and the first `wanted` that equal it.
-  auto above_it = [&](uint32_t k) { return all_taken ? k != kAbsent : k > known; };
-  auto equals_it = [&](uint32_t k) { return !all_taken && k == known; };
-  uint32_t more = 0, equal = 0;
-  for (int i = threadIdx.x; i < here; i += kThreads) {
-    more += above_it(keys[i]);
-    equal += equals_it(keys[i]);
-  }
-  more = __reduce_add_sync(kFullMask, more);
-  equal = __reduce_add_sync(kFullMask, equal);
-  if (lane == 0) {
-    of_warps[warp][0] = more;
-    of_warps[warp][1] = equal;
-  }
-  __syncthreads();
-  more = equal = 0;
-  for (int i = 0; i < kWarps; ++i) {
-    more += of_warps[i][0];
-    equal += of_warps[i][1];
-  }
-  if (threadIdx.x < ctas) {
-    send32(smem_at(&counted[rank][0]), threadIdx.x, more);
-    send32(smem_at(&counted[rank][1]), threadIdx.x, equal);
-  }
-  if (ctas > 1)
-    cluster_meet();
+  uint32_t known, wanted;
+  if (ctas == 1)
+    find_here(keys, here, a.count, scratch, known, wanted, lane, warp);
   else
-    __syncthreads();
-  uint32_t more_before = 0, equal_before = 0, more_all = 0, equal_all = 0;
-  for (int r = 0; r < ctas; ++r) {
-    if (r < rank) {
-      more_before += counted[r][0];
-      equal_before += counted[r][1];
+    find_in_cluster(keys, here, a.count, scratch, known, wanted, ctas, rank, lane);
+  uint32_t more_before = 0, equal_before = 0;
+  if (ctas > 1) {
+    uint32_t more = 0, equal = 0;
+    for (int i = threadIdx.x; i < here; i += kThreads) {
+      more += keys[i] > known;
+      equal += keys[i] == known;
     }
-    more_all += counted[r][0];
-    equal_all += counted[r][1];
+    const Totals all = totals(scratch, more, equal, 0, 0, lane, warp);
+    if (threadIdx.x < ctas) {
+      send32(smem_at(&scratch.counted[rank][0]), threadIdx.x, all.x);
+      send32(smem_at(&scratch.counted[rank][1]), threadIdx.x, all.y);
+    }
+    cluster_meet();
+    for (int r = 0; r < rank; ++r) {
+      more_before += scratch.counted[r][0];
+      equal_before += scratch.counted[r][1];
+    }
   }
   // Written in order, a block of threads at a time.
   for (int i0 = 0; i0 < here; i0 += kThreads) {
     const int i = i0 + threadIdx.x;
     const uint32_t k = i < here ? keys[i] : kAbsent;
-    const uint32_t m = __ballot_sync(kFullMask, above_it(k)), e = __ballot_sync(kFullMask, equals_it(k));
+    const uint32_t m = __ballot_sync(kFullMask, k > known), e = __ballot_sync(kFullMask, k == known);
     __syncthreads();
     if (lane == 0) {
-      of_warps[warp][0] = __popc(m);
-      of_warps[warp][1] = __popc(e);
+      scratch.of_warps[warp][0] = __popc(m);
+      scratch.of_warps[warp][1] = __popc(e);
     }
     __syncthreads();
-    const uint32_t below = (1u << lane) - 1;
-    uint32_t m_at = more_before + __popc(m & below), e_at = equal_before + __popc(e & below);
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) {
-        m_at += of_warps[w][0];
-        e_at += of_warps[w][1];
-      }
-      more_before += of_warps[w][0];
-      equal_before += of_warps[w][1];
-    }
-    const bool chosen = above_it(k) || (equals_it(k) && e_at < wanted);
-    if (chosen) out[m_at + min(e_at, all_taken ? 0u : wanted)] = from + i;
+    const uint32_t below = (1u << lane) - 1, wm = lane < kWarps ? scratch.of_warps[lane][0] : 0u, we = lane < kWarps ? scratch.of_warps[lane][1] : 0u;
+    const uint32_t m_at = more_before + __popc(m & below) + __reduce_add_sync(kFullMask, lane < warp ? wm : 0u);
+    const uint32_t e_at = equal_before + __popc(e & below) + __reduce_add_sync(kFullMask, lane < warp ? we : 0u);
+    more_before += __reduce_add_sync(kFullMask, wm);
+    equal_before += __reduce_add_sync(kFullMask, we);
+    if (k > known || (k == known && e_at < wanted)) out[m_at + min(e_at, wanted)] = from + i;
   }
-  const uint32_t chosen = more_all + (all_taken ? 0u : min(equal_all, wanted));
-  if (rank == 0)
-    for (int i = chosen + threadIdx.x; i < a.count; i += kThreads) out[i] = -1;
+  if (rank == ctas - 1)  // whose counts are of all
+    for (uint32_t i = more_before + min(equal_before, wanted) + threadIdx.x; i < (uint32_t)a.count; i += kThreads) out[i] = -1;
 }
 
 }  // namespace
@@ -376,7 +517,7 @@ cudaError_t launch_summarise(const KvPages& cache, const Summary& summary, const
                              int64_t B, int64_t max_pages, const int32_t* first, const int32_t* lengths, bool pdl,
                              const DeviceInfo& dev, cudaStream_t stream) {
   // Warps in all: the GPU full once, a page a warp at least.
-  const int64_t most = (int64_t)dev.num_sms * 16, heads = B * cache.heads;
+  const int64_t most = (int64_t)dev.num_sms * 32, heads = B * cache.heads;
   int64_t shares = (most + heads - 1) / heads;
   if (shares > max_pages) shares = max_pages;
   cudaLaunchAttribute attr[1];
@@ -424,7 +565,8 @@ static cudaError_t launch_select_chunks(SelectArgs a, const KvPages& cache, cons
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)share * 4;
+  const bool gather = a.max_pages <= kGathered;
+  cfg.dynamicSmemBytes = (size_t)(gather ? a.max_pages : share) * 4;
   if (ctas > 1) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)ctas;
@@ -446,7 +588,7 @@ static cudaError_t launch_select_chunks(SelectArgs a, const KvPages& cache, cons
     part.lengths += b;
     part.blocks += b * cache.heads * a.count;
     cfg.gridDim = dim3((unsigned)ctas, (unsigned)cache.heads, (unsigned)(B - b < kMostSeqs ? B - b : kMostSeqs));
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, part, cache, summary, share);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, part, cache, summary, share, gather);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
