@@ -2,7 +2,7 @@
 // attention.cu says how it works and what bounds it; MODE says what a CTA's rows and tokens are:
 // the tokens of one sequence (kClusters, kSharedOut: attention.cu), the pages that a list names
 // (kBlocks: attention_blocks.cu), the tokens that a group of rows shares, and a row's own tokens
-// joined with those (kPrefix, kOwn: attention_shared.cu).
+// joined with those (kPrefix, kOwn, kPacked: attention_shared.cu).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,6 +25,7 @@ constexpr int kPortableCluster = 8;
 constexpr int kSms = 152;
 constexpr int kOtherSmem = 1024 + 640;  // of a CTA, beside the dynamic: the system's and the static arrays
 constexpr int kLeastSteps = 2;    // steps a warp at least: short rows take fewer CTAs
+constexpr int kWarpSteps = 4;     // kPacked: steps a warp at most, while a row has fewer than four warps
 constexpr int kShareSeqs = 1024;  // sequences that a CTA adds up to find its row
 constexpr int kSortSeqs = kThreads;  // sequences that a CTA ranks by length
 constexpr float kLimit = 256.0f;  // the largest weight before the reference moves
@@ -337,7 +338,8 @@ enum Mode {
   kSharedOut,  // the same, its tokens split in proportion over CTAs that leave parts behind
   kBlocks,     // a key head of a sequence and the pages that its list names, over a cluster
   kPrefix,     // a key head of a group of sequences and the tokens that they share; leaves parts behind
-  kOwn         // a key head of a sequence and its tokens behind the shared ones, joined with kPrefix's parts
+  kOwn,        // a key head of a sequence and its tokens behind the shared ones, joined with kPrefix's parts
+  kPacked      // the same, up to four rows of a sequence a CTA: one, two or four warps a row, by its tokens
 };
 
 // How rows are shared out.
@@ -352,7 +354,7 @@ struct Shares {
   // kBlocks: the pages' columns, `count` a key head of a sequence
   const int32_t* blocks;
   int count;
-  // kPrefix, kOwn: sequences a group, the tokens that each group shares, every sequence's length, and
+  // kPrefix, kOwn, kPacked: sequences a group, the tokens that each group shares, every sequence's length, and
   // q heads a key head (kPrefix's `group` holds those of all the group's sequences)
   int group_rows;
   const int32_t* shared;
@@ -418,6 +420,41 @@ __device__ __forceinline__ Part find_part(const AttendArgs& a, int64_t most, int
   return {__shfl_sync(kFullMask, b, owner), row, i - row * n, n};
 }
 
+// kPacked: this CTA's sequence, its first row there and how many warps a row has.
+struct Pack {
+  int64_t b;
+  int row, warps;  // warps == 0: the CTA has nothing
+};
+template <int T>
+__device__ __forceinline__ Pack find_pack(const AttendArgs& a, const Shares& sh, int64_t most) {
+  const int lane = threadIdx.x & 31, here = blockIdx.x;
+  const int each = ((int)a.B + 31) / 32, from = min((int)a.B, lane * each), to = min((int)a.B, from + each);
+  auto warps_of = [&](int b) {
+    Span<T> span(a.lengths[b], most, 0);
+    span.first = min(span.len, (uint32_t)max(0, sh.shared[b / sh.group_rows]));
+    const int steps = span.steps();
+    return steps <= kWarpSteps ? 1 : steps <= 2 * kWarpSteps ? 2 : 4;
+  };
+  auto ctas_of = [&](int b) { return (sh.rows_a_seq * warps_of(b) + kWarps - 1) / kWarps; };
+  int ctas = 0;
+  for (int b = from; b < to; ++b) ctas += ctas_of(b);
+  int upto = ctas;  // CTAs of this lane's sequences and all before
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(kFullMask, upto, o);
+    if (lane >= o) upto += n;
+  }
+  const uint32_t mine = __ballot_sync(kFullMask, here >= upto - ctas && here < upto);
+  if (mine == 0) return {0, 0, 0};
+  int b = from, at = upto - ctas;
+  if ((mine >> lane) & 1u)
+    for (int n; n = ctas_of(b), here >= at + n; ++b) at += n;
+  const int owner = __ffs(mine) - 1;
+  b = __shfl_sync(kFullMask, b, owner);
+  const int warps = warps_of(b);
+  return {b, (here - __shfl_sync(kFullMask, at, owner)) * (kWarps / warps), warps};
+}
+
 // The sequence that comes at place `at` when the longest is first (of equal ones, and
 // beyond 2^24 tokens, the one with the lowest number).  A key holds length and number:
 // one compare a pair of sequences.
@@ -440,7 +477,7 @@ __device__ __forceinline__ int64_t by_length(const AttendArgs& a, int at) {
   return found;
 }
 
-// kOwn: adds the parts `first`, `first` + `every`, ... of what the sequence's group shares to a warp's own
+// kOwn, kPacked: adds the parts `first`, `first` + `every`, ... of what the sequence's group shares to a warp's own
 // partials, in shared memory at `at`.  A lane takes 4 dims of a head; four parts are on their way together.
 template <int PARTIAL, int DT>
 __device__ __forceinline__ void add_prefix(const AttendArgs& a, const KvPages& c, const Shares& sh, int64_t b, int hk,
@@ -542,7 +579,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   // The CTA's row (sequence b, head `row` of its key heads and groups of q heads)
   // and its place among the row's CTAs.
   int64_t b;
-  int row, split, splits;
+  int row, split, splits, row_warps = kWarps;
   if (MODE == kSharedOut || (MODE == kPrefix && sh.splits == 0)) {
     const Part p = find_part<S::kTokens>(a, most, rows_a_seq);
     if (p.parts == 0) return;
@@ -551,6 +588,15 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     split = p.part;
     splits = p.parts;
     if (split == 0 && threadIdx.x == 0) sh.rows[b * rows_a_seq + row] = make_int2(blockIdx.x, splits);
+  } else if constexpr (MODE == kPacked) {
+    const Pack p = find_pack<S::kTokens>(a, sh, most);
+    row_warps = p.warps;
+    if (row_warps == 0) return;
+    b = p.b;
+    row = p.row + warp / row_warps;
+    if (row >= rows_a_seq) return;  // whole rows' warps: nobody waits for them
+    split = 0;
+    splits = 1;
   } else {
     splits = sh.splits;
     split = blockIdx.x & (splits - 1);
@@ -560,6 +606,17 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     if (MODE == kPrefix && split == 0 && threadIdx.x == 0) sh.rows[b * rows_a_seq + row] = make_int2(blockIdx.x, splits);
   }
 
+  constexpr bool kBehind = MODE == kOwn || MODE == kPacked;  // tokens behind the shared ones
+  const int workers = splits * row_warps, first_warp = MODE == kPacked ? warp & ~(row_warps - 1) : 0, me = split * row_warps + warp - first_warp;
+  // the warps of a row meet
+  auto meet = [&]() {
+    if (MODE != kPacked || row_warps == kWarps)
+      __syncthreads();
+    else if (row_warps == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / 2) : "memory");
+  };
   const int hk = sh.groups == 1 ? row : row / sh.groups, first_of_group = (row - hk * sh.groups) * kRowHeads;
   const int heads = min(kRowHeads, group - first_of_group), hq = hk * group + first_of_group;
   // q of the row's heads, on its way while the pages are looked up: 0.2 us of the smallest
@@ -569,7 +626,7 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   const uint32_t of_group = MODE == kPrefix ? first_of_group + min(g, heads - 1) : 0;
   const uint32_t member = MODE == kPrefix ? of_group / (uint32_t)sh.heads_a_key : 0, in_key = of_group - member * sh.heads_a_key;
   float2 qx[S::kSteps], qy[S::kSteps];
-  if (warp == 0) {
+  if (MODE == kPacked || warp == 0) {
     const float* q = MODE == kPrefix ? a.q + (b * sh.group_rows + member) * a.q_stride + (int64_t)(hk * sh.heads_a_key + in_key) * D
                                      : a.q + b * a.q_stride + (int64_t)(hq + min(g, heads - 1)) * D;
 #pragma unroll
@@ -611,13 +668,13 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
       if (c.page_shift == 4) page[1] = t + 16 < columns ? table[(t + 16) >> 4] : -1;
     }
   };
-  const uint32_t lap = (uint32_t)splits * (kWarps * S::kTokens);
-  uint32_t t_ask = (uint32_t)(split * kWarps + warp) * S::kTokens;
-  if (MODE != kOwn && a.window <= 0) look_up(t_ask);  // the first page is known before the length
+  const uint32_t lap = (uint32_t)workers * S::kTokens;
+  uint32_t t_ask = (uint32_t)me * S::kTokens;
+  if (!kBehind && a.window <= 0) look_up(t_ask);  // the first page is known before the length
   Span<S::kTokens> span(MODE == kBlocks ? 0 : a.lengths[b], most, a.window);
   if constexpr (MODE == kBlocks) span.len = (uint32_t)most;
-  if constexpr (MODE == kOwn) span.first = min(span.len, (uint32_t)max(0, sh.shared[b / sh.group_rows]));
-  if (MODE == kOwn || a.window > 0) {
+  if constexpr (kBehind) span.first = min(span.len, (uint32_t)max(0, sh.shared[b / sh.group_rows]));
+  if (kBehind || a.window > 0) {
     t_ask += span.begin();
     look_up(t_ask);
   }
@@ -676,9 +733,11 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   // next, the dims of a k-step in the order the key words give them.  Kept in shared
   // memory behind the rings and read again in every step: in registers it was 20 to 64
   // of them a thread, a CTA less an SM, and spills.
-  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem), q_area = base + (uint32_t)S::kSmem;
+  // kPacked: each warp has parts of its own.
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+  const uint32_t q_area = base + (uint32_t)S::kSmem + (MODE == kPacked ? warp * (min(kRowHeads, group) * S::kHeadBytes + kRowHeads * 4) : 0);
   const uint32_t thirds = q_area + S::kSteps * heads * 64, q_scales = q_area + heads * S::kHeadBytes;
-  if (warp == 0) {
+  if (MODE == kPacked || warp == 0) {
     // scale log2(e) is a pair: its second part goes into q's last, so a row's logits have no
     // rounding of it in common
     const float factor = a.factor, more = a.factor_rest;
@@ -719,7 +778,10 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
       if (qd == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(q_scales + 4 * g), "f"(up) : "memory");
     }
   }
-  __syncthreads();
+  if constexpr (MODE == kPacked)
+    __syncwarp();
+  else
+    __syncthreads();
   const uint32_t q_lane = min(g, heads - 1) * 4 + qd, q_stride = heads * 64;  // [k-step][head][lane]: no bank twice
   const float row_scale = lds_float(q_scales + 4 * min(g, heads - 1));
 
@@ -955,12 +1017,11 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     part[DT] = ref;
     part[DT + 1] = sum;
   }
-  if constexpr (MODE == kOwn) {
+  if constexpr (kBehind) {
     __syncwarp();
-    add_prefix<S::kPartial, DT>(a, c, sh, b, hk, first_of_group, heads, split * kWarps + warp, splits * kWarps,
-                                base + warp * S::kWarpBytes, lane);
+    add_prefix<S::kPartial, DT>(a, c, sh, b, hk, first_of_group, heads, me, workers, base + warp * S::kWarpBytes, lane);
   }
-  __syncthreads();
+  meet();
 
   auto of_warps = [&](int h, int d) {
     const uint32_t p = base + h * S::kPartial;
@@ -970,6 +1031,14 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   auto finish = [&](int h, int d, const Joined& j) {
     a.out[b * a.out_stride + (int64_t)(hq + h) * D + d] = output_of(j.value, j.m, j.sum);
   };
+  if constexpr (MODE == kPacked) {
+    for (int i = threadIdx.x - 32 * first_warp; i < heads * D; i += 32 * row_warps) {
+      const int h = head_of(i), d = i - h * D;
+      const uint32_t p = base + first_warp * S::kWarpBytes + h * S::kPartial;
+      finish(h, d, join<kWarps>(p + 4 * d, S::kWarpBytes, p + 4 * DT, S::kWarpBytes, row_warps));
+    }
+    return;
+  }
   if (MODE == kSharedOut || MODE == kPrefix || splits == 1) {
     const bool whole = MODE != kPrefix && splits == 1;
     float* part = whole ? nullptr : sh.parts + (int64_t)blockIdx.x * min(kRowHeads, group) * (D + 4);
@@ -1065,23 +1134,24 @@ inline void set_factor(AttendArgs& a) {  // scale log2(e), to the base of the we
   a.factor_rest = (float)(a.factor != 0.0f ? factor / a.factor - 1.0 : 0.0);
 }
 
-// A grid of sh.splits CTAs a row, as clusters, in launches of as many sequences as a grid holds.
-template <int FORMAT, int DT, Mode MODE>
-cudaError_t launch_clusters(const AttendArgs& a, const KvPages& c, Shares sh, int smem, bool pdl, cudaStream_t stream) {
+// `a_seq` CTAs a sequence, in clusters of `cluster`, in launches of as many sequences as a grid holds.
+template <typename Kernel>
+cudaError_t launch_grids(Kernel kernel, const AttendArgs& a, const KvPages& c, Shares sh, int64_t a_seq, int cluster, int smem, bool pdl,
+                         cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
-  const int64_t per_launch = (int64_t)0x7fffffff / ((int64_t)sh.rows_a_seq * sh.splits);  // sequences a grid holds
+  const int64_t per_launch = (int64_t)0x7fffffff / a_seq;  // sequences a grid holds
   for (sh.b0 = 0; sh.b0 < a.B; sh.b0 += per_launch) {
     const int64_t n = a.B - sh.b0 < per_launch ? a.B - sh.b0 : per_launch;
-    cfg.gridDim = dim3((unsigned)(n * sh.rows_a_seq * sh.splits), 1, 1);
+    cfg.gridDim = dim3((unsigned)(n * a_seq), 1, 1);
     cfg.numAttrs = 0;
-    if (sh.splits > 1) {
+    if (cluster > 1) {
       attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-      attr[cfg.numAttrs].val.clusterDim.x = (unsigned)sh.splits;
+      attr[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
       attr[cfg.numAttrs].val.clusterDim.y = 1;
       attr[cfg.numAttrs].val.clusterDim.z = 1;
       ++cfg.numAttrs;
@@ -1091,10 +1161,16 @@ cudaError_t launch_clusters(const AttendArgs& a, const KvPages& c, Shares sh, in
       attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
       ++cfg.numAttrs;
     }
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, attend_kernel<FORMAT, DT, MODE>, a, c, sh);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, c, sh);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
+}
+
+// sh.splits CTAs a row, a cluster.
+template <int FORMAT, int DT, Mode MODE>
+cudaError_t launch_clusters(const AttendArgs& a, const KvPages& c, const Shares& sh, int smem, bool pdl, cudaStream_t stream) {
+  return launch_grids(attend_kernel<FORMAT, DT, MODE>, a, c, sh, (int64_t)sh.rows_a_seq * sh.splits, sh.splits, smem, pdl, stream);
 }
 
 // f(format, padded head size) of a cache, as constants.

@@ -24,6 +24,7 @@ struct Sizes {
   bool wide;
 };
 constexpr int64_t kWideHeads = 24;
+constexpr int64_t kPackedRows = 300;  // a row a key head of a sequence: from so many on they fill the GPU without clusters
 Sizes sizes_of(int64_t B, int q_heads, int kv_heads, int head_dim, int64_t groups) {
   Sizes s;
   s.group_rows = B / groups;
@@ -47,6 +48,8 @@ cudaError_t launch_shape(AttendArgs a, const KvPages& c, const int32_t* shared, 
   static thread_local int configured_device = -1, most_cluster;
   if (configured_device != dev.device) {
     cudaError_t err = allow_shared_memory<S>(attend_kernel<FORMAT, DT, kPrefix>);
+    if (err == cudaSuccess)
+      err = cudaFuncSetAttribute(attend_kernel<FORMAT, DT, kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem + kWarps * kRowHeads * (S::kHeadBytes + 4));
     if (err == cudaSuccess) err = allow_clusters<S>(attend_kernel<FORMAT, DT, kOwn>, &most_cluster);
     if (err != cudaSuccess) return err;
     configured_device = dev.device;
@@ -106,9 +109,14 @@ cudaError_t launch_shape(AttendArgs a, const KvPages& c, const int32_t* shared, 
   sh.groups = (sh.group + kRowHeads - 1) / kRowHeads;
   sh.rows_a_seq = c.heads * sh.groups;
   const int heads = sh.group < kRowHeads ? sh.group : kRowHeads;
+  const int64_t rows = a.B * sh.rows_a_seq;
+  if (rows >= kPackedRows && a.B <= kShareSeqs) {
+    smem = (int)S::kSmem + kWarps * (heads * S::kHeadBytes + kRowHeads * 4);
+    return launch_grids(attend_kernel<FORMAT, DT, kPacked>, a, c, sh, sh.rows_a_seq, 1, smem, true, stream);
+  }
   smem = (int)S::kSmem + heads * S::kHeadBytes + kRowHeads * 4;
   const int own_ctas = resident_ctas<S>(dev, smem + received_bytes(heads, c.head_dim, kMaxCluster));
-  sh.splits = splits_for(a.B * sh.rows_a_seq, steps, own_ctas, most_cluster);
+  sh.splits = splits_for(rows, steps, own_ctas, most_cluster);
   sh.splits_log2 = 0;
   while ((1 << sh.splits_log2) < sh.splits) ++sh.splits_log2;
   return launch_clusters<FORMAT, DT, kOwn>(a, c, sh, smem + received_bytes(heads, c.head_dim, sh.splits), true, stream);

@@ -11,6 +11,8 @@
 // w = max(p_i - q_i, 0) (p_i where all drafts are taken, or where w is 0 everywhere).  Every
 // weight counts as a whole number of 2^-s, s = 62 - ceil(log2 V), so that sums of V of them are exact
 // in 64 bits whatever their order, and the token is the first whose running sum passes r * total.
+#include <type_traits>
+
 #include "serve.cuh"
 
 namespace bitlinear {
@@ -250,13 +252,13 @@ __device__ __forceinline__ float4 load_four(const float* row, int64_t v, int64_t
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 
-// A CTA's run of the row in turns of four values a thread; the weights of NV turns stay in registers, and where
+// A warp takes a run of the row in turns of four values a lane; the weights of NV turns stay in registers, and where
 // there are more of them (NV == 0) the run that has the token is walked through again.  Sums are told warp by
-// warp, so that the cluster meets once.  ALIGNED: rows start on 16 bytes.
-template <int NV, bool ALIGNED>
-__global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(VerifyArgs a) {
+// warp: the cluster meets once, and every warp then knows whether the token is in its run.  ALIGNED: rows start on
+// 16 bytes.  CTAS: as many fit an SM.
+template <int NV, bool ALIGNED, int CTAS>
+__global__ void __launch_bounds__(kVerifyThreads, CTAS) verify_kernel(VerifyArgs a) {
   __shared__ unsigned long long told[2][kMostCtas * kVerifyWarps];
-  __shared__ unsigned long long turns[(NV ? NV : 1) * kVerifyWarps];  // of each turn and warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ctas = gridDim.x, rank = blockIdx.x;
   pdl_release_dependents();
@@ -291,13 +293,14 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(VerifyArgs a)
   const float* p = a.p + (b * (K + 1) + n) * V;
   const float* q = refused ? a.q + (b * K + n) * V : nullptr;
 
-  const int64_t fours = (V + 3) / 4, share = (fours + ctas - 1) / ctas, from = min(fours, rank * share), to = min(fours, from + share);
-  auto weights = [&](int64_t i) {
+  const int fours = (int)((V + 3) / 4), share = (fours + ctas * kVerifyWarps - 1) / (ctas * kVerifyWarps);
+  const int from = min(fours, (rank * kVerifyWarps + warp) * share), to = min(fours, from + share);
+  auto weights = [&](int i) {
     float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (i < to) {
-      w = load_four<ALIGNED>(p, 4 * i, V);
+      w = load_four<ALIGNED>(p, 4 * (int64_t)i, V);
       if (q) {
-        const float4 d = load_four<ALIGNED>(q, 4 * i, V);
+        const float4 d = load_four<ALIGNED>(q, 4 * (int64_t)i, V);
         w = make_float4(__fsub_rn(w.x, d.x), __fsub_rn(w.y, d.y), __fsub_rn(w.z, d.z), __fsub_rn(w.w, d.w));
       }
     }
@@ -308,40 +311,34 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(VerifyArgs a)
   float4 held[kHeld];
   unsigned long long total = 0, before = 0, mine = 0;
   for (int attempt = 0;; ++attempt) {
-    unsigned long long s = 0;
+    mine = 0;
     if constexpr (NV > 0) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) held[j] = weights(from + threadIdx.x + j * kVerifyThreads);
-      if (attempt > 0) __syncthreads();  // the first attempt's sums are read
+      for (int j = 0; j < NV; ++j) held[j] = weights(from + lane + 32 * j);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const unsigned long long t = warp_sum(sum_of(held[j]));
-        if (lane == 0) turns[j * kVerifyWarps + warp] = t;
-        s += t;
-      }
+      for (int j = 0; j < NV; ++j) mine += sum_of(held[j]);
     } else {
-      for (int64_t i = from + threadIdx.x; i < to; i += kVerifyThreads) s += sum_of(weights(i));
-      s = warp_sum(s);
+      for (int i = from + lane; i < to; i += 32) mine += sum_of(weights(i));
     }
+    mine = warp_sum(mine);
+    const int here = rank * kVerifyWarps + warp;
     if (ctas == 1) {
-      if (lane == 0) told[attempt][warp] = s;
+      if (lane == 0) told[attempt][warp] = mine;
       __syncthreads();
     } else {
       if (attempt == 0) cluster_wait();  // all of the cluster's CTAs have begun
-      if (lane < ctas) send64(smem_at(told[attempt] + rank * kVerifyWarps + warp), lane, s);
+      if (lane < ctas) send64(smem_at(told[attempt] + here), lane, mine);
       cluster_arrive();
       cluster_wait();
     }
-    unsigned long long all = 0, ahead = 0, here = 0;
+    unsigned long long all = 0, ahead = 0;
     for (int i = lane; i < ctas * kVerifyWarps; i += 32) {
       const unsigned long long t = told[attempt][i];
       all += t;
-      ahead += i < rank * kVerifyWarps ? t : 0ull;
-      here += i / kVerifyWarps == rank ? t : 0ull;
+      ahead += i < here ? t : 0ull;
     }
     total = warp_sum(all);
     before = warp_sum(ahead);
-    mine = warp_sum(here);
     if (total != 0 || !q) break;
     q = nullptr;  // nothing is left of p - q: p itself
   }
@@ -358,44 +355,25 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(VerifyArgs a)
   const float r = fminf(fmaxf(last, 0.0f), 0.99999994f);
   const unsigned long long goal = __umul64hi((unsigned long long)((double)r * 18446744073709551616.0), total);
   if (total == 0 || goal < before || goal >= before + mine) return;
-  // This CTA's run has it.  `upto`: the weights ahead of this lane's four, whose first is v; writes the token if one of
-  // them passes the goal.
-  auto look_at = [&](const float4& w, unsigned long long upto, int64_t v) {
+  // This warp's run has it.
+  auto look_at = [&](const float4& w, int i) {  // the i-th four of the row, a lane each
+    unsigned long long s = sum_of(w), upto = before + warp_upto(s, lane);
+    before = __shfl_sync(kFullMask, upto, 31);
+    upto -= s;
     const float x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const unsigned long long u = units(x[j], a.scale);
-      if (upto <= goal && upto + u > goal) a.tokens[b * (K + 1) + n] = (int32_t)(v + j);
+      if (upto <= goal && upto + u > goal) a.tokens[b * (K + 1) + n] = (int32_t)(4 * i + j);
       upto += u;
     }
   };
   if constexpr (NV > 0) {
-    unsigned long long at = before;  // ahead of turn j of this warp
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const unsigned long long t = lane < kVerifyWarps ? turns[j * kVerifyWarps + lane] : 0ull;
-      const unsigned long long ahead = warp_sum(lane < warp ? t : 0ull), all = warp_sum(t);
-      if (goal >= at + ahead && goal < at + all) {  // this warp's, perhaps
-        const unsigned long long s = sum_of(held[j]);
-        look_at(held[j], at + ahead + warp_upto(s, lane) - s, 4 * (from + threadIdx.x + j * kVerifyThreads));
-      }
-      at += all;
-    }
+    for (int j = 0; j < NV; ++j)
+      if (before <= goal) look_at(held[j], from + lane + 32 * j);
   } else {
-    unsigned long long at = before;
-    for (int64_t i0 = from; i0 < to; i0 += kVerifyThreads) {
-      const int64_t i = i0 + threadIdx.x;
-      const float4 w = weights(i);
-      const unsigned long long s = sum_of(w), in_warp = warp_upto(s, lane);
-      __syncthreads();
-      if (lane == 31) turns[warp] = in_warp;
-      __syncthreads();
-      const unsigned long long t = lane < kVerifyWarps ? turns[lane] : 0ull;
-      const unsigned long long ahead = warp_sum(lane < warp ? t : 0ull), all = warp_sum(t);
-      look_at(w, at + ahead + in_warp - s, 4 * i);
-      if (at + all > goal) return;
-      at += all;
-    }
+    for (int i = from; i < to && before <= goal; i += 32) look_at(weights(i + lane), i + lane);
   }
 }
 
@@ -455,12 +433,20 @@ cudaError_t launch_verify(const float* p, const float* q, const int32_t* draft, 
   int ctas = 1;
   while (ctas < kMostCtas && (fours > (int64_t)ctas * kVerifyThreads * 7 || (fours > (int64_t)ctas * kVerifyThreads && B * ctas < 4 * (int64_t)dev.num_sms)))
     ctas *= 2;
-  const int64_t held = ((fours + ctas - 1) / ctas + kVerifyThreads - 1) / kVerifyThreads;
+  const int64_t held = ((fours + ctas * kVerifyWarps - 1) / (ctas * kVerifyWarps) + 31) / 32;
   const bool aligned = V % 4 == 0;
-  const auto kernel = held <= 1   ? (aligned ? verify_kernel<1, true> : verify_kernel<1, false>)
-                      : held <= 4 ? (aligned ? verify_kernel<4, true> : verify_kernel<4, false>)
-                      : held <= 7 ? (aligned ? verify_kernel<7, true> : verify_kernel<7, false>)
-                                  : (aligned ? verify_kernel<0, true> : verify_kernel<0, false>);
+  // Seven turns take more registers than four CTAs an SM have: 8.5 us for one sequence of 50000 tokens with two and
+  // 10.2 with four, 18.7 and 16.7 for 64.
+  const bool few = B * ctas <= 2 * (int64_t)dev.num_sms;
+  const auto of_turns = [&](auto turns) {
+    constexpr int NV = decltype(turns)::value;
+    if (few) return aligned ? verify_kernel<NV, true, 2> : verify_kernel<NV, false, 2>;
+    return aligned ? verify_kernel<NV, true, 4> : verify_kernel<NV, false, 4>;
+  };
+  const auto kernel = held <= 1   ? of_turns(std::integral_constant<int, 1>())
+                      : held <= 4 ? of_turns(std::integral_constant<int, 4>())
+                      : held <= 7 ? of_turns(std::integral_constant<int, 7>())
+                                  : of_turns(std::integral_constant<int, 0>());
   int bits = 62;
   while (((int64_t)1 << (62 - bits)) < V) --bits;
   const float scale = (float)((int64_t)1 << bits);

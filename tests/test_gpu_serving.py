@@ -92,6 +92,18 @@ def test_shared(fmt, groups, R, Hq, Hkv, D, S, own, page):
 
 
 @pytest.mark.parametrize("fmt", attention_plain.FORMATS)
+@pytest.mark.parametrize("groups,R,Hq,Hkv,D,S,own,page", [(1, 80, 4, 4, 48, 70, 30, 16), (2, 31, 10, 5, 80, 100, 700, 32), (5, 4, 48, 16, 128, 33, 400, 16),
+                                                           (1, 40, 72, 8, 64, 50, 300, 64), (60, 5, 2, 1, 240, 20, 500, 16), (1, 1100, 1, 1, 16, 40, 20, 16)])
+def test_shared_of_many_rows(fmt, groups, R, Hq, Hkv, D, S, own, page):
+    """Enough rows that one CTA takes several of them: one, two or four warps a row, by the tokens of its own."""
+    rng = np.random.default_rng(own)
+    shared = rng.integers(max(1, S // 2), S + 1, groups)
+    more = rng.integers(0, 20, groups * R)
+    more[::7] = rng.integers(0, own + 1, len(more[::7]))
+    run_shared(fmt, groups, R, Hq, Hkv, D, shared, np.repeat(shared, R) + more, page, seed=S)
+
+
+@pytest.mark.parametrize("fmt", attention_plain.FORMATS)
 @pytest.mark.parametrize("R,Hq,Hkv,D,n", [(5, 4, 4, 80, 100), (2, 8, 2, 128, 31), (9, 8, 1, 64, 47), (20, 4, 1, 96, 333)])
 def test_drafted_rows_share_everything(fmt, R, Hq, Hkv, D, n):
     """Rows of one sequence that see one token more each; the longest sees all that is shared."""
