@@ -3,24 +3,26 @@
 // A row of work is 128 q heads (all of a group's rows' for one key head, or 128 of them) and a run
 // of the group's shared tokens, in tiles of 128:
 //   S = Q K^T (TMEM), P = 2^(S - ref) in registers, back to TMEM as the next product's A operand, O = P V (TMEM).
-// fp32 accuracy takes two MMAs for one: q and the weights are split into two fp16 parts (22 bits), codes are exact
-// in fp16.  q's row is scaled to 2^13 .. 2^14 and the weights to at most 2^15, so that what a leading part
-// leaves is still a whole fp16 (its last place 2^-38 of the row's largest q, 2^-36 of the largest weight) and
-// both parts add up in one accumulator, the small ones first.  bf16 values become fp16 under a power
-// of two that a tile of 128 tokens has in common (below): those above 2^-22 of the tile's largest are exact.
+// fp32 accuracy takes two MMAs for one, or three.  Codes are exact in fp16, and q and the weights are split into two fp16
+// parts (22 bits): q's row is scaled to 2^13 .. 2^14 and the weights to at most 2^15, so that what a leading part
+// leaves is still a whole fp16 (its last place 2^-38 of the row's largest q, 2^-36 of the largest weight), and
+// both parts add up in one accumulator, the small ones first.  bf16 keys are used as they are, with q in three
+// bf16 parts (24 bits).  bf16 values become fp16 under a power of two that a tile of 128 tokens has in common
+// (below): those above 2^-28 of the tile's largest are exact.
 // Each tile's O starts from zero and is added to fp32 sums in registers: the tensor cores' adder cuts toward
 // zero, and a chain of tiles in it would show.
 //
 // 28 warps: two groups of eight that turn logits into weights and add up O, each for every other tile with a
 // reference and sums of its own (two threads a row, half of a tile's tokens and half of the dims each: they tell each
-// other their largest logits); eight that widen K and V
-// widen the codes and lay them out for the MMA (128-byte swizzle, the same image for both: K is the B
-// operand along its rows, V across them); one that looks pages up, four tiles ahead, and
-// asks for them to come into L2; one thread that issues the products of S and one that issues those of O.
-// Two S, two O, two K and two V are in flight; a weight overwrites its logit's place.
+// other their largest logits); eight that widen codes (bf16: values) and lay them out for the MMA (128-byte swizzle,
+// the same image for both: K is the B operand along its rows, V across them); one that looks pages up, four
+// tiles ahead, and asks for them to come into L2; one that copies rows as they are needed (bulk copies, TMA for
+// bf16); one thread that issues the products of S and one that issues those of O.  Two S and two O are in
+// flight, K and V tiles take turns in one ring, and a weight overwrites its logit's place.
 #include "attend.cuh"
 #include "serve.cuh"
 #include "tc_util.cuh"
+#include "tensor_map.cuh"
 
 namespace bitlinear {
 namespace {
@@ -38,15 +40,19 @@ constexpr int kLaunchRegisters = 72, kAddRegisters = 104, kBringRegisters = 32, 
 static_assert(512 * kAddRegisters + kBringThreads * kBringRegisters + 128 * kIssueRegisters <= kWideThreads * kLaunchRegisters,
               "more registers than were launched with would be waited for");
 
+struct Maps {  // of a bf16 cache: [page][head and token][dim], boxes of 16 tokens of 64 dims
+  CUtensorMap keys, values;
+};
 struct Entry {
-  int64_t row[kTile / 16];  // of each 16 tokens: ((page * heads) + head) * page_size + offset, or -1
+  // of each 16 tokens: ((page * heads) + head) * page_size + offset (bf16: the page above 32 bits of the rest), or -1
+  int64_t row[kTile / 16];
 };
 
 // What the roles tell each other.
 template <bool BF16>
 struct State {
-  float k_steps[kEntries][BF16 ? 4 : kTile], v_steps[kEntries][BF16 ? 4 : kTile];  // bf16: a tile's power of two, first
-  float v_most[kEntries][4];
+  float k_steps[kEntries][BF16 ? 4 : kTile], v_steps[kEntries][BF16 ? 4 : kTile];
+  float v_most[kEntries][4];  // the largest of the latter, by warp; bf16: a tile's power of two, first
   Entry entries[kEntries];
   float row_tops[2][2][kRows];  // by tile's parity and half of its tokens; before the first tile q's scales, in the first
   uint32_t tops[2][8];
@@ -62,13 +68,13 @@ struct Wide {
   static constexpr int kBytes = kBf16 ? 2 : 1;
   static constexpr int kPanels = (DT + 63) / 64;
   static constexpr int kOperand = kPanels * kPanel;
-  static constexpr int kLanes = 8 * kBytes;            // lanes of a token's row, 16 bytes each
-  static constexpr int kPieces = DT * kBytes / 16;     // of them that a row fills
-  static constexpr int kTurn = kBringThreads / kLanes; // tokens that are widened at once
-  static constexpr int kStages = 3;                    // K and V tiles as operands
-  static constexpr int kRaw = kTile * DT * kBytes;     // and as they come, rows of the cache's size side by side
-  static constexpr int kRaws = kBf16 ? 2 : 3;
-  static constexpr int kOperands = 2 * kOperand + kStages * kOperand + kRaws * kRaw;  // Q's parts first
+  static constexpr int kPieces = DT / 16;              // 16-byte pieces of a token's 8-bit codes
+  static constexpr int kTurn = kBringThreads / 8;      // tokens whose codes are widened at once
+  static constexpr int kStages = kBf16 ? 4 : 3;        // K and V tiles as operands
+  static constexpr int kRaw = kTile * DT;              // and 8-bit codes as they come, rows of the cache's size side by side
+  static constexpr int kRaws = kBf16 ? 0 : 3;          // (bf16 comes as operands)
+  static constexpr int kParts = kBf16 ? 3 : 2;         // of q
+  static constexpr int kOperands = kParts * kOperand + kStages * kOperand + kRaws * kRaw;  // Q's parts first
   static constexpr int kNeed = kOperands + (int)sizeof(State<kBf16>);
   // the base is rounded up to 1024, where it is not there already (a kernel without static arrays has it there)
   static constexpr int kSmem = kNeed + 1024 < 232448 ? kNeed + 1024 : 232448;
@@ -106,6 +112,11 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[16]) {
                  "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
+}
+__device__ __forceinline__ float largest_of(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ float4 lds_float4(uint32_t a) {
   const uint4 w = lds128(a);
@@ -154,12 +165,13 @@ __device__ __forceinline__ void drain(unsigned long long* bar, uint32_t parity, 
 }
 
 template <int FORMAT, int DT>
-__global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs a, KvPages c, Shares sh, int* status) {
+__global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs a, KvPages c, Shares sh, const __grid_constant__ Maps maps,
+                                                                      int* status) {
   using W = Wide<FORMAT, DT>;
   extern __shared__ __align__(1024) uint8_t raw[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = c.head_dim;
   const uint32_t base = ((uint32_t)__cvta_generic_to_shared(raw) + 1023u) & ~1023u;
-  const uint32_t q_at = base, stage_at = base + 2 * W::kOperand, raw_at = stage_at + W::kStages * W::kOperand;
+  const uint32_t q_at = base, stage_at = base + W::kParts * W::kOperand, raw_at = stage_at + W::kStages * W::kOperand;
   uint32_t given;
   asm volatile("mov.u32 %0, %%dynamic_smem_size;" : "=r"(given));
   if (base + W::kNeed > (uint32_t)__cvta_generic_to_shared(raw) + given) {  // not where it was expected
@@ -274,25 +286,39 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         for (int j = 0; j < 4; ++j) {
           const int i = i0 + kBring * j;
           const float2 x = mul2(make_float2(w[j].x, w[j].y), both(factor)), y = mul2(make_float2(w[j].z, w[j].w), both(factor));
-          const float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
-          const int e = clamp_exponent(exponent_of(__uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(top)))));
-          const float2 up = both(power2(13 - e)), rest_up = both(power2(13 - e) * more);
-          uint32_t lead[2], rest[2];
+          uint32_t words[W::kParts][2];
+          if constexpr (W::kBf16) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 z = k ? y : x, v = mul2(z, up);
-            const __half2 h = __floats2half2_rn(v.x, v.y);
-            const float2 d = fma2(z, rest_up, fma2(__half22float2(h), both(-1.0f), v));
-            const __half2 g = __floats2half2_rn(d.x, d.y);
-            lead[k] = *reinterpret_cast<const uint32_t*>(&h);
-            rest[k] = *reinterpret_cast<const uint32_t*>(&g);
+            for (int k = 0; k < 2; ++k) {
+              float u = k ? y.x : x.x, v = k ? y.y : x.y;
+              const float2 rest = mul2(make_float2(u, v), both(more));
+              words[0][k] = next_part(u, v);
+              words[1][k] = next_part(u, v);
+              u += rest.x;
+              v += rest.y;
+              words[2][k] = next_part(u, v);
+            }
+          } else {
+            const float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
+            const int e = clamp_exponent(exponent_of(__uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(top)))));
+            const float2 up = both(power2(13 - e)), rest_up = both(power2(13 - e) * more);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float2 z = k ? y : x, v = mul2(z, up);
+              const __half2 h = __floats2half2_rn(v.x, v.y);
+              const float2 d = fma2(z, rest_up, fma2(__half22float2(h), both(-1.0f), v));
+              const __half2 g = __floats2half2_rn(d.x, d.y);
+              words[0][k] = *reinterpret_cast<const uint32_t*>(&h);
+              words[1][k] = *reinterpret_cast<const uint32_t*>(&g);
+            }
+            if (lane == 0) st.row_tops[0][0][i] = power2(e - 13);
           }
           if (4 * lane < DT) {
             const uint32_t at = q_at + of_panel(i, 4 * lane) + (lane & 1) * 8;
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(lead[0]), "r"(lead[1]) : "memory");
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + W::kOperand), "r"(rest[0]), "r"(rest[1]) : "memory");
+#pragma unroll
+            for (int k = 0; k < W::kParts; ++k)
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + k * W::kOperand), "r"(words[k][0]), "r"(words[k][1]) : "memory");
           }
-          if (lane == 0) st.row_tops[0][0][i] = power2(e - 13);
         }
       }
       tc::fence_proxy_async_smem();
@@ -300,7 +326,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       if (lane == 0) tc::mbar_arrive(&st.q_full);
     }
     tc::named_bar_sync(3, 32 * kBring);
-    const float row_scale = st.row_tops[0][0][r];
+    const float unit = W::kBf16 ? 1.0f : st.row_tops[0][0][r];  // of a logit in S
     tc::named_bar_sync(3, 32 * kBring);
     const bool none = (warp & 3) * 32 >= heads;  // rows of no q head: whatever comes of them is theirs
     const uint32_t row_end = there ? min(len, (uint32_t)max(0, sh.lengths[seq])) : 0u;
@@ -333,9 +359,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       const bool whole = __all_sync(kFullMask, ok == 0xfu && count == kSide);
       const uint32_t ks = (uint32_t)__cvta_generic_to_shared(st.k_steps[entry]) + (W::kBf16 ? 0 : 4 * kSide * side);
       const uint32_t vs = (uint32_t)__cvta_generic_to_shared(st.v_steps[entry]) + (W::kBf16 ? 0 : 4 * kSide * side);
-      float unit = row_scale;
-      if constexpr (W::kBf16) unit = fmaxf(unit * lds_float(ks), 1.1754944e-38f);  // a masked logit times 0 is none
-      // The 16 logits (over `unit`) of granule g.  Loops over granules stay rolled up: code is fetched as it runs, and
+      // The 16 logits over `unit` of granule g.  Loops over granules stay rolled up: code is fetched as it runs, and
       // unrolled they took three times as long.
       auto logits = [&](int g, uint32_t (&s)[16], float2 (&x)[8]) {
 #pragma unroll
@@ -372,15 +396,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         for (int k = 0; k < kTogether; ++k) {
           logits(g + k, s[k], x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
+          for (int i = 0; i < 8; ++i) top = largest_of(top, x[i].x, x[i].y);
         }
       }
       st.row_tops[par][side][r] = top;
-      wait(&st.stage_full[place_of_v(n) % W::kStages], place_of_v(n) / W::kStages);  // the values' steps
       tc::named_bar_sync(1 + par, 256);
-      const float4 vm = lds_float4((uint32_t)__cvta_generic_to_shared(st.v_most[entry]));
-      const float v_top = at_least(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), kLeastStep);
-      top = fmaxf(top, st.row_tops[par][1 - side][r]) * unit + log2_of(v_top);  // of a weight
+      top = fmaxf(top, st.row_tops[par][1 - side][r]) * unit;
+      if constexpr (!W::kBf16) {  // of a weight: a power times the value's step
+        const float4 vm = lds_float4((uint32_t)__cvta_generic_to_shared(st.v_most[entry]));
+        top += log2_of(at_least(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), kLeastStep));
+      }
       if (top > ref + kMost) {
         const float next = top - kTarget, down = exp2_of(ref - next);  // 0 from the first reference
         ref = next;
@@ -398,14 +423,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         logits(g, s, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          x[i] = fma2(x[i], both(unit), both(-ref));
+          x[i] = W::kBf16 ? add2(x[i], both(-ref)) : fma2(x[i], both(unit), both(-ref));
           x[i] = make_float2(exp2_of(x[i].x), exp2_of(x[i].y));
           more = add2(more, x[i]);
         }
-        if constexpr (W::kBf16) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], both(v_top));
-        } else {
+        if constexpr (!W::kBf16) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float4 v = lds_float4(vs + (16 * g + 4 * i) * 4);
@@ -422,10 +444,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       __syncwarp();
       if (lane == 0) {
         tc::mbar_arrive(&st.p_full[par]);
-        tc::mbar_arrive(&st.meta_empty[entry]);
+        if (!W::kBf16) tc::mbar_arrive(&st.meta_empty[entry]);
       }
       sums = add2(sums, more);
       wait(&st.o_full[par], n >> 1);
+      float2 v_unit = both(1.0f);
+      if constexpr (W::kBf16) {  // the values' power of two
+        v_unit = both(st.v_most[entry][0]);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&st.meta_empty[entry]);
+      }
       tc::tc_fence_after();
 #pragma unroll
       for (int d = 0; d < kDims; d += 16) {  // 8 or 16 dims
@@ -437,7 +465,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         tmem_loaded(o);
 #pragma unroll
         for (int i = 0; i < (d + 16 <= kDims ? 8 : 4); ++i)
-          out[d / 2 + i] = add2(out[d / 2 + i], make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])));
+          out[d / 2 + i] = W::kBf16 ? fma2(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), v_unit, out[d / 2 + i])
+                                    : add2(out[d / 2 + i], make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])));
       }
     }
     // The two groups meet in what was K's and V's place, [dim][row], 129 apart, then references and sums: each
@@ -494,106 +523,103 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     // ------------------------------------------------------- keys and values, widened
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBringRegisters));
     const int tid = threadIdx.x - 32 * kBring;
-    constexpr int kDims = 16 / W::kBytes, kTurns = kTile / W::kTurn;
-    // A thread takes the same 16 bytes of every kTurn-th token's row.
-    const int of_turn = tid / W::kLanes, chunk = tid % W::kLanes, row_bytes = D * W::kBytes;
-    const bool loads = chunk * kDims < D, stores = chunk < W::kPieces, turned = !W::kBf16 && (chunk & 4);
-    // and 128 kTurn bytes on for each turn; the second panel's pieces go in the other order, so that each
-    // eighth of a store meets every bank once
-    const uint32_t place = of_panel(of_turn, kDims * chunk) ^ (turned ? 16 : 0);
-    // bf16: the exponent that a tile's largest value is taken to have, K's and V's (the last one's): put to 2^8, so
-    // that it may be up to 2^7 more, or 2^8 less, before the tile is done again with its own
-    int taken[2] = {127, 127};
+    auto done = [&](int stage) {
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&st.stage_full[stage]);
+    };
+    if constexpr (!W::kBf16) {
+      // A thread takes the same 16 bytes of every kTurn-th token's row.
+      const int of_turn = tid / 8, chunk = tid % 8;
+      const bool loads = 16 * chunk < D, stores = chunk < W::kPieces, turned = chunk & 4;
+      // and 128 kTurn bytes on for each turn; the second panel's pieces go in the other order, so that each
+      // eighth of a store meets every bank once
+      const uint32_t place = of_panel(of_turn, 16 * chunk) ^ (turned ? 16 : 0);
 #pragma unroll 1
-    for (int i = 0; i < 2 * tiles; ++i) {
-      int operand, n;
-      at_place(i, operand, n);
-      const int entry = n % kEntries, stage = i % W::kStages, slot = i % W::kRaws;
-      const uint32_t to = stage_at + stage * W::kOperand + place, from = raw_at + slot * W::kRaw + of_turn * row_bytes + 16 * chunk;
-      wait(&st.raw_full[slot], i / W::kRaws);
-      // the tokens that are there: of a turn's 16 the page, and the first `count`
-      const uint32_t ok = alive ? st.entry_ok[entry] : 0u;
-      const int count = (int)(len - begin) - n * kTile;
-      if constexpr (!W::kBf16) {  // their steps, of the operand that comes
-        if (tid < kTile) {
-          float* steps = operand ? st.v_steps[entry] : st.k_steps[entry];
-          float step = tid < count && ((ok >> (tid >> 4)) & 1u) ? steps[tid] : 0.0f;
-          if (operand) {
+      for (int i = 0; i < 2 * tiles; ++i) {
+        int operand, n;
+        at_place(i, operand, n);
+        const int entry = n % kEntries, stage = i % W::kStages, slot = i % W::kRaws;
+        const uint32_t to = stage_at + stage * W::kOperand + place, from = raw_at + slot * W::kRaw + of_turn * D + 16 * chunk;
+        wait(&st.raw_full[slot], i / W::kRaws);
+        // the tokens that are there: of each 16 those whose page is, and the first `count`
+        const uint32_t ok = alive ? st.entry_ok[entry] : 0u;
+        const int count = (int)(len - begin) - n * kTile;
+        const bool whole = ok == 0xffu && count >= kTile;
+        if (!operand) {  // the steps of both come with the keys, so that weights need not wait for values
+          const int token = tid % kTile;
+          float* steps = tid < kTile ? st.k_steps[entry] : st.v_steps[entry];
+          float step = token < count && ((ok >> (token >> 4)) & 1u) ? steps[token] : 0.0f;
+          if (tid >= kTile) {
             const uint32_t m = __reduce_max_sync(kFullMask, __float_as_uint(step));
-            if (lane == 0) st.v_most[entry][warp - kBring] = __uint_as_float(m);
+            if (lane == 0) st.v_most[entry][warp - kBring - kTile / 32] = __uint_as_float(m);
             step = at_least(step, kLeastStep);
           }
-          steps[tid] = step;
+          steps[token] = step;
         }
-      }
-      if (i >= W::kStages) wait(&st.stage_empty[stage], i / W::kStages - 1);
-      uint32_t largest = 0;  // bf16: of the results, two halves
-      const int mine = operand ? taken[1] : taken[0];
-      const bool whole = ok == 0xffu && count >= kTile;
-      auto widen_turns = [&](float scale) {
-        largest = 0;
-        if (!stores) return;
+        if (i >= W::kStages) wait(&st.stage_empty[stage], i / W::kStages - 1);
+        if (stores) {
 #pragma unroll
-        for (int t = 0; t < kTurns; ++t) {
-          const int token = t * W::kTurn + of_turn;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (loads && (whole || (token < count && ((ok >> (token >> 4)) & 1u)))) w = lds128(from + t * W::kTurn * row_bytes);
-          uint32_t h[8];
-          if constexpr (W::kBf16) {
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 f = mul2(make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u)), both(scale));
-              const __half2 x = __floats2half2_rn(f.x, f.y);
-              h[j] = *reinterpret_cast<const uint32_t*>(&x);
-              const __half2 y = __hmax2_nan(__habs2(x), *reinterpret_cast<const __half2*>(&largest));
-              largest = *reinterpret_cast<const uint32_t*>(&y);
-            }
-          } else {
+          for (int t = 0; t < kTile / W::kTurn; ++t) {
+            const int token = t * W::kTurn + of_turn;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (loads && (whole || (token < count && ((ok >> (token >> 4)) & 1u)))) w = lds128(from + t * W::kTurn * D);
+            uint32_t h[8];
             widen<FORMAT>(turned ? w.z : w.x, h[0], h[1]);
             widen<FORMAT>(turned ? w.w : w.y, h[2], h[3]);
             widen<FORMAT>(turned ? w.x : w.z, h[4], h[5]);
             widen<FORMAT>(turned ? w.y : w.w, h[6], h[7]);
+            tc::st_shared_v4(to + t * W::kTurn * 128, h[0], h[1], h[2], h[3]);
             tc::st_shared_v4((to + t * W::kTurn * 128) ^ 16, h[4], h[5], h[6], h[7]);
           }
-          tc::st_shared_v4(to + t * W::kTurn * 128, h[0], h[1], h[2], h[3]);
         }
-      };
-      widen_turns(W::kBf16 ? power2(135 - mine) : 1.0f);
-      if constexpr (W::kBf16) {
-        auto largest_of_all = [&](uint32_t mine) {
-          mine = __reduce_max_sync(kFullMask, max(mine & 0xffffu, mine >> 16));
-          if (lane == 0) st.tops[i & 1][warp - kBring] = mine;
-          tc::named_bar_sync(4, kBringThreads);
-          return __reduce_max_sync(kFullMask, st.tops[i & 1][lane & 7]);
-        };
-        int used = mine;
-        const uint32_t m = largest_of_all(largest);  // as an fp16 value's bits
-        if (m >= 0x7c00u || m < 0x3c00u) {  // infinite or no number, or below 1: by its own exponent
-          uint32_t top = 0;
-          if (stores && loads)
-            for (int t = 0; t < kTurns; ++t) {
-              const int token = t * W::kTurn + of_turn;
-              if (token >= count || !((ok >> (token >> 4)) & 1u)) continue;
-              const uint4 w = lds128(from + t * W::kTurn * row_bytes);
-              top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-            }
-          tc::named_bar_sync(4, kBringThreads);  // the first maximum is read
-          const int e = (int)(largest_of_all(top) >> 7);
-          used = e == 0 ? mine : max(30, min(230, e));
-          if (used != mine) widen_turns(power2(135 - used));
-          (operand ? taken[1] : taken[0]) = used;
-        }
-        if (tid == 0) {
-          (operand ? st.v_most[entry] : st.k_steps[entry])[0] = power2(used - 135);
-          if (operand) st.v_most[entry][1] = st.v_most[entry][2] = st.v_most[entry][3] = 0.0f;
-        }
+        done(stage);
+        if (lane == 0) tc::mbar_arrive(&st.raw_empty[slot]);
       }
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(&st.stage_full[stage]);
-        tc::mbar_arrive(&st.raw_empty[slot]);
+    } else {
+      // bf16 values become fp16 where they are, under the power of two that puts the tile's largest to 2^14 .. 2^15
+      // (an infinity or a NaN stays what it is); those of tokens that are not there become 0.
+      constexpr int kTurns = W::kOperand / (kBringThreads * 16);
+#pragma unroll 1
+      for (int n = 0; n < tiles; ++n) {
+        const int i = place_of_v(n), entry = n % kEntries, stage = i % W::kStages;
+        // how often the place has had values before: the even ones every other tile's, the last one's odd place none
+        wait(&st.raw_full[stage], i & 1 ? 0 : n >> 1);
+        const uint32_t ok = alive ? st.entry_ok[entry] : 0u;
+        const int count = (int)(len - begin) - n * kTile;
+        const bool whole = ok == 0xffu && count >= kTile;
+        const uint32_t at = stage_at + stage * W::kOperand + 16 * tid;
+        auto counts = [&](int t) {  // whether turn t's piece of this thread is of a token that is there
+          const int token = (tid >> 3) + (t * (kBringThreads / 8)) % kTile;
+          return whole || (token < count && ((ok >> (token >> 4)) & 1u));
+        };
+        uint32_t top = 0;
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+          if (!counts(t)) continue;
+          const uint4 w = lds128(at + t * kBringThreads * 16);
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+        }
+        top = __reduce_max_sync(kFullMask, max(top & 0xffffu, top >> 16));
+        if (lane == 0) st.tops[n & 1][warp - kBring] = top;
+        tc::named_bar_sync(4, kBringThreads);
+        const int e = max(30, min(230, (int)(__reduce_max_sync(kFullMask, st.tops[n & 1][lane & 7]) >> 7)));
+        const float2 scale = both(power2(141 - e));
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (counts(t)) w = lds128(at + t * kBringThreads * 16);
+          uint32_t* u[4] = {&w.x, &w.y, &w.z, &w.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = mul2(make_float2(__uint_as_float(*u[k] << 16), __uint_as_float(*u[k] & 0xffff0000u)), scale);
+            const __half2 x = __floats2half2_rn(f.x, f.y);
+            *u[k] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          tc::st_shared_v4(at + t * kBringThreads * 16, w.x, w.y, w.z, w.w);
+        }
+        if (tid == 0) st.v_most[entry][0] = power2(e - 141);
+        done(stage);
       }
     }
   } else {
@@ -601,7 +627,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     if (warp == kIssue) {
       // ----------------------------------------------------- S = Q K^T
       if (lane == 0) {
-        const uint32_t idesc = tc::make_idesc(kRows, kTile);
+        // bf16 is format 1 of both operands, fp16 0
+        const uint32_t idesc = tc::make_idesc(kRows, kTile) | (W::kBf16 ? 1u << 7 | 1u << 10 : 0u);
         wait(&st.q_full, 0);
 #pragma unroll 1
         for (int n = 0; n < tiles; ++n) {
@@ -612,7 +639,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
             tc::tc_fence_after();
             uint32_t add = 0;
 #pragma unroll 1
-            for (int part = 1; part >= 0; --part) {
+            for (int part = W::kParts - 1; part >= 0; --part) {
 #pragma unroll
               for (int k = 0; k < DT / 16; ++k) {
                 const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
@@ -664,17 +691,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       for (int n = 0; n < tiles; ++n) {
         const int entry = n % kEntries;
         const uint32_t t = begin + n * kTile + 16 * half;
-        int64_t at = -1;
+        int64_t at = -1, row = 0;
         if (t < len) {
           const int32_t page = table[t >> c.page_shift];
-          if (page >= 0 && page < c.num_pages) at = (((int64_t)page * c.heads) << c.page_shift) + head_row + (t & ((1u << c.page_shift) - 1));
+          if (page >= 0 && page < c.num_pages) {
+            const int64_t in_page = head_row + (t & ((1u << c.page_shift) - 1)), page_row = ((int64_t)page * c.heads) << c.page_shift;
+            row = page_row + in_page;
+            at = W::kBf16 ? (int64_t)page << 32 | in_page : row;
+          }
         }
         if (n >= kEntries) wait(&st.meta_empty[entry], n / kEntries - 1);
         if (lane < 8) st.entries[entry].row[half] = at;
         const uint32_t ok = __ballot_sync(kFullMask, at >= 0) & 0xffu;
         if (lane == 0) st.entry_ok[entry] = ok;
         if (lane < 16 && at >= 0) {  // 16 tokens of a head are one run of bytes
-          const uint8_t* from = static_cast<const uint8_t*>(lane < 8 ? c.k : c.v) + at * D * W::kBytes;
+          const uint8_t* from = static_cast<const uint8_t*>(lane < 8 ? c.k : c.v) + row * D * W::kBytes;
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(16 * D * W::kBytes) : "memory");
         }
         __syncwarp();
@@ -682,32 +713,57 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       }
     } else {
       // ----------------------------------------------------- copies of the cache's rows: a lane 16 tokens, or their steps
-      const int row_bytes = D * W::kBytes, half = lane & 7;
+      const int half = lane & 7;
 #pragma unroll 1
       for (int i = 0; i < 2 * tiles; ++i) {
         int operand, n;
         at_place(i, operand, n);
-        const int entry = n % kEntries, slot = i % W::kRaws;
+        const int entry = n % kEntries, stage = i % W::kStages;
         if (!operand) wait(&st.meta_full[entry], n / kEntries);
-        if (i >= W::kRaws) wait(&st.raw_empty[slot], i / W::kRaws - 1);
         const int64_t first = st.entries[entry].row[half];
         const int rows = min(16, (int)(len - begin) - n * kTile - 16 * half);
-        const bool copies = alive && first >= 0 && rows > 0 && lane < (W::kBf16 ? 8 : 16);
-        const uint32_t bytes = lane < 8 ? rows * row_bytes : 64;
-        const uint32_t all = __reduce_add_sync(kFullMask, copies ? bytes : 0u);
-        if (lane == 0) tc::mbar_arrive_expect_tx(&st.raw_full[slot], all);
-        __syncwarp();
-        if (copies) {
-          if (lane < 8)
-            tc::bulk_copy_g2s(raw_at + slot * W::kRaw + 16 * half * row_bytes, static_cast<const uint8_t*>(operand ? c.v : c.k) + first * row_bytes, bytes, &st.raw_full[slot]);
-          else
-            tc::bulk_copy_g2s((uint32_t)__cvta_generic_to_shared(&(operand ? st.v_steps : st.k_steps)[entry][16 * half]), (operand ? c.v_step : c.k_step) + first, bytes, &st.raw_full[slot]);
+        if constexpr (W::kBf16) {
+          // by TMA into their place as an operand, a lane 16 tokens and a panel; whole boxes, of which the tokens that
+          // are not there do not count
+          if (i >= W::kStages) wait(&st.stage_empty[stage], i / W::kStages - 1);
+          unsigned long long* bar = operand ? &st.raw_full[stage] : &st.stage_full[stage];
+          const bool copies = alive && first >= 0 && rows > 0 && lane < 8 * W::kPanels;
+          const uint32_t all = __popc(__ballot_sync(kFullMask, copies)) * 2048u;
+          if (!operand && lane < kBringThreads / 32 - 1) tc::mbar_arrive(bar);  // as many arrive as where warps widen
+          if (lane == 31) tc::mbar_arrive_expect_tx(bar, all);
+          __syncwarp();
+          if (copies)
+            asm volatile(
+                "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                    stage_at + stage * W::kOperand + (lane >> 3) * kPanel + half * 2048),
+                "l"(reinterpret_cast<uint64_t>(operand ? &maps.values : &maps.keys)), "r"((lane >> 3) * 64), "r"((int)first), "r"((int)(first >> 32)),
+                "r"(tc::smem_u32(bar))
+                : "memory");
+        } else {
+          const int slot = i % W::kRaws;
+          if (i >= W::kRaws) wait(&st.raw_empty[slot], i / W::kRaws - 1);
+          const bool copies = alive && first >= 0 && rows > 0 && lane < (operand ? 8 : 24);  // rows; k's steps, v's steps
+          const uint32_t bytes = lane < 8 ? rows * D : 64;
+          const uint32_t all = __reduce_add_sync(kFullMask, copies ? bytes : 0u);
+          if (lane == 0) tc::mbar_arrive_expect_tx(&st.raw_full[slot], all);
+          __syncwarp();
+          if (copies) {
+            if (lane < 8)
+              tc::bulk_copy_g2s(raw_at + slot * W::kRaw + 16 * half * D, static_cast<const uint8_t*>(operand ? c.v : c.k) + first * D, bytes, &st.raw_full[slot]);
+            else
+              tc::bulk_copy_g2s((uint32_t)__cvta_generic_to_shared(&(lane < 16 ? st.k_steps : st.v_steps)[entry][16 * half]), (lane < 16 ? c.k_step : c.v_step) + first, bytes, &st.raw_full[slot]);
+          }
         }
         __syncwarp();
       }
-      // none of them is on its way when the CTA ends, also after a wait that has run out
-      if (lane == 0)
-        for (int i = max(0, 2 * tiles - W::kRaws); i < 2 * tiles; ++i) drain(&st.raw_full[i % W::kRaws], (i / W::kRaws) & 1, status);
+      // No copy is on its way when the CTA ends.  Each was waited for by the role that used it, but after a wait that
+      // has run out: then for a millisecond at most, long after the last one.
+      if (lane == 0 && !alive) {
+        const unsigned long long t0 = tc::global_timer();
+#pragma unroll 1
+        while (tc::global_timer() - t0 < 1000000ull) {
+        }
+      }
     }
     __syncwarp();
   }
@@ -754,7 +810,19 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, Shares sh, int64
     sh.splits = 1;
     cfg.gridDim = dim3((unsigned)rows, 1, 1);
   }
-  return cudaLaunchKernelEx(&cfg, kernel, a, c, sh, dev.status);
+  Maps maps = {};
+  if constexpr (W::kBf16) {
+    const cuuint64_t sizes[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.heads << c.page_shift, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[2] = {sizes[0] * 2, sizes[0] * sizes[1] * 2};
+    const cuuint32_t box[3] = {64, 16, 1}, each[3] = {1, 1, 1};
+    const EncodeTiledFn encode = encode_fn();
+    for (int i = 0; i < 2; ++i)
+      if (!encode || encode(i ? &maps.values : &maps.keys, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, i ? c.v : c.k, sizes, strides, box, each,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorUnknown;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, a, c, sh, maps, dev.status);
 }
 
 }  // namespace

@@ -50,6 +50,7 @@
 
 #include "common.cuh"
 #include "tc_util.cuh"
+#include "tensor_map.cuh"
 
 namespace bitlinear {
 namespace {
@@ -734,22 +735,6 @@ cudaError_t launch_split(PrefillParams& p, bool pdl, const DeviceInfo& dev, cuda
   p.KB = KB / best_s;
   p.num_tiles = (int)(tiles * best_s);
   return launch_impl<SWAP, BIG>(p, pdl, dev, stream);
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  }
-  return fn;
 }
 
 PrefillParams common_params(const int8_t* xq, const float* sx, int64_t M, const DecodeMatrix* mats, int nmats,
