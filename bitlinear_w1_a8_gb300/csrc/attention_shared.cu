@@ -132,9 +132,25 @@ size_t attention_shared_workspace_bytes(int64_t B, int q_heads, int kv_heads, in
   return need > alone ? need : alone;
 }
 
+// Whether attention that reads a group's tokens again for each of its rows is faster: it is one launch, the second
+// reading is of L2, and few rows do not fill the GPU either way.  By the bytes that all rows read at most, the
+// table's columns filled; us, shared against alone, of 32 heads of 80 dims in int8 and 8 of 128 in bf16 under 32 q heads:
+//   int8   rows  4 x 2048 tokens (42 MB) 13.8 / 11.8   4 x 4096 (84 MB) 15.8 / 18.8    8 x 1024 (42 MB) 13.4 / 11.7   16 x 1024 (84 MB) 14.9 / 17.6
+//   (wide)      32 x  512 (84 MB)        22.2 / 17.9  32 x 1024 (168 MB) 24.5 / 29.9  64 x  256 (84 MB) 21.7 / 21.7
+//   bf16 (wide)  8 x 4096 (134 MB)       22.8 / 20.8  16 x 2048 (134 MB) 22.1 / 21.0  32 x 1024 (134 MB) 22.0 / 20.0  64 x 1024 (268 MB) 28.2 / 37.6
+// and of 2 rows of 38 tokens, 16 heads of 128 dims: 8.7 / 3.2.
+constexpr double kAloneBytes = 56e6, kAloneBytesWide = 112e6;
+bool faster_alone(const AttendArgs& a, const KvPages& c, bool wide) {
+  const double code = c.format == BITLINEAR_KV_BF16 ? 2 : 1;
+  const double bytes = (double)a.B * (double)a.max_pages * (double)(1 << c.page_shift) * c.heads * c.head_dim * 2 * code;
+  return bytes <= (wide ? kAloneBytesWide : kAloneBytes);
+}
+
 cudaError_t launch_attention_shared(const AttendArgs& a, const KvPages& cache, const int32_t* shared, int64_t groups,
                                     void* workspace, bool pdl, const DeviceInfo& dev, cudaStream_t stream) {
-  if (groups == a.B) return launch_attention(a, cache, workspace, pdl, dev, stream);  // nothing is shared
+  // Nothing is shared, or too little.
+  if (groups == a.B || faster_alone(a, cache, sizes_of(a.B, a.q_heads, cache.heads, cache.head_dim, groups).wide))
+    return launch_attention(a, cache, workspace, pdl, dev, stream);
   return of_shape(cache, [&](auto format, auto dims) {
     return launch_shape<decltype(format)::value, decltype(dims)::value>(a, cache, shared, groups, workspace, pdl, dev, stream);
   });

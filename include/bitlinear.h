@@ -538,7 +538,7 @@ size_t bitlinear_attention_shared_workspace(int64_t B, int num_q_heads, int num_
  * system prompt or a document behind which each row has tokens of its own, or a sequence
  * that several drafted tokens go on from.  Rows b of group g are g * R .. (g + 1) * R - 1, R =
  * B / num_groups; the first shared[g] tokens of their sequences are read, and multiplied, once for
- * all of them.
+ * all of them (over a page table of few columns they are attended to row by row, where that is faster).
  *   page_table, lengths  as for bitlinear_attention: each row's own table and whole length,
  *              shared tokens included.  The tables of a group's rows name the same pages for its
  *              shared tokens; where they do not, which row's are read is unspecified.

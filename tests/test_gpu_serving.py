@@ -64,18 +64,29 @@ def shared_case(fmt, groups, R, Hq, Hkv, D, shared, lengths, page, seed, one_lis
     return cache, q, table
 
 
+def wide_table(table, cache):
+    """The table with columns that no length reaches, as many as make the call share: over few columns it attends row by row."""
+    pages, heads, page, D = cache[0].shape
+    a_column = len(table) * page * heads * D * 2 * cache[0].element_size()
+    wide = np.full((len(table), max(table.shape[1], 120_000_000 // a_column)), -1)
+    wide[:, :table.shape[1]] = table
+    return ints(wide)
+
+
 def run_shared(fmt, groups, R, Hq, Hkv, D, shared, lengths, page=32, seed=0, one_list=False, scale=None, spare=0, flags=0):
     cache, q, table = shared_case(fmt, groups, R, Hq, Hkv, D, shared, lengths, page, seed, one_list, spare)
     out, full = guarded(q.numel(), torch.float32, 7.5)
     out = out.view(q.shape)
     need = bl.bitlinear_attention_shared_workspace(groups * R, Hq, Hkv, D, groups)
     ws, ws_full = guarded(max(need, 16), torch.uint8, 0x5a)
-    bl.bitlinear_attention_shared(q.cuda(), cache, ints(table), ints(lengths), ints(shared), out, ws, scale=scale, flags=flags)
-    torch.cuda.synchronize()
     want, bound = attention_plain.attend(q.numpy(), cache, table, lengths, page, D ** -0.5 if scale is None else scale)
-    within(out, want, bound)
-    check_canary(full, 7.5)
-    check_canary(ws_full, 0x5a)
+    for columns in (ints(table), wide_table(table, cache)):
+        out.fill_(float("nan"))
+        bl.bitlinear_attention_shared(q.cuda(), cache, columns, ints(lengths), ints(shared), out, ws, scale=scale, flags=flags)
+        torch.cuda.synchronize()
+        within(out, want, bound)
+        check_canary(full, 7.5)
+        check_canary(ws_full, 0x5a)
     return out, (cache, q, table)
 
 
@@ -128,7 +139,7 @@ def test_shared_borders(R, G):
         attention_plain.fill_row(cache, "int8", torch.tensor(table[b, t // page].astype(np.int64), device="cuda"), torch.tensor(t % page, device="cuda"), *x)
     out = torch.full(q.shape, 3.0, device="cuda")
     ws = torch.empty(bl.bitlinear_attention_shared_workspace(5 * R, 2 * G, 2, 64, 5), dtype=torch.uint8, device="cuda")
-    bl.bitlinear_attention_shared(q.cuda(), cache, ints(table), ints(lengths), ints(shared), out, ws)
+    bl.bitlinear_attention_shared(q.cuda(), cache, wide_table(table, cache), ints(lengths), ints(shared), out, ws)
     want, bound = attention_plain.attend(q.numpy(), cache, table, lengths, page, 64 ** -0.5)
     within(out, want, bound)
     assert (out[lengths <= 0] == 0).all()
@@ -145,7 +156,7 @@ def test_shared_pages_out_of_range(R, G):
     out = torch.empty(q.shape, device="cuda")
     ws = torch.empty(bl.bitlinear_attention_shared_workspace(R, 2 * G, 2, 80, 1), dtype=torch.uint8, device="cuda")
     table[1, 6] = table[0, 6]
-    bl.bitlinear_attention_shared(q.cuda(), cache, ints(table), ints(lengths), ints([S]), out, ws)
+    bl.bitlinear_attention_shared(q.cuda(), cache, wide_table(table, cache), ints(lengths), ints([S]), out, ws)
     want, bound = attention_plain.attend(q.numpy(), cache, table, lengths, page, 80 ** -0.5)
     within(out, want, bound)
 
@@ -157,11 +168,12 @@ def test_shared_strides_scales_and_agreement():
     cache, q, table = shared_case("fp8", 1, R, Hq, Hkv, D, [S], lengths, page, 21)
     wide_q, wide_out = torch.full((R, 3, Hq, D), float("nan"), device="cuda"), torch.full((R, 2, Hq, D), 4.0, device="cuda")
     wide_q[:, 1] = q.cuda()
-    wide_table = torch.full((R, table.shape[1] + 5), -1, dtype=torch.int32, device="cuda")
-    wide_table[:, :table.shape[1]] = ints(table)
+    columns = wide_table(table, cache)
+    padded = torch.full((R, columns.shape[1] + 5), -1, dtype=torch.int32, device="cuda")
+    padded[:, :table.shape[1]] = ints(table)
     ws = torch.empty(bl.bitlinear_attention_shared_workspace(R, Hq, Hkv, D, 1), dtype=torch.uint8, device="cuda")
     for scale in (0.3, -0.2, 0.0):
-        bl.bitlinear_attention_shared(wide_q[:, 1], cache, wide_table[:, :table.shape[1]], ints(lengths), ints([S]), wide_out[:, 1], ws, scale=scale)
+        bl.bitlinear_attention_shared(wide_q[:, 1], cache, padded[:, :columns.shape[1]], ints(lengths), ints([S]), wide_out[:, 1], ws, scale=scale)
         want, bound = attention_plain.attend(q.numpy(), cache, table, lengths, page, scale)
         within(wide_out[:, 1], want, bound)
         assert (wide_out[:, 0] == 4.0).all()
@@ -170,7 +182,7 @@ def test_shared_strides_scales_and_agreement():
     bl.bitlinear_attention(q.cuda(), cache, ints(table), ints(lengths), plain_out)
     assert torch.equal(alone, plain_out)
     one = torch.empty(R, Hq, D, device="cuda")  # a table of stride 0: every row one list
-    bl.bitlinear_attention_shared(q.cuda(), cache, ints(table[:1]).expand(R, -1), ints(np.full(R, 120)), ints([120]), one, ws)
+    bl.bitlinear_attention_shared(q.cuda(), cache, wide_table(table, cache)[:1].expand(R, -1), ints(np.full(R, 120)), ints([120]), one, ws)
     want, bound = attention_plain.attend(q.numpy(), cache, np.repeat(table[:1], R, 0), np.full(R, 120), page, D ** -0.5)
     within(one, want, bound)
 
@@ -182,7 +194,7 @@ def test_shared_values_that_are_not_finite(R, G):
     lengths = S + 1 + np.arange(R) % 11
     cache, q, table = shared_case("bf16", 1, R, 2 * G, 2, D, [S], lengths, page, 31)
     ws = torch.empty(bl.bitlinear_attention_shared_workspace(R, 2 * G, 2, D, 1), dtype=torch.uint8, device="cuda")
-    run = lambda: (bl.bitlinear_attention_shared(q.cuda(), cache, ints(table), ints(lengths), ints([S]), out, ws), out.cpu())[1]  # noqa: E731
+    run = lambda: (bl.bitlinear_attention_shared(q.cuda(), cache, wide_table(table, cache), ints(lengths), ints([S]), out, ws), out.cpu())[1]  # noqa: E731
     out = torch.empty(q.shape, device="cuda")
     clean = run()
     assert torch.isfinite(clean).all()
@@ -211,7 +223,7 @@ def test_shared_replayed_and_on_other_streams(R, Hq, Hkv, D, S):
     lengths = S + 1 + np.arange(R) % 90
     cache, q, table = shared_case("int8", 1, R, Hq, Hkv, D, [S], lengths, page, 41)
     ws = torch.empty(bl.bitlinear_attention_shared_workspace(R, Hq, Hkv, D, 1), dtype=torch.uint8, device="cuda")
-    q, table = q.cuda(), ints(table)
+    q, table = q.cuda(), wide_table(table, cache)
     shared, n = ints([S]), ints(lengths)
     first, second, replayed = (torch.empty(q.shape, device="cuda") for _ in range(3))
     half, n_half = ints([S // 2]), ints(np.full(R, S // 2))
