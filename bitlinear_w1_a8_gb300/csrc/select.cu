@@ -15,6 +15,8 @@
 // page has a larger product with those codes.  A key head's score is the largest of its q heads'.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "serve.cuh"
 
 namespace bitlinear {
@@ -26,29 +28,49 @@ constexpr float kLeastTop = 1e-5f;
 
 constexpr int kSumThreads = 128;
 constexpr int kSumWarps = kSumThreads / 32;
+constexpr int kSumCtas = 8;  // of an SM
+constexpr int kDims = 8;    // of a thread
+constexpr int kTurns = 4;   // rows that a thread has on their way together
 
-// 16 bytes of a row of codes as fp32 values, times the row's step.
+// Eight codes as fp32 values times their row's step: 8 bytes of int8 or e4m3, 16 of bf16 (no step).
 template <int FORMAT>
-__device__ __forceinline__ void widen16(uint4 w, float step, float (&x)[FORMAT == BITLINEAR_KV_BF16 ? 8 : 16]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+using Codes = std::conditional_t<FORMAT == BITLINEAR_KV_BF16, uint4, uint2>;
+template <int FORMAT>
+__device__ __forceinline__ void widen(Codes<FORMAT> w, float step, float (&x)[kDims]) {
+  if constexpr (FORMAT == BITLINEAR_KV_BF16) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (FORMAT == BITLINEAR_KV_BF16) {
+    for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(u[i] << 16);
       x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    } else if constexpr (FORMAT == BITLINEAR_KV_INT8) {
+    }
+  } else if constexpr (FORMAT == BITLINEAR_KV_INT8) {
+    // code + 128 in the mantissa of 2^23: exact, and not on the unit that converts (a quarter of the rate)
+    const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[4 * i + j] = __fmul_rn((float)((int)(u[i] << (24 - 8 * j)) >> 24), step);
-    } else {
+    for (int i = 0; i < kDims; ++i)
+      x[i] = __fmul_rn(__uint_as_float(__byte_perm(u[i / 4], 0x4b000000u, 0x7650 | i % 4)) - 8388736.0f, step);
+  } else {
+    const uint32_t u[2] = {w.x, w.y};
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t h = half2_of_e4m3x2((uint16_t)(u[i] >> (16 * j)));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        x[4 * i + 2 * j] = __fmul_rn(f.x, step);
-        x[4 * i + 2 * j + 1] = __fmul_rn(f.y, step);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = half2_of_e4m3x2((uint16_t)(u[i / 2] >> (16 * (i % 2))));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      x[2 * i] = __fmul_rn(f.x, step);
+      x[2 * i + 1] = __fmul_rn(f.y, step);
     }
   }
+}
+
+__device__ __forceinline__ float least_of(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float most_of(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 struct SummariseArgs {
@@ -56,33 +78,35 @@ struct SummariseArgs {
   Summary summary;
   const int32_t *table, *first, *lengths;
   int64_t table_stride, max_pages;
-  int shares;  // warps a key head of a sequence, each every shares-th of its pages
+  int shares;  // CTAs a key head of a sequence, each every shares-th of its pages
 };
 
-// A warp takes a page of a head: a lane 16 bytes of a row, as many rows a turn as fit.
+// A CTA takes a page of a head, a thread eight dims of every few rows, eight rows on their way at once.
 template <int FORMAT>
-__global__ void __launch_bounds__(kSumThreads) summarise_kernel(SummariseArgs a) {
-  constexpr int kDims = FORMAT == BITLINEAR_KV_BF16 ? 8 : 16;  // of a lane
+__global__ void __launch_bounds__(kSumThreads, kSumCtas) summarise_kernel(SummariseArgs a) {
   constexpr int kBytes = FORMAT == BITLINEAR_KV_BF16 ? 2 : 1;
+  __shared__ __align__(16) float least[kSumThreads * kDims], most[kSumThreads * kDims];
+  __shared__ uint32_t tops[kSumWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_release_dependents();
   pdl_wait_primary();
   const KvPages& c = a.c;
-  const uint32_t part = blockIdx.x * kSumWarps + warp;  // of the key head
   const int hk = blockIdx.y;
   const int64_t b = blockIdx.z;
-  if (part >= (uint32_t)a.shares) return;
-  const int D = c.head_dim, chunks = D / kDims, rows = 32 / chunks;  // rows a turn, 1 at least
-  const int row = lane / chunks, chunk = lane - row * chunks;
+  const int D = c.head_dim, chunks = D / kDims, rows = kSumThreads / chunks;  // rows a turn, 4 at least
+  const int row = threadIdx.x / chunks, chunk = threadIdx.x - row * chunks;
   const int page_size = 1 << c.page_shift;
   const int64_t length = max((int64_t)0, min((int64_t)a.lengths[b], a.max_pages << c.page_shift));
-  const int64_t begin = max(0, a.first[b]) >> c.page_shift, end = (length + page_size - 1) >> c.page_shift;
-  for (int64_t column = begin + part; column < end; column += a.shares) {
-    const int32_t page = a.table[b * a.table_stride + column];
+  const int begin = (max(0, a.first[b]) >> c.page_shift) + blockIdx.x, end = (int)((length + page_size - 1) >> c.page_shift);
+  const int32_t* table = a.table + b * a.table_stride;
+  int32_t next = begin < end ? table[begin] : -1;
+  for (int column = begin; column < end; column += a.shares) {
+    const int32_t page = next;
+    if (column + a.shares < end) next = table[column + a.shares];
     if (page < 0 || page >= c.num_pages) continue;
-    const int here = (int)min((int64_t)page_size, length - (column << c.page_shift));
+    const int here = (int)min((int64_t)page_size, length - ((int64_t)column << c.page_shift));
     const int64_t head = (int64_t)page * c.heads + hk, first_row = head << c.page_shift;
-    const uint8_t* k = static_cast<const uint8_t*>(c.k) + first_row * D * kBytes + 16 * chunk;
+    const uint8_t* k = static_cast<const uint8_t*>(c.k) + (first_row * D + kDims * chunk) * kBytes;
     const float* steps = FORMAT == BITLINEAR_KV_BF16 ? nullptr : c.k_step + first_row;
     float lo[kDims], hi[kDims];
 #pragma unroll
@@ -90,49 +114,67 @@ __global__ void __launch_bounds__(kSumThreads) summarise_kernel(SummariseArgs a)
       lo[i] = INFINITY;
       hi[i] = -INFINITY;
     }
-    if (row < rows) {
-#pragma unroll 8
-      for (int t = row; t < here; t += rows) {
-        float x[kDims];
-        widen16<FORMAT>(__ldg(reinterpret_cast<const uint4*>(k + (int64_t)t * D * kBytes)), FORMAT == BITLINEAR_KV_BF16 ? 1.0f : __ldg(steps + t), x);
+    for (int t0 = row; t0 < here; t0 += kTurns * rows) {
+      Codes<FORMAT> w[kTurns];
+      float step[kTurns];
+#pragma unroll
+      for (int n = 0; n < kTurns; ++n) {  // past the last token: that token again
+        const int t = min(t0 + n * rows, here - 1);
+        w[n] = __ldg(reinterpret_cast<const Codes<FORMAT>*>(k + t * D * kBytes));
+        step[n] = FORMAT == BITLINEAR_KV_BF16 ? 1.0f : __ldg(steps + t);
+      }
+#pragma unroll
+      for (int n = 0; n < kTurns; n += 2) {
+        if (t0 - row + n * rows >= here) break;  // for all threads alike
+        float x[kDims], y[kDims];
+        widen<FORMAT>(w[n], step[n], x);
+        widen<FORMAT>(w[n + 1], step[n + 1], y);
 #pragma unroll
         for (int i = 0; i < kDims; ++i) {
-          lo[i] = fminf(lo[i], x[i]);
-          hi[i] = fmaxf(hi[i], x[i]);
+          lo[i] = least_of(lo[i], x[i], y[i]);
+          hi[i] = most_of(hi[i], x[i], y[i]);
         }
       }
     }
-    // the rows of a turn meet in the first row's lanes
-    for (int r = 1; r < rows; ++r) {
+    __syncthreads();  // the last page's are read
+    if (row < rows) {
 #pragma unroll
-      for (int i = 0; i < kDims; ++i) {
-        lo[i] = fminf(lo[i], __shfl_sync(kFullMask, lo[i], (chunk + r * chunks) & 31));
-        hi[i] = fmaxf(hi[i], __shfl_sync(kFullMask, hi[i], (chunk + r * chunks) & 31));
+      for (int i = 0; i < kDims; i += 4) {
+        *reinterpret_cast<float4*>(&least[row * D + kDims * chunk + i]) = make_float4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
+        *reinterpret_cast<float4*>(&most[row * D + kDims * chunk + i]) = make_float4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
       }
     }
-    float top = kLeastTop;
+    __syncthreads();
+    // a dim or two a thread
+    const int taken = min(rows, here);
+    float dim_lo[2], dim_hi[2], top = kLeastTop;
 #pragma unroll
-    for (int i = 0; i < kDims; ++i) top = row == 0 ? fmaxf(top, fmaxf(fabsf(lo[i]), fabsf(hi[i]))) : top;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+    for (int i = 0; i < 2; ++i) {
+      const int d = threadIdx.x + i * kSumThreads;
+      if (d >= D) break;
+      dim_lo[i] = least[d];
+      dim_hi[i] = most[d];
+#pragma unroll 4
+      for (int r = 1; r < taken; ++r) {
+        dim_lo[i] = fminf(dim_lo[i], least[r * D + d]);
+        dim_hi[i] = fmaxf(dim_hi[i], most[r * D + d]);
+      }
+      top = fmaxf(top, fmaxf(fabsf(dim_lo[i]), fabsf(dim_hi[i])));
+    }
+    const uint32_t warp_top = __reduce_max_sync(kFullMask, __float_as_uint(top));  // above 0: ordered as their bits
+    if (lane == 0) tops[warp] = warp_top;
+    __syncthreads();
+    top = __uint_as_float(__reduce_max_sync(kFullMask, tops[lane & (kSumWarps - 1)]));
     const float s = __fdiv_rn(127.0f, top);
-    if (row == 0) {
-      int8_t lower[kDims], upper[kDims];
+    int8_t* to = a.summary.bounds + head * 2 * D;
 #pragma unroll
-      for (int i = 0; i < kDims; ++i) {
-        lower[i] = (int8_t)(int)fmaxf(floorf(__fmul_rn(lo[i], s)), -127.0f);
-        upper[i] = (int8_t)(int)fminf(ceilf(__fmul_rn(hi[i], s)), 127.0f);
-      }
-      int8_t* to = a.summary.bounds + head * 2 * D + kDims * chunk;
-      if constexpr (kDims == 16) {
-        *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(lower);
-        *reinterpret_cast<uint4*>(to + D) = *reinterpret_cast<const uint4*>(upper);
-      } else {
-        *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(lower);
-        *reinterpret_cast<uint2*>(to + D) = *reinterpret_cast<const uint2*>(upper);
-      }
-      if (chunk == 0) a.summary.step[head] = __fdiv_rn(top, 127.0f);
+    for (int i = 0; i < 2; ++i) {
+      const int d = threadIdx.x + i * kSumThreads;
+      if (d >= D) break;
+      to[d] = (int8_t)(int)fmaxf(floorf(__fmul_rn(dim_lo[i], s)), -127.0f);
+      to[D + d] = (int8_t)(int)fminf(ceilf(__fmul_rn(dim_hi[i], s)), 127.0f);
     }
+    if (threadIdx.x == 0) a.summary.step[head] = __fdiv_rn(top, 127.0f);
   }
 }
 
@@ -516,10 +558,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, KvPages 
 cudaError_t launch_summarise(const KvPages& cache, const Summary& summary, const int32_t* table, int64_t table_stride,
                              int64_t B, int64_t max_pages, const int32_t* first, const int32_t* lengths, bool pdl,
                              const DeviceInfo& dev, cudaStream_t stream) {
-  // Warps in all: the GPU full once, a page a warp at least.
-  const int64_t most = (int64_t)dev.num_sms * 32, heads = B * cache.heads;
-  int64_t shares = (most + heads - 1) / heads;
-  if (shares > max_pages) shares = max_pages;
+  // As many CTAs as are resident together, in equal rounds of pages.
+  const int64_t resident = (int64_t)dev.num_sms * kSumCtas, heads = B * cache.heads;
+  const int64_t rounds = (max_pages * heads + resident - 1) / resident, shares = (max_pages + rounds - 1) / rounds;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
@@ -536,7 +577,7 @@ cudaError_t launch_summarise(const KvPages& cache, const Summary& summary, const
   constexpr int64_t kMostSeqs = 65535;
   for (int64_t b = 0; b < B; b += kMostSeqs) {
     const SummariseArgs a = {cache, summary, table + b * table_stride, first + b, lengths + b, table_stride, max_pages, (int)shares};
-    cfg.gridDim = dim3((unsigned)((shares + kSumWarps - 1) / kSumWarps), (unsigned)cache.heads, (unsigned)(B - b < kMostSeqs ? B - b : kMostSeqs));
+    cfg.gridDim = dim3((unsigned)shares, (unsigned)cache.heads, (unsigned)(B - b < kMostSeqs ? B - b : kMostSeqs));
     const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
     if (err != cudaSuccess) return err;
   }
