@@ -25,7 +25,6 @@ constexpr int kPortableCluster = 8;
 constexpr int kSms = 152;
 constexpr int kOtherSmem = 1024 + 640;  // of a CTA, beside the dynamic: the system's and the static arrays
 constexpr int kLeastSteps = 2;    // steps a warp at least: short rows take fewer CTAs
-constexpr int kWarpSteps = 4;     // kPacked: steps a warp at most, while a row has fewer than four warps
 constexpr int kShareSeqs = 1024;  // sequences that a CTA adds up to find its row
 constexpr int kSortSeqs = kThreads;  // sequences that a CTA ranks by length
 constexpr float kLimit = 256.0f;  // the largest weight before the reference moves
@@ -101,6 +100,10 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return v;
+}
+__device__ __forceinline__ float4 lds_float4(uint32_t a) {
+  const uint4 w = lds128(a);
+  return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
 }
 __device__ __forceinline__ float2 lds_float2(uint32_t a) {
   float2 v;
@@ -363,6 +366,8 @@ struct Shares {
   int prefix_tiles;  // rows a key head of a group, of
   int prefix_heads;  // so many q heads, and
   int slot_heads;    // their places in a part
+  // kPacked: warps a row at least, and steps a warp at most while the row has fewer than four
+  int least_warps, warp_steps;
 };
 
 // Tokens first <= t < len of a sequence that count, in steps of T from first / T on.
@@ -433,7 +438,7 @@ __device__ __forceinline__ Pack find_pack(const AttendArgs& a, const Shares& sh,
     Span<T> span(a.lengths[b], most, 0);
     span.first = min(span.len, (uint32_t)max(0, sh.shared[b / sh.group_rows]));
     const int steps = span.steps();
-    return steps <= kWarpSteps ? 1 : steps <= 2 * kWarpSteps ? 2 : 4;
+    return max(sh.least_warps, steps <= sh.warp_steps ? 1 : steps <= 2 * sh.warp_steps ? 2 : 4);
   };
   auto ctas_of = [&](int b) { return (sh.rows_a_seq * warps_of(b) + kWarps - 1) / kWarps; };
   int ctas = 0;
@@ -477,79 +482,137 @@ __device__ __forceinline__ int64_t by_length(const AttendArgs& a, int at) {
   return found;
 }
 
-// kOwn, kPacked: adds the parts `first`, `first` + `every`, ... of what the sequence's group shares to a warp's own
-// partials, in shared memory at `at`.  A lane takes 4 dims of a head; four parts are on their way together.
-template <int PARTIAL, int DT>
-__device__ __forceinline__ void add_prefix(const AttendArgs& a, const KvPages& c, const Shares& sh, int64_t b, int hk,
-                                           int first_head, int heads, int first, int every, uint32_t at, int lane) {
+// A head's sums of a lane's dims 4 lane .. 4 lane + 3 (and 128 more), under reference m.
+template <int DT>
+struct HeadSums {
+  static constexpr int kTurns = (DT + 127) / 128;
+  float4 v[kTurns];
+  float m, sum;
+};
+// Adds the parts `first`, `first` + `every`, ... below `end` of a head, the first of which lies at p and the next ones
+// `apart` floats on.  Parts on their way together: 8, or 4 of 256 dims.
+template <int DT>
+__device__ __forceinline__ void add_parts(HeadSums<DT>& t, const float* p, int64_t apart, int first, int every, int end, int D, int lane) {
+  constexpr int kTurns = HeadSums<DT>::kTurns, kTogether = 8 / kTurns;
+  for (int i = first; i < end; i += kTogether * every) {
+    float2 s[kTogether];
+    float4 x[kTogether][kTurns];
+    float top = t.m;
+#pragma unroll
+    for (int n = 0; n < kTogether; ++n) {
+      const bool have = i + n * every < end;
+      const float* q = p + (i + n * every) * apart;
+      s[n] = have ? *reinterpret_cast<const float2*>(q + D) : make_float2(kUnset, 0.0f);
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k) {
+        const int d = 4 * lane + 128 * k;
+        x[n][k] = have && d < D ? *reinterpret_cast<const float4*>(q + d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      top = fmaxf(top, s[n].x);
+    }
+    const float down = exp2_of(t.m - top);
+    t.m = top;
+    t.sum *= down;
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) t.v[k] = make_float4(t.v[k].x * down, t.v[k].y * down, t.v[k].z * down, t.v[k].w * down);
+#pragma unroll
+    for (int n = 0; n < kTogether; ++n) {
+      const float f = exp2_of(s[n].x - top);
+      t.sum = fmaf(s[n].y, f, t.sum);
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k) {
+        t.v[k].x = fmaf(x[n][k].x, f, t.v[k].x);
+        t.v[k].y = fmaf(x[n][k].y, f, t.v[k].y);
+        t.v[k].z = fmaf(x[n][k].z, f, t.v[k].z);
+        t.v[k].w = fmaf(x[n][k].w, f, t.v[k].w);
+      }
+    }
+  }
+}
+
+// kOwn, kPacked: where the parts of what the sequence's group shares lie, of q head `lane` of the row's: the first
+// part's floats and how many there are.
+struct HeadParts {
+  int64_t at;
+  int n;
+};
+__device__ __forceinline__ HeadParts parts_of(const KvPages& c, const Shares& sh, int64_t b, int hk, int first_head, int heads, int lane) {
   const int64_t g = b / sh.group_rows;
-  const int member = (int)(b - g * sh.group_rows), D = c.head_dim;
-  if (sh.shared[g] <= 0) return;  // then no CTA had the group's rows
-  const int rows = sh.slot_heads;
+  if (lane >= heads || sh.shared[g] <= 0) return {0, 0};  // nothing shared: no CTA had the group's rows
+  const int of_group = (int)(b - g * sh.group_rows) * sh.heads_a_key + first_head + lane, tile = of_group / sh.prefix_heads;
+  const int2 row = sh.rows[(g * c.heads + hk) * sh.prefix_tiles + tile];
+  return {((int64_t)row.x * sh.slot_heads + of_group - tile * sh.prefix_heads) * (c.head_dim + 4), row.y};
+}
+
+// kOwn: adds the parts `first`, `first` + `every`, ... to a warp's own partials at `at`.
+template <int PARTIAL, int DT>
+__device__ __forceinline__ void add_prefix(const KvPages& c, const Shares& sh, const HeadParts& of, int heads, int first, int every,
+                                           uint32_t at, int lane) {
+  const int D = c.head_dim;
   for (int h = 0; h < heads; ++h) {
-    const int of_group = member * sh.heads_a_key + first_head + h;
-    const int tile = of_group / sh.prefix_heads;
-    const int2 row = sh.rows[(g * c.heads + hk) * sh.prefix_tiles + tile];
-    const float* p = sh.parts + ((int64_t)row.x * rows + of_group - tile * sh.prefix_heads) * (D + 4);
+    const int64_t p = __shfl_sync(kFullMask, of.at, h);
+    const int n = __shfl_sync(kFullMask, of.n, h);
     const uint32_t mine = at + h * PARTIAL;
-    constexpr int kTurns = (DT + 127) / 128;  // of 4 dims a lane
+    HeadSums<DT> t;
     const float2 own = lds_float2(mine + 4 * DT);
-    float m = own.x, sum = own.y;
-    float4 v[kTurns];
+    t.m = own.x;
+    t.sum = own.y;
 #pragma unroll
-    for (int k = 0; k < kTurns; ++k) {
+    for (int k = 0; k < t.kTurns; ++k) {
       const int d = 4 * lane + 128 * k;
-      v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (d < D) {
-        const uint4 w = lds128(mine + 4 * d);
-        v[k] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
-      }
+      t.v[k] = d < D ? lds_float4(mine + 4 * d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    constexpr int kTogether = 4;
-    for (int i = first; i < row.y; i += kTogether * every) {
-      float2 s[kTogether];
-      float4 x[kTogether][kTurns];
-      float top = m;
-#pragma unroll
-      for (int n = 0; n < kTogether; ++n) {
-        const bool have = i + n * every < row.y;
-        const float* q = p + (int64_t)(i + n * every) * rows * (D + 4);
-        s[n] = have ? *reinterpret_cast<const float2*>(q + D) : make_float2(kUnset, 0.0f);
-#pragma unroll
-        for (int k = 0; k < kTurns; ++k) {
-          const int d = 4 * lane + 128 * k;
-          x[n][k] = have && d < D ? *reinterpret_cast<const float4*>(q + d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-        top = fmaxf(top, s[n].x);
-      }
-      const float down = exp2_of(m - top);
-      m = top;
-      sum *= down;
-#pragma unroll
-      for (int k = 0; k < kTurns; ++k) v[k] = make_float4(v[k].x * down, v[k].y * down, v[k].z * down, v[k].w * down);
-#pragma unroll
-      for (int n = 0; n < kTogether; ++n) {
-        const float f = exp2_of(s[n].x - m);
-        sum = fmaf(s[n].y, f, sum);
-#pragma unroll
-        for (int k = 0; k < kTurns; ++k) {
-          v[k].x = fmaf(x[n][k].x, f, v[k].x);
-          v[k].y = fmaf(x[n][k].y, f, v[k].y);
-          v[k].z = fmaf(x[n][k].z, f, v[k].z);
-          v[k].w = fmaf(x[n][k].w, f, v[k].w);
-        }
-      }
-    }
+    add_parts<DT>(t, sh.parts + p, (int64_t)sh.slot_heads * (D + 4), first, every, n, D, lane);
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < kTurns; ++k) {
+    for (int k = 0; k < t.kTurns; ++k) {
       const int d = 4 * lane + 128 * k;
       if (d < D)
-        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + 4 * d), "f"(v[k].x), "f"(v[k].y), "f"(v[k].z), "f"(v[k].w) : "memory");
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + 4 * d), "f"(t.v[k].x), "f"(t.v[k].y), "f"(t.v[k].z), "f"(t.v[k].w) : "memory");
     }
     if (lane == 0) {
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + 4 * DT), "f"(m) : "memory");
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + 4 * DT + 4), "f"(sum) : "memory");
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + 4 * DT), "f"(t.m) : "memory");
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + 4 * DT + 4), "f"(t.sum) : "memory");
+    }
+  }
+}
+
+// kPacked: a row's output.  A head is a warp's: its parts, then the own partials of the row's warps, at `at` and
+// `apart` bytes on.
+template <int PARTIAL, int DT>
+__device__ __forceinline__ void finish_packed(const KvPages& c, const Shares& sh, const HeadParts& of, int heads, int me, int warps,
+                                              uint32_t at, int apart, float* out, int lane) {
+  const int D = c.head_dim;
+  for (int h = me; h < heads; h += warps) {
+    HeadSums<DT> t;
+    t.m = kUnset;
+    t.sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < t.kTurns; ++k) t.v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    add_parts<DT>(t, sh.parts + __shfl_sync(kFullMask, of.at, h), (int64_t)sh.slot_heads * (D + 4), 0, 1, __shfl_sync(kFullMask, of.n, h), D, lane);
+    for (int w = 0; w < warps; ++w) {
+      const uint32_t own = at + w * apart + h * PARTIAL;
+      const float2 s = lds_float2(own + 4 * DT);
+      const float top = fmaxf(t.m, s.x), down = exp2_of(t.m - top), f = exp2_of(s.x - top);
+      t.m = top;
+      t.sum = fmaf(s.y, f, t.sum * down);
+#pragma unroll
+      for (int k = 0; k < t.kTurns; ++k) {
+        const int d = 4 * lane + 128 * k;
+        const float4 x = d < D ? lds_float4(own + 4 * d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        t.v[k] = make_float4(fmaf(x.x, f, t.v[k].x * down), fmaf(x.y, f, t.v[k].y * down), fmaf(x.z, f, t.v[k].z * down), fmaf(x.w, f, t.v[k].w * down));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < t.kTurns; ++k) {
+      const int d = 4 * lane + 128 * k;
+      if (d < D) {
+        float* to = out + h * D + d;
+        to[0] = output_of(t.v[k].x, t.m, t.sum);
+        to[1] = output_of(t.v[k].y, t.m, t.sum);
+        to[2] = output_of(t.v[k].z, t.m, t.sum);
+        to[3] = output_of(t.v[k].w, t.m, t.sum);
+      }
     }
   }
 }
@@ -573,7 +636,9 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     __syncwarp();
   }
   if (kCluster && sh.splits > 1) cluster_arrive();  // waited for before the first word goes to another CTA
-  pdl_wait_primary();
+  // kOwn, kPacked: begun when every CTA of the shared tokens' kernel has waited for what was before; its parts are
+  // waited for where they are added.
+  if constexpr (MODE != kOwn && MODE != kPacked) pdl_wait_primary();
   if constexpr (MODE == kPrefix) pdl_release_dependents();
 
   // The CTA's row (sequence b, head `row` of its key heads and groups of q heads)
@@ -1017,11 +1082,19 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
     part[DT] = ref;
     part[DT + 1] = sum;
   }
-  if constexpr (kBehind) {
-    __syncwarp();
-    add_prefix<S::kPartial, DT>(a, c, sh, b, hk, first_of_group, heads, me, workers, base + warp * S::kWarpBytes, lane);
+  if constexpr (MODE == kPacked) {
+    meet();
+    pdl_wait_primary();
+    finish_packed<S::kPartial, DT>(c, sh, parts_of(c, sh, b, hk, first_of_group, heads, lane), heads, me, row_warps, base + first_warp * S::kWarpBytes,
+                                   S::kWarpBytes, a.out + b * a.out_stride + (int64_t)hq * D, lane);
+    return;
   }
-  meet();
+  if constexpr (MODE == kOwn) {
+    __syncwarp();
+    pdl_wait_primary();
+    add_prefix<S::kPartial, DT>(c, sh, parts_of(c, sh, b, hk, first_of_group, heads, lane), heads, me, workers, base + warp * S::kWarpBytes, lane);
+  }
+  __syncthreads();
 
   auto of_warps = [&](int h, int d) {
     const uint32_t p = base + h * S::kPartial;
@@ -1031,14 +1104,6 @@ attend_kernel(AttendArgs a, KvPages c, Shares sh) {
   auto finish = [&](int h, int d, const Joined& j) {
     a.out[b * a.out_stride + (int64_t)(hq + h) * D + d] = output_of(j.value, j.m, j.sum);
   };
-  if constexpr (MODE == kPacked) {
-    for (int i = threadIdx.x - 32 * first_warp; i < heads * D; i += 32 * row_warps) {
-      const int h = head_of(i), d = i - h * D;
-      const uint32_t p = base + first_warp * S::kWarpBytes + h * S::kPartial;
-      finish(h, d, join<kWarps>(p + 4 * d, S::kWarpBytes, p + 4 * DT, S::kWarpBytes, row_warps));
-    }
-    return;
-  }
   if (MODE == kSharedOut || MODE == kPrefix || splits == 1) {
     const bool whole = MODE != kPrefix && splits == 1;
     float* part = whole ? nullptr : sh.parts + (int64_t)blockIdx.x * min(kRowHeads, group) * (D + 4);

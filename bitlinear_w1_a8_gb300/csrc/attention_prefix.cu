@@ -118,10 +118,6 @@ __device__ __forceinline__ float largest_of(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float4 lds_float4(uint32_t a) {
-  const uint4 w = lds128(a);
-  return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
-}
 // Two values as the leading fp16 parts and what they leave, both whole.
 __device__ __forceinline__ void parts_of(float2 w, uint32_t& lead, uint32_t& rest) {
   const __half2 h = __floats2half2_rn(w.x, w.y);
@@ -218,10 +214,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     part = p.part;
     parts = p.parts;
   } else {
-    b = blockIdx.x / (uint32_t)sh.rows_a_seq;
-    row = blockIdx.x - (uint32_t)b * sh.rows_a_seq;
-    part = 0;
-    parts = 1;
+    const uint32_t at = blockIdx.x / (uint32_t)sh.splits;
+    b = at / (uint32_t)sh.rows_a_seq;
+    row = at - (uint32_t)b * sh.rows_a_seq;
+    part = blockIdx.x - at * sh.splits;
+    parts = sh.splits;
   }
   if (warp == kIssue) tc::tmem_alloc(&st.tmem_at, 512);
   if (part == 0 && threadIdx.x == 0) sh.rows[b * sh.rows_a_seq + row] = make_int2(blockIdx.x, parts);
@@ -329,7 +326,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     const float unit = W::kBf16 ? 1.0f : st.row_tops[0][0][r];  // of a logit in S
     tc::named_bar_sync(3, 32 * kBring);
     const bool none = (warp & 3) * 32 >= heads;  // rows of no q head: whatever comes of them is theirs
-    const uint32_t row_end = there ? min(len, (uint32_t)max(0, sh.lengths[seq])) : 0u;
+    const uint32_t row_end = there ? min(len, (uint32_t)max(0, sh.lengths[seq])) : len;  // beside none: masked as the others are
 
     constexpr int kSide = kTile / 2, kGranules = kSide / 16;  // tokens of this thread, and 16s of them
     constexpr int kDims = DT / 2;                             // and dims
@@ -802,13 +799,13 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, Shares sh, int64
   }
   const int sms = dev.num_sms < kSms ? dev.num_sms : kSms;
   const int64_t steps = ((a.max_pages << c.page_shift) + kTile - 1) / kTile;
-  // in proportion to the tokens where rows round up to whole CTAs well below the GPU, else a CTA a row
+  // In proportion to the tokens where rows round up to whole CTAs well below the GPU, else as many CTAs a row as it has room for.
   if (a.B <= kShareSeqs && rows <= sms / 3 && steps_fit(rows, steps)) {
     sh.splits = 0;
     cfg.gridDim = dim3((unsigned)sms, 1, 1);
   } else {
-    sh.splits = 1;
-    cfg.gridDim = dim3((unsigned)rows, 1, 1);
+    sh.splits = rows < sms ? (int)(sms / rows) : 1;
+    cfg.gridDim = dim3((unsigned)(rows * sh.splits), 1, 1);
   }
   Maps maps = {};
   if constexpr (W::kBf16) {
