@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       }
     } else {
       // bf16 values become fp16 where they are, under the power of two that puts the tile's largest to 2^14 .. 2^15
-      // (an infinity or a NaN stays what it is); those of tokens that are not there become 0.
+      // (what is below 2^-32 of that is rounded to a multiple of 2^-38); those of tokens that are not there become 0.
       constexpr int kTurns = W::kOperand / (kBringThreads * 16);
 #pragma unroll 1
       for (int n = 0; n < tiles; ++n) {
@@ -600,7 +600,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         top = __reduce_max_sync(kFullMask, max(top & 0xffffu, top >> 16));
         if (lane == 0) st.tops[n & 1][warp - kBring] = top;
         tc::named_bar_sync(4, kBringThreads);
-        const int e = max(30, min(230, (int)(__reduce_max_sync(kFullMask, st.tops[n & 1][lane & 7]) >> 7)));
+        top = __reduce_max_sync(kFullMask, st.tops[n & 1][lane & 7]);
+        const int e = max(30, min(254, (int)(top >> 7)));
         const float2 scale = both(power2(141 - e));
 #pragma unroll
         for (int t = 0; t < kTurns; ++t) {
@@ -615,7 +616,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
           }
           tc::st_shared_v4(at + t * kBringThreads * 16, w.x, w.y, w.z, w.w);
         }
-        if (tid == 0) st.v_most[entry][0] = power2(e - 141);
+        // beside an infinity or a NaN the others are lost: whoever meets the tile has NaN
+        if (tid == 0) st.v_most[entry][0] = top >= 0x7f80u ? NAN : power2(e - 141);
         done(stage);
       }
     }

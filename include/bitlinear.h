@@ -548,9 +548,10 @@ size_t bitlinear_attention_shared_workspace(int64_t B, int num_q_heads, int num_
  *   num_groups a divisor of B.  B * num_q_heads < 2^31.
  *   workspace  as for bitlinear_attention, at least bitlinear_attention_shared_workspace() bytes; NULL
  *              only where that is 0 or num_groups == B.
- * Every other argument, and results, as for bitlinear_attention; a NaN or an infinity in a shared token
- * that counts for one of a group's rows may reach each of them.  Nothing past the longest row
- * of a group is read.  Results do not depend on timing.
+ * Every other argument, and results, as for bitlinear_attention, but that a NaN or an infinity in a shared
+ * token that counts for one of a group's rows may reach each of them, and every dim of the heads that meet it; and that
+ * of a bf16 value as little as 2^-39 of the largest of its key head among 128 shared tokens may be lost.
+ * Nothing past the longest row of a group is read.  Results do not depend on timing.
  * Errors: as bitlinear_attention. */
 bitlinear_status bitlinear_attention_shared(const float* q, int64_t q_stride, int64_t B, int num_q_heads,
                                             const bitlinear_kv_pages* cache, const int32_t* page_table,
@@ -570,8 +571,8 @@ typedef struct bitlinear_kv_summary {
  * With lo_d and hi_d the least and largest of dim d over the page's tokens before lengths[b] (each the fp32
  * product code * step of the cache): a = max(max_d |lo_d|, max_d |hi_d|, 1e-5), s = 127 / a, step = a / 127,
  *   lower_d = max(floor(lo_d * s), -127), upper_d = min(ceil(hi_d * s), 127), every step in fp32.
- * Pages out of range and those of other tokens stay as they were; a page that two sequences name is
- * either's.  Keys that are not finite give unspecified bounds of their page and head.
+ * Pages out of range and those of other tokens stay as they were; a page in which two sequences have different
+ * numbers of tokens is unspecified, and so are the bounds of a page and head with keys that are not finite.
  *   B >= 0 (0 enqueues nothing); page_table: B rows, as for bitlinear_attention; first, lengths device
  *   int32 [B].
  * Errors: BITLINEAR_ERR_NULL, BITLINEAR_ERR_SHAPE, BITLINEAR_ERR_ALIGN, BITLINEAR_ERR_UNSUPPORTED,

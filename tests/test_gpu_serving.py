@@ -671,3 +671,146 @@ def test_the_binding_with_and_without_the_compiled_marshal(compiled, monkeypatch
                  lambda: bl.bitlinear_kv_summarise(cache, (s[0].float(), s[1]), table, i, i)):
         with pytest.raises(TypeError):
             call()
+
+
+# ------------------------------------------------------------------ ranges of values, and of addresses
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_shared_bf16_values_of_many_magnitudes(D):
+    """Tiles of 128 tokens on the tensor cores whose values are 2^40 apart, one of zeros, one of a single large value.
+
+    A value loses 2^-39 of its tile's largest at most, beside the bound of all formats: weighted as the values are."""
+    R, G, Hkv, S, page = 40, 2, 2, 900, 64
+    lengths = S + np.arange(R) % 7
+    cache, q, table = shared_case("bf16", 1, R, G * Hkv, Hkv, D, [S], lengths, page, 71)
+    size = np.ones(960)
+    size[128:256], size[256:384], size[384:512], size[512:640] = 2.0 ** 20, 0.0, 2.0 ** -20, 2.0 ** -90
+    largest = np.zeros((Hkv, 960))
+    for t in range(S):
+        cache[1][table[0, t // page], :, t % page] *= size[t]
+    cache[1][table[0, 700 // page], :, 700 % page, 5] = 3e4
+    want, bound = attention_plain.attend(q.numpy(), cache, table, lengths, page, D ** -0.5)
+    held = attention_plain.held(cache, "v")
+    for t0 in range(0, S, 128):
+        rows = [(table[0, t // page], t % page) for t in range(t0, min(S, t0 + 128))]
+        largest[:, t0:t0 + 128] = np.max([np.abs(held[p, :, o]).max(-1) for p, o in rows], 0)[:, None]
+    keys = attention_plain.held(cache, "k")
+    for b in range(R):
+        for h in range(G * Hkv):
+            k = np.stack([keys[table[b, t // page], h // G, t % page] for t in range(lengths[b])])
+            w = np.exp((x := D ** -0.5 * (k @ q[b, h].double().numpy())) - x.max())
+            bound[b, h] += 1.01 * 2.0 ** -39 * (w @ largest[h // G, :lengths[b]]) / w.sum()
+    out = torch.empty(q.shape, device="cuda")
+    ws = torch.empty(bl.bitlinear_attention_shared_workspace(R, G * Hkv, Hkv, D, 1), dtype=torch.uint8, device="cuda")
+    bl.bitlinear_attention_shared(q.cuda(), cache, wide_table(table, cache), ints(lengths), ints([S]), out, ws)
+    within(out, want, bound)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("R,G", [(4, 2), (64, 4)])
+def test_shared_values_that_are_infinite(fmt, R, G):
+    """An infinity among shared values: no finite number where it counts, the other key head as before; in a step likewise."""
+    S, page, D = 300, 16, 64
+    lengths = S + 1 + np.arange(R) % 11
+    cache, q, table = shared_case(fmt, 1, R, 2 * G, 2, D, [S], lengths, page, 31)
+    ws = torch.empty(bl.bitlinear_attention_shared_workspace(R, 2 * G, 2, D, 1), dtype=torch.uint8, device="cuda")
+    out, columns = torch.empty(q.shape, device="cuda"), wide_table(table, cache)
+    run = lambda: (bl.bitlinear_attention_shared(q.cuda(), cache, columns, ints(lengths), ints([S]), out, ws), out.cpu())[1]  # noqa: E731
+    clean = run()
+    assert torch.isfinite(clean).all()
+    if fmt == "bf16":
+        cache[1][table[0, 5], 1, 3, 7] = float("inf")
+        got = run()
+        assert not torch.isfinite(got[:, G:, 7]).any()
+        others = torch.arange(D) != 7
+        same = (got[:, G:] == clean[:, G:]) | torch.isnan(got[:, G:])
+        assert same[:, :, others].all()
+    else:
+        cache[3][table[0, 5], 1, 3] = float("inf")
+        assert not torch.isfinite(run()[:, G:]).any()
+    assert torch.equal(run()[:, :G], clean[:, :G])
+
+
+def test_garbage_behind_the_tokens_is_not_met():
+    """The largest finite values where no token is, in the tile that shared tokens end in."""
+    R, G, Hkv, S, page, D = 64, 2, 2, 333, 64, 96
+    lengths = S + np.arange(R) % 3
+    cache, q, table = shared_case("bf16", 1, R, G * Hkv, Hkv, D, [S], lengths, page, 77)
+    for c in cache[:2]:
+        c[torch.isnan(c)] = 3e38
+    out = torch.empty(q.shape, device="cuda")
+    ws = torch.empty(bl.bitlinear_attention_shared_workspace(R, G * Hkv, Hkv, D, 1), dtype=torch.uint8, device="cuda")
+    bl.bitlinear_attention_shared(q.cuda(), cache, wide_table(table, cache), ints(lengths), ints([S]), out, ws)
+    want, bound = attention_plain.attend(q.numpy(), cache, table, lengths, page, D ** -0.5)
+    within(out, want, bound)
+
+
+@pytest.mark.parametrize("fmt", attention_plain.FORMATS)
+def test_caches_of_more_than_4_gib(fmt):
+    """The same pages at the end of a cache whose codes pass 2^32 bytes: the same bits from every operator."""
+    Hkv, G, D, page, S = 8, 4, 128, 64, 512  # whole pages: in one that rows share, all have as many tokens
+    a_page = Hkv * page * D * (2 if fmt == "bf16" else 1)
+    for R in (6, 64):  # the tensor cores' path among them
+        lengths = S + 1 + np.arange(R) % 90
+        cache, q, table = shared_case(fmt, 1, R, Hkv * G, Hkv, D, [S], lengths, page, 81)
+        pages = cache[0].shape[0]
+        first = (1 << 32) // a_page + 5
+        large = tuple(None if c is None else torch.empty(first + pages, *c.shape[1:], dtype=c.dtype, device="cuda") for c in cache)
+        for big, c in zip(large, cache):
+            if big is not None:
+                big[first:] = c
+        ws = torch.empty(bl.bitlinear_attention_shared_workspace(R, Hkv * G, Hkv, D, 1), dtype=torch.uint8, device="cuda")
+        columns, n, share, q = wide_table(table, cache), ints(lengths), ints([S]), q.cuda()
+        got = []
+        for c, t in ((cache, columns), (large, torch.where(columns >= 0, columns + first, columns))):
+            out, listed = torch.empty(q.shape, device="cuda"), torch.empty(q.shape, device="cuda")
+            summary = new_summary(c)
+            blocks = torch.empty(R, Hkv, 4, dtype=torch.int32, device="cuda")
+            bl.bitlinear_attention_shared(q, c, t, n, share, out, ws)
+            bl.bitlinear_kv_summarise(c, summary, t, torch.zeros_like(n), n)
+            bl.bitlinear_attention_select(q, c, summary, t[:, :table.shape[1]], n, blocks)
+            bl.bitlinear_attention_blocks(q, c, t, n, blocks, listed)
+            torch.cuda.synchronize()
+            got.append((out, blocks, listed, summary[0][-pages:], summary[1][-pages:]))
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ the compiled marshal
+
+
+@pytest.fixture
+def stand_ins():
+    import ctypes
+    lib = bl.load_library()
+    if bl._marshal is None:
+        pytest.skip("bitlinear_marshal was not built")
+    address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    yield lambda f: bl._marshal.bind_serving(*[address(f)] * len(bl._SERVING))
+    bl._marshal.bind_serving(*(address(getattr(lib, "bitlinear_" + n)) for n in bl._SERVING))
+
+
+def serving_calls():
+    x, i = torch.zeros(2, 2, 64, device="cuda"), ints([1, 1])
+    cache = tuple(torch.zeros(4, 2, 16, 64, dtype=torch.int8, device="cuda") for _ in "kv") + tuple(torch.zeros(4, 2, 16, device="cuda") for _ in "kv")
+    table, s = ints([[0, 1], [2, 3]]), (torch.zeros(4, 2, 2, 64, dtype=torch.int8, device="cuda"), torch.zeros(4, 2, device="cuda"))
+    blocks, two = torch.zeros(2, 2, 1, dtype=torch.int32, device="cuda"), torch.zeros(2, 2, device="cuda")
+    m = bl._marshal
+    return {"attention_shared": m.attention_shared(x, cache, table, i, i[:1], x.clone(), None, None, 0, None),
+            "kv_summarise": m.kv_summarise(cache, s, table, i, i, 0, None),
+            "attention_select": m.attention_select(x, cache, s, table, i, blocks, 1, 1, 0, None),
+            "attention_blocks": m.attention_blocks(x, cache, table, i, blocks, x.clone(), None, 0, None),
+            "softmax": m.softmax(two, two, None, 0, None),
+            "verify": m.verify(x, x[:, :1].clone(), i.view(2, 1), two, ints([[0, 0], [0, 0]]), i, 0, None)}
+
+
+def test_the_marshal_returns_the_librarys_status_and_lets_other_threads_run(stand_ins):
+    """Stand-ins for the entry points: nothing is launched."""
+    import ctypes
+    status = bl.load_library().bitlinear_abi_version
+    stand_ins(status)
+    assert serving_calls() == dict.fromkeys(bl._SERVING, status())
+    stand_ins(ctypes.pythonapi.PyGILState_Check)
+    assert serving_calls() == dict.fromkeys(bl._SERVING, 0)
+    assert ctypes.pythonapi.PyGILState_Check() == 1
