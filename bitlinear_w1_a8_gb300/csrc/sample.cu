@@ -13,8 +13,8 @@
 // in 64 bits whatever their order, and the token is the first whose running sum passes r * total.
 //
 // Measured.  softmax: 320 rows of 50000 28.9 us, 128 MB, 4.4 TB/s (a copy's 19.1 us): rows come in four rounds of clusters,
-// each of which reads, meets once and writes; one row 3.6 us, latency.  Streaming rows through shared memory under resident
-// CTAs took 38, five CTAs an SM 32.4.  verify: 64 sequences of 4 drafts over 50000 tokens 14.6 us (3.8 us of bytes): the
+// each of which reads, meets once and writes; one row 3.6 us, latency.  Rows streamed through rings in shared memory under
+// resident CTAs took 43.3 where this took 33.9; five CTAs an SM 32.4 for 30.5.  verify: 64 sequences of 4 drafts over 50000 tokens 14.6 us (3.8 us of bytes): the
 // drafts' probabilities, then the two rows they point to, then the cluster's meeting, one after the other; one sequence 7.0.
 #include <type_traits>
 

@@ -18,8 +18,8 @@
 // rounds and a half of CTAs whose loads, join in shared memory and lookups follow one another (a warp waits for memory half
 // of its time); of the page that a token was just written to, 16 sequences of 32 heads: 4.0 us, latency.  A warp a page,
 // whose lanes join by shuffles, took 10.6 and 8.7.  The choice of 32 of 256 pages for 16 sequences of 32 heads: 9.2 us, of 64 of 2048
-// for one of 8 key heads 11.0: latency, a dozen meetings of a CTA's threads among it (a byte at a time over all keys, the
-// way of more than 8192 pages, took 14 and 19).
+// for one of 8 key heads 11.0: latency, a dozen meetings of a CTA's threads among it (a byte at a time over all CTAs'
+// keys, the way of more than 8192 pages, and bounds that waited for q's codes took 16 and 22).
 #include <cuda_fp16.h>
 
 #include <type_traits>
