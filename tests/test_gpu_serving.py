@@ -814,3 +814,90 @@ def test_the_marshal_returns_the_librarys_status_and_lets_other_threads_run(stan
     stand_ins(ctypes.pythonapi.PyGILState_Check)
     assert serving_calls() == dict.fromkeys(bl._SERVING, 0)
     assert ctypes.pythonapi.PyGILState_Check() == 1
+
+
+# ------------------------------------------------------------------ largest sizes, and calls at the same time
+
+
+@pytest.mark.parametrize("fmt", attention_plain.FORMATS)
+def test_pages_of_4096_tokens(fmt):
+    lengths, page = [5000, 4096, 1], 4096
+    cache, table = filled_cache(fmt, 3, 1, 16, lengths, page, 8)
+    bounds, step = new_summary(cache)
+    bl.bitlinear_kv_summarise(cache, (bounds, step), ints(table), ints([0, 0, 0]), ints(lengths))
+    ids = [(table[b, j], min(page, n - j * page)) for b, n in enumerate(lengths) for j in range(-(-n // page))]
+    want_b, want_s = plain.summaries(cache, *zip(*ids))
+    at = [i for i, _ in ids]
+    np.testing.assert_array_equal(bounds.cpu().numpy()[at], want_b)
+    np.testing.assert_array_equal(step.cpu().numpy()[at], want_s)
+    q = normal((3, 2, 16), 9)
+    blocks = ints([[[1, 0]], [[0, -1]], [[0, 1]]])
+    out = torch.empty(q.shape, device="cuda")
+    bl.bitlinear_attention_blocks(q.cuda(), cache, ints(table), ints(lengths), blocks, out)
+    want, bound = plain.attend_blocks(q.numpy(), cache, table, lengths, blocks.cpu().numpy(), page, 0.25)
+    within(out, want, bound)
+
+
+def test_as_many_blocks_as_there_may_be():
+    """4096 of a row's columns in any order, most of them none."""
+    page, L, rng = 16, 3000, np.random.default_rng(3)
+    cache, table = filled_cache("int8", 2, 2, 80, [L, 40], page, 12)
+    blocks = np.where(rng.random((2, 2, 4096)) < 0.02, rng.integers(0, table.shape[1], (2, 2, 4096)), rng.choice([-1, -2 ** 31, 2 ** 31 - 1, 10 ** 5], (2, 2, 4096)))
+    q = normal((2, 6, 80), 13)
+    out = torch.empty(q.shape, device="cuda")
+    bl.bitlinear_attention_blocks(q.cuda(), cache, ints(table), ints([L, 40]), ints(blocks), out)
+    want, bound = plain.attend_blocks(q.numpy(), cache, table, [L, 40], blocks, page, 80 ** -0.5)
+    within(out, want, bound)
+
+
+def test_as_many_drafts_as_there_may_be():
+    K, V = 65535, 8
+    p = probabilities((1, K + 1, V), 5)
+    q, uniform = p[:, :K].clone(), torch.rand(1, K + 1, generator=torch.Generator().manual_seed(6))
+    draft = torch.randint(0, V, (1, K), dtype=torch.int32, generator=torch.Generator().manual_seed(7))
+    for refused in (None, 65000):
+        if refused is not None:
+            q[0, refused], uniform[0, refused] = 1.0, 0.999
+        tokens, accepted = torch.empty(1, K + 1, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+        bl.bitlinear_verify(p.cuda(), q.cuda(), draft.cuda(), uniform.cuda(), tokens, accepted)
+        want_tokens, want_accepted = plain.verify(p.numpy(), q.numpy(), draft.numpy(), uniform.numpy())
+        np.testing.assert_array_equal(tokens.cpu().numpy(), want_tokens)
+        assert accepted.item() == want_accepted[0] == (K if refused is None else refused)
+
+
+def test_calls_at_the_same_time():
+    """Two streams, each with calls of its own on its own workspace, beside matrix products on the tensor cores: the bits of each alone."""
+    cases = [("bf16", 1, 64, 32, 8, 128, [700]), ("int8", 4, 10, 16, 16, 80, [900, 500, 40, 333])]
+    runs = []
+    for i, (fmt, groups, R, Hq, Hkv, D, shared) in enumerate(cases):
+        lengths = np.repeat(shared, R) + np.random.default_rng(i).integers(1, 60, groups * R)
+        cache, q, table = shared_case(fmt, groups, R, Hq, Hkv, D, shared, lengths, 32, 60 + i)
+        ws = torch.empty(bl.bitlinear_attention_shared_workspace(groups * R, Hq, Hkv, D, groups), dtype=torch.uint8, device="cuda")
+        y = torch.randn(40, 50000, device="cuda")
+        args = q.cuda(), cache, wide_table(table, cache), ints(lengths), ints(shared)
+        alone = torch.empty(q.shape, device="cuda"), torch.empty_like(y)
+        bl.bitlinear_attention_shared(*args, alone[0], ws)
+        bl.bitlinear_softmax(y, alone[1])
+        runs.append((args, ws, y, alone, torch.cuda.Stream()))
+    W = torch.randn(1024, 1024, device="cuda")
+    packed, sw = torch.empty(bl.bitlinear_packed_bytes(1024, 1024), dtype=torch.uint8, device="cuda"), torch.empty(1, device="cuda")
+    bl.bitlinear_quantize_weights(W, packed, sw, torch.empty(bl.bitlinear_quantize_weights_workspace(1024, 1024), dtype=torch.uint8, device="cuda"))
+    x, third = torch.randn(512, 1024, device="cuda"), torch.cuda.Stream()
+    xq, sx, y0, y1 = torch.empty(512, 1024, dtype=torch.int8, device="cuda"), torch.empty(512, device="cuda"), torch.empty(512, 1024, device="cuda"), torch.empty(512, 1024, device="cuda")
+    bl.bitlinear_linear(x, [(packed, sw, y0)], xq, sx)
+    torch.cuda.synchronize()
+    got = [[(torch.empty_like(alone[0]), torch.empty_like(alone[1])) for _ in range(6)] for _, _, _, alone, _ in runs]
+    torch.cuda.synchronize()
+    for turn in range(6):
+        for (args, ws, y, _, stream), outs in zip(runs, got):
+            with torch.cuda.stream(stream):
+                bl.bitlinear_attention_shared(*args, outs[turn][0], ws, flags=bl.FLAG_PDL)
+                bl.bitlinear_softmax(y, outs[turn][1], flags=bl.FLAG_PDL)
+        with torch.cuda.stream(third):
+            bl.bitlinear_linear(x, [(packed, sw, y1)], xq, sx)
+    torch.cuda.synchronize()
+    for (_, _, _, alone, _), outs in zip(runs, got):
+        for o in outs:
+            assert torch.equal(o[0], alone[0]) and torch.equal(o[1], alone[1])
+    assert torch.equal(y0, y1)
+    assert bl.bitlinear_device_status() == 0
