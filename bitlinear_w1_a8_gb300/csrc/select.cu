@@ -18,7 +18,7 @@
 // rounds and a half of CTAs whose loads, join in shared memory and lookups follow one another (a warp waits for memory half
 // of its time); of the page that a token was just written to, 16 sequences of 32 heads: 4.0 us, latency.  A warp a page,
 // whose lanes join by shuffles, took 10.6 and 8.7.  The choice of 32 of 256 pages for 16 sequences of 32 heads: 9.2 us, of 64 of 2048
-// for one of 8 key heads 11.0: latency, a dozen meetings of a CTA's threads among it (a byte at a time over all CTAs'
+// for one of 8 key heads 8.7: latency, a dozen meetings of a CTA's threads among it (a byte at a time over all CTAs'
 // keys, the way of more than 8192 pages, and bounds that waited for q's codes took 16 and 22).
 #include <cuda_fp16.h>
 
@@ -405,14 +405,19 @@ __device__ __forceinline__ void find_in_cluster(const uint32_t* keys, int here, 
   }
 }
 
+// A lane's 16 of a page's bounds at a time: LANES of them (a power of two) have a row, of lower or of upper bounds, a
+// warp 16 / LANES pages an instruction and kLoads of these on their way.  (Two lanes a page, each reading a row from end to
+// end, took 3.9 us for 256 pages of 128 dims where this takes 2.1: every load touched 32 lines.)
+constexpr int kLoads = 8;
+
 // A cluster chooses for one key head of one sequence.  Every CTA scores a run of the pages; up to kGathered of them
 // (`gather`) all keys go to the first CTA, which chooses, and beyond each keeps its own and writes its chosen
 // pages where those of the CTAs before it end.
-template <int CHUNKS>  // of 16 dims, at most
+template <int LANES>  // dims / 16 at most
 __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, KvPages c, Summary summary, int share, bool gather) {
   extern __shared__ __align__(16) uint8_t smem[];
   uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
-  __shared__ __align__(16) int8_t codes[kHeadsAtOnce][2][CHUNKS * 16];  // parts below and above 0
+  __shared__ __align__(16) int8_t codes[kHeadsAtOnce][2][LANES * 16];  // parts below and above 0
   __shared__ float steps[kHeadsAtOnce];
   __shared__ Scratch scratch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -430,29 +435,37 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, KvPages 
   const int32_t* table = a.table + b * a.table_stride;
   int32_t* out = a.blocks + (b * c.heads + hk) * a.count;
 
-  // two lanes a page: one the lower bounds, one the upper
-  const int mine = threadIdx.x / 2, side = threadIdx.x & 1;
-  uint4 w[CHUNKS];
+  constexpr int kTogether = 16 / LANES, kPages = kLoads * kTogether;  // pages of an instruction, and of a warp
+  static_assert(kLoads == 8 && LANES >= 4, "three halvings leave a page a lane");
+  const int chunk = lane & (LANES - 1), side = (lane / LANES) & 1;
+  const int mine = ((lane & 1) << 2 | (lane & 2) | ((lane >> 2) & 1)) * kTogether + lane / (2 * LANES);  // the page that this lane ends with
+  const bool writes = (lane & (2 * LANES - 1)) < 8;  // one of those that end with it
+  uint4 w[kLoads];
   float step;
-  bool there;
-  auto bring = [&](int i) {
-    const int32_t page = i < here ? table[from + i] : -1;
-    there = page >= 0 && page < c.num_pages;
-    const int64_t head = (int64_t)(there ? page : 0) * c.heads + hk;
-    const uint4* bounds = reinterpret_cast<const uint4*>(summary.bounds + (head * 2 + side) * D);
+  int32_t page_here;
+  auto look_up = [&](int i0) { return lane < kPages && i0 + warp * kPages + lane < here ? table[from + i0 + warp * kPages + lane] : -1; };
+  int32_t listed = look_up(0);
+  auto bring = [&](int i0) {
+    if (listed >= c.num_pages) listed = -1;
 #pragma unroll
-    for (int k = 0; k < CHUNKS; ++k) w[k] = there && k < chunks ? __ldg(bounds + k) : make_uint4(0, 0, 0, 0);
-    step = there ? __ldg(summary.step + head) : 0.0f;
+    for (int j = 0; j < kLoads; ++j) {
+      const int32_t page = __shfl_sync(kFullMask, listed, j * kTogether + lane / (2 * LANES));
+      w[j] = page >= 0 && chunk < chunks ? __ldg(reinterpret_cast<const uint4*>(summary.bounds + (((int64_t)page * c.heads + hk) * 2 + side) * D) + chunk)
+                                         : make_uint4(0, 0, 0, 0);
+    }
+    page_here = __shfl_sync(kFullMask, listed, mine);
+    step = page_here >= 0 ? __ldg(summary.step + (int64_t)page_here * c.heads + hk) : 0.0f;
+    listed = look_up(i0 + kWarps * kPages);
   };
-  bring(mine);  // on their way while q is turned into codes
+  bring(0);  // on their way while q is turned into codes
   for (int h0 = 0; h0 < group; h0 += kHeadsAtOnce) {
     const int heads = min(kHeadsAtOnce, group - h0);
     if (h0 > 0) __syncthreads();
     for (int h = warp; h < heads; h += kWarps) {  // a warp quantises a head
       const float* q = a.q + b * a.q_stride + (hk * group + h0 + h) * D;
-      float x[(CHUNKS * 16 + 31) / 32], top = kLeastTop;
+      float x[(LANES * 16 + 31) / 32], top = kLeastTop;
 #pragma unroll
-      for (int i = 0; i < (CHUNKS * 16 + 31) / 32; ++i) {
+      for (int i = 0; i < (LANES * 16 + 31) / 32; ++i) {
         x[i] = lane + 32 * i < D ? q[lane + 32 * i] : 0.0f;
         top = fmaxf(top, fabsf(x[i]));
       }
@@ -460,7 +473,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, KvPages 
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
       const float s = __fdiv_rn(127.0f, top);
 #pragma unroll
-      for (int i = 0; i < (CHUNKS * 16 + 31) / 32; ++i) {
+      for (int i = 0; i < (LANES * 16 + 31) / 32; ++i) {
         if (lane + 32 * i < D) {
           const int code = max(-127, min(127, __float2int_rn(__fmul_rn(x[i], s))));
           codes[h][0][lane + 32 * i] = (int8_t)min(code, 0);
@@ -470,33 +483,38 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, KvPages 
       if (lane == 0) steps[h] = __fdiv_rn(top, 127.0f);
     }
     __syncthreads();
-    for (int i0 = 0; i0 < here; i0 += kThreads / 2) {
-      const int i = i0 + mine, column = from + i;
-      if (i0 > 0 || h0 > 0) bring(i);
+    if (h0 > 0) listed = look_up(0);
+    for (int i0 = 0; i0 < here; i0 += kWarps * kPages) {
+      const int i = i0 + warp * kPages + mine, column = from + i;
+      if (i0 > 0 || h0 > 0) bring(i0);
       float best = -INFINITY;
       bool nan = false;
       for (int h = 0; h < heads; ++h) {
-        int acc = 0;
+        const uint4 x = *reinterpret_cast<const uint4*>(&codes[h][side][16 * chunk]);
+        int acc[kLoads];
 #pragma unroll
-        for (int k = 0; k < CHUNKS; ++k) {
-          if (k < chunks) {
-            const uint4 x = *reinterpret_cast<const uint4*>(&codes[h][side][16 * k]);
-            acc = __dp4a((int)w[k].x, (int)x.x, acc);
-            acc = __dp4a((int)w[k].y, (int)x.y, acc);
-            acc = __dp4a((int)w[k].z, (int)x.z, acc);
-            acc = __dp4a((int)w[k].w, (int)x.w, acc);
+        for (int j = 0; j < kLoads; ++j)
+          acc[j] = __dp4a((int)w[j].w, (int)x.w, __dp4a((int)w[j].z, (int)x.z, __dp4a((int)w[j].y, (int)x.y, __dp4a((int)w[j].x, (int)x.x, 0))));
+        // three halvings: a lane keeps half of its loads and gives the others away
+#pragma unroll
+        for (int n = kLoads / 2, o = 1; n > 0; n /= 2, o *= 2) {
+#pragma unroll
+          for (int j = 0; j < n; ++j) {
+            const bool upper = lane & o;
+            acc[j] = (upper ? acc[j + n] : acc[j]) + __shfl_xor_sync(kFullMask, upper ? acc[j] : acc[j + n], o);
           }
         }
-        acc += __shfl_xor_sync(kFullMask, acc, 1);
-        const float score = __fmul_rn(__fmul_rn((float)acc, step), steps[h]);
+#pragma unroll
+        for (int o = 8; o < 2 * LANES; o *= 2) acc[0] += __shfl_xor_sync(kFullMask, acc[0], o);
+        const float score = __fmul_rn(__fmul_rn((float)acc[0], step), steps[h]);
         nan |= score != score;
         best = fmaxf(best, score);
       }
-      if (i < here && side == 0) {
+      if (i < here && writes) {
         uint32_t key = nan ? 1u : key_of(best);
         if (h0 > 0) key = keys[i] == 1u || key == 1u ? 1u : max(key, keys[i]);
         if (h0 + heads >= group && (column < a.keep_first || column >= pages - a.keep_last)) key = kKept;
-        keys[i] = there ? key : kAbsent;
+        keys[i] = page_here >= 0 ? key : kAbsent;
       }
     }
   }
@@ -538,24 +556,30 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, KvPages 
       equal_before += scratch.counted[r][1];
     }
   }
-  // Written in order, a block of threads at a time.
-  for (int i0 = 0; i0 < here; i0 += kThreads) {
-    const int i = i0 + threadIdx.x;
-    const uint32_t k = i < here ? keys[i] : kAbsent;
-    const uint32_t m = __ballot_sync(kFullMask, k > known), e = __ballot_sync(kFullMask, k == known);
-    __syncthreads();
-    if (lane == 0) {
-      scratch.of_warps[warp][0] = __popc(m);
-      scratch.of_warps[warp][1] = __popc(e);
-    }
-    __syncthreads();
-    const uint32_t below = (1u << lane) - 1, wm = lane < kWarps ? scratch.of_warps[lane][0] : 0u, we = lane < kWarps ? scratch.of_warps[lane][1] : 0u;
-    const uint32_t m_at = more_before + __popc(m & below) + __reduce_add_sync(kFullMask, lane < warp ? wm : 0u);
-    const uint32_t e_at = equal_before + __popc(e & below) + __reduce_add_sync(kFullMask, lane < warp ? we : 0u);
-    more_before += __reduce_add_sync(kFullMask, wm);
-    equal_before += __reduce_add_sync(kFullMask, we);
-    if (k > known || (k == known && e_at < wanted)) out[m_at + min(e_at, wanted)] = from + i;
+  // Written in order: a thread has a run of the keys, and counts what is before it.
+  const int each = (here + kThreads - 1) / kThreads, first = min(here, (int)threadIdx.x * each), last = min(here, first + each);
+  uint32_t counts = 0;  // more above, equal below
+  for (int i = first; i < last; ++i) counts += (uint32_t)(keys[i] > known) << 16 | (uint32_t)(keys[i] == known);
+  uint32_t upto = counts;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(kFullMask, upto, o);
+    if (lane >= o) upto += x;
   }
+  __syncthreads();
+  if (lane == 31) scratch.of_warps[warp][0] = upto;
+  __syncthreads();
+  const uint32_t of_warp = lane < kWarps ? scratch.of_warps[lane][0] : 0u;
+  const uint32_t before = upto - counts + __reduce_add_sync(kFullMask, lane < warp ? of_warp : 0u), whole = __reduce_add_sync(kFullMask, of_warp);
+  uint32_t m_at = more_before + (before >> 16), e_at = equal_before + (before & 0xffffu);
+  for (int i = first; i < last; ++i) {
+    const uint32_t k = keys[i];
+    if (k > known || (k == known && e_at < wanted)) out[m_at + min(e_at, wanted)] = from + i;
+    m_at += k > known;
+    e_at += k == known;
+  }
+  more_before += whole >> 16;
+  equal_before += whole & 0xffffu;
   if (rank == ctas - 1)  // whose counts are of all
     for (uint32_t i = more_before + min(equal_before, wanted) + threadIdx.x; i < (uint32_t)a.count; i += kThreads) out[i] = -1;
 }
@@ -591,17 +615,17 @@ cudaError_t launch_summarise(const KvPages& cache, const Summary& summary, const
   return cudaSuccess;
 }
 
-template <int CHUNKS>
-static cudaError_t launch_select_chunks(SelectArgs a, const KvPages& cache, const Summary& summary, bool pdl,
+template <int LANES>
+static cudaError_t launch_select_lanes(SelectArgs a, const KvPages& cache, const Summary& summary, bool pdl,
                                         const DeviceInfo& dev, cudaStream_t stream) {
-  constexpr int kMostShare = 24576;  // pages a CTA: 96 KB of keys
+  constexpr int kMostShare = 24576;  // pages a CTA: 96 KB of keys, counted in 16 bits
   const int64_t heads = a.B * cache.heads;
   int ctas = 1;
   while (ctas < kMostCtas && (a.max_pages > (int64_t)ctas * kMostShare ||
-                              (a.max_pages > (int64_t)ctas * kThreads / 2 && heads * ctas * 2 <= 4 * dev.num_sms)))
+                              (a.max_pages > (int64_t)ctas * 128 && heads * ctas * 2 <= 4 * dev.num_sms)))
     ctas *= 2;
   const int share = (int)((a.max_pages + ctas - 1) / ctas);
-  const auto kernel = select_kernel<CHUNKS>;
+  const auto kernel = select_kernel<LANES>;
   static thread_local int configured_device = -1;
   if (configured_device != dev.device) {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShare * 4);
@@ -644,9 +668,9 @@ static cudaError_t launch_select_chunks(SelectArgs a, const KvPages& cache, cons
 
 cudaError_t launch_select(const SelectArgs& a, const KvPages& cache, const Summary& summary, bool pdl,
                           const DeviceInfo& dev, cudaStream_t stream) {
-  if (cache.head_dim <= 80) return launch_select_chunks<5>(a, cache, summary, pdl, dev, stream);
-  if (cache.head_dim <= 128) return launch_select_chunks<8>(a, cache, summary, pdl, dev, stream);
-  return launch_select_chunks<16>(a, cache, summary, pdl, dev, stream);
+  if (cache.head_dim <= 64) return launch_select_lanes<4>(a, cache, summary, pdl, dev, stream);
+  if (cache.head_dim <= 128) return launch_select_lanes<8>(a, cache, summary, pdl, dev, stream);
+  return launch_select_lanes<16>(a, cache, summary, pdl, dev, stream);
 }
 
 }  // namespace bitlinear
