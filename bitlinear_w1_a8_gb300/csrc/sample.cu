@@ -14,8 +14,8 @@
 //
 // Measured.  softmax: 320 rows of 50000 28.9 us, 128 MB, 4.4 TB/s (a copy's 19.1 us): rows come in four rounds of clusters,
 // each of which reads, meets once and writes; one row 3.6 us, latency.  Rows streamed through rings in shared memory under
-// resident CTAs took 43.3 where this took 33.9; five CTAs an SM 32.4 for 30.5.  verify: 64 sequences of 4 drafts over 50000 tokens 14.6 us (3.8 us of bytes): the
-// drafts' probabilities, then the two rows they point to, then the cluster's meeting, one after the other; one sequence 7.0.
+// resident CTAs took 43.3 where this took 33.9; five CTAs an SM 32.4 for 30.5.  verify: 64 sequences of 4 drafts over 50000 tokens 11.2 us (3.8 us of bytes): the
+// drafts' probabilities, then the two rows they point to, then the cluster's meeting, one after the other; one sequence 5.6.
 #include <type_traits>
 
 #include "serve.cuh"
@@ -224,10 +224,16 @@ __global__ void __launch_bounds__(THREADS) softmax_kernel(const float* __restric
 
 // ---------------------------------------------------------------- verification
 
-// A weight in units of 1 / `scale`, a power of two; what is not above 0 (NaN among it) is 0, what is above
-// 2 counts as 2.
-__device__ __forceinline__ unsigned long long units(float w, float scale) {
-  return w > 0.0f ? __float2ull_rn(fminf(w, 2.0f) * scale) : 0ull;
+// A weight in units of 2^-places (31 to 62), to the nearest, ties to even; what is not above 0 (NaN among it) is 0, what is
+// above 2 counts as 2.  By shifts: the conversion to 64 bits runs on the fp64 pipe, which it kept busy for half of the
+// kernel's time (64 sequences of 50000 tokens 14.6 us with it, 11.6 so).
+__device__ __forceinline__ unsigned long long units(float w, int places) {
+  const uint32_t u = __float_as_uint(fminf(w, 2.0f)), m = (u & 0x7fffffu) | 0x800000u;
+  const int shift = (int)(u >> 23) - 150 + places;  // the weight is m 2^(its exponent's field - 150), below 2^-126 nothing is left
+  const int down = min(31, max(1, -shift));
+  const uint32_t rounded = (m + (1u << (down - 1)) - 1u + ((m >> down) & 1u)) >> down;
+  const unsigned long long units = shift >= 0 ? (unsigned long long)m << shift : rounded;
+  return w > 0.0f ? units : 0ull;
 }
 
 struct VerifyArgs {
@@ -236,7 +242,7 @@ struct VerifyArgs {
   int32_t *tokens, *accepted;
   int64_t V;
   int K;
-  float scale;  // units of a weight of 1
+  int places;  // a weight counts in units of 2^-places
 };
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
@@ -297,7 +303,9 @@ __global__ void __launch_bounds__(kVerifyThreads, CTAS) verify_kernel(VerifyArgs
     bool take = false;
     if (drafted) {
       const float px = __ldg(a.p + (b * (K + 1) + i) * V + x), qx = __ldg(a.q + (b * K + i) * V + x);
-      take = (double)u * (double)qx < (double)px;
+      // exactly: the rounded product, and what the rounding left where that decides; in fp64 (a slow pipe) where it may not be whole
+      const float h = __fmul_rn(u, qx);
+      take = fabsf(h) >= 7.8886091e-31f && fabsf(h) < INFINITY ? h < px || (h == px && __fmaf_rn(u, qx, -h) < 0.0f) : (double)u * (double)qx < (double)px;
     }
     const uint32_t taken = __ballot_sync(kFullMask, take), drafts = __ballot_sync(kFullMask, drafted);
     const int run = taken == kFullMask ? 32 : __ffs(~taken) - 1;
@@ -323,7 +331,7 @@ __global__ void __launch_bounds__(kVerifyThreads, CTAS) verify_kernel(VerifyArgs
     }
     return w;
   };
-  auto sum_of = [&](const float4& w) { return units(w.x, a.scale) + units(w.y, a.scale) + units(w.z, a.scale) + units(w.w, a.scale); };
+  auto sum_of = [&](const float4& w) { return units(w.x, a.places) + units(w.y, a.places) + units(w.z, a.places) + units(w.w, a.places); };
   constexpr int kHeld = NV ? NV : 1;
   float4 held[kHeld];
   unsigned long long total = 0, before = 0, mine = 0;
@@ -370,7 +378,10 @@ __global__ void __launch_bounds__(kVerifyThreads, CTAS) verify_kernel(VerifyArgs
   }
   // The first token whose running sum is above floor(r * total): r in [0, 1) as a 64-bit fraction.
   const float r = fminf(fmaxf(last, 0.0f), 0.99999994f);
-  const unsigned long long goal = __umul64hi((unsigned long long)((double)r * 18446744073709551616.0), total);
+  const uint32_t r_bits = __float_as_uint(r), r_m = (r_bits & 0x7fffffu) | 0x800000u;
+  const int r_shift = (int)(r_bits >> 23) - 150 + 64;  // below 40; from -23 on nothing is left
+  const unsigned long long fraction = r_shift >= 0 ? (unsigned long long)r_m << r_shift : r_m >> min(31, -r_shift);
+  const unsigned long long goal = __umul64hi(fraction, total);
   if (total == 0 || goal < before || goal >= before + mine) return;
   // This warp's run has it.
   auto look_at = [&](const float4& w, int i) {  // the i-th four of the row, a lane each
@@ -380,7 +391,7 @@ __global__ void __launch_bounds__(kVerifyThreads, CTAS) verify_kernel(VerifyArgs
     const float x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const unsigned long long u = units(x[j], a.scale);
+      const unsigned long long u = units(x[j], a.places);
       if (upto <= goal && upto + u > goal) a.tokens[b * (K + 1) + n] = (int32_t)(4 * i + j);
       upto += u;
     }
@@ -456,8 +467,8 @@ cudaError_t launch_verify(const float* p, const float* q, const int32_t* draft, 
     ctas *= 2;
   const int64_t held = ((fours + ctas * kVerifyWarps - 1) / (ctas * kVerifyWarps) + 31) / 32;
   const bool aligned = V % 4 == 0;
-  // Seven turns take more registers than four CTAs an SM have: 8.5 us for one sequence of 50000 tokens with two and
-  // 10.2 with four, 18.7 and 16.7 for 64.
+  // Seven turns take more registers than four CTAs an SM have: 5.6 us for one sequence of 50000 tokens with two and
+  // 6.8 with four, 13.5 and 11.0 for 64.
   const bool few = B * ctas <= 2 * (int64_t)dev.num_sms;
   const auto of_turns = [&](auto turns) {
     constexpr int NV = decltype(turns)::value;
@@ -470,10 +481,9 @@ cudaError_t launch_verify(const float* p, const float* q, const int32_t* draft, 
                                   : of_turns(std::integral_constant<int, 0>());
   int bits = 62;
   while (((int64_t)1 << (62 - bits)) < V) --bits;
-  const float scale = (float)((int64_t)1 << bits);
   for (int64_t b = 0; b < B; b += kMostRows) {
     const int64_t rows = B - b < kMostRows ? B - b : kMostRows;
-    const VerifyArgs a = {p + b * (K + 1) * V, q + b * K * V, uniform + b * (K + 1), draft + b * K, tokens + b * (K + 1), accepted + b, V, K, scale};
+    const VerifyArgs a = {p + b * (K + 1) * V, q + b * K * V, uniform + b * (K + 1), draft + b * K, tokens + b * (K + 1), accepted + b, V, K, bits};
     const cudaError_t err = launch_grid(kernel, kVerifyThreads, dim3((unsigned)ctas, (unsigned)rows, 1), ctas, 0, pdl, stream, a);
     if (err != cudaSuccess) return err;
   }
