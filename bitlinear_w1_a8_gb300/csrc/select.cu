@@ -39,6 +39,18 @@ constexpr int kSumCtas = 8;  // of an SM
 constexpr int kDims = 8;    // of a thread
 constexpr int kTurns = 4;   // rows that a thread has on their way together
 
+// Two fp32 sums, or products, an instruction, each rounded as alone.
+__device__ __forceinline__ float2 plus2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z;}" : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 times2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z;}" : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 // Eight codes as fp32 values times their row's step: 8 bytes of int8 or e4m3, 16 of bf16 (no step).
 template <int FORMAT>
 using Codes = std::conditional_t<FORMAT == BITLINEAR_KV_BF16, uint4, uint2>;
@@ -55,8 +67,13 @@ __device__ __forceinline__ void widen(Codes<FORMAT> w, float step, float (&x)[kD
     // code + 128 in the mantissa of 2^23: exact, and not on the unit that converts (a quarter of the rate)
     const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
 #pragma unroll
-    for (int i = 0; i < kDims; ++i)
-      x[i] = __fmul_rn(__uint_as_float(__byte_perm(u[i / 4], 0x4b000000u, 0x7650 | i % 4)) - 8388736.0f, step);
+    for (int i = 0; i < kDims; i += 2) {
+      const float2 b = make_float2(__uint_as_float(__byte_perm(u[i / 4], 0x4b000000u, 0x7650 | i % 4)),
+                                   __uint_as_float(__byte_perm(u[i / 4], 0x4b000000u, 0x7650 | (i + 1) % 4)));
+      const float2 f = times2(plus2(b, make_float2(-8388736.0f, -8388736.0f)), make_float2(step, step));
+      x[i] = f.x;
+      x[i + 1] = f.y;
+    }
   } else {
     const uint32_t u[2] = {w.x, w.y};
 #pragma unroll
