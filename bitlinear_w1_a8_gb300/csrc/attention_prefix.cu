@@ -20,14 +20,13 @@
 // bf16); one thread that issues the products of S and one that issues those of O.  Two S and two O are in
 // flight, K and V tiles take turns in one ring, and a weight overwrites its logit's place.
 //
-// Measured: 256 q heads over 16384 tokens, 8 key heads of 128, bf16: 44.7 us, 16 tiles a CTA at ~3800 cycles each beside
-// ~12,000 to begin (q's parts, lookups, the first copies) and to hand over.  The tensor pipe is busy 46 cycles of 100 (55 on
-// an SM that has work); five MMAs a tile need ~2700.  What bounds a bf16 tile is the turning of its values to fp16 where
-// they lie (two passes of eight warps, ~3300 cycles), which a place of the ring waits for before it can be copied to again;
-// an 8-bit one the widening (64 rows over 2039 tokens, 32 heads of 80: 17.5 us, 4 tiles of ~4500 cycles).
-// Slower: four widening warps (66 us for 61); one pass that holds the values in registers (spills; 64); a thread a row
-// in the adding groups (its loops are fetched, not issued); unrolled loops (three times as long: the code is fetched as it
-// runs); an even 9 CTAs a row for 8 (64.3 for 64.7).
+// Measured: 256 q heads over 16384 tokens, 8 key heads of 128, bf16: ~42 us, 15 tiles a CTA at ~4000 cycles each beside ~17,000 to
+// the first weights' product and ~7,000 to hand over.  What bounds it: a tile's logits, weights, their product and the place
+// for the next but one's logits follow one another (1600 + 4200 + 1500 cycles), for two tiles at a time; five MMAs a tile need
+// 2700, and with what TMA, the turning of values and both operands of the MMAs read and write of shared memory it is busy
+// for ~3300.  The tensor pipe is busy 55 cycles of 100 on an SM that has work.
+// Slower: a thread a row in the adding groups (its loops are fetched, not issued); unrolled loops (three times as long: the
+// code is fetched as it runs); values turned in one pass that holds them in registers (spills).
 #include "attend.cuh"
 #include "serve.cuh"
 #include "tc_util.cuh"
@@ -49,7 +48,7 @@ constexpr int kLaunchRegisters = 72, kAddRegisters = 104, kBringRegisters = 32, 
 static_assert(512 * kAddRegisters + kBringThreads * kBringRegisters + 128 * kIssueRegisters <= kWideThreads * kLaunchRegisters,
               "more registers than were launched with would be waited for");
 
-struct Maps {  // of a bf16 cache: [page][head and token][dim], boxes of 16 tokens of 64 dims
+struct Maps {  // of a bf16 cache: [page][head and token][dim], boxes of 64 dims of a page's tokens, 128 at most
   CUtensorMap keys, values;
 };
 struct Entry {
@@ -227,7 +226,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     b = at / (uint32_t)sh.rows_a_seq;
     row = at - (uint32_t)b * sh.rows_a_seq;
     part = blockIdx.x - at * sh.splits;
-    parts = sh.splits;
+    // as few parts as leave the longest as short
+    const int steps = max(1, Span<kTile>(a.lengths[b], most, 0).steps()), each = (steps + sh.splits - 1) / sh.splits;
+    parts = (steps + each - 1) / each;
+    if (part >= parts) return;
   }
   if (warp == kIssue) tc::tmem_alloc(&st.tmem_at, 512);
   if (part == 0 && threadIdx.x == 0) sh.rows[b * sh.rows_a_seq + row] = make_int2(blockIdx.x, parts);
@@ -245,6 +247,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
     parts = min(steps, part + each);
   }
   const uint32_t begin = (uint32_t)part * kTile;
+  // the first tile's pages are on their way while the CTA meets
+  const int32_t* table = a.table + b * a.table_stride;
+  int32_t page = -1;
+  if (warp == kIssue + 2 && begin + 16 * (lane & 7) < len) page = table[(begin + 16 * (lane & 7)) >> c.page_shift];
+  if constexpr (W::kBf16) {
+    if (warp == kIssue + 3 && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &maps.values : &maps.keys) : "memory");
+  }
   const int tiles = max(0, min(parts, (int)((len + kTile - 1) / kTile)) - part);
   tc::tc_fence_before();
   __syncthreads();
@@ -692,7 +701,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       }
     } else if (warp == kIssue + 2) {
       // ----------------------------------------------------- pages
-      const int32_t* table = a.table + b * a.table_stride;
       const int64_t head_row = (int64_t)hk << c.page_shift;
       const int half = lane & 7;
 #pragma unroll 1
@@ -701,7 +709,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         const uint32_t t = begin + n * kTile + 16 * half;
         int64_t at = -1, row = 0;
         if (t < len) {
-          const int32_t page = table[t >> c.page_shift];
+          if (n > 0) page = table[t >> c.page_shift];
           if (page >= 0 && page < c.num_pages) {
             const int64_t in_page = head_row + (t & ((1u << c.page_shift) - 1)), page_row = ((int64_t)page * c.heads) << c.page_shift;
             row = page_row + in_page;
@@ -712,16 +720,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         if (lane < 8) st.entries[entry].row[half] = at;
         const uint32_t ok = __ballot_sync(kFullMask, at >= 0) & 0xffu;
         if (lane == 0) st.entry_ok[entry] = ok;
-        if (lane < 16 && at >= 0) {  // 16 tokens of a head are one run of bytes
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&st.meta_full[entry]);
+        if (n > 0 && lane < 16 && at >= 0) {  // 16 tokens of a head are one run of bytes
           const uint8_t* from = static_cast<const uint8_t*>(lane < 8 ? c.k : c.v) + row * D * W::kBytes;
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(16 * D * W::kBytes) : "memory");
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&st.meta_full[entry]);
       }
     } else {
-      // ----------------------------------------------------- copies of the cache's rows: a lane 16 tokens, or their steps
-      const int half = lane & 7;
+      // ----------------------------------------------------- copies of the cache's rows, or of their steps: a lane a page's
+      // part of the tile by TMA (16 tokens a lane: 51.9 us for 51.0 of 64 rows over 16384 tokens of 8 key heads of 128, ~110 cycles a
+      // copy, one after the other), 16 tokens by bulk copies (a page's part: 55.4 for 52.0, fp8).
+      const int half = lane & 7, run = W::kBf16 ? min(kTile, 1 << c.page_shift) : 16;
+      const bool leads = (16 * half & (run - 1)) == 0;
 #pragma unroll 1
       for (int i = 0; i < 2 * tiles; ++i) {
         int operand, n;
@@ -729,14 +740,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         const int entry = n % kEntries, stage = i % W::kStages;
         if (!operand) wait(&st.meta_full[entry], n / kEntries);
         const int64_t first = st.entries[entry].row[half];
-        const int rows = min(16, (int)(len - begin) - n * kTile - 16 * half);
+        const int rows = min(run, (int)(len - begin) - n * kTile - 16 * half);
         if constexpr (W::kBf16) {
-          // by TMA into their place as an operand, a lane 16 tokens and a panel; whole boxes, of which the tokens that
-          // are not there do not count
+          // by TMA into their place as an operand, a lane a panel of the page's; whole boxes, of which the tokens that are
+          // not there do not count
           if (i >= W::kStages) wait(&st.stage_empty[stage], i / W::kStages - 1);
           unsigned long long* bar = operand ? &st.raw_full[stage] : &st.stage_full[stage];
-          const bool copies = alive && first >= 0 && rows > 0 && lane < 8 * W::kPanels;
-          const uint32_t all = __popc(__ballot_sync(kFullMask, copies)) * 2048u;
+          const bool copies = alive && first >= 0 && rows > 0 && leads && lane < 8 * W::kPanels;
+          const uint32_t all = __popc(__ballot_sync(kFullMask, copies)) * 128u * run;
           if (!operand && lane < kBringThreads / 32 - 1) tc::mbar_arrive(bar);  // as many arrive as where warps widen
           if (lane == 31) tc::mbar_arrive_expect_tx(bar, all);
           __syncwarp();
@@ -750,8 +761,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         } else {
           const int slot = i % W::kRaws;
           if (i >= W::kRaws) wait(&st.raw_empty[slot], i / W::kRaws - 1);
-          const bool copies = alive && first >= 0 && rows > 0 && lane < (operand ? 8 : 24);  // rows; k's steps, v's steps
-          const uint32_t bytes = lane < 8 ? rows * D : 64;
+          const bool copies = alive && first >= 0 && rows > 0 && leads && lane < (operand ? 8 : 24);  // rows; k's steps, v's steps
+          const uint32_t bytes = lane < 8 ? rows * D : (rows + 15) / 16 * 64;
           const uint32_t all = __reduce_add_sync(kFullMask, copies ? bytes : 0u);
           if (lane == 0) tc::mbar_arrive_expect_tx(&st.raw_full[slot], all);
           __syncwarp();
@@ -810,8 +821,9 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, Shares sh, int64
   }
   const int sms = dev.num_sms < kSms ? dev.num_sms : kSms;
   const int64_t steps = ((a.max_pages << c.page_shift) + kTile - 1) / kTile;
-  // In proportion to the tokens where rows round up to whole CTAs well below the GPU, else as many CTAs a row as it has room for.
-  if (a.B <= kShareSeqs && rows <= sms / 3 && steps_fit(rows, steps)) {
+  // In proportion to the tokens where groups differ and rows round up to whole CTAs well below the GPU, else as many CTAs a
+  // row as there is room for.
+  if (a.B > 1 && a.B <= kShareSeqs && rows <= sms / 3 && steps_fit(rows, steps)) {
     sh.splits = 0;
     cfg.gridDim = dim3((unsigned)sms, 1, 1);
   } else {
@@ -822,7 +834,7 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, Shares sh, int64
   if constexpr (W::kBf16) {
     const cuuint64_t sizes[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.heads << c.page_shift, (cuuint64_t)c.num_pages};
     const cuuint64_t strides[2] = {sizes[0] * 2, sizes[0] * sizes[1] * 2};
-    const cuuint32_t box[3] = {64, 16, 1}, each[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(1 << c.page_shift < kTile ? 1 << c.page_shift : kTile), 1}, each[3] = {1, 1, 1};
     const EncodeTiledFn encode = encode_fn();
     for (int i = 0; i < 2; ++i)
       if (!encode || encode(i ? &maps.values : &maps.keys, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, i ? c.v : c.k, sizes, strides, box, each,

@@ -14,7 +14,7 @@
 // lookups; 64 rows behind 2039 tokens, up to 256 each of their own, 35.7 us (8.5): eight readings of the prefix out of L2
 // (21 us, instructions: the schedulers issue in 53 cycles of 100), and own tokens whose warps begin and end with each
 // row (2048 rows, 20 us alone, two thirds of it behind the first launch); 64 rows of 8 key heads of 128 behind 16384 tokens, bf16,
-// 54.0 us (12.3): 44.7 of it the tensor cores' part (attention_prefix.cu), the rest the wait for SMs, lookups and the join.
+// 51.0 us (12.3): ~42 of it the tensor cores' part (attention_prefix.cu), the rest the wait for SMs, lookups and the join.
 #include "attend.cuh"
 #include "serve.cuh"
 
