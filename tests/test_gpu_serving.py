@@ -901,3 +901,19 @@ def test_calls_at_the_same_time():
             assert torch.equal(o[0], alone[0]) and torch.equal(o[1], alone[1])
     assert torch.equal(y0, y1)
     assert bl.bitlinear_device_status() == 0
+
+
+@pytest.mark.parametrize("columns", [1, 31, 32, 33, 63, 64, 65])
+@pytest.mark.parametrize("count", [1, 32, 256, 257])
+def test_select_of_few_pages(columns, count):
+    """Both sides of the borders between what a warp ranks and what bins find, with ties, absent pages and short rows."""
+    page, D, B, rng = 16, 80, 6, np.random.default_rng(columns + count)
+    q = normal((B, 4, D), columns).numpy()
+    bounds, step = random_summary(9, 2, D, count)  # few pages that the tables repeat: ties
+    table = rng.integers(0, 9, (B, columns))
+    table[rng.random(table.shape) < 0.1] = -1
+    lengths = [columns * page, columns * page - 9, 1, 0, rng.integers(1, columns * page + 1), 10 ** 6]
+    for keep in ((0, 0), (1, 1), (3, 40)):
+        got = run_select(q, bounds, step, table, lengths, page, *keep, count)
+        for b in range(B):
+            np.testing.assert_array_equal(got[b], plain.choose(q[b], bounds, step, table[b], lengths[b], page, *keep, count), err_msg=f"{keep} {b}")
