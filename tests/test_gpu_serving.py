@@ -917,3 +917,13 @@ def test_select_of_few_pages(columns, count):
         got = run_select(q, bounds, step, table, lengths, page, *keep, count)
         for b in range(B):
             np.testing.assert_array_equal(got[b], plain.choose(q[b], bounds, step, table[b], lengths[b], page, *keep, count), err_msg=f"{keep} {b}")
+
+
+@pytest.mark.parametrize("fmt", attention_plain.FORMATS)
+@pytest.mark.parametrize("page,groups,R,D,S", [(128, 1, 40, 96, 700), (512, 2, 24, 128, 1300), (4096, 1, 70, 64, 5000), (16, 3, 50, 112, 300), (32, 60, 24, 32, 130)])
+def test_shared_on_the_tensor_cores_of_any_page_size(fmt, page, groups, R, D, S):
+    """A tile's part of a page: from 16 tokens to the whole tile; one group in equal runs, a few by their tokens, many with as many CTAs as fit."""
+    rng = np.random.default_rng(page)
+    shared = rng.integers(S // 2, S + 1, groups)
+    shared[-1] = S
+    run_shared(fmt, groups, R, 4, 2, D, shared, np.repeat(shared, R) + rng.integers(0, 20, groups * R), page, seed=page)
