@@ -12,8 +12,9 @@
 // weight counts as a whole number of 2^-s, s = 62 - ceil(log2 V), so that sums of V of them are exact
 // in 64 bits whatever their order, and the token is the first whose running sum passes r * total.
 //
-// Measured.  softmax: 320 rows of 50000 28.9 us, 128 MB, 4.4 TB/s (a copy's 19.1 us): rows come in four rounds of clusters,
-// each of which reads, meets once and writes; one row 3.6 us, latency.  Rows streamed through rings in shared memory under
+// Measured.  softmax: 320 rows of 50000 25.3 us, 128 MB, 5.1 TB/s (a copy's 19.1 us): rows come in four rounds of clusters,
+// each of which reads, meets once and writes (28.7 us while every warp told every CTA its sums: each then waits for what it
+// published); one row 3.6 us, latency.  Rows streamed through rings in shared memory under
 // resident CTAs took 43.3 where this took 33.9; five CTAs an SM 32.4 for 30.5.  verify: 64 sequences of 4 drafts over 50000 tokens 11.2 us (3.8 us of bytes): the
 // drafts' probabilities, then the two rows they point to, then the cluster's meeting, one after the other; one sequence 5.6.
 #include <type_traits>
@@ -31,6 +32,7 @@ __device__ __forceinline__ void send64(uint32_t at, int rank, unsigned long long
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(r), "l"(v) : "memory");
 }
+__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }  // publishes nothing
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ float exp2_of(float x) {
@@ -82,17 +84,30 @@ __device__ __forceinline__ unsigned long long order_key(float x, int64_t v) {
 
 constexpr int kRowThreads = 256;  // of a CTA
 
-// The cluster's exchange: every warp tells every CTA its word; `told` has room for all.
-template <int WARPS>
-__device__ __forceinline__ void tell(unsigned long long* told, unsigned long long mine, int ctas, int rank, int lane, int warp) {
-  if (ctas == 1) {
-    if (lane == 0) told[warp] = mine;
-    __syncthreads();
-  } else {
-    if (lane < ctas) send64(smem_at(told + rank * WARPS + warp), lane, mine);
-    cluster_arrive();
-    cluster_wait();
+// The cluster's exchange: a CTA's words, one a warp, are joined to one, which it tells every CTA: one warp publishes,
+// the others have nothing to.  `told` has room for WARPS + kMostCtas words; the CTAs' begin at WARPS.
+template <int WARPS, typename Join>
+__device__ __forceinline__ void tell(unsigned long long* told, unsigned long long mine, int ctas, int rank, int lane, int warp, Join join) {
+  if (lane == 0) told[warp] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    const unsigned long long all = join(told, WARPS);
+    if (ctas == 1) {
+      if (lane == 0) told[WARPS] = all;
+    } else if (lane < ctas) {
+      send64(smem_at(told + WARPS + rank), lane, all);
+    }
   }
+  if (ctas == 1) {
+    __syncthreads();
+    return;
+  }
+  __syncwarp();
+  if (warp == 0)
+    cluster_arrive();
+  else
+    cluster_begun();
+  cluster_wait();
 }
 
 // A row's probabilities from what its threads hold: `each` calls its argument with (chunk, its values) for
@@ -113,11 +128,14 @@ __device__ __forceinline__ void finish_row(const Row& r, float* out, float T, fl
     });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine = max(mine, __shfl_xor_sync(kFullMask, mine, o));
-    tell<WARPS>(told, mine, ctas, rank, lane, warp);
-    unsigned long long best = 0;
-    for (int i = lane; i < ctas * WARPS; i += 32) best = max(best, told[i]);
+    const auto largest = [&](const unsigned long long* t, int n) {
+      unsigned long long best = lane < n ? t[lane] : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(kFullMask, best, o));
+      for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(kFullMask, best, o));
+      return best;
+    };
+    tell<WARPS>(told, mine, ctas, rank, lane, warp, largest);
+    const unsigned long long best = largest(told + WARPS, ctas);
     const int64_t at = best ? (int64_t)(uint32_t)~(uint32_t)best : -1;
     each([&](int i, float4&) {
       const int64_t d = at < 0 ? -1 : at - (4 * (int64_t)i - r.shift);
@@ -138,16 +156,20 @@ __device__ __forceinline__ void finish_row(const Row& r, float* out, float T, fl
   });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
-  tell<WARPS>(told, packed(m, s), ctas, rank, lane, warp);
-  float M = -INFINITY, S = 0.0f;
-  for (int i = lane; i < ctas * WARPS; i += 32) M = fmaxf(M, __uint_as_float((uint32_t)(told[i] >> 32)));
+  const auto joined = [&](const unsigned long long* t, int n) {
+    const unsigned long long word = lane < n ? t[lane] : packed(-INFINITY, 0.0f);
+    const float of = __uint_as_float((uint32_t)(word >> 32));
+    float most = of;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-  const float top = M == -INFINITY ? 0.0f : M;
-  for (int i = lane; i < ctas * WARPS; i += 32)
-    S += __uint_as_float((uint32_t)told[i]) * exp2_of((__uint_as_float((uint32_t)(told[i] >> 32)) - top) * c);
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFullMask, most, o));
+    float sum = __uint_as_float((uint32_t)word) * exp2_of((of - (most == -INFINITY ? 0.0f : most)) * c);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(kFullMask, S, o);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
+    return packed(most, sum);
+  };
+  tell<WARPS>(told, packed(m, s), ctas, rank, lane, warp, joined);
+  const unsigned long long row = joined(told + WARPS, ctas);
+  const float M = __uint_as_float((uint32_t)(row >> 32)), S = __uint_as_float((uint32_t)row), top = M == -INFINITY ? 0.0f : M;
   const float inverse = S == 0.0f ? 0.0f : 1.0f / S;
   const float f = AGAIN ? inverse : exp2_of((m - top) * c) * inverse;
   each([&](int i, float4& v) {
@@ -169,16 +191,16 @@ __device__ __forceinline__ float largest_of(float m, const float4& v) { return f
 
 // A row a cluster.  A CTA keeps its share of the row in registers, NV chunks a thread; NV == 0: any number of
 // them, read a second and a third time.  ALIGNED: V is a multiple of four, so that every chunk is whole (320 rows of
-// 50000 28.6 us with it, 31.8 without; 50001 31.7).  Every warp sums under a maximum of its own and tells it to every CTA, so
+// 50000 25.3 us with it; 50001 27.4).  Every warp sums under a maximum of its own, so
 // the cluster meets once.
 template <int THREADS, int NV, bool ALIGNED>
 __global__ void __launch_bounds__(THREADS) softmax_kernel(const float* __restrict__ y, float* __restrict__ p,
                                                           const float* __restrict__ temperature, int64_t V) {
   constexpr int kWarps = THREADS / 32;
-  __shared__ unsigned long long told[kMostCtas * kWarps];
+  __shared__ unsigned long long told[kWarps + kMostCtas];
   const int ctas = gridDim.x, rank = blockIdx.x;
   pdl_release_dependents();
-  if (ctas > 1) cluster_arrive();  // waited for before the first word goes to another CTA
+  if (ctas > 1) cluster_begun();  // waited for before the first word goes to another CTA
   pdl_wait_primary();
   const int64_t m_row = blockIdx.y;
   const float* in = y + m_row * V;
@@ -285,7 +307,7 @@ __global__ void __launch_bounds__(kVerifyThreads, CTAS) verify_kernel(VerifyArgs
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ctas = gridDim.x, rank = blockIdx.x;
   pdl_release_dependents();
-  if (ctas > 1) cluster_arrive();  // waited for before the first word goes to another CTA
+  if (ctas > 1) cluster_begun();  // waited for before the first word goes to another CTA
   pdl_wait_primary();
   const int64_t b = blockIdx.y;
   const int K = a.K;

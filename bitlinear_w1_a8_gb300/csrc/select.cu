@@ -217,6 +217,7 @@ __device__ __forceinline__ void send32(uint32_t at, int rank, uint32_t v) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(r), "r"(v) : "memory");
 }
+__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }  // publishes nothing
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_meet() {
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, KvPages 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int ctas = gridDim.x, rank = blockIdx.x;
   pdl_release_dependents();
-  if (!FEW && ctas > 1) cluster_arrive();  // waited for before the first word goes to another CTA
+  if (!FEW && ctas > 1) cluster_begun();  // waited for before the first word goes to another CTA
   pdl_wait_primary();
   const int64_t b = (int64_t)blockIdx.z, hk = blockIdx.y;
   const int D = c.head_dim, chunks = D / 16, group = a.q_heads / c.heads;
