@@ -363,8 +363,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       if (none) {
         if (lane == 0) tc::mbar_arrive(&st.p_full[par]);
         tc::named_bar_sync(1 + par, 256);
-        if (lane == 0) tc::mbar_arrive(&st.meta_empty[entry]);
         wait(&st.o_full[par], n >> 1);
+        if (lane == 0) tc::mbar_arrive(&st.meta_empty[entry]);
         continue;
       }
       tc::tc_fence_after();
@@ -457,18 +457,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
       tc::tmem_st_wait();
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(&st.p_full[par]);
-        if (!W::kBf16) tc::mbar_arrive(&st.meta_empty[entry]);
-      }
+      if (lane == 0) tc::mbar_arrive(&st.p_full[par]);
       sums = add2(sums, more);
       wait(&st.o_full[par], n >> 1);
       float2 v_unit = both(1.0f);
       if constexpr (W::kBf16) {  // the values' power of two
         v_unit = both(st.v_most[entry][0]);
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&st.meta_empty[entry]);
       }
+      // Not before O: the weights wait for keys alone, and the copies and the laying out of the tile's values read its entry
+      // too.  O shows that they have.
+      if (lane == 0) tc::mbar_arrive(&st.meta_empty[entry]);
       tc::tc_fence_after();
 #pragma unroll
       for (int d = 0; d < kDims; d += 16) {  // 8 or 16 dims
