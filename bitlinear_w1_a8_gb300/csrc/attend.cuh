@@ -25,7 +25,6 @@ constexpr int kPortableCluster = 8;
 constexpr int kSms = 152;
 constexpr int kOtherSmem = 1024 + 640;  // of a CTA, beside the dynamic: the system's and the static arrays
 constexpr int kLeastSteps = 2;    // steps a warp at least: short rows take fewer CTAs
-constexpr int kShareSeqs = 1024;  // sequences that a CTA adds up to find its row
 constexpr int kSortSeqs = kThreads;  // sequences that a CTA ranks by length
 constexpr float kLimit = 256.0f;  // the largest weight before the reference moves
 constexpr float kUnset = -1e30f;  // a reference below every logit

@@ -36,7 +36,7 @@ namespace bitlinear {
 namespace {
 
 constexpr int kRows = kPrefixWide;      // q heads of a CTA: the MMA's rows
-constexpr int kTile = 128;              // tokens
+constexpr int kTile = kPrefixTile;      // tokens
 constexpr int kWideThreads = 896;
 constexpr int kBring = 16, kIssue = 24;  // the first warps that bring keys and values, and that issue
 constexpr int kBringThreads = 256;
@@ -820,15 +820,8 @@ cudaError_t launch_shape(const AttendArgs& a, const KvPages& c, Shares sh, int64
   }
   const int sms = dev.num_sms < kSms ? dev.num_sms : kSms;
   const int64_t steps = ((a.max_pages << c.page_shift) + kTile - 1) / kTile;
-  // In proportion to the tokens where groups differ and rows round up to whole CTAs well below the GPU, else as many CTAs a
-  // row as there is room for.
-  if (a.B > 1 && a.B <= kShareSeqs && rows <= sms / 3 && steps_fit(rows, steps)) {
-    sh.splits = 0;
-    cfg.gridDim = dim3((unsigned)sms, 1, 1);
-  } else {
-    sh.splits = rows < sms ? (int)(sms / rows) : 1;
-    cfg.gridDim = dim3((unsigned)(rows * sh.splits), 1, 1);
-  }
+  sh.splits = wide_splits(a.B, rows, steps, sms);
+  cfg.gridDim = dim3((unsigned)(sh.splits ? rows * sh.splits : sms), 1, 1);
   Maps maps = {};
   if constexpr (W::kBf16) {
     const cuuint64_t sizes[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.heads << c.page_shift, (cuuint64_t)c.num_pages};

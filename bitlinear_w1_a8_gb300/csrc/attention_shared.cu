@@ -47,23 +47,6 @@ size_t workspace_of(const Sizes& s, int head_dim) {
   return (size_t)s.slots * s.heads * (head_dim + 4) * sizeof(float) + (size_t)s.rows * sizeof(int2);
 }
 
-// The tensor cores take 128 q heads of a key head in the time of 32, and ~8 us more to begin and to end.
-// us, eight a CTA / 128 on the tensor cores, one group, up to 64 tokens of each row's own:
-//   q heads a key head           24             32             48             64             96             128
-//   int8, 32 heads of 80   512   11.8 / 16.9    12.3 / 16.9    16.7 / 24.1    17.3 / 24.8    23.6 / 28.5    29.2 / 33.1
-//                         2048   18.1 / 27.8    20.0 / 28.2    23.7 / 29.2    27.2 / 29.5    41.0 / 35.3    49.9 / 39.8
-//                         8192   30.2 / 50.4    38.4 / 50.7    52.2 / 53.3    69.5 / 54.1   108.7 / 59.2   136.4 / 66.4
-//                        32768   89.1 / 142.2  125.5 / 142.5  166.4 / 153.1  241.9 / 154.1  377.5 / 159.6  479.9 / 173.2
-//   bf16, 8 of 128         512   15.7 / 21.0    14.9 / 18.6    16.7 / 21.3    17.3 / 19.5    18.6 / 22.0    17.3 / 19.6
-//                         2048   17.8 / 24.4    18.3 / 21.0    20.8 / 22.0    21.3 / 22.2    26.3 / 23.1    27.8 / 22.7
-//                         8192   25.3 / 29.5    26.8 / 26.8    35.0 / 27.8    40.0 / 28.2    58.9 / 29.2    71.2 / 28.9
-//                        32768   55.5 / 56.3    65.4 / 50.9    94.1 / 52.4   115.2 / 52.1   189.6 / 53.4   245.6 / 53.1
-// Tokens are those that the table has room for.
-bool wide_wins(const AttendArgs& a, const KvPages& c, int64_t groups) {
-  const int64_t heads = a.B / groups * (a.q_heads / c.heads), tokens = a.max_pages << c.page_shift;
-  return c.head_dim <= 128 && heads >= (c.format == BITLINEAR_KV_BF16 ? 28 : 40) + 65536 / tokens;
-}
-
 constexpr int64_t kPackedRows = 300;  // a row a key head of a sequence: from so many on they fill the GPU without clusters
 
 template <int FORMAT, int DT>
@@ -80,7 +63,7 @@ cudaError_t launch_shape(AttendArgs a, const KvPages& c, const int32_t* shared, 
     if (err != cudaSuccess) return err;
     configured_device = dev.device;
   }
-  const bool wide = wide_wins(a, c, groups);
+  const bool wide = wide_wins(a.B / groups * (a.q_heads / c.heads), a.max_pages << c.page_shift, c.head_dim, S::kBytes);
   const Sizes sizes = sizes_of(a.B, a.q_heads, c.heads, groups, wide);
   const int64_t steps = ((a.max_pages << c.page_shift) + S::kTokens - 1) / S::kTokens;
 
@@ -166,25 +149,11 @@ size_t attention_shared_workspace_bytes(int64_t B, int q_heads, int kv_heads, in
   return need > alone ? need : alone;
 }
 
-// Whether attention that reads a group's tokens again for each of its rows is faster: it is one launch, and the
-// second reading is of L2.  By the bytes that all rows read at most, the table's columns filled; us, shared / alone, one
-// group, up to 64 tokens of each row's own:
-//   32 heads of 80, int8, 24 rows x  512 tokens (63 MB) 11.8 / 20.0    16 heads of 128, int8, 24 x  512 (50 MB) 12.5 / 13.9
-//   8 of 128 under 32 q heads, fp8, 16 x 2048 (67 MB) 20.2 / 16.3      24 x 2048 (100 MB) 21.7 / 21.7
-//   the same, bf16, 8 x 2048 (67 MB) 18.3 / 14.5                       16 x 2048 (134 MB) 21.3 / 22.7
-// and of 2 rows of 38 tokens, 16 heads of 128 dims: 8.7 / 3.1.
-constexpr double kAloneBytes = 36e6;  // for each of the q heads of a key head, up to three
-bool faster_alone(const AttendArgs& a, const KvPages& c) {
-  const double code = c.format == BITLINEAR_KV_BF16 ? 2 : 1;
-  const double bytes = (double)a.B * (double)a.max_pages * (double)(1 << c.page_shift) * c.heads * c.head_dim * 2 * code;
-  const int group = a.q_heads / c.heads;
-  return bytes <= kAloneBytes * (group < 3 ? group : 3);
-}
-
 cudaError_t launch_attention_shared(const AttendArgs& a, const KvPages& cache, const int32_t* shared, int64_t groups,
                                     void* workspace, bool pdl, const DeviceInfo& dev, cudaStream_t stream) {
   // Nothing is shared, or too little.
-  if (groups == a.B || faster_alone(a, cache))
+  if (groups == a.B || faster_alone(a.B, a.max_pages << cache.page_shift, cache.heads, cache.head_dim,
+                                    cache.format == BITLINEAR_KV_BF16 ? 2 : 1, a.q_heads / cache.heads))
     return launch_attention(a, cache, workspace, pdl, dev, stream);
   return of_shape(cache, [&](auto format, auto dims) {
     return launch_shape<decltype(format)::value, decltype(dims)::value>(a, cache, shared, groups, workspace, pdl, dev, stream);

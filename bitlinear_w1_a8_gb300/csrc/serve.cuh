@@ -41,8 +41,7 @@ cudaError_t launch_select(const SelectArgs& a, const KvPages& cache, const Summa
 cudaError_t launch_attention_blocks(const AttendArgs& a, const KvPages& cache, const int32_t* blocks, int count, bool pdl,
                                     const DeviceInfo& dev, cudaStream_t stream);
 
-// attention_prefix.cu: the shared tokens of groups (a.B of them, a.lengths tokens each) for 128 q heads a CTA.
-constexpr int kPrefixWide = 128;
+// attention_prefix.cu: the shared tokens of groups (a.B of them, a.lengths tokens each) for kPrefixWide q heads a CTA.
 struct PrefixRows {
   int group, tiles;             // q heads of a group for a key head, in tiles of 128
   int group_rows, heads_a_key;  // its sequences, and their q heads a key head
