@@ -121,7 +121,9 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) summarise_kernel(Summar
   const int row = threadIdx.x / chunks, chunk = threadIdx.x - row * chunks;
   const int page_size = 1 << c.page_shift;
   const int64_t length = max((int64_t)0, min((int64_t)a.lengths[b], a.max_pages << c.page_shift));
-  const int begin = (max(0, a.first[b]) >> c.page_shift) + blockIdx.x, end = (int)((length + page_size - 1) >> c.page_shift);
+  const int first = max(0, a.first[b]);
+  // no page of a range of no token, not the one that both ends lie in either
+  const int begin = (first >> c.page_shift) + blockIdx.x, end = first < length ? (int)((length + page_size - 1) >> c.page_shift) : 0;
   const int32_t* table = a.table + b * a.table_stride;
   int32_t next = begin < end ? table[begin] : -1;
   for (int column = begin; column < end; column += a.shares) {

@@ -567,7 +567,7 @@ typedef struct bitlinear_kv_summary {
 } bitlinear_kv_summary;
 
 /* Writes the summaries of the pages that hold the tokens first[b] <= t < lengths[b] of B sequences:
- * first 0 for a prompt, lengths - 1 for the token that a decode step has just appended.
+ * first 0 for a prompt, lengths - 1 for the token that a decode step has just appended, lengths or more for none.
  * With lo_d and hi_d the least and largest of dim d over the page's tokens before lengths[b] (each the fp32
  * product code * step of the cache): a = max(max_d |lo_d|, max_d |hi_d|, 1e-5), s = 127 / a, step = a / 127,
  *   lower_d = max(floor(lo_d * s), -127), upper_d = min(ceil(hi_d * s), 127), every step in fp32.
