@@ -840,6 +840,11 @@ def _blocks(blocks, B, pages, at):
     return blocks.shape[2]
 
 
+def _as_int(n) -> int:
+    """n as a C int takes it: what is beyond 32 bits is the nearest inside, not its last 32 bits."""
+    return max(-2 ** 31, min(2 ** 31 - 1, int(n)))
+
+
 def bitlinear_attention_select(q, cache, summary, page_table, lengths, blocks, keep_first: int = 1, keep_last: int = 1,
                                flags: int = 0, stream=None):
     """blocks [B, heads, count] (int32) = the pages (columns of the page table) of the largest scores for
@@ -862,8 +867,8 @@ def bitlinear_attention_select(q, cache, summary, page_table, lengths, blocks, k
     count = _blocks(blocks, shape[0], pages, at)
     _check(load_library().bitlinear_attention_select(
         q.data_ptr(), q_stride, shape[0], shape[1], pages, _kv_summary(summary, pages, at), page_table.data_ptr(), table_stride,
-        max_pages, lengths.data_ptr(), int(keep_first), int(keep_last), blocks.data_ptr(), count, flags, _stream(stream)),
-        "bitlinear_attention_select")
+        max_pages, lengths.data_ptr(), _as_int(keep_first), _as_int(keep_last), blocks.data_ptr(), _as_int(count), flags,
+        _stream(stream)), "bitlinear_attention_select")
 
 
 def bitlinear_attention_blocks(q, cache, page_table, lengths, blocks, out, scale: float | None = None, flags: int = 0, stream=None):
@@ -878,7 +883,7 @@ def bitlinear_attention_blocks(q, cache, page_table, lengths, blocks, out, scale
     at, pages, tensors, written = _attention_tensors(q, cache, page_table, lengths, out)
     count = _blocks(blocks, q.shape[0], pages, at)
     _check(load_library().bitlinear_attention_blocks(
-        *tensors, blocks.data_ptr(), count, pages.head_dim ** -0.5 if scale is None else scale, *written, flags,
+        *tensors, blocks.data_ptr(), _as_int(count), pages.head_dim ** -0.5 if scale is None else scale, *written, flags,
         _stream(stream)), "bitlinear_attention_blocks")
 
 
@@ -925,6 +930,6 @@ def bitlinear_verify(p, q, draft, uniform, tokens, accepted, flags: int = 0, str
     _need_on(uniform, at, f32, "uniform", (B, K + 1))
     _need_on(tokens, at, i32, "tokens", (B, K + 1))
     _need_on(accepted, at, i32, "accepted", (B,))
-    _check(load_library().bitlinear_verify(p.data_ptr(), _ptr(q) if K else None, B, K, N, _ptr(draft) if K else None,
+    _check(load_library().bitlinear_verify(p.data_ptr(), _ptr(q) if K else None, B, _as_int(K), N, _ptr(draft) if K else None,
                                            uniform.data_ptr(), tokens.data_ptr(), accepted.data_ptr(), flags,
                                            _stream(stream)), "bitlinear_verify")

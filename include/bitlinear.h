@@ -588,7 +588,8 @@ bitlinear_status bitlinear_kv_summarise(const bitlinear_kv_pages* cache, const b
  * head's score is the largest of its q heads'.
  *   cache      gives num_pages, num_heads, page_size and head_dim; its pointers are checked, its
  *              codes not read.
- *   keep_first, keep_last  pages at the sequence's start and end that are chosen whatever their score, >= 0.
+ *   keep_first, keep_last  pages at the sequence's start and end that are chosen whatever their score, >= 0; the
+ *              earliest of them where they are more than count.
  *   blocks     device int32 [B, num_heads, count], written: the columns of the page table that are chosen, in
  *              order, then -1.  A page whose number is out of range is not chosen; of equal scores the
  *              earlier page is; a score that is NaN comes last.
