@@ -3,8 +3,10 @@ import numpy as np
 import pytest
 import torch
 
+import attention_plain
 import bitlinear_w1_a8_gb300 as bl
-from test_gpu_serving import filled_cache, ints, new_summary, normal, random_summary
+from serving_ways import way
+from test_gpu_serving import filled_cache, ints, new_summary, normal, random_summary, shared_case, wide_table
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +55,37 @@ def test_kept_pages_beyond_32_bits(compiled, monkeypatch):
         for keep in (dict(keep_first=-many), dict(keep_last=-many)):
             with pytest.raises(bl.BitLinearError):
                 run(**keep)
+
+
+# ------------------------------------------------------------------ a row's own tokens
+
+
+@pytest.mark.parametrize("fmt", attention_plain.FORMATS)
+@pytest.mark.parametrize("R,G,want", [(4, 1, "eight"), (24, 4, "wide"), (160, 1, "wide"), (39, 8, "wide"), (20, 1, "eight"), (150, 1, "wide")])
+def test_a_number_that_is_not_finite_stays_with_its_row(fmt, R, G, want):
+    """A NaN in one row's own token, in a page of its own: that row's heads of that key head alone, over clusters and in packed rows."""
+    S, page, D, Hkv = 90, 16, 64, 2
+    lengths = S + 25 + np.arange(R) % 11
+    cache, q, table = shared_case(fmt, 1, R, Hkv * G, Hkv, D, [S], lengths, page, 31)
+    columns = wide_table(table, cache)
+    assert way(fmt, 1, R, Hkv * G, Hkv, D, columns.shape[1], page) == want
+    out = torch.empty(q.shape, device="cuda")
+    ws = torch.empty(bl.bitlinear_attention_shared_workspace(R, Hkv * G, Hkv, D, 1), dtype=torch.uint8, device="cuda")
+    run = lambda: (bl.bitlinear_attention_shared(q.cuda(), cache, columns, ints(lengths), ints([S]), out, ws), out.cpu())[1]  # noqa: E731
+    clean = run()
+    assert torch.isfinite(clean).all()
+    row = R // 2 + 1
+    t = int(lengths[row]) - 1
+    at = table[row, t // page]
+    assert t >= S and (table[:, t // page] == at).sum() == 1  # this row's alone
+    rest = torch.ones(R, dtype=torch.bool)
+    rest[row] = False
+    for i in (0, 1):  # keys, then values
+        held = cache[i] if fmt == "bf16" else cache[2 + i]
+        kept = held[at, 0, t % page].clone()
+        held[at, 0, t % page] = float("nan")
+        got = run()
+        assert torch.isnan(got[row, :G]).all()
+        assert torch.equal(got[rest], clean[rest]) and torch.equal(got[row, G:], clean[row, G:])
+        held[at, 0, t % page] = kept
+    assert torch.equal(run(), clean)
