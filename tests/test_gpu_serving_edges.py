@@ -5,8 +5,10 @@ import torch
 
 import attention_plain
 import bitlinear_w1_a8_gb300 as bl
+import serving_plain as plain
+from harness import check_canary, guarded
 from serving_ways import way
-from test_gpu_serving import filled_cache, ints, new_summary, normal, random_summary, shared_case, wide_table
+from test_gpu_serving import filled_cache, ints, new_summary, normal, random_summary, shared_case, wide_table, within
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +91,49 @@ def test_a_number_that_is_not_finite_stays_with_its_row(fmt, R, G, want):
         assert torch.equal(got[rest], clean[rest]) and torch.equal(got[row, G:], clean[row, G:])
         held[at, 0, t % page] = kept
     assert torch.equal(run(), clean)
+
+
+# ------------------------------------------------------------------ probabilities
+
+
+TEMPERATURES = [1.0, 0.3, 7.0, 0.0, 1e-20, 2e30, float("nan"), -1.0, float("inf")]
+
+
+@pytest.mark.parametrize("V", [3, 129, 1000, 2000, 4099, 7171, 14000, 50001, 57348, 65536, 65537, 131075, 300008])
+def test_softmax_of_every_temperature(V):
+    """Each way of a row (held by one CTA, by up to eight, read again), at every kind of temperature, out of place and in place: maxima
+    in the first and the last run, equal ones in two of them, a masked end, logits far apart."""
+    M = len(TEMPERATURES)
+    y = normal((M, V), V, 3.0)
+    y[:, V - 1] = y[:, V // 3] = 40.0       # the largest in two CTAs; where one is chosen it is the earlier
+    y[0, V // 2] = -np.inf
+    y[4, V // 3] = 39.0                     # and in the last alone
+    y[5] *= 1e30                            # of 1e30, which the temperature counts as, and not of 2e30
+    y[8] *= 1e30
+    t = torch.tensor(TEMPERATURES)
+    p, full = guarded(M * V, torch.float32, 4.5)
+    p = p.view(M, V)
+    bl.bitlinear_softmax(y.cuda(), p, t.cuda())
+    want, bound = plain.softmax(y.numpy(), t.numpy())
+    within(p, want, bound)
+    check_canary(full, 4.5)
+    for m in (3, 4, 6, 7):
+        assert p[m].sum() == 1 and p[m].argmax().item() == (V - 1 if m == 4 else V // 3)
+    both, full = guarded(M * V, torch.float32, 4.5)
+    both = both.view(M, V)
+    both.copy_(y)
+    bl.bitlinear_softmax(both, both, t.cuda())
+    assert torch.equal(both, p)
+    check_canary(full, 4.5)
+
+
+@pytest.mark.parametrize("M,V", [(320, 129), (700, 1003), (320, 4096), (64, 65536), (33, 100003)])
+def test_softmax_in_place_of_many_rows(M, V):
+    """p is y: what another buffer gets, and the same in every call."""
+    y, t = normal((M, V), M, 3.0).cuda(), (torch.arange(M) % 5 * 0.4).cuda()
+    p = torch.empty_like(y)
+    bl.bitlinear_softmax(y, p, t)
+    for _ in range(3):
+        x = y.clone()
+        bl.bitlinear_softmax(x, x, t)
+        assert torch.equal(x, p)
