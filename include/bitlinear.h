@@ -584,8 +584,9 @@ bitlinear_status bitlinear_kv_summarise(const bitlinear_kv_pages* cache, const b
 /* Chooses pages of each sequence for each key head by a cheap score.  With c = q's codes, as
  * bitlinear_quant_act takes them (c_d = rne(q_d * (127 / m)), m = max(max|q|, 1e-5)), the score of page j for a q head is
  *   (acc * step_j) * (m / 127),  acc = sum_d max(c_d lower_d, c_d upper_d) (exact),
- * two fp32 products: no key of the page has a larger product with those codes (for scale > 0).  A key
- * head's score is the largest of its q heads'.
+ * two fp32 products: no key of the page has a larger product with those codes (for scale > 0), but for the roundings of the
+ * bounds, the step and the score, which may leave it short by 2^-21 * m * step_j * sum_d |c_d|.  A key head's score is the
+ * largest of its q heads'.
  *   cache      gives num_pages, num_heads, page_size and head_dim; its pointers are checked, its
  *              codes not read.
  *   keep_first, keep_last  pages at the sequence's start and end that are chosen whatever their score, >= 0; the
