@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "serve.cuh"
+#include "shares.h"
 
 namespace bitlinear {
 namespace {
@@ -628,9 +629,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, KvPages 
 cudaError_t launch_summarise(const KvPages& cache, const Summary& summary, const int32_t* table, int64_t table_stride,
                              int64_t B, int64_t max_pages, const int32_t* first, const int32_t* lengths, bool pdl,
                              const DeviceInfo& dev, cudaStream_t stream) {
-  // As many CTAs as are resident together, in equal rounds of pages.
-  const int64_t resident = (int64_t)dev.num_sms * kSumCtas, heads = B * cache.heads;
-  const int64_t rounds = (max_pages * heads + resident - 1) / resident, shares = (max_pages + rounds - 1) / rounds;
+  const int64_t shares = page_shares(max_pages, B * cache.heads, (int64_t)dev.num_sms * kSumCtas);
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;

@@ -1,6 +1,6 @@
 // shares.h -- the arithmetic by which attention.cu shares rows out over CTAs in proportion
-// to their steps, and by which attention_shared.cu and attention_prefix.cu choose their way and their
-// CTAs.  Plain functions of numbers, for the host, the device and tests.
+// to their steps, and by which attention_shared.cu, attention_prefix.cu and select.cu choose their way and
+// their CTAs.  Plain functions of numbers, for the host, the device and tests.
 #pragma once
 
 #include <stdint.h>
@@ -63,6 +63,14 @@ inline bool wide_wins(int64_t heads, int64_t tokens, int head_dim, int code_byte
 inline int wide_splits(int64_t groups, int64_t rows, int64_t steps, int sms) {
   if (groups > 1 && groups <= kShareSeqs && rows <= sms / 3 && steps_fit(rows, steps)) return 0;
   return rows < sms ? (int)(sms / rows) : 1;
+}
+
+// CTAs that share the pages of each of `heads` key heads (of all sequences): as many as are resident together, in equal
+// rounds of pages.  max_pages <= 2^30 and heads <= 2^42, whose product does not fit.
+inline int64_t page_shares(int64_t max_pages, int64_t heads, int64_t resident) {
+  if (heads >= resident) return 1;
+  const int64_t rounds = (max_pages * heads + resident - 1) / resident;
+  return (max_pages + rounds - 1) / rounds;
 }
 
 }  // namespace bitlinear

@@ -15,6 +15,7 @@ int alone(int64_t B, int64_t tokens, int kv_heads, int head_dim, int code, int h
 int wide(int64_t heads, int64_t tokens, int head_dim, int code) { return wide_wins(heads, tokens, head_dim, code); }
 int splits(int64_t groups, int64_t rows, int64_t steps, int sms) { return wide_splits(groups, rows, steps, sms); }
 int share(int total, int spare, int least) { return share_of_steps(total, spare, least); }
+int64_t pages(int64_t max_pages, int64_t heads, int64_t resident) { return page_shares(max_pages, heads, resident); }
 int q_heads() { return kPrefixWide; }
 int tile() { return kPrefixTile; }
 }
@@ -31,6 +32,7 @@ def rules():
         lib = ctypes.CDLL(lib)
     i64, i = ctypes.c_int64, ctypes.c_int
     lib.alone.argtypes, lib.wide.argtypes, lib.splits.argtypes = [i64, i64, i, i, i, i], [i64, i64, i, i], [i64, i64, i64, i]
+    lib.pages.argtypes, lib.pages.restype = [i64, i64, i64], i64
     return lib
 
 

@@ -1,4 +1,6 @@
 """The rules by which attention of rows that share a prefix chooses its way and its CTAs (csrc/shares.h, compiled here)."""
+import random
+
 import pytest
 
 from serving_ways import SMS, rules, way, wide_tiles
@@ -29,3 +31,14 @@ def test_parts_have_their_places(sms):
                     assert groups > 1 and rows < sms and rows * steps < 1 << 31
                 else:
                     assert rows * splits <= max(rows, sms) <= max(rows, SMS)
+
+
+def test_summaries_are_shared_out_up_to_the_largest_sizes():
+    """Equal rounds of resident CTAs; sizes whose product passes 64 bits (one page list for all rows) as well."""
+    rng = random.Random(1)
+    sizes = [(1 << 30, 1 << 34), (1 << 30, 1 << 42), (1 << 30, 1), (1, 1 << 42), (1, 1), (1 << 30, 1215), (1 << 30, 1216)]
+    sizes += [(int(2 ** rng.uniform(0, 30)), int(2 ** rng.uniform(0, 42))) for _ in range(2000)]
+    for pages, heads in sizes:
+        for resident in (1216, 1184, 128):
+            rounds = -(-pages * heads // resident)
+            assert rules().pages(pages, heads, resident) == -(-pages // rounds), (pages, heads, resident)
