@@ -752,8 +752,9 @@ bitlinear_status bitlinear_attention_shared(const float* q, int64_t q_stride, in
   bitlinear_status st = check_attention(q, q_stride, B, num_q_heads, cache, page_table, table_stride, max_pages, lengths,
                                         scale, out, out_stride, flags, &c);
   if (st != BITLINEAR_OK) return st;
-  if (num_groups < 1 || B % num_groups != 0 || B * num_q_heads > 0x7fffffffLL) return BITLINEAR_ERR_SHAPE;
+  if (num_groups < 0 || B * num_q_heads > 0x7fffffffLL) return BITLINEAR_ERR_SHAPE;
   if (B == 0) return BITLINEAR_OK;
+  if (num_groups == 0 || B % num_groups != 0) return BITLINEAR_ERR_SHAPE;
   if (!shared) return BITLINEAR_ERR_NULL;
   if (!aligned_to(shared, 4)) return BITLINEAR_ERR_ALIGN;
   const size_t need = attention_shared_workspace_bytes(B, num_q_heads, c.heads, c.head_dim, num_groups);

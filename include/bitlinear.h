@@ -545,7 +545,7 @@ size_t bitlinear_attention_shared_workspace(int64_t B, int num_q_heads, int num_
  *   shared     device int32 [num_groups]; 0 or below: none.  A row shorter than that attends to its
  *              own lengths[b] tokens alone, so the rows of drafted tokens (lengths n + 1, n + 2, ...,
  *              one page list) may share everything: shared[g] the longest.
- *   num_groups a divisor of B.  B * num_q_heads < 2^31.
+ *   num_groups a divisor of B (any number, 0 too, where B is 0).  B * num_q_heads < 2^31.
  *   workspace  as for bitlinear_attention, at least bitlinear_attention_shared_workspace() bytes; NULL
  *              only where that is 0 or num_groups == B.
  * Every other argument, and results, as for bitlinear_attention, but that a NaN or an infinity in a shared
