@@ -623,7 +623,9 @@ bitlinear_status bitlinear_attention_blocks(const float* q, int64_t q_stride, in
  *   temperature  device fp32 [M], or NULL (1 everywhere).  One that is not at least 1e-30 (0, for instance) gives 1 at
  *                the row's first maximum (bitlinear_argmax's) and 0 elsewhere; one above 1e30 counts as that.
  * A logit of -infinity has no probability; a row of them is a row of zeros.  With a temperature that is at
- * least 1e-30, a NaN or +infinity in a row gives a row of NaN.
+ * least 1e-30, a NaN or +infinity in a row gives a row of NaN.  With z = (y[m, n] - max) / T_m, the exponentials' arguments
+ * are rounded to fp32 and what is below 2^-126 of the largest is 0: a probability is off by at most
+ * 1.01 * 2^-24 * (12 |z| + 12 sum(p |z|) + 116 + N / 2^14) of itself, and 2^-125.
  * Errors: BITLINEAR_ERR_NULL, BITLINEAR_ERR_SHAPE, BITLINEAR_ERR_ALIGN (y, p 16 bytes, temperature 4),
  * BITLINEAR_ERR_UNSUPPORTED (flag), BITLINEAR_ERR_CUDA. */
 bitlinear_status bitlinear_softmax(const float* y, int64_t M, int64_t N, const float* temperature, float* p, int flags,

@@ -137,3 +137,27 @@ def test_softmax_in_place_of_many_rows(M, V):
         x = y.clone()
         bl.bitlinear_softmax(x, x, t)
         assert torch.equal(x, p)
+
+
+# ------------------------------------------------------------------ nothing to do
+
+
+@pytest.mark.parametrize("compiled", [True, False])
+def test_a_batch_without_rows(compiled, monkeypatch):
+    """Every call of a step takes an empty batch: no groups, no rows, no sequences."""
+    if not compiled:
+        monkeypatch.setattr(bl, "_marshal", None)
+    cache = tuple(torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    summary, none = new_summary(cache), torch.empty(0, dtype=torch.int32, device="cuda")
+    x, table = torch.empty(0, 4, 64, device="cuda"), none.view(0, 1).expand(0, 3)
+    blocks = torch.empty(0, 2, 5, dtype=torch.int32, device="cuda")
+    bl.bitlinear_attention_shared(x, cache, table, none, none, x.clone())
+    bl.bitlinear_kv_summarise(cache, summary, table, none, none)
+    bl.bitlinear_attention_select(x, cache, summary, table, none, blocks)
+    bl.bitlinear_attention_blocks(x, cache, table, none, blocks, x.clone())
+    y = torch.empty(0, 7, device="cuda")
+    bl.bitlinear_softmax(y, y)
+    p = torch.empty(0, 3, 7, device="cuda")
+    bl.bitlinear_verify(p, p[:, :2], none.view(0, 1).expand(0, 2), torch.empty(0, 3, device="cuda"), none.view(0, 1).expand(0, 3), none)
+    torch.cuda.synchronize()
+    assert (summary[0] == 99).all()
