@@ -12,10 +12,10 @@
 // weight counts as a whole number of 2^-s, s = 62 - ceil(log2 V), so that sums of V of them are exact
 // in 64 bits whatever their order, and the token is the first whose running sum passes r * total.
 //
-// Measured.  softmax: 320 rows of 50000 25.0 us, 128 MB, 5.1 TB/s (a copy's 19.1 us): rows come in four rounds of clusters,
+// Measured.  softmax: 320 rows of 50000 25.7 us, 128 MB, 5.0 TB/s (a copy's 19.1 us): rows come in four rounds of clusters,
 // each of which reads, meets once and writes (28.7 us while every warp told every CTA its sums: each then waits for what it
 // published); one row 3.6 us, latency.  Rows streamed through rings in shared memory under
-// resident CTAs took 43.3 where this took 33.9; five CTAs an SM 32.4 for 30.5.  verify: 64 sequences of 4 drafts over 50000 tokens 11.2 us (3.8 us of bytes): the
+// resident CTAs took 43.3 where this took 33.9.  verify: 64 sequences of 4 drafts over 50000 tokens 11.2 us (3.8 us of bytes): the
 // drafts' probabilities, then the two rows they point to, then the cluster's meeting, one after the other; one sequence 5.6.
 #include <type_traits>
 
@@ -51,14 +51,17 @@ struct Row {
       : V(V_), shift((int)((reinterpret_cast<uintptr_t>(row) >> 2) & 3)), chunks((int)((V_ + shift + 3) / 4)), lo(shift > 0), hi((int)((V_ + shift) / 4)) {}
   __device__ __forceinline__ bool whole(int i) const { return i >= lo && i < hi; }
 };
-// The output may be the logits' own buffer, so logits are read by coherent loads.  ONCE: they are not read again, and left
-// out of L1 (320 rows of 50000 24.9 us, 25.9 without).
+// The output may be the logits' own buffer, so logits are read by coherent loads.  ONCE: they are not read again, and come
+// by relaxed loads (320 rows of 50000 out of DRAM 27.7 us, 28.4 by plain ones that leave L1 alone).
 template <bool ONCE>
 __device__ __forceinline__ float4 load4(const float4* p) {
-  if constexpr (!ONCE) return *p;
-  float4 x;
-  asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(p) : "memory");
-  return x;
+  if constexpr (ONCE) {
+    float4 x;
+    asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(p) : "memory");
+    return x;
+  } else {
+    return *p;
+  }
 }
 template <bool ONCE>
 __device__ __forceinline__ float4 load_chunk(const float* row, const Row& r, int i, float none) {
@@ -200,13 +203,13 @@ __device__ __forceinline__ void finish_row(const Row& r, float* out, float T, fl
 __device__ __forceinline__ float largest_of(float m, const float4& v) { return fmaxf(m, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w))); }
 
 // CTAs an SM, as many as the registers of NV chunks allow; said, because the compiler stops short of it (seven chunks: 54
-// registers where 48 do, in place 21.7 us for 19.7 on 320 rows of 50000).
+// registers where 48 do, in place 21.7 us for 19.6 on 320 rows of 50000).
 __host__ __device__ constexpr int softmax_ctas(int nv, bool aligned) { return nv == 7 ? (aligned ? 5 : 4) : nv == 4 ? 6 : 8; }
 
 // p may be y: a thread has read a chunk for the last time when it writes it.
 // A row a cluster.  A CTA keeps its share of the row in registers, NV chunks a thread; NV == 0: any number of
 // them, read a second and a third time.  ALIGNED: V is a multiple of four, so that every chunk is whole (320 rows of
-// 50000 25.0 us; of 50001 26.0).  Every warp sums under a maximum of its own, so
+// 50000 25.7 us; of 50001 26.8).  Every warp sums under a maximum of its own, so
 // the cluster meets once.
 template <int THREADS, int NV, bool ALIGNED>
 __global__ void __launch_bounds__(THREADS, softmax_ctas(NV, ALIGNED)) softmax_kernel(const float* y, float* p, const float* __restrict__ temperature, int64_t V) {
