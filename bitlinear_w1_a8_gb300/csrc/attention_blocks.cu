@@ -4,8 +4,8 @@
 // page through two look-ups (list, page table), and the work of a row is known on the host.
 //
 // Bound as attention.cu's by the widening of the codes beside the bytes: 32 pages of 64 tokens each of 16 sequences, 32 heads of
-// 80, int8: 37.9 us, 174 MB, 4.6 TB/s, one CTA a row and 512 of 608 places; 64 pages of 64 of one sequence, 8 key heads of 128,
-// bf16: 9.8 us, four steps a warp; 8 of 32, 16 heads, fp8: 4.5 us, latency.
+// 80, int8: 38.1 us, 174 MB, 4.6 TB/s, one CTA a row and 512 of 608 places; 64 pages of 64 of one sequence, 8 key heads of 128,
+// bf16: 9.8 us, four steps a warp; 8 of 32, 16 heads, fp8: 4.6 us, latency.
 #include "attend.cuh"
 #include "serve.cuh"
 

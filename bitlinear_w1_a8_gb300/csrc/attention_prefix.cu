@@ -24,7 +24,7 @@
 // the first weights' product and ~7,000 to hand over.  What bounds it: a tile's logits, weights, their product and the place
 // for the next but one's logits follow one another (1600 + 4200 + 1500 cycles), for two tiles at a time; five MMAs a tile need
 // 2700, and with what TMA, the turning of values and both operands of the MMAs read and write of shared memory it is busy
-// for ~3300.  The tensor pipe is busy 55 cycles of 100 on an SM that has work.
+// for ~3300.  The tensor pipe is busy 53 cycles of 100 on an SM that has work.
 // Slower: a thread a row in the adding groups (its loops are fetched, not issued); unrolled loops (three times as long: the
 // code is fetched as it runs); values turned in one pass that holds them in registers (spills).
 #include "attend.cuh"

@@ -7,14 +7,16 @@
 //   out = (P_shared + P_own) / (sum_shared + sum_own), each sum under its reference, joined as the
 // parts of one sequence are (attend.cuh).  Two launches: the shared tokens, split over CTAs
 // that leave their parts in the workspace, and each row's own tokens with the join.  The second begins while
-// the first runs, as places on the SMs come free, and waits for it where it adds the parts.
+// the first runs, as places on the SMs come free, and waits for it where it adds the parts.  shares.h has the rules by which a
+// call goes one way or another, with what they were measured by.
 //
 // Measured (graph replays; the least is of bytes read once at 6684 GB/s): eight sequences of up to 2048 tokens with five
-// drafted rows each, 32 heads of 80, int8, 20.4 us (10.1): the least time of a step a warp, two launches and the
+// drafted rows each, 32 heads of 80, int8, 20.6 us (10.1): the least time of a step a warp, two launches and the
 // lookups; 64 rows behind 2039 tokens, up to 256 each of their own, 35.7 us (8.5): eight readings of the prefix out of L2
 // (21 us, instructions: the schedulers issue in 53 cycles of 100), and own tokens whose warps begin and end with each
 // row (2048 rows, 20 us alone, two thirds of it behind the first launch); 64 rows of 8 key heads of 128 behind 16384 tokens, bf16,
-// 51.0 us (12.3): ~42 of it the tensor cores' part (attention_prefix.cu), the rest the wait for SMs, lookups and the join.
+// 51.0 us (12.3; of fp8 53.5, of int8 55.1): ~42 of it the tensor cores' part (attention_prefix.cu), the rest the wait for SMs, lookups
+// and the join.
 #include "attend.cuh"
 #include "serve.cuh"
 

@@ -15,11 +15,11 @@
 // page has a larger product with those codes by more than the roundings, six of 2^-24 of step max|q| sum |c_d| at most.  A
 // key head's score is the largest of its q heads'.
 //
-// Measured.  Summaries of three prompts of up to 2039 tokens, 32 heads of 80, int8: 10.3 us for 15 MB (2.2 us of copying): two
+// Measured.  Summaries of three prompts of up to 2039 tokens, 32 heads of 80, int8: 9.7 us for 15 MB (2.2 us of copying): two
 // rounds and a half of CTAs whose loads, join in shared memory and lookups follow one another (a warp waits for memory half
-// of its time); of the page that a token was just written to, 16 sequences of 32 heads: 4.0 us, latency.  A warp a page,
-// whose lanes join by shuffles, took 10.6 and 8.7.  The choice of 32 of 256 pages for 16 sequences of 32 heads: 9.2 us, of 64 of 2048
-// for one of 8 key heads 8.7: latency, a dozen meetings of a CTA's threads among it (a byte at a time over all CTAs'
+// of its time); of the page that a token was just written to, 16 sequences of 32 heads: 3.9 us, latency.  A warp a page,
+// whose lanes join by shuffles, took 10.6 and 8.7.  The choice of 32 of 256 pages for 16 sequences of 32 heads: 8.9 us, of 64 of 2048
+// for one of 8 key heads 8.4: latency, a dozen meetings of a CTA's threads among it (a byte at a time over all CTAs'
 // keys, the way of more than 8192 pages, and bounds that waited for q's codes took 16 and 22).
 #include <cuda_fp16.h>
 
