@@ -774,19 +774,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) prefix_wide_kernel(AttendArgs
         }
         __syncwarp();
       }
-      // No copy is on its way when the CTA ends.  Each was waited for by the role that used it, but after a wait that
-      // has run out: then for a millisecond at most, long after the last one.
-      if (lane == 0 && !alive) {
-        const unsigned long long t0 = tc::global_timer();
-#pragma unroll 1
-        while (tc::global_timer() - t0 < 1000000ull) {
-        }
-      }
     }
     __syncwarp();
   }
   tc::tc_fence_before();
   __syncthreads();
+  // No copy is on its way when the CTA ends.  Each was waited for by the role that used it, but after a wait that has
+  // run out, in whatever role: then for a millisecond, long after the last one.
+  if (warp == kIssue + 3 && lane == 0 && *reinterpret_cast<volatile int*>(&st.abort_flag)) {
+    const unsigned long long t0 = tc::global_timer();
+#pragma unroll 1
+    while (tc::global_timer() - t0 < 1000000ull) {
+    }
+  }
   if (warp == kIssue) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);

@@ -6,7 +6,7 @@ eight warps turn the logits of every other tile into weights.  The model runs th
 arrival counts, with copies and products that end whenever they like (some values very late), and asserts what the
 kernel relies on: an entry of the page ring, its mask, its steps and its values' power of two are those of the tile in
 hand wherever a role reads them; a place of the operand ring holds what the product in flight takes; S, the weights over it and O are
-not written while someone still has them; no wait meets a later phase; every role ends, after an abort too.
+not written while someone still has them; no wait meets a later phase; every role ends, after an abort too, and no copy outlives the CTA.
 
 Ring sizes, arrival counts and the place where an entry is given back are read from the source.  A negative control (the
 entry given back once the weights are written, which nothing orders behind the same tile's values) must fail.
@@ -43,7 +43,9 @@ def constants(bf16):
         arrivals = re.finditer(r"(.*)tc::mbar_arrive\(&st\.meta_empty\[entry\]\)", branch)
         first = next(m for m in arrivals if not (bf16 and "!W::kBf16" in m.group(1)))
         behind.append(first.start() > waited)
-    return dict(bf16=bf16, entries=number(r"kEntries = (\d+);"), meta_empty=number(r"mbar_init\(&st\.meta_empty\[i\], (\d+)\)"),
+    # copies that nobody waited for any more are waited for at the end: once all roles have met, or by the copying warp alone?
+    at_end = text.index("No copy is on its way when the CTA ends") > text.rindex("__syncthreads();")
+    return dict(bf16=bf16, at_end=at_end, entries=number(r"kEntries = (\d+);"), meta_empty=number(r"mbar_init\(&st\.meta_empty\[i\], (\d+)\)"),
                 stages=pick(both), raws=pick(raws), behind=behind)
 
 
@@ -69,6 +71,7 @@ def simulate(c, tiles, seed, abort_at=None):
             "s_full": [Bar(1) for _ in range(2)], "p_full": [Bar(8) for _ in range(2)], "o_full": [Bar(1) for _ in range(2)]}
     st = {"t": 0, "abort": False}
     pending = []
+    copying = {"now": 0, "gave_up": False}
     entry, mask, steps, unit = ([None] * E for _ in range(4))
     operand_at = [None] * stages   # what a place of the ring holds
     taken = [0] * stages           # products in flight that read it
@@ -96,7 +99,7 @@ def simulate(c, tiles, seed, abort_at=None):
         def wait(self, name, which, phase):
             bar = bars[name][which]
             while self.alive and bar.completed <= phase:
-                if st["abort"]:
+                if st["abort"] and rnd.random() < 0.5:
                     self.alive = False
                     return
                 yield
@@ -127,7 +130,11 @@ def simulate(c, tiles, seed, abort_at=None):
             yield
 
     def land(after, what):
-        pending.append([st["t"] + after, what])
+        def landed():
+            copying["now"] -= 1
+            what()
+        copying["now"] += 1
+        pending.append([st["t"] + after, landed])
 
     def lookups():
         r = Role()
@@ -171,6 +178,7 @@ def simulate(c, tiles, seed, abort_at=None):
                     arrive("raw_full", slot)
                 land(after if r.alive else 1, here)
             yield
+        copying["gave_up"] = not r.alive
 
     def widen8(w):
         r = Role()
@@ -289,6 +297,8 @@ def simulate(c, tiles, seed, abort_at=None):
         if pending and idle % 50 == 49 and rnd.random() < 0.5:  # nothing else may have moved: to the next end of a copy
             st["t"] = max(st["t"], min(p[0] for p in pending) - 1)
         assert idle < 60000, f"no progress: {tiles} tiles, seed {seed}, abort at {abort_at}"
+    waits = st["abort"] if c["at_end"] else copying["gave_up"]
+    assert copying["now"] == 0 or waits, "the CTA ends under a copy"
 
 
 @pytest.mark.parametrize("bf16", [False, True])
@@ -304,6 +314,8 @@ def test_every_role_ends_after_an_abort(bf16):
     c = constants(bf16)
     for seed in range(25):
         simulate(c, 9, seed, abort_at=random.Random(seed).randint(1, 400))
+    for seed in range(300):  # late ones: the last copies are on their way
+        simulate(c, 2, seed, abort_at=random.Random(seed).randint(1, 120))
 
 
 def test_negative_control_entries_given_back_with_the_weights():
